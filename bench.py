@@ -80,6 +80,7 @@ KERNEL_SOURCES = {
     "int8": _COMMON_SOURCES + _DECODE_SOURCES + ("append.cu", "append_int8.cu"),
     "cow": _COMMON_SOURCES + ("append.cu",),
     "prefill": _COMMON_SOURCES + ("prefill.cu",),
+    "rope": _COMMON_SOURCES + ("rope.cu",),
 }
 
 

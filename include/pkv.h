@@ -426,6 +426,90 @@ pkv_status pkv_paged_decode_step_int8(const void* q, const void* k_new, const vo
                                       size_t workspace_bytes, int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions, fused with the append.  The first rot_dim elements of
+ * every query and key head are rot_dim / 2 pairs -- elements (2 i, 2 i + 1) in
+ * the interleaved layout, (i, i + rot_dim / 2) in the half one -- and pair
+ * (x, y) number i of a token at position p becomes
+ *     (a (x cos t - y sin t), a (x sin t + y cos t)),   t = p f_i
+ * with a = amplitude; the elements from rot_dim on pass through.
+ *
+ * pkv_rope_plan (host, no CUDA call) lays out the frequencies of
+ *     f_i = base^(-2 i / rot_dim),   i < rot_dim / 2
+ * scaled for a context longer than original_context:
+ *   PKV_ROPE_NONE        as they are
+ *   PKV_ROPE_LINEAR      f_i / factor
+ *   PKV_ROPE_BASE        base replaced by base factor^(rot_dim / (rot_dim - 2))
+ *   PKV_ROPE_RAMP        f_i (1 - w_i) + f_i / factor w_i, where w_i rises
+ *                        from 0 to 1 over the pairs between the one that makes
+ *                        high_turns full turns in original_context positions
+ *                        (rounded down) and the one that makes low_turns
+ *                        (rounded up); amplitude 0.1 ln(factor) + 1
+ *   PKV_ROPE_WAVELENGTH  f_i w + f_i / factor (1 - w), w = (n - low_turns) /
+ *                        (high_turns - low_turns) clamped to [0, 1], n the
+ *                        full turns of f_i in original_context positions
+ * into turns[rot_dim / 2] (host): f_i / (2 pi), full turns per position, in
+ * units of 2^-64 (rounded).  A position times it, modulo 2^64, is the angle
+ * modulo one turn, so far positions lose nothing but p times f_i's rounding.  amplitude: 1
+ * but for PKV_ROPE_RAMP.  The caller copies turns to the device once.
+ * PKV_ERR_INVALID_ARG: an odd or non-positive rot_dim, base <= 1, factor < 1,
+ * low_turns <= 0 or high_turns <= low_turns (where they are used).
+ *
+ * pkv_rope_append: q_out[t] takes the turned q[t]; the cache slot
+ * slot_mapping[t] (as in pkv_kv_append) takes the turned k_new[t] and v_new[t]
+ * as it is.  The rotation is fp32 and each turned element is rounded once, to
+ * dtype or to the cache's FP8 format (fl32(x) / scale[h] as
+ * pkv_kv_append_fp8 / _e5m2; v rows are stored bit for bit as those calls
+ * store them).
+ *   q, k_new, v_new    dtype; token t's heads, [H, head_dim] contiguous, start
+ *                      t * stride elements from the pointer, so they may be
+ *                      slices of one projection's output.  Strides: multiples
+ *                      of 8, at least H head_dim.
+ *   q_out              as q, with its own stride; q_out == q with the same
+ *                      stride turns q in place.  Other overlaps are undefined.
+ *   positions          device int32 [T]; a negative one marks a padding token,
+ *                      of which nothing is read or written.
+ *   slot_mapping       device int64 [T]; negative: no append for the token (q
+ *                      is turned all the same); past the pool: skipped and
+ *                      PKV_ERR_OOB in err_flag.
+ *   turns, amplitude   from pkv_rope_plan, turns in device memory.
+ * q and q_out may both be NULL (append only), or k_new and v_new (turn q only;
+ * the caches and slots are then not used).  rot_dim: a multiple of 16 up to
+ * head_dim (else PKV_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+typedef enum { PKV_ROPE_HALF = 0, PKV_ROPE_INTERLEAVED = 1 } pkv_rope_layout;
+typedef enum {
+  PKV_ROPE_NONE = 0,
+  PKV_ROPE_LINEAR = 1,
+  PKV_ROPE_BASE = 2,
+  PKV_ROPE_RAMP = 3,
+  PKV_ROPE_WAVELENGTH = 4
+} pkv_rope_scaling;
+
+pkv_status pkv_rope_plan(int rot_dim, double base, pkv_rope_scaling scaling, double factor, double original_context,
+                         double low_turns, double high_turns, uint64_t* turns, float* amplitude);
+
+pkv_status pkv_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                           int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                           int64_t num_tokens, const uint64_t* turns, int rot_dim, pkv_rope_layout layout,
+                           float amplitude, void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                           int64_t num_blocks, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                           pkv_dtype dtype, int32_t* err_flag, void* stream);
+pkv_status pkv_rope_append_fp8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                               const void* v_new, int64_t v_stride, const int32_t* positions,
+                               const int64_t* slot_mapping, int64_t num_tokens, const uint64_t* turns, int rot_dim,
+                               pkv_rope_layout layout, float amplitude, void* q_out, int64_t q_out_stride,
+                               uint8_t* k_cache, uint8_t* v_cache, int64_t num_blocks, const float* k_scale,
+                               const float* v_scale, int num_q_heads, int num_kv_heads, int head_dim,
+                               int block_size, pkv_dtype dtype, int32_t* err_flag, void* stream);
+pkv_status pkv_rope_append_e5m2(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                const void* v_new, int64_t v_stride, const int32_t* positions,
+                                const int64_t* slot_mapping, int64_t num_tokens, const uint64_t* turns, int rot_dim,
+                                pkv_rope_layout layout, float amplitude, void* q_out, int64_t q_out_stride,
+                                uint8_t* k_cache, uint8_t* v_cache, int64_t num_blocks, const float* k_scale,
+                                const float* v_scale, int num_q_heads, int num_kv_heads, int head_dim,
+                                int block_size, pkv_dtype dtype, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Host-side block pool ("Series 03 ...", sections 3.2-3.3; "What a KV cache
  * is ...", section 3.2): a preallocated set of block ids handed out on demand,
  * with reference counts for blocks shared by several block tables.  Policy: a

@@ -26,10 +26,14 @@ __all__ = [
     "StepGraph", "pkv_kv_quantize_int8", "pkv_kv_append_int8", "pkv_paged_decode_attention_int8",
     "pkv_kv_append_e5m2", "pkv_paged_decode_attention_e5m2", "pkv_paged_decode_step_e5m2",
     "pkv_paged_decode_step_int8",
+    "PKV_ROPE_HALF", "PKV_ROPE_INTERLEAVED", "pkv_rope_plan", "pkv_rope_append", "pkv_rope_append_fp8",
+    "pkv_rope_append_e5m2",
 ]
 
 PKV_F16 = 0
 PKV_BF16 = 1
+PKV_ROPE_HALF = 0
+PKV_ROPE_INTERLEAVED = 1
 PKV_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024   # as in pkv.h
 _DIR = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_DIR, "libpkv.so")
@@ -56,7 +60,7 @@ def prefill_lib():
         _prefill_lib = pl
     return _prefill_lib
 
-_p, _i, _i64, _sz, _f = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
+_p, _i, _i64, _sz, _f, _d = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float, C.c_double
 _SIGS = {
     "pkv_version": (_i, []),
     "pkv_status_string": (C.c_char_p, [_i]),
@@ -105,6 +109,13 @@ _SIGS = {
                                              _i, _p, _sz, _p, _p]),
     "pkv_paged_decode_step_int8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _f, _p, _i,
                                         _i, _p, _p, _sz, _p, _p]),
+    "pkv_rope_plan": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, C.POINTER(_f)]),
+    "pkv_rope_append": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i, _i, _f, _p, _i64, _p, _p, _i64,
+                             _i, _i, _i, _i, _i, _p, _p]),
+    "pkv_rope_append_fp8": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i, _i, _f, _p, _i64, _p, _p,
+                                 _i64, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
+    "pkv_rope_append_e5m2": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i, _i, _f, _p, _i64, _p, _p,
+                                  _i64, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
 }
 _PREFILL_SIG = [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _f, _p, _i, _p, _p]
 for _name, (_res, _args) in _SIGS.items():
@@ -432,6 +443,86 @@ def pkv_paged_decode_step_int8(q, k_new, v_new, k_cache, v_cache, slab_params, b
         _ptr(context_lens), q.shape[0], q.shape[1], hkv, d, bs, block_tables.shape[1], nb, max_context_len, scale,
         _ptr(out), _dtype_code(q, q_dtype), partition_tokens, _ptr(slot_mapping_out), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+
+
+_ROPE_LAYOUTS = {"half": PKV_ROPE_HALF, "interleaved": PKV_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
+
+
+def pkv_rope_plan(rot_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_context: float = 8192.0, low_turns: float = 1.0, high_turns: float | None = None):
+    """The frequencies of a rotation, scaled for long contexts: (turns,
+    amplitude), turns a numpy int64 array [rot_dim / 2] (the bits of the
+    uint64 the library takes) to be copied to the device once.  scaling:
+    "none", "linear", "base", "ramp" or "wavelength"; high_turns defaults to
+    32 ("ramp") or 4 ("wavelength")."""
+    import numpy as np
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    turns = np.zeros(max(rot_dim // 2, 1), dtype=np.int64)
+    amp = _f(0.0)
+    high = high_turns if high_turns is not None else (4.0 if scaling == "wavelength" else 32.0)
+    _check("pkv_rope_plan", lib.pkv_rope_plan(rot_dim, base, _ROPE_SCALINGS[scaling], factor, original_context,
+                                              low_turns, high, turns.ctypes.data, C.byref(amp)))
+    return turns, amp.value
+
+
+def _token_stride(t, name: str) -> int:
+    """Elements between the tokens of t [T, H, D], whose heads are contiguous."""
+    if t is None:
+        return 0
+    n, h, d = t.shape
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, scales, layout, amplitude,
+          dtype, err_flag, stream):
+    some = q if q is not None else k_new
+    if k_new is not None:
+        nb, hkv, bs, d = k_cache.shape
+        if k_new.shape != v_new.shape or k_new.shape[1:] != (hkv, d):
+            raise ValueError("k_new and v_new must be [T, num_kv_heads, head_dim] of the cache")
+        if slot_mapping.numel() != positions.numel():
+            raise ValueError("slot_mapping and positions differ in length")
+    else:
+        nb, hkv, bs, d = 0, 0, 16, q.shape[2]
+    if q is not None and q.shape != q_out.shape:
+        raise ValueError("q and q_out differ in shape")
+    for t in (q, k_new):
+        if t is not None and (t.shape[0] != positions.numel() or t.shape[2] != d):
+            raise ValueError("q, k_new and positions differ in tokens or head_dim")
+    _check(fn, getattr(lib, fn)(
+        _ptr(q), _token_stride(q, "q"), _ptr(k_new), _token_stride(k_new, "k_new"), _ptr(v_new),
+        _token_stride(v_new, "v_new"), _ptr(positions), _ptr(slot_mapping), positions.numel(), _ptr(turns),
+        2 * turns.numel(), _ROPE_LAYOUTS.get(layout, layout), amplitude, _ptr(q_out), _token_stride(q_out, "q_out"),
+        _ptr(k_cache), _ptr(v_cache), nb, *scales, 0 if q is None else q.shape[1], hkv, d, bs,
+        _dtype_code(some, dtype), _ptr(err_flag), _stream(stream)))
+
+
+def pkv_rope_append(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, *, layout="half",
+                    amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
+    """Turn q [T, Hq, D] into q_out, and append the turned k_new and v_new
+    [T, Hkv, D] to their slots.  q and q_out, or k_new and v_new (with the
+    caches and slots), may be None.  The token stride is free; q_out may be q.
+    turns, amplitude: from pkv_rope_plan (turns on the device)."""
+    _rope("pkv_rope_append", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, (), layout,
+          amplitude, dtype, err_flag, stream)
+
+
+def pkv_rope_append_fp8(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, *,
+                        layout="half", amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
+    """pkv_rope_append into an E4M3 cache (uint8 codes, fp32 per-head scales)."""
+    _rope("pkv_rope_append_fp8", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache,
+          (_ptr(k_scale), _ptr(v_scale)), layout, amplitude, dtype, err_flag, stream)
+
+
+def pkv_rope_append_e5m2(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale,
+                         *, layout="half", amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
+    """pkv_rope_append into an E5M2 cache (uint8 codes, fp32 per-head scales)."""
+    _rope("pkv_rope_append_e5m2", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache,
+          (_ptr(k_scale), _ptr(v_scale)), layout, amplitude, dtype, err_flag, stream)
 
 
 def pkv_blocks_needed(num_tokens: int, block_size: int = 16) -> int:
