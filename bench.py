@@ -81,6 +81,7 @@ KERNEL_SOURCES = {
     "cow": _COMMON_SOURCES + ("append.cu",),
     "prefill": _COMMON_SOURCES + ("prefill.cu",),
     "rope": _COMMON_SOURCES + ("rope.cu",),
+    "sparse": _COMMON_SOURCES + _DECODE_SOURCES + ("block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu"),
 }
 
 

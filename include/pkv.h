@@ -510,6 +510,94 @@ pkv_status pkv_rope_append_e5m2(const void* q, int64_t q_stride, const void* k_n
                                 int block_size, pkv_dtype dtype, int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Block-sparse decode: attention over the blocks of a long context that a
+ * cheap score picks for each (sequence, KV head).
+ *
+ * pkv_kv_block_bounds: bounds[id, h] = the elementwise minimum, then maximum,
+ * of the rows of block id that hold tokens ([num_blocks, num_kv_heads, 2,
+ * head_dim] of dtype, exact; a NaN key element gives NaN), for the blocks of
+ * every sequence that hold its last new_lens[b] tokens: the new ones after an
+ * append, whose first block may have held older rows as well.  new_lens NULL:
+ * all blocks of the context.  max_new_len: an upper bound of new_lens (of
+ * context_lens when NULL); it sizes the launch, and blocks past it are left
+ * as they are and reported as PKV_ERR_OOB.  _fp8 / _e5m2: over codes; the
+ * bounds are the codes' values, before the per-head scale, in bounds_dtype
+ * (exact in both).  A block that two sequences share must hold the same rows
+ * for both (full, or equal lengths).  Bounds of other blocks stay.
+ *
+ * pkv_block_scores: for i < ceil(context_lens[b] / 16), with (lo, hi) the
+ * bounds of block_tables[b][i],
+ *     scores[b, g, i] = scale k_scale[g] max_h sum_d max(q_d lo_d, q_d hi_d)
+ * over the query heads h of KV head g: no token of the block has a larger
+ * scaled logit for any of them.  fp32 [batch, num_kv_heads,
+ * max_blocks_per_seq]; entries past the context stay as they are.  k_scale:
+ * device [num_kv_heads], NULL = 1.  scale >= 0.  Elements must be finite for
+ * a defined score; a NaN or an infinity in q or the bounds gives NaN or an
+ * infinity.  A table entry outside the pool scores -infinity and reports
+ * PKV_ERR_OOB.  max_context_len as in pkv_paged_decode_attention.
+ *
+ * pkv_select_blocks: the blocks to attend to, ascending, in selected [batch,
+ * num_kv_heads, budget] int32: every block when there are at most budget of
+ * them, else the first num_first, the last num_last and the highest-scoring
+ * others (ties to the lowest index; NaN above +infinity, -0 equal to +0);
+ * entries behind the list are -1.  num_first + num_last <= budget.  scores:
+ * any fp32 [batch, num_kv_heads, max_blocks_per_seq].
+ *
+ * pkv_paged_decode_attention_sparse[_fp8 / _e5m2]: pkv_paged_decode_attention
+ * over the tokens of the listed blocks only: of selected[b, g] the first
+ * min(budget, ceil(context_lens[b] / 16)) entries count, in any order; a
+ * negative entry is skipped, one listed twice counts twice, one behind the
+ * context is skipped and reported as PKV_ERR_OOB.  The context's last block
+ * contributes its tokens only.  No tokens listed gives out = 0.
+ *   workspace   at least pkv_decode_workspace_bytes(batch, num_q_heads,
+ *               num_kv_heads, head_dim, budget, 16 budget, 0).
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_kv_block_bounds(const void* k_cache, const int32_t* block_tables, const int32_t* context_lens,
+                               const int32_t* new_lens, int max_new_len, int batch, int num_kv_heads, int head_dim,
+                               int block_size, int max_blocks_per_seq, int64_t num_blocks, void* bounds,
+                               pkv_dtype dtype, int32_t* err_flag, void* stream);
+pkv_status pkv_kv_block_bounds_fp8(const uint8_t* k_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                   const int32_t* new_lens, int max_new_len, int batch, int num_kv_heads,
+                                   int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                                   void* bounds, pkv_dtype bounds_dtype, int32_t* err_flag, void* stream);
+pkv_status pkv_kv_block_bounds_e5m2(const uint8_t* k_cache, const int32_t* block_tables,
+                                    const int32_t* context_lens, const int32_t* new_lens, int max_new_len, int batch,
+                                    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                    int64_t num_blocks, void* bounds, pkv_dtype bounds_dtype, int32_t* err_flag,
+                                    void* stream);
+pkv_status pkv_block_scores(const void* q, const void* bounds, const int32_t* block_tables,
+                            const int32_t* context_lens, const float* k_scale, int batch, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                            int64_t num_blocks, int max_context_len, float scale, float* scores, pkv_dtype dtype,
+                            int32_t* err_flag, void* stream);
+pkv_status pkv_select_blocks(const float* scores, const int32_t* context_lens, int batch, int num_kv_heads,
+                             int block_size, int max_blocks_per_seq, int num_first, int num_last, int budget,
+                             int32_t* selected, int32_t* err_flag, void* stream);
+pkv_status pkv_paged_decode_attention_sparse(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens,
+                                             const int32_t* selected, int budget, int batch, int num_q_heads,
+                                             int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                             int64_t num_blocks, float scale, void* out, pkv_dtype dtype,
+                                             void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                             void* stream);
+pkv_status pkv_paged_decode_attention_sparse_fp8(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                                 const float* k_scale, const float* v_scale,
+                                                 const int32_t* block_tables, const int32_t* context_lens,
+                                                 const int32_t* selected, int budget, int batch, int num_q_heads,
+                                                 int num_kv_heads, int head_dim, int block_size,
+                                                 int max_blocks_per_seq, int64_t num_blocks, float scale, void* out,
+                                                 pkv_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                                                 int32_t* err_flag, void* stream);
+pkv_status pkv_paged_decode_attention_sparse_e5m2(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                                  const float* k_scale, const float* v_scale,
+                                                  const int32_t* block_tables, const int32_t* context_lens,
+                                                  const int32_t* selected, int budget, int batch, int num_q_heads,
+                                                  int num_kv_heads, int head_dim, int block_size,
+                                                  int max_blocks_per_seq, int64_t num_blocks, float scale, void* out,
+                                                  pkv_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                                                  int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Host-side block pool ("Series 03 ...", sections 3.2-3.3; "What a KV cache
  * is ...", section 3.2): a preallocated set of block ids handed out on demand,
  * with reference counts for blocks shared by several block tables.  Policy: a

@@ -28,6 +28,9 @@ __all__ = [
     "pkv_paged_decode_step_int8",
     "PKV_ROPE_HALF", "PKV_ROPE_INTERLEAVED", "pkv_rope_plan", "pkv_rope_append", "pkv_rope_append_fp8",
     "pkv_rope_append_e5m2",
+    "pkv_kv_block_bounds", "pkv_kv_block_bounds_fp8", "pkv_kv_block_bounds_e5m2", "pkv_block_scores",
+    "pkv_select_blocks", "pkv_paged_decode_attention_sparse", "pkv_paged_decode_attention_sparse_fp8",
+    "pkv_paged_decode_attention_sparse_e5m2",
 ]
 
 PKV_F16 = 0
@@ -109,6 +112,17 @@ _SIGS = {
                                              _i, _p, _sz, _p, _p]),
     "pkv_paged_decode_step_int8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _f, _p, _i,
                                         _i, _p, _p, _sz, _p, _p]),
+    "pkv_kv_block_bounds": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _p, _i, _p, _p]),
+    "pkv_kv_block_bounds_fp8": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _p, _i, _p, _p]),
+    "pkv_kv_block_bounds_e5m2": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _p, _i, _p, _p]),
+    "pkv_block_scores": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _f, _p, _i, _p, _p]),
+    "pkv_select_blocks": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p]),
+    "pkv_paged_decode_attention_sparse": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _f, _p, _i,
+                                               _p, _sz, _p, _p]),
+    "pkv_paged_decode_attention_sparse_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64,
+                                                   _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_paged_decode_attention_sparse_e5m2": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64,
+                                                    _f, _p, _i, _p, _sz, _p, _p]),
     "pkv_rope_plan": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, C.POINTER(_f)]),
     "pkv_rope_append": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i, _i, _f, _p, _i64, _p, _p, _i64,
                              _i, _i, _i, _i, _i, _p, _p]),
@@ -523,6 +537,101 @@ def pkv_rope_append_e5m2(q, k_new, v_new, positions, slot_mapping, turns, q_out,
     """pkv_rope_append into an E5M2 cache (uint8 codes, fp32 per-head scales)."""
     _rope("pkv_rope_append_e5m2", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache,
           (_ptr(k_scale), _ptr(v_scale)), layout, amplitude, dtype, err_flag, stream)
+
+
+def _block_bounds(fn, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream):
+    nb, hkv, bs, d = k_cache.shape
+    if tuple(bounds.shape) != (nb, hkv, 2, d):
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
+    _check(fn, getattr(lib, fn)(
+        _ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(new_lens), max_new_len, context_lens.numel(), hkv, d,
+        bs, block_tables.shape[1], nb, _ptr(bounds), _dtype_code(bounds, dtype), _ptr(err_flag), _stream(stream)))
+
+
+def pkv_kv_block_bounds(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None, dtype=None,
+                        err_flag=None, stream=None) -> None:
+    """Elementwise minimum and maximum of the cached keys per (block, KV head),
+    into bounds [NB, Hkv, 2, D], for the blocks of each sequence's last
+    new_lens tokens (None: its whole context)."""
+    _block_bounds("pkv_kv_block_bounds", k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype,
+                  err_flag, stream)
+
+
+def pkv_kv_block_bounds_fp8(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None,
+                            dtype=None, err_flag=None, stream=None) -> None:
+    """pkv_kv_block_bounds over an E4M3 cache: 16-bit bounds of the codes'
+    values, before the per-head scale."""
+    _block_bounds("pkv_kv_block_bounds_fp8", k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype,
+                  err_flag, stream)
+
+
+def pkv_kv_block_bounds_e5m2(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None,
+                             dtype=None, err_flag=None, stream=None) -> None:
+    """pkv_kv_block_bounds over an E5M2 cache."""
+    _block_bounds("pkv_kv_block_bounds_e5m2", k_cache, block_tables, context_lens, bounds, new_lens, max_new_len,
+                  dtype, err_flag, stream)
+
+
+def pkv_block_scores(q, bounds, block_tables, context_lens, scores, *, scale: float, max_context_len: int,
+                     k_scale=None, dtype=None, err_flag=None, stream=None) -> None:
+    """Upper bounds of every block's scaled logits, scores fp32 [B, Hkv,
+    max_blocks], from the block bounds [NB, Hkv, 2, D]."""
+    b, hq, d = q.shape
+    nb, hkv = bounds.shape[:2]
+    if tuple(scores.shape) != (b, hkv, block_tables.shape[1]) or tuple(bounds.shape[2:]) != (2, d):
+        raise ValueError("scores must be [batch, num_kv_heads, max_blocks], bounds [num_blocks, num_kv_heads, 2, "
+                         "head_dim]")
+    if bounds.dtype != q.dtype:
+        raise TypeError("bounds and q differ in dtype")
+    _check("pkv_block_scores", lib.pkv_block_scores(
+        _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), _ptr(k_scale), b, hq, hkv, d, 16,
+        block_tables.shape[1], nb, max_context_len, scale, _ptr(scores), _dtype_code(q, dtype), _ptr(err_flag),
+        _stream(stream)))
+
+
+def pkv_select_blocks(scores, context_lens, selected, *, num_first: int = 1, num_last: int = 1, err_flag=None,
+                      stream=None) -> None:
+    """selected int32 [B, Hkv, budget]: the first num_first, the last num_last
+    and the highest-scoring other blocks, ascending, -1 behind the list."""
+    b, hkv, blocks = scores.shape
+    if tuple(selected.shape[:2]) != (b, hkv):
+        raise ValueError("selected must be [batch, num_kv_heads, budget]")
+    _check("pkv_select_blocks", lib.pkv_select_blocks(
+        _ptr(scores), _ptr(context_lens), b, hkv, 16, blocks, num_first, num_last, selected.shape[2], _ptr(selected),
+        _ptr(err_flag), _stream(stream)))
+
+
+def _sparse(fn, q, k_cache, v_cache, scales, block_tables, context_lens, selected, out, scale, workspace, dtype,
+            err_flag, stream):
+    b, hq, d = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    if tuple(selected.shape[:2]) != (b, hkv):
+        raise ValueError("selected must be [batch, num_kv_heads, budget]")
+    _check(fn, getattr(lib, fn)(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_tables), _ptr(context_lens), _ptr(selected),
+        selected.shape[2], b, hq, hkv, d, bs, block_tables.shape[1], nb, scale, _ptr(out), _dtype_code(q, dtype),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+
+
+def pkv_paged_decode_attention_sparse(q, k_cache, v_cache, block_tables, context_lens, selected, out, *,
+                                      scale: float, workspace, dtype=None, err_flag=None, stream=None) -> None:
+    """Decode attention over the blocks that selected [B, Hkv, budget] lists."""
+    _sparse("pkv_paged_decode_attention_sparse", q, k_cache, v_cache, (), block_tables, context_lens, selected, out,
+            scale, workspace, dtype, err_flag, stream)
+
+
+def pkv_paged_decode_attention_sparse_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected,
+                                          out, *, scale: float, workspace, q_dtype=None, err_flag=None,
+                                          stream=None) -> None:
+    _sparse("pkv_paged_decode_attention_sparse_fp8", q, k_cache, v_cache, (_ptr(k_scale), _ptr(v_scale)), block_tables,
+            context_lens, selected, out, scale, workspace, q_dtype, err_flag, stream)
+
+
+def pkv_paged_decode_attention_sparse_e5m2(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                                           selected, out, *, scale: float, workspace, q_dtype=None, err_flag=None,
+                                           stream=None) -> None:
+    _sparse("pkv_paged_decode_attention_sparse_e5m2", q, k_cache, v_cache, (_ptr(k_scale), _ptr(v_scale)),
+            block_tables, context_lens, selected, out, scale, workspace, q_dtype, err_flag, stream)
 
 
 def pkv_blocks_needed(num_tokens: int, block_size: int = 16) -> int:

@@ -121,7 +121,8 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
                          pkv_dtype dtype, int partition_tokens, void* workspace, size_t workspace_bytes,
                          int32_t* err_flag, void* stream, const void* k_new = nullptr, const void* v_new = nullptr,
                          int64_t* slots_out = nullptr, int num_layers = 1, int layer = 0,
-                         const void* slab_params = nullptr, bool wait_first = false) {
+                         const void* slab_params = nullptr, bool wait_first = false,
+                         const int32_t* selected = nullptr, int budget = 0) {
   // kv_kind: 0 = 16-bit cache, 1 = E4M3 with per-head scales, 2 = INT8 with
   // per-(block, head) min-max parameters, 3 = E5M2 with per-head scales
   const bool fp8 = kv_kind == 1 || kv_kind == 3, int8 = kv_kind == 2;
@@ -154,7 +155,10 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
 
   if (int8 && (!slab_params || (reinterpret_cast<uintptr_t>(slab_params) & 15u) || k_new != nullptr))
     return PKV_ERR_INVALID_ARG;
-  DecodeLauncher launch = int8 ? decode_launcher_int8(dtype, head_dim, group)
+  DecodeLauncher launch = selected != nullptr && !int8
+                              ? (fp8 ? decode_launcher_listed_fp8(kv_kind, dtype, head_dim, group)
+                                     : decode_launcher_listed_16(dtype, head_dim, group))
+                        : int8 ? decode_launcher_int8(dtype, head_dim, group)
                         : kv_kind == 3 ? decode_launcher_e5m2(dtype, head_dim, group)
                         : fp8 ? decode_launcher_e4m3(dtype, head_dim, group)
                               : (dtype == PKV_F16 ? decode_launcher_f16(head_dim, group)
@@ -192,6 +196,8 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   p.n_kv_heads = n_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.max_nblk = (max_context_len + kBlockSize - 1) / kBlockSize;
+  p.selected = selected;
+  p.budget = budget;
   p.part_blocks = partition_tokens / kBlockSize;
   // (-1: the launched variant's default cost per (sequence, KV head))
   p.unit_cost = std::max(-1, std::min(1 << 16, env_int("PKV_UNIT_COST", -1)));
@@ -390,6 +396,54 @@ extern "C" pkv_status pkv_paged_decode_step_layer(const void* q, const void* k_n
                        num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
                        max_context_len, scale, out, dtype, partition_tokens, workspace, workspace_bytes, err_flag,
                        stream, k_new, v_new, slot_mapping_out, num_layers, layer);
+}
+
+// Decode over listed blocks: the work of a (sequence, KV head) is bounded by
+// its list, so the split and the combine take budget blocks as the bound.
+static pkv_status sparse_common(int kv_kind, const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                const int32_t* context_lens, const int32_t* selected, int budget, int batch,
+                                int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                int max_blocks_per_seq, int64_t num_blocks, float scale, void* out, pkv_dtype q_dtype,
+                                void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  if (budget <= 0 || budget > INT32_MAX / kBlockSize || (batch > 0 && selected == nullptr))
+    return PKV_ERR_INVALID_ARG;
+  return decode_common(kv_kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, batch,
+                       num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                       budget * kBlockSize, scale, out, q_dtype, 0, workspace, workspace_bytes, err_flag, stream,
+                       nullptr, nullptr, nullptr, 1, 0, nullptr, false, selected, budget);
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_sparse(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+    const int32_t* selected, int budget, int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int max_blocks_per_seq, int64_t num_blocks, float scale, void* out, pkv_dtype dtype, void* workspace,
+    size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  return sparse_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, selected, budget, batch,
+                       num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale, out,
+                       dtype, workspace, workspace_bytes, err_flag, stream);
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_sparse_fp8(
+    const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* block_tables, const int32_t* context_lens, const int32_t* selected, int budget, int batch,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    float scale, void* out, pkv_dtype q_dtype, void* workspace, size_t workspace_bytes, int32_t* err_flag,
+    void* stream) {
+  return sparse_common(1, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, budget, batch,
+                       num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale, out,
+                       q_dtype, workspace, workspace_bytes, err_flag, stream);
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_sparse_e5m2(
+    const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* block_tables, const int32_t* context_lens, const int32_t* selected, int budget, int batch,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+    float scale, void* out, pkv_dtype q_dtype, void* workspace, size_t workspace_bytes, int32_t* err_flag,
+    void* stream) {
+  return sparse_common(3, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, budget, batch,
+                       num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale, out,
+                       q_dtype, workspace, workspace_bytes, err_flag, stream);
 }
 
 // One decode step over every layer of a layer-major cache, captured once into

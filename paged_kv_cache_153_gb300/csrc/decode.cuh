@@ -56,6 +56,16 @@
 // the previous kernel, and the consumer of the last block of every (sequence,
 // KV head) overwrites that row of its staged block with the new row, so no
 // block of the grid depends on another's write.
+//
+// Source of a sequence's blocks (template parameter SRC).  kWhole: its whole
+// context, as above.  kListed: per (sequence, KV head) a list of logical
+// blocks ([B, Hkv, budget]; the first min(blocks of b, budget) entries count,
+// negative ones are skipped), so every head of a sequence still has the same
+// number of blocks and the split is unchanged; the producer looks a block up
+// in the list and then in the table, and hands its valid rows to the consumer
+// with the stage.  kRest: the blocks behind a prefix that the sequence's group
+// shares, attended to elsewhere; a (sequence, KV head) held by one range is
+// left as an fp32 state too, for the merge with the prefix's.
 #pragma once
 
 #include <cuda.h>
@@ -102,10 +112,19 @@ struct DecodeParams {
   float qk_scale_log2;           // softmax scale * log2(e)
   unsigned long long wait_limit_ns;   // limit of each pipeline wait (kWaitLimitNs unless overridden)
   int combine_early;             // 1: the combine releases the next launch at its start (else after its wait)
+  const int32_t* selected;       // kListed: [B, Hkv, budget] logical blocks
+  int budget;
+  const int32_t* group_starts;   // kRest: [num_groups + 1] first sequence of each group
+  const int32_t* prefix_lens;    // kRest: [num_groups] tokens each group shares
+  int num_groups;
+  float* rest_ml;                // kRest: [B, Hq, 2] (m, l) and
+  float* rest_o;                 // [B, Hq, D] o of pairs that one range holds
   int wait_first;                // 1: the previous kernel (the INT8 step's append) writes the last block of
                                  // every (sequence, KV head): the producer waits for it before it loads such a
                                  // block, the consumers before their first global write
 };
+
+enum Source { kWhole = 0, kListed = 1, kRest = 2 };
 
 struct SegDesc {
   int b, g, i0, i1;              // logical blocks [i0, i1) of (b, g)
@@ -121,21 +140,34 @@ struct ProdSeg {
   int slot;                      // as SegDesc::slot
   int64_t r;                     // its range
   int64_t f_end, f_hi;           // flat end of the segment and of its range
+  int skip;                      // kRest: blocks of the shared prefix, ahead of logical block 0
 };
 
-// number of blocks of sequence b after clamping to the table and the bound
-__device__ __forceinline__ int seq_blocks(const DecodeParams& p, int ctx, int32_t* err) {
+// number of blocks of sequence b after clamping to cap: the table and the
+// bound (a list's length bounds the work instead: the table alone)
+__device__ __forceinline__ int seq_blocks(int cap, int ctx, int32_t* err) {
   if (ctx < 0) {
     record_error(err, PKV_ERR_OOB);
     return 0;
   }
   int nb = (ctx + kBlockSize - 1) / kBlockSize;
-  const int cap = min(p.max_blocks_per_seq, p.max_nblk);
   if (nb > cap) {
     record_error(err, PKV_ERR_OOB);
     nb = cap;
   }
   return nb;
+}
+
+// whole blocks of the prefix that sequence b shares with its group (0 outside
+// every group): the group is the last one that starts at or before b
+__device__ __forceinline__ int shared_blocks(const int32_t* starts, const int32_t* prefix_lens, int num_groups, int b) {
+  int lo = 0, hi = num_groups;   // smallest j with starts[j] > b
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] > b) hi = mid; else lo = mid + 1;
+  }
+  if (lo == 0 || starts[lo] <= b) return 0;
+  return max(prefix_lens[lo - 1], 0) / kBlockSize;
 }
 
 // Partition mode: the flat space of W blocks is cut into NP = ceil(W / P)
@@ -384,7 +416,7 @@ __device__ __noinline__ void clear_rows(uint32_t vslab, int r0, int lane) {
 // ---------------------------------------------------------------------------
 // the decode kernel
 // ---------------------------------------------------------------------------
-template <typename QT, typename KV, int D, int G, int NW, bool MMA>
+template <typename QT, typename KV, int D, int G, int NW, bool MMA, Source SRC>
 __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<D, G, NW, KV, MMA>;
   extern __shared__ unsigned char smem_raw[];
@@ -450,8 +482,14 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
     int nb = 0;
     if (b < p.batch) {
       const int ctx = p.context_lens[b];
-      nb = seq_blocks(p, ctx, p.err);
+      nb = seq_blocks(SRC == kListed ? p.max_blocks_per_seq : min(p.max_blocks_per_seq, p.max_nblk), ctx, p.err);
       ntok[b] = min(max(ctx, 0), nb * kBlockSize);
+      if constexpr (SRC == kListed) nb = min(nb, p.budget);
+      if constexpr (SRC == kRest) {
+        const int skip = min(nb, shared_blocks(p.group_starts, p.prefix_lens, p.num_groups, b));
+        nb -= skip;
+        ntok[b] = max(ntok[b] - skip * kBlockSize, 0);
+      }
     }
     int x = nb, y = nb > 0 ? 1 : 0;   // inclusive block-wide scans: blocks, non-empty sequences
 #pragma unroll
@@ -623,6 +661,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
       sg.i1 = sg.i0 + static_cast<int>(sg.f_end - f);
       sg.r = r;
       sg.f_hi = f_hi;
+      sg.skip = 0;
+      if constexpr (SRC == kRest) sg.skip = shared_blocks(p.group_starts, p.prefix_lens, p.num_groups, lo);
       sg.slot = -1;
       if (!(sg.i0 == 0 && sg.i1 == sg.nb)) {
         const int64_t sl = (f == f_lo) ? 2 * r : 2 * r + 1;
@@ -648,15 +688,30 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
       }
       return first_from(cur.r + r_step, sg);
     };
-    // table entry i0 + w + lane of a segment (0 past its end)
-    auto table_at = [&](const ProdSeg& sg, int w) -> int {
-      return (sg.i0 + w + lane < sg.i1)
-                 ? p.block_tables[static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + sg.i0 + w + lane]
-                 : 0;
+    // table entry i0 + w + lane of a segment (0 past its end); rows: for a
+    // listed block, its valid rows (0 with id kSkip: an entry that is skipped)
+    constexpr int kSkip = INT32_MIN;
+    auto table_at = [&](const ProdSeg& sg, int w, int& rows) -> int {
+      rows = 0;
+      if (sg.i0 + w + lane >= sg.i1) return 0;
+      const int32_t* row = p.block_tables + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + sg.skip;
+      if constexpr (SRC == kListed) {
+        const int i = p.selected[(static_cast<int64_t>(sg.b) * Hkv + sg.g) * p.budget + sg.i0 + w + lane];
+        if (i < 0) return kSkip;
+        if (i >= (ntok[sg.b] + kBlockSize - 1) / kBlockSize) {   // behind the context
+          record_error(p.err, PKV_ERR_OOB);
+          return kSkip;
+        }
+        rows = min(kBlockSize, ntok[sg.b] - i * kBlockSize);
+        return row[i];
+      }
+      return row[sg.i0 + w + lane];
     };
+    if constexpr (SRC == kListed) pdl_wait();   // (the lists may be the previous kernel's)
     ProdSeg cur;
     bool have = first_from(blockIdx.x, cur);
-    int ids = have ? table_at(cur, 0) : 0;
+    int rows = 0;
+    int ids = have ? table_at(cur, 0, rows) : 0;
     // Stopping.  A wait that runs out, or an abort raised by a consumer, stops
     // the producer: every decision to stop is a vote of the whole warp, and
     // after it no barrier receives another arrival (a stage or query slot
@@ -703,7 +758,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
       const int nseg = cur.i1 - cur.i0;
       bool stop = false;
       for (int w0 = 0; w0 < nseg && !stop; w0 += 32) {
-        const int nxt_ids = (w0 + 32 < nseg) ? table_at(cur, w0 + 32) : (have_nxt ? table_at(nxt, 0) : 0);
+        int nxt_rows = 0;
+        const int nxt_ids =
+            (w0 + 32 < nseg) ? table_at(cur, w0 + 32, nxt_rows) : (have_nxt ? table_at(nxt, 0, nxt_rows) : 0);
         const int cnt = min(32, nseg - w0);
         // INT8: each lane loads its block's (k_min, k_max, v_min, v_max) now,
         // while the window is issued, and stores them into the stage itself
@@ -732,7 +789,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
               *abort_flag = 1;                                   // the stage is left as it is
             } else {
               const bool ok = ids >= 0 && ids < p.num_blocks;
-              stage_ok[s] = ok ? 1 : 0;
+              stage_ok[s] = !ok ? 0 : SRC == kListed ? rows : 1;
               issued[s] = static_cast<int>(use);
               unsigned char* dst = ring + static_cast<size_t>(s) * T::kStage;
               if (ok) {
@@ -759,8 +816,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
                   bulk_g2s(dst + T::kSlab, vbase + slab, T::kSlab, &full_bar[s], pol_stream);
                 }
               } else {
-                // an id outside the pool: the stage's phase completes with no data
-                record_error(p.err, PKV_ERR_OOB);
+                // an id outside the pool (or a skipped entry): the stage's phase
+                // completes with no data
+                if (SRC != kListed || ids != kSkip) record_error(p.err, PKV_ERR_OOB);
                 mbar_arrive(&full_bar[s]);
               }
             }
@@ -771,6 +829,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
         }
         k += cnt;
         ids = nxt_ids;
+        rows = nxt_rows;
       }
       cur = nxt;
       have = have_nxt;
@@ -907,7 +966,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
           break;
         }
         const int i = d.i0 + ii;
-        const int n_valid = stage_ok[s] ? min(kBlockSize, d.n_tokens - i * kBlockSize) : 0;
+        const int n_valid =
+            SRC == kListed ? stage_ok[s] : stage_ok[s] ? min(kBlockSize, d.n_tokens - i * kBlockSize) : 0;
         const uint32_t kslab = smem_u32(ring + static_cast<size_t>(s) * T::kStage);
         const uint32_t vslab = kslab + T::kSlab;
         if (ii == patch_ii && n_valid > 0) {
@@ -919,7 +979,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
         }
         // (INT8 codes are finite: a zero p needs no cleared row)
         if constexpr (!kInt8)
-          if (n_valid > 0 && n_valid < kBlockSize) clear_rows<D, T::kEsz, true>(vslab, n_valid, lane);
+          if ((SRC == kListed || n_valid > 0) && n_valid < kBlockSize) clear_rows<D, T::kEsz, true>(vslab, n_valid, lane);
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         if constexpr (kFp8) {
 #pragma unroll
@@ -1168,7 +1228,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
           break;
         }
         const int i = d.i0 + ii;
-        const int n_valid = stage_ok[s] ? min(kBlockSize, d.n_tokens - i * kBlockSize) : 0;
+        const int n_valid =
+            SRC == kListed ? stage_ok[s] : stage_ok[s] ? min(kBlockSize, d.n_tokens - i * kBlockSize) : 0;
         const unsigned char* kslab = ring + static_cast<size_t>(s) * T::kStage;
         const unsigned char* vslab = kslab + T::kSlab;
         if (ii == patch_ii && n_valid > 0) {
@@ -1179,7 +1240,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
                                                scales[Hkv + d.g], lane);
         }
         if constexpr (!kInt8)   // (INT8 codes are finite: a zero p needs no cleared row)
-          if (n_valid > 0 && n_valid < kBlockSize) clear_rows<D, T::kEsz, false>(smem_u32(vslab), n_valid, lane);
+          if ((SRC == kListed || n_valid > 0) && n_valid < kBlockSize) clear_rows<D, T::kEsz, false>(smem_u32(vslab), n_valid, lane);
 
         // ---- scores: partial dot products over this lane's 8 elements ----
         float part[T::kNV];
@@ -1349,7 +1410,11 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
         O += wgt * m2[h * D + e];
       }
       O *= vscale;
-      if (d.slot == -1) {
+      if (SRC == kRest && d.slot == -1) {
+        const int64_t row = static_cast<int64_t>(d.b) * p.n_q_heads + d.g * G + h;
+        p.rest_o[row * D + e] = O;
+        if (e == 0) *reinterpret_cast<float2*>(p.rest_ml + row * 2) = make_float2(M, L);
+      } else if (d.slot == -1) {
         const float r = (L > 0.f) ? O / L : 0.f;
         auto* o = static_cast<typename QT::storage*>(p.out);
         o[(static_cast<int64_t>(d.b) * p.n_q_heads + d.g * G + h) * D + e] = to_out(r, QT{});

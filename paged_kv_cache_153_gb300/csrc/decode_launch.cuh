@@ -26,10 +26,10 @@ constexpr int kSmemPerSm = 233472;        // shared memory per SM on sm_100-clas
 constexpr int kSmemReservedPerCta = 1024; // system-reserved shared memory per resident block
 constexpr int kMaxStagesPerWarp = 8;
 
-template <typename QT, typename KV, int D, int G, int NW, bool MMA>
+template <typename QT, typename KV, int D, int G, int NW, bool MMA, Source SRC>
 pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t stream) {
   using Tr = DecodeTraits<D, G, NW, KV, MMA>;
-  auto kern = paged_decode_kernel<QT, KV, D, G, NW, MMA>;
+  auto kern = paged_decode_kernel<QT, KV, D, G, NW, MMA, SRC>;
   int max_optin = 0, dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
   if (cuda_failed(cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev),
@@ -124,7 +124,8 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   // against 77); a grid smaller than the GPU has no tail to overlap (4 short
   // sequences: 9.65 us against 9.28).  There the combine releases after its
   // wait.
-  p.combine_early = (occ <= 2 && grid == li.num_sms * occ) ? 1 : 0;
+  // (kRest: the merge that follows reads the shared prefix's states as well)
+  p.combine_early = (SRC != kRest && occ <= 2 && grid == li.num_sms * occ) ? 1 : 0;
   li.grid = grid;
   li.stages = stages;
   if constexpr (MMA) {
@@ -138,7 +139,7 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   if (cuda_failed(launch_pdl(kern, dim3(grid), dim3(Tr::kThreads), smem, stream, p), "paged_decode_kernel launch"))
     return PKV_ERR_CUDA;
   const int units = p.batch * p.n_kv_heads;
-  if (units > 0) {
+  if (SRC != kRest && units > 0) {
     // a partition split of long contexts can leave many pieces per (sequence,
     // KV head) (one per range it meets): merge those with several lanes per output
     const bool wide = p.part_blocks > 0 && (p.max_nblk + p.part_blocks - 1) / p.part_blocks >= 16;
@@ -159,6 +160,9 @@ DecodeLauncher decode_launcher_bf16(int head_dim, int group);
 DecodeLauncher decode_launcher_e4m3(int q_dtype, int head_dim, int group);
 DecodeLauncher decode_launcher_e5m2(int q_dtype, int head_dim, int group);
 DecodeLauncher decode_launcher_int8(int q_dtype, int head_dim, int group);
+// blocks from lists (kv as decode_common's kv_kind: 0 = q's 16-bit type, 1 = E4M3, 3 = E5M2)
+DecodeLauncher decode_launcher_listed_16(int q_dtype, int head_dim, int group);
+DecodeLauncher decode_launcher_listed_fp8(int kv_kind, int q_dtype, int head_dim, int group);
 
 constexpr int kCoreWarps = 8;   // consumer warps of the CUDA-core variant
 constexpr int kMmaWarps = 4;    // consumer warps of the tensor-core variant
@@ -167,31 +171,31 @@ constexpr int kMmaWarps = 4;    // consumer warps of the tensor-core variant
 // one-byte (E4M3, E5M2 or INT8) cache with 128-byte rows, uses the tensor-core
 // consumer (the q-group times a 16-token block is an MMA tile), and so does
 // an INT8 cache with 128-byte rows at G = 1.
-template <typename QT, typename KV, int D, int G>
+template <typename QT, typename KV, int D, int G, Source SRC>
 DecodeLauncher pick_variant() {
   // (an INT8 cache with 128-byte rows takes the tensor-core consumer for every
   // group size: its V slabs are stored transposed for that consumer)
   if constexpr ((G >= 2 || std::is_same<KV, U8>::value) && (KV::kBytes == 2 || D * KV::kBytes == 128))
-    return launch_decode_variant<QT, KV, D, G, kMmaWarps, true>;
+    return launch_decode_variant<QT, KV, D, G, kMmaWarps, true, SRC>;
   else
-    return launch_decode_variant<QT, KV, D, G, kCoreWarps, false>;
+    return launch_decode_variant<QT, KV, D, G, kCoreWarps, false, SRC>;
 }
 
-template <typename QT, typename KV, int D>
+template <typename QT, typename KV, int D, Source SRC>
 DecodeLauncher pick_group(int group) {
   switch (group) {
-    case 1: return pick_variant<QT, KV, D, 1>();
-    case 2: return pick_variant<QT, KV, D, 2>();
-    case 4: return pick_variant<QT, KV, D, 4>();
-    case 8: return pick_variant<QT, KV, D, 8>();
+    case 1: return pick_variant<QT, KV, D, 1, SRC>();
+    case 2: return pick_variant<QT, KV, D, 2, SRC>();
+    case 4: return pick_variant<QT, KV, D, 4, SRC>();
+    case 8: return pick_variant<QT, KV, D, 8, SRC>();
     default: return nullptr;
   }
 }
 
-template <typename QT, typename KV>
+template <typename QT, typename KV, Source SRC = kWhole>
 DecodeLauncher pick_dim_group(int head_dim, int group) {
-  if (head_dim == 64) return pick_group<QT, KV, 64>(group);
-  if (head_dim == 128) return pick_group<QT, KV, 128>(group);
+  if (head_dim == 64) return pick_group<QT, KV, 64, SRC>(group);
+  if (head_dim == 128) return pick_group<QT, KV, 128, SRC>(group);
   return nullptr;
 }
 
