@@ -79,9 +79,10 @@ KERNEL_SOURCES = {
     "decode": _COMMON_SOURCES + _DECODE_SOURCES,
     "int8": _COMMON_SOURCES + _DECODE_SOURCES + ("append.cu", "append_int8.cu"),
     "cow": _COMMON_SOURCES + ("append.cu",),
-    "prefill": _COMMON_SOURCES + ("prefill.cu",),
+    "prefill": _COMMON_SOURCES + ("prefill.cu", "tcgen05.cuh"),
     "rope": _COMMON_SOURCES + ("rope.cu",),
     "sparse": _COMMON_SOURCES + _DECODE_SOURCES + ("block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu"),
+    "prefix_decode": _COMMON_SOURCES + _DECODE_SOURCES + ("decode_rest.cu", "prefix.h", "prefix.cu", "tcgen05.cuh"),
 }
 
 

@@ -598,6 +598,42 @@ pkv_status pkv_paged_decode_attention_sparse_e5m2(const void* q, const uint8_t* 
                                                   int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Decode attention for sequences that share a prefix ("Series 03 ...", section
+ * 3.3: shared prompts keep one copy of their blocks): the result of
+ * pkv_paged_decode_attention, with the prefix's K and V read once per group
+ * and KV head instead of once per sequence.  The sequences are cut into
+ * consecutive groups, group j being sequences group_starts[j] ..
+ * group_starts[j + 1] - 1 (group_starts[0] = 0, group_starts[num_groups] =
+ * batch; a group may be empty or a single sequence), and the first
+ * prefix_lens[j] / 16 (rounded down) entries of their block table rows are the
+ * same ids; the remaining tokens are each sequence's own.  A sequence shorter
+ * than its group's whole shared blocks is attended to through its own row
+ * alone (so a padding sequence of length 0 gives 0 and its row is not read);
+ * the prefix is read through the row of the first sequence that covers it.
+ *   group_starts, prefix_lens   device int32 [num_groups + 1], [num_groups].
+ *   max_prefix_len              an upper bound of prefix_lens; it sizes the
+ *                               launch only.
+ *   scale                       > 0.
+ *   workspace                   at least pkv_prefix_workspace_bytes(...), no
+ *                               initialisation needed; not shared by calls
+ *                               that run at the same time.
+ * 16-bit caches; at most 1024 groups (PKV_ERR_UNSUPPORTED beyond).  Group
+ * starts that are not as described report PKV_ERR_OOB in err_flag, and the
+ * outputs are then unspecified.  Other arguments, requirements and errors as
+ * in pkv_paged_decode_attention.
+ * ------------------------------------------------------------------------- */
+size_t pkv_prefix_workspace_bytes(int batch, int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                  int max_blocks_per_seq, int max_context_len, int max_prefix_len);
+pkv_status pkv_paged_decode_attention_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens,
+                                             const int32_t* group_starts, const int32_t* prefix_lens,
+                                             int num_groups, int batch, int num_q_heads, int num_kv_heads,
+                                             int head_dim, int block_size, int max_blocks_per_seq,
+                                             int64_t num_blocks, int max_context_len, int max_prefix_len,
+                                             float scale, void* out, pkv_dtype dtype, void* workspace,
+                                             size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Host-side block pool ("Series 03 ...", sections 3.2-3.3; "What a KV cache
  * is ...", section 3.2): a preallocated set of block ids handed out on demand,
  * with reference counts for blocks shared by several block tables.  Policy: a

@@ -31,6 +31,7 @@ __all__ = [
     "pkv_kv_block_bounds", "pkv_kv_block_bounds_fp8", "pkv_kv_block_bounds_e5m2", "pkv_block_scores",
     "pkv_select_blocks", "pkv_paged_decode_attention_sparse", "pkv_paged_decode_attention_sparse_fp8",
     "pkv_paged_decode_attention_sparse_e5m2",
+    "pkv_prefix_workspace_bytes", "pkv_paged_decode_attention_prefix",
 ]
 
 PKV_F16 = 0
@@ -123,6 +124,9 @@ _SIGS = {
                                                    _f, _p, _i, _p, _sz, _p, _p]),
     "pkv_paged_decode_attention_sparse_e5m2": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64,
                                                     _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "pkv_paged_decode_attention_prefix": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _i, _i,
+                                               _f, _p, _i, _p, _sz, _p, _p]),
     "pkv_rope_plan": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, C.POINTER(_f)]),
     "pkv_rope_append": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i, _i, _f, _p, _i64, _p, _p, _i64,
                              _i, _i, _i, _i, _i, _p, _p]),
@@ -632,6 +636,32 @@ def pkv_paged_decode_attention_sparse_e5m2(q, k_cache, v_cache, k_scale, v_scale
                                            stream=None) -> None:
     _sparse("pkv_paged_decode_attention_sparse_e5m2", q, k_cache, v_cache, (_ptr(k_scale), _ptr(v_scale)),
             block_tables, context_lens, selected, out, scale, workspace, q_dtype, err_flag, stream)
+
+
+def pkv_prefix_workspace_bytes(batch: int, num_groups: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                               max_blocks_per_seq: int, max_context_len: int, max_prefix_len: int) -> int:
+    n = lib.pkv_prefix_workspace_bytes(batch, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                       max_context_len, max_prefix_len)
+    if n == 0:
+        raise PkvError("pkv_prefix_workspace_bytes", 1)
+    return n
+
+
+def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, out,
+                                      *, scale: float, max_context_len: int, max_prefix_len: int, workspace,
+                                      dtype=None, err_flag=None, stream=None) -> None:
+    """Decode attention of sequences that share prefixes: group j, sequences
+    group_starts[j] .. group_starts[j + 1] - 1, shares its first
+    prefix_lens[j] tokens' whole blocks."""
+    b, hq, d = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    if group_starts.numel() != prefix_lens.numel() + 1:
+        raise ValueError("group_starts must have one entry more than prefix_lens")
+    _check("pkv_paged_decode_attention_prefix", lib.pkv_paged_decode_attention_prefix(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(group_starts),
+        _ptr(prefix_lens), prefix_lens.numel(), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len,
+        max_prefix_len, scale, _ptr(out), _dtype_code(q, dtype), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
 
 
 def pkv_blocks_needed(num_tokens: int, block_size: int = 16) -> int:

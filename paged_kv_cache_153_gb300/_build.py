@@ -26,7 +26,7 @@ PREFILL_LIB_PATH = os.path.join(PKG_DIR, "libpkv_prefill.so")
 
 CUDA_SOURCES = ["append.cu", "api.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e4m3.cu", "decode_e5m2.cu",
                 "noalloc.cu", "decode_int8.cu", "append_int8.cu", "rope.cu",
-                "block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu"]
+                "block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu", "decode_rest.cu", "prefix.cu"]
 PREFILL_SOURCES = ["prefill.cu"]
 CXX_SOURCES = ["pool.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -9,6 +9,7 @@
 
 #include "decode_launch.cuh"
 #include "host_util.h"
+#include "prefix.h"
 
 #include <cudaTypedefs.h>
 
@@ -114,6 +115,18 @@ bool ws_layout(int batch, int n_kv_heads, int group, int head_dim, int max_block
   return true;
 }
 
+// the decode over what lies behind shared prefixes: its extra inputs, and what
+// the merge that follows needs of the launch
+struct RestCall {
+  const int32_t* group_starts;
+  const int32_t* prefix_lens;
+  int num_groups;
+  float* ml;
+  float* o;
+  DecodeParams params;   // out
+  int grid;              // out
+};
+
 pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                          const float* v_scale, const int32_t* block_tables, const int32_t* context_lens,
                          int batch, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
@@ -122,7 +135,7 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
                          int32_t* err_flag, void* stream, const void* k_new = nullptr, const void* v_new = nullptr,
                          int64_t* slots_out = nullptr, int num_layers = 1, int layer = 0,
                          const void* slab_params = nullptr, bool wait_first = false,
-                         const int32_t* selected = nullptr, int budget = 0) {
+                         const int32_t* selected = nullptr, int budget = 0, RestCall* rest = nullptr) {
   // kv_kind: 0 = 16-bit cache, 1 = E4M3 with per-head scales, 2 = INT8 with
   // per-(block, head) min-max parameters, 3 = E5M2 with per-head scales
   const bool fp8 = kv_kind == 1 || kv_kind == 3, int8 = kv_kind == 2;
@@ -155,7 +168,8 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
 
   if (int8 && (!slab_params || (reinterpret_cast<uintptr_t>(slab_params) & 15u) || k_new != nullptr))
     return PKV_ERR_INVALID_ARG;
-  DecodeLauncher launch = selected != nullptr && !int8
+  DecodeLauncher launch = rest != nullptr ? decode_launcher_rest(dtype, head_dim, group)
+                        : selected != nullptr && !int8
                               ? (fp8 ? decode_launcher_listed_fp8(kv_kind, dtype, head_dim, group)
                                      : decode_launcher_listed_16(dtype, head_dim, group))
                         : int8 ? decode_launcher_int8(dtype, head_dim, group)
@@ -198,6 +212,13 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   p.max_nblk = (max_context_len + kBlockSize - 1) / kBlockSize;
   p.selected = selected;
   p.budget = budget;
+  if (rest != nullptr) {
+    p.group_starts = rest->group_starts;
+    p.prefix_lens = rest->prefix_lens;
+    p.num_groups = rest->num_groups;
+    p.rest_ml = rest->ml;
+    p.rest_o = rest->o;
+  }
   p.part_blocks = partition_tokens / kBlockSize;
   // (-1: the launched variant's default cost per (sequence, KV head))
   p.unit_cost = std::max(-1, std::min(1 << 16, env_int("PKV_UNIT_COST", -1)));
@@ -217,7 +238,49 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   li.max_ctas_per_sm = std::max(0, std::min(kMaxCtasPerSm, env_int("PKV_CTAS_PER_SM", 0)));
   li.stages = env_int("PKV_STAGES", 0);
   li.part_ranges_cap = w.ranges_cap;
-  return launch(p, li, static_cast<cudaStream_t>(stream));
+  const pkv_status st = launch(p, li, static_cast<cudaStream_t>(stream));
+  if (rest != nullptr) {
+    rest->params = p;
+    rest->grid = li.grid;
+  }
+  return st;
+}
+
+// Workspace of the shared-prefix decode: the decode's own | [B, Hq, 2] and
+// [B, Hq, D] fp32 states of its single-range pairs | the groups' geometry |
+// [rows, 2] and [rows, D] fp32 states of the prefix's pieces (stored 32 bytes
+// at a time), from a 256-byte boundary of the caller's workspace on.
+struct PrefixWs {
+  WsLayout decode;
+  size_t rest_ml, rest_o, groups, ml, o, total;
+};
+
+bool prefix_ws(int batch, int num_groups, int n_q_heads, int n_kv_heads, int head_dim, int max_blocks_per_seq,
+               int max_context_len, int num_sms, PrefixWs* w) {
+  if (!ws_layout(batch, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_blocks_per_seq, max_context_len, 0, num_sms,
+                 &w->decode))
+    return false;
+  const size_t heads = static_cast<size_t>(batch) * n_q_heads;
+  const size_t rows = heads + static_cast<size_t>(kPrefixUnitRows) * num_sms;
+  size_t at = round256(w->decode.total);
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += round256(n);
+    return here;
+  };
+  w->rest_ml = take(heads * 2 * sizeof(float));
+  w->rest_o = take(heads * head_dim * sizeof(float));
+  w->groups = take((static_cast<size_t>(num_groups) + 1) * sizeof(PrefixGroup));
+  w->ml = take(rows * 2 * sizeof(float));
+  w->o = take(rows * head_dim * sizeof(float));
+  w->total = at + 256;
+  return true;
+}
+
+bool prefix_shape_ok(int batch, int num_groups, int num_q_heads, int num_kv_heads, int max_blocks_per_seq,
+                     int max_context_len, int max_prefix_len) {
+  return batch >= 0 && num_groups >= 0 && num_q_heads > 0 && num_kv_heads > 0 && num_q_heads % num_kv_heads == 0 &&
+         max_blocks_per_seq > 0 && max_context_len >= 0 && max_prefix_len >= 0;
 }
 
 }  // namespace
@@ -444,6 +507,95 @@ extern "C" pkv_status pkv_paged_decode_attention_sparse_e5m2(
   return sparse_common(3, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, budget, batch,
                        num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale, out,
                        q_dtype, workspace, workspace_bytes, err_flag, stream);
+}
+
+extern "C" size_t pkv_prefix_workspace_bytes(int batch, int num_groups, int num_q_heads, int num_kv_heads,
+                                             int head_dim, int max_blocks_per_seq, int max_context_len,
+                                             int max_prefix_len) {
+  if (!prefix_shape_ok(batch, num_groups, num_q_heads, num_kv_heads, max_blocks_per_seq, max_context_len,
+                       max_prefix_len))
+    return 0;
+  const int num_sms = sm_count();
+  PrefixWs w;
+  if (num_sms <= 0 || !prefix_ws(batch, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                 max_context_len, num_sms, &w))
+    return 0;
+  return w.total;
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_prefix(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+    const int32_t* group_starts, const int32_t* prefix_lens, int num_groups, int batch, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks, int max_context_len,
+    int max_prefix_len, float scale, void* out, pkv_dtype dtype, void* workspace, size_t workspace_bytes,
+    int32_t* err_flag, void* stream) {
+  if (!prefix_shape_ok(batch, num_groups, num_q_heads, num_kv_heads, max_blocks_per_seq, max_context_len,
+                       max_prefix_len) ||
+      num_blocks < 0 || !std::isfinite(scale) || scale <= 0.f)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+  const int group = num_q_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
+  if (num_groups > kMaxPrefixGroups) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if (num_groups == 0 || !q || !k_cache || !v_cache || !block_tables || !context_lens || !group_starts ||
+      !prefix_lens || !out || !workspace)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace))
+    return PKV_ERR_INVALID_ARG;
+  const int num_sms = sm_count();
+  if (num_sms <= 0) return PKV_ERR_CUDA;
+  PrefixWs w;
+  if (!prefix_ws(batch, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, max_context_len, num_sms,
+                 &w))
+    return PKV_ERR_INVALID_ARG;
+  if (workspace_bytes < w.total) return PKV_ERR_WORKSPACE;
+  const int64_t rows = num_blocks * num_kv_heads * kBlockSize;
+  if (rows > INT32_MAX) return PKV_ERR_UNSUPPORTED;   // TMA row coordinates are 32-bit
+  if (num_blocks == 0) return PKV_ERR_INVALID_ARG;
+  char* ws = reinterpret_cast<char*>(round256(reinterpret_cast<uintptr_t>(workspace)));
+  PrefixParams p{};
+  if (!encode_cache_tmap(&p.tmap_k, k_cache, rows, head_dim, 2) ||
+      !encode_cache_tmap(&p.tmap_v, v_cache, rows, head_dim, 2))
+    return PKV_ERR_CUDA;
+  p.q = q;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.group_starts = group_starts;
+  p.prefix_lens = prefix_lens;
+  p.groups = reinterpret_cast<PrefixGroup*>(ws + w.groups);
+  p.ml = reinterpret_cast<float*>(ws + w.ml);
+  p.o = reinterpret_cast<float*>(ws + w.o);
+  p.err = err_flag;
+  p.num_blocks = num_blocks;
+  p.batch = batch;
+  p.num_groups = num_groups;
+  p.n_q_heads = num_q_heads;
+  p.n_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_nblk = (max_context_len + kBlockSize - 1) / kBlockSize;
+  p.qk_scale_log2 = scale * kLog2e;
+  // as many ranges as SMs, but no more than there can be key tiles
+  const int64_t units = static_cast<int64_t>(num_kv_heads) *
+                        (num_groups + static_cast<int64_t>(batch) * group / kPrefixUnitRows);
+  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_prefix_len) + 127) / 128);
+  const int ranges = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(1, units * tiles)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  pkv_status st = launch_prefix(p, ranges, group, head_dim, dtype, s);
+  if (st != PKV_OK) return st;
+  RestCall rest{};
+  rest.group_starts = group_starts;
+  rest.prefix_lens = prefix_lens;
+  rest.num_groups = num_groups;
+  rest.ml = reinterpret_cast<float*>(ws + w.rest_ml);
+  rest.o = reinterpret_cast<float*>(ws + w.rest_o);
+  st = decode_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, batch, num_q_heads,
+                     num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len, scale, out,
+                     dtype, 0, ws, w.decode.total, err_flag, stream, nullptr, nullptr, nullptr, 1, 0, nullptr,
+                     false, nullptr, 0, &rest);
+  if (st != PKV_OK) return st;
+  return launch_prefix_merge(p, ranges, rest.params, rest.grid, group, head_dim, dtype, s);
 }
 
 // One decode step over every layer of a layer-major cache, captured once into

@@ -158,16 +158,24 @@ __device__ __forceinline__ int seq_blocks(int cap, int ctx, int32_t* err) {
   return nb;
 }
 
-// whole blocks of the prefix that sequence b shares with its group (0 outside
-// every group): the group is the last one that starts at or before b
-__device__ __forceinline__ int shared_blocks(const int32_t* starts, const int32_t* prefix_lens, int num_groups, int b) {
-  int lo = 0, hi = num_groups;   // smallest j with starts[j] > b
+// Does a sequence of ctx tokens take part in its group's prefix of `blocks`
+// whole blocks?  One that is shorter keeps to its own table (cap: the blocks
+// that a table and the length's bound allow).
+__device__ __forceinline__ bool shares_prefix(int blocks, int ctx, int cap) {
+  return blocks > 0 && blocks <= cap && blocks <= ctx / kBlockSize;
+}
+
+// blocks that sequence b takes from its group's prefix: the group is the last
+// one that starts at or before b (0 outside every group)
+__device__ __forceinline__ int prefix_blocks(const DecodeParams& p, int b) {
+  int lo = 0, hi = p.num_groups;   // smallest j with group_starts[j] > b
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (starts[mid] > b) hi = mid; else lo = mid + 1;
+    if (p.group_starts[mid] > b) hi = mid; else lo = mid + 1;
   }
-  if (lo == 0 || starts[lo] <= b) return 0;
-  return max(prefix_lens[lo - 1], 0) / kBlockSize;
+  if (lo == 0 || p.group_starts[lo] <= b) return 0;
+  const int blocks = max(p.prefix_lens[lo - 1], 0) / kBlockSize;
+  return shares_prefix(blocks, p.context_lens[b], min(p.max_blocks_per_seq, p.max_nblk)) ? blocks : 0;
 }
 
 // Partition mode: the flat space of W blocks is cut into NP = ceil(W / P)
@@ -486,9 +494,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
       ntok[b] = min(max(ctx, 0), nb * kBlockSize);
       if constexpr (SRC == kListed) nb = min(nb, p.budget);
       if constexpr (SRC == kRest) {
-        const int skip = min(nb, shared_blocks(p.group_starts, p.prefix_lens, p.num_groups, b));
+        const int skip = prefix_blocks(p, b);
         nb -= skip;
-        ntok[b] = max(ntok[b] - skip * kBlockSize, 0);
+        ntok[b] -= skip * kBlockSize;
       }
     }
     int x = nb, y = nb > 0 ? 1 : 0;   // inclusive block-wide scans: blocks, non-empty sequences
@@ -662,7 +670,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kerne
       sg.r = r;
       sg.f_hi = f_hi;
       sg.skip = 0;
-      if constexpr (SRC == kRest) sg.skip = shared_blocks(p.group_starts, p.prefix_lens, p.num_groups, lo);
+      if constexpr (SRC == kRest) sg.skip = prefix_blocks(p, lo);
       sg.slot = -1;
       if (!(sg.i0 == 0 && sg.i1 == sg.nb)) {
         const int64_t sl = (f == f_lo) ? 2 * r : 2 * r + 1;

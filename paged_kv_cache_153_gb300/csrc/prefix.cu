@@ -1,0 +1,709 @@
+// Decode attention over prefixes that sequences share, and the merge with each
+// sequence's own blocks (sm_103a).
+//
+// What is computed.  The sequences of a group hold the same blocks for their
+// first P tokens.  For every query head of them
+//   m = max_j s_j,  l = sum_j 2^(s_j - m),  o = sum_j 2^(s_j - m) V_j   (j < P)
+// with s_j = scale log2(e) <q, K_j>: the state of an online softmax, which the
+// merge joins with the state of the sequence's other blocks (the decode
+// kernel's kRest variant) into
+//   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+//
+// Why.  Read per sequence, the prefix costs n P rows of K and V; together, the
+// group's n G query rows of a KV head (G query heads per KV head) are one
+// matrix against it: P rows read once, and products that fill the tensor
+// cores.  Up to about 256 rows the reads bound it, beyond that the products.
+//
+// Work.  A unit is up to 256 query rows of one (group, KV head); its cost is
+// its number of 128-key tiles.  The units' costs lie on one axis, cut into
+// equal ranges, one per thread block; a range meets one or more units, and
+// each meeting leaves one fp32 state per row (a piece).
+//
+// Tiles.  Two chains of S = Q K^T -> softmax -> O += P V run at a time, each
+// with its own S / P columns, O columns and softmax warps, so that the tensor
+// cores work for one while the other's softmax runs:
+//   more than 128 rows   the chains are two row tiles against the same K / V
+//                        tiles, each tile loaded once for both;
+//   up to 128 rows       the chains are the even and the odd key tiles of one
+//                        row tile; their states are joined in registers.
+// K / V tiles are 8 cache blocks, gathered by TMA boxes of [16 rows x 128 B]
+// into 128-byte-swizzled K-major tiles, two stages each.  P overwrites its own
+// S in TMEM (32 columns of scores become 16 of P pairs, and for bf16 16 more
+// of the remainder); the product reads it from there.  bf16 P is multiplied as
+// two bf16 parts (p truncated, and the rounded remainder: exact to 2^-16),
+// because one bf16 rounding of p (2^-9) would be as large as the output's own;
+// fp16 P (2^-12) is used as it is.  The row reference m moves only when a
+// tile's maximum exceeds it by more than 2^8.
+//
+// Warps 0-3 and 4-7: softmax of chain 0 and 1, one thread per row; warp 8:
+// TMA producer; warp 9: TMEM owner, and its elected lane issues every MMA, in
+// the order Q K of op k + 2 behind P V of op k (the same columns: MMAs of one
+// thread run in issue order).  Waits are bounded as in the other kernels.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "host_util.h"
+#include "pkv_common.cuh"
+#include "prefix.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+constexpr int kXThreads = 320;
+constexpr int kXTile = 128;                       // query rows of a chain's tile, and keys of a K / V tile
+constexpr int kXTileBlocks = kXTile / kBlockSize;
+constexpr int kXStages = 2;                       // of K and of V
+constexpr float kXRescaleLog2 = 8.f;
+constexpr int kXHalf = kXTile * 128;              // bytes of a 64-column half of a 16-bit tile
+
+template <int D>
+struct PrefixSmem {
+  static constexpr int kTileBytes = kXTile * D * 2;
+  static constexpr int kQ = 0;                                 // [2] row tiles
+  static constexpr int kK = 2 * kTileBytes;                    // [kXStages]
+  static constexpr int kV = kK + kXStages * kTileBytes;
+  static constexpr int kBar = kV + kXStages * kTileBytes;      // 256 bytes
+  static constexpr int kRed = kBar + 256;                      // float2 [2][128]: a chain's (m, l)
+  static constexpr int kGroups = kRed + 2 * kXTile * 8;        // PrefixGroup [num_groups + 1]
+  static size_t bytes(int num_groups) {
+    return 1024 + kGroups + sizeof(PrefixGroup) * (static_cast<size_t>(num_groups) + 1);
+  }
+};
+
+// 16-byte chunk c of row r in a tile: 64-column halves, 8-row atoms of 1 KiB,
+// chunk index XOR row within the atom
+__device__ __forceinline__ uint32_t xtile_off(int r, int c) {
+  return (c >> 3) * kXHalf + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// 32 bytes in one store
+__device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// a piece of a range: key tiles [t0, t1) of one unit
+struct PrefixSeg {
+  int64_t next;                  // cost position behind it
+  int64_t row;                   // first row of its states
+  int group, g, unit, rows, t0, t1;
+  bool share;                    // two row tiles (else two key streams)
+};
+
+__device__ __forceinline__ int prefix_units(int rows) { return (rows + kPrefixUnitRows - 1) / kPrefixUnitRows; }
+__device__ __forceinline__ int prefix_tiles(int blocks) { return (blocks + kXTileBlocks - 1) / kXTileBlocks; }
+
+__device__ __forceinline__ PrefixSeg prefix_segment(const PrefixGroup* groups, int num_groups, int n_q_heads,
+                                                    int64_t pos, int64_t end, int64_t range) {
+  int lo = 0, hi = num_groups - 1;   // the last group that starts at or before pos (a non-empty one)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (groups[mid].cost <= pos) lo = mid; else hi = mid - 1;
+  }
+  const PrefixGroup gr = groups[lo];
+  const int kt = prefix_tiles(gr.blocks), units = prefix_units(gr.rows);
+  const int64_t rem = pos - gr.cost;
+  const int64_t u = rem / kt;
+  PrefixSeg s;
+  s.group = lo;
+  s.g = static_cast<int>(u / units);
+  s.unit = static_cast<int>(u % units);
+  s.t0 = static_cast<int>(rem - u * kt);
+  s.t1 = static_cast<int>(min(static_cast<int64_t>(kt), s.t0 + (end - pos)));
+  s.next = pos + (s.t1 - s.t0);
+  s.rows = min(kPrefixUnitRows, gr.rows - s.unit * kPrefixUnitRows);
+  s.share = s.rows > kXTile;
+  s.row = piece_row(gr.start, n_q_heads, s.g, gr.rows, s.unit, range);
+  return s;
+}
+
+template <typename QT, int D, int G>
+__global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using L = PrefixSmem<D>;
+  constexpr bool kSplit = std::is_same<QT, BF16>::value;
+  extern __shared__ unsigned char xsm_raw[];
+  unsigned char* sm = xsm_raw + ((1024 - (smem_u32(xsm_raw) & 1023)) & 1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
+  uint64_t* k_full = bars;                    // [2] K tile landed
+  uint64_t* k_empty = k_full + kXStages;      // [2] its Q K^T done
+  uint64_t* v_full = k_empty + kXStages;
+  uint64_t* v_empty = v_full + kXStages;
+  uint64_t* s_full = v_empty + kXStages;      // [2] per chain: scores ready
+  uint64_t* p_full = s_full + 2;              // [2] per chain, 128 arrivals: P written, O rescaled
+  uint64_t* pv_done = p_full + 2;             // [2] per chain
+  uint64_t* q_ready = pv_done + 2;            // 256 arrivals per piece
+  uint64_t* mma_idle = q_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float2* red = reinterpret_cast<float2*>(sm + L::kRed);
+  PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::kGroups);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_release();   // (the next kernel, over the sequences' own blocks, reads only inputs before its wait)
+
+  // ---- the groups: shared blocks, first covering sequence, cost ------------
+  for (int j = warp; j < p.num_groups; j += kXThreads / 32) {
+    const int raw0 = p.group_starts[j], raw1 = p.group_starts[j + 1];
+    const int s0 = min(max(raw0, 0), p.batch), s1 = min(max(raw1, s0), p.batch);
+    if ((raw0 != s0 || raw1 != s1 || (j == 0 && raw0 != 0) || (j == p.num_groups - 1 && raw1 != p.batch)) && lane == 0)
+      record_error(p.err, PKV_ERR_OOB);
+    const int blocks = max(p.prefix_lens[j], 0) / kBlockSize;
+    int owner = -1;
+    if (blocks > 0)
+      for (int b0 = s0; b0 < s1 && owner < 0; b0 += 32) {
+        const int b = b0 + lane;
+        const bool covers = b < s1 && shares_prefix(blocks, p.context_lens[b], min(p.max_blocks_per_seq, p.max_nblk));
+        const uint32_t m = __ballot_sync(0xffffffffu, covers);
+        if (m) owner = b0 + __ffs(m) - 1;
+      }
+    if (lane == 0) {
+      PrefixGroup gr;
+      gr.start = s0;
+      gr.rows = (s1 - s0) * G;
+      gr.blocks = owner >= 0 ? blocks : 0;
+      gr.owner = owner;
+      gr.cost = static_cast<int64_t>(p.n_kv_heads) * prefix_units(gr.rows) * prefix_tiles(gr.blocks);
+      groups[j] = gr;
+    }
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < kXStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&s_full[c], 1);
+      mbar_init(&p_full[c], kXTile);
+      mbar_init(&pv_done[c], 1);
+    }
+    mbar_init(q_ready, 2 * kXTile);
+    mbar_init(mma_idle, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == 0) {   // exclusive prefix of the costs
+    int64_t carry = 0;
+    for (int j0 = 0; j0 < p.num_groups; j0 += 32) {
+      const int j = j0 + lane;
+      const int64_t own = j < p.num_groups ? groups[j].cost : 0;
+      int64_t x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += u;
+      }
+      if (j < p.num_groups) groups[j].cost = carry + x - own;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) groups[p.num_groups] = PrefixGroup{carry, p.batch, 0, 0, -1};
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (blockIdx.x == 0)
+    for (int j = tid; j <= p.num_groups; j += kXThreads) p.groups[j] = groups[j];
+  const uint32_t tmem = *tmem_slot;
+  const int64_t V = groups[p.num_groups].cost, R = gridDim.x, range = blockIdx.x;
+  const int64_t first = (range * V) / R, end = ((range + 1) * V) / R;
+  auto segment = [&](int64_t pos) { return prefix_segment(groups, p.num_groups, p.n_q_heads, pos, end, range); };
+
+  if (warp < 8) {
+    // ============================ softmax / epilogue ============================
+    const int chain = warp >> 2, r = tid & (kXTile - 1);
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + chain * kXTile;
+    const uint32_t t_o = tmem + lane_base + 2 * kXTile;          // chain c's columns at + c D
+    uint32_t ops = 0;                                            // this chain's operations so far
+    bool ok = true;
+    for (int64_t pos = first; pos < end;) {
+      const PrefixSeg sg = segment(pos);
+      pos = sg.next;
+      const PrefixGroup gr = groups[sg.group];
+      const int n_tiles = sg.t1 - sg.t0;
+      const int unit_row = sg.share ? chain * kXTile + r : r;    // row of the unit
+      const bool live = unit_row < sg.rows;
+      {
+        // stage this row of Q (zeros behind the unit's rows); with one row tile
+        // the two warpgroups share it
+        const int row = sg.unit * kPrefixUnitRows + (live ? unit_row : 0);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const unsigned char*>(p.q) +
+            ((static_cast<int64_t>(gr.start) + row / G) * p.n_q_heads + sg.g * G + row % G) * D * 2);
+        const uint32_t dst = smem_u32(sm + L::kQ + (sg.share ? chain * L::kTileBytes : 0));
+        const int c0 = sg.share ? 0 : chain * (D / 16), c1 = sg.share ? D / 8 : c0 + D / 16;
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) {
+          const uint4 v = live ? src[c] : make_uint4(0, 0, 0, 0);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + xtile_off(r, c)), "r"(v.x), "r"(v.y),
+                       "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();   // (the previous piece's reads of O come before the MMAs this releases)
+        mbar_arrive(q_ready);
+      }
+      float m_ref = -INFINITY, l_run = 0.f;
+      int mine = 0;                                              // operations of this chain in this piece
+      const int step = sg.share ? 1 : 2;
+      for (int n = sg.share ? 0 : chain; n < n_tiles && ok; n += step, ++mine, ++ops) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[chain], ops & 1, p.err)) && !*abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        // keys of the tile that the prefix holds (whole blocks; the last tile may be short)
+        const int valid = min(kXTile, (gr.blocks - (sg.t0 + n) * kXTileBlocks) * kBlockSize);
+        float v[64];
+        tmem_ld64(t_s, v);
+        if (valid < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = i < valid ? v[i] : -INFINITY;
+        }
+        float mx = max64(v);
+        tmem_ld64(t_s + 64, v);
+        if (valid < kXTile) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = 64 + i < valid ? v[i] : -INFINITY;
+        }
+        mx = fmaxf(mx, max64(v));
+        const float m_tile = mx * p.qk_scale_log2;
+        float alpha = 1.f;
+        if (m_tile > m_ref + kXRescaleLog2) {
+          alpha = ex2_approx(m_ref - m_tile);
+          m_ref = m_tile;
+        }
+        if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O may be touched once the chain's previous P V has completed
+          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + chain * D + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st32(t_o + chain * D + c, o);
+          }
+        }
+        const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        const uint64_t scale2 = f32x2(p.qk_scale_log2, p.qk_scale_log2), nref2 = f32x2(nref, nref);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        // the columns in registers are the upper 64; the lower ones are read again
+#pragma unroll 1
+        for (int half = 1; half >= 0; --half) {
+          if (half == 0) {
+            tmem_ld64(t_s, v);
+            if (valid < 64) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] = i < valid ? v[i] : -INFINITY;
+            }
+          }
+          uint32_t pk2[64];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t* pk = pk2 + 32 * c;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = f32x2_split(fma_f32x2(f32x2(v[32 * c + i], v[32 * c + i + 1]), scale2, nref2));
+              const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+              const uint64_t e01 = f32x2(e0, e1);
+              acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
+              if constexpr (kSplit) {
+                const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+                pk[i / 2] = __byte_perm(b0, b1, 0x7632);
+                const float2 lo = f32x2_split(
+                    sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
+                pk[16 + i / 2] = pack2(lo.x, lo.y, QT{});
+              } else {
+                pk[i / 2] = pack2(e0, e1, QT{});
+              }
+            }
+            if constexpr (!kSplit) tmem_st16u(t_s + 64 * half + 32 * c, pk);
+          }
+          if constexpr (kSplit) tmem_st64u(t_s + 64 * half, pk2);
+        }
+        const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        tmem_wait_st();
+        l_run = l_run * alpha + (s0.x + s0.y);
+        tc_fence_before();
+        mbar_arrive(&p_full[chain]);
+      }
+      // the piece's states; both warpgroups meet here (a failed wait ends both)
+      if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
+      if (!sg.share) red[chain * kXTile + r] = make_float2(m_ref, l_run);
+      if (named_bar_red_or(1, 2 * kXTile, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int64_t out_row = sg.row + unit_row;
+      if (sg.share) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(t_o + chain * D + c, o);
+          if (live)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) st_global_v8(p.o + out_row * D + c + i, o + i);
+        }
+        if (live) *reinterpret_cast<float2*>(p.ml + out_row * 2) = make_float2(m_ref, l_run);
+      } else {
+        // join the two key streams: each warpgroup takes half of the columns
+        const float2 a = red[r], b = red[kXTile + r];
+        const float m = fmaxf(a.x, b.x), ref = (m == -INFINITY) ? 0.f : m;
+        const float wa = ex2_approx(a.x - ref), wb = ex2_approx(b.x - ref);
+#pragma unroll 1
+        for (int c = chain * (D / 2); c < (chain + 1) * (D / 2); c += 32) {
+          float o[32];
+          tmem_ld32(t_o + c, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= wa;
+          if (n_tiles > 1) {
+            float o2[32];
+            tmem_ld32(t_o + D + c, o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(o2[i], wb, o[i]);
+          }
+          if (live)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) st_global_v8(p.o + out_row * D + c + i, o + i);
+        }
+        if (live && chain == 0)
+          *reinterpret_cast<float2*>(p.ml + out_row * 2) = make_float2(m, a.y * wa + b.y * wb);
+        tc_fence_before();
+        named_bar_sync(2, 2 * kXTile);   // both have read red and the other's O
+        tc_fence_after();
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp == 8) {
+    // ============================ TMA producer ============================
+    uint32_t tiles = 0;                  // tiles loaded so far (K and V alike)
+    uint32_t issued_k = 0, issued_v = 0;
+    bool good = true;
+    for (int64_t pos = first; pos < end && good;) {
+      const PrefixSeg sg = segment(pos);
+      pos = sg.next;
+      const PrefixGroup gr = groups[sg.group];
+      const uint64_t pol = prefix_units(gr.rows) > 1 ? policy_evict_last() : policy_evict_first();
+      const int32_t* row = p.block_tables + static_cast<int64_t>(gr.owner) * p.max_blocks_per_seq;
+      auto fetch_id = [&](int t) -> int {
+        const int blk = t * kXTileBlocks + lane;
+        return (t < sg.t1 && lane < kXTileBlocks && blk < gr.blocks) ? row[blk] : -1;
+      };
+      // cache row of this lane's block: a block behind the prefix, or a bad id,
+      // is read from rows outside the tensor, which TMA fills with zeros
+      auto to_row = [&](int t, int id) -> int {
+        const int blk = t * kXTileBlocks + lane;
+        if (lane < kXTileBlocks && blk < gr.blocks && (id < 0 || id >= p.num_blocks)) {
+          record_error(p.err, PKV_ERR_OOB);
+          id = -1;
+        }
+        return (id >= 0) ? (id * p.n_kv_heads + sg.g) * kBlockSize : -2 * kBlockSize;
+      };
+      auto load = [&](bool is_v, int y) -> bool {
+        const uint32_t s = tiles % kXStages, use = tiles / kXStages;
+        uint64_t* full = is_v ? &v_full[s] : &k_full[s];
+        uint64_t* empty = is_v ? &v_empty[s] : &k_empty[s];
+        const bool freed = use == 0 || mbar_wait(empty, (use - 1) & 1, p.err);
+        if (!__all_sync(0xffffffffu, freed && !*abort_flag)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(full, L::kTileBytes);
+        __syncwarp();
+        if (lane < kXTileBlocks) {
+          unsigned char* dst = sm + (is_v ? L::kV : L::kK) + s * L::kTileBytes + lane * 2048;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_2d(dst + h * kXHalf, is_v ? &p.tmap_v : &p.tmap_k, h * 64, y, full, pol);
+        }
+        __syncwarp();
+        (is_v ? issued_v : issued_k) = tiles + 1;
+        return true;
+      };
+      int id = fetch_id(sg.t0);
+      for (int t = sg.t0; t < sg.t1 && good; ++t) {
+        const int y = to_row(t, id);
+        id = fetch_id(t + 1);
+        good = load(false, y) && load(true, y);
+        ++tiles;
+      }
+    }
+    if (!good) *abort_flag = 1;
+    if (*abort_flag && lane == 0) {
+      // loads this warp issued that nobody may have waited for (bounded)
+      const unsigned long long deadline = global_ns() + kWaitLimitNs;
+      for (uint32_t t = issued_k > kXStages ? issued_k - kXStages : 0; t < issued_k; ++t)
+        mbar_wait_until(&k_full[t % kXStages], (t / kXStages) & 1, deadline);
+      for (uint32_t t = issued_v > kXStages ? issued_v - kXStages : 0; t < issued_v; ++t)
+        mbar_wait_until(&v_full[t % kXStages], (t / kXStages) & 1, deadline);
+    }
+  } else {
+    // ============================ MMA issuer (warp 9) ============================
+    constexpr int kPasses = kSplit ? 2 : 1;
+    constexpr uint32_t kIdQK = umma_idesc<QT>(false, kXTile), kIdPV = umma_idesc<QT>(true, D);
+    bool ok = true;
+    if (lane == 0) {
+      uint32_t tile0 = 0, piece = 0;       // K / V tiles and pieces before the current piece
+      uint32_t done[2] = {0, 0};           // P V operations of each chain so far
+      for (int64_t pos = first; pos < end && ok; ++piece) {
+        const PrefixSeg sg = segment(pos);
+        pos = sg.next;
+        const int n_tiles = sg.t1 - sg.t0;
+        const int n_ops = sg.share ? 2 * n_tiles : n_tiles;
+        auto qk = [&](int k) -> bool {
+          const uint32_t t = tile0 + (sg.share ? k >> 1 : k), s = t % kXStages;
+          const int c = k & 1;
+          if (!mbar_wait(&k_full[s], (t / kXStages) & 1, p.err) || *abort_flag) return false;
+          const uint64_t a0 =
+              umma_desc(smem_u32(sm + L::kQ + (sg.share ? c * L::kTileBytes : 0)), 16, 1024);
+          const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + s * L::kTileBytes), 16, 1024);
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t koff = static_cast<uint64_t>(((ks >> 2) * kXHalf + (ks & 3) * 32) >> 4);
+            umma_f16(tmem + c * kXTile, a0 + koff, b0 + koff, kIdQK, ks > 0);
+          }
+          umma_commit(&s_full[c]);
+          if (!sg.share || c == 1) umma_commit(&k_empty[s]);
+          return true;
+        };
+        auto pv = [&](int k) -> bool {
+          const uint32_t t = tile0 + (sg.share ? k >> 1 : k), s = t % kXStages;
+          const int c = k & 1;
+          if (!mbar_wait(&p_full[c], done[c] & 1, p.err) || !mbar_wait(&v_full[s], (t / kXStages) & 1, p.err) ||
+              *abort_flag)
+            return false;
+          ++done[c];
+          tc_fence_after();
+          const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + s * L::kTileBytes), kXHalf, 1024);
+          const uint32_t a0 = tmem + c * kXTile, d = tmem + 2 * kXTile + c * D;
+#pragma unroll
+          for (int pass = 0; pass < kPasses; ++pass)
+#pragma unroll
+            for (int ks = 0; ks < kXTile / 16; ++ks)
+              umma_f16_tmem_a(d, a0 + 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1),
+                              b0 + static_cast<uint64_t>((ks * 2048) >> 4), kIdPV, k > 1 || ks > 0 || pass > 0);
+          umma_commit(&pv_done[c]);
+          if (!sg.share || c == 1) umma_commit(&v_empty[s]);
+          return true;
+        };
+        ok = mbar_wait(q_ready, piece & 1, p.err) && !*abort_flag;
+        for (int k = 0; k < min(2, n_ops) && ok; ++k) ok = qk(k);
+        for (int k = 0; k < n_ops && ok; ++k) ok = pv(k) && (k + 2 >= n_ops || qk(k + 2));
+        tile0 += n_tiles;
+      }
+      if (!ok) *abort_flag = 1;
+      // every MMA has completed before TMEM is released
+      umma_commit(mma_idle);
+      mbar_wait(mma_idle, 0, p.err);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// The merge: one warp per (sequence, query head).  Lane l owns D / 32
+// consecutive outputs and joins the states of the prefix's pieces (one per
+// range that the row's unit meets), then those of the sequence's own blocks:
+// the pieces in the decode kernel's partial slots, or the one state it left
+// for a pair that one range holds.
+// ---------------------------------------------------------------------------
+constexpr int kMergeWarps = 8;
+
+template <int N>
+struct MergeState {
+  float m = -INFINITY, l = 0.f, o[N] = {};
+  __device__ __forceinline__ void add(float2 ml, const float* v) {
+    const float mn = fmaxf(m, ml.x);
+    const float ref = (mn == -INFINITY) ? 0.f : mn;
+    const float a = exp2f(m - ref), w = exp2f(ml.x - ref);
+    l = l * a + w * ml.y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = o[i] * a + w * v[i];
+    m = mn;
+  }
+};
+
+template <typename QT, int D, int G>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ranges, const __grid_constant__ DecodeParams rest,
+                        int rest_grid) {
+  constexpr int N = D / 32;
+  constexpr int kBatch = 4;        // pieces whose loads are issued together
+  const int lane = threadIdx.x & 31;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  pdl_wait_and_release();
+  if (u >= static_cast<int64_t>(p.batch) * p.n_q_heads) return;
+  const int b = static_cast<int>(u / p.n_q_heads), head = static_cast<int>(u % p.n_q_heads);
+  const int g = head / G, h = head % G;
+  MergeState<N> st;
+  auto load = [&](const float* src, float* v) {
+    if constexpr (N == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src + 4 * lane);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src + 2 * lane);
+      v[0] = x.x, v[1] = x.y;
+    }
+  };
+  // pieces r0..r1: state of piece r at index at(r) of (ml, o), live(r) false where a range holds none
+  auto walk = [&](int64_t r0, int64_t r1, const float* ml, const float* o, auto&& live, auto&& at) {
+    for (int64_t rb = r0; rb <= r1; rb += kBatch) {
+      float2 x[kBatch];
+      float v[kBatch][N];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int64_t r = rb + q;
+        const bool use = r <= r1 && live(r);
+        const int64_t i = use ? at(r) : 0;
+        x[q] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[q][e] = 0.f;
+        if (use) {
+          x[q] = *reinterpret_cast<const float2*>(ml + i * 2);
+          load(o + i * D, v[q]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) st.add(x[q], v[q]);
+    }
+  };
+
+  // ---- the shared prefix ----
+  int j = -1;                      // the last group that starts at or before b
+  for (int j0 = 0; j0 < p.num_groups; j0 += 32) {
+    const uint32_t m = __ballot_sync(0xffffffffu, j0 + lane < p.num_groups && p.groups[j0 + lane].start <= b);
+    if (m) j = j0 + 31 - __clz(m);
+  }
+  if (j >= 0) {
+    const PrefixGroup gr = p.groups[j];
+    const int row = (b - gr.start) * G + h;
+    if (gr.blocks > 0 && row < gr.rows &&
+        shares_prefix(gr.blocks, p.context_lens[b], min(p.max_blocks_per_seq, p.max_nblk))) {
+      const int64_t V = p.groups[p.num_groups].cost, R = ranges;
+      const int kt = prefix_tiles(gr.blocks), unit = row / kPrefixUnitRows;
+      const int64_t lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt, hi = lo + kt;
+      const int64_t r0 = ((lo + 1) * R + V - 1) / V - 1, r1 = (hi * R + V - 1) / V - 1;   // largest r with r V / R <= x
+      const int64_t base = piece_row(gr.start, p.n_q_heads, g, gr.rows, unit, 0) + row % kPrefixUnitRows;
+      walk(r0, r1, p.ml, p.o,
+           [&](int64_t r) { return max(lo, (r * V) / R) < min(hi, ((r + 1) * V) / R); },
+           [&](int64_t r) { return base + r * kPrefixUnitRows; });
+    }
+  }
+  // ---- the sequence's own blocks ----
+  const int64_t c0 = rest.ws_cum[b];
+  const int nb = rest.ws_cum[b + 1] - rest.ws_cum[b];
+  if (nb > 0) {
+    const CombineSpan sp = combine_span(rest, g, c0, nb, rest.ws_cum[rest.batch], rest.ws_cum[rest.batch + 1 + b],
+                                        rest.ws_cum[2 * rest.batch + 1], rest_grid);
+    if (sp.r0 == sp.r1) {
+      float v[N];
+      load(rest.rest_o + u * D, v);
+      st.add(*reinterpret_cast<const float2*>(rest.rest_ml + u * 2), v);
+    } else {
+      walk(sp.r0, sp.r1, rest.ws_ml, rest.ws_o, [&](int64_t r) { return combine_has_piece(sp, rest, r, rest_grid); },
+           [&](int64_t r) { return combine_slot(sp, r) * G + h; });
+    }
+  }
+  const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+  auto* out = static_cast<typename QT::storage*>(rest.out) + u * D + N * lane;
+  if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack2(st.o[0] * inv, st.o[1] * inv, QT{}), pack2(st.o[2] * inv, st.o[3] * inv, QT{}));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack2(st.o[0] * inv, st.o[1] * inv, QT{});
+}
+
+namespace {
+
+template <typename QT, int D, int G>
+pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t stream) {
+  auto kern = prefix_kernel<QT, D, G>;
+  int dev = 0;
+  if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  if (dev < 0 || dev >= kMaxDevices) return PKV_ERR_UNSUPPORTED;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(PrefixSmem<D>::bytes(kMaxPrefixGroups))),
+                      "cudaFuncSetAttribute"))
+        return PKV_ERR_CUDA;
+      done[dev] = true;
+    }
+  }
+  return cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(kXThreads),
+                                PrefixSmem<D>::bytes(p.num_groups), stream, p),
+                     "prefix_kernel launch")
+             ? PKV_ERR_CUDA
+             : PKV_OK;
+}
+
+template <typename QT, int D, int G>
+pkv_status launch_merge_variant(const PrefixParams& p, int ranges, const DecodeParams& rest, int rest_grid,
+                                cudaStream_t stream) {
+  const int64_t units = static_cast<int64_t>(p.batch) * p.n_q_heads;
+  const int64_t grid = (units + kMergeWarps - 1) / kMergeWarps;
+  if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  return cuda_failed(launch_pdl(prefix_merge_kernel<QT, D, G>, dim3(static_cast<unsigned>(grid)),
+                                dim3(kMergeWarps * 32), 0, stream, p, ranges, rest, rest_grid),
+                     "prefix_merge_kernel launch")
+             ? PKV_ERR_CUDA
+             : PKV_OK;
+}
+
+// calls f with the type, head_dim and group as template arguments
+template <typename F>
+pkv_status dispatch(pkv_dtype dtype, int head_dim, int group, F&& f) {
+  auto by_group = [&](auto qt, auto d) -> pkv_status {
+    switch (group) {
+      case 1: return f(qt, d, std::integral_constant<int, 1>{});
+      case 2: return f(qt, d, std::integral_constant<int, 2>{});
+      case 4: return f(qt, d, std::integral_constant<int, 4>{});
+      case 8: return f(qt, d, std::integral_constant<int, 8>{});
+      default: return PKV_ERR_UNSUPPORTED;
+    }
+  };
+  auto by_dim = [&](auto qt) -> pkv_status {
+    return head_dim == 64 ? by_group(qt, std::integral_constant<int, 64>{})
+                          : by_group(qt, std::integral_constant<int, 128>{});
+  };
+  return dtype == PKV_F16 ? by_dim(F16{}) : by_dim(BF16{});
+}
+
+}  // namespace
+
+pkv_status launch_prefix(PrefixParams& p, int ranges, int group, int head_dim, pkv_dtype dtype, cudaStream_t stream) {
+  return dispatch(dtype, head_dim, group, [&](auto qt, auto d, auto g) {
+    return launch_prefix_variant<decltype(qt), decltype(d)::value, decltype(g)::value>(p, ranges, stream);
+  });
+}
+
+pkv_status launch_prefix_merge(const PrefixParams& p, int ranges, const DecodeParams& rest, int rest_grid, int group,
+                               int head_dim, pkv_dtype dtype, cudaStream_t stream) {
+  return dispatch(dtype, head_dim, group, [&](auto qt, auto d, auto g) {
+    return launch_merge_variant<decltype(qt), decltype(d)::value, decltype(g)::value>(p, ranges, rest, rest_grid,
+                                                                                      stream);
+  });
+}
+
+}  // namespace pkv
