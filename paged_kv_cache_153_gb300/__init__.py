@@ -174,11 +174,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        # the raw handle of the current stream, without the Stream object that
+        # torch.cuda.current_stream() builds (3 us a call, half of a small one's host time)
+        raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        _current_stream = lambda: raw(device())   # noqa: E731
+    return _current_stream()
 
 
 def _dtype_code(t, dtype) -> int:
@@ -485,38 +494,39 @@ def pkv_rope_plan(rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
     return turns, amp.value
 
 
-def _token_stride(t, name: str) -> int:
-    """Elements between the tokens of t [T, H, D], whose heads are contiguous."""
-    if t is None:
-        return 0
-    n, h, d = t.shape
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+def _token_stride(t, name: str, heads: int, d: int) -> int:
+    """Elements between the tokens of t [T, heads, d], whose heads are contiguous."""
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return stride[0] if t.shape[0] > 1 else heads * d
 
 
 def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, scales, layout, amplitude,
           dtype, err_flag, stream):
-    some = q if q is not None else k_new
+    n = positions.numel()
+    q_args, kv_args, hq, hkv, nb, bs = (None, 0, None, 0), (None, 0, None, 0), 0, 0, 0, 16
+    if q is not None:
+        shape = q.shape
+        t, hq, d = shape
+        if t != n or q_out.shape != shape:
+            raise ValueError("q, q_out and positions differ in shape")
+        q_args = q.data_ptr(), _token_stride(q, "q", hq, d), q_out.data_ptr(), _token_stride(q_out, "q_out", hq, d)
     if k_new is not None:
-        nb, hkv, bs, d = k_cache.shape
-        if k_new.shape != v_new.shape or k_new.shape[1:] != (hkv, d):
+        nb, hkv, bs, dk = k_cache.shape
+        shape = k_new.shape
+        if shape != (n, hkv, dk) or v_new.shape != shape or (q is not None and dk != d):
             raise ValueError("k_new and v_new must be [T, num_kv_heads, head_dim] of the cache")
-        if slot_mapping.numel() != positions.numel():
+        if slot_mapping.numel() != n:
             raise ValueError("slot_mapping and positions differ in length")
-    else:
-        nb, hkv, bs, d = 0, 0, 16, q.shape[2]
-    if q is not None and q.shape != q_out.shape:
-        raise ValueError("q and q_out differ in shape")
-    for t in (q, k_new):
-        if t is not None and (t.shape[0] != positions.numel() or t.shape[2] != d):
-            raise ValueError("q, k_new and positions differ in tokens or head_dim")
+        d = dk
+        kv_args = (k_new.data_ptr(), _token_stride(k_new, "k_new", hkv, d), v_new.data_ptr(),
+                   _token_stride(v_new, "v_new", hkv, d))
     _check(fn, getattr(lib, fn)(
-        _ptr(q), _token_stride(q, "q"), _ptr(k_new), _token_stride(k_new, "k_new"), _ptr(v_new),
-        _token_stride(v_new, "v_new"), _ptr(positions), _ptr(slot_mapping), positions.numel(), _ptr(turns),
-        2 * turns.numel(), _ROPE_LAYOUTS.get(layout, layout), amplitude, _ptr(q_out), _token_stride(q_out, "q_out"),
-        _ptr(k_cache), _ptr(v_cache), nb, *scales, 0 if q is None else q.shape[1], hkv, d, bs,
-        _dtype_code(some, dtype), _ptr(err_flag), _stream(stream)))
+        q_args[0], q_args[1], *kv_args, positions.data_ptr(), _ptr(slot_mapping), n, turns.data_ptr(),
+        2 * turns.numel(), _ROPE_LAYOUTS.get(layout, layout), amplitude, q_args[2], q_args[3], _ptr(k_cache),
+        _ptr(v_cache), nb, *scales, hq, hkv, d, bs, _dtype_code(k_new if q is None else q, dtype), _ptr(err_flag),
+        _stream(stream)))
 
 
 def pkv_rope_append(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, *, layout="half",

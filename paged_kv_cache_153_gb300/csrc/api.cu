@@ -2,6 +2,7 @@
 // planning and dispatch to the compiled kernel variants.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <mutex>
@@ -74,10 +75,13 @@ int env_int(const char* name, int fallback) {
 constexpr int kMaxCtasPerSm = 4;   // partial slots are sized for this many blocks per SM
 
 int sm_count() {
+  static std::atomic<int> counts[kMaxDevices];   // (a device's count does not change: asked once)
   int dev = 0, n = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return 0;
+  if (dev >= 0 && dev < kMaxDevices && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cuda_failed(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute"))
     return 0;
+  if (dev >= 0 && dev < kMaxDevices) counts[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

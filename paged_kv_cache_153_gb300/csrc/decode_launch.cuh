@@ -26,42 +26,66 @@ constexpr int kSmemPerSm = 233472;        // shared memory per SM on sm_100-clas
 constexpr int kSmemReservedPerCta = 1024; // system-reserved shared memory per resident block
 constexpr int kMaxStagesPerWarp = 8;
 
+// the runtime's answers about one kernel variant on one device
+constexpr int kOccupancyEntries = 8;
+struct VariantCache {
+  size_t dyn_max;                // 0: not asked yet
+  struct {
+    size_t smem;
+    int blocks;
+  } occ[kOccupancyEntries];
+  unsigned next;
+};
+
 template <typename QT, typename KV, int D, int G, int NW, bool MMA, Source SRC>
 pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t stream) {
   using Tr = DecodeTraits<D, G, NW, KV, MMA>;
   auto kern = paged_decode_kernel<QT, KV, D, G, NW, MMA, SRC>;
-  int max_optin = 0, dev = 0;
+  int dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
-  if (cuda_failed(cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev),
-                  "cudaDeviceGetAttribute"))
-    return PKV_ERR_CUDA;
-  cudaFuncAttributes fattr;
-  if (cuda_failed(cudaFuncGetAttributes(&fattr, kern), "cudaFuncGetAttributes")) return PKV_ERR_CUDA;
-  // dynamic shared memory may use what the static part leaves of the opt-in limit
-  const size_t dyn_max = static_cast<size_t>(max_optin) - fattr.sharedSizeBytes;
-  // the opt-in is a per-device function attribute: set it once per device
-  static std::mutex attr_mu;
-  static bool attr_done[kMaxDevices] = {};
   if (dev < 0 || dev >= kMaxDevices) return PKV_ERR_UNSUPPORTED;
-  {
-    std::lock_guard<std::mutex> lock(attr_mu);
-    if (!attr_done[dev]) {
-      if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(dyn_max)),
-                      "cudaFuncSetAttribute"))
-        return PKV_ERR_CUDA;
-      attr_done[dev] = true;
-    }
+  // What the runtime answers about this kernel is asked once per device: the
+  // shared memory a block may opt in to (and the opt-in itself), and the
+  // occupancy of the shared-memory sizes in use (asking each time made a small
+  // call's host time 6.9 us, against 5.9).
+  static std::mutex cache_mu;
+  static VariantCache caches[kMaxDevices] = {};
+  std::unique_lock<std::mutex> lock(cache_mu);
+  VariantCache& cache = caches[dev];
+  if (cache.dyn_max == 0) {
+    int max_optin = 0;
+    cudaFuncAttributes fattr;
+    if (cuda_failed(cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev),
+                    "cudaDeviceGetAttribute") ||
+        cuda_failed(cudaFuncGetAttributes(&fattr, kern), "cudaFuncGetAttributes"))
+      return PKV_ERR_CUDA;
+    // dynamic shared memory may use what the static part leaves of the opt-in limit
+    const size_t dyn = static_cast<size_t>(max_optin) - fattr.sharedSizeBytes;
+    if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn)),
+                    "cudaFuncSetAttribute"))
+      return PKV_ERR_CUDA;
+    cache.dyn_max = dyn;
   }
+  const size_t dyn_max = cache.dyn_max;
+  auto occupancy = [&](size_t smem, int* occ) -> bool {
+    for (const auto& e : cache.occ)
+      if (e.smem == smem) {
+        *occ = e.blocks;
+        return true;
+      }
+    if (cuda_failed(cudaOccupancyMaxActiveBlocksPerMultiprocessor(occ, kern, Tr::kThreads, smem),
+                    "cudaOccupancyMaxActiveBlocksPerMultiprocessor"))
+      return false;
+    cache.occ[cache.next++ % kOccupancyEntries] = {smem, *occ};
+    return true;
+  };
   // Stages come in multiples of NW (each consumer warp owns stages/NW of them).
   // By default, the ring fills the SM's shared memory across as many resident
   // blocks as the registers allow (capped by max_ctas_per_sm).
   int occ = 0;
   size_t smem = Tr::smem_bytes(NW, p.batch, p.n_kv_heads);
   if (smem > dyn_max) return PKV_ERR_UNSUPPORTED;   // batch too large for one block's shared memory
-  if (cuda_failed(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, Tr::kThreads, smem),
-                  "cudaOccupancyMaxActiveBlocksPerMultiprocessor"))
-    return PKV_ERR_CUDA;
+  if (!occupancy(smem, &occ)) return PKV_ERR_CUDA;
   if (occ < 1) return PKV_ERR_UNSUPPORTED;
   // Upper bound on the (sequence, KV head, block) work items, from max_context_len.
   const int64_t w_max = static_cast<int64_t>(p.batch) * p.n_kv_heads *
@@ -99,9 +123,8 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   while (spw > 1 && Tr::smem_bytes(NW * spw, p.batch, p.n_kv_heads) > dyn_max) --spw;
   const int stages = NW * spw;
   smem = Tr::smem_bytes(stages, p.batch, p.n_kv_heads);
-  if (cuda_failed(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, Tr::kThreads, smem),
-                  "cudaOccupancyMaxActiveBlocksPerMultiprocessor"))
-    return PKV_ERR_CUDA;
+  if (!occupancy(smem, &occ)) return PKV_ERR_CUDA;
+  lock.unlock();
   if (occ < 1) return PKV_ERR_UNSUPPORTED;
   occ = std::min(occ, want);
   int grid = li.num_sms * occ;
