@@ -467,7 +467,7 @@ pkv_status pkv_paged_decode_step_int8(const void* q, const void* k_new, const vo
  *   q_out              as q, with its own stride; q_out == q with the same
  *                      stride turns q in place.  Other overlaps are undefined.
  *   positions          device int32 [T]; a negative one marks a padding token,
- *                      of which nothing is read or written.
+ *                      for which nothing is written.
  *   slot_mapping       device int64 [T]; negative: no append for the token (q
  *                      is turned all the same); past the pool: skipped and
  *                      PKV_ERR_OOB in err_flag.

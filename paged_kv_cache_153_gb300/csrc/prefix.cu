@@ -523,9 +523,12 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
 // consecutive outputs and joins the states of the prefix's pieces (one per
 // range that the row's unit meets), then those of the sequence's own blocks:
 // the pieces in the decode kernel's partial slots, or the one state it left
-// for a pair that one range holds.
+// for a pair that one range holds.  Which ranges hold a piece takes two 64-bit
+// divisions each: the lanes find it for 32 ranges at a time, and only the
+// pieces themselves are walked (every lane dividing for every piece made the
+// merge 14 us of a 93 us call).
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
 
 template <int N>
 struct MergeState {
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ranges, const __grid_constant__ DecodeParams rest,
                         int rest_grid) {
   constexpr int N = D / 32;
-  constexpr int kBatch = 4;        // pieces whose loads are issued together
+  constexpr int kBatch = 8;        // pieces whose loads are issued together
   const int lane = threadIdx.x & 31;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
   pdl_wait_and_release();
@@ -565,54 +568,69 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   };
   // pieces r0..r1: state of piece r at index at(r) of (ml, o), live(r) false where a range holds none
   auto walk = [&](int64_t r0, int64_t r1, const float* ml, const float* o, auto&& live, auto&& at) {
-    for (int64_t rb = r0; rb <= r1; rb += kBatch) {
-      float2 x[kBatch];
-      float v[kBatch][N];
+    for (int64_t rb = r0; rb <= r1; rb += 32) {
+      const int64_t mine = rb + lane;
+      const bool use = mine <= r1 && live(mine);
+      const int64_t index = use ? at(mine) : 0;
+      const float2 state =
+          use ? *reinterpret_cast<const float2*>(ml + index * 2) : make_float2(-INFINITY, 0.f);
+      uint32_t left = __ballot_sync(0xffffffffu, use);
+      while (left) {
+        float v[kBatch][N];
+        int src[kBatch];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const int64_t r = rb + q;
-        const bool use = r <= r1 && live(r);
-        const int64_t i = use ? at(r) : 0;
-        x[q] = make_float2(-INFINITY, 0.f);
+        for (int q = 0; q < kBatch; ++q) {
+          src[q] = left ? __ffs(left) - 1 : -1;
+          left &= left - 1;        // (0 stays 0)
+          const int64_t i = __shfl_sync(0xffffffffu, index, src[q] < 0 ? 0 : src[q]);
+          if (src[q] >= 0) load(o + i * D, v[q]);
+        }
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[q][e] = 0.f;
-        if (use) {
-          x[q] = *reinterpret_cast<const float2*>(ml + i * 2);
-          load(o + i * D, v[q]);
+        for (int q = 0; q < kBatch; ++q) {
+          const int from = src[q] < 0 ? 0 : src[q];
+          const float2 x = make_float2(__shfl_sync(0xffffffffu, state.x, from), __shfl_sync(0xffffffffu, state.y, from));
+          if (src[q] >= 0) st.add(x, v[q]);
         }
       }
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) st.add(x[q], v[q]);
     }
   };
 
+  // everything whose address depends on (b, head) alone is loaded at once
+  const int ctx = p.context_lens[b];
+  const int64_t c0 = rest.ws_cum[b];
+  const int nb = rest.ws_cum[b + 1] - static_cast<int>(c0);
+  const int64_t tot = rest.ws_cum[rest.batch], ne_b = rest.ws_cum[rest.batch + 1 + b],
+                tot_ne = rest.ws_cum[2 * rest.batch + 1];
+  const int64_t V = p.groups[p.num_groups].cost;
+
   // ---- the shared prefix ----
-  int j = -1;                      // the last group that starts at or before b
+  // the last group that starts at or before b: found by the lane that holds it
+  PrefixGroup gr{0, 0, 0, 0, -1};
   for (int j0 = 0; j0 < p.num_groups; j0 += 32) {
-    const uint32_t m = __ballot_sync(0xffffffffu, j0 + lane < p.num_groups && p.groups[j0 + lane].start <= b);
-    if (m) j = j0 + 31 - __clz(m);
+    PrefixGroup own{0, INT32_MAX, 0, 0, -1};
+    if (j0 + lane < p.num_groups) own = p.groups[j0 + lane];
+    const uint32_t m = __ballot_sync(0xffffffffu, own.start <= b);
+    if (m == 0) continue;
+    const int from = 31 - __clz(m);
+    gr.cost = __shfl_sync(0xffffffffu, own.cost, from);
+    gr.start = __shfl_sync(0xffffffffu, own.start, from);
+    gr.rows = __shfl_sync(0xffffffffu, own.rows, from);
+    gr.blocks = __shfl_sync(0xffffffffu, own.blocks, from);
   }
-  if (j >= 0) {
-    const PrefixGroup gr = p.groups[j];
-    const int row = (b - gr.start) * G + h;
-    if (gr.blocks > 0 && row < gr.rows &&
-        shares_prefix(gr.blocks, p.context_lens[b], min(p.max_blocks_per_seq, p.max_nblk))) {
-      const int64_t V = p.groups[p.num_groups].cost, R = ranges;
-      const int kt = prefix_tiles(gr.blocks), unit = row / kPrefixUnitRows;
-      const int64_t lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt, hi = lo + kt;
-      const int64_t r0 = ((lo + 1) * R + V - 1) / V - 1, r1 = (hi * R + V - 1) / V - 1;   // largest r with r V / R <= x
-      const int64_t base = piece_row(gr.start, p.n_q_heads, g, gr.rows, unit, 0) + row % kPrefixUnitRows;
-      walk(r0, r1, p.ml, p.o,
-           [&](int64_t r) { return max(lo, (r * V) / R) < min(hi, ((r + 1) * V) / R); },
-           [&](int64_t r) { return base + r * kPrefixUnitRows; });
-    }
+  const int row = (b - gr.start) * G + h;
+  if (row < gr.rows && shares_prefix(gr.blocks, ctx, min(p.max_blocks_per_seq, p.max_nblk))) {
+    const int64_t R = ranges;
+    const int kt = prefix_tiles(gr.blocks), unit = row / kPrefixUnitRows;
+    const int64_t lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt, hi = lo + kt;
+    const int64_t r0 = ((lo + 1) * R + V - 1) / V - 1, r1 = (hi * R + V - 1) / V - 1;   // largest r with r V / R <= x
+    const int64_t base = piece_row(gr.start, p.n_q_heads, g, gr.rows, unit, 0) + row % kPrefixUnitRows;
+    walk(r0, r1, p.ml, p.o,
+         [&](int64_t r) { return max(lo, (r * V) / R) < min(hi, ((r + 1) * V) / R); },
+         [&](int64_t r) { return base + r * kPrefixUnitRows; });
   }
   // ---- the sequence's own blocks ----
-  const int64_t c0 = rest.ws_cum[b];
-  const int nb = rest.ws_cum[b + 1] - rest.ws_cum[b];
   if (nb > 0) {
-    const CombineSpan sp = combine_span(rest, g, c0, nb, rest.ws_cum[rest.batch], rest.ws_cum[rest.batch + 1 + b],
-                                        rest.ws_cum[2 * rest.batch + 1], rest_grid);
+    const CombineSpan sp = combine_span(rest, g, c0, nb, tot, ne_b, tot_ne, rest_grid);
     if (sp.r0 == sp.r1) {
       float v[N];
       load(rest.rest_o + u * D, v);

@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
   pdl_wait();   // (writes the cache and q_out: no early release of the next launch)
+  // (the position and the slot travel together with the rows)
   const int32_t pos = p.positions[t];
-  if (pos < 0) return;   // a padding token (the whole block)
+  int64_t slot = p.k ? p.slots[t] : -1;
   const int D = p.head_dim, R = p.rot_dim;
   // a row's items: its pair chunks, then the chunks that pass through
   const int pairs = HALF ? R / 16 : R / 8;
@@ -95,27 +96,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int q_rows = p.q ? p.n_q_heads : 0, kv_rows = p.k ? p.n_kv_heads : 0;
   const int qk_items = (q_rows + kv_rows) * per_row;
   const int items = qk_items + kv_rows * (D / 8);
-  int64_t slot = -1;
-  if (kv_rows) {
-    slot = p.slots[t];
-    if (slot >= p.num_slots) {
-      if (tid == 0) record_error(p.err, PKV_ERR_OOB);
-      slot = -1;
-    }
-  }
-  // first row of the slot in head 0's slab; heads are 16 rows apart
-  const int64_t row0 = (slot / kBlockSize) * p.n_kv_heads * kBlockSize + slot % kBlockSize;
+  int64_t row0 = 0;
 
   struct Item {
-    const unsigned char* src;    // null: nothing to do
-    unsigned char* dst;
     int chunk;                   // 16-byte chunk of the row (its first, for a pair)
-    int row;                     // KV head (k and v)
-    int kind;                    // 0: q, 1: k, 2: v
+    int row;                     // query or KV head
+    int kind;                    // 0: q, 1: k, 2: v, -1: nothing to do
     bool turn;
   };
   auto item_at = [&](int i) -> Item {
-    Item it{nullptr, nullptr, 0, 0, 0, false};
+    Item it{0, 0, -1, false};
     if (i >= items) return it;
     if (i < qk_items) {
       const int r = i / per_row, x = i - r * per_row;
@@ -129,28 +119,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
       it.chunk = x - it.row * per_v;
       it.kind = 2;
     }
-    if (it.kind != 0 && slot < 0) return it;
-    if (it.kind == 0) {
-      it.src = p.q + t * p.q_stride + static_cast<int64_t>(it.row) * D * 2;
-      it.dst = p.q_out + t * p.q_out_stride + static_cast<int64_t>(it.row) * D * 2;
-    } else {
-      const int64_t row = (row0 + static_cast<int64_t>(it.row) * kBlockSize) * D * KV::kBytes;
-      it.src = (it.kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + static_cast<int64_t>(it.row) * D * 2;
-      it.dst = (it.kind == 1 ? p.k_cache : p.v_cache) + row;
-    }
     return it;
   };
   auto load = [&](const Item& it, uint4& a, uint4& b) {
-    if (it.src == nullptr) return;
-    a = *reinterpret_cast<const uint4*>(it.src + it.chunk * 16);
-    if (HALF && it.turn) b = *reinterpret_cast<const uint4*>(it.src + (it.chunk + R / 16) * 16);
+    if (it.kind < 0) return;
+    const unsigned char* src = (it.kind == 0   ? p.q + t * p.q_stride
+                                : it.kind == 1 ? p.k + t * p.k_stride
+                                               : p.v + t * p.v_stride) +
+                               (static_cast<int64_t>(it.row) * D + it.chunk * 8) * 2;
+    a = __ldcs(reinterpret_cast<const uint4*>(src));
+    if (HALF && it.turn) b = __ldcs(reinterpret_cast<const uint4*>(src + R));   // (R / 2 elements further)
   };
   auto finish = [&](const Item& it, const uint4& a, const uint4& b) {
-    if (it.src == nullptr) return;
+    if (it.kind < 0 || (it.kind > 0 && slot < 0)) return;
     const float scale =
         (KV::kBytes == 1 && it.kind != 0) ? (it.kind == 1 ? p.k_scale[it.row] : p.v_scale[it.row]) : 1.f;
     const int esz = it.kind == 0 ? 2 : KV::kBytes;
-    unsigned char* dst = it.dst + it.chunk * 8 * esz;
+    unsigned char* dst =
+        it.kind == 0 ? p.q_out + t * p.q_out_stride + static_cast<int64_t>(it.row) * D * 2
+                     : (it.kind == 1 ? p.k_cache : p.v_cache) +
+                           (row0 + static_cast<int64_t>(it.row) * kBlockSize) * D * KV::kBytes;
+    dst += it.chunk * 8 * esz;
     if (!it.turn) {
       if (it.kind == 0)
         copy8<IN, IN>(dst, a, 1.f);
@@ -194,6 +183,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     it[u] = item_at(tid + u * kRopeThreads);
     load(it[u], a[u], b[u]);
   }
+  if (pos < 0) return;   // a padding token (the whole block)
+  if (slot >= p.num_slots) {
+    if (tid == 0) record_error(p.err, PKV_ERR_OOB);
+    slot = -1;
+  }
+  // first row of the slot in head 0's slab; heads are 16 rows apart
+  row0 = (slot / kBlockSize) * p.n_kv_heads * kBlockSize + slot % kBlockSize;
   if (tid < R / 2) {
     const int64_t turn = static_cast<int64_t>(p.turns[tid] * static_cast<uint64_t>(pos));
     float s, c;

@@ -176,7 +176,7 @@ def test_in_place_and_parts(pkv):
 
 def test_padding_and_slots_out_of_range(pkv):
     c = Case(pkv, tokens=12, hq=4, hkv=2, d=64, rot=32, dtype="bf16", seed=4)
-    c.pos[3] = -1                        # padding: nothing of it is read or written
+    c.pos[3] = -1                        # padding: nothing is written for it
     c.slots[5] = -1                      # turned, not appended
     good = c.slots.clone()
     c.run()

@@ -151,6 +151,50 @@ def test_bounds(pkv, dtype, kv, d, hkv):
     assert int(case.err.item()) == 0
 
 
+def device_bounds(case):
+    """Bounds of every block of every context, on the GPU in the keys' type."""
+    k = case.kc.view(FP8[case.kv]).float() if case.kv else case.kc.float()
+    want = torch.full((case.nb, case.hkv, 2, case.d), 7.0, device="cuda")
+    row = torch.arange(16, device="cuda")
+    for b, n in enumerate(case.lens_h):
+        ids = case.tab[b, :-(-int(n) // 16)].long()
+        past = (torch.arange(len(ids), device="cuda")[:, None] * 16 + row >= int(n))[:, None, :, None]
+        want[ids, :, 0] = k[ids].masked_fill(past, float("inf")).amin(2)
+        want[ids, :, 1] = k[ids].masked_fill(past, float("-inf")).amax(2)
+    return want
+
+
+@pytest.mark.parametrize("dtype,kv,hkv,d", [("bf16", None, 3, 128), ("f16", None, 1, 64), ("bf16", "e4m3", 8, 128),
+                                            ("f16", "e5m2", 5, 64)])
+def test_bounds_of_large_mixed_batches(pkv, dtype, kv, hkv, d):
+    # enough slabs that the work is dealt flat over the sequences
+    rng = np.random.default_rng(hkv)
+    lens = [0, 1, 40000, 17, 0] + [int(x) for x in rng.integers(0, 9000, size=60)] + [0, 16]
+    case = Case(lens, hkv=hkv, hq=hkv, d=d, dtype=dtype, kv=kv, seed=hkv)
+    bounds = torch.full((case.nb, hkv, 2, d), 7.0, dtype=gu.TORCH_16[dtype], device="cuda")
+    run_bounds(pkv, case, bounds)
+    assert torch.equal(bounds.float(), device_bounds(case)) and int(case.err.item()) == 0
+    # the newest tokens only: as many, up to the whole context
+    new = [min(n, 5000) for n in lens]
+    part = torch.full_like(bounds, 7.0)
+    run_bounds(pkv, case, part, new)
+    kept = torch.ones(case.nb, dtype=torch.bool)
+    for b, (n, m) in enumerate(zip(lens, new)):
+        if m:
+            kept[case.tab_h[b, (n - m) // 16:-(-n // 16)]] = False
+    kept = kept.cuda()
+    assert torch.all(part[kept] == 7.0) and torch.equal(part[~kept], bounds[~kept]) and int(case.err.item()) == 0
+    # a bad id and a context past its table are reported, the rest is done
+    case.tab[2, 100] = case.nb
+    case.lens[4] = 16 * case.width + 1
+    case.tab[4] = case.tab[2, 0]
+    again = torch.full_like(bounds, 7.0)
+    run_bounds(pkv, case, again)
+    assert int(case.err.item()) == 4
+    ids = case.tab[5, :-(-lens[5] // 16)].long()
+    assert torch.equal(again[ids], bounds[ids])
+
+
 def test_bounds_keep_a_nan_and_infinities(pkv):
     case = Case([40], hkv=1, hq=1, d=64, dtype="f16", seed=3)
     ids = case.tab_h[0]
@@ -214,6 +258,59 @@ def test_scores(pkv, dtype, d, hq, hkv):
                     mass = (np.abs(qg) * np.abs(lo_hi[i]).max(0)).sum(1).max() * factor[g]
                     assert abs(got[b, g, i] - ref) <= mass * (2 * d + 4) * 2.0 ** -23
     assert int(case.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 8, 128), ("f16", 8, 1, 64), ("bf16", 5, 5, 128),
+                                            ("f16", 64, 8, 128), ("bf16", 40, 20, 64), ("f16", 3, 3, 64)])
+def test_scores_of_large_mixed_batches(pkv, dtype, hq, hkv, d):
+    # enough blocks that persistent thread blocks take them from one list
+    rng = np.random.default_rng(hq)
+    lens = [0, 1, 60000, 17, 0] + [int(x) for x in rng.integers(0, 20000, size=90)] + [0, 16]
+    g = torch.Generator(device="cuda").manual_seed(hq)
+    t = gu.TORCH_16[dtype]
+    nblk = [-(-n // 16) for n in lens]
+    width, nb, per = max(nblk) + 2, sum(nblk) + 5, hq // hkv
+    ids = torch.randperm(nb, generator=g, device="cuda", dtype=torch.int32)
+    tab = torch.full((len(lens), width), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(nblk):
+        tab[b, :n] = ids[sum(nblk[:b]):sum(nblk[:b]) + n]
+    x = torch.randn((nb, hkv, 2, d), generator=g, device="cuda").to(t)
+    bounds = torch.stack([x.amin(2), x.amax(2)], 2).contiguous()
+    bounds[ids[sum(nblk):].long()] = float("nan")
+    q = torch.randn((len(lens), hq, d), generator=g, device="cuda").to(t)
+    scores = torch.full((len(lens), hkv, width), -7.0, device="cuda")
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    k_scale = torch.rand(hkv, generator=g, device="cuda") + 0.5
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        pkv.pkv_block_scores(q, bounds, tab, lens_t, scores, scale=0.1, max_context_len=60000, k_scale=k_scale,
+                             err_flag=err)
+        torch.cuda.synchronize()
+    call()
+    assert int(err.item()) == 0
+    factor = 0.1 * k_scale.double()[:, None]
+    for b in [0, 1, 2, 3, 4, 5, 30, 60, 94, 95, 96]:
+        n = nblk[b]
+        assert torch.all(scores[b, :, n:] == -7.0)
+        if n == 0:
+            continue
+        bd = bounds[tab[b, :n].long()].double()
+        best, mass = None, None
+        for h in range(per):
+            qh = q[b].view(hkv, per, d)[:, h].double()
+            s = torch.maximum(qh[:, None] * bd[:, :, 0].transpose(0, 1), qh[:, None] * bd[:, :, 1].transpose(0, 1)).sum(-1)
+            m = (qh.abs()[:, None] * bd.abs().amax(2).transpose(0, 1)).sum(-1)
+            best, mass = (s, m) if best is None else (torch.maximum(best, s), torch.maximum(mass, m))
+        # (the limit of test_scores: 2 D products summed, the factors' roundings)
+        assert torch.all((scores[b, :, :n].double() - best * factor).abs() <= mass * factor * (2 * d + 4) * 2.0 ** -23)
+    # bad ids score -infinity, their neighbours as before
+    before = scores.clone()
+    tab[2, 77], tab[2, 78] = nb, -3
+    call()
+    assert int(err.item()) == 4 and torch.all(scores[2, :, 77:79] == float("-inf"))
+    scores[2, :, 77:79] = before[2, :, 77:79]
+    assert torch.equal(scores, before)
 
 
 def test_scores_bound_the_logits(pkv):
@@ -293,6 +390,19 @@ def test_select(pkv, kind, budget, first, last):
             want = osp.select_blocks(scores[b, g].numpy(), -(-n // 16), first, last, budget)
             want = want + [-1] * (budget - len(want))
             assert got[b, g].tolist() == want, (b, g, n)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("budget", [1, 60, 255, 256, 700, 4096])
+def test_select_among_thousands(pkv, kind, budget):
+    lens = [16 * 4098, 16 * 6001 - 5, 16 * 8197, 16 * 8210, 16 * 17000]
+    scores = make_scores(kind, (len(lens), 2, 17003), budget)
+    got, err = run_select(pkv, scores.cuda(), lens, budget + 3, 1, 2)
+    assert err == 0
+    for b, n in enumerate(lens):
+        for g in range(2):
+            want = osp.select_blocks(scores[b, g].numpy(), -(-n // 16), 1, 2, budget + 3)
+            assert got[b, g].tolist() == want + [-1] * (budget + 3 - len(want)), (b, g)
 
 
 def test_select_many_blocks_and_units(pkv):
