@@ -31,7 +31,8 @@ bool cuda_failed(cudaError_t e, const char* what) {
   return true;
 }
 
-bool encode_cache_tmap(CUtensorMap* map, const void* base, int64_t rows, int head_dim, int elt_bytes) {
+// the driver's tensor-map encoder (null, with the reason kept, when it cannot be had)
+static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static cudaError_t lookup_err = cudaSuccess;
@@ -45,8 +46,13 @@ bool encode_cache_tmap(CUtensorMap* map, const void* base, int64_t rows, int hea
   if (encode == nullptr) {
     cuda_failed(lookup_err == cudaSuccess ? cudaErrorSymbolNotFound : lookup_err,
                 "cudaGetDriverEntryPointByVersion(cuTensorMapEncodeTiled)");
-    return false;
   }
+  return encode;
+}
+
+bool encode_cache_tmap(CUtensorMap* map, const void* base, int64_t rows, int head_dim, int elt_bytes) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (encode == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim) * elt_bytes};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt_bytes), 16};
@@ -63,6 +69,27 @@ bool encode_cache_tmap(CUtensorMap* map, const void* base, int64_t rows, int hea
 }
 
 namespace {
+
+// Tiled TMA view of queries [batch, n_q_heads, head_dim] (16-bit) with boxes of
+// [128 / group sequences, group heads, 64 elements] and the 128-byte swizzle.
+bool encode_query_tmap(CUtensorMap* map, const void* base, int batch, int n_q_heads, int head_dim, int group) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(n_q_heads),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                                 static_cast<cuuint64_t>(head_dim) * 2 * n_q_heads};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (encode == nullptr) return false;
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled: CUresult %d", static_cast<int>(r));
+    return false;
+  }
+  return true;
+}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -561,9 +588,9 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   char* ws = reinterpret_cast<char*>(round256(reinterpret_cast<uintptr_t>(workspace)));
   PrefixParams p{};
   if (!encode_cache_tmap(&p.tmap_k, k_cache, rows, head_dim, 2) ||
-      !encode_cache_tmap(&p.tmap_v, v_cache, rows, head_dim, 2))
+      !encode_cache_tmap(&p.tmap_v, v_cache, rows, head_dim, 2) ||
+      !encode_query_tmap(&p.tmap_q, q, batch, num_q_heads, head_dim, group))
     return PKV_ERR_CUDA;
-  p.q = q;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.group_starts = group_starts;
@@ -583,7 +610,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   // as many ranges as SMs, but no more than there can be key tiles
   const int64_t units = static_cast<int64_t>(num_kv_heads) *
                         (num_groups + static_cast<int64_t>(batch) * group / kPrefixUnitRows);
-  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_prefix_len) + 127) / 128);
+  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_prefix_len) + 63) / 64);
   const int ranges = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(1, units * tiles)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   pkv_status st = launch_prefix(p, ranges, group, head_dim, dtype, s);

@@ -253,9 +253,7 @@ struct DecodeTraits {
   static constexpr int kNV = kTPG * G;                         // partial scores per lane
   static constexpr int kNF = (kNV >= kLPT) ? kNV / kLPT : 1;   // held scores after reduce-scatter
   static_assert(kNF == (G >= 2 ? G / 2 : 1), "lane/head mapping");
-  static_assert(!MMA || ((G >= 2 || std::is_same<KV, U8>::value) && G <= 8 && (D * kEsz) % 128 == 0 &&
-                          (kEsz == 2 || D * kEsz == 128)),
-                "tensor-core variant");
+  static_assert(!MMA || (G <= 8 && (D * kEsz) % 128 == 0 && (kEsz == 2 || D * kEsz == 128)), "tensor-core variant");
   // INT8 through the tensor cores: V slabs are stored transposed ([d][16]
   // token columns, see append_int8.cu) and staged by a plain 1-D copy
   static constexpr bool kVT = MMA && std::is_same<KV, U8>::value;
@@ -425,7 +423,7 @@ __device__ __noinline__ void clear_rows(uint32_t vslab, int r0, int lane) {
 // the decode kernel
 // ---------------------------------------------------------------------------
 template <typename QT, typename KV, int D, int G, int NW, bool MMA, Source SRC>
-__global__ void __launch_bounds__((NW + 1) * 32, MMA ? 3 : 1) paged_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1) paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<D, G, NW, KV, MMA>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =

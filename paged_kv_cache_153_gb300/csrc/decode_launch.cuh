@@ -25,6 +25,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kSmemPerSm = 233472;        // shared memory per SM on sm_100-class parts (228 KiB)
 constexpr int kSmemReservedPerCta = 1024; // system-reserved shared memory per resident block
 constexpr int kMaxStagesPerWarp = 8;
+constexpr size_t kRestSmem = 64 * 1024;   // kRest: what the shared-prefix kernel leaves free on its SM
 
 // the runtime's answers about one kernel variant on one device
 constexpr int kOccupancyEntries = 8;
@@ -64,6 +65,10 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
     if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn)),
                     "cudaFuncSetAttribute"))
       return PKV_ERR_CUDA;
+    if (SRC == kRest && cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                         cudaSharedmemCarveoutMaxShared),
+                                    "cudaFuncSetAttribute"))
+      return PKV_ERR_CUDA;
     cache.dyn_max = dyn;
   }
   const size_t dyn_max = cache.dyn_max;
@@ -96,7 +101,7 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   // stage ring per block beats more consumer warps (with the combine released
   // early, below: the mixed-length 64-sequence GQA batch 76.1 us at 2 against
   // 77.4 at 3).
-  const int want = li.max_ctas_per_sm > 0 ? li.max_ctas_per_sm : (MMA && Tr::kEsz == 1) ? 3 : 2;
+  const int want = SRC == kRest ? 1 : li.max_ctas_per_sm > 0 ? li.max_ctas_per_sm : (MMA && Tr::kEsz == 1) ? 3 : 2;
   // Cost of one (sequence, KV head) in the balanced split, in quarter blocks:
   // the per-segment work (query load, cross-warp merge, output or partial
   // write) and the consumer warps left idle by short segments.  Measured on
@@ -113,7 +118,8 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   } else {
     for (int cand = kMaxStagesPerWarp; cand >= 1; --cand) {
       const size_t s = Tr::smem_bytes(NW * cand, p.batch, p.n_kv_heads);
-      if (s <= dyn_max && static_cast<size_t>(occ) * (s + kSmemReservedPerCta) <= kSmemPerSm) {
+      if (s <= (SRC == kRest ? std::min(dyn_max, kRestSmem) : dyn_max) &&
+          static_cast<size_t>(occ) * (s + kSmemReservedPerCta) <= kSmemPerSm) {
         spw = cand;
         break;
       }
@@ -161,18 +167,20 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   }
   if (cuda_failed(launch_pdl(kern, dim3(grid), dim3(Tr::kThreads), smem, stream, p), "paged_decode_kernel launch"))
     return PKV_ERR_CUDA;
-  const int units = p.batch * p.n_kv_heads;
-  if (SRC != kRest && units > 0) {
-    // a partition split of long contexts can leave many pieces per (sequence,
-    // KV head) (one per range it meets): merge those with several lanes per output
-    const bool wide = p.part_blocks > 0 && (p.max_nblk + p.part_blocks - 1) / p.part_blocks >= 16;
-    const cudaError_t e =
-        wide ? launch_pdl(paged_decode_combine_wide_kernel<QT, D, G>, dim3(units),
-                          dim3(combine_threads<D, G>()), 0, stream, p, grid)
-             : launch_pdl(paged_decode_combine_warps_kernel<QT, D, G>,
-                          dim3((units + kCombineWarps - 1) / kCombineWarps), dim3(kCombineWarps * 32), 0, stream,
-                          p, grid);
-    if (cuda_failed(e, "combine kernel launch")) return PKV_ERR_CUDA;
+  if constexpr (SRC != kRest) {
+    const int units = p.batch * p.n_kv_heads;
+    if (units > 0) {
+      // a partition split of long contexts can leave many pieces per (sequence,
+      // KV head) (one per range it meets): merge those with several lanes per output
+      const bool wide = p.part_blocks > 0 && (p.max_nblk + p.part_blocks - 1) / p.part_blocks >= 16;
+      const cudaError_t e =
+          wide ? launch_pdl(paged_decode_combine_wide_kernel<QT, D, G>, dim3(units),
+                            dim3(combine_threads<D, G>()), 0, stream, p, grid)
+               : launch_pdl(paged_decode_combine_warps_kernel<QT, D, G>,
+                            dim3((units + kCombineWarps - 1) / kCombineWarps), dim3(kCombineWarps * 32), 0, stream,
+                            p, grid);
+      if (cuda_failed(e, "combine kernel launch")) return PKV_ERR_CUDA;
+    }
   }
   return PKV_OK;
 }
@@ -191,6 +199,7 @@ DecodeLauncher decode_launcher_rest(int q_dtype, int head_dim, int group);
 
 constexpr int kCoreWarps = 8;   // consumer warps of the CUDA-core variant
 constexpr int kMmaWarps = 4;    // consumer warps of the tensor-core variant
+constexpr int kRestWarps = 3;   // and of kRest, which shares its SM with the prefix kernel (4 warps at 128 registers)
 
 // G = 1 uses the CUDA-core consumer; G >= 2 over a 16-bit cache, or over a
 // one-byte (E4M3, E5M2 or INT8) cache with 128-byte rows, uses the tensor-core
@@ -200,7 +209,9 @@ template <typename QT, typename KV, int D, int G, Source SRC>
 DecodeLauncher pick_variant() {
   // (an INT8 cache with 128-byte rows takes the tensor-core consumer for every
   // group size: its V slabs are stored transposed for that consumer)
-  if constexpr ((G >= 2 || std::is_same<KV, U8>::value) && (KV::kBytes == 2 || D * KV::kBytes == 128))
+  if constexpr (SRC == kRest)
+    return launch_decode_variant<QT, KV, D, G, kRestWarps, true, SRC>;
+  else if constexpr ((G >= 2 || std::is_same<KV, U8>::value) && (KV::kBytes == 2 || D * KV::kBytes == 128))
     return launch_decode_variant<QT, KV, D, G, kMmaWarps, true, SRC>;
   else
     return launch_decode_variant<QT, KV, D, G, kCoreWarps, false, SRC>;

@@ -19,26 +19,33 @@
 // equal ranges, one per thread block; a range meets one or more units, and
 // each meeting leaves one fp32 state per row (a piece).
 //
-// Tiles.  Two chains of S = Q K^T -> softmax -> O += P V run at a time, each
-// with its own S / P columns, O columns and softmax warps, so that the tensor
-// cores work for one while the other's softmax runs:
+// Tiles.  Two chains of S = Q K^T -> softmax -> O += P V run at a time over
+// 64-key tiles, each with two S / P buffers, its O columns and four softmax
+// warps, so that the tensor cores work on other operations while one's softmax
+// runs:
 //   more than 128 rows   the chains are two row tiles against the same K / V
 //                        tiles, each tile loaded once for both;
 //   up to 128 rows       the chains are the even and the odd key tiles of one
 //                        row tile; their states are joined in registers.
-// K / V tiles are 8 cache blocks, gathered by TMA boxes of [16 rows x 128 B]
-// into 128-byte-swizzled K-major tiles, two stages each.  P overwrites its own
-// S in TMEM (32 columns of scores become 16 of P pairs, and for bf16 16 more
-// of the remainder); the product reads it from there.  bf16 P is multiplied as
-// two bf16 parts (p truncated, and the rounded remainder: exact to 2^-16),
-// because one bf16 rounding of p (2^-9) would be as large as the output's own;
-// fp16 P (2^-12) is used as it is.  The row reference m moves only when a
-// tile's maximum exceeds it by more than 2^8.
+// Q tiles come by one TMA box per 64 columns (G heads x 128 / G sequences: the
+// rows of a unit in order); K / V tiles are 4 cache blocks, gathered by boxes of
+// [16 rows x 128 B] into 128-byte-swizzled K-major tiles, three stages each.  P
+// overwrites its own S in TMEM (32 columns of scores become 16 of P pairs, and
+// for bf16 16 more of the remainder); the product reads it from there.  bf16 P
+// is multiplied as two bf16 parts (p truncated, and the rounded remainder:
+// exact to 2^-16), because one bf16 rounding of p (2^-9) would be as large as
+// the output's own; fp16 P (2^-12) is used as it is.  The row reference m moves
+// only when a tile's maximum exceeds it by more than 2^8.
 //
 // Warps 0-3 and 4-7: softmax of chain 0 and 1, one thread per row; warp 8:
 // TMA producer; warp 9: TMEM owner, and its elected lane issues every MMA, in
-// the order Q K of op k + 2 behind P V of op k (the same columns: MMAs of one
+// the order Q K of op k + 4 behind P V of op k (the same columns: MMAs of one
 // thread run in issue order).  Waits are bounded as in the other kernels.
+//
+// Beside it.  The kernel leaves room on its SM (registers: 128 a thread; shared
+// memory: about 64 KiB) for one thread block of the decode over the sequences'
+// own blocks, which is bound by memory where this one is bound by the tensor
+// cores; that kernel launches as soon as this one has started.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -52,30 +59,37 @@
 namespace pkv {
 
 constexpr int kXThreads = 320;
-constexpr int kXTile = 128;                       // query rows of a chain's tile, and keys of a K / V tile
-constexpr int kXTileBlocks = kXTile / kBlockSize;
-constexpr int kXStages = 2;                       // of K and of V
+constexpr int kXRows = 128;                       // query rows of a chain's tile
+constexpr int kXKeys = 64;                        // keys of a K / V tile
+constexpr int kXTileBlocks = kXKeys / kBlockSize;
+constexpr int kXStages = 3;                       // of K and of V
+constexpr int kXAhead = 4;                        // Q K^T operations in flight: two S / P buffers of two chains
 constexpr float kXRescaleLog2 = 8.f;
-constexpr int kXHalf = kXTile * 128;              // bytes of a 64-column half of a 16-bit tile
+constexpr int kXHalfQ = kXRows * 128;             // bytes of a 64-column half of a Q tile
+constexpr int kXHalfKV = kXKeys * 128;            // and of a K / V tile
 
 template <int D>
 struct PrefixSmem {
-  static constexpr int kTileBytes = kXTile * D * 2;
+  static constexpr int kQTile = kXRows * D * 2, kKVTile = kXKeys * D * 2;
   static constexpr int kQ = 0;                                 // [2] row tiles
-  static constexpr int kK = 2 * kTileBytes;                    // [kXStages]
-  static constexpr int kV = kK + kXStages * kTileBytes;
-  static constexpr int kBar = kV + kXStages * kTileBytes;      // 256 bytes
+  static constexpr int kK = 2 * kQTile;                        // [kXStages]
+  static constexpr int kV = kK + kXStages * kKVTile;
+  static constexpr int kBar = kV + kXStages * kKVTile;         // 256 bytes
   static constexpr int kRed = kBar + 256;                      // float2 [2][128]: a chain's (m, l)
-  static constexpr int kGroups = kRed + 2 * kXTile * 8;        // PrefixGroup [num_groups + 1]
+  static constexpr int kGroups = kRed + 2 * kXRows * 8;        // PrefixGroup [num_groups + 1]
   static size_t bytes(int num_groups) {
     return 1024 + kGroups + sizeof(PrefixGroup) * (static_cast<size_t>(num_groups) + 1);
   }
 };
 
-// 16-byte chunk c of row r in a tile: 64-column halves, 8-row atoms of 1 KiB,
-// chunk index XOR row within the atom
-__device__ __forceinline__ uint32_t xtile_off(int r, int c) {
-  return (c >> 3) * kXHalf + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+// tiled TMA load of a 3-D box
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+      "%3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
 }
 
 // 32 bytes in one store
@@ -83,6 +97,38 @@ __device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+// Write 32 consecutive columns of a warp's 32 rows (lane = row; o: its 32
+// columns; dst: column 0 of the warp's row 0; rows from n on are not written).
+// Four lanes exchange 32-byte pieces first, so that a store covers the whole
+// 128 bytes of 8 rows instead of a quarter of 32.
+template <int D>
+__device__ __forceinline__ void store_rows32(float* dst, const float* o, int n, int lane) {
+  float t[4][8];   // piece j: columns 8 j .. of this lane's row, then of row 4 (lane / 4) + j
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[j][e] = o[8 * j + e];
+#pragma unroll
+  for (int m = 1; m <= 2; m <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((j & m) == 0) {
+        // lanes with bit m clear give piece j + m and get piece j of their partner's row
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float give = up ? t[j][e] : t[j + m][e];
+          const float got = __shfl_xor_sync(0xffffffffu, give, m);
+          if (up) t[j][e] = got; else t[j + m][e] = got;
+        }
+      }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = (lane & ~3) + j;
+    if (row < n) st_global_v8(dst + static_cast<int64_t>(row) * D + 8 * (lane & 3), t[j]);
+  }
 }
 
 // a piece of a range: key tiles [t0, t1) of one unit
@@ -115,43 +161,69 @@ __device__ __forceinline__ PrefixSeg prefix_segment(const PrefixGroup* groups, i
   s.t1 = static_cast<int>(min(static_cast<int64_t>(kt), s.t0 + (end - pos)));
   s.next = pos + (s.t1 - s.t0);
   s.rows = min(kPrefixUnitRows, gr.rows - s.unit * kPrefixUnitRows);
-  s.share = s.rows > kXTile;
+  s.share = s.rows > kXRows;
   s.row = piece_row(gr.start, n_q_heads, s.g, gr.rows, s.unit, range);
   return s;
 }
 
+// (512 threads a block as far as the registers go: 128 a thread)
 template <typename QT, int D, int G>
-__global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = PrefixSmem<D>;
   constexpr bool kSplit = std::is_same<QT, BF16>::value;
   extern __shared__ unsigned char xsm_raw[];
   unsigned char* sm = xsm_raw + ((1024 - (smem_u32(xsm_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
-  uint64_t* k_full = bars;                    // [2] K tile landed
-  uint64_t* k_empty = k_full + kXStages;      // [2] its Q K^T done
+  uint64_t* k_full = bars;                    // [kXStages] K tile landed
+  uint64_t* k_empty = k_full + kXStages;      // [kXStages] its Q K^T done
   uint64_t* v_full = k_empty + kXStages;
   uint64_t* v_empty = v_full + kXStages;
-  uint64_t* s_full = v_empty + kXStages;      // [2] per chain: scores ready
-  uint64_t* p_full = s_full + 2;              // [2] per chain, 128 arrivals: P written, O rescaled
-  uint64_t* pv_done = p_full + 2;             // [2] per chain
-  uint64_t* q_ready = pv_done + 2;            // 256 arrivals per piece
-  uint64_t* mma_idle = q_ready + 1;
+  uint64_t* s_full = v_empty + kXStages;      // [2 chains][2] scores ready
+  uint64_t* p_full = s_full + 4;              // [2 chains][2] 128 arrivals: P written, O rescaled
+  uint64_t* pv_done = p_full + 4;             // [2] per chain
+  uint64_t* q_full = pv_done + 2;             // Q of a piece landed
+  uint64_t* mma_idle = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((4 * kXStages + 4 + 4 + 2 + 1 + 1 + 1) * 8 <= 256, "barrier block overflows its 256 bytes");
   float2* red = reinterpret_cast<float2*>(sm + L::kRed);
   PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::kGroups);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 8 * 32) {
+    *abort_flag = 0;
+    for (int s = 0; s < kXStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], kXRows);
+    }
+    mbar_init(&pv_done[0], 1);
+    mbar_init(&pv_done[1], 1);
+    mbar_init(q_full, 1);
+    mbar_init(mma_idle, 1);
+    fence_mbar_init();
+  }
   pdl_wait();
   pdl_release();   // (the next kernel, over the sequences' own blocks, reads only inputs before its wait)
 
   // ---- the groups: shared blocks, first covering sequence, cost ------------
   for (int j = warp; j < p.num_groups; j += kXThreads / 32) {
-    const int raw0 = p.group_starts[j], raw1 = p.group_starts[j + 1];
+    const int raw0 = p.group_starts[j], raw1 = p.group_starts[j + 1], len = p.prefix_lens[j];
     const int s0 = min(max(raw0, 0), p.batch), s1 = min(max(raw1, s0), p.batch);
     if ((raw0 != s0 || raw1 != s1 || (j == 0 && raw0 != 0) || (j == p.num_groups - 1 && raw1 != p.batch)) && lane == 0)
       record_error(p.err, PKV_ERR_OOB);
-    const int blocks = max(p.prefix_lens[j], 0) / kBlockSize;
+    const int blocks = max(len, 0) / kBlockSize;
     int owner = -1;
     if (blocks > 0)
       for (int b0 = s0; b0 < s1 && owner < 0; b0 += 32) {
@@ -169,29 +241,6 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
       gr.cost = static_cast<int64_t>(p.n_kv_heads) * prefix_units(gr.rows) * prefix_tiles(gr.blocks);
       groups[j] = gr;
     }
-  }
-  if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (tid == 0) {
-    *abort_flag = 0;
-    for (int s = 0; s < kXStages; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
-    }
-    for (int c = 0; c < 2; ++c) {
-      mbar_init(&s_full[c], 1);
-      mbar_init(&p_full[c], kXTile);
-      mbar_init(&pv_done[c], 1);
-    }
-    mbar_init(q_ready, 2 * kXTile);
-    mbar_init(mma_idle, 1);
-    fence_mbar_init();
   }
   __syncthreads();
   if (warp == 0) {   // exclusive prefix of the costs
@@ -219,172 +268,143 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
   const int64_t V = groups[p.num_groups].cost, R = gridDim.x, range = blockIdx.x;
   const int64_t first = (range * V) / R, end = ((range + 1) * V) / R;
   auto segment = [&](int64_t pos) { return prefix_segment(groups, p.num_groups, p.n_q_heads, pos, end, range); };
+  // S / P buffer x = 2 chain + buffer at columns 64 x, O of a chain at 256 + chain D
+  constexpr int kOCol = 4 * kXKeys;
 
   if (warp < 8) {
     // ============================ softmax / epilogue ============================
-    const int chain = warp >> 2, r = tid & (kXTile - 1);
+    const int chain = warp >> 2, r = tid & (kXRows - 1);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + chain * kXTile;
-    const uint32_t t_o = tmem + lane_base + 2 * kXTile;          // chain c's columns at + c D
+    const uint32_t t_o = tmem + lane_base + kOCol;
     uint32_t ops = 0;                                            // this chain's operations so far
     bool ok = true;
     for (int64_t pos = first; pos < end;) {
       const PrefixSeg sg = segment(pos);
       pos = sg.next;
-      const PrefixGroup gr = groups[sg.group];
       const int n_tiles = sg.t1 - sg.t0;
-      const int unit_row = sg.share ? chain * kXTile + r : r;    // row of the unit
-      const bool live = unit_row < sg.rows;
-      {
-        // stage this row of Q (zeros behind the unit's rows); with one row tile
-        // the two warpgroups share it
-        const int row = sg.unit * kPrefixUnitRows + (live ? unit_row : 0);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const unsigned char*>(p.q) +
-            ((static_cast<int64_t>(gr.start) + row / G) * p.n_q_heads + sg.g * G + row % G) * D * 2);
-        const uint32_t dst = smem_u32(sm + L::kQ + (sg.share ? chain * L::kTileBytes : 0));
-        const int c0 = sg.share ? 0 : chain * (D / 16), c1 = sg.share ? D / 8 : c0 + D / 16;
-#pragma unroll 8
-        for (int c = c0; c < c1; ++c) {
-          const uint4 v = live ? src[c] : make_uint4(0, 0, 0, 0);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + xtile_off(r, c)), "r"(v.x), "r"(v.y),
-                       "r"(v.z), "r"(v.w)
-                       : "memory");
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();   // (the previous piece's reads of O come before the MMAs this releases)
-        mbar_arrive(q_ready);
-      }
+      const int blocks = groups[sg.group].blocks;
       float m_ref = -INFINITY, l_run = 0.f;
       int mine = 0;                                              // operations of this chain in this piece
       const int step = sg.share ? 1 : 2;
-      for (int n = sg.share ? 0 : chain; n < n_tiles && ok; n += step, ++mine, ++ops) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[chain], ops & 1, p.err)) && !*abort_flag;
-        ok = __all_sync(0xffffffffu, ok);
+      for (int n = sg.share ? 0 : chain; n < n_tiles; n += step, ++mine, ++ops) {
+        const int x = 2 * chain + (ops & 1);
+        const uint32_t t_s = tmem + lane_base + x * kXKeys;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], (ops >> 1) & 1, p.err) && !*abort_flag);
         if (!ok) break;
         tc_fence_after();
         // keys of the tile that the prefix holds (whole blocks; the last tile may be short)
-        const int valid = min(kXTile, (gr.blocks - (sg.t0 + n) * kXTileBlocks) * kBlockSize);
+        const int valid = min(kXKeys, (blocks - (sg.t0 + n) * kXTileBlocks) * kBlockSize);
         float v[64];
         tmem_ld64(t_s, v);
-        if (valid < 64) {
+        if (valid < kXKeys) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = i < valid ? v[i] : -INFINITY;
         }
-        float mx = max64(v);
-        tmem_ld64(t_s + 64, v);
-        if (valid < kXTile) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) v[i] = 64 + i < valid ? v[i] : -INFINITY;
-        }
-        mx = fmaxf(mx, max64(v));
-        const float m_tile = mx * p.qk_scale_log2;
+        const float m_tile = max64(v) * p.qk_scale_log2;
         float alpha = 1.f;
         if (m_tile > m_ref + kXRescaleLog2) {
           alpha = ex2_approx(m_ref - m_tile);
           m_ref = m_tile;
         }
         if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O may be touched once the chain's previous P V has completed
+          // O may be touched once the chain's previous P V has completed (the
+          // one before it has: these scores were asked for behind it)
           ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + chain * D + c, o);
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(t_o + chain * D + c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(t_o + chain * D + c, o);
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(t_o + chain * D + c, o);
           }
         }
         const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const uint64_t scale2 = f32x2(p.qk_scale_log2, p.qk_scale_log2), nref2 = f32x2(nref, nref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        // the columns in registers are the upper 64; the lower ones are read again
-#pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-          if (half == 0) {
-            tmem_ld64(t_s, v);
-            if (valid < 64) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] = i < valid ? v[i] : -INFINITY;
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 e2 = f32x2_split(fma_f32x2(f32x2(v[32 * c + i], v[32 * c + i + 1]), scale2, nref2));
+            const float e0 = ex2_approx(e2.x), e1 = ex2_approx(e2.y);
+            const uint64_t e01 = f32x2(e0, e1);
+            acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
+            if constexpr (kSplit) {
+              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+              pk[i / 2] = __byte_perm(b0, b1, 0x7632);
+              const float2 lo = f32x2_split(
+                  sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
+              pk[16 + i / 2] = pack2(lo.x, lo.y, QT{});
+            } else {
+              pk[i / 2] = pack2(e0, e1, QT{});
             }
           }
-          uint32_t pk2[64];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t* pk = pk2 + 32 * c;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 x = f32x2_split(fma_f32x2(f32x2(v[32 * c + i], v[32 * c + i + 1]), scale2, nref2));
-              const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
-              const uint64_t e01 = f32x2(e0, e1);
-              acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
-              if constexpr (kSplit) {
-                const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
-                pk[i / 2] = __byte_perm(b0, b1, 0x7632);
-                const float2 lo = f32x2_split(
-                    sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
-                pk[16 + i / 2] = pack2(lo.x, lo.y, QT{});
-              } else {
-                pk[i / 2] = pack2(e0, e1, QT{});
-              }
-            }
-            if constexpr (!kSplit) tmem_st16u(t_s + 64 * half + 32 * c, pk);
-          }
-          if constexpr (kSplit) tmem_st64u(t_s + 64 * half, pk2);
+          if constexpr (kSplit)
+            tmem_st32u(t_s + 32 * c, pk);
+          else
+            tmem_st16u(t_s + 32 * c, pk);
         }
         const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
         tmem_wait_st();
         l_run = l_run * alpha + (s0.x + s0.y);
         tc_fence_before();
-        mbar_arrive(&p_full[chain]);
+        mbar_arrive(&p_full[x]);
       }
-      // the piece's states; both warpgroups meet here (a failed wait ends both)
-      if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
-      if (!sg.share) red[chain * kXTile + r] = make_float2(m_ref, l_run);
-      if (named_bar_red_or(1, 2 * kXTile, !ok)) {
+      // the piece's states; both warpgroups meet here (a failed wait ends both).
+      // The last scores only say that the P V two operations back is done (Q K^T
+      // runs that far ahead), and a parity names one of two neighbouring phases:
+      // so the one before the last is waited for first.
+      for (int back = min(mine, 2); back >= 1 && ok; --back)
+        ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - back) & 1, p.err));
+      if (!sg.share) red[chain * kXRows + r] = make_float2(m_ref, l_run);
+      if (named_bar_red_or(1, 2 * kXRows, !ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int64_t out_row = sg.row + unit_row;
+      const int row0 = (sg.share ? chain * kXRows : 0) + (warp & 3) * 32;   // the warp's first row of the unit
+      const int n_rows = sg.rows - row0;                                    // those that exist (of 32)
+      float* dst = p.o + (sg.row + row0) * D;
       if (sg.share) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(t_o + chain * D + c, o);
-          if (live)
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) st_global_v8(p.o + out_row * D + c + i, o + i);
+          store_rows32<D>(dst + c, o, n_rows, lane);
         }
-        if (live) *reinterpret_cast<float2*>(p.ml + out_row * 2) = make_float2(m_ref, l_run);
+        if (lane < n_rows) *reinterpret_cast<float2*>(p.ml + (sg.row + row0 + lane) * 2) = make_float2(m_ref, l_run);
       } else {
         // join the two key streams: each warpgroup takes half of the columns
-        const float2 a = red[r], b = red[kXTile + r];
+        const float2 a = red[r], b = red[kXRows + r];
         const float m = fmaxf(a.x, b.x), ref = (m == -INFINITY) ? 0.f : m;
         const float wa = ex2_approx(a.x - ref), wb = ex2_approx(b.x - ref);
+        if (n_rows > 0) {
 #pragma unroll 1
-        for (int c = chain * (D / 2); c < (chain + 1) * (D / 2); c += 32) {
-          float o[32];
-          tmem_ld32(t_o + c, o);
+          for (int c = chain * (D / 2); c < (chain + 1) * (D / 2); c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= wa;
-          if (n_tiles > 1) {
-            float o2[32];
-            tmem_ld32(t_o + D + c, o2);
+            for (int i = 0; i < 32; ++i) o[i] *= wa;
+            if (n_tiles > 1) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(o2[i], wb, o[i]);
+              for (int h = 0; h < 32; h += 16) {
+                float o2[16];
+                tmem_ld16(t_o + D + c + h, o2);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[h + i] = fmaf(o2[i], wb, o[h + i]);
+              }
+            }
+            store_rows32<D>(dst + c, o, n_rows, lane);
           }
-          if (live)
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) st_global_v8(p.o + out_row * D + c + i, o + i);
+          if (lane < n_rows && chain == 0)
+            *reinterpret_cast<float2*>(p.ml + (sg.row + row0 + lane) * 2) = make_float2(m, a.y * wa + b.y * wb);
         }
-        if (live && chain == 0)
-          *reinterpret_cast<float2*>(p.ml + out_row * 2) = make_float2(m, a.y * wa + b.y * wb);
         tc_fence_before();
-        named_bar_sync(2, 2 * kXTile);   // both have read red and the other's O
+        named_bar_sync(2, 2 * kXRows);   // both have read red and the other's O
         tc_fence_after();
       }
     }
@@ -392,7 +412,7 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
   } else if (warp == 8) {
     // ============================ TMA producer ============================
     uint32_t tiles = 0;                  // tiles loaded so far (K and V alike)
-    uint32_t issued_k = 0, issued_v = 0;
+    uint32_t issued_k = 0, issued_v = 0, issued_q = 0;
     bool good = true;
     for (int64_t pos = first; pos < end && good;) {
       const PrefixSeg sg = segment(pos);
@@ -404,37 +424,53 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
         const int blk = t * kXTileBlocks + lane;
         return (t < sg.t1 && lane < kXTileBlocks && blk < gr.blocks) ? row[blk] : -1;
       };
+      int id = fetch_id(sg.t0);
+      // Q of the piece, once every Q K^T of the one before has read its tiles
+      if (tiles > 0) {
+        const uint32_t last = tiles - 1;
+        good = __all_sync(0xffffffffu,
+                          mbar_wait(&k_empty[last % kXStages], (last / kXStages) & 1, p.err) && !*abort_flag);
+        if (!good) break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(q_full, L::kQTile * (sg.share ? 2 : 1));
+      ++issued_q;
+      __syncwarp();
+      if (lane < (sg.share ? 2 : 1) * (D / 64)) {
+        const int c = lane / (D / 64), h = lane % (D / 64);
+        tma_load_3d(sm + L::kQ + c * L::kQTile + h * kXHalfQ, &p.tmap_q, h * 64, sg.g * G,
+                    gr.start + (sg.unit * kPrefixUnitRows + c * kXRows) / G, q_full, policy_evict_last());
+      }
+      __syncwarp();
       // cache row of this lane's block: a block behind the prefix, or a bad id,
       // is read from rows outside the tensor, which TMA fills with zeros
-      auto to_row = [&](int t, int id) -> int {
+      auto to_row = [&](int t, int block_id) -> int {
         const int blk = t * kXTileBlocks + lane;
-        if (lane < kXTileBlocks && blk < gr.blocks && (id < 0 || id >= p.num_blocks)) {
+        if (lane < kXTileBlocks && blk < gr.blocks && (block_id < 0 || block_id >= p.num_blocks)) {
           record_error(p.err, PKV_ERR_OOB);
-          id = -1;
+          block_id = -1;
         }
-        return (id >= 0) ? (id * p.n_kv_heads + sg.g) * kBlockSize : -2 * kBlockSize;
+        return (block_id >= 0) ? (block_id * p.n_kv_heads + sg.g) * kBlockSize : -2 * kBlockSize;
       };
+      // lane j + 4 h: half h of the tile's block j
       auto load = [&](bool is_v, int y) -> bool {
         const uint32_t s = tiles % kXStages, use = tiles / kXStages;
         uint64_t* full = is_v ? &v_full[s] : &k_full[s];
         uint64_t* empty = is_v ? &v_empty[s] : &k_empty[s];
         const bool freed = use == 0 || mbar_wait(empty, (use - 1) & 1, p.err);
         if (!__all_sync(0xffffffffu, freed && !*abort_flag)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(full, L::kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(full, L::kKVTile);
         __syncwarp();
-        if (lane < kXTileBlocks) {
-          unsigned char* dst = sm + (is_v ? L::kV : L::kK) + s * L::kTileBytes + lane * 2048;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_2d(dst + h * kXHalf, is_v ? &p.tmap_v : &p.tmap_k, h * 64, y, full, pol);
+        if (lane < kXTileBlocks * (D / 64)) {
+          const int j = lane % kXTileBlocks, h = lane / kXTileBlocks;
+          tma_load_2d(sm + (is_v ? L::kV : L::kK) + s * L::kKVTile + h * kXHalfKV + j * 2048,
+                      is_v ? &p.tmap_v : &p.tmap_k, h * 64, y, full, pol);
         }
         __syncwarp();
         (is_v ? issued_v : issued_k) = tiles + 1;
         return true;
       };
-      int id = fetch_id(sg.t0);
       for (int t = sg.t0; t < sg.t1 && good; ++t) {
-        const int y = to_row(t, id);
+        const int y = __shfl_sync(0xffffffffu, to_row(t, id), lane % kXTileBlocks);
         id = fetch_id(t + 1);
         good = load(false, y) && load(true, y);
         ++tiles;
@@ -444,6 +480,7 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
     if (*abort_flag && lane == 0) {
       // loads this warp issued that nobody may have waited for (bounded)
       const unsigned long long deadline = global_ns() + kWaitLimitNs;
+      if (issued_q > 0) mbar_wait_until(q_full, (issued_q - 1) & 1, deadline);
       for (uint32_t t = issued_k > kXStages ? issued_k - kXStages : 0; t < issued_k; ++t)
         mbar_wait_until(&k_full[t % kXStages], (t / kXStages) & 1, deadline);
       for (uint32_t t = issued_v > kXStages ? issued_v - kXStages : 0; t < issued_v; ++t)
@@ -452,11 +489,11 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
   } else {
     // ============================ MMA issuer (warp 9) ============================
     constexpr int kPasses = kSplit ? 2 : 1;
-    constexpr uint32_t kIdQK = umma_idesc<QT>(false, kXTile), kIdPV = umma_idesc<QT>(true, D);
+    constexpr uint32_t kIdQK = umma_idesc<QT>(false, kXKeys), kIdPV = umma_idesc<QT>(true, D);
     bool ok = true;
     if (lane == 0) {
       uint32_t tile0 = 0, piece = 0;       // K / V tiles and pieces before the current piece
-      uint32_t done[2] = {0, 0};           // P V operations of each chain so far
+      uint32_t asked[2] = {0, 0}, done[2] = {0, 0};   // Q K^T and P V operations of each chain so far
       for (int64_t pos = first; pos < end && ok; ++piece) {
         const PrefixSeg sg = segment(pos);
         pos = sg.next;
@@ -464,44 +501,43 @@ __global__ void __launch_bounds__(kXThreads, 1) prefix_kernel(const __grid_const
         const int n_ops = sg.share ? 2 * n_tiles : n_tiles;
         auto qk = [&](int k) -> bool {
           const uint32_t t = tile0 + (sg.share ? k >> 1 : k), s = t % kXStages;
-          const int c = k & 1;
+          const int c = k & 1, x = 2 * c + (asked[c] & 1);
           if (!mbar_wait(&k_full[s], (t / kXStages) & 1, p.err) || *abort_flag) return false;
-          const uint64_t a0 =
-              umma_desc(smem_u32(sm + L::kQ + (sg.share ? c * L::kTileBytes : 0)), 16, 1024);
-          const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + s * L::kTileBytes), 16, 1024);
+          ++asked[c];
+          const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (sg.share ? c * L::kQTile : 0)), 16, 1024);
+          const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + s * L::kKVTile), 16, 1024);
           tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t koff = static_cast<uint64_t>(((ks >> 2) * kXHalf + (ks & 3) * 32) >> 4);
-            umma_f16(tmem + c * kXTile, a0 + koff, b0 + koff, kIdQK, ks > 0);
-          }
-          umma_commit(&s_full[c]);
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_f16(tmem + x * kXKeys, a0 + static_cast<uint64_t>(((ks >> 2) * kXHalfQ + (ks & 3) * 32) >> 4),
+                     b0 + static_cast<uint64_t>(((ks >> 2) * kXHalfKV + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
+          umma_commit(&s_full[x]);
           if (!sg.share || c == 1) umma_commit(&k_empty[s]);
           return true;
         };
         auto pv = [&](int k) -> bool {
           const uint32_t t = tile0 + (sg.share ? k >> 1 : k), s = t % kXStages;
-          const int c = k & 1;
-          if (!mbar_wait(&p_full[c], done[c] & 1, p.err) || !mbar_wait(&v_full[s], (t / kXStages) & 1, p.err) ||
-              *abort_flag)
+          const int c = k & 1, x = 2 * c + (done[c] & 1);
+          if (!mbar_wait(&p_full[x], (done[c] >> 1) & 1, p.err) ||
+              !mbar_wait(&v_full[s], (t / kXStages) & 1, p.err) || *abort_flag)
             return false;
           ++done[c];
           tc_fence_after();
-          const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + s * L::kTileBytes), kXHalf, 1024);
-          const uint32_t a0 = tmem + c * kXTile, d = tmem + 2 * kXTile + c * D;
+          const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + s * L::kKVTile), kXHalfKV, 1024);
+          const uint32_t a0 = tmem + x * kXKeys, d = tmem + kOCol + c * D;
 #pragma unroll
           for (int pass = 0; pass < kPasses; ++pass)
 #pragma unroll
-            for (int ks = 0; ks < kXTile / 16; ++ks)
+            for (int ks = 0; ks < kXKeys / 16; ++ks)
               umma_f16_tmem_a(d, a0 + 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1),
                               b0 + static_cast<uint64_t>((ks * 2048) >> 4), kIdPV, k > 1 || ks > 0 || pass > 0);
           umma_commit(&pv_done[c]);
           if (!sg.share || c == 1) umma_commit(&v_empty[s]);
           return true;
         };
-        ok = mbar_wait(q_ready, piece & 1, p.err) && !*abort_flag;
-        for (int k = 0; k < min(2, n_ops) && ok; ++k) ok = qk(k);
-        for (int k = 0; k < n_ops && ok; ++k) ok = pv(k) && (k + 2 >= n_ops || qk(k + 2));
+        ok = mbar_wait(q_full, piece & 1, p.err) && !*abort_flag;
+        for (int k = 0; k < min(kXAhead, n_ops) && ok; ++k) ok = qk(k);
+        for (int k = 0; k < n_ops && ok; ++k) ok = pv(k) && (k + kXAhead >= n_ops || qk(k + kXAhead));
         tile0 += n_tiles;
       }
       if (!ok) *abort_flag = 1;
@@ -664,6 +700,10 @@ pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t strea
     if (!done[dev]) {
       if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(PrefixSmem<D>::bytes(kMaxPrefixGroups))),
+                      "cudaFuncSetAttribute") ||
+          // (the SM's whole shared memory, so that what this kernel leaves is the next one's)
+          cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           cudaSharedmemCarveoutMaxShared),
                       "cudaFuncSetAttribute"))
         return PKV_ERR_CUDA;
       done[dev] = true;

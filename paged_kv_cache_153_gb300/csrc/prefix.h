@@ -11,7 +11,7 @@ namespace pkv {
 constexpr int kMaxPrefixGroups = 1024;   // groups whose geometry a thread block keeps in shared memory
 constexpr int kPrefixUnitRows = 256;     // query rows of one unit of work: two tiles of 128
 
-// one group's share of the work; cost counts (unit, 128-key tile) pairs
+// one group's share of the work; cost counts (unit, 64-key tile) pairs
 struct PrefixGroup {
   int64_t cost;                  // of all groups before it
   int32_t start;                 // its first sequence
@@ -23,7 +23,7 @@ struct PrefixGroup {
 struct PrefixParams {
   CUtensorMap tmap_k;            // [NB * Hkv * 16 rows, D] 16-bit, [16 x 64] boxes, 128B swizzle
   CUtensorMap tmap_v;
-  const void* q;                 // [B, Hq, D]
+  CUtensorMap tmap_q;            // [B, Hq, D] 16-bit, boxes of [128 / G, G, 64], 128B swizzle
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* group_starts;   // [num_groups + 1]
