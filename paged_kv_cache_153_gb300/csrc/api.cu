@@ -610,7 +610,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   // as many ranges as SMs, but no more than there can be key tiles
   const int64_t units = static_cast<int64_t>(num_kv_heads) *
                         (num_groups + static_cast<int64_t>(batch) * group / kPrefixUnitRows);
-  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_prefix_len) + 63) / 64);
+  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_prefix_len) + 127) / 128);
   const int ranges = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(1, units * tiles)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   pkv_status st = launch_prefix(p, ranges, group, head_dim, dtype, s);

@@ -565,7 +565,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
   auto first_writes = [&]() {
     if (writes_done) return;
     writes_done = true;
-    pdl_wait();
+    // (kRest runs beside the shared-prefix kernel: that kernel started after
+    // everything before it had completed, and touches none of what this one
+    // writes, so nothing is waited for until the end)
+    if constexpr (SRC != kRest) pdl_wait();
     if (blockIdx.x == 0 && p.ws_cum != nullptr)
       for (int b = tid; b <= p.batch; b += NW * 32) {
         p.ws_cum[b] = cum[b];
@@ -1436,6 +1439,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
     ++j;
   }
   first_writes();   // (a consumer group that wrote nothing: the wait, prefixes and new rows)
+  // (the merge that follows waits for this grid alone: it completes after the prefix kernel's)
+  if constexpr (SRC == kRest) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------

@@ -20,27 +20,28 @@
 // each meeting leaves one fp32 state per row (a piece).
 //
 // Tiles.  Two chains of S = Q K^T -> softmax -> O += P V run at a time over
-// 64-key tiles, each with two S / P buffers, its O columns and four softmax
-// warps, so that the tensor cores work on other operations while one's softmax
-// runs:
+// 128-key tiles, each with its own S / P columns, O columns and four softmax
+// warps, so that the tensor cores work for one while the other's softmax runs:
 //   more than 128 rows   the chains are two row tiles against the same K / V
 //                        tiles, each tile loaded once for both;
 //   up to 128 rows       the chains are the even and the odd key tiles of one
 //                        row tile; their states are joined in registers.
 // Q tiles come by one TMA box per 64 columns (G heads x 128 / G sequences: the
-// rows of a unit in order); K / V tiles are 4 cache blocks, gathered by boxes of
-// [16 rows x 128 B] into 128-byte-swizzled K-major tiles, three stages each.  P
-// overwrites its own S in TMEM (32 columns of scores become 16 of P pairs, and
-// for bf16 16 more of the remainder); the product reads it from there.  bf16 P
-// is multiplied as two bf16 parts (p truncated, and the rounded remainder:
-// exact to 2^-16), because one bf16 rounding of p (2^-9) would be as large as
-// the output's own; fp16 P (2^-12) is used as it is.  The row reference m moves
-// only when a tile's maximum exceeds it by more than 2^8.
+// rows of a unit in order); K / V tiles are 8 cache blocks, gathered by boxes of
+// [16 rows x 128 B] into 128-byte-swizzled K-major tiles (one stage of K, two of
+// V).  P overwrites its own S in TMEM (32 columns of scores become 16 of P
+// pairs, and for bf16 16 more of the remainder); the product reads it from
+// there.  bf16 P is multiplied as two bf16 parts (p truncated, and the rounded
+// remainder: exact to 2^-16), because one bf16 rounding of p (2^-9) would be as
+// large as the output's own; fp16 P (2^-12) is used as it is.  The row
+// reference m moves only when a tile's maximum exceeds it by more than 2^8.
+// 64-key tiles with two score buffers per chain, which hide the softmax's
+// latency entirely, were slower (67 us against 54 alone on 64 sequences behind
+// 32768 tokens): a [128 x 64 x 16] MMA takes as long as a [128 x 128 x 16] one.
 //
 // Warps 0-3 and 4-7: softmax of chain 0 and 1, one thread per row; warp 8:
-// TMA producer; warp 9: TMEM owner, and its elected lane issues every MMA, in
-// the order Q K of op k + 4 behind P V of op k (the same columns: MMAs of one
-// thread run in issue order).  Waits are bounded as in the other kernels.
+// TMA producer; warp 9: TMEM owner and Q K^T issuer, warp 10: P V issuer.
+// Waits are bounded as in the other kernels.
 //
 // Beside it.  The kernel leaves room on its SM (registers: 128 a thread; shared
 // memory: about 64 KiB) for one thread block of the decode over the sequences'
@@ -58,12 +59,11 @@
 
 namespace pkv {
 
-constexpr int kXThreads = 320;
+constexpr int kXThreads = 352;
 constexpr int kXRows = 128;                       // query rows of a chain's tile
-constexpr int kXKeys = 64;                        // keys of a K / V tile
+constexpr int kXKeys = 128;                       // keys of a K / V tile
 constexpr int kXTileBlocks = kXKeys / kBlockSize;
-constexpr int kXStages = 3;                       // of K and of V
-constexpr int kXAhead = 4;                        // Q K^T operations in flight: two S / P buffers of two chains
+constexpr int kXKStages = 1, kXVStages = 2;       // K and V tiles in shared memory
 constexpr float kXRescaleLog2 = 8.f;
 constexpr int kXHalfQ = kXRows * 128;             // bytes of a 64-column half of a Q tile
 constexpr int kXHalfKV = kXKeys * 128;            // and of a K / V tile
@@ -72,9 +72,9 @@ template <int D>
 struct PrefixSmem {
   static constexpr int kQTile = kXRows * D * 2, kKVTile = kXKeys * D * 2;
   static constexpr int kQ = 0;                                 // [2] row tiles
-  static constexpr int kK = 2 * kQTile;                        // [kXStages]
-  static constexpr int kV = kK + kXStages * kKVTile;
-  static constexpr int kBar = kV + kXStages * kKVTile;         // 256 bytes
+  static constexpr int kK = 2 * kQTile;                        // [kXKStages]
+  static constexpr int kV = kK + kXKStages * kKVTile;          // [kXVStages]
+  static constexpr int kBar = kV + kXVStages * kKVTile;        // 256 bytes
   static constexpr int kRed = kBar + 256;                      // float2 [2][128]: a chain's (m, l)
   static constexpr int kGroups = kRed + 2 * kXRows * 8;        // PrefixGroup [num_groups + 1]
   static size_t bytes(int num_groups) {
@@ -174,18 +174,18 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   extern __shared__ unsigned char xsm_raw[];
   unsigned char* sm = xsm_raw + ((1024 - (smem_u32(xsm_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
-  uint64_t* k_full = bars;                    // [kXStages] K tile landed
-  uint64_t* k_empty = k_full + kXStages;      // [kXStages] its Q K^T done
-  uint64_t* v_full = k_empty + kXStages;
-  uint64_t* v_empty = v_full + kXStages;
-  uint64_t* s_full = v_empty + kXStages;      // [2 chains][2] scores ready
-  uint64_t* p_full = s_full + 4;              // [2 chains][2] 128 arrivals: P written, O rescaled
-  uint64_t* pv_done = p_full + 4;             // [2] per chain
+  uint64_t* k_full = bars;                    // [kXKStages] K tile landed
+  uint64_t* k_empty = k_full + kXKStages;     // [kXKStages] its Q K^T done
+  uint64_t* v_full = k_empty + kXKStages;     // [kXVStages] V tile landed
+  uint64_t* v_empty = v_full + kXVStages;     // [kXVStages] its P V done
+  uint64_t* s_full = v_empty + kXVStages;     // [2] per chain: scores ready
+  uint64_t* p_full = s_full + 2;              // [2] per chain, 128 arrivals: P written, O rescaled
+  uint64_t* pv_done = p_full + 2;             // [2] per chain
   uint64_t* q_full = pv_done + 2;             // Q of a piece landed
-  uint64_t* mma_idle = q_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
+  uint64_t* mma_idle = q_full + 1;            // [2] an issuer's MMAs done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((4 * kXStages + 4 + 4 + 2 + 1 + 1 + 1) * 8 <= 256, "barrier block overflows its 256 bytes");
+  static_assert((2 * kXKStages + 2 * kXVStages + 2 + 2 + 2 + 1 + 2 + 1) * 8 <= 256, "barrier block overflows");
   float2* red = reinterpret_cast<float2*>(sm + L::kRed);
   PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::kGroups);
 
@@ -198,20 +198,21 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   }
   if (tid == 8 * 32) {
     *abort_flag = 0;
-    for (int s = 0; s < kXStages; ++s) {
+    for (int s = 0; s < kXKStages; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < kXVStages; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int x = 0; x < 4; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], kXRows);
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&s_full[c], 1);
+      mbar_init(&p_full[c], kXRows);
+      mbar_init(&pv_done[c], 1);
+      mbar_init(&mma_idle[c], 1);
     }
-    mbar_init(&pv_done[0], 1);
-    mbar_init(&pv_done[1], 1);
     mbar_init(q_full, 1);
-    mbar_init(mma_idle, 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -268,14 +269,14 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   const int64_t V = groups[p.num_groups].cost, R = gridDim.x, range = blockIdx.x;
   const int64_t first = (range * V) / R, end = ((range + 1) * V) / R;
   auto segment = [&](int64_t pos) { return prefix_segment(groups, p.num_groups, p.n_q_heads, pos, end, range); };
-  // S / P buffer x = 2 chain + buffer at columns 64 x, O of a chain at 256 + chain D
-  constexpr int kOCol = 4 * kXKeys;
+  // S / P of a chain at columns 128 chain, its O at 256 + chain D
+  constexpr int kOCol = 2 * kXKeys;
 
   if (warp < 8) {
     // ============================ softmax / epilogue ============================
     const int chain = warp >> 2, r = tid & (kXRows - 1);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_o = tmem + lane_base + kOCol;
+    const uint32_t t_s = tmem + lane_base + chain * kXKeys, t_o = tmem + lane_base + kOCol;
     uint32_t ops = 0;                                            // this chain's operations so far
     bool ok = true;
     for (int64_t pos = first; pos < end;) {
@@ -287,28 +288,31 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       int mine = 0;                                              // operations of this chain in this piece
       const int step = sg.share ? 1 : 2;
       for (int n = sg.share ? 0 : chain; n < n_tiles; n += step, ++mine, ++ops) {
-        const int x = 2 * chain + (ops & 1);
-        const uint32_t t_s = tmem + lane_base + x * kXKeys;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], (ops >> 1) & 1, p.err) && !*abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[chain], ops & 1, p.err) && !*abort_flag);
         if (!ok) break;
         tc_fence_after();
         // keys of the tile that the prefix holds (whole blocks; the last tile may be short)
         const int valid = min(kXKeys, (blocks - (sg.t0 + n) * kXTileBlocks) * kBlockSize);
         float v[64];
-        tmem_ld64(t_s, v);
-        if (valid < kXKeys) {
+        auto load_half = [&](int half) {
+          tmem_ld64(t_s + 64 * half, v);
+          if (valid < 64 * (half + 1)) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) v[i] = i < valid ? v[i] : -INFINITY;
-        }
-        const float m_tile = max64(v) * p.qk_scale_log2;
+            for (int i = 0; i < 64; ++i) v[i] = 64 * half + i < valid ? v[i] : -INFINITY;
+          }
+        };
+        load_half(0);
+        float mx = max64(v);
+        load_half(1);
+        mx = fmaxf(mx, max64(v));
+        const float m_tile = mx * p.qk_scale_log2;
         float alpha = 1.f;
         if (m_tile > m_ref + kXRescaleLog2) {
           alpha = ex2_approx(m_ref - m_tile);
           m_ref = m_tile;
         }
         if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O may be touched once the chain's previous P V has completed (the
-          // one before it has: these scores were asked for behind it)
+          // (the chain's previous P V has completed: these scores were asked for behind it)
           ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
           if (!ok) break;
           tc_fence_after();
@@ -324,42 +328,43 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const uint64_t scale2 = f32x2(p.qk_scale_log2, p.qk_scale_log2), nref2 = f32x2(nref, nref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        // the columns in registers are the upper 64; the lower ones are read again
+#pragma unroll 1
+        for (int half = 1; half >= 0; --half) {
+          if (half == 0) load_half(0);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 e2 = f32x2_split(fma_f32x2(f32x2(v[32 * c + i], v[32 * c + i + 1]), scale2, nref2));
-            const float e0 = ex2_approx(e2.x), e1 = ex2_approx(e2.y);
-            const uint64_t e01 = f32x2(e0, e1);
-            acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
-            if constexpr (kSplit) {
-              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
-              pk[i / 2] = __byte_perm(b0, b1, 0x7632);
-              const float2 lo = f32x2_split(
-                  sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
-              pk[16 + i / 2] = pack2(lo.x, lo.y, QT{});
-            } else {
-              pk[i / 2] = pack2(e0, e1, QT{});
+            for (int i = 0; i < 32; i += 2) {
+              const float2 e2 = f32x2_split(fma_f32x2(f32x2(v[32 * c + i], v[32 * c + i + 1]), scale2, nref2));
+              const float e0 = ex2_approx(e2.x), e1 = ex2_approx(e2.y);
+              const uint64_t e01 = f32x2(e0, e1);
+              acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
+              if constexpr (kSplit) {
+                const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+                pk[i / 2] = __byte_perm(b0, b1, 0x7632);
+                const float2 lo = f32x2_split(
+                    sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
+                pk[16 + i / 2] = pack2(lo.x, lo.y, QT{});
+              } else {
+                pk[i / 2] = pack2(e0, e1, QT{});
+              }
             }
+            if constexpr (kSplit)
+              tmem_st32u(t_s + 64 * half + 32 * c, pk);
+            else
+              tmem_st16u(t_s + 64 * half + 32 * c, pk);
           }
-          if constexpr (kSplit)
-            tmem_st32u(t_s + 32 * c, pk);
-          else
-            tmem_st16u(t_s + 32 * c, pk);
         }
         const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
         tmem_wait_st();
         l_run = l_run * alpha + (s0.x + s0.y);
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&p_full[chain]);
       }
-      // the piece's states; both warpgroups meet here (a failed wait ends both).
-      // The last scores only say that the P V two operations back is done (Q K^T
-      // runs that far ahead), and a parity names one of two neighbouring phases:
-      // so the one before the last is waited for first.
-      for (int back = min(mine, 2); back >= 1 && ok; --back)
-        ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - back) & 1, p.err));
+      // the piece's states; both warpgroups meet here (a failed wait ends both)
+      if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
       if (!sg.share) red[chain * kXRows + r] = make_float2(m_ref, l_run);
       if (named_bar_red_or(1, 2 * kXRows, !ok)) {
         ok = false;
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       if (tiles > 0) {
         const uint32_t last = tiles - 1;
         good = __all_sync(0xffffffffu,
-                          mbar_wait(&k_empty[last % kXStages], (last / kXStages) & 1, p.err) && !*abort_flag);
+                          mbar_wait(&k_empty[last % kXKStages], (last / kXKStages) & 1, p.err) && !*abort_flag);
         if (!good) break;
       }
       if (lane == 0) mbar_arrive_expect_tx(q_full, L::kQTile * (sg.share ? 2 : 1));
@@ -451,9 +456,9 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         }
         return (block_id >= 0) ? (block_id * p.n_kv_heads + sg.g) * kBlockSize : -2 * kBlockSize;
       };
-      // lane j + 4 h: half h of the tile's block j
+      // lane j + 8 h: half h of the tile's block j
       auto load = [&](bool is_v, int y) -> bool {
-        const uint32_t s = tiles % kXStages, use = tiles / kXStages;
+        const uint32_t stages = is_v ? kXVStages : kXKStages, s = tiles % stages, use = tiles / stages;
         uint64_t* full = is_v ? &v_full[s] : &k_full[s];
         uint64_t* empty = is_v ? &v_empty[s] : &k_empty[s];
         const bool freed = use == 0 || mbar_wait(empty, (use - 1) & 1, p.err);
@@ -481,69 +486,74 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       // loads this warp issued that nobody may have waited for (bounded)
       const unsigned long long deadline = global_ns() + kWaitLimitNs;
       if (issued_q > 0) mbar_wait_until(q_full, (issued_q - 1) & 1, deadline);
-      for (uint32_t t = issued_k > kXStages ? issued_k - kXStages : 0; t < issued_k; ++t)
-        mbar_wait_until(&k_full[t % kXStages], (t / kXStages) & 1, deadline);
-      for (uint32_t t = issued_v > kXStages ? issued_v - kXStages : 0; t < issued_v; ++t)
-        mbar_wait_until(&v_full[t % kXStages], (t / kXStages) & 1, deadline);
+      for (uint32_t t = issued_k > kXKStages ? issued_k - kXKStages : 0; t < issued_k; ++t)
+        mbar_wait_until(&k_full[t % kXKStages], (t / kXKStages) & 1, deadline);
+      for (uint32_t t = issued_v > kXVStages ? issued_v - kXVStages : 0; t < issued_v; ++t)
+        mbar_wait_until(&v_full[t % kXVStages], (t / kXVStages) & 1, deadline);
     }
   } else {
-    // ============================ MMA issuer (warp 9) ============================
+    // ============================ MMA issuers (warps 9, 10) ============================
+    // Warp 9 issues Q K^T, warp 10 P V, one elected lane each: a commit holds its
+    // thread until the MMA queue has drained to a few entries, and a wait costs
+    // about 100 clocks even when it is over; meanwhile the other feeds the queue.
     constexpr int kPasses = kSplit ? 2 : 1;
     constexpr uint32_t kIdQK = umma_idesc<QT>(false, kXKeys), kIdPV = umma_idesc<QT>(true, D);
+    const bool qk_warp = (warp == 9);
     bool ok = true;
     if (lane == 0) {
       uint32_t tile0 = 0, piece = 0;       // K / V tiles and pieces before the current piece
-      uint32_t asked[2] = {0, 0}, done[2] = {0, 0};   // Q K^T and P V operations of each chain so far
+      uint32_t count[2] = {0, 0};          // this issuer's operations of each chain so far
       for (int64_t pos = first; pos < end && ok; ++piece) {
         const PrefixSeg sg = segment(pos);
         pos = sg.next;
         const int n_tiles = sg.t1 - sg.t0;
         const int n_ops = sg.share ? 2 * n_tiles : n_tiles;
-        auto qk = [&](int k) -> bool {
-          const uint32_t t = tile0 + (sg.share ? k >> 1 : k), s = t % kXStages;
-          const int c = k & 1, x = 2 * c + (asked[c] & 1);
-          if (!mbar_wait(&k_full[s], (t / kXStages) & 1, p.err) || *abort_flag) return false;
-          ++asked[c];
-          const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (sg.share ? c * L::kQTile : 0)), 16, 1024);
-          const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + s * L::kKVTile), 16, 1024);
-          tc_fence_after();
+        if (qk_warp) ok = mbar_wait(q_full, piece & 1, p.err);
+        for (int k = 0; k < n_ops && ok; ++k) {
+          const uint32_t t = tile0 + (sg.share ? k >> 1 : k);
+          const int c = k & 1;
+          const bool last_use = !sg.share || c == 1;   // of the tile
+          if (qk_warp) {
+            // S of the chain once the P V that read P from its columns is done
+            const uint32_t s = t % kXKStages;
+            ok = mbar_wait(&k_full[s], (t / kXKStages) & 1, p.err) &&
+                 (count[c] == 0 || mbar_wait(&pv_done[c], (count[c] - 1) & 1, p.err)) && !*abort_flag;
+            if (!ok) break;
+            ++count[c];
+            const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (sg.share ? c * L::kQTile : 0)), 16, 1024);
+            const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + s * L::kKVTile), 16, 1024);
+            tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_f16(tmem + x * kXKeys, a0 + static_cast<uint64_t>(((ks >> 2) * kXHalfQ + (ks & 3) * 32) >> 4),
-                     b0 + static_cast<uint64_t>(((ks >> 2) * kXHalfKV + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
-          umma_commit(&s_full[x]);
-          if (!sg.share || c == 1) umma_commit(&k_empty[s]);
-          return true;
-        };
-        auto pv = [&](int k) -> bool {
-          const uint32_t t = tile0 + (sg.share ? k >> 1 : k), s = t % kXStages;
-          const int c = k & 1, x = 2 * c + (done[c] & 1);
-          if (!mbar_wait(&p_full[x], (done[c] >> 1) & 1, p.err) ||
-              !mbar_wait(&v_full[s], (t / kXStages) & 1, p.err) || *abort_flag)
-            return false;
-          ++done[c];
-          tc_fence_after();
-          const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + s * L::kKVTile), kXHalfKV, 1024);
-          const uint32_t a0 = tmem + x * kXKeys, d = tmem + kOCol + c * D;
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_f16(tmem + c * kXKeys, a0 + static_cast<uint64_t>(((ks >> 2) * kXHalfQ + (ks & 3) * 32) >> 4),
+                       b0 + static_cast<uint64_t>(((ks >> 2) * kXHalfKV + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
+            umma_commit(&s_full[c]);
+            if (last_use) umma_commit(&k_empty[s]);
+          } else {
+            const uint32_t s = t % kXVStages;
+            ok = mbar_wait(&v_full[s], (t / kXVStages) & 1, p.err) && mbar_wait(&p_full[c], count[c] & 1, p.err) &&
+                 !*abort_flag;
+            if (!ok) break;
+            ++count[c];
+            tc_fence_after();
+            const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + s * L::kKVTile), kXHalfKV, 1024);
+            const uint32_t a0 = tmem + c * kXKeys, d = tmem + kOCol + c * D;
 #pragma unroll
-          for (int pass = 0; pass < kPasses; ++pass)
+            for (int pass = 0; pass < kPasses; ++pass)
 #pragma unroll
-            for (int ks = 0; ks < kXKeys / 16; ++ks)
-              umma_f16_tmem_a(d, a0 + 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1),
-                              b0 + static_cast<uint64_t>((ks * 2048) >> 4), kIdPV, k > 1 || ks > 0 || pass > 0);
-          umma_commit(&pv_done[c]);
-          if (!sg.share || c == 1) umma_commit(&v_empty[s]);
-          return true;
-        };
-        ok = mbar_wait(q_full, piece & 1, p.err) && !*abort_flag;
-        for (int k = 0; k < min(kXAhead, n_ops) && ok; ++k) ok = qk(k);
-        for (int k = 0; k < n_ops && ok; ++k) ok = pv(k) && (k + kXAhead >= n_ops || qk(k + kXAhead));
+              for (int ks = 0; ks < kXKeys / 16; ++ks)
+                umma_f16_tmem_a(d, a0 + 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1),
+                                b0 + static_cast<uint64_t>((ks * 2048) >> 4), kIdPV, k > 1 || ks > 0 || pass > 0);
+            umma_commit(&pv_done[c]);
+            if (last_use) umma_commit(&v_empty[s]);
+          }
+        }
         tile0 += n_tiles;
       }
       if (!ok) *abort_flag = 1;
-      // every MMA has completed before TMEM is released
-      umma_commit(mma_idle);
-      mbar_wait(mma_idle, 0, p.err);
+      // every MMA of this lane has completed before TMEM is released
+      umma_commit(&mma_idle[qk_warp ? 0 : 1]);
+      mbar_wait(&mma_idle[qk_warp ? 0 : 1], 0, p.err);
     }
     __syncwarp();
   }

@@ -11,7 +11,7 @@ namespace pkv {
 constexpr int kMaxPrefixGroups = 1024;   // groups whose geometry a thread block keeps in shared memory
 constexpr int kPrefixUnitRows = 256;     // query rows of one unit of work: two tiles of 128
 
-// one group's share of the work; cost counts (unit, 64-key tile) pairs
+// one group's share of the work; cost counts (unit, 128-key tile) pairs
 struct PrefixGroup {
   int64_t cost;                  // of all groups before it
   int32_t start;                 // its first sequence
