@@ -1450,6 +1450,14 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
 // piece is in slot 2 r0 when its first block opens range r0, else 2 r0 + 1;
 // every later piece is in slot 2 r of its range r (the range's first segment).
 // ---------------------------------------------------------------------------
+// a / b of non-negative values: 32-bit division where they fit (a quarter of
+// the 64-bit one's instructions, on the path between a merge's wait and its loads)
+__device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 struct CombineSpan {
   int64_t r0, r1;
   bool first_is_head;
@@ -1475,10 +1483,10 @@ __device__ __forceinline__ CombineSpan combine_span(const DecodeParams& p, int g
     s.r1 = part_range_of(S0 + nb - 1, s.W, R, p.part_blocks);
     s.first_is_head = (S0 == part_range_start(s.r0, s.W, R, p.part_blocks));
   } else {
-    s.r0 = ((s.pos0 + 1) * R + s.V - 1) / s.V - 1;   // largest r with floor(r V / R) <= pos0
+    s.r0 = div_nonneg((s.pos0 + 1) * R + s.V - 1, s.V) - 1;   // largest r with floor(r V / R) <= pos0
     const int64_t posl = s.pos0 + static_cast<int64_t>(kBlockCost) * (nb - 1);
-    s.r1 = ((posl + 1) * R + s.V - 1) / s.V - 1;
-    s.first_is_head = (S0 == 0) || ((s.r0 * s.V) / R > u0 - kBlockCost);
+    s.r1 = div_nonneg((posl + 1) * R + s.V - 1, s.V) - 1;
+    s.first_is_head = (S0 == 0) || (div_nonneg(s.r0 * s.V, R) > u0 - kBlockCost);
   }
   return s;
 }
@@ -1489,8 +1497,8 @@ __device__ __forceinline__ bool combine_has_piece(const CombineSpan& s, const De
   if (p.part_blocks)
     return part_range_start(r + 1, s.W, R, p.part_blocks) > part_range_start(r, s.W, R, p.part_blocks);
   if (r == s.r0) return true;
-  const int64_t i = ((r * s.V) / R - s.pos0 + kBlockCost - 1) / kBlockCost;
-  return s.pos0 + static_cast<int64_t>(kBlockCost) * i < ((r + 1) * s.V) / R;
+  const int64_t i = (div_nonneg(r * s.V, R) - s.pos0 + kBlockCost - 1) / kBlockCost;
+  return s.pos0 + static_cast<int64_t>(kBlockCost) * i < div_nonneg((r + 1) * s.V, R);
 }
 
 __device__ __forceinline__ int64_t combine_slot(const CombineSpan& s, int64_t r) {

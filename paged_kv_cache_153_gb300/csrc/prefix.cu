@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + chain * kXKeys, t_o = tmem + lane_base + kOCol;
     uint32_t ops = 0;                                            // this chain's operations so far
+    // A failed wait ends a warp's work but not its walk over the pieces: the two
+    // warpgroups meet at named barriers, which must find all of them.
     bool ok = true;
     for (int64_t pos = first; pos < end;) {
       const PrefixSeg sg = segment(pos);
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       float m_ref = -INFINITY, l_run = 0.f;
       int mine = 0;                                              // operations of this chain in this piece
       const int step = sg.share ? 1 : 2;
-      for (int n = sg.share ? 0 : chain; n < n_tiles; n += step, ++mine, ++ops) {
+      for (int n = sg.share ? 0 : chain; n < n_tiles && ok; n += step, ++mine, ++ops) {
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[chain], ops & 1, p.err) && !*abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -363,12 +365,13 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         tc_fence_before();
         mbar_arrive(&p_full[chain]);
       }
-      // the piece's states; both warpgroups meet here (a failed wait ends both)
+      // the piece's states, once the last P V is done
       if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
-      if (!sg.share) red[chain * kXRows + r] = make_float2(m_ref, l_run);
-      if (named_bar_red_or(1, 2 * kXRows, !ok)) {
-        ok = false;
-        break;
+      if (!ok) *abort_flag = 1;
+      if (!sg.share) {
+        red[chain * kXRows + r] = make_float2(m_ref, l_run);
+        // (a failure on either side keeps both from writing)
+        if (named_bar_red_or(1, 2 * kXRows, !ok)) ok = false;
       }
       tc_fence_after();
       const int row0 = (sg.share ? chain * kXRows : 0) + (warp & 3) * 32;   // the warp's first row of the unit
@@ -376,18 +379,19 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       float* dst = p.o + (sg.row + row0) * D;
       if (sg.share) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D && ok; c += 32) {
           float o[32];
           tmem_ld32(t_o + chain * D + c, o);
           store_rows32<D>(dst + c, o, n_rows, lane);
         }
-        if (lane < n_rows) *reinterpret_cast<float2*>(p.ml + (sg.row + row0 + lane) * 2) = make_float2(m_ref, l_run);
+        if (ok && lane < n_rows)
+          *reinterpret_cast<float2*>(p.ml + (sg.row + row0 + lane) * 2) = make_float2(m_ref, l_run);
       } else {
         // join the two key streams: each warpgroup takes half of the columns
         const float2 a = red[r], b = red[kXRows + r];
         const float m = fmaxf(a.x, b.x), ref = (m == -INFINITY) ? 0.f : m;
         const float wa = ex2_approx(a.x - ref), wb = ex2_approx(b.x - ref);
-        if (n_rows > 0) {
+        if (ok && n_rows > 0) {
 #pragma unroll 1
           for (int c = chain * (D / 2); c < (chain + 1) * (D / 2); c += 32) {
             float o[32];
@@ -413,7 +417,6 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         tc_fence_after();
       }
     }
-    if (!ok) *abort_flag = 1;
   } else if (warp == 8) {
     // ============================ TMA producer ============================
     uint32_t tiles = 0;                  // tiles loaded so far (K and V alike)
@@ -569,10 +572,12 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
 // consecutive outputs and joins the states of the prefix's pieces (one per
 // range that the row's unit meets), then those of the sequence's own blocks:
 // the pieces in the decode kernel's partial slots, or the one state it left
-// for a pair that one range holds.  Which ranges hold a piece takes two 64-bit
-// divisions each: the lanes find it for 32 ranges at a time, and only the
-// pieces themselves are walked (every lane dividing for every piece made the
-// merge 14 us of a 93 us call).
+// for a pair that one range holds.
+// It is all latency: what it needs of the geometry is loaded at once after the
+// wait; then the lanes find the pieces (which take two divisions each) of 32
+// ranges at a time, prefix and own blocks in one list, and their states are
+// loaded 8 at a time.  (Every lane dividing for every piece, one list after the
+// other: 14 us of a 93 us call.)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
 
@@ -612,35 +617,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       v[0] = x.x, v[1] = x.y;
     }
   };
-  // pieces r0..r1: state of piece r at index at(r) of (ml, o), live(r) false where a range holds none
-  auto walk = [&](int64_t r0, int64_t r1, const float* ml, const float* o, auto&& live, auto&& at) {
-    for (int64_t rb = r0; rb <= r1; rb += 32) {
-      const int64_t mine = rb + lane;
-      const bool use = mine <= r1 && live(mine);
-      const int64_t index = use ? at(mine) : 0;
-      const float2 state =
-          use ? *reinterpret_cast<const float2*>(ml + index * 2) : make_float2(-INFINITY, 0.f);
-      uint32_t left = __ballot_sync(0xffffffffu, use);
-      while (left) {
-        float v[kBatch][N];
-        int src[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          src[q] = left ? __ffs(left) - 1 : -1;
-          left &= left - 1;        // (0 stays 0)
-          const int64_t i = __shfl_sync(0xffffffffu, index, src[q] < 0 ? 0 : src[q]);
-          if (src[q] >= 0) load(o + i * D, v[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const int from = src[q] < 0 ? 0 : src[q];
-          const float2 x = make_float2(__shfl_sync(0xffffffffu, state.x, from), __shfl_sync(0xffffffffu, state.y, from));
-          if (src[q] >= 0) st.add(x, v[q]);
-        }
-      }
-    }
-  };
-
   // everything whose address depends on (b, head) alone is loaded at once
   const int ctx = p.context_lens[b];
   const int64_t c0 = rest.ws_cum[b];
@@ -664,26 +640,63 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     gr.blocks = __shfl_sync(0xffffffffu, own.blocks, from);
   }
   const int row = (b - gr.start) * G + h;
+  const int64_t R = ranges;
+  int64_t lo = 0, hi = 0, r0 = 0, n_pre = 0, base = 0;     // the unit's cost span; its ranges r0 .. r0 + n_pre - 1
   if (row < gr.rows && shares_prefix(gr.blocks, ctx, min(p.max_blocks_per_seq, p.max_nblk))) {
-    const int64_t R = ranges;
     const int kt = prefix_tiles(gr.blocks), unit = row / kPrefixUnitRows;
-    const int64_t lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt, hi = lo + kt;
-    const int64_t r0 = ((lo + 1) * R + V - 1) / V - 1, r1 = (hi * R + V - 1) / V - 1;   // largest r with r V / R <= x
-    const int64_t base = piece_row(gr.start, p.n_q_heads, g, gr.rows, unit, 0) + row % kPrefixUnitRows;
-    walk(r0, r1, p.ml, p.o,
-         [&](int64_t r) { return max(lo, (r * V) / R) < min(hi, ((r + 1) * V) / R); },
-         [&](int64_t r) { return base + r * kPrefixUnitRows; });
+    lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt;
+    hi = lo + kt;
+    r0 = div_nonneg((lo + 1) * R + V - 1, V) - 1;          // largest r with r V / R <= lo
+    n_pre = div_nonneg(hi * R + V - 1, V) - r0;
+    base = piece_row(gr.start, p.n_q_heads, g, gr.rows, unit, 0) + row % kPrefixUnitRows;
   }
   // ---- the sequence's own blocks ----
+  CombineSpan sp{};
+  int64_t n_own = 0;
   if (nb > 0) {
-    const CombineSpan sp = combine_span(rest, g, c0, nb, tot, ne_b, tot_ne, rest_grid);
-    if (sp.r0 == sp.r1) {
-      float v[N];
-      load(rest.rest_o + u * D, v);
-      st.add(*reinterpret_cast<const float2*>(rest.rest_ml + u * 2), v);
-    } else {
-      walk(sp.r0, sp.r1, rest.ws_ml, rest.ws_o, [&](int64_t r) { return combine_has_piece(sp, rest, r, rest_grid); },
-           [&](int64_t r) { return combine_slot(sp, r) * G + h; });
+    sp = combine_span(rest, g, c0, nb, tot, ne_b, tot_ne, rest_grid);
+    n_own = sp.r1 - sp.r0 + 1;
+  }
+  for (int64_t x0 = 0; x0 < n_pre + n_own; x0 += 32) {
+    const int64_t x = x0 + lane;
+    const float *ml = nullptr, *o = nullptr;
+    if (x < n_pre) {
+      const int64_t r = r0 + x;
+      if (max(lo, div_nonneg(r * V, R)) < min(hi, div_nonneg((r + 1) * V, R))) {
+        const int64_t i = base + r * kPrefixUnitRows;
+        ml = p.ml + i * 2;
+        o = p.o + i * D;
+      }
+    } else if (x < n_pre + n_own) {
+      const int64_t r = sp.r0 + (x - n_pre);
+      if (n_own == 1) {
+        ml = rest.rest_ml + u * 2;
+        o = rest.rest_o + u * D;
+      } else if (combine_has_piece(sp, rest, r, rest_grid)) {
+        const int64_t i = combine_slot(sp, r) * G + h;
+        ml = rest.ws_ml + i * 2;
+        o = rest.ws_o + i * D;
+      }
+    }
+    const float2 state = ml != nullptr ? *reinterpret_cast<const float2*>(ml) : make_float2(-INFINITY, 0.f);
+    uint32_t left = __ballot_sync(0xffffffffu, ml != nullptr);
+    while (left) {
+      float v[kBatch][N];
+      int src[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        src[q] = left ? __ffs(left) - 1 : -1;
+        left &= left - 1;          // (0 stays 0)
+        const float* from = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), src[q] < 0 ? 0 : src[q]));
+        if (src[q] >= 0) load(from, v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int from = src[q] < 0 ? 0 : src[q];
+        const float2 one = make_float2(__shfl_sync(0xffffffffu, state.x, from), __shfl_sync(0xffffffffu, state.y, from));
+        if (src[q] >= 0) st.add(one, v[q]);
+      }
     }
   }
   const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
