@@ -581,20 +581,6 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
 
-template <int N>
-struct MergeState {
-  float m = -INFINITY, l = 0.f, o[N] = {};
-  __device__ __forceinline__ void add(float2 ml, const float* v) {
-    const float mn = fmaxf(m, ml.x);
-    const float ref = (mn == -INFINITY) ? 0.f : mn;
-    const float a = exp2f(m - ref), w = exp2f(ml.x - ref);
-    l = l * a + w * ml.y;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * a + w * v[i];
-    m = mn;
-  }
-};
-
 template <typename QT, int D, int G>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ranges, const __grid_constant__ DecodeParams rest,
@@ -607,7 +593,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (u >= static_cast<int64_t>(p.batch) * p.n_q_heads) return;
   const int b = static_cast<int>(u / p.n_q_heads), head = static_cast<int>(u % p.n_q_heads);
   const int g = head / G, h = head % G;
-  MergeState<N> st;
+  float M = -INFINITY, L = 0.f, O[N] = {};
   auto load = [&](const float* src, float* v) {
     if constexpr (N == 4) {
       const float4 x = *reinterpret_cast<const float4*>(src + 4 * lane);
@@ -680,6 +666,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     }
     const float2 state = ml != nullptr ? *reinterpret_cast<const float2*>(ml) : make_float2(-INFINITY, 0.f);
     uint32_t left = __ballot_sync(0xffffffffu, ml != nullptr);
+    // each piece's weight against the maximum over all of them (the lanes', then
+    // the earlier rounds'), so that only the outputs are summed in turn
+    float m = state.x;
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float mn = fmaxf(M, m), ref = (mn == -INFINITY) ? 0.f : mn;
+    const float keep = exp2f(M - ref), w = exp2f(state.x - ref);
+    float l = w * state.y;
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    L = L * keep + l;
+    M = mn;
+#pragma unroll
+    for (int e = 0; e < N; ++e) O[e] *= keep;
     while (left) {
       float v[kBatch][N];
       int src[kBatch];
@@ -693,19 +693,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       }
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const int from = src[q] < 0 ? 0 : src[q];
-        const float2 one = make_float2(__shfl_sync(0xffffffffu, state.x, from), __shfl_sync(0xffffffffu, state.y, from));
-        if (src[q] >= 0) st.add(one, v[q]);
+        const float wq = __shfl_sync(0xffffffffu, w, src[q] < 0 ? 0 : src[q]);
+        if (src[q] >= 0)
+#pragma unroll
+          for (int e = 0; e < N; ++e) O[e] = fmaf(wq, v[q][e], O[e]);
       }
     }
   }
-  const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
   auto* out = static_cast<typename QT::storage*>(rest.out) + u * D + N * lane;
   if constexpr (N == 4)
     *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack2(st.o[0] * inv, st.o[1] * inv, QT{}), pack2(st.o[2] * inv, st.o[3] * inv, QT{}));
+        make_uint2(pack2(O[0] * inv, O[1] * inv, QT{}), pack2(O[2] * inv, O[3] * inv, QT{}));
   else
-    *reinterpret_cast<uint32_t*>(out) = pack2(st.o[0] * inv, st.o[1] * inv, QT{});
+    *reinterpret_cast<uint32_t*>(out) = pack2(O[0] * inv, O[1] * inv, QT{});
 }
 
 namespace {
