@@ -154,6 +154,7 @@ struct RestCall {
   int num_groups;
   float* ml;
   float* o;
+  size_t smem;           // shared memory that the prefix kernel leaves on its SM
   DecodeParams params;   // out
   int grid;              // out
 };
@@ -269,6 +270,7 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   li.max_ctas_per_sm = std::max(0, std::min(kMaxCtasPerSm, env_int("PKV_CTAS_PER_SM", 0)));
   li.stages = env_int("PKV_STAGES", 0);
   li.part_ranges_cap = w.ranges_cap;
+  li.rest_smem = rest != nullptr ? rest->smem : 0;
   const pkv_status st = launch(p, li, static_cast<cudaStream_t>(stream));
   if (rest != nullptr) {
     rest->params = p;
@@ -612,6 +614,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
                         (num_groups + static_cast<int64_t>(batch) * group / kPrefixUnitRows);
   const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_prefix_len) + 127) / 128);
   const int ranges = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(1, units * tiles)));
+  p.q_tiles = static_cast<int64_t>(batch) * group > 128 ? 2 : 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   pkv_status st = launch_prefix(p, ranges, group, head_dim, dtype, s);
   if (st != PKV_OK) return st;
@@ -621,6 +624,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   rest.num_groups = num_groups;
   rest.ml = reinterpret_cast<float*>(ws + w.rest_ml);
   rest.o = reinterpret_cast<float*>(ws + w.rest_o);
+  rest.smem = kSmemPerSm - 2 * kSmemReservedPerCta - prefix_smem_bytes(head_dim, p.q_tiles, num_groups);
   st = decode_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, batch, num_q_heads,
                      num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len, scale, out,
                      dtype, 0, ws, w.decode.total, err_flag, stream, nullptr, nullptr, nullptr, 1, 0, nullptr,

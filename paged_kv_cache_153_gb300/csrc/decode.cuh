@@ -276,8 +276,9 @@ struct DecodeTraits {
     return (scales_off(stages) + 4 * 2 * n_kv_heads + 15) & ~static_cast<size_t>(15);
   }
   // + 1024 bytes so that the base can be rounded up to a 1024-byte boundary
-  static __host__ __device__ size_t smem_bytes(int stages, int batch, int n_kv_heads) {
-    return 1024 + cum_off(stages, n_kv_heads) + 4 * (3 * static_cast<size_t>(batch) + 3);
+  // (kRest: a fourth int per sequence, its skipped blocks)
+  static __host__ __device__ size_t smem_bytes(int stages, int batch, int n_kv_heads, Source src) {
+    return 1024 + cum_off(stages, n_kv_heads) + 4 * ((src == kRest ? 4 : 3) * static_cast<size_t>(batch) + 3);
   }
 };
 
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
   int* cum = reinterpret_cast<int*>(smem + T::cum_off(S, p.n_kv_heads));   // [B + 1] block prefix
   int* ntok = cum + p.batch + 1;                                             // [B]
   int* ne = ntok + p.batch;                                                  // [B + 1] non-empty prefix
+  int* skipped = ne + p.batch + 1;                                           // kRest: [B] shared blocks
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hkv = p.n_kv_heads;
@@ -493,6 +495,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
       if constexpr (SRC == kListed) nb = min(nb, p.budget);
       if constexpr (SRC == kRest) {
         const int skip = prefix_blocks(p, b);
+        skipped[b] = skip;
         nb -= skip;
         ntok[b] -= skip * kBlockSize;
       }
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
       sg.r = r;
       sg.f_hi = f_hi;
       sg.skip = 0;
-      if constexpr (SRC == kRest) sg.skip = prefix_blocks(p, lo);
+      if constexpr (SRC == kRest) sg.skip = skipped[lo];
       sg.slot = -1;
       if (!(sg.i0 == 0 && sg.i1 == sg.nb)) {
         const int64_t sl = (f == f_lo) ? 2 * r : 2 * r + 1;
@@ -763,7 +766,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
       // occupy distinct stages, so their lanes wait and issue in parallel;
       // the __syncwarp between sub-batches keeps each stage's uses in order.
       const int g = cur.g;
-      const int sub = S < 32 ? S : 32;
+      // (kRest's ring is two or three blocks per consumer warp deep: a sub-batch
+      // of one block per warp refills a stage without waiting for all of them)
+      const int sub = SRC == kRest ? NW : S < 32 ? S : 32;
       const int nseg = cur.i1 - cur.i0;
       bool stop = false;
       for (int w0 = 0; w0 < nseg && !stop; w0 += 32) {

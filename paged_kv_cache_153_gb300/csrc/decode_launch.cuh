@@ -17,6 +17,7 @@ struct LaunchInfo {
   int stages;              // 0 = fill the SM's shared memory; else a request (rounded to the warp count)
   int grid;                // out: decode grid used
   int64_t part_ranges_cap; // partition mode: max ranges the workspace holds
+  size_t rest_smem;        // kRest: shared memory for one block, beside the shared-prefix kernel's
 };
 
 using DecodeLauncher = pkv_status (*)(DecodeParams&, LaunchInfo&, cudaStream_t);
@@ -25,7 +26,6 @@ constexpr int kMaxDevices = 64;
 constexpr int kSmemPerSm = 233472;        // shared memory per SM on sm_100-class parts (228 KiB)
 constexpr int kSmemReservedPerCta = 1024; // system-reserved shared memory per resident block
 constexpr int kMaxStagesPerWarp = 8;
-constexpr size_t kRestSmem = 64 * 1024;   // kRest: what the shared-prefix kernel leaves free on its SM
 
 // the runtime's answers about one kernel variant on one device
 constexpr int kOccupancyEntries = 8;
@@ -88,7 +88,7 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   // By default, the ring fills the SM's shared memory across as many resident
   // blocks as the registers allow (capped by max_ctas_per_sm).
   int occ = 0;
-  size_t smem = Tr::smem_bytes(NW, p.batch, p.n_kv_heads);
+  size_t smem = Tr::smem_bytes(NW, p.batch, p.n_kv_heads, SRC);
   if (smem > dyn_max) return PKV_ERR_UNSUPPORTED;   // batch too large for one block's shared memory
   if (!occupancy(smem, &occ)) return PKV_ERR_CUDA;
   if (occ < 1) return PKV_ERR_UNSUPPORTED;
@@ -117,8 +117,8 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
     spw = std::max(1, li.stages / NW);
   } else {
     for (int cand = kMaxStagesPerWarp; cand >= 1; --cand) {
-      const size_t s = Tr::smem_bytes(NW * cand, p.batch, p.n_kv_heads);
-      if (s <= (SRC == kRest ? std::min(dyn_max, kRestSmem) : dyn_max) &&
+      const size_t s = Tr::smem_bytes(NW * cand, p.batch, p.n_kv_heads, SRC);
+      if (s <= (SRC == kRest ? std::min(dyn_max, li.rest_smem) : dyn_max) &&
           static_cast<size_t>(occ) * (s + kSmemReservedPerCta) <= kSmemPerSm) {
         spw = cand;
         break;
@@ -126,9 +126,9 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
     }
   }
   spw = std::min(spw, kMaxStagesPerWarp);
-  while (spw > 1 && Tr::smem_bytes(NW * spw, p.batch, p.n_kv_heads) > dyn_max) --spw;
+  while (spw > 1 && Tr::smem_bytes(NW * spw, p.batch, p.n_kv_heads, SRC) > dyn_max) --spw;
   const int stages = NW * spw;
-  smem = Tr::smem_bytes(stages, p.batch, p.n_kv_heads);
+  smem = Tr::smem_bytes(stages, p.batch, p.n_kv_heads, SRC);
   if (!occupancy(smem, &occ)) return PKV_ERR_CUDA;
   lock.unlock();
   if (occ < 1) return PKV_ERR_UNSUPPORTED;

@@ -44,9 +44,10 @@
 // Waits are bounded as in the other kernels.
 //
 // Beside it.  The kernel leaves room on its SM (registers: 128 a thread; shared
-// memory: about 64 KiB) for one thread block of the decode over the sequences'
-// own blocks, which is bound by memory where this one is bound by the tensor
-// cores; that kernel launches as soon as this one has started.
+// memory: about 64 KiB, or 96 where no unit has more than 128 rows) for one
+// thread block of the decode over the sequences' own blocks, which is bound by
+// memory where this one is bound by the tensor cores; that kernel launches as
+// soon as this one has started.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -71,14 +72,15 @@ constexpr int kXHalfKV = kXKeys * 128;            // and of a K / V tile
 template <int D>
 struct PrefixSmem {
   static constexpr int kQTile = kXRows * D * 2, kKVTile = kXKeys * D * 2;
-  static constexpr int kQ = 0;                                 // [2] row tiles
-  static constexpr int kK = 2 * kQTile;                        // [kXKStages]
+  static constexpr int kK = 0;                                 // [kXKStages]
   static constexpr int kV = kK + kXKStages * kKVTile;          // [kXVStages]
-  static constexpr int kBar = kV + kXVStages * kKVTile;        // 256 bytes
-  static constexpr int kRed = kBar + 256;                      // float2 [2][128]: a chain's (m, l)
-  static constexpr int kGroups = kRed + 2 * kXRows * 8;        // PrefixGroup [num_groups + 1]
-  static size_t bytes(int num_groups) {
-    return 1024 + kGroups + sizeof(PrefixGroup) * (static_cast<size_t>(num_groups) + 1);
+  static constexpr int kBar = kV + kXVStages * kKVTile;        // 1024 bytes, of which barriers 256
+  static constexpr int kQ = kBar + 1024;                       // [q_tiles] row tiles
+  // behind them: float2 [2][128], a chain's (m, l); PrefixGroup [num_groups + 1]
+  static __host__ __device__ constexpr int red(int q_tiles) { return kQ + q_tiles * kQTile; }
+  static __host__ __device__ constexpr int groups(int q_tiles) { return red(q_tiles) + 2 * kXRows * 8; }
+  static size_t bytes(int q_tiles, int num_groups) {
+    return 1024 + groups(q_tiles) + sizeof(PrefixGroup) * (static_cast<size_t>(num_groups) + 1);
   }
 };
 
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((2 * kXKStages + 2 * kXVStages + 2 + 2 + 2 + 1 + 2 + 1) * 8 <= 256, "barrier block overflows");
-  float2* red = reinterpret_cast<float2*>(sm + L::kRed);
-  PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::kGroups);
+  float2* red = reinterpret_cast<float2*>(sm + L::red(p.q_tiles));
+  PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::groups(p.q_tiles));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 9) {
@@ -573,8 +575,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
 // range that the row's unit meets), then those of the sequence's own blocks:
 // the pieces in the decode kernel's partial slots, or the one state it left
 // for a pair that one range holds.
-// It is all latency: what it needs of the geometry is loaded at once after the
-// wait; then the lanes find the pieces (which take two divisions each) of 32
+// It is all latency.  Small calls work out the geometry from the inputs while
+// the other kernels run; others read what those left.  Then the lanes find the pieces (which take two divisions each) of 32
 // ranges at a time, prefix and own blocks in one list, and their states are
 // loaded 8 at a time.  (Every lane dividing for every piece, one list after the
 // other: 14 us of a 93 us call.)
@@ -589,8 +591,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   constexpr int kBatch = 8;        // pieces whose loads are issued together
   const int lane = threadIdx.x & 31;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
-  pdl_wait_and_release();
-  if (u >= static_cast<int64_t>(p.batch) * p.n_q_heads) return;
+  // (every warp waits, at the latest here: this grid completes after the others)
+  if (u >= static_cast<int64_t>(p.batch) * p.n_q_heads) {
+    pdl_wait();
+    return;
+  }
   const int b = static_cast<int>(u / p.n_q_heads), head = static_cast<int>(u % p.n_q_heads);
   const int g = head / G, h = head % G;
   float M = -INFINITY, L = 0.f, O[N] = {};
@@ -603,32 +608,89 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       v[0] = x.x, v[1] = x.y;
     }
   };
-  // everything whose address depends on (b, head) alone is loaded at once
+  // ---- the geometry: this sequence's group, the cost of all groups, the
+  // blocks of the sequences before it, its own and all ----
+  const int cap = min(p.max_blocks_per_seq, p.max_nblk);
   const int ctx = p.context_lens[b];
-  const int64_t c0 = rest.ws_cum[b];
-  const int nb = rest.ws_cum[b + 1] - static_cast<int>(c0);
-  const int64_t tot = rest.ws_cum[rest.batch], ne_b = rest.ws_cum[rest.batch + 1 + b],
-                tot_ne = rest.ws_cum[2 * rest.batch + 1];
-  const int64_t V = p.groups[p.num_groups].cost;
-
-  // ---- the shared prefix ----
-  // the last group that starts at or before b: found by the lane that holds it
   PrefixGroup gr{0, 0, 0, 0, -1};
-  for (int j0 = 0; j0 < p.num_groups; j0 += 32) {
-    PrefixGroup own{0, INT32_MAX, 0, 0, -1};
-    if (j0 + lane < p.num_groups) own = p.groups[j0 + lane];
-    const uint32_t m = __ballot_sync(0xffffffffu, own.start <= b);
-    if (m == 0) continue;
-    const int from = 31 - __clz(m);
-    gr.cost = __shfl_sync(0xffffffffu, own.cost, from);
-    gr.start = __shfl_sync(0xffffffffu, own.start, from);
-    gr.rows = __shfl_sync(0xffffffffu, own.rows, from);
-    gr.blocks = __shfl_sync(0xffffffffu, own.blocks, from);
+  int64_t V, c0, tot, ne_b, tot_ne;
+  int nb;
+  if (p.batch <= kCombineLocalPrefix && p.num_groups <= 32) {
+    // small calls: from the inputs, as the two kernels take it, before the wait.
+    // Lane j holds group j's bounds and whether a sequence covers its blocks.
+    int start = INT32_MAX, stop = INT32_MAX, blocks = 0;
+    if (lane < p.num_groups) {
+      start = min(max(p.group_starts[lane], 0), p.batch);
+      stop = min(max(p.group_starts[lane + 1], start), p.batch);
+      blocks = max(p.prefix_lens[lane], 0) / kBlockSize;
+    }
+    uint32_t covered = 0;                                  // groups with a covering sequence
+    int before = 0, mine = 0, all = 0, ne_before = 0, ne_all = 0;
+    for (int i0 = 0; i0 < p.batch; i0 += 32) {
+      const int i = i0 + lane;
+      const int len = i < p.batch ? p.context_lens[i] : 0;
+      int j = -1;                                          // its group: the last that starts at or before it
+      for (int k = 0; k < p.num_groups; ++k)
+        if (__shfl_sync(0xffffffffu, start, k) <= i) j = k;
+      const int shared = __shfl_sync(0xffffffffu, blocks, max(j, 0));
+      const int end = __shfl_sync(0xffffffffu, stop, max(j, 0));
+      const bool shares = i < p.batch && j >= 0 && i < end && shares_prefix(shared, len, cap);
+      int n = i < p.batch && len > 0 ? min((len + kBlockSize - 1) / kBlockSize, cap) : 0;
+      if (shares) n -= shared;
+      covered |= __reduce_or_sync(0xffffffffu, shares ? 1u << j : 0u);
+      all += n;
+      ne_all += n > 0;
+      before += i < b ? n : 0;
+      ne_before += i < b && n > 0;
+      mine += i == b ? n : 0;
+    }
+    c0 = __reduce_add_sync(0xffffffffu, before);
+    nb = __reduce_add_sync(0xffffffffu, mine);
+    tot = __reduce_add_sync(0xffffffffu, all);
+    ne_b = __reduce_add_sync(0xffffffffu, ne_before);
+    tot_ne = __reduce_add_sync(0xffffffffu, ne_all);
+    const int rows = lane < p.num_groups ? (stop - start) * G : 0;
+    if (!((covered >> lane) & 1u)) blocks = 0;
+    int64_t cost = static_cast<int64_t>(p.n_kv_heads) * prefix_units(rows) * prefix_tiles(blocks);
+    const int64_t own = cost;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, cost, k);
+      if (lane >= k) cost += x;
+    }
+    V = __shfl_sync(0xffffffffu, cost, 31);
+    const uint32_t m = __ballot_sync(0xffffffffu, start <= b);
+    const int from = m ? 31 - __clz(m) : 0;
+    gr.cost = __shfl_sync(0xffffffffu, cost - own, from);
+    gr.start = __shfl_sync(0xffffffffu, start, from);
+    gr.rows = m ? __shfl_sync(0xffffffffu, rows, from) : 0;
+    gr.blocks = __shfl_sync(0xffffffffu, blocks, from);
+    pdl_wait_and_release();
+  } else {
+    // else from what the two kernels leave in the workspace
+    pdl_wait_and_release();
+    c0 = rest.ws_cum[b];
+    nb = rest.ws_cum[b + 1] - static_cast<int>(c0);
+    tot = rest.ws_cum[rest.batch];
+    ne_b = rest.ws_cum[rest.batch + 1 + b];
+    tot_ne = rest.ws_cum[2 * rest.batch + 1];
+    V = p.groups[p.num_groups].cost;
+    for (int j0 = 0; j0 < p.num_groups; j0 += 32) {
+      PrefixGroup own{0, INT32_MAX, 0, 0, -1};
+      if (j0 + lane < p.num_groups) own = p.groups[j0 + lane];
+      const uint32_t m = __ballot_sync(0xffffffffu, own.start <= b);
+      if (m == 0) continue;
+      const int from = 31 - __clz(m);
+      gr.cost = __shfl_sync(0xffffffffu, own.cost, from);
+      gr.start = __shfl_sync(0xffffffffu, own.start, from);
+      gr.rows = __shfl_sync(0xffffffffu, own.rows, from);
+      gr.blocks = __shfl_sync(0xffffffffu, own.blocks, from);
+    }
   }
   const int row = (b - gr.start) * G + h;
   const int64_t R = ranges;
   int64_t lo = 0, hi = 0, r0 = 0, n_pre = 0, base = 0;     // the unit's cost span; its ranges r0 .. r0 + n_pre - 1
-  if (row < gr.rows && shares_prefix(gr.blocks, ctx, min(p.max_blocks_per_seq, p.max_nblk))) {
+  if (row < gr.rows && shares_prefix(gr.blocks, ctx, cap)) {
     const int kt = prefix_tiles(gr.blocks), unit = row / kPrefixUnitRows;
     lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt;
     hi = lo + kt;
@@ -723,7 +785,7 @@ pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t strea
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
       if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(PrefixSmem<D>::bytes(kMaxPrefixGroups))),
+                                           static_cast<int>(PrefixSmem<D>::bytes(2, kMaxPrefixGroups))),
                       "cudaFuncSetAttribute") ||
           // (the SM's whole shared memory, so that what this kernel leaves is the next one's)
           cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -734,7 +796,7 @@ pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t strea
     }
   }
   return cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(kXThreads),
-                                PrefixSmem<D>::bytes(p.num_groups), stream, p),
+                                PrefixSmem<D>::bytes(p.q_tiles, p.num_groups), stream, p),
                      "prefix_kernel launch")
              ? PKV_ERR_CUDA
              : PKV_OK;
@@ -773,6 +835,10 @@ pkv_status dispatch(pkv_dtype dtype, int head_dim, int group, F&& f) {
 }
 
 }  // namespace
+
+size_t prefix_smem_bytes(int head_dim, int q_tiles, int num_groups) {
+  return head_dim == 64 ? PrefixSmem<64>::bytes(q_tiles, num_groups) : PrefixSmem<128>::bytes(q_tiles, num_groups);
+}
 
 pkv_status launch_prefix(PrefixParams& p, int ranges, int group, int head_dim, pkv_dtype dtype, cudaStream_t stream) {
   return dispatch(dtype, head_dim, group, [&](auto qt, auto d, auto g) {

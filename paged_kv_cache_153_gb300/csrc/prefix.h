@@ -35,6 +35,7 @@ struct PrefixParams {
   int64_t num_blocks;
   int batch, num_groups, n_q_heads, n_kv_heads, max_blocks_per_seq;
   int max_nblk;                  // ceil(max_context_len / 16)
+  int q_tiles;                   // row tiles in shared memory: 2, or 1 where no unit has more than 128 rows
   float qk_scale_log2;
 };
 
@@ -47,6 +48,8 @@ __host__ __device__ inline int64_t piece_row(int64_t group_start, int n_q_heads,
          static_cast<int64_t>(unit_in_head) * kPrefixUnitRows + range * kPrefixUnitRows;
 }
 
+// dynamic shared memory of the prefix kernel
+size_t prefix_smem_bytes(int head_dim, int q_tiles, int num_groups);
 // ranges: the grid of the prefix kernel
 pkv_status launch_prefix(PrefixParams& p, int ranges, int group, int head_dim, pkv_dtype dtype, cudaStream_t stream);
 pkv_status launch_prefix_merge(const PrefixParams& p, int ranges, const DecodeParams& rest, int rest_grid, int group,
