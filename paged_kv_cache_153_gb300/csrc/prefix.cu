@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   PrefixGroup gr{0, 0, 0, 0, -1};
   int64_t V, c0, tot, ne_b, tot_ne;
   int nb;
-  if (p.batch <= kCombineLocalPrefix && p.num_groups <= 32) {
+  const bool local = p.batch <= kCombineLocalPrefix && p.num_groups <= 32;
+  if (local) {
     // small calls: from the inputs, as the two kernels take it, before the wait.
     // Lane j holds group j's bounds and whether a sequence covers its blocks.
     int start = INT32_MAX, stop = INT32_MAX, blocks = 0;
@@ -665,7 +666,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     gr.start = __shfl_sync(0xffffffffu, start, from);
     gr.rows = m ? __shfl_sync(0xffffffffu, rows, from) : 0;
     gr.blocks = __shfl_sync(0xffffffffu, blocks, from);
-    pdl_wait_and_release();
   } else {
     // else from what the two kernels leave in the workspace
     pdl_wait_and_release();
@@ -705,9 +705,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     sp = combine_span(rest, g, c0, nb, tot, ne_b, tot_ne, rest_grid);
     n_own = sp.r1 - sp.r0 + 1;
   }
-  for (int64_t x0 = 0; x0 < n_pre + n_own; x0 += 32) {
-    const int64_t x = x0 + lane;
-    const float *ml = nullptr, *o = nullptr;
+  // state x of the list (null: its range holds none of the pair's)
+  auto locate = [&](int64_t x, const float*& ml, const float*& o) {
+    ml = o = nullptr;
     if (x < n_pre) {
       const int64_t r = r0 + x;
       if (max(lo, div_nonneg(r * V, R)) < min(hi, div_nonneg((r + 1) * V, R))) {
@@ -726,6 +726,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         o = rest.ws_o + i * D;
       }
     }
+  };
+  const float *ml, *o;
+  locate(lane, ml, o);
+  if (local) pdl_wait_and_release();
+  for (int64_t x0 = 0; x0 < n_pre + n_own; x0 += 32) {
+    if (x0 > 0) locate(x0 + lane, ml, o);
     const float2 state = ml != nullptr ? *reinterpret_cast<const float2*>(ml) : make_float2(-INFINITY, 0.f);
     uint32_t left = __ballot_sync(0xffffffffu, ml != nullptr);
     // each piece's weight against the maximum over all of them (the lanes', then
