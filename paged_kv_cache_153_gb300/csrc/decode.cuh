@@ -178,6 +178,14 @@ __device__ __forceinline__ int prefix_blocks(const DecodeParams& p, int b) {
   return shares_prefix(blocks, p.context_lens[b], min(p.max_blocks_per_seq, p.max_nblk)) ? blocks : 0;
 }
 
+// a / b of non-negative values: 32-bit division where they fit (a quarter of
+// the 64-bit one's instructions, on the path to a thread block's first load)
+__device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Partition mode: the flat space of W blocks is cut into NP = ceil(W / P)
 // partitions of P = part_blocks blocks (the last may be shorter), and range r
 // of R owns the consecutive partitions [floor(r NP / R), floor((r + 1) NP / R)).
@@ -228,7 +236,7 @@ __device__ __forceinline__ int64_t blocks_before_cost(int64_t v, const int* cum,
   const int nb = cum[lo + 1] - cum[lo];
   const int64_t unit = static_cast<int64_t>(kBlockCost) * nb + A;
   const int64_t rem = v - seq_cost(cum, ne, lo, Hkv, A);
-  const int64_t g = rem / unit, w = rem % unit;
+  const int64_t g = div_nonneg(rem, unit), w = rem - g * unit;
   const int64_t cnt = (w <= A) ? 0 : min(static_cast<int64_t>(nb), (w - A + kBlockCost - 1) / kBlockCost);
   return static_cast<int64_t>(Hkv) * cum[lo] + g * nb + cnt;
 }
@@ -653,8 +661,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
         lo = part_range_start(r, W, R, p.part_blocks);
         hi = part_range_start(r + 1, W, R, p.part_blocks);
       } else {
-        lo = blocks_before_cost((r * V) / R, cum, ne, p.batch, Hkv, A);
-        hi = blocks_before_cost(((r + 1) * V) / R, cum, ne, p.batch, Hkv, A);
+        lo = blocks_before_cost(div_nonneg(r * V, R), cum, ne, p.batch, Hkv, A);
+        hi = blocks_before_cost(div_nonneg((r + 1) * V, R), cum, ne, p.batch, Hkv, A);
       }
     };
     // the segment that starts at block f of range r = [f_lo, f_hi)
@@ -667,8 +675,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
       sg.b = lo;
       sg.nb = cum[lo + 1] - cum[lo];
       const int64_t rem = f - static_cast<int64_t>(Hkv) * cum[lo];
-      sg.g = static_cast<int>(rem / sg.nb);
-      sg.i0 = static_cast<int>(rem % sg.nb);
+      sg.g = static_cast<int>(div_nonneg(rem, sg.nb));
+      sg.i0 = static_cast<int>(rem - static_cast<int64_t>(sg.g) * sg.nb);
       sg.f_end = min(f_hi, f + (sg.nb - sg.i0));
       sg.i1 = sg.i0 + static_cast<int>(sg.f_end - f);
       sg.r = r;
@@ -1455,14 +1463,6 @@ __global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1)
 // piece is in slot 2 r0 when its first block opens range r0, else 2 r0 + 1;
 // every later piece is in slot 2 r of its range r (the range's first segment).
 // ---------------------------------------------------------------------------
-// a / b of non-negative values: 32-bit division where they fit (a quarter of
-// the 64-bit one's instructions, on the path between a merge's wait and its loads)
-__device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0)
-    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 struct CombineSpan {
   int64_t r0, r1;
   bool first_is_head;

@@ -154,11 +154,11 @@ __device__ __forceinline__ PrefixSeg prefix_segment(const PrefixGroup* groups, i
   const PrefixGroup gr = groups[lo];
   const int kt = prefix_tiles(gr.blocks), units = prefix_units(gr.rows);
   const int64_t rem = pos - gr.cost;
-  const int64_t u = rem / kt;
+  const int64_t u = div_nonneg(rem, kt);
   PrefixSeg s;
   s.group = lo;
-  s.g = static_cast<int>(u / units);
-  s.unit = static_cast<int>(u % units);
+  s.g = static_cast<int>(div_nonneg(u, units));
+  s.unit = static_cast<int>(u - static_cast<int64_t>(s.g) * units);
   s.t0 = static_cast<int>(rem - u * kt);
   s.t1 = static_cast<int>(min(static_cast<int64_t>(kt), s.t0 + (end - pos)));
   s.next = pos + (s.t1 - s.t0);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     for (int j = tid; j <= p.num_groups; j += kXThreads) p.groups[j] = groups[j];
   const uint32_t tmem = *tmem_slot;
   const int64_t V = groups[p.num_groups].cost, R = gridDim.x, range = blockIdx.x;
-  const int64_t first = (range * V) / R, end = ((range + 1) * V) / R;
+  const int64_t first = div_nonneg(range * V, R), end = div_nonneg((range + 1) * V, R);
   auto segment = [&](int64_t pos) { return prefix_segment(groups, p.num_groups, p.n_q_heads, pos, end, range); };
   // S / P of a chain at columns 128 chain, its O at 256 + chain D
   constexpr int kOCol = 2 * kXKeys;
