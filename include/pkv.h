@@ -465,12 +465,14 @@ pkv_status pkv_paged_decode_step_int8(const void* q, const void* k_new, const vo
  *                      slices of one projection's output.  Strides: multiples
  *                      of 8, at least H head_dim.
  *   q_out              as q, with its own stride; q_out == q with the same
- *                      stride turns q in place.  Other overlaps are undefined.
+ *                      stride turns q in place.  Other overlaps, of it or of
+ *                      the caches with an input, are undefined.
  *   positions          device int32 [T]; a negative one marks a padding token,
  *                      for which nothing is written.
  *   slot_mapping       device int64 [T]; negative: no append for the token (q
  *                      is turned all the same); past the pool: skipped and
- *                      PKV_ERR_OOB in err_flag.
+ *                      PKV_ERR_OOB in err_flag.  The slots of one call are
+ *                      distinct.
  *   turns, amplitude   from pkv_rope_plan, turns in device memory.
  * q and q_out may both be NULL (append only), or k_new and v_new (turn q only;
  * the caches and slots are then not used).  rot_dim: a multiple of 16 up to

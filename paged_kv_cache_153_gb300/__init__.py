@@ -190,14 +190,18 @@ def _stream(stream) -> int | None:
     return _current_stream()
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t, dtype) -> int:
     if dtype is not None:
         return dtype
-    import torch
-    if t.dtype == torch.float16:
-        return PKV_F16
-    if t.dtype == torch.bfloat16:
-        return PKV_BF16
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float16: PKV_F16, torch.bfloat16: PKV_BF16})
+    code = _dtype_codes.get(t.dtype)
+    if code is not None:
+        return code
     raise TypeError(f"cannot infer the 16-bit kind of {t.dtype}; pass dtype=PKV_F16/PKV_BF16")
 
 
@@ -472,7 +476,29 @@ def pkv_paged_decode_step_int8(q, k_new, v_new, k_cache, v_cache, slab_params, b
         workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
 
 
-_ROPE_LAYOUTS = {"half": PKV_ROPE_HALF, "interleaved": PKV_ROPE_INTERLEAVED}
+_int32_dtype = None
+
+
+def _int32(*tensors) -> None:
+    """Index tensors must be contiguous int32: another type would be read as
+    garbage indices."""
+    global _int32_dtype
+    if _int32_dtype is None:
+        import torch
+        _int32_dtype = torch.int32
+    for t in tensors:
+        if t is not None and (t.dtype is not _int32_dtype or not t.is_contiguous()):
+            raise TypeError("tables, lengths, positions and lists must be contiguous int32 tensors")
+
+
+def _contiguous(*tensors) -> None:
+    for t in tensors:
+        if not t.is_contiguous():
+            raise ValueError("q, out, caches, bounds, scores and slots must be contiguous")
+
+
+_ROPE_LAYOUTS = {"half": PKV_ROPE_HALF, "interleaved": PKV_ROPE_INTERLEAVED, PKV_ROPE_HALF: PKV_ROPE_HALF,
+                 PKV_ROPE_INTERLEAVED: PKV_ROPE_INTERLEAVED}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
 
 
@@ -504,6 +530,9 @@ def _token_stride(t, name: str, heads: int, d: int) -> int:
 
 def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, scales, layout, amplitude,
           dtype, err_flag, stream):
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"unknown layout {layout!r}")
+    _int32(positions)
     n = positions.numel()
     q_args, kv_args, hq, hkv, nb, bs = (None, 0, None, 0), (None, 0, None, 0), 0, 0, 0, 16
     if q is not None:
@@ -517,14 +546,15 @@ def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v
         shape = k_new.shape
         if shape != (n, hkv, dk) or v_new.shape != shape or (q is not None and dk != d):
             raise ValueError("k_new and v_new must be [T, num_kv_heads, head_dim] of the cache")
-        if slot_mapping.numel() != n:
-            raise ValueError("slot_mapping and positions differ in length")
+        if slot_mapping.numel() != n or slot_mapping.element_size() != 8:
+            raise ValueError("slot_mapping must be int64, one slot per position")
+        _contiguous(slot_mapping, k_cache, v_cache)
         d = dk
         kv_args = (k_new.data_ptr(), _token_stride(k_new, "k_new", hkv, d), v_new.data_ptr(),
                    _token_stride(v_new, "v_new", hkv, d))
     _check(fn, getattr(lib, fn)(
         q_args[0], q_args[1], *kv_args, positions.data_ptr(), _ptr(slot_mapping), n, turns.data_ptr(),
-        2 * turns.numel(), _ROPE_LAYOUTS.get(layout, layout), amplitude, q_args[2], q_args[3], _ptr(k_cache),
+        2 * turns.numel(), _ROPE_LAYOUTS[layout], amplitude, q_args[2], q_args[3], _ptr(k_cache),
         _ptr(v_cache), nb, *scales, hq, hkv, d, bs, _dtype_code(k_new if q is None else q, dtype), _ptr(err_flag),
         _stream(stream)))
 
@@ -557,6 +587,8 @@ def _block_bounds(fn, k_cache, block_tables, context_lens, bounds, new_lens, max
     nb, hkv, bs, d = k_cache.shape
     if tuple(bounds.shape) != (nb, hkv, 2, d):
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
+    _int32(block_tables, context_lens, new_lens)
+    _contiguous(k_cache, bounds)
     _check(fn, getattr(lib, fn)(
         _ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(new_lens), max_new_len, context_lens.numel(), hkv, d,
         bs, block_tables.shape[1], nb, _ptr(bounds), _dtype_code(bounds, dtype), _ptr(err_flag), _stream(stream)))
@@ -597,6 +629,8 @@ def pkv_block_scores(q, bounds, block_tables, context_lens, scores, *, scale: fl
                          "head_dim]")
     if bounds.dtype != q.dtype:
         raise TypeError("bounds and q differ in dtype")
+    _int32(block_tables, context_lens)
+    _contiguous(q, bounds, scores)
     _check("pkv_block_scores", lib.pkv_block_scores(
         _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), _ptr(k_scale), b, hq, hkv, d, 16,
         block_tables.shape[1], nb, max_context_len, scale, _ptr(scores), _dtype_code(q, dtype), _ptr(err_flag),
@@ -610,6 +644,8 @@ def pkv_select_blocks(scores, context_lens, selected, *, num_first: int = 1, num
     b, hkv, blocks = scores.shape
     if tuple(selected.shape[:2]) != (b, hkv):
         raise ValueError("selected must be [batch, num_kv_heads, budget]")
+    _int32(context_lens, selected)
+    _contiguous(scores)
     _check("pkv_select_blocks", lib.pkv_select_blocks(
         _ptr(scores), _ptr(context_lens), b, hkv, 16, blocks, num_first, num_last, selected.shape[2], _ptr(selected),
         _ptr(err_flag), _stream(stream)))
@@ -621,6 +657,8 @@ def _sparse(fn, q, k_cache, v_cache, scales, block_tables, context_lens, selecte
     nb, hkv, bs, _ = k_cache.shape
     if tuple(selected.shape[:2]) != (b, hkv):
         raise ValueError("selected must be [batch, num_kv_heads, budget]")
+    _int32(block_tables, context_lens, selected)
+    _contiguous(q, k_cache, v_cache, out)
     _check(fn, getattr(lib, fn)(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_tables), _ptr(context_lens), _ptr(selected),
         selected.shape[2], b, hq, hkv, d, bs, block_tables.shape[1], nb, scale, _ptr(out), _dtype_code(q, dtype),
@@ -667,6 +705,8 @@ def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context
     nb, hkv, bs, _ = k_cache.shape
     if group_starts.numel() != prefix_lens.numel() + 1:
         raise ValueError("group_starts must have one entry more than prefix_lens")
+    _int32(block_tables, context_lens, group_starts, prefix_lens)
+    _contiguous(q, k_cache, v_cache, out)
     _check("pkv_paged_decode_attention_prefix", lib.pkv_paged_decode_attention_prefix(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(group_starts),
         _ptr(prefix_lens), prefix_lens.numel(), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len,

@@ -128,6 +128,13 @@ def test_row_counts_around_the_tiles(pkv, n, dtype):
     assert int(case.err.item()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,n", [(2, 2, 64, 200), (2, 2, 128, 300), (16, 2, 64, 40), (4, 2, 64, 129)])
+def test_row_tiles_of_other_groups_and_dims(pkv, hq, hkv, d, n):
+    case = Case([(1040, [(11 * i) % 70 for i in range(n)])], hq=hq, hkv=hkv, d=d, dtype="bf16", seed=n)
+    case.check(case.run(pkv), range(0, n, max(1, n // 7)))
+    assert int(case.err.item()) == 0
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 8, 64), (8, 1, 128)])
 def test_many_groups(pkv, hq, hkv, d):
     groups = [(1500, [10, 20, 1]), (0, [100, 7]), (48, []), (16, [3]), (4000, [1] * 40), (33, [64, 2]), (640, [0] * 5)]
@@ -254,9 +261,46 @@ def test_device_errors(pkv):
         assert broken(lambda c: c.starts.copy_(torch.tensor(starts))) == 4, starts
 
 
+def test_contexts_past_the_declared_bound(pkv):
+    # as in the dense decode: clamped to the bound and reported
+    case = Case([(512, [30, 9]), (64, [400])], seed=21)
+    case.max_ctx = 523
+    out = case.run(pkv)
+    assert int(case.err.item()) == 4
+    case.check(out, [1, 2])
+    case = Case([(512, [30, 9]), (64, [100])], seed=22)
+    case.max_ctx = 170                               # shorter than the first group's prefix
+    out = case.run(pkv)
+    assert int(case.err.item()) == 4
+    case.check(out, [2])
+
+
+def test_far_blocks_of_a_large_pool(pkv):
+    # blocks past 4 GiB of the cache
+    case = Case([(256, [20, 33])], hq=16, hkv=8, seed=23)
+    near = case.run(pkv)
+    nb = 140000
+    move = {int(i): nb - 1 - k for k, i in enumerate(np.unique(case.tab_h[case.tab_h >= 0]))}
+    for name in ("kc", "vc"):
+        big = torch.zeros((nb, 8, 16, 128), dtype=torch.bfloat16, device="cuda")
+        small = getattr(case, name)
+        for i, j in move.items():
+            big[j] = small[i]
+        setattr(case, name, big)
+    case.tab_h = np.vectorize(lambda i: move.get(int(i), -1))(case.tab_h).astype(np.int32)
+    case.tab.copy_(torch.from_numpy(case.tab_h))
+    assert torch.equal(case.run(pkv), near) and int(case.err.item()) == 0
+
+
 def test_refusals(pkv):
     case = Case([(512, [30, 9])], seed=20)
     ws = case.workspace(pkv)
+    for name in ("lens", "tab", "pre", "starts"):
+        keep = getattr(case, name)
+        setattr(case, name, keep.long())
+        with pytest.raises(TypeError):
+            case.run(pkv, ws)
+        setattr(case, name, keep)
     with pytest.raises(pkv.PkvError) as e:
         case.run(pkv, ws[:-1])
     assert e.value.status == 6

@@ -254,6 +254,32 @@ def test_binding_refuses_shapes_that_do_not_fit(pkv):
         pkv.pkv_rope_append(c.q, c.k, c.v, pos, slots[:4], c.turns, c.q_out, *c.caches)
     with pytest.raises(ValueError):
         pkv.pkv_rope_append(c.q, None, None, pos, None, c.turns, c.q_out[:3], None, None)
+    with pytest.raises(ValueError):
+        pkv.pkv_rope_append(c.q, None, None, pos, None, c.turns, c.q_out, None, None, layout="other")
+    with pytest.raises(TypeError):
+        pkv.pkv_rope_append(c.q, None, None, pos.long(), None, c.turns, c.q_out, None, None)
+    with pytest.raises(ValueError):
+        pkv.pkv_rope_append(c.q, c.k, c.v, pos, slots.int(), c.turns, c.q_out, *c.caches)
+    with pytest.raises(pkv.PkvError) as e:   # one row of q for every token
+        pkv.pkv_rope_append(c.q[:1].expand(5, 4, 64), None, None, pos, None, c.turns, c.q_out, None, None)
+    assert e.value.status == 1
+    pkv.pkv_rope_append(c.q[:0], None, None, pos[:0], None, c.turns, c.q_out[:0], None, None)   # no tokens
     with pytest.raises(pkv.PkvError) as e:   # 24 turned elements
         pkv.pkv_rope_append(c.q, None, None, pos, None, c.turns[:12], c.q_out, None, None)
     assert e.value.status == 2
+
+
+def test_far_slots_of_a_large_pool(pkv):
+    # slots past 4 GiB of the cache: byte offsets need 64 bits
+    nb = 140000                          # 32 KiB a block: 4.6 GB
+    c = Case(pkv, tokens=6, hq=8, hkv=8, d=128, rot=128, dtype="bf16", seed=10)
+    far = torch.zeros((2, nb, 8, 16, 128), dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([16 * nb - 1, 0, 16 * nb - 40, 17, 16 * (nb - 9) + 3, 16 * 131072], device="cuda")
+    pkv.pkv_rope_append(c.q, c.k, c.v, c.pos.cuda(), slots, c.turns, c.q_out, far[0], far[1], layout=c.layout,
+                        amplitude=c.amp, err_flag=c.err)
+    c.run()                              # the same rows, near
+    for i in range(2):
+        near = c.caches[i][c.slots // 16, :, c.slots % 16]
+        assert torch.equal(far[i][slots // 16, :, slots % 16], near)
+        assert int((far[i] != 0).any(-1).any(1).sum()) == 6
+    assert int(c.err.item()) == 0

@@ -505,6 +505,20 @@ def test_binding_refuses_shapes_that_do_not_fit(pkv):
     with pytest.raises(ValueError):
         pkv.pkv_block_scores(case.q, bounds, case.tab, case.lens, torch.zeros((1, 2, 9), device="cuda"), scale=1.0,
                              max_context_len=100)
+    lists = torch.zeros((1, 2, 4), dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):       # index types and strides
+        case.attention(pkv, lists.long())
+    with pytest.raises(TypeError):
+        case.attention(pkv, torch.zeros((1, 2, 8), dtype=torch.int32, device="cuda")[..., ::2])
+    with pytest.raises(ValueError):
+        pkv.pkv_select_blocks(torch.zeros((1, 2, 14), device="cuda")[..., ::2], case.lens, lists)
+    with pytest.raises(TypeError):
+        pkv.pkv_select_blocks(torch.zeros((1, 2, 7), device="cuda"), case.lens.long(), lists)
+    q = case.q
+    case.q = torch.zeros((1, 8, 256), dtype=q.dtype, device="cuda")[..., ::2]
+    with pytest.raises(ValueError):
+        case.attention(pkv, lists)
+    case.q = q
     with pytest.raises(TypeError):
         pkv.pkv_block_scores(case.q, bounds.half(), case.tab, case.lens, torch.zeros((1, 2, 7), device="cuda"),
                              scale=1.0, max_context_len=100)
@@ -580,6 +594,24 @@ def test_a_decode_step_end_to_end(pkv, dtype):
         for n, t in ref.items():
             live = ~torch.isnan(buf[n].float())
             assert torch.equal(buf[n][live], t[live]) and (n == "scores" or bool(live.all()))
+
+
+def test_two_streams_each_with_its_workspace(pkv):
+    a, b = Case([4000, 1300, 20], seed=20), Case([900] * 9, hq=16, hkv=4, dtype="f16", seed=21)
+    jobs = []
+    for case in (a, b):
+        sel = random_lists(case, 30, seed=4)
+        n = pkv.pkv_decode_workspace_bytes(len(case.lens_h), case.hq, case.hkv, case.d, 30, 480)
+        jobs.append((case, sel, case.attention(pkv, sel), torch.empty_like(case.q),
+                     torch.empty(n, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for case, sel, _, out, ws, stream in jobs:
+            pkv.pkv_paged_decode_attention_sparse(case.q, case.kc, case.vc, case.tab, case.lens, sel, out,
+                                                  scale=case.scale, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, ref, out, _, _ in jobs:
+        assert torch.equal(out, ref)
 
 
 def test_far_blocks_of_a_large_pool(pkv):
