@@ -2,8 +2,9 @@
 
 Argument marshalling only: every function here extracts device pointers,
 sizes and the current CUDA stream from torch tensors and calls the C entry
-point of the same name (declared in include/pkv.h).  All arithmetic runs in
-the library's CUDA kernels; there is no CPU fallback.  Importing this module
+point of the same name (declared in include/pkv.h): the per-step calls through
+the module _call (csrc/pycall.cpp), the others through ctypes.  All arithmetic
+runs in the library's CUDA kernels; there is no CPU fallback.  Importing this module
 fails loudly when the library has not been built (``__graft_entry__.build()``
 or ``python -m paged_kv_cache_153_gb300._build``).
 
@@ -46,6 +47,7 @@ if not os.path.exists(library_path):
     raise ImportError(f"{library_path} is missing: build it with __graft_entry__.build() "
                       "(the CUDA path has no fallback)")
 lib = C.CDLL(library_path)
+from . import _call  # noqa: E402  (built with the library; finds it next to itself)
 
 # The prefill kernel lives in a library of its own (pkv_prefill.h), loaded on
 # first use, so that a process that only decodes never loads it.
@@ -208,7 +210,7 @@ def _dtype_code(t, dtype) -> int:
 def pkv_slot_mapping(block_tables, positions, slot_mapping, *, num_blocks: int, seq_idx=None,
                      position_offset: int = 0, block_size: int = 16, err_flag=None, stream=None) -> None:
     n = positions.numel()
-    _check("pkv_slot_mapping", lib.pkv_slot_mapping(
+    _check("pkv_slot_mapping", _call.pkv_slot_mapping(
         _ptr(block_tables), block_tables.shape[1], num_blocks, _ptr(seq_idx), _ptr(positions),
         position_offset, n, block_size, _ptr(slot_mapping), _ptr(err_flag), _stream(stream)))
 
@@ -216,14 +218,14 @@ def pkv_slot_mapping(block_tables, positions, slot_mapping, *, num_blocks: int, 
 def pkv_kv_append(k_new, v_new, slot_mapping, k_cache, v_cache, *, dtype=None, err_flag=None,
                   stream=None) -> None:
     nb, hkv, bs, d = k_cache.shape
-    _check("pkv_kv_append", lib.pkv_kv_append(
+    _check("pkv_kv_append", _call.pkv_kv_append(
         _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache),
         nb, hkv, d, bs, _dtype_code(k_new, dtype), _ptr(err_flag), _stream(stream)))
 
 
 def _append_fp8(fn, k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, in_dtype, err_flag, stream):
     nb, hkv, bs, d = k_cache.shape
-    _check(fn, getattr(lib, fn)(
+    _check(fn, getattr(_call, fn)(
         _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache),
         nb, _ptr(k_scale), _ptr(v_scale), hkv, d, bs, _dtype_code(k_new, in_dtype), _ptr(err_flag),
         _stream(stream)))
@@ -258,7 +260,7 @@ def pkv_paged_decode_attention(q, k_cache, v_cache, block_tables, context_lens, 
                                err_flag=None, stream=None) -> None:
     b, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    _check("pkv_paged_decode_attention", lib.pkv_paged_decode_attention(
+    _check("pkv_paged_decode_attention", _call.pkv_paged_decode_attention(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), b, hq, hkv, d, bs,
         block_tables.shape[1], nb, max_context_len, scale, _ptr(out), _dtype_code(q, dtype), partition_tokens,
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
@@ -268,7 +270,7 @@ def _decode_fp8(fn, q, k_cache, v_cache, k_scale, v_scale, block_tables, context
                 max_context_len, workspace, partition_tokens, q_dtype, err_flag, stream):
     b, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    _check(fn, getattr(lib, fn)(
+    _check(fn, getattr(_call, fn)(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
         _ptr(context_lens), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len, scale, _ptr(out),
         _dtype_code(q, q_dtype), partition_tokens, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -294,7 +296,7 @@ def pkv_paged_decode_step(q, k_new, v_new, k_cache, v_cache, block_tables, conte
                           dtype=None, err_flag=None, stream=None) -> None:
     b, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    _check("pkv_paged_decode_step", lib.pkv_paged_decode_step(
+    _check("pkv_paged_decode_step", _call.pkv_paged_decode_step(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), b,
         hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len, scale, _ptr(out), _dtype_code(q, dtype),
         partition_tokens, _ptr(slot_mapping_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -305,7 +307,7 @@ def _step_fp8(fn, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tab
               max_context_len, workspace, partition_tokens, slot_mapping_out, q_dtype, err_flag, stream):
     b, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    _check(fn, getattr(lib, fn)(
+    _check(fn, getattr(_call, fn)(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
         _ptr(block_tables), _ptr(context_lens), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len, scale,
         _ptr(out), _dtype_code(q, q_dtype), partition_tokens, _ptr(slot_mapping_out), _ptr(workspace),
@@ -335,7 +337,7 @@ def pkv_paged_decode_attention_noalloc(q, k_cache, v_cache, block_tables, contex
     caller workspace (for callers that cannot allocate)."""
     b, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    _check("pkv_paged_decode_attention_noalloc", lib.pkv_paged_decode_attention_noalloc(
+    _check("pkv_paged_decode_attention_noalloc", _call.pkv_paged_decode_attention_noalloc(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), b, hq, hkv, d, bs,
         block_tables.shape[1], nb, max_context_len, scale, _ptr(out), _dtype_code(q, dtype), partition_tokens,
         _ptr(err_flag), _stream(stream)))
@@ -347,7 +349,7 @@ def pkv_decode_step_host(h_q, h_k_new, h_v_new, h_block_tables, h_context_lens, 
                          err_flag=None, stream=None) -> None:
     b, hq, d = h_q.shape
     nb, hkv, bs, _ = k_cache.shape
-    _check("pkv_decode_step_host", lib.pkv_decode_step_host(
+    _check("pkv_decode_step_host", _call.pkv_decode_step_host(
         _ptr(h_q), _ptr(h_k_new), _ptr(h_v_new), _ptr(h_block_tables), _ptr(h_context_lens), _ptr(h_out),
         _ptr(d_q), _ptr(d_k_new), _ptr(d_v_new), _ptr(d_block_tables), _ptr(d_context_lens), _ptr(d_slots),
         _ptr(d_out), _ptr(k_cache), _ptr(v_cache), b, hq, hkv, d, bs, h_block_tables.shape[1], nb,
@@ -359,7 +361,7 @@ def pkv_copy_blocks(src_blocks, dst_blocks, k_cache, v_cache, *, err_flag=None, 
     """Copy-on-write block copy on the device: block dst_blocks[i] of both
     caches takes block src_blocks[i] (int32 device tensors of equal length)."""
     nb, hkv, bs, d = k_cache.shape
-    _check("pkv_copy_blocks", lib.pkv_copy_blocks(
+    _check("pkv_copy_blocks", _call.pkv_copy_blocks(
         _ptr(src_blocks), _ptr(dst_blocks), src_blocks.numel(), _ptr(k_cache), _ptr(v_cache), nb, hkv, d, bs,
         k_cache.element_size(), _ptr(err_flag), _stream(stream)))
 
@@ -398,7 +400,7 @@ def pkv_paged_decode_step_layer(q, k_new, v_new, k_cache, v_cache, block_tables,
     """The fused decode step on layer ``layer`` of a layer-major cache
     [NB, L, Hkv, 16, D]."""
     nb, n_layers, hkv, bs, d = k_cache.shape
-    _check("pkv_paged_decode_step_layer", lib.pkv_paged_decode_step_layer(
+    _check("pkv_paged_decode_step_layer", _call.pkv_paged_decode_step_layer(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         q.shape[0], q.shape[1], hkv, d, bs, block_tables.shape[1], nb, n_layers, layer, max_context_len, scale,
         _ptr(out), _dtype_code(q, dtype), partition_tokens, _ptr(slot_mapping_out), _ptr(workspace),
@@ -426,7 +428,7 @@ class StepGraph:
         self._h = h
 
     def launch(self, stream=None) -> None:
-        _check("pkv_step_graph_launch", lib.pkv_step_graph_launch(self._h, _stream(stream)))
+        _check("pkv_step_graph_launch", _call.pkv_step_graph_launch(self._h.value, _stream(stream)))
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -439,7 +441,7 @@ def pkv_kv_quantize_int8(k_src, v_src, k_cache, v_cache, slab_params, *, rows_us
                          err_flag=None, stream=None) -> None:
     """INT8 codes and per-(block, head) (k_min, k_max, v_min, v_max) of 16-bit pools."""
     nb, hkv, bs, d = k_cache.shape
-    _check("pkv_kv_quantize_int8", lib.pkv_kv_quantize_int8(
+    _check("pkv_kv_quantize_int8", _call.pkv_kv_quantize_int8(
         _ptr(k_src), _ptr(v_src), _ptr(k_cache), _ptr(v_cache), _ptr(slab_params), _ptr(rows_used), nb, hkv, d, bs,
         _dtype_code(k_src, dtype), _ptr(err_flag), _stream(stream)))
 
@@ -447,7 +449,7 @@ def pkv_kv_quantize_int8(k_src, v_src, k_cache, v_cache, slab_params, *, rows_us
 def pkv_kv_append_int8(k_new, v_new, slot_mapping, k_cache, v_cache, slab_params, *, dtype=None, err_flag=None,
                        stream=None) -> None:
     nb, hkv, bs, d = k_cache.shape
-    _check("pkv_kv_append_int8", lib.pkv_kv_append_int8(
+    _check("pkv_kv_append_int8", _call.pkv_kv_append_int8(
         _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache),
         _ptr(slab_params), nb, hkv, d, bs, _dtype_code(k_new, dtype), _ptr(err_flag), _stream(stream)))
 
@@ -456,7 +458,7 @@ def pkv_paged_decode_attention_int8(q, k_cache, v_cache, slab_params, block_tabl
                                     scale: float, max_context_len: int, workspace, partition_tokens: int = 0,
                                     q_dtype=None, err_flag=None, stream=None) -> None:
     nb, hkv, bs, d = k_cache.shape
-    _check("pkv_paged_decode_attention_int8", lib.pkv_paged_decode_attention_int8(
+    _check("pkv_paged_decode_attention_int8", _call.pkv_paged_decode_attention_int8(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(slab_params), _ptr(block_tables), _ptr(context_lens),
         q.shape[0], q.shape[1], hkv, d, bs, block_tables.shape[1], nb, max_context_len, scale, _ptr(out),
         _dtype_code(q, q_dtype), partition_tokens, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -469,7 +471,7 @@ def pkv_paged_decode_step_int8(q, k_new, v_new, k_cache, v_cache, slab_params, b
     """The INT8 decode step in one decode launch (head_dim 128): the new rows
     are appended with re-quantisation of their blocks, then attention."""
     nb, hkv, bs, d = k_cache.shape
-    _check("pkv_paged_decode_step_int8", lib.pkv_paged_decode_step_int8(
+    _check("pkv_paged_decode_step_int8", _call.pkv_paged_decode_step_int8(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(slab_params), _ptr(block_tables),
         _ptr(context_lens), q.shape[0], q.shape[1], hkv, d, bs, block_tables.shape[1], nb, max_context_len, scale,
         _ptr(out), _dtype_code(q, q_dtype), partition_tokens, _ptr(slot_mapping_out), _ptr(workspace),
@@ -552,7 +554,7 @@ def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v
         d = dk
         kv_args = (k_new.data_ptr(), _token_stride(k_new, "k_new", hkv, d), v_new.data_ptr(),
                    _token_stride(v_new, "v_new", hkv, d))
-    _check(fn, getattr(lib, fn)(
+    _check(fn, getattr(_call, fn)(
         q_args[0], q_args[1], *kv_args, positions.data_ptr(), _ptr(slot_mapping), n, turns.data_ptr(),
         2 * turns.numel(), _ROPE_LAYOUTS[layout], amplitude, q_args[2], q_args[3], _ptr(k_cache),
         _ptr(v_cache), nb, *scales, hq, hkv, d, bs, _dtype_code(k_new if q is None else q, dtype), _ptr(err_flag),
@@ -589,7 +591,7 @@ def _block_bounds(fn, k_cache, block_tables, context_lens, bounds, new_lens, max
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
     _int32(block_tables, context_lens, new_lens)
     _contiguous(k_cache, bounds)
-    _check(fn, getattr(lib, fn)(
+    _check(fn, getattr(_call, fn)(
         _ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(new_lens), max_new_len, context_lens.numel(), hkv, d,
         bs, block_tables.shape[1], nb, _ptr(bounds), _dtype_code(bounds, dtype), _ptr(err_flag), _stream(stream)))
 
@@ -631,7 +633,7 @@ def pkv_block_scores(q, bounds, block_tables, context_lens, scores, *, scale: fl
         raise TypeError("bounds and q differ in dtype")
     _int32(block_tables, context_lens)
     _contiguous(q, bounds, scores)
-    _check("pkv_block_scores", lib.pkv_block_scores(
+    _check("pkv_block_scores", _call.pkv_block_scores(
         _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), _ptr(k_scale), b, hq, hkv, d, 16,
         block_tables.shape[1], nb, max_context_len, scale, _ptr(scores), _dtype_code(q, dtype), _ptr(err_flag),
         _stream(stream)))
@@ -646,7 +648,7 @@ def pkv_select_blocks(scores, context_lens, selected, *, num_first: int = 1, num
         raise ValueError("selected must be [batch, num_kv_heads, budget]")
     _int32(context_lens, selected)
     _contiguous(scores)
-    _check("pkv_select_blocks", lib.pkv_select_blocks(
+    _check("pkv_select_blocks", _call.pkv_select_blocks(
         _ptr(scores), _ptr(context_lens), b, hkv, 16, blocks, num_first, num_last, selected.shape[2], _ptr(selected),
         _ptr(err_flag), _stream(stream)))
 
@@ -659,7 +661,7 @@ def _sparse(fn, q, k_cache, v_cache, scales, block_tables, context_lens, selecte
         raise ValueError("selected must be [batch, num_kv_heads, budget]")
     _int32(block_tables, context_lens, selected)
     _contiguous(q, k_cache, v_cache, out)
-    _check(fn, getattr(lib, fn)(
+    _check(fn, getattr(_call, fn)(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_tables), _ptr(context_lens), _ptr(selected),
         selected.shape[2], b, hq, hkv, d, bs, block_tables.shape[1], nb, scale, _ptr(out), _dtype_code(q, dtype),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
@@ -707,7 +709,7 @@ def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context
         raise ValueError("group_starts must have one entry more than prefix_lens")
     _int32(block_tables, context_lens, group_starts, prefix_lens)
     _contiguous(q, k_cache, v_cache, out)
-    _check("pkv_paged_decode_attention_prefix", lib.pkv_paged_decode_attention_prefix(
+    _check("pkv_paged_decode_attention_prefix", _call.pkv_paged_decode_attention_prefix(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(group_starts),
         _ptr(prefix_lens), prefix_lens.numel(), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len,
         max_prefix_len, scale, _ptr(out), _dtype_code(q, dtype), _ptr(workspace),

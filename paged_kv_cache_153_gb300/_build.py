@@ -1,12 +1,13 @@
-"""Build libpkv.so and libpkv_prefill.so in-tree for sm_103a with nvcc (no
-cmake, no torch extension).
+"""Build libpkv.so, libpkv_prefill.so and the binding's _call.so in-tree for
+sm_103a with nvcc (no cmake, no torch extension).
 
 The translation units compile in parallel.  Both shared libraries are linked
 with the static CUDA runtime so they load without extra library paths.  The
 prefill kernel (thread-block clusters sharing K/V loads by TMA multicast) sits
 in libpkv_prefill.so of its own, so that a process that only decodes never
 loads it; that library takes its error reporting from libpkv.so, found next to
-it through an $ORIGIN run path.
+it through an $ORIGIN run path.  _call.so is a CPython module that converts the
+arguments of the per-step calls and calls libpkv.so.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -23,12 +25,14 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libpkv.so")
 PREFILL_LIB_PATH = os.path.join(PKG_DIR, "libpkv_prefill.so")
+CALL_PATH = os.path.join(PKG_DIR, "_call.so")
 
 CUDA_SOURCES = ["append.cu", "api.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e4m3.cu", "decode_e5m2.cu",
                 "noalloc.cu", "decode_int8.cu", "append_int8.cu", "rope.cu",
                 "block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu", "decode_rest.cu", "prefix.cu"]
 PREFILL_SOURCES = ["prefill.cu"]
 CXX_SOURCES = ["pool.cpp"]
+CALL_SOURCES = ["pycall.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -48,7 +52,7 @@ def _source_digest() -> str:
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode())
                     h.update(f.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS).encode())
+    h.update(" ".join(ARCH + NVCC_FLAGS + [sysconfig.get_paths()["include"]]).encode())
     return h.hexdigest()
 
 
@@ -59,12 +63,12 @@ def _run(cmd: list[str]) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libpkv.so and libpkv_prefill.so next to this file;
-    skip when up to date."""
+    """Compile and link libpkv.so, libpkv_prefill.so and _call.so next to this
+    file; skip when up to date."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     stamp = os.path.join(BUILD_DIR, "libpkv.stamp")
     digest = _source_digest()
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(PREFILL_LIB_PATH) and os.path.exists(stamp):
+    if not force and all(os.path.exists(p) for p in (LIB_PATH, PREFILL_LIB_PATH, CALL_PATH, stamp)):
         with open(stamp) as f:
             if f.read().strip() == digest:
                 return LIB_PATH
@@ -73,9 +77,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for src in CUDA_SOURCES + PREFILL_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         jobs.append([nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-    for src in CXX_SOURCES:
+    for src in CXX_SOURCES + CALL_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
-        jobs.append([nvcc, *NVCC_FLAGS, "-x", "c++", "-c", os.path.join(CSRC, src), "-o", obj])
+        jobs.append([nvcc, *NVCC_FLAGS, "-I" + sysconfig.get_paths()["include"], "-x", "c++", "-c",
+                     os.path.join(CSRC, src), "-o", obj])
     with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
         for cmd, _ in zip(jobs, ex.map(_run, jobs)):
             if verbose:
@@ -89,6 +94,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *pobjs, "-L" + PKG_DIR, "-lpkv",
           "-Xlinker", "-rpath,$ORIGIN"])
     os.replace(tmp, PREFILL_LIB_PATH)
+    cobjs = [os.path.join(BUILD_DIR, s.rsplit(".", 1)[0] + ".o") for s in CALL_SOURCES]
+    tmp = CALL_PATH + ".tmp"
+    _run([nvcc, "-shared", "-cudart", "none", "-o", tmp, *cobjs, "-L" + PKG_DIR, "-lpkv", "-Xlinker",
+          "-rpath,$ORIGIN"])
+    os.replace(tmp, CALL_PATH)
     with open(stamp, "w") as f:
         f.write(digest)
     return LIB_PATH
