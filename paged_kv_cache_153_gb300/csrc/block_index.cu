@@ -92,12 +92,12 @@ struct RowChunk {
 // Flat is taken when the launch by sequence would be more than kFlatWaves
 // times the resident warps.  On GB300: bounds of 32 contexts of 2048..32768
 // tokens (E4M3, 389 MB) 64.2 us flat, 120 by sequence; scores of 64 contexts of
-// 1024..32768 (141 MB) 27.9 against 27.4, but with two of 131072 among 62 of
-// 1000 (83 MB) 18.1 against 71.5; one step's bounds of 64 sequences stay by
+// 1024..32768 (141 MB) 27.3 against 27.4, but with two of 131072 among 62 of
+// 1000 (83 MB) 16.8 against 71.5; one step's bounds of 64 sequences stay by
 // sequence (2.1 us).
 // ---------------------------------------------------------------------------
 constexpr int kFlatWaves = 2;
-constexpr int kFlatMaxBatch = 1000;              // whose counts fit in shared memory beside the stages
+constexpr int kFlatMaxBatch = 900;               // whose counts fit in shared memory beside the stages
 
 // cum[b] = units of the sequences before b, cum[batch] = all (whole block; ends synchronised)
 template <int THREADS, typename F>
@@ -451,13 +451,15 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const __
 // kScoreHeads KV heads; one warp copies a unit's bounds into a ring of stages
 // -- one 1-D bulk copy of up to 4 KiB per block, its heads being contiguous --
 // with the unit's queries behind them, and 8 warps take its (16 blocks, head)
-// products from there.  Rows lie 64 bytes past a multiple of 128 apart, so a
+// products from there.  The bulk copies set the pace: a thread block gets one
+// about every 185 clocks, which at 4 KiB each is this SM's share of HBM (half the
+// heads per unit, 2 KiB, took twice as long, with 8 warps or 12).  Rows lie 64 bytes past a multiple of 128 apart, so a
 // quarter warp's 16-byte loads touch every bank once.
 constexpr int kScoreConsumers = 8;
 constexpr int kScoreThreads = (kScoreConsumers + 1) * 32;
 constexpr int kScoreStages = 3;
 constexpr int kScoreMaxTile = 128;
-constexpr int kScoreStageBytes = 73 * 1024;       // three of them, and 1000 counts, fit one SM
+constexpr int kScoreStageBytes = 73 * 1024;       // three of them, and the counts, fit one SM
 
 template <int D>
 constexpr int kScoreHeads = 4096 / (4 * D);
@@ -482,7 +484,7 @@ struct ScoreLayout {
   }
   __host__ __device__ size_t bytes(int batch) const {
     return 128 + static_cast<size_t>(kScoreStages) * (stage + sizeof(ScoreUnit)) + 16 * kScoreStages +
-           (static_cast<size_t>(batch) + 1) * sizeof(int);
+           (2 * static_cast<size_t>(batch) + 1) * sizeof(int);
   }
 };
 
@@ -496,6 +498,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
   uint64_t* full = reinterpret_cast<uint64_t*>(units + kScoreStages);
   uint64_t* empty = full + kScoreStages;
   int* cum = reinterpret_cast<int*>(empty + kScoreStages);   // [batch + 1] tiles
+  int* scored = cum + p.batch + 1;                           // [batch] blocks
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < kScoreStages; ++s) {
@@ -506,44 +509,56 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
   }
   pdl_wait_and_release();
   scan_units<kScoreThreads>(p.batch, cum, warp_sum, [&](int b) {
-    return (scored_blocks(p, b, blockIdx.x == 0) + lay.tile - 1) / lay.tile;
+    scored[b] = scored_blocks(p, b, blockIdx.x == 0);
+    return (scored[b] + lay.tile - 1) / lay.tile;
   });
   const int chunks = (p.n_kv_heads + lay.heads - 1) / lay.heads;
   const int64_t total = static_cast<int64_t>(cum[p.batch]) * chunks;
 
   if (warp == kScoreConsumers) {
-    // ---- producer: stage s of unit k is its (k % stages)-th ----
+    // ---- producer: stage s of unit k is its (k % stages)-th.  The next unit's
+    // table entries are loaded before this one's stage is waited for and filled. ----
     const uint64_t pol = policy_evict_first();
+    struct Next {
+      int b, i0, g0, n;
+      int32_t ids[kScoreMaxTile / 32];
+    };
+    auto fetch = [&](int64_t u) {
+      Next x;
+      x.n = -1;
+      x.b = x.i0 = x.g0 = 0;
+      if (u < total) {
+        const int64_t t = u / chunks;
+        x.g0 = static_cast<int>(u - t * chunks) * lay.heads;
+        x.b = unit_sequence(cum, p.batch, static_cast<int>(t));
+        x.i0 = (static_cast<int>(t) - cum[x.b]) * lay.tile;
+        x.n = min(lay.tile, scored[x.b] - x.i0);
+      }
+      const int32_t* row = p.block_tables + static_cast<int64_t>(x.b) * p.max_blocks_per_seq + x.i0;
+#pragma unroll
+      for (int k = 0; k < kScoreMaxTile / 32; ++k) x.ids[k] = 32 * k + lane < x.n ? row[32 * k + lane] : -1;
+      return x;
+    };
     uint32_t k = 0;
     bool ok = true;
+    Next cur = fetch(blockIdx.x);
     for (int64_t u = blockIdx.x; ok; u += gridDim.x, ++k) {
       const int s = k % kScoreStages;
-      ScoreUnit d;
-      d.n = -1;
-      d.b = d.i0 = d.g0 = 0;
-      int32_t ids[kScoreMaxTile / 32];
-      int n_live = 0;
-      if (u < total) {
-        const int t = static_cast<int>(u / chunks);
-        d.g0 = static_cast<int>(u % chunks) * lay.heads;
-        d.b = unit_sequence(cum, p.batch, t);
-        d.i0 = (t - cum[d.b]) * lay.tile;
-        d.n = min(lay.tile, scored_blocks(p, d.b, false) - d.i0);
-        const int32_t* row = p.block_tables + static_cast<int64_t>(d.b) * p.max_blocks_per_seq + d.i0;
-#pragma unroll
-        for (int x = 0; x < kScoreMaxTile / 32; ++x) {
-          const bool in = 32 * x + lane < d.n;
-          ids[x] = in ? row[32 * x + lane] : -1;
-          const bool live = ids[x] >= 0 && ids[x] < p.num_blocks;
-          if (in && !live) record_error(p.err, PKV_ERR_OOB);
-          if (!live) ids[x] = -1;
-          d.live[x] = __ballot_sync(0xffffffffu, live);
-          n_live += __popc(d.live[x]);
-        }
-      }
+      const Next nxt = fetch(u + gridDim.x);
       ok = k < kScoreStages || mbar_wait(&empty[s], (k / kScoreStages - 1) & 1, p.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      ScoreUnit d;
+      d.b = cur.b, d.i0 = cur.i0, d.g0 = cur.g0, d.n = cur.n;
+      int n_live = 0;
+#pragma unroll
+      for (int x = 0; x < kScoreMaxTile / 32; ++x) {
+        const bool live = cur.ids[x] >= 0 && cur.ids[x] < p.num_blocks;
+        if (32 * x + lane < cur.n && !live) record_error(p.err, PKV_ERR_OOB);
+        if (!live) cur.ids[x] = -1;
+        d.live[x] = __ballot_sync(0xffffffffu, live);
+        n_live += __popc(d.live[x]);
+      }
       if (lane == 0) units[s] = d;
       if (d.n < 0) {
         if (lane == 0) mbar_arrive(&full[s]);
@@ -559,10 +574,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
       __syncwarp();
 #pragma unroll
       for (int x = 0; x < kScoreMaxTile / 32; ++x)
-        if (ids[x] >= 0)
+        if (cur.ids[x] >= 0)
           bulk_g2s(dst + (32 * x + lane) * lay.row,
-                   p.bounds + (static_cast<int64_t>(ids[x]) * p.n_kv_heads + d.g0) * 4 * D, heads * 4 * D, &full[s], pol);
+                   p.bounds + (static_cast<int64_t>(cur.ids[x]) * p.n_kv_heads + d.g0) * 4 * D, heads * 4 * D, &full[s],
+                   pol);
       __syncwarp();
+      cur = nxt;
     }
     if (!ok) {
       // a wait ran out: let the copies in flight land (bounded) before the block's memory goes
