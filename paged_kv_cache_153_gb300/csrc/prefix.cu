@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int row = (b - gr.start) * G + h;
   const int64_t R = ranges;
   int64_t lo = 0, hi = 0, r0 = 0, n_pre = 0, base = 0;     // the unit's cost span; its ranges r0 .. r0 + n_pre - 1
-  if (row < gr.rows && shares_prefix(gr.blocks, ctx, cap)) {
+  // (row < 0: group starts that are not as documented, none at or before b)
+  if (row >= 0 && row < gr.rows && shares_prefix(gr.blocks, ctx, cap)) {
     const int kt = prefix_tiles(gr.blocks), unit = row / kPrefixUnitRows;
     lo = gr.cost + (static_cast<int64_t>(g) * prefix_units(gr.rows) + unit) * kt;
     hi = lo + kt;

@@ -261,6 +261,15 @@ def test_device_errors(pkv):
         assert broken(lambda c: c.starts.copy_(torch.tensor(starts))) == 4, starts
 
 
+def test_group_starts_far_behind_the_first_sequence(pkv):
+    # no group starts at or before most of the sequences: reported, and what the
+    # others' states would be is not read
+    case = Case([(512, [30] * 130)], seed=24)
+    case.starts.copy_(torch.tensor([100, 130]))
+    case.run(pkv)
+    assert int(case.err.item()) == 4
+
+
 def test_contexts_past_the_declared_bound(pkv):
     # as in the dense decode: clamped to the bound and reported
     case = Case([(512, [30, 9]), (64, [400])], seed=21)
