@@ -99,6 +99,9 @@ int env_int(const char* name, int fallback) {
   return std::atoi(v);
 }
 
+// blocks of n >= 0 tokens (n + 15 may pass 2^31)
+int token_blocks(int n) { return n / kBlockSize + (n % kBlockSize != 0); }
+
 constexpr int kMaxCtasPerSm = 4;   // partial slots are sized for this many blocks per SM
 
 int sm_count() {
@@ -132,7 +135,7 @@ bool ws_layout(int batch, int n_kv_heads, int group, int head_dim, int max_block
   // ranges than partitions
   int64_t ranges = static_cast<int64_t>(num_sms) * kMaxCtasPerSm;
   if (partition_tokens > 0) {
-    const int64_t nblk = std::min<int64_t>(max_blocks_per_seq, (max_context_len + kBlockSize - 1) / kBlockSize);
+    const int64_t nblk = std::min<int64_t>(max_blocks_per_seq, token_blocks(max_context_len));
     const int64_t w_max = static_cast<int64_t>(batch) * n_kv_heads * nblk;
     const int64_t pb = partition_tokens / kBlockSize;
     ranges = std::min(ranges, std::max<int64_t>((w_max + pb - 1) / pb, 1));
@@ -241,7 +244,7 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   p.n_q_heads = n_q_heads;
   p.n_kv_heads = n_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
-  p.max_nblk = (max_context_len + kBlockSize - 1) / kBlockSize;
+  p.max_nblk = token_blocks(max_context_len);
   p.selected = selected;
   p.budget = budget;
   if (rest != nullptr) {
@@ -607,7 +610,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   p.n_q_heads = num_q_heads;
   p.n_kv_heads = num_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
-  p.max_nblk = (max_context_len + kBlockSize - 1) / kBlockSize;
+  p.max_nblk = token_blocks(max_context_len);
   p.qk_scale_log2 = scale * kLog2e;
   // as many ranges as SMs, but no more than there can be key tiles
   const int64_t units = static_cast<int64_t>(num_kv_heads) *

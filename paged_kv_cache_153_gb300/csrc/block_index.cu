@@ -168,7 +168,7 @@ __device__ __forceinline__ Touched touched_blocks(const BoundsParams& p, int b, 
   Touched t;
   t.ctx = ctx;
   t.first = (ctx - fresh) / kBlockSize;
-  t.last = fresh == 0 ? t.first : (ctx + kBlockSize - 1) / kBlockSize;
+  t.last = fresh == 0 ? t.first : (ctx - 1) / kBlockSize + 1;
   if (t.last - t.first > p.max_touched) {   // more new tokens than max_new_len
     bad = true;
     t.last = t.first + p.max_touched;
@@ -878,14 +878,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 constexpr int kMaxGridYZ = 65535;
 
 // Thread blocks of the flat form (0: by sequence), for `items` warps of work at
-// most: 24 warps per SM, with 4 to 8 KiB each in flight.
+// most: 24 warps per SM, with 4 to 8 KiB each in flight.  (Its unit counts are
+// 32-bit: by sequence beyond.)
 bool flat_grid(int64_t items, int warps_per_block, int batch, int* blocks) {
   int dev = 0, sms = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice") ||
       cuda_failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute"))
     return false;
   const int resident = sms * 24 / warps_per_block;
-  *blocks = (items > static_cast<int64_t>(kFlatWaves) * resident * warps_per_block && batch <= kFlatMaxBatch)
+  *blocks = (items > static_cast<int64_t>(kFlatWaves) * resident * warps_per_block && items <= INT32_MAX &&
+             batch <= kFlatMaxBatch)
                 ? resident
                 : 0;
   return true;

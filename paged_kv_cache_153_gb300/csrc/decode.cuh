@@ -143,6 +143,11 @@ struct ProdSeg {
   int skip;                      // kRest: blocks of the shared prefix, ahead of logical block 0
 };
 
+// blocks of ctx >= 0 tokens (unsigned: the sum may pass 2^31)
+__device__ __forceinline__ int ctx_blocks(int ctx) {
+  return static_cast<int>((static_cast<uint32_t>(ctx) + kBlockSize - 1) / kBlockSize);
+}
+
 // number of blocks of sequence b after clamping to cap: the table and the
 // bound (a list's length bounds the work instead: the table alone)
 __device__ __forceinline__ int seq_blocks(int cap, int ctx, int32_t* err) {
@@ -150,7 +155,7 @@ __device__ __forceinline__ int seq_blocks(int cap, int ctx, int32_t* err) {
     record_error(err, PKV_ERR_OOB);
     return 0;
   }
-  int nb = (ctx + kBlockSize - 1) / kBlockSize;
+  int nb = ctx_blocks(ctx);
   if (nb > cap) {
     record_error(err, PKV_ERR_OOB);
     nb = cap;
@@ -1657,7 +1662,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     long long v0 = 0, v1 = 0, v2 = 0, v3 = 0, v4 = 0;
     for (int i = lane; i < p.batch; i += 32) {
       const int ctx = p.context_lens[i];
-      const int n = ctx < 0 ? 0 : min((ctx + kBlockSize - 1) / kBlockSize, min(p.max_blocks_per_seq, p.max_nblk));
+      const int n = ctx < 0 ? 0 : min(ctx_blocks(ctx), min(p.max_blocks_per_seq, p.max_nblk));
       v2 += n;
       v3 += n > 0;
       if (i < b) {

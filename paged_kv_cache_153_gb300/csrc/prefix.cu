@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       const int shared = __shfl_sync(0xffffffffu, blocks, max(j, 0));
       const int end = __shfl_sync(0xffffffffu, stop, max(j, 0));
       const bool shares = i < p.batch && j >= 0 && i < end && shares_prefix(shared, len, cap);
-      int n = i < p.batch && len > 0 ? min((len + kBlockSize - 1) / kBlockSize, cap) : 0;
+      int n = i < p.batch && len > 0 ? min(ctx_blocks(len), cap) : 0;
       if (shares) n -= shared;
       covered |= __reduce_or_sync(0xffffffffu, shares ? 1u << j : 0u);
       all += n;

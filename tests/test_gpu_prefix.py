@@ -270,6 +270,32 @@ def test_group_starts_far_behind_the_first_sequence(pkv):
     assert int(case.err.item()) == 4
 
 
+def test_lengths_at_the_end_of_int32(pkv):
+    # a bound that promises nothing changes no result
+    case = Case([(512, [30, 9]), (64, [100])], seed=25)
+    want = case.run(pkv)
+    case.max_ctx = case.max_pre = 2 ** 31 - 1
+    assert torch.equal(case.run(pkv), want) and int(case.err.item()) == 0
+    dense = torch.empty_like(case.q)
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(3, 8, 2, 128, case.width, case.max_ctx), dtype=torch.uint8,
+                     device="cuda")
+    pkv.pkv_paged_decode_attention(case.q, case.kc, case.vc, case.tab, case.lens, dense, scale=case.scale,
+                                   max_context_len=case.max_ctx, workspace=ws, err_flag=case.err)
+    torch.cuda.synchronize()
+    case.check(dense)
+    assert int(case.err.item()) == 0
+    # a context as long: clamped and reported (both forms of the merge), the others as they were
+    for groups in ([(512, [30, 9]), (64, [100])], [(512, [30] * 300), (64, [100])]):
+        case = Case(groups, seed=26)
+        want = case.run(pkv)
+        for n in (2 ** 31 - 1, 2 ** 31 - 16):
+            case.lens[0] = n
+            out = case.run(pkv)
+            assert int(case.err.item()) == 4
+            case.check(out, [1, len(case.lens_h) - 1])
+            case.err.zero_()
+
+
 def test_contexts_past_the_declared_bound(pkv):
     # as in the dense decode: clamped to the bound and reported
     case = Case([(512, [30, 9]), (64, [400])], seed=21)

@@ -492,6 +492,28 @@ def test_attention_device_errors(pkv):
     assert int(case.err.item()) == 4
 
 
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 16])
+def test_lengths_at_the_end_of_int32(pkv, n):
+    # a context as long is clamped to its table and reported, in every step
+    case = Case([1000, 700], seed=14)
+    bounds = torch.zeros((case.nb, 2, 2, 128), dtype=torch.bfloat16, device="cuda")
+    case.lens[1] = n
+    run_bounds(pkv, case, bounds)
+    assert int(case.err.item()) == 4
+    scores = torch.zeros((2, 2, case.width), device="cuda")
+    case.err.zero_()
+    pkv.pkv_block_scores(case.q, bounds, case.tab, case.lens, scores, scale=1.0, max_context_len=2 ** 31 - 1,
+                         err_flag=case.err)
+    torch.cuda.synchronize()
+    assert int(case.err.item()) == 4 and torch.isfinite(scores[0]).all()
+    got, err = run_select(pkv, scores, [1000, n], 4, 1, 1)
+    assert err == 4 and got[1, 0, 0] == 0 and got[1, 0, -1] == case.width - 1
+    sel = random_lists(case, 10, seed=3)
+    case.err.zero_()
+    case.attention(pkv, sel)
+    assert int(case.err.item()) == 4
+
+
 def test_binding_refuses_shapes_that_do_not_fit(pkv):
     case = Case([100], seed=14)
     sel = torch.zeros((1, 3, 4), dtype=torch.int32, device="cuda")
