@@ -499,6 +499,19 @@ def _contiguous(*tensors) -> None:
             raise ValueError("q, out, caches, bounds, scores and slots must be contiguous")
 
 
+def _caches(k_cache, v_cache, itemsize: int) -> None:
+    """Both caches alike, of the element size that the call writes and reads."""
+    if k_cache.element_size() != itemsize or (v_cache is not k_cache and (
+            v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype)):
+        raise ValueError("caches must have one shape and the call's element type")
+    _contiguous(k_cache, v_cache)
+
+
+def _per_sequence(b: int, block_tables, context_lens) -> None:
+    if block_tables.shape[0] != b or context_lens.numel() != b:
+        raise ValueError("block_tables and context_lens must have a row per sequence")
+
+
 _ROPE_LAYOUTS = {"half": PKV_ROPE_HALF, "interleaved": PKV_ROPE_INTERLEAVED, PKV_ROPE_HALF: PKV_ROPE_HALF,
                  PKV_ROPE_INTERLEAVED: PKV_ROPE_INTERLEAVED}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
@@ -535,6 +548,8 @@ def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v
     if layout not in _ROPE_LAYOUTS:
         raise ValueError(f"unknown layout {layout!r}")
     _int32(positions)
+    if turns.element_size() != 8 or turns.is_floating_point():
+        raise TypeError("turns must be the int64 tensor of pkv_rope_plan")
     n = positions.numel()
     q_args, kv_args, hq, hkv, nb, bs = (None, 0, None, 0), (None, 0, None, 0), 0, 0, 0, 16
     if q is not None:
@@ -550,7 +565,8 @@ def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v
             raise ValueError("k_new and v_new must be [T, num_kv_heads, head_dim] of the cache")
         if slot_mapping.numel() != n or slot_mapping.element_size() != 8:
             raise ValueError("slot_mapping must be int64, one slot per position")
-        _contiguous(slot_mapping, k_cache, v_cache)
+        _contiguous(slot_mapping)
+        _caches(k_cache, v_cache, 1 if scales else 2)
         d = dk
         kv_args = (k_new.data_ptr(), _token_stride(k_new, "k_new", hkv, d), v_new.data_ptr(),
                    _token_stride(v_new, "v_new", hkv, d))
@@ -590,7 +606,9 @@ def _block_bounds(fn, k_cache, block_tables, context_lens, bounds, new_lens, max
     if tuple(bounds.shape) != (nb, hkv, 2, d):
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
     _int32(block_tables, context_lens, new_lens)
-    _contiguous(k_cache, bounds)
+    _caches(k_cache, k_cache, 2 if fn == "pkv_kv_block_bounds" else 1)
+    _contiguous(bounds)
+    _per_sequence(context_lens.numel() if new_lens is None else new_lens.numel(), block_tables, context_lens)
     _check(fn, getattr(_call, fn)(
         _ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(new_lens), max_new_len, context_lens.numel(), hkv, d,
         bs, block_tables.shape[1], nb, _ptr(bounds), _dtype_code(bounds, dtype), _ptr(err_flag), _stream(stream)))
@@ -633,6 +651,9 @@ def pkv_block_scores(q, bounds, block_tables, context_lens, scores, *, scale: fl
         raise TypeError("bounds and q differ in dtype")
     _int32(block_tables, context_lens)
     _contiguous(q, bounds, scores)
+    _per_sequence(b, block_tables, context_lens)
+    if scores.element_size() != 4:
+        raise TypeError("scores must be fp32")
     _check("pkv_block_scores", _call.pkv_block_scores(
         _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), _ptr(k_scale), b, hq, hkv, d, 16,
         block_tables.shape[1], nb, max_context_len, scale, _ptr(scores), _dtype_code(q, dtype), _ptr(err_flag),
@@ -648,6 +669,8 @@ def pkv_select_blocks(scores, context_lens, selected, *, num_first: int = 1, num
         raise ValueError("selected must be [batch, num_kv_heads, budget]")
     _int32(context_lens, selected)
     _contiguous(scores)
+    if scores.element_size() != 4 or context_lens.numel() != b:
+        raise ValueError("scores must be fp32, with a context length per sequence")
     _check("pkv_select_blocks", _call.pkv_select_blocks(
         _ptr(scores), _ptr(context_lens), b, hkv, 16, blocks, num_first, num_last, selected.shape[2], _ptr(selected),
         _ptr(err_flag), _stream(stream)))
@@ -660,7 +683,11 @@ def _sparse(fn, q, k_cache, v_cache, scales, block_tables, context_lens, selecte
     if tuple(selected.shape[:2]) != (b, hkv):
         raise ValueError("selected must be [batch, num_kv_heads, budget]")
     _int32(block_tables, context_lens, selected)
-    _contiguous(q, k_cache, v_cache, out)
+    _contiguous(q, out)
+    _caches(k_cache, v_cache, 1 if scales else 2)
+    _per_sequence(b, block_tables, context_lens)
+    if out.shape != q.shape:
+        raise ValueError("q and out differ in shape")
     _check(fn, getattr(_call, fn)(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_tables), _ptr(context_lens), _ptr(selected),
         selected.shape[2], b, hq, hkv, d, bs, block_tables.shape[1], nb, scale, _ptr(out), _dtype_code(q, dtype),
@@ -708,7 +735,11 @@ def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context
     if group_starts.numel() != prefix_lens.numel() + 1:
         raise ValueError("group_starts must have one entry more than prefix_lens")
     _int32(block_tables, context_lens, group_starts, prefix_lens)
-    _contiguous(q, k_cache, v_cache, out)
+    _contiguous(q, out)
+    _caches(k_cache, v_cache, 2)
+    _per_sequence(b, block_tables, context_lens)
+    if out.shape != q.shape:
+        raise ValueError("q and out differ in shape")
     _check("pkv_paged_decode_attention_prefix", _call.pkv_paged_decode_attention_prefix(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(group_starts),
         _ptr(prefix_lens), prefix_lens.numel(), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len,
