@@ -3,10 +3,11 @@
 Argument marshalling only: every function here extracts device pointers,
 sizes and the current CUDA stream from torch tensors and calls the C entry
 point of the same name (declared in include/pkv.h): the per-step calls through
-the module _call (csrc/pycall.cpp), the others through ctypes.  All arithmetic
-runs in the library's CUDA kernels; there is no CPU fallback.  Importing this module
-fails loudly when the library has not been built (``__graft_entry__.build()``
-or ``python -m paged_kv_cache_153_gb300._build``).
+the module _call (csrc/pycall.cpp, and pytensor.cpp, which takes the tensors
+themselves), the others through ctypes.  All arithmetic runs in the library's
+CUDA kernels; there is no CPU fallback.  Importing this module fails loudly when
+the library has not been built (``__graft_entry__.build()`` or
+``python -m paged_kv_cache_153_gb300._build``).
 
 Tensors: 16-bit data is passed as torch.float16 / torch.bfloat16 (or any
 2-byte dtype, tagged with ``dtype``), E4M3 caches as torch.uint8, tables and
@@ -47,6 +48,8 @@ if not os.path.exists(library_path):
     raise ImportError(f"{library_path} is missing: build it with __graft_entry__.build() "
                       "(the CUDA path has no fallback)")
 lib = C.CDLL(library_path)
+import torch  # noqa: E402, F401  (first: _call takes its tensors)
+
 from . import _call  # noqa: E402  (built with the library; finds it next to itself)
 
 # The prefill kernel lives in a library of its own (pkv_prefill.h), loaded on
@@ -478,42 +481,6 @@ def pkv_paged_decode_step_int8(q, k_new, v_new, k_cache, v_cache, slab_params, b
         workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
 
 
-_int32_dtype = None
-
-
-def _int32(*tensors) -> None:
-    """Index tensors must be contiguous int32: another type would be read as
-    garbage indices."""
-    global _int32_dtype
-    if _int32_dtype is None:
-        import torch
-        _int32_dtype = torch.int32
-    for t in tensors:
-        if t is not None and (t.dtype is not _int32_dtype or not t.is_contiguous()):
-            raise TypeError("tables, lengths, positions and lists must be contiguous int32 tensors")
-
-
-def _contiguous(*tensors) -> None:
-    for t in tensors:
-        if not t.is_contiguous():
-            raise ValueError("q, out, caches, bounds, scores and slots must be contiguous")
-
-
-def _caches(k_cache, v_cache, itemsize: int) -> None:
-    """Both caches alike, of the element size that the call writes and reads."""
-    if k_cache.element_size() != itemsize or (v_cache is not k_cache and (
-            v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype)):
-        raise ValueError("caches must have one shape and the call's element type")
-    _contiguous(k_cache, v_cache)
-
-
-def _per_sequence(b: int, block_tables, context_lens) -> None:
-    if block_tables.shape[0] != b or context_lens.numel() != b:
-        raise ValueError("block_tables and context_lens must have a row per sequence")
-
-
-_ROPE_LAYOUTS = {"half": PKV_ROPE_HALF, "interleaved": PKV_ROPE_INTERLEAVED, PKV_ROPE_HALF: PKV_ROPE_HALF,
-                 PKV_ROPE_INTERLEAVED: PKV_ROPE_INTERLEAVED}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
 
 
@@ -535,83 +502,31 @@ def pkv_rope_plan(rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
     return turns, amp.value
 
 
-def _token_stride(t, name: str, heads: int, d: int) -> int:
-    """Elements between the tokens of t [T, heads, d], whose heads are contiguous."""
-    stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != d):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return stride[0] if t.shape[0] > 1 else heads * d
-
-
-def _rope(fn, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, scales, layout, amplitude,
-          dtype, err_flag, stream):
-    if layout not in _ROPE_LAYOUTS:
-        raise ValueError(f"unknown layout {layout!r}")
-    _int32(positions)
-    if turns.element_size() != 8 or turns.is_floating_point():
-        raise TypeError("turns must be the int64 tensor of pkv_rope_plan")
-    n = positions.numel()
-    q_args, kv_args, hq, hkv, nb, bs = (None, 0, None, 0), (None, 0, None, 0), 0, 0, 0, 16
-    if q is not None:
-        shape = q.shape
-        t, hq, d = shape
-        if t != n or q_out.shape != shape:
-            raise ValueError("q, q_out and positions differ in shape")
-        q_args = q.data_ptr(), _token_stride(q, "q", hq, d), q_out.data_ptr(), _token_stride(q_out, "q_out", hq, d)
-    if k_new is not None:
-        nb, hkv, bs, dk = k_cache.shape
-        shape = k_new.shape
-        if shape != (n, hkv, dk) or v_new.shape != shape or (q is not None and dk != d):
-            raise ValueError("k_new and v_new must be [T, num_kv_heads, head_dim] of the cache")
-        if slot_mapping.numel() != n or slot_mapping.element_size() != 8:
-            raise ValueError("slot_mapping must be int64, one slot per position")
-        _contiguous(slot_mapping)
-        _caches(k_cache, v_cache, 1 if scales else 2)
-        d = dk
-        kv_args = (k_new.data_ptr(), _token_stride(k_new, "k_new", hkv, d), v_new.data_ptr(),
-                   _token_stride(v_new, "v_new", hkv, d))
-    _check(fn, getattr(_call, fn)(
-        q_args[0], q_args[1], *kv_args, positions.data_ptr(), _ptr(slot_mapping), n, turns.data_ptr(),
-        2 * turns.numel(), _ROPE_LAYOUTS[layout], amplitude, q_args[2], q_args[3], _ptr(k_cache),
-        _ptr(v_cache), nb, *scales, hq, hkv, d, bs, _dtype_code(k_new if q is None else q, dtype), _ptr(err_flag),
-        _stream(stream)))
-
-
 def pkv_rope_append(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, *, layout="half",
                     amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
     """Turn q [T, Hq, D] into q_out, and append the turned k_new and v_new
     [T, Hkv, D] to their slots.  q and q_out, or k_new and v_new (with the
     caches and slots), may be None.  The token stride is free; q_out may be q.
     turns, amplitude: from pkv_rope_plan (turns on the device)."""
-    _rope("pkv_rope_append", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, (), layout,
-          amplitude, dtype, err_flag, stream)
+    _check("pkv_rope_append", _call.rope_append(
+        0, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, None, None, layout, amplitude,
+        dtype, err_flag, stream))
 
 
 def pkv_rope_append_fp8(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, *,
                         layout="half", amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
     """pkv_rope_append into an E4M3 cache (uint8 codes, fp32 per-head scales)."""
-    _rope("pkv_rope_append_fp8", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache,
-          (_ptr(k_scale), _ptr(v_scale)), layout, amplitude, dtype, err_flag, stream)
+    _check("pkv_rope_append_fp8", _call.rope_append(
+        1, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, layout,
+        amplitude, dtype, err_flag, stream))
 
 
 def pkv_rope_append_e5m2(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale,
                          *, layout="half", amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
     """pkv_rope_append into an E5M2 cache (uint8 codes, fp32 per-head scales)."""
-    _rope("pkv_rope_append_e5m2", q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache,
-          (_ptr(k_scale), _ptr(v_scale)), layout, amplitude, dtype, err_flag, stream)
-
-
-def _block_bounds(fn, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream):
-    nb, hkv, bs, d = k_cache.shape
-    if tuple(bounds.shape) != (nb, hkv, 2, d):
-        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache")
-    _int32(block_tables, context_lens, new_lens)
-    _caches(k_cache, k_cache, 2 if fn == "pkv_kv_block_bounds" else 1)
-    _contiguous(bounds)
-    _per_sequence(context_lens.numel() if new_lens is None else new_lens.numel(), block_tables, context_lens)
-    _check(fn, getattr(_call, fn)(
-        _ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(new_lens), max_new_len, context_lens.numel(), hkv, d,
-        bs, block_tables.shape[1], nb, _ptr(bounds), _dtype_code(bounds, dtype), _ptr(err_flag), _stream(stream)))
+    _check("pkv_rope_append_e5m2", _call.rope_append(
+        2, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, layout,
+        amplitude, dtype, err_flag, stream))
 
 
 def pkv_kv_block_bounds(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None, dtype=None,
@@ -619,100 +534,63 @@ def pkv_kv_block_bounds(k_cache, block_tables, context_lens, bounds, *, max_new_
     """Elementwise minimum and maximum of the cached keys per (block, KV head),
     into bounds [NB, Hkv, 2, D], for the blocks of each sequence's last
     new_lens tokens (None: its whole context)."""
-    _block_bounds("pkv_kv_block_bounds", k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype,
-                  err_flag, stream)
+    _check("pkv_kv_block_bounds", _call.block_bounds(
+        0, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream))
 
 
 def pkv_kv_block_bounds_fp8(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None,
                             dtype=None, err_flag=None, stream=None) -> None:
     """pkv_kv_block_bounds over an E4M3 cache: 16-bit bounds of the codes'
     values, before the per-head scale."""
-    _block_bounds("pkv_kv_block_bounds_fp8", k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype,
-                  err_flag, stream)
+    _check("pkv_kv_block_bounds_fp8", _call.block_bounds(
+        1, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream))
 
 
 def pkv_kv_block_bounds_e5m2(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None,
                              dtype=None, err_flag=None, stream=None) -> None:
     """pkv_kv_block_bounds over an E5M2 cache."""
-    _block_bounds("pkv_kv_block_bounds_e5m2", k_cache, block_tables, context_lens, bounds, new_lens, max_new_len,
-                  dtype, err_flag, stream)
+    _check("pkv_kv_block_bounds_e5m2", _call.block_bounds(
+        2, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream))
 
 
 def pkv_block_scores(q, bounds, block_tables, context_lens, scores, *, scale: float, max_context_len: int,
                      k_scale=None, dtype=None, err_flag=None, stream=None) -> None:
     """Upper bounds of every block's scaled logits, scores fp32 [B, Hkv,
     max_blocks], from the block bounds [NB, Hkv, 2, D]."""
-    b, hq, d = q.shape
-    nb, hkv = bounds.shape[:2]
-    if tuple(scores.shape) != (b, hkv, block_tables.shape[1]) or tuple(bounds.shape[2:]) != (2, d):
-        raise ValueError("scores must be [batch, num_kv_heads, max_blocks], bounds [num_blocks, num_kv_heads, 2, "
-                         "head_dim]")
-    if bounds.dtype != q.dtype:
-        raise TypeError("bounds and q differ in dtype")
-    _int32(block_tables, context_lens)
-    _contiguous(q, bounds, scores)
-    _per_sequence(b, block_tables, context_lens)
-    if scores.element_size() != 4:
-        raise TypeError("scores must be fp32")
-    _check("pkv_block_scores", _call.pkv_block_scores(
-        _ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens), _ptr(k_scale), b, hq, hkv, d, 16,
-        block_tables.shape[1], nb, max_context_len, scale, _ptr(scores), _dtype_code(q, dtype), _ptr(err_flag),
-        _stream(stream)))
+    _check("pkv_block_scores", _call.block_scores(
+        q, bounds, block_tables, context_lens, scores, scale, max_context_len, k_scale, dtype, err_flag, stream))
 
 
 def pkv_select_blocks(scores, context_lens, selected, *, num_first: int = 1, num_last: int = 1, err_flag=None,
                       stream=None) -> None:
     """selected int32 [B, Hkv, budget]: the first num_first, the last num_last
     and the highest-scoring other blocks, ascending, -1 behind the list."""
-    b, hkv, blocks = scores.shape
-    if tuple(selected.shape[:2]) != (b, hkv):
-        raise ValueError("selected must be [batch, num_kv_heads, budget]")
-    _int32(context_lens, selected)
-    _contiguous(scores)
-    if scores.element_size() != 4 or context_lens.numel() != b:
-        raise ValueError("scores must be fp32, with a context length per sequence")
-    _check("pkv_select_blocks", _call.pkv_select_blocks(
-        _ptr(scores), _ptr(context_lens), b, hkv, 16, blocks, num_first, num_last, selected.shape[2], _ptr(selected),
-        _ptr(err_flag), _stream(stream)))
-
-
-def _sparse(fn, q, k_cache, v_cache, scales, block_tables, context_lens, selected, out, scale, workspace, dtype,
-            err_flag, stream):
-    b, hq, d = q.shape
-    nb, hkv, bs, _ = k_cache.shape
-    if tuple(selected.shape[:2]) != (b, hkv):
-        raise ValueError("selected must be [batch, num_kv_heads, budget]")
-    _int32(block_tables, context_lens, selected)
-    _contiguous(q, out)
-    _caches(k_cache, v_cache, 1 if scales else 2)
-    _per_sequence(b, block_tables, context_lens)
-    if out.shape != q.shape:
-        raise ValueError("q and out differ in shape")
-    _check(fn, getattr(_call, fn)(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_tables), _ptr(context_lens), _ptr(selected),
-        selected.shape[2], b, hq, hkv, d, bs, block_tables.shape[1], nb, scale, _ptr(out), _dtype_code(q, dtype),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+    _check("pkv_select_blocks", _call.select_blocks(
+        scores, context_lens, selected, num_first, num_last, err_flag, stream))
 
 
 def pkv_paged_decode_attention_sparse(q, k_cache, v_cache, block_tables, context_lens, selected, out, *,
                                       scale: float, workspace, dtype=None, err_flag=None, stream=None) -> None:
     """Decode attention over the blocks that selected [B, Hkv, budget] lists."""
-    _sparse("pkv_paged_decode_attention_sparse", q, k_cache, v_cache, (), block_tables, context_lens, selected, out,
-            scale, workspace, dtype, err_flag, stream)
+    _check("pkv_paged_decode_attention_sparse", _call.sparse_decode(
+        0, q, k_cache, v_cache, None, None, block_tables, context_lens, selected, out, scale, workspace,
+        dtype, err_flag, stream))
 
 
 def pkv_paged_decode_attention_sparse_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected,
                                           out, *, scale: float, workspace, q_dtype=None, err_flag=None,
                                           stream=None) -> None:
-    _sparse("pkv_paged_decode_attention_sparse_fp8", q, k_cache, v_cache, (_ptr(k_scale), _ptr(v_scale)), block_tables,
-            context_lens, selected, out, scale, workspace, q_dtype, err_flag, stream)
+    _check("pkv_paged_decode_attention_sparse_fp8", _call.sparse_decode(
+        1, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, out, scale, workspace,
+        q_dtype, err_flag, stream))
 
 
 def pkv_paged_decode_attention_sparse_e5m2(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                                            selected, out, *, scale: float, workspace, q_dtype=None, err_flag=None,
                                            stream=None) -> None:
-    _sparse("pkv_paged_decode_attention_sparse_e5m2", q, k_cache, v_cache, (_ptr(k_scale), _ptr(v_scale)),
-            block_tables, context_lens, selected, out, scale, workspace, q_dtype, err_flag, stream)
+    _check("pkv_paged_decode_attention_sparse_e5m2", _call.sparse_decode(
+        2, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, out, scale, workspace,
+        q_dtype, err_flag, stream))
 
 
 def pkv_prefix_workspace_bytes(batch: int, num_groups: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -730,21 +608,9 @@ def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context
     """Decode attention of sequences that share prefixes: group j, sequences
     group_starts[j] .. group_starts[j + 1] - 1, shares its first
     prefix_lens[j] tokens' whole blocks."""
-    b, hq, d = q.shape
-    nb, hkv, bs, _ = k_cache.shape
-    if group_starts.numel() != prefix_lens.numel() + 1:
-        raise ValueError("group_starts must have one entry more than prefix_lens")
-    _int32(block_tables, context_lens, group_starts, prefix_lens)
-    _contiguous(q, out)
-    _caches(k_cache, v_cache, 2)
-    _per_sequence(b, block_tables, context_lens)
-    if out.shape != q.shape:
-        raise ValueError("q and out differ in shape")
-    _check("pkv_paged_decode_attention_prefix", _call.pkv_paged_decode_attention_prefix(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(group_starts),
-        _ptr(prefix_lens), prefix_lens.numel(), b, hq, hkv, d, bs, block_tables.shape[1], nb, max_context_len,
-        max_prefix_len, scale, _ptr(out), _dtype_code(q, dtype), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+    _check("pkv_paged_decode_attention_prefix", _call.prefix_decode(
+        q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, out, scale, max_context_len,
+        max_prefix_len, workspace, dtype, err_flag, stream))
 
 
 def pkv_blocks_needed(num_tokens: int, block_size: int = 16) -> int:

@@ -7,11 +7,13 @@ prefill kernel (thread-block clusters sharing K/V loads by TMA multicast) sits
 in libpkv_prefill.so of its own, so that a process that only decodes never
 loads it; that library takes its error reporting from libpkv.so, found next to
 it through an $ORIGIN run path.  _call.so is a CPython module that converts the
-arguments of the per-step calls and calls libpkv.so.
+arguments of the per-step calls, torch tensors among them, and calls libpkv.so;
+it alone is compiled against torch's headers.
 """
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -32,7 +34,7 @@ CUDA_SOURCES = ["append.cu", "api.cu", "decode_f16.cu", "decode_bf16.cu", "decod
                 "block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu", "decode_rest.cu", "prefix.cu"]
 PREFILL_SOURCES = ["prefill.cu"]
 CXX_SOURCES = ["pool.cpp"]
-CALL_SOURCES = ["pycall.cpp"]
+CALL_SOURCES = ["pycall.cpp", "pytensor.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -44,6 +46,18 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libpkv.so")
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed: the binding takes its tensors")
+    return spec.submodule_search_locations[0]
+
+
+def _torch_version() -> str:
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f.read()
+
+
 def _source_digest() -> str:
     h = hashlib.sha256()
     for d in (CSRC, INCLUDE):
@@ -52,7 +66,7 @@ def _source_digest() -> str:
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode())
                     h.update(f.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS + [sysconfig.get_paths()["include"]]).encode())
+    h.update(" ".join(ARCH + NVCC_FLAGS + [sysconfig.get_paths()["include"], _torch_version()]).encode())
     return h.hexdigest()
 
 
@@ -79,8 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         jobs.append([nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
     for src in CXX_SOURCES + CALL_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
-        jobs.append([nvcc, *NVCC_FLAGS, "-I" + sysconfig.get_paths()["include"], "-x", "c++", "-c",
-                     os.path.join(CSRC, src), "-o", obj])
+        jobs.append([nvcc, *NVCC_FLAGS, "-I" + sysconfig.get_paths()["include"], "-isystem",
+                     os.path.join(_torch_dir(), "include"), "-x", "c++", "-c", os.path.join(CSRC, src), "-o", obj])
     with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
         for cmd, _ in zip(jobs, ex.map(_run, jobs)):
             if verbose:
@@ -96,8 +110,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, PREFILL_LIB_PATH)
     cobjs = [os.path.join(BUILD_DIR, s.rsplit(".", 1)[0] + ".o") for s in CALL_SOURCES]
     tmp = CALL_PATH + ".tmp"
-    _run([nvcc, "-shared", "-cudart", "none", "-o", tmp, *cobjs, "-L" + PKG_DIR, "-lpkv", "-Xlinker",
-          "-rpath,$ORIGIN"])
+    _run([nvcc, "-shared", "-cudart", "none", "-o", tmp, *cobjs, "-L" + PKG_DIR, "-lpkv",
+          "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+          "-Xlinker", "-rpath,$ORIGIN"])
     os.replace(tmp, CALL_PATH)
     with open(stamp, "w") as f:
         f.write(digest)

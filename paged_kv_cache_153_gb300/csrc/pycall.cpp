@@ -3,52 +3,14 @@
 // plain numbers and addresses (None = NULL).  The same calls through ctypes
 // spend about 85 ns per argument on conversions, 2 us of a call whose kernels
 // run for as long; here it is under 0.3 us.
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
+#include "pycall.h"
 
-#include <cstdint>
-#include <limits>
 #include <tuple>
-#include <type_traits>
 #include <utility>
-
-#include "../../include/pkv.h"
 
 namespace {
 
-// a Python argument as a C one; false with an exception set
-template <typename T>
-bool convert(PyObject* o, T& out) {
-  if constexpr (std::is_pointer<T>::value) {
-    out = nullptr;
-    if (o == Py_None) return true;
-    void* p = PyLong_AsVoidPtr(o);
-    if (p == nullptr && PyErr_Occurred()) return false;
-    out = static_cast<T>(p);
-    return true;
-  } else if constexpr (std::is_floating_point<T>::value) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) return false;
-    out = static_cast<T>(v);
-    return true;
-  } else {
-    using I = typename std::conditional_t<std::is_enum<T>::value, std::common_type<int>, std::common_type<T>>::type;
-    if constexpr (std::is_same<I, size_t>::value) {
-      const size_t v = PyLong_AsSize_t(o);
-      if (v == static_cast<size_t>(-1) && PyErr_Occurred()) return false;
-      out = v;
-    } else {
-      const long long v = PyLong_AsLongLong(o);
-      if (v == -1 && PyErr_Occurred()) return false;
-      if (v < std::numeric_limits<I>::min() || v > std::numeric_limits<I>::max()) {
-        PyErr_SetString(PyExc_OverflowError, "argument does not fit its C type");
-        return false;
-      }
-      out = static_cast<T>(static_cast<I>(v));
-    }
-    return true;
-  }
-}
+using pkv_py::convert;
 
 template <auto F>
 struct Call;
@@ -97,18 +59,6 @@ PyMethodDef methods[] = {
     PKV_CALL(pkv_decode_step_host),
     PKV_CALL(pkv_copy_blocks),
     PKV_CALL(pkv_step_graph_launch),
-    PKV_CALL(pkv_rope_append),
-    PKV_CALL(pkv_rope_append_fp8),
-    PKV_CALL(pkv_rope_append_e5m2),
-    PKV_CALL(pkv_kv_block_bounds),
-    PKV_CALL(pkv_kv_block_bounds_fp8),
-    PKV_CALL(pkv_kv_block_bounds_e5m2),
-    PKV_CALL(pkv_block_scores),
-    PKV_CALL(pkv_select_blocks),
-    PKV_CALL(pkv_paged_decode_attention_sparse),
-    PKV_CALL(pkv_paged_decode_attention_sparse_fp8),
-    PKV_CALL(pkv_paged_decode_attention_sparse_e5m2),
-    PKV_CALL(pkv_paged_decode_attention_prefix),
     {nullptr, nullptr, 0, nullptr},
 };
 
@@ -116,4 +66,11 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__call(void) { return PyModule_Create(&module_def); }
+PyMODINIT_FUNC PyInit__call(void) {
+  PyObject* m = PyModule_Create(&module_def);
+  if (m != nullptr && PyModule_AddFunctions(m, pkv_py::tensor_methods) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
