@@ -627,7 +627,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   rest.num_groups = num_groups;
   rest.ml = reinterpret_cast<float*>(ws + w.rest_ml);
   rest.o = reinterpret_cast<float*>(ws + w.rest_o);
-  rest.smem = kSmemPerSm - 2 * kSmemReservedPerCta - prefix_smem_bytes(head_dim, p.q_tiles, num_groups);
+  rest.smem = kSmemPerSm - 2 * kSmemReservedPerCta - prefix_smem_bytes(head_dim, num_groups);
   st = decode_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, batch, num_q_heads,
                      num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len, scale, out,
                      dtype, 0, ws, w.decode.total, err_flag, stream, nullptr, nullptr, nullptr, 1, 0, nullptr,

@@ -437,7 +437,7 @@ __device__ __noinline__ void clear_rows(uint32_t vslab, int r0, int lane) {
 // the decode kernel
 // ---------------------------------------------------------------------------
 template <typename QT, typename KV, int D, int G, int NW, bool MMA, Source SRC>
-__global__ void __launch_bounds__((NW + 1) * 32, SRC == kRest ? 4 : MMA ? 3 : 1) paged_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRest && MMA ? 3 : 1) paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<D, G, NW, KV, MMA>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =

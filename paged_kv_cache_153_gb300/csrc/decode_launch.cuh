@@ -199,7 +199,7 @@ DecodeLauncher decode_launcher_rest(int q_dtype, int head_dim, int group);
 
 constexpr int kCoreWarps = 8;   // consumer warps of the CUDA-core variant
 constexpr int kMmaWarps = 4;    // consumer warps of the tensor-core variant
-constexpr int kRestWarps = 3;   // and of kRest, which shares its SM with the prefix kernel (4 warps at 128 registers)
+constexpr int kRestWarps = 4;   // and of kRest, which shares its SM with the prefix kernel (5 warps at 128 registers)
 
 // G = 1 uses the CUDA-core consumer; G >= 2 over a 16-bit cache, or over a
 // one-byte (E4M3, E5M2 or INT8) cache with 128-byte rows, uses the tensor-core

@@ -28,8 +28,9 @@
 //                        row tile; their states are joined in registers.
 // Q tiles come by one TMA box per 64 columns (G heads x 128 / G sequences: the
 // rows of a unit in order); K / V tiles are 8 cache blocks, gathered by boxes of
-// [16 rows x 128 B] into 128-byte-swizzled K-major tiles (one stage of K, two of
-// V).  P overwrites its own S in TMEM (32 columns of scores become 16 of P
+// [16 rows x 128 B] into 128-byte-swizzled K-major tiles (one stage of K; of V
+// two beside one row tile, one beside two, where a tile serves both chains and
+// its load has half of a period to arrive).  P overwrites its own S in TMEM (32 columns of scores become 16 of P
 // pairs, and for bf16 16 more of the remainder); the product reads it from
 // there.  bf16 P is multiplied as two bf16 parts (p truncated, and the rounded
 // remainder: exact to 2^-16), because one bf16 rounding of p (2^-9) would be as
@@ -43,11 +44,14 @@
 // TMA producer; warp 9: TMEM owner and Q K^T issuer, warp 10: P V issuer.
 // Waits are bounded as in the other kernels.
 //
-// Beside it.  The kernel leaves room on its SM (registers: 128 a thread; shared
-// memory: about 64 KiB, or 96 where no unit has more than 128 rows) for one
-// thread block of the decode over the sequences' own blocks, which is bound by
-// memory where this one is bound by the tensor cores; that kernel launches as
-// soon as this one has started.
+// Beside it.  The kernel leaves room on its SM (registers: 128 a thread, three
+// warps to a scheduler and two to one, so that a scheduler has room for one or
+// two more; about 94 KiB of shared memory) for one thread block of five warps of
+// the decode over the sequences' own blocks, which is bound by memory where this
+// one is bound by the tensor cores; that kernel launches as soon as this one has
+// started.  64 sequences of 16 to 2048 tokens behind 32768: 63.8 us (66.1 with two
+// stages of V, which leave the other block three consumer warps of two stages
+// each instead of four; 103 where the two do not fit an SM together).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -64,7 +68,8 @@ constexpr int kXThreads = 352;
 constexpr int kXRows = 128;                       // query rows of a chain's tile
 constexpr int kXKeys = 128;                       // keys of a K / V tile
 constexpr int kXTileBlocks = kXKeys / kBlockSize;
-constexpr int kXKStages = 1, kXVStages = 2;       // K and V tiles in shared memory
+// K tiles in shared memory: one; V tiles: two beside one row tile, one beside two
+constexpr int kXVStages = 2;
 constexpr float kXRescaleLog2 = 8.f;
 constexpr int kXHalfQ = kXRows * 128;             // bytes of a 64-column half of a Q tile
 constexpr int kXHalfKV = kXKeys * 128;            // and of a K / V tile
@@ -72,15 +77,16 @@ constexpr int kXHalfKV = kXKeys * 128;            // and of a K / V tile
 template <int D>
 struct PrefixSmem {
   static constexpr int kQTile = kXRows * D * 2, kKVTile = kXKeys * D * 2;
-  static constexpr int kK = 0;                                 // [kXKStages]
-  static constexpr int kV = kK + kXKStages * kKVTile;          // [kXVStages]
-  static constexpr int kBar = kV + kXVStages * kKVTile;        // 1024 bytes, of which barriers 256
-  static constexpr int kQ = kBar + 1024;                       // [q_tiles] row tiles
-  // behind them: float2 [2][128], a chain's (m, l); PrefixGroup [num_groups + 1]
-  static __host__ __device__ constexpr int red(int q_tiles) { return kQ + q_tiles * kQTile; }
-  static __host__ __device__ constexpr int groups(int q_tiles) { return red(q_tiles) + 2 * kXRows * 8; }
-  static size_t bytes(int q_tiles, int num_groups) {
-    return 1024 + groups(q_tiles) + sizeof(PrefixGroup) * (static_cast<size_t>(num_groups) + 1);
+  static_assert(kQTile == kKVTile, "the second row tile takes the second V stage's place");
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + kKVTile;                      // V stage 0
+  static constexpr int kV1 = kV + kKVTile;                     // V stage 1, or row tile 0
+  static __host__ __device__ constexpr int q(int q_tiles) { return kV1 + (2 - q_tiles) * kQTile; }   // row tiles
+  static constexpr int kBar = kV1 + 2 * kKVTile;               // 1024 bytes, of which barriers 256
+  static constexpr int kRed = kBar + 1024;                     // float2 [2][128], a chain's (m, l)
+  static constexpr int kGroups = kRed + 2 * kXRows * 8;        // PrefixGroup [num_groups + 1]
+  static size_t bytes(int num_groups) {
+    return 1024 + kGroups + sizeof(PrefixGroup) * (static_cast<size_t>(num_groups) + 1);
   }
 };
 
@@ -176,9 +182,9 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   extern __shared__ unsigned char xsm_raw[];
   unsigned char* sm = xsm_raw + ((1024 - (smem_u32(xsm_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
-  uint64_t* k_full = bars;                    // [kXKStages] K tile landed
-  uint64_t* k_empty = k_full + kXKStages;     // [kXKStages] its Q K^T done
-  uint64_t* v_full = k_empty + kXKStages;     // [kXVStages] V tile landed
+  uint64_t* k_full = bars;                    // K tile landed
+  uint64_t* k_empty = k_full + 1;             // its Q K^T done
+  uint64_t* v_full = k_empty + 1;             // [kXVStages] V tile landed
   uint64_t* v_empty = v_full + kXVStages;     // [kXVStages] its P V done
   uint64_t* s_full = v_empty + kXVStages;     // [2] per chain: scores ready
   uint64_t* p_full = s_full + 2;              // [2] per chain, 128 arrivals: P written, O rescaled
@@ -187,9 +193,13 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   uint64_t* mma_idle = q_full + 1;            // [2] an issuer's MMAs done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * kXKStages + 2 * kXVStages + 2 + 2 + 2 + 1 + 2 + 1) * 8 <= 256, "barrier block overflows");
-  float2* red = reinterpret_cast<float2*>(sm + L::red(p.q_tiles));
-  PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::groups(p.q_tiles));
+  static_assert((2 + 2 * kXVStages + 2 + 2 + 2 + 1 + 2 + 1) * 8 <= 256, "barrier block overflows");
+  float2* red = reinterpret_cast<float2*>(sm + L::kRed);
+  PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(sm + L::kGroups);
+  // V stages, as a shift: tile t is in stage t & (stages - 1), its use t >> v_shift
+  const uint32_t v_shift = 2 - p.q_tiles;
+  auto v_stage = [&](uint32_t s) { return sm + (s == 0 ? L::kV : L::kV1); };
+  unsigned char* q_sm = sm + L::q(p.q_tiles);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 9) {
@@ -200,10 +210,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   }
   if (tid == 8 * 32) {
     *abort_flag = 0;
-    for (int s = 0; s < kXKStages; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-    }
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
     for (int s = 0; s < kXVStages; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
@@ -437,9 +445,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       int id = fetch_id(sg.t0);
       // Q of the piece, once every Q K^T of the one before has read its tiles
       if (tiles > 0) {
-        const uint32_t last = tiles - 1;
-        good = __all_sync(0xffffffffu,
-                          mbar_wait(&k_empty[last % kXKStages], (last / kXKStages) & 1, p.err) && !*abort_flag);
+        good = __all_sync(0xffffffffu, mbar_wait(k_empty, (tiles - 1) & 1, p.err) && !*abort_flag);
         if (!good) break;
       }
       if (lane == 0) mbar_arrive_expect_tx(q_full, L::kQTile * (sg.share ? 2 : 1));
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       __syncwarp();
       if (lane < (sg.share ? 2 : 1) * (D / 64)) {
         const int c = lane / (D / 64), h = lane % (D / 64);
-        tma_load_3d(sm + L::kQ + c * L::kQTile + h * kXHalfQ, &p.tmap_q, h * 64, sg.g * G,
+        tma_load_3d(q_sm + c * L::kQTile + h * kXHalfQ, &p.tmap_q, h * 64, sg.g * G,
                     gr.start + (sg.unit * kPrefixUnitRows + c * kXRows) / G, q_full, policy_evict_last());
       }
       __syncwarp();
@@ -463,16 +469,16 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       };
       // lane j + 8 h: half h of the tile's block j
       auto load = [&](bool is_v, int y) -> bool {
-        const uint32_t stages = is_v ? kXVStages : kXKStages, s = tiles % stages, use = tiles / stages;
-        uint64_t* full = is_v ? &v_full[s] : &k_full[s];
-        uint64_t* empty = is_v ? &v_empty[s] : &k_empty[s];
+        const uint32_t shift = is_v ? v_shift : 0, s = tiles & ((1u << shift) - 1), use = tiles >> shift;
+        uint64_t* full = is_v ? &v_full[s] : k_full;
+        uint64_t* empty = is_v ? &v_empty[s] : k_empty;
         const bool freed = use == 0 || mbar_wait(empty, (use - 1) & 1, p.err);
         if (!__all_sync(0xffffffffu, freed && !*abort_flag)) return false;
         if (lane == 0) mbar_arrive_expect_tx(full, L::kKVTile);
         __syncwarp();
         if (lane < kXTileBlocks * (D / 64)) {
           const int j = lane % kXTileBlocks, h = lane / kXTileBlocks;
-          tma_load_2d(sm + (is_v ? L::kV : L::kK) + s * L::kKVTile + h * kXHalfKV + j * 2048,
+          tma_load_2d((is_v ? v_stage(s) : sm + L::kK) + h * kXHalfKV + j * 2048,
                       is_v ? &p.tmap_v : &p.tmap_k, h * 64, y, full, pol);
         }
         __syncwarp();
@@ -491,10 +497,10 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       // loads this warp issued that nobody may have waited for (bounded)
       const unsigned long long deadline = global_ns() + kWaitLimitNs;
       if (issued_q > 0) mbar_wait_until(q_full, (issued_q - 1) & 1, deadline);
-      for (uint32_t t = issued_k > kXKStages ? issued_k - kXKStages : 0; t < issued_k; ++t)
-        mbar_wait_until(&k_full[t % kXKStages], (t / kXKStages) & 1, deadline);
-      for (uint32_t t = issued_v > kXVStages ? issued_v - kXVStages : 0; t < issued_v; ++t)
-        mbar_wait_until(&v_full[t % kXVStages], (t / kXVStages) & 1, deadline);
+      if (issued_k > 0) mbar_wait_until(k_full, (issued_k - 1) & 1, deadline);
+      const uint32_t stages = 1u << v_shift;
+      for (uint32_t t = issued_v > stages ? issued_v - stages : 0; t < issued_v; ++t)
+        mbar_wait_until(&v_full[t & (stages - 1)], (t >> v_shift) & 1, deadline);
     }
   } else {
     // ============================ MMA issuers (warps 9, 10) ============================
@@ -520,28 +526,27 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
           const bool last_use = !sg.share || c == 1;   // of the tile
           if (qk_warp) {
             // S of the chain once the P V that read P from its columns is done
-            const uint32_t s = t % kXKStages;
-            ok = mbar_wait(&k_full[s], (t / kXKStages) & 1, p.err) &&
+            ok = mbar_wait(k_full, t & 1, p.err) &&
                  (count[c] == 0 || mbar_wait(&pv_done[c], (count[c] - 1) & 1, p.err)) && !*abort_flag;
             if (!ok) break;
             ++count[c];
-            const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (sg.share ? c * L::kQTile : 0)), 16, 1024);
-            const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + s * L::kKVTile), 16, 1024);
+            const uint64_t a0 = umma_desc(smem_u32(q_sm + (sg.share ? c * L::kQTile : 0)), 16, 1024);
+            const uint64_t b0 = umma_desc(smem_u32(sm + L::kK), 16, 1024);
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
               umma_f16(tmem + c * kXKeys, a0 + static_cast<uint64_t>(((ks >> 2) * kXHalfQ + (ks & 3) * 32) >> 4),
                        b0 + static_cast<uint64_t>(((ks >> 2) * kXHalfKV + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
             umma_commit(&s_full[c]);
-            if (last_use) umma_commit(&k_empty[s]);
+            if (last_use) umma_commit(k_empty);
           } else {
-            const uint32_t s = t % kXVStages;
-            ok = mbar_wait(&v_full[s], (t / kXVStages) & 1, p.err) && mbar_wait(&p_full[c], count[c] & 1, p.err) &&
+            const uint32_t s = t & ((1u << v_shift) - 1);
+            ok = mbar_wait(&v_full[s], (t >> v_shift) & 1, p.err) && mbar_wait(&p_full[c], count[c] & 1, p.err) &&
                  !*abort_flag;
             if (!ok) break;
             ++count[c];
             tc_fence_after();
-            const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + s * L::kKVTile), kXHalfKV, 1024);
+            const uint64_t b0 = umma_desc(smem_u32(v_stage(s)), kXHalfKV, 1024);
             const uint32_t a0 = tmem + c * kXKeys, d = tmem + kOCol + c * D;
 #pragma unroll
             for (int pass = 0; pass < kPasses; ++pass)
@@ -792,7 +797,7 @@ pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t strea
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
       if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(PrefixSmem<D>::bytes(2, kMaxPrefixGroups))),
+                                           static_cast<int>(PrefixSmem<D>::bytes(kMaxPrefixGroups))),
                       "cudaFuncSetAttribute") ||
           // (the SM's whole shared memory, so that what this kernel leaves is the next one's)
           cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -803,7 +808,7 @@ pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t strea
     }
   }
   return cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(kXThreads),
-                                PrefixSmem<D>::bytes(p.q_tiles, p.num_groups), stream, p),
+                                PrefixSmem<D>::bytes(p.num_groups), stream, p),
                      "prefix_kernel launch")
              ? PKV_ERR_CUDA
              : PKV_OK;
@@ -843,8 +848,8 @@ pkv_status dispatch(pkv_dtype dtype, int head_dim, int group, F&& f) {
 
 }  // namespace
 
-size_t prefix_smem_bytes(int head_dim, int q_tiles, int num_groups) {
-  return head_dim == 64 ? PrefixSmem<64>::bytes(q_tiles, num_groups) : PrefixSmem<128>::bytes(q_tiles, num_groups);
+size_t prefix_smem_bytes(int head_dim, int num_groups) {
+  return head_dim == 64 ? PrefixSmem<64>::bytes(num_groups) : PrefixSmem<128>::bytes(num_groups);
 }
 
 pkv_status launch_prefix(PrefixParams& p, int ranges, int group, int head_dim, pkv_dtype dtype, cudaStream_t stream) {
