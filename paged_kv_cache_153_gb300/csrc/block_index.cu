@@ -620,6 +620,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
   }
 }
 
+// the most that a flat launch asks for
+constexpr int kFlatMaxSmem = 128 + kScoreStages * (kScoreStageBytes + static_cast<int>(sizeof(ScoreUnit))) +
+                             16 * kScoreStages + (2 * kFlatMaxBatch + 1) * static_cast<int>(sizeof(int));
+static_assert(kFlatMaxSmem + 64 <= 227 * 1024, "stages and counts fit one SM");
+
 struct SelectParams {
   const float* scores;           // [B, Hkv, max_blocks_per_seq]
   const int32_t* context_lens;
@@ -896,8 +901,9 @@ bool flat_grid(int64_t items, int warps_per_block, int batch, int* blocks) {
 template <typename P>
 pkv_status launch_flat(void (*kern)(P), int threads, int blocks, const P& p, size_t smem, cudaStream_t stream,
                        const char* what) {
+  // (the same limit each time: another thread's call may come between this and the launch)
   if (smem > 32 * 1024 &&
-      cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+      cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFlatMaxSmem),
                   "cudaFuncSetAttribute"))
     return PKV_ERR_CUDA;
   return cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(static_cast<unsigned>(threads)), smem,

@@ -618,6 +618,42 @@ def test_a_decode_step_end_to_end(pkv, dtype):
             assert torch.equal(buf[n][live], t[live]) and (n == "scores" or bool(live.all()))
 
 
+def test_scores_from_two_threads(pkv):
+    # two shapes of the flat form at a time: neither call takes the other's shared-memory limit
+    import threading
+    g = torch.Generator(device="cuda").manual_seed(31)
+
+    def make(b, hq, hkv, d, width, nb=500):
+        q = torch.randn((b, hq, d), generator=g, device="cuda").bfloat16()
+        bounds = torch.randn((nb, hkv, 2, d), generator=g, device="cuda").bfloat16()
+        tab = torch.randint(0, nb, (b, width), generator=g, device="cuda", dtype=torch.int32)
+        lens = torch.randint(1, 16 * width + 1, (b,), generator=g, device="cuda", dtype=torch.int32)
+        return (q, bounds, tab, lens), *(torch.zeros((b, hkv, width), device="cuda") for _ in range(2))
+    work = [make(40, 32, 8, 128, 1024), make(800, 4, 1, 64, 600)]
+
+    def call(item, out, stream=None):
+        pkv.pkv_block_scores(*item[0], out, scale=0.1, max_context_len=16 * out.shape[2], stream=stream)
+    failures = []
+
+    def loop(item, stream):
+        try:
+            for _ in range(200):
+                call(item, item[2], stream)
+        except Exception as e:   # noqa: BLE001 (reported below)
+            failures.append(e)
+    for item in work:
+        call(item, item[1])
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=loop, args=(item, torch.cuda.Stream())) for item in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, failures[0]
+    assert all(torch.equal(want, got) for _, want, got in work)
+
+
 def test_two_streams_each_with_its_workspace(pkv):
     a, b = Case([4000, 1300, 20], seed=20), Case([900] * 9, hq=16, hkv=4, dtype="f16", seed=21)
     jobs = []
