@@ -6,6 +6,7 @@
 // decode 9.8 against 4.9).
 #include "pycall.h"
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -26,7 +27,17 @@ const at::Tensor& need(PyObject* o, int dims, const char* what) {
   return t;
 }
 
-void* address(PyObject* o) { return o == Py_None ? nullptr : need(o, -1, "").data_ptr(); }
+thread_local int call_device;   // the current device, asked once per call (-1: not yet)
+
+// t's address, on the device that the call will launch on
+void* ptr(const at::Tensor& t) {
+  if (t.is_cuda() && call_device < 0) call_device = c10::cuda::current_device();
+  if (!t.is_cuda() || t.get_device() != call_device)
+    refuse(PyExc_ValueError, "tensors must be on the current CUDA device");
+  return t.data_ptr();
+}
+
+void* address(PyObject* o) { return o == Py_None ? nullptr : ptr(need(o, -1, "")); }
 
 template <typename T>
 T number(PyObject* o) {
@@ -107,6 +118,7 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", N, n);
     return nullptr;
   }
+  call_device = -1;
   try {
     return F(args);
   } catch (const Refused&) {
@@ -155,7 +167,7 @@ PyObject* rope_append(PyObject* const* a) {
     if (tq.size(0) != n || to.sizes() != tq.sizes())
       refuse(PyExc_ValueError, "q, q_out and positions differ in shape");
     hq = to_int(tq.size(1)), d = to_int(tq.size(2));
-    q = tq.data_ptr(), q_out = to.data_ptr();
+    q = ptr(tq), q_out = ptr(to);
     q_stride = token_stride(tq, "q: a token's heads must be contiguous");
     o_stride = token_stride(to, "q_out: a token's heads must be contiguous");
     typed = &tq;
@@ -171,15 +183,15 @@ PyObject* rope_append(PyObject* const* a) {
       refuse(PyExc_ValueError, "slot_mapping must be contiguous int64, one slot per position");
     caches_check(ck, cv, kind == 0 ? 2 : 1);
     d = to_int(ck.size(3));
-    k = tk.data_ptr(), v = tv.data_ptr(), kc = ck.data_ptr(), vc = cv.data_ptr();
+    k = ptr(tk), v = ptr(tv), kc = ptr(ck), vc = ptr(cv);
     k_stride = token_stride(tk, "k_new: a token's heads must be contiguous");
     v_stride = token_stride(tv, "v_new: a token's heads must be contiguous");
     if (!has_q) typed = &tk;
   }
   if (typed == nullptr) refuse(PyExc_ValueError, "q, or k_new and v_new, must be given");
-  const auto* pos_p = static_cast<const int32_t*>(pos.data_ptr());
+  const auto* pos_p = static_cast<const int32_t*>(ptr(pos));
   const auto* slots = static_cast<const int64_t*>(address(a[5]));
-  const auto* turns_p = static_cast<const uint64_t*>(turns.data_ptr());
+  const auto* turns_p = static_cast<const uint64_t*>(ptr(turns));
   const auto* ks = static_cast<const float*>(address(a[10]));
   const auto* vs = static_cast<const float*>(address(a[11]));
   const int rot = to_int(2 * turns.numel());
@@ -214,19 +226,19 @@ PyObject* block_bounds(PyObject* const* a) {
     const at::Tensor& t = need(a[5], -1, "");
     index_check(t);
     if (t.numel() != len.numel()) refuse(PyExc_ValueError, "new_lens and context_lens differ in length");
-    fresh = static_cast<const int32_t*>(t.data_ptr());
+    fresh = static_cast<const int32_t*>(ptr(t));
   }
   cache_check(kc, kind == 0 ? 2 : 1);
   contiguous(out);
   per_sequence(len.numel(), tab, len);
-  const auto* tp = static_cast<const int32_t*>(tab.data_ptr());
-  const auto* lp = static_cast<const int32_t*>(len.data_ptr());
+  const auto* tp = static_cast<const int32_t*>(ptr(tab));
+  const auto* lp = static_cast<const int32_t*>(ptr(len));
   const int max_new = number<int>(a[6]), b = to_int(len.numel()), hkv = to_int(kc.size(1)), d = to_int(kc.size(3)),
             bs = to_int(kc.size(2)), width = to_int(tab.size(1));
   const int64_t nb = kc.size(0);
   const pkv_dtype dt = dtype_of(out, a[7]);
   auto* err = static_cast<int32_t*>(address(a[8]));
-  void *s = stream_of(a[9]), *k = kc.data_ptr(), *o = out.data_ptr();
+  void *s = stream_of(a[9]), *k = ptr(kc), *o = ptr(out);
   if (kind == 0)
     return status([&] {
       return pkv_kv_block_bounds(k, tp, lp, fresh, max_new, b, hkv, d, bs, width, nb, o, dt, err, s);
@@ -263,10 +275,10 @@ PyObject* block_scores(PyObject* const* a) {
   const auto* ks = static_cast<const float*>(address(a[7]));
   const pkv_dtype dt = dtype_of(q, a[8]);
   auto* err = static_cast<int32_t*>(address(a[9]));
-  void *s = stream_of(a[10]), *qp = q.data_ptr(), *lp = lo_hi.data_ptr();
-  const auto* tp = static_cast<const int32_t*>(tab.data_ptr());
-  const auto* np = static_cast<const int32_t*>(len.data_ptr());
-  auto* op = static_cast<float*>(out.data_ptr());
+  void *s = stream_of(a[10]), *qp = ptr(q), *lp = ptr(lo_hi);
+  const auto* tp = static_cast<const int32_t*>(ptr(tab));
+  const auto* np = static_cast<const int32_t*>(ptr(len));
+  auto* op = static_cast<float*>(ptr(out));
   return status([&] {
     return pkv_block_scores(qp, lp, tp, np, ks, bi, hq, h, di, 16, w, nb, max_ctx, scale, op, dt, err, s);
   });
@@ -283,9 +295,9 @@ PyObject* select_blocks(PyObject* const* a) {
   contiguous(sc);
   if (sc.scalar_type() != at::kFloat || len.numel() != sc.size(0))
     refuse(PyExc_ValueError, "scores must be fp32, with a context length per sequence");
-  const auto* sp = static_cast<const float*>(sc.data_ptr());
-  const auto* lp = static_cast<const int32_t*>(len.data_ptr());
-  auto* op = static_cast<int32_t*>(sel.data_ptr());
+  const auto* sp = static_cast<const float*>(ptr(sc));
+  const auto* lp = static_cast<const int32_t*>(ptr(len));
+  auto* op = static_cast<int32_t*>(ptr(sel));
   const int b = to_int(sc.size(0)), h = to_int(sc.size(1)), w = to_int(sc.size(2)), budget = to_int(sel.size(2)),
             first = number<int>(a[3]), last = number<int>(a[4]);
   auto* err = static_cast<int32_t*>(address(a[5]));
@@ -313,8 +325,8 @@ struct Attention {
     per_sequence(tq.size(0), t, l);
     if (o.sizes() != tq.sizes()) refuse(PyExc_ValueError, "q and out differ in shape");
     if (kc.size(3) != tq.size(2)) refuse(PyExc_ValueError, "q and the caches differ in head_dim");
-    q = tq.data_ptr(), k = kc.data_ptr(), v = vc.data_ptr(), out = o.data_ptr(), ws = w.data_ptr();
-    tab = static_cast<const int32_t*>(t.data_ptr()), len = static_cast<const int32_t*>(l.data_ptr());
+    q = ptr(tq), k = ptr(kc), v = ptr(vc), out = ptr(o), ws = ptr(w);
+    tab = static_cast<const int32_t*>(ptr(t)), len = static_cast<const int32_t*>(ptr(l));
     b = to_int(tq.size(0)), hq = to_int(tq.size(1)), d = to_int(tq.size(2)), width = to_int(t.size(1));
     nb = kc.size(0), hkv = to_int(kc.size(1)), bs = to_int(kc.size(2));
     ws_bytes = w.nbytes();
@@ -330,7 +342,7 @@ PyObject* sparse_decode(PyObject* const* a) {
   const Attention x(a[1], a[2], a[3], a[6], a[7], a[9], a[11], kind == 0 ? 2 : 1);
   if (sel.size(0) != x.b || sel.size(1) != x.hkv)
     refuse(PyExc_ValueError, "selected must be [batch, num_kv_heads, budget]");
-  const auto* lists = static_cast<const int32_t*>(sel.data_ptr());
+  const auto* lists = static_cast<const int32_t*>(ptr(sel));
   const int budget = to_int(sel.size(2));
   const float scale = number<float>(a[10]);
   const pkv_dtype dt = dtype_of(THPVariable_Unpack(a[1]), a[12]);
@@ -359,8 +371,8 @@ PyObject* prefix_decode(PyObject* const* a) {
   index_check(starts);
   index_check(pre);
   const Attention x(a[0], a[1], a[2], a[3], a[4], a[7], a[11], 2);
-  const auto* sp = static_cast<const int32_t*>(starts.data_ptr());
-  const auto* pp = static_cast<const int32_t*>(pre.data_ptr());
+  const auto* sp = static_cast<const int32_t*>(ptr(starts));
+  const auto* pp = static_cast<const int32_t*>(ptr(pre));
   const int groups = to_int(pre.numel()), max_ctx = number<int>(a[9]), max_pre = number<int>(a[10]);
   const float scale = number<float>(a[8]);
   const pkv_dtype dt = dtype_of(THPVariable_Unpack(a[0]), a[12]);

@@ -58,6 +58,21 @@ def test_attention_over_fp8_caches(pkv):
             sparse_fp8(pkv, **bad)
 
 
+def test_tensors_of_another_device(pkv):
+    # (all that these calls get is on the host)
+    for call in (sparse, sparse_fp8, prefix):
+        with pytest.raises(ValueError, match="device"):
+            call(pkv)
+    with pytest.raises(ValueError, match="device"):
+        pkv.pkv_block_scores(Q, BOUNDS, TAB, LENS, SCORES, scale=1.0, max_context_len=64, stream=0)
+    with pytest.raises(ValueError, match="device"):
+        pkv.pkv_select_blocks(SCORES, LENS, LISTS, stream=0)
+    with pytest.raises(ValueError, match="device"):
+        pkv.pkv_rope_append(Q, NEW, NEW, LENS, SLOTS, TURNS, Q, K16, K16, stream=0)
+    with pytest.raises(ValueError, match="device"):
+        pkv.pkv_kv_block_bounds(K16, TAB, LENS, BOUNDS, max_new_len=1, stream=0)
+
+
 def test_block_index(pkv):
     def bounds(k, new=None, tab=TAB, fn="pkv_kv_block_bounds"):
         getattr(pkv, fn)(k, tab, LENS, BOUNDS, max_new_len=1, new_lens=new, stream=0)
