@@ -581,8 +581,8 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
   auto first_writes = [&]() {
     if (writes_done) return;
     writes_done = true;
-    // (kRest runs beside the shared-prefix kernel: that kernel started after
-    // everything before it had completed, and touches none of what this one
+    // (kRest runs beside the shared-prefix kernel: that kernel released it after
+    // everything before had completed, and touches none of what this one
     // writes, so nothing is waited for until the end)
     if constexpr (SRC != kRest) pdl_wait();
     if (blockIdx.x == 0 && p.ws_cum != nullptr)

@@ -48,10 +48,11 @@
 // warps to a scheduler and two to one, so that a scheduler has room for one or
 // two more; about 94 KiB of shared memory) for one thread block of five warps of
 // the decode over the sequences' own blocks, which is bound by memory where this
-// one is bound by the tensor cores; that kernel launches as soon as this one has
-// started.  64 sequences of 16 to 2048 tokens behind 32768: 63.8 us (66.1 with two
-// stages of V, which leave the other block three consumer warps of two stages
-// each instead of four; 103 where the two do not fit an SM together).
+// one is bound by the tensor cores; that kernel launches as soon as the wait for
+// the previous one is over.  64 sequences of 16 to 2048 tokens behind 32768: 61.8 us
+// (63.8 without the early start; 66.1 also with two stages of V, which leave the
+// other block three consumer warps of two stages each instead of four; 103 where
+// the two do not fit an SM together).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -225,8 +226,11 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     mbar_init(q_full, 1);
     fence_mbar_init();
   }
-  pdl_wait();
-  pdl_release();   // (the next kernel, over the sequences' own blocks, reads only inputs before its wait)
+  // Early start, as in the decode kernel: until the waits below (the producer's
+  // before Q, the softmax warps' before their first store) this kernel reads
+  // lengths, group bounds and tables only, which no kernel that releases early
+  // writes.  The producer then releases the next kernel, the decode over the
+  // sequences' own blocks, which so starts after everything before this one.
 
   // ---- the groups: shared blocks, first covering sequence, cost ------------
   for (int j = warp; j < p.num_groups; j += kXThreads / 32) {
@@ -273,8 +277,10 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0) {
+    pdl_wait();
     for (int j = tid; j <= p.num_groups; j += kXThreads) p.groups[j] = groups[j];
+  }
   const uint32_t tmem = *tmem_slot;
   const int64_t V = groups[p.num_groups].cost, R = gridDim.x, range = blockIdx.x;
   const int64_t first = div_nonneg(range * V, R), end = div_nonneg((range + 1) * V, R);
@@ -291,6 +297,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     // A failed wait ends a warp's work but not its walk over the pieces: the two
     // warpgroups meet at named barriers, which must find all of them.
     bool ok = true;
+    pdl_wait();
     for (int64_t pos = first; pos < end;) {
       const PrefixSeg sg = segment(pos);
       pos = sg.next;
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     // ============================ TMA producer ============================
     uint32_t tiles = 0;                  // tiles loaded so far (K and V alike)
     uint32_t issued_k = 0, issued_v = 0, issued_q = 0;
-    bool good = true;
+    bool good = true, waited = false;
     for (int64_t pos = first; pos < end && good;) {
       const PrefixSeg sg = segment(pos);
       pos = sg.next;
@@ -443,6 +450,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         return (t < sg.t1 && lane < kXTileBlocks && blk < gr.blocks) ? row[blk] : -1;
       };
       int id = fetch_id(sg.t0);
+      if (!waited) pdl_wait_and_release();
+      waited = true;
       // Q of the piece, once every Q K^T of the one before has read its tiles
       if (tiles > 0) {
         good = __all_sync(0xffffffffu, mbar_wait(k_empty, (tiles - 1) & 1, p.err) && !*abort_flag);
@@ -492,6 +501,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         ++tiles;
       }
     }
+    if (!waited) pdl_wait_and_release();
     if (!good) *abort_flag = 1;
     if (*abort_flag && lane == 0) {
       // loads this warp issued that nobody may have waited for (bounded)
