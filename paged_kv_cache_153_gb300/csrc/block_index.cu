@@ -15,9 +15,11 @@
 // highest scores, ties to the lowest index, in ascending order.
 //
 // All three are bound by memory (or by latency, for a few sequences): a key
-// slab, a bounds row and a score are each read once.  They let the next kernel
-// launch as soon as their own wait is over: what they write (bounds, scores,
-// lists) no kernel of this library reads before its own wait.
+// slab, a bounds row and a score are each read once.  Early start, as in the
+// decode kernel: before they wait for the previous kernel they read lengths,
+// tables and (bounds) the cache, which no kernel that releases early writes.
+// They let the next kernel launch as soon as their own wait is over: what they
+// write (bounds, scores, lists) no kernel of this library reads before its own.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -91,10 +93,10 @@ struct RowChunk {
 //                 takes an equal run of consecutive units.
 // Flat is taken when the launch by sequence would be more than kFlatWaves
 // times the resident warps.  On GB300: bounds of 32 contexts of 2048..32768
-// tokens (E4M3, 389 MB) 64.2 us flat, 120 by sequence; scores of 64 contexts of
-// 1024..32768 (141 MB) 27.3 against 27.4, but with two of 131072 among 62 of
-// 1000 (83 MB) 16.8 against 71.5; one step's bounds of 64 sequences stay by
-// sequence (2.1 us).
+// tokens (E4M3, 389 MB) 60.6 us flat, 111 by sequence; scores of 64 contexts of
+// 1024..32768 (141 MB) 26.1 against 27.6, but with two of 131072 among 62 of
+// 1000 (83 MB) 16.0 against 70.4; one step's bounds of 64 sequences stay by
+// sequence (1.8 us).
 // ---------------------------------------------------------------------------
 constexpr int kFlatWaves = 2;
 constexpr int kFlatMaxBatch = 900;               // whose counts fit in shared memory beside the stages
@@ -196,9 +198,10 @@ struct BoundsSlab {
     const unsigned char* src = slab + (lane % kLPR) * 16;
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
-      // (a row past the context is replaced by row 0, which holds a token)
+      // (a row past the context is replaced by row 0, which holds a token; from
+      // L2, where a fused step that released this launch early has its new rows)
       const int r = l * kRows + lane / kLPR;
-      v[l] = __ldcs(reinterpret_cast<const uint4*>(src + (r < rows ? r : 0) * kRow));
+      v[l] = __ldcg(reinterpret_cast<const uint4*>(src + (r < rows ? r : 0) * kRow));
     }
   }
   template <typename OT>
@@ -257,9 +260,12 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const _
   using S = BoundsSlab<KV, D>;
   const int lane = threadIdx.x & 31;
   const int item = blockIdx.x * kBoundsWarps + static_cast<int>(threadIdx.x >> 5);
-  pdl_wait_and_release();
-  if (item >= p.max_touched * p.n_kv_heads) return;
+  if (item >= p.max_touched * p.n_kv_heads) {
+    pdl_wait_and_release();
+    return;
+  }
   const int g = item % p.n_kv_heads, step = item / p.n_kv_heads;
+  bool waited = false;
   for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
     const Touched t = touched_blocks(p, b, item == 0 && lane == 0);
     const int i = t.first + step;
@@ -272,8 +278,11 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const _
     const int64_t slab = static_cast<int64_t>(id) * p.n_kv_heads + g;
     S s;
     s.load(p.k_cache + slab * kBlockSize * S::kRow, min(kBlockSize, t.ctx - i * kBlockSize), lane);
+    if (!waited) pdl_wait_and_release();
+    waited = true;
     s.store(p.bounds + slab * 4 * D, lane, OT{});
   }
+  if (!waited) pdl_wait_and_release();
 }
 
 template <typename KV, typename OT, int D>
@@ -283,7 +292,6 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, 3) block_bounds_flat_kernel
   extern __shared__ int cum[];                     // [batch + 1] touched blocks
   __shared__ int warp_sum[kBoundsWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait_and_release();
   scan_units<kBoundsWarps * 32>(p.batch, cum, warp_sum, [&](int b) {
     const Touched t = touched_blocks(p, b, blockIdx.x == 0);
     return t.last - t.first;
@@ -292,6 +300,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, 3) block_bounds_flat_kernel
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kBoundsWarps;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + warp;
   const int64_t end = (w + 1) * total / warps;
+  bool waited = false;
   // 32 slabs at a time: each lane finds one, then the warp reduces them in turn
   for (int64_t s0 = w * total / warps; s0 < end; s0 += 32) {
     int64_t slab = -1;
@@ -320,11 +329,14 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, 3) block_bounds_flat_kernel
         if (k + u >= n) at[u] = -1;
         if (at[u] >= 0) s[u].load(p.k_cache + at[u] * kBlockSize * S::kRow, r, lane);
       }
+      if (!waited) pdl_wait_and_release();
+      waited = true;
 #pragma unroll
       for (int u = 0; u < kSlabs; ++u)
         if (at[u] >= 0) s[u].store(p.bounds + at[u] * 4 * D, lane, OT{});
     }
   }
+  if (!waited) pdl_wait_and_release();
 }
 
 struct ScoreParams {
@@ -413,18 +425,23 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const __
   const int lane = threadIdx.x & 31, r4 = lane >> 2, q4 = lane & 3;
   const int item = blockIdx.x * kScoreWarps + static_cast<int>(threadIdx.x >> 5);
   const int g = item % p.n_kv_heads, i0 = item / p.n_kv_heads * 16;
-  pdl_wait_and_release();
+  bool waited = false;
   for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
     const int nblk = scored_blocks(p, b, item == 0 && lane == 0);
     if (i0 >= nblk) continue;
     // rows r4 and r4 + 8 (a row behind the context, or of a bad id, is not read)
     const int32_t* row = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
     uint4 a[2][2 * kChunks];
+    int32_t ids[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ids[h] = i0 + r4 + 8 * h < nblk ? row[i0 + r4 + 8 * h] : -1;
+    if (!waited) pdl_wait_and_release();   // (the bounds may be the previous kernel's)
+    waited = true;
     bool live[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = i0 + r4 + 8 * h;
-      const int32_t id = i < nblk ? row[i] : -1;
+      const int32_t id = ids[h];
       live[h] = id >= 0 && id < p.num_blocks;
       if (i < nblk && !live[h] && q4 == 0 && g == 0) record_error(p.err, PKV_ERR_OOB);
       const unsigned char* src =
@@ -445,6 +462,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const __
     for (int h = 0; h < 2; ++h)
       if (q4 == 0 && i0 + r4 + 8 * h < nblk) out[r4 + 8 * h] = live[h] ? s[h] * sc : -INFINITY;
   }
+  if (!waited) pdl_wait_and_release();
 }
 
 // Flat: a persistent thread block takes units of `tile` blocks and up to
@@ -507,7 +525,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
     }
     fence_mbar_init();
   }
-  pdl_wait_and_release();
   scan_units<kScoreThreads>(p.batch, cum, warp_sum, [&](int b) {
     scored[b] = scored_blocks(p, b, blockIdx.x == 0);
     return (scored[b] + lay.tile - 1) / lay.tile;
@@ -542,6 +559,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
     uint32_t k = 0;
     bool ok = true;
     Next cur = fetch(blockIdx.x);
+    pdl_wait_and_release();   // (the bounds may be the previous kernel's)
     for (int64_t u = blockIdx.x; ok; u += gridDim.x, ++k) {
       const int s = k % kScoreStages;
       const Next nxt = fetch(u + gridDim.x);
@@ -590,6 +608,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
     return;
   }
   // ---- consumers ----
+  pdl_wait();
   const int r4 = lane >> 2, q4 = lane & 3;
   for (uint32_t k = 0;; ++k) {
     const int s = k % kScoreStages;
@@ -682,8 +701,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   const int b = static_cast<int>(unit / p.n_kv_heads);
   for (int x = tid; x < kSelBins; x += kSelThreads) bins[x] = 0;
   if (tid == 0) n_listed = 0;
-  pdl_wait_and_release();
   const int ctx = p.context_lens[b];
+  pdl_wait_and_release();
   int n = ctx <= 0 ? 0 : static_cast<int>((static_cast<int64_t>(ctx) + kBlockSize - 1) / kBlockSize);
   if (ctx < 0 || n > p.max_blocks_per_seq) {
     if (tid == 0) record_error(p.err, PKV_ERR_OOB);

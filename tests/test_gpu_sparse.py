@@ -618,6 +618,39 @@ def test_a_decode_step_end_to_end(pkv, dtype):
             assert torch.equal(buf[n][live], t[live]) and (n == "scores" or bool(live.all()))
 
 
+@pytest.mark.parametrize("b,hkv", [(3, 2), (64, 8)])
+def test_bounds_right_behind_fused_steps(pkv, b, hkv):
+    # launches that start early, one behind the other: a step appends, the bounds read its rows
+    steps, d, hq = 24, 128, 4 * hkv
+    rng = np.random.default_rng(33)
+    start = rng.integers(1, 700, size=b).astype(np.int32)
+    width = (int(start.max()) + steps + 15) // 16
+    nb = b * width
+    g = torch.Generator(device="cuda").manual_seed(33)
+    kc, vc = (torch.randn((nb, hkv, 16, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    tab = torch.randperm(nb, generator=g, device="cuda").to(torch.int32).view(b, width)
+    lens = [torch.from_numpy(start + i).cuda() for i in range(steps + 1)]
+    q = torch.randn((b, hq, d), generator=g, device="cuda").bfloat16()
+    new = torch.randn((2, steps, b, hkv, d), generator=g, device="cuda").bfloat16()
+    bounds = torch.zeros((nb, hkv, 2, d), dtype=torch.bfloat16, device="cuda")
+    one, out = torch.ones(b, dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    top = int(start.max()) + steps
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(b, hq, hkv, d, width, top), dtype=torch.uint8, device="cuda")
+    pkv.pkv_kv_block_bounds(kc, tab, lens[0], bounds, max_new_len=top)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        pkv.pkv_paged_decode_step(q, new[0, i], new[1, i], kc, vc, tab, lens[i + 1], out, scale=d ** -0.5,
+                                  max_context_len=top, workspace=ws)
+        pkv.pkv_kv_block_bounds(kc, tab, lens[i + 1], bounds, new_lens=one, max_new_len=1)
+    torch.cuda.synchronize()
+    k, got, ids = kc.double().cpu().numpy(), bounds.double().cpu().numpy(), tab.cpu().numpy()
+    for s in range(b):
+        n = int(start[s]) + steps
+        for i in range(-(-n // 16)):
+            rows = k[ids[s, i], :, :min(16, n - 16 * i)]
+            assert np.array_equal(got[ids[s, i], :, 0], rows.min(1)) and np.array_equal(got[ids[s, i], :, 1], rows.max(1))
+
+
 def test_scores_from_two_threads(pkv):
     # two shapes of the flat form at a time: neither call takes the other's shared-memory limit
     import threading
