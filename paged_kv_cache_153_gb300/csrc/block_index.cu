@@ -666,10 +666,13 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 // memory (beyond 8192 of them, chunks of 8192 are read again in each step).
 //   1. smallest and largest key: the candidates' spread is far below 32 bits,
 //      so a histogram over it separates them at once;
-//   2. with many candidates and few to keep, a histogram of the 512 threads'
-//      own maxima first: the K-th highest of them is a lower bound of the K-th
-//      highest candidate, and only candidates above it are counted from then
-//      on (a shared-memory increment for each of 8192 took half of the time);
+//   2. with at least a candidate per thread and at most 256 to keep, a histogram
+//      of the 512 threads' own maxima: the K-th highest of them is a lower bound
+//      of the K-th highest candidate.  The candidates from it on, seldom many
+//      more than K, are listed in order, and if there are at most 256 of them,
+//      each is ranked among them and the K highest are the answer (11.3 to 10.4
+//      us in the batch below);
+//   else:
 //   3. 2048 bins over the bracket; the bin of the K-th highest candidate
 //      becomes the bracket, until it holds at most 64 (or one key only);
 //   4. the bracket's candidates are ranked among themselves: the K-th one's
@@ -678,13 +681,15 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 //   5. what lies above the threshold becomes a bit per candidate; a scan over
 //      the words' bit counts gives each word its place in the list.
 // Bound by instructions and barriers, not by the 5.6 MB of scores: 512 pairs of
-// 512 to 8192 blocks take 11.5 us (14.1 with the keys in registers and every
-// pass unrolled, which missed the instruction cache; 15.3 reading the scores
-// again in each pass; 18 with 256 threads or 1024).
+// 512 to 8192 blocks take 10.4 us (by steps 3 to 5 alone, before step 2: 14.1 with
+// the keys in registers and every pass unrolled, which missed the instruction
+// cache; 15.3 reading the scores again in each pass; 18 with 256 threads or 1024).
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelChunk = 8192;
 constexpr int kSelRank = 64;
+constexpr int kSelShort = 256;
+static_assert(kSelRank <= kSelShort && kSelShort <= kSelThreads, "a thread per listed candidate");
 static_assert(kSelChunk / 32 <= kSelThreads, "a thread per word of a chunk's bits");
 
 __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SelectParams p) {
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   __shared__ uint32_t bins[kSelBins];
   __shared__ uint32_t red[2][kSelWarps];
   __shared__ uint32_t pick[3];
-  __shared__ uint64_t listed[kSelRank];
+  __shared__ uint64_t listed[kSelShort];
   __shared__ uint32_t n_listed;
   __shared__ uint32_t bits[kSelChunk / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -794,16 +799,53 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     for (int x = tid; x < kSelBins; x += kSelThreads) bins[x] = 0;
     __syncthreads();
   };
-  if (need <= kSelThreads / 2 && cand >= 8 * kSelThreads) {
+  int32_t* dst = out + p.num_first;
+  bool dirty = false;
+  if (need <= kSelShort && cand >= kSelThreads && cand <= kSelChunk) {
     const int shift = shift_of();
     atomicAdd(&bins[(own_max - base) >> shift], 1u);       // (every thread has candidates here)
     __syncthreads();
     find_bin(need);
     base += pick[0] << shift;
     span = hi - base;
-    clear_bins();
+    dirty = true;
+    // the candidates from base on, in order
+#pragma unroll 4
+    for (int i0 = warp * 32; i0 < cand; i0 += kSelThreads) {
+      const int i = i0 + lane;
+      const uint32_t mask = __ballot_sync(full, i < cand && keys[i] >= base);
+      if (lane == 0) bits[i0 >> 5] = mask;
+    }
+    __syncthreads();
+    uint32_t mask = 32 * tid < cand ? bits[tid] : 0u;
+    const uint32_t own = __popc(mask);
+    const uint32_t upto = scan(own);
+    if (tid == kSelThreads - 1) pick[0] = upto;
+    for (uint32_t at = upto - own; mask != 0 && at < kSelShort; ++at) {
+      const uint32_t i = 32 * tid + __ffs(mask) - 1;
+      // (higher key first, then lower index: one 64-bit order)
+      listed[at] = (static_cast<uint64_t>(keys[i]) << 32) | (full - i);
+      mask &= mask - 1;
+    }
+    __syncthreads();
+    const int m = static_cast<int>(pick[0]);
+    if (m <= kSelShort) {
+      uint32_t above = 0;
+      const uint64_t mine = tid < m ? listed[tid] : 0u;
+      if (warp * 32 < m) {
+#pragma unroll 8
+        for (int x = 0; x < m; ++x) above += listed[x] > mine;
+      }
+      const bool keep = tid < m && above < need;
+      const uint32_t kept = __ballot_sync(full, keep);
+      if (lane == 0) red[1][warp] = __popc(kept);
+      __syncthreads();
+      const uint32_t before = __reduce_add_sync(full, lane < warp ? red[1][lane % kSelWarps] : 0u);
+      const uint32_t at = before + __popc(kept & ((1u << lane) - 1));
+      if (keep && at < room) dst[at] = c0 + static_cast<int>(full - static_cast<uint32_t>(mine));
+      return;
+    }
   }
-  bool dirty = false;
   while (inside > kSelRank && span > 0) {
     const int shift = shift_of();
     if (dirty) clear_bins();
@@ -864,7 +906,6 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     }
   }
 
-  int32_t* dst = out + p.num_first;
   uint32_t done = 0;                                       // kept in earlier chunks
   for (int from = 0; from < cand; from += kSelChunk) {
     const int m = min(kSelChunk, cand - from), words = (m + 31) / 32;
