@@ -669,10 +669,10 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 //   2. with at least a candidate per thread and at most 256 to keep, a histogram
 //      of the 512 threads' own maxima: the K-th highest of them is a lower bound
 //      of the K-th highest candidate.  The candidates from it on, seldom many
-//      more than K, are listed in order, and if there are at most 256 of them,
-//      each is ranked among them and the K highest are the answer (11.3 to 10.4
-//      us in the batch below);
-//   else:
+//      more than K, are listed in order (of up to 8192), and if there are at
+//      most 256 of them, each is ranked among them and the K highest are the
+//      answer (11.3 to 10.4 us in the batch below);
+//   else, among what is left:
 //   3. 2048 bins over the bracket; the bin of the K-th highest candidate
 //      becomes the bracket, until it holds at most 64 (or one key only);
 //   4. the bracket's candidates are ranked among themselves: the K-th one's
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   };
   int32_t* dst = out + p.num_first;
   bool dirty = false;
-  if (need <= kSelShort && cand >= kSelThreads && cand <= kSelChunk) {
+  if (need <= kSelShort && cand >= kSelThreads) {
     const int shift = shift_of();
     atomicAdd(&bins[(own_max - base) >> shift], 1u);       // (every thread has candidates here)
     __syncthreads();
@@ -809,6 +809,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     base += pick[0] << shift;
     span = hi - base;
     dirty = true;
+  }
+  if (dirty && cand <= kSelChunk) {
     // the candidates from base on, in order
 #pragma unroll 4
     for (int i0 = warp * 32; i0 < cand; i0 += kSelThreads) {
