@@ -449,8 +449,9 @@ pkv_status pkv_paged_decode_step_int8(const void* q, const void* k_new, const vo
  *                        full turns of f_i in original_context positions
  * into turns[rot_dim / 2] (host): f_i / (2 pi), full turns per position, in
  * units of 2^-64 (rounded).  A position times it, modulo 2^64, is the angle
- * modulo one turn, so far positions lose nothing but p times f_i's rounding.  amplitude: 1
- * but for PKV_ROPE_RAMP.  The caller copies turns to the device once.
+ * modulo one turn, so far positions lose nothing but p times f_i's rounding.
+ * amplitude: 1 but for PKV_ROPE_RAMP.  The caller copies turns to the device
+ * once.
  * PKV_ERR_INVALID_ARG: an odd or non-positive rot_dim, base <= 1, factor < 1,
  * low_turns <= 0 or high_turns <= low_turns (where they are used).
  *

@@ -31,7 +31,7 @@ bool cuda_failed(cudaError_t e, const char* what) {
   return true;
 }
 
-// the driver's tensor-map encoder (null, with the reason kept, when it cannot be had)
+// cuTensorMapEncodeTiled, looked up once (null, with the reason kept, when it cannot be had)
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;

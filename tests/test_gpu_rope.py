@@ -196,6 +196,33 @@ def test_padding_and_slots_out_of_range(pkv):
     assert torch.equal(touched, c.caches)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kv", ["fp8", "e5m2"])
+def test_every_16_bit_value_under_many_scales(pkv, dtype, kv):
+    # v rows get the codes of the plain append (an IEEE division): ordinary scales, powers of two, scales
+    # whose quotients are often exact or ties, and scales at the ends of the range or outside it
+    scales = [1.0, 0.5, 2.0 ** -9, 0.0234567, 1.5, 0.75, 3.0, 1.1, 0.9999999, 448.0, 1e-30, 1e-38, 1e-44, 3e38, 0.0,
+              -0.7, float("inf"), float("nan"), 2.0 ** 100, 2.0 ** -100, 7.3e29, 1.3e-29, 5.0, 1 / 3]
+    h = len(scales)
+    x = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(gu.TORCH_16[dtype]).view(512, 1, 128)
+    v = x.expand(512, h, 128).contiguous().cuda()
+    s = torch.tensor(scales, dtype=torch.float32, device="cuda")
+    caches = [torch.zeros((32, h, 16, 128), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    slots = torch.arange(512, dtype=torch.int64, device="cuda")
+    pos = torch.zeros(512, dtype=torch.int32, device="cuda")
+    turns = torch.from_numpy(pkv.pkv_rope_plan(128)[0]).cuda()
+    getattr(pkv, f"pkv_rope_append_{kv}")(None, v, v, pos, slots, turns, None, caches[0], caches[1], s, s)
+    getattr(pkv, f"pkv_kv_append_{kv}")(v, v, slots, caches[2], caches[3], s, s)
+    torch.cuda.synchronize()
+    assert torch.equal(caches[1], caches[3])
+    # and k rows at position 0, where the rotation is x 1 - y 0: the same but for what 0 times infinity and the
+    # sign of a zero change
+    y = torch.roll(x.double(), 64, 2)
+    plain = (torch.isfinite(x.double()) & torch.isfinite(y) & (x.double() != 0)).expand(512, h, 128)
+    plain = plain.reshape(32, 16, h, 128).transpose(1, 2).cuda()
+    assert torch.equal(caches[0][plain], caches[2][plain])
+
+
 def test_nonfinite_values_stay_in_their_pair(pkv):
     c = Case(pkv, tokens=4, hq=2, hkv=1, d=64, rot=64, dtype="bf16", seed=5)
     c.q[1, 0, 3] = float("inf")
