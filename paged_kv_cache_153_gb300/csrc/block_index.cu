@@ -471,8 +471,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const __
 // with the unit's queries behind them, and 8 warps take its (16 blocks, head)
 // products from there.  The bulk copies set the pace: a thread block gets one
 // about every 185 clocks, which at 4 KiB each is this SM's share of HBM (half the
-// heads per unit, 2 KiB, took twice as long, with 8 warps or 12).  Rows lie 64 bytes past a multiple of 128 apart, so a
-// quarter warp's 16-byte loads touch every bank once.
+// heads per unit, 2 KiB, took twice as long, with 8 warps or 12).  Rows lie 64
+// bytes past a multiple of 128 apart, so a quarter warp's 16-byte loads touch
+// every bank once.
 constexpr int kScoreConsumers = 8;
 constexpr int kScoreThreads = (kScoreConsumers + 1) * 32;
 constexpr int kScoreStages = 3;

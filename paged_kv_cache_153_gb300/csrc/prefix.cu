@@ -591,10 +591,10 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
 // the pieces in the decode kernel's partial slots, or the one state it left
 // for a pair that one range holds.
 // It is all latency.  Small calls work out the geometry from the inputs while
-// the other kernels run; others read what those left.  Then the lanes find the pieces (which take two divisions each) of 32
-// ranges at a time, prefix and own blocks in one list, and their states are
-// loaded 8 at a time.  (Every lane dividing for every piece, one list after the
-// other: 14 us of a 93 us call.)
+// the other kernels run; others read what those left.  Then the lanes find the
+// pieces (which take two divisions each) of 32 ranges at a time, prefix and own
+// blocks in one list, and their states are loaded 8 at a time.  (Every lane
+// dividing for every piece, one list after the other: 14 us of a 93 us call.)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
 
