@@ -57,13 +57,27 @@ void* stream_of(PyObject* o) {
   return s;
 }
 
-// PKV_F16 / PKV_BF16 of t, or as given
-pkv_dtype dtype_of(const at::Tensor& t, PyObject* given) {
-  if (given != Py_None) return number<pkv_dtype>(given);
-  if (t.scalar_type() == at::kHalf) return PKV_F16;
-  if (t.scalar_type() == at::kBFloat16) return PKV_BF16;
-  refuse(PyExc_TypeError, "cannot infer the 16-bit kind; pass dtype=PKV_F16/PKV_BF16");
-}
+// The 16-bit type of a call: PKV_F16 / PKV_BF16 by t, or as given.  Where it is
+// given, tensors of any two-byte type hold its bits; else all have t's own type.
+struct Type16 {
+  pkv_dtype code;
+  bool given;
+  at::ScalarType own;
+  Type16(const at::Tensor& t, PyObject* tag) : code(PKV_F16), given(tag != Py_None), own(t.scalar_type()) {
+    if (given) {
+      code = number<pkv_dtype>(tag);
+      check(t);
+    } else if (own == at::kBFloat16) {
+      code = PKV_BF16;
+    } else if (own != at::kHalf) {
+      refuse(PyExc_TypeError, "cannot infer the 16-bit kind; pass dtype=PKV_F16/PKV_BF16");
+    }
+  }
+  void check(const at::Tensor& t) const {
+    if (given ? t.element_size() != 2 : t.scalar_type() != own)
+      refuse(PyExc_TypeError, "the 16-bit tensors of a call must have one type, or two-byte elements and dtype given");
+  }
+};
 
 // Index tensors are contiguous int32: another type would be read as garbage indices.
 void index_check(const at::Tensor& t) {
@@ -87,6 +101,30 @@ void caches_check(const at::Tensor& k, const at::Tensor& v, int64_t itemsize) {
     refuse(PyExc_ValueError, "caches must have one shape and type");
   cache_check(k, itemsize);
   contiguous(v);
+}
+
+// What a cache holds, its element size being right: kind 0 the call's 16-bit
+// type; 1 (E4M3) and 2 (E5M2) codes of any one-byte type but the other format's.
+void cache_type(const at::Tensor& t, int kind, const Type16& type) {
+  if (kind == 0)
+    type.check(t);
+  else if (t.scalar_type() == (kind == 1 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn))
+    refuse(PyExc_TypeError, "the cache holds the other FP8 format's codes");
+}
+
+// scales per KV head (None: none given)
+void scales_check(PyObject* o, int64_t heads) {
+  if (o == Py_None) return;
+  const at::Tensor& t = need(o, -1, "");
+  if (t.scalar_type() != at::kFloat || !t.is_contiguous()) refuse(PyExc_TypeError, "scales must be contiguous fp32");
+  if (t.numel() != heads) refuse(PyExc_ValueError, "scales must have one entry per KV head");
+}
+
+// the device error word (None: none given)
+void flag_check(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = need(o, -1, "");
+  if (t.scalar_type() != at::kInt || t.numel() < 1) refuse(PyExc_TypeError, "err_flag must be int32, one entry");
 }
 
 void per_sequence(int64_t b, const at::Tensor& tables, const at::Tensor& lens) {
@@ -155,22 +193,23 @@ PyObject* rope_append(PyObject* const* a) {
   }
   const at::Tensor &pos = need(a[4], -1, ""), &turns = need(a[6], 1, "turns must be [rot_dim / 2]");
   index_check(pos);
-  if (turns.element_size() != 8 || turns.is_floating_point() || !turns.is_contiguous())
+  if ((turns.scalar_type() != at::kLong && turns.scalar_type() != at::kUInt64) || !turns.is_contiguous())
     refuse(PyExc_TypeError, "turns must be the int64 tensor of pkv_rope_plan");
+  if (!has_q && !has_k) refuse(PyExc_ValueError, "q, or k_new and v_new, must be given");
+  const Type16 type(need(has_q ? a[1] : a[2], -1, ""), a[14]);
+  flag_check(a[15]);
   const int64_t n = pos.numel();
   void *q = nullptr, *q_out = nullptr, *k = nullptr, *v = nullptr, *kc = nullptr, *vc = nullptr;
   int64_t q_stride = 0, o_stride = 0, k_stride = 0, v_stride = 0, nb = 0;
   int hq = 0, hkv = 0, d = 0, bs = 16;
-  const at::Tensor* typed = nullptr;
   if (has_q) {
     const at::Tensor &tq = need(a[1], 3, "q must be [T, num_q_heads, head_dim]"), &to = need(a[7], -1, "");
     if (tq.size(0) != n || to.sizes() != tq.sizes())
       refuse(PyExc_ValueError, "q, q_out and positions differ in shape");
+    type.check(to);
     hq = to_int(tq.size(1)), d = to_int(tq.size(2));
-    q = ptr(tq), q_out = ptr(to);
     q_stride = token_stride(tq, "q: a token's heads must be contiguous");
     o_stride = token_stride(to, "q_out: a token's heads must be contiguous");
-    typed = &tq;
   }
   if (has_k) {
     const at::Tensor &tk = need(a[2], 3, "k_new must be [T, num_kv_heads, head_dim]"), &tv = need(a[3], -1, ""),
@@ -182,13 +221,17 @@ PyObject* rope_append(PyObject* const* a) {
     if (ts.numel() != n || ts.scalar_type() != at::kLong || !ts.is_contiguous())
       refuse(PyExc_ValueError, "slot_mapping must be contiguous int64, one slot per position");
     caches_check(ck, cv, kind == 0 ? 2 : 1);
+    type.check(tk);
+    type.check(tv);
+    cache_type(ck, kind, type);
     d = to_int(ck.size(3));
-    k = ptr(tk), v = ptr(tv), kc = ptr(ck), vc = ptr(cv);
+    scales_check(a[10], hkv);
+    scales_check(a[11], hkv);
     k_stride = token_stride(tk, "k_new: a token's heads must be contiguous");
     v_stride = token_stride(tv, "v_new: a token's heads must be contiguous");
-    if (!has_q) typed = &tk;
+    k = ptr(tk), v = ptr(tv), kc = ptr(ck), vc = ptr(cv);
   }
-  if (typed == nullptr) refuse(PyExc_ValueError, "q, or k_new and v_new, must be given");
+  if (has_q) q = address(a[1]), q_out = address(a[7]);
   const auto* pos_p = static_cast<const int32_t*>(ptr(pos));
   const auto* slots = static_cast<const int64_t*>(address(a[5]));
   const auto* turns_p = static_cast<const uint64_t*>(ptr(turns));
@@ -196,7 +239,7 @@ PyObject* rope_append(PyObject* const* a) {
   const auto* vs = static_cast<const float*>(address(a[11]));
   const int rot = to_int(2 * turns.numel());
   const float amplitude = number<float>(a[13]);
-  const pkv_dtype dt = dtype_of(*typed, a[14]);
+  const pkv_dtype dt = type.code;
   auto* err = static_cast<int32_t*>(address(a[15]));
   void* s = stream_of(a[16]);
   if (kind == 0)
@@ -221,22 +264,24 @@ PyObject* block_bounds(PyObject* const* a) {
     refuse(PyExc_ValueError, "bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache");
   index_check(tab);
   index_check(len);
-  const int32_t* fresh = nullptr;
   if (a[5] != Py_None) {
     const at::Tensor& t = need(a[5], -1, "");
     index_check(t);
     if (t.numel() != len.numel()) refuse(PyExc_ValueError, "new_lens and context_lens differ in length");
-    fresh = static_cast<const int32_t*>(ptr(t));
   }
   cache_check(kc, kind == 0 ? 2 : 1);
   contiguous(out);
   per_sequence(len.numel(), tab, len);
+  const Type16 type(out, a[7]);
+  cache_type(kc, kind, type);
+  flag_check(a[8]);
+  const auto* fresh = static_cast<const int32_t*>(address(a[5]));
   const auto* tp = static_cast<const int32_t*>(ptr(tab));
   const auto* lp = static_cast<const int32_t*>(ptr(len));
   const int max_new = number<int>(a[6]), b = to_int(len.numel()), hkv = to_int(kc.size(1)), d = to_int(kc.size(3)),
             bs = to_int(kc.size(2)), width = to_int(tab.size(1));
   const int64_t nb = kc.size(0);
-  const pkv_dtype dt = dtype_of(out, a[7]);
+  const pkv_dtype dt = type.code;
   auto* err = static_cast<int32_t*>(address(a[8]));
   void *s = stream_of(a[9]), *k = ptr(kc), *o = ptr(out);
   if (kind == 0)
@@ -268,12 +313,15 @@ PyObject* block_scores(PyObject* const* a) {
   contiguous(lo_hi);
   contiguous(out);
   per_sequence(b, tab, len);
+  const Type16 type(q, a[8]);
+  scales_check(a[7], hkv);
+  flag_check(a[9]);
   const int bi = to_int(b), hq = to_int(q.size(1)), h = to_int(hkv), di = to_int(d), w = to_int(width),
             max_ctx = number<int>(a[6]);
   const int64_t nb = lo_hi.size(0);
   const float scale = number<float>(a[5]);
   const auto* ks = static_cast<const float*>(address(a[7]));
-  const pkv_dtype dt = dtype_of(q, a[8]);
+  const pkv_dtype dt = type.code;
   auto* err = static_cast<int32_t*>(address(a[9]));
   void *s = stream_of(a[10]), *qp = ptr(q), *lp = ptr(lo_hi);
   const auto* tp = static_cast<const int32_t*>(ptr(tab));
@@ -295,6 +343,7 @@ PyObject* select_blocks(PyObject* const* a) {
   contiguous(sc);
   if (sc.scalar_type() != at::kFloat || len.numel() != sc.size(0))
     refuse(PyExc_ValueError, "scores must be fp32, with a context length per sequence");
+  flag_check(a[5]);
   const auto* sp = static_cast<const float*>(ptr(sc));
   const auto* lp = static_cast<const int32_t*>(ptr(len));
   auto* op = static_cast<int32_t*>(ptr(sel));
@@ -312,8 +361,10 @@ struct Attention {
   int b, hq, hkv, d, bs, width;
   int64_t nb;
   size_t ws_bytes;
+  pkv_dtype dtype;
+  // kind as in cache_type; the scales and the flag are only checked here
   Attention(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* tab_, PyObject* len_, PyObject* out_, PyObject* ws_,
-            int64_t itemsize) {
+            int kind, PyObject* dtype_, PyObject* k_scale, PyObject* v_scale, PyObject* flag) {
     const at::Tensor &tq = need(q_, 3, "q must be [batch, num_q_heads, head_dim]"), &kc = need(k_, 4, kCacheDims),
                      &vc = need(v_, -1, ""), &t = need(tab_, 2, kTableDims), &l = need(len_, -1, ""),
                      &o = need(out_, -1, ""), &w = need(ws_, -1, "");
@@ -321,10 +372,18 @@ struct Attention {
     index_check(l);
     contiguous(tq);
     contiguous(o);
-    caches_check(kc, vc, itemsize);
+    caches_check(kc, vc, kind == 0 ? 2 : 1);
     per_sequence(tq.size(0), t, l);
     if (o.sizes() != tq.sizes()) refuse(PyExc_ValueError, "q and out differ in shape");
     if (kc.size(3) != tq.size(2)) refuse(PyExc_ValueError, "q and the caches differ in head_dim");
+    const Type16 type(tq, dtype_);
+    type.check(o);
+    cache_type(kc, kind, type);
+    dtype = type.code;
+    scales_check(k_scale, kc.size(1));
+    scales_check(v_scale, kc.size(1));
+    flag_check(flag);
+    if (!w.is_contiguous()) refuse(PyExc_ValueError, "the workspace must be contiguous");
     q = ptr(tq), k = ptr(kc), v = ptr(vc), out = ptr(o), ws = ptr(w);
     tab = static_cast<const int32_t*>(ptr(t)), len = static_cast<const int32_t*>(ptr(l));
     b = to_int(tq.size(0)), hq = to_int(tq.size(1)), d = to_int(tq.size(2)), width = to_int(t.size(1));
@@ -339,13 +398,13 @@ PyObject* sparse_decode(PyObject* const* a) {
   const int kind = number<int>(a[0]);
   const at::Tensor& sel = need(a[8], 3, "selected must be [batch, num_kv_heads, budget]");
   index_check(sel);
-  const Attention x(a[1], a[2], a[3], a[6], a[7], a[9], a[11], kind == 0 ? 2 : 1);
+  const Attention x(a[1], a[2], a[3], a[6], a[7], a[9], a[11], kind, a[12], a[4], a[5], a[13]);
   if (sel.size(0) != x.b || sel.size(1) != x.hkv)
     refuse(PyExc_ValueError, "selected must be [batch, num_kv_heads, budget]");
   const auto* lists = static_cast<const int32_t*>(ptr(sel));
   const int budget = to_int(sel.size(2));
   const float scale = number<float>(a[10]);
-  const pkv_dtype dt = dtype_of(THPVariable_Unpack(a[1]), a[12]);
+  const pkv_dtype dt = x.dtype;
   const auto* ks = static_cast<const float*>(address(a[4]));
   const auto* vs = static_cast<const float*>(address(a[5]));
   auto* err = static_cast<int32_t*>(address(a[13]));
@@ -370,12 +429,12 @@ PyObject* prefix_decode(PyObject* const* a) {
     refuse(PyExc_ValueError, "group_starts must have one entry more than prefix_lens");
   index_check(starts);
   index_check(pre);
-  const Attention x(a[0], a[1], a[2], a[3], a[4], a[7], a[11], 2);
+  const Attention x(a[0], a[1], a[2], a[3], a[4], a[7], a[11], 0, a[12], Py_None, Py_None, a[13]);
   const auto* sp = static_cast<const int32_t*>(ptr(starts));
   const auto* pp = static_cast<const int32_t*>(ptr(pre));
   const int groups = to_int(pre.numel()), max_ctx = number<int>(a[9]), max_pre = number<int>(a[10]);
   const float scale = number<float>(a[8]);
-  const pkv_dtype dt = dtype_of(THPVariable_Unpack(a[0]), a[12]);
+  const pkv_dtype dt = x.dtype;
   auto* err = static_cast<int32_t*>(address(a[13]));
   void* s = stream_of(a[14]);
   return status([&] {
