@@ -3,8 +3,8 @@
 Argument marshalling only: every function here extracts device pointers,
 sizes and the current CUDA stream from torch tensors and calls the C entry
 point of the same name (declared in include/pkv.h): the per-step calls through
-the module _call (csrc/pycall.cpp, and pytensor.cpp, which takes the tensors
-themselves), the others through ctypes.  All arithmetic runs in the library's
+the modules _call (csrc/pycall.cpp) and _tensor (csrc/pytensor.cpp, which takes
+the tensors themselves), the others through ctypes.  All arithmetic runs in the library's
 CUDA kernels; there is no CPU fallback.  Importing this module fails loudly when
 the library has not been built (``__graft_entry__.build()`` or
 ``python -m paged_kv_cache_153_gb300._build``).
@@ -19,6 +19,8 @@ one entry per KV head, err_flag is int32.
 from __future__ import annotations
 
 import ctypes as C
+import importlib
+import importlib.util
 import os
 
 __all__ = [
@@ -51,9 +53,22 @@ if not os.path.exists(library_path):
     raise ImportError(f"{library_path} is missing: build it with __graft_entry__.build() "
                       "(the CUDA path has no fallback)")
 lib = C.CDLL(library_path)
-import torch  # noqa: E402, F401  (first: _call takes its tensors)
 
 from . import _call  # noqa: E402  (built with the library; finds it next to itself)
+
+
+class _TensorCalls:
+    """Stands for module _tensor until the first of its calls, which imports it
+    with torch (and so takes this object's place); the other calls need no torch."""
+
+    def __getattr__(self, name):
+        import torch  # noqa: F401  (first: _tensor.so uses its libraries)
+        return getattr(importlib.import_module("._tensor", __name__), name)
+
+
+if importlib.util.find_spec("torch") is not None and not os.path.exists(os.path.join(_DIR, "_tensor.so")):
+    raise ImportError("_tensor.so is missing: build it with __graft_entry__.build()")
+_tensor = _TensorCalls()
 
 # The prefill kernel lives in a library of its own (pkv_prefill.h), loaded on
 # first use, so that a process that only decodes never loads it.
@@ -511,7 +526,7 @@ def pkv_rope_append(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_ca
     [T, Hkv, D] to their slots.  q and q_out, or k_new and v_new (with the
     caches and slots), may be None.  The token stride is free; q_out may be q.
     turns, amplitude: from pkv_rope_plan (turns on the device)."""
-    _check("pkv_rope_append", _call.rope_append(
+    _check("pkv_rope_append", _tensor.rope_append(
         0, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, None, None, layout, amplitude,
         dtype, err_flag, stream))
 
@@ -519,7 +534,7 @@ def pkv_rope_append(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_ca
 def pkv_rope_append_fp8(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, *,
                         layout="half", amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
     """pkv_rope_append into an E4M3 cache (uint8 codes, fp32 per-head scales)."""
-    _check("pkv_rope_append_fp8", _call.rope_append(
+    _check("pkv_rope_append_fp8", _tensor.rope_append(
         1, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, layout,
         amplitude, dtype, err_flag, stream))
 
@@ -527,7 +542,7 @@ def pkv_rope_append_fp8(q, k_new, v_new, positions, slot_mapping, turns, q_out, 
 def pkv_rope_append_e5m2(q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale,
                          *, layout="half", amplitude: float = 1.0, dtype=None, err_flag=None, stream=None) -> None:
     """pkv_rope_append into an E5M2 cache (uint8 codes, fp32 per-head scales)."""
-    _check("pkv_rope_append_e5m2", _call.rope_append(
+    _check("pkv_rope_append_e5m2", _tensor.rope_append(
         2, q, k_new, v_new, positions, slot_mapping, turns, q_out, k_cache, v_cache, k_scale, v_scale, layout,
         amplitude, dtype, err_flag, stream))
 
@@ -537,7 +552,7 @@ def pkv_kv_block_bounds(k_cache, block_tables, context_lens, bounds, *, max_new_
     """Elementwise minimum and maximum of the cached keys per (block, KV head),
     into bounds [NB, Hkv, 2, D], for the blocks of each sequence's last
     new_lens tokens (None: its whole context)."""
-    _check("pkv_kv_block_bounds", _call.block_bounds(
+    _check("pkv_kv_block_bounds", _tensor.block_bounds(
         0, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream))
 
 
@@ -545,14 +560,14 @@ def pkv_kv_block_bounds_fp8(k_cache, block_tables, context_lens, bounds, *, max_
                             dtype=None, err_flag=None, stream=None) -> None:
     """pkv_kv_block_bounds over an E4M3 cache: 16-bit bounds of the codes'
     values, before the per-head scale."""
-    _check("pkv_kv_block_bounds_fp8", _call.block_bounds(
+    _check("pkv_kv_block_bounds_fp8", _tensor.block_bounds(
         1, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream))
 
 
 def pkv_kv_block_bounds_e5m2(k_cache, block_tables, context_lens, bounds, *, max_new_len: int, new_lens=None,
                              dtype=None, err_flag=None, stream=None) -> None:
     """pkv_kv_block_bounds over an E5M2 cache."""
-    _check("pkv_kv_block_bounds_e5m2", _call.block_bounds(
+    _check("pkv_kv_block_bounds_e5m2", _tensor.block_bounds(
         2, k_cache, block_tables, context_lens, bounds, new_lens, max_new_len, dtype, err_flag, stream))
 
 
@@ -560,7 +575,7 @@ def pkv_block_scores(q, bounds, block_tables, context_lens, scores, *, scale: fl
                      k_scale=None, dtype=None, err_flag=None, stream=None) -> None:
     """Upper bounds of every block's scaled logits, scores fp32 [B, Hkv,
     max_blocks], from the block bounds [NB, Hkv, 2, D]."""
-    _check("pkv_block_scores", _call.block_scores(
+    _check("pkv_block_scores", _tensor.block_scores(
         q, bounds, block_tables, context_lens, scores, scale, max_context_len, k_scale, dtype, err_flag, stream))
 
 
@@ -568,14 +583,14 @@ def pkv_select_blocks(scores, context_lens, selected, *, num_first: int = 1, num
                       stream=None) -> None:
     """selected int32 [B, Hkv, budget]: the first num_first, the last num_last
     and the highest-scoring other blocks, ascending, -1 behind the list."""
-    _check("pkv_select_blocks", _call.select_blocks(
+    _check("pkv_select_blocks", _tensor.select_blocks(
         scores, context_lens, selected, num_first, num_last, err_flag, stream))
 
 
 def pkv_paged_decode_attention_sparse(q, k_cache, v_cache, block_tables, context_lens, selected, out, *,
                                       scale: float, workspace, dtype=None, err_flag=None, stream=None) -> None:
     """Decode attention over the blocks that selected [B, Hkv, budget] lists."""
-    _check("pkv_paged_decode_attention_sparse", _call.sparse_decode(
+    _check("pkv_paged_decode_attention_sparse", _tensor.sparse_decode(
         0, q, k_cache, v_cache, None, None, block_tables, context_lens, selected, out, scale, workspace,
         dtype, err_flag, stream))
 
@@ -583,7 +598,7 @@ def pkv_paged_decode_attention_sparse(q, k_cache, v_cache, block_tables, context
 def pkv_paged_decode_attention_sparse_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected,
                                           out, *, scale: float, workspace, q_dtype=None, err_flag=None,
                                           stream=None) -> None:
-    _check("pkv_paged_decode_attention_sparse_fp8", _call.sparse_decode(
+    _check("pkv_paged_decode_attention_sparse_fp8", _tensor.sparse_decode(
         1, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, out, scale, workspace,
         q_dtype, err_flag, stream))
 
@@ -591,7 +606,7 @@ def pkv_paged_decode_attention_sparse_fp8(q, k_cache, v_cache, k_scale, v_scale,
 def pkv_paged_decode_attention_sparse_e5m2(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                                            selected, out, *, scale: float, workspace, q_dtype=None, err_flag=None,
                                            stream=None) -> None:
-    _check("pkv_paged_decode_attention_sparse_e5m2", _call.sparse_decode(
+    _check("pkv_paged_decode_attention_sparse_e5m2", _tensor.sparse_decode(
         2, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected, out, scale, workspace,
         q_dtype, err_flag, stream))
 
@@ -611,7 +626,7 @@ def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context
     """Decode attention of sequences that share prefixes: group j, sequences
     group_starts[j] .. group_starts[j + 1] - 1, shares its first
     prefix_lens[j] tokens' whole blocks."""
-    _check("pkv_paged_decode_attention_prefix", _call.prefix_decode(
+    _check("pkv_paged_decode_attention_prefix", _tensor.prefix_decode(
         q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, out, scale, max_context_len,
         max_prefix_len, workspace, dtype, err_flag, stream))
 

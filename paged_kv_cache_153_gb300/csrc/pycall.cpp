@@ -67,10 +67,5 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, methods, 
 }  // namespace
 
 PyMODINIT_FUNC PyInit__call(void) {
-  PyObject* m = PyModule_Create(&module_def);
-  if (m != nullptr && PyModule_AddFunctions(m, pkv_py::tensor_methods) != 0) {
-    Py_DECREF(m);
-    return nullptr;
-  }
-  return m;
+  return PyModule_Create(&module_def);
 }

@@ -1,4 +1,4 @@
-// Shared by the two files of module _call.
+// Shared by the modules _call (pycall.cpp) and _tensor (pytensor.cpp).
 #pragma once
 
 #define PY_SSIZE_T_CLEAN
@@ -45,8 +45,5 @@ bool convert(PyObject* o, T& out) {
     return true;
   }
 }
-
-// the calls that take torch tensors (pytensor.cpp)
-extern PyMethodDef tensor_methods[];
 
 }  // namespace pkv_py

@@ -1,5 +1,5 @@
-// The tensor calls of module _call: the rotary append, the block index, the
-// sparse and the shared-prefix decode, straight from torch tensors.  Each reads
+// Module _tensor: the rotary append, the block index, the sparse and the
+// shared-prefix decode, straight from torch tensors.  Each reads
 // shapes, strides and addresses, refuses what does not fit, and calls the
 // library's entry point; the same steps in Python take 2 to 6 us of a call
 // whose kernels run for 2 to 8 (rope: 8.3 us a call in Python, 2.9 here; sparse
@@ -447,9 +447,7 @@ PyObject* prefix_decode(PyObject* const* a) {
 #define PKV_TENSOR_CALL(f, n) \
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<n, &f>)), METH_FASTCALL, nullptr}
 
-}  // namespace
-
-PyMethodDef tensor_methods[] = {
+PyMethodDef methods[] = {
     PKV_TENSOR_CALL(rope_append, 17),
     PKV_TENSOR_CALL(block_bounds, 10),
     PKV_TENSOR_CALL(block_scores, 11),
@@ -459,4 +457,9 @@ PyMethodDef tensor_methods[] = {
     {nullptr, nullptr, 0, nullptr},
 };
 
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_tensor", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
 }  // namespace pkv_py
+
+PyMODINIT_FUNC PyInit__tensor(void) { return PyModule_Create(&pkv_py::module_def); }
