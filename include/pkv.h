@@ -620,7 +620,9 @@ pkv_status pkv_paged_decode_attention_sparse_e5m2(const void* q, const uint8_t* 
  *   workspace                   at least pkv_prefix_workspace_bytes(...), no
  *                               initialisation needed; not shared by calls
  *                               that run at the same time.
- * 16-bit caches; at most 1024 groups (PKV_ERR_UNSUPPORTED beyond).  Group
+ * 16-bit caches; at most 1024 groups, and a batch whose counts (16 bytes a
+ * sequence) fit one thread block's shared memory, as 10,000 sequences always do
+ * (PKV_ERR_UNSUPPORTED beyond, with nothing launched).  Group
  * starts that are not as described report PKV_ERR_OOB in err_flag, and the
  * outputs are then unspecified.  Other arguments, requirements and errors as
  * in pkv_paged_decode_attention.

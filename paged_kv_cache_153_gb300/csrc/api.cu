@@ -158,6 +158,8 @@ struct RestCall {
   float* ml;
   float* o;
   size_t smem;           // shared memory that the prefix kernel leaves on its SM
+  pkv_status (*before)(void*);   // launches the prefix kernel
+  void* before_arg;
   DecodeParams params;   // out
   int grid;              // out
 };
@@ -273,7 +275,11 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   li.max_ctas_per_sm = std::max(0, std::min(kMaxCtasPerSm, env_int("PKV_CTAS_PER_SM", 0)));
   li.stages = env_int("PKV_STAGES", 0);
   li.part_ranges_cap = w.ranges_cap;
-  li.rest_smem = rest != nullptr ? rest->smem : 0;
+  if (rest != nullptr) {
+    li.rest_smem = rest->smem;
+    li.before = rest->before;
+    li.before_arg = rest->before_arg;
+  }
   const pkv_status st = launch(p, li, static_cast<cudaStream_t>(stream));
   if (rest != nullptr) {
     rest->params = p;
@@ -574,6 +580,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   const int group = num_q_heads / num_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
   if (num_groups > kMaxPrefixGroups) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * num_q_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;   // (the merge's grid)
   if (batch == 0) return PKV_OK;
   if (num_groups == 0 || !q || !k_cache || !v_cache || !block_tables || !context_lens || !group_starts ||
       !prefix_lens || !out || !workspace)
@@ -619,19 +626,22 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   const int ranges = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(1, units * tiles)));
   p.q_tiles = static_cast<int64_t>(batch) * group > 128 ? 2 : 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  pkv_status st = launch_prefix(p, ranges, group, head_dim, dtype, s);
-  if (st != PKV_OK) return st;
+  auto launch_first = [&]() { return launch_prefix(p, ranges, group, head_dim, dtype, s); };
   RestCall rest{};
+  // (a batch whose counts do not fit is refused by the second launch's set-up,
+  // so the first one waits for that)
+  rest.before = [](void* f) { return (*static_cast<decltype(launch_first)*>(f))(); };
+  rest.before_arg = &launch_first;
   rest.group_starts = group_starts;
   rest.prefix_lens = prefix_lens;
   rest.num_groups = num_groups;
   rest.ml = reinterpret_cast<float*>(ws + w.rest_ml);
   rest.o = reinterpret_cast<float*>(ws + w.rest_o);
   rest.smem = kSmemPerSm - 2 * kSmemReservedPerCta - prefix_smem_bytes(head_dim, num_groups);
-  st = decode_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, batch, num_q_heads,
-                     num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len, scale, out,
-                     dtype, 0, ws, w.decode.total, err_flag, stream, nullptr, nullptr, nullptr, 1, 0, nullptr,
-                     false, nullptr, 0, &rest);
+  const pkv_status st = decode_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, batch,
+                                      num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                                      max_context_len, scale, out, dtype, 0, ws, w.decode.total, err_flag, stream,
+                                      nullptr, nullptr, nullptr, 1, 0, nullptr, false, nullptr, 0, &rest);
   if (st != PKV_OK) return st;
   return launch_prefix_merge(p, ranges, rest.params, rest.grid, group, head_dim, dtype, s);
 }
