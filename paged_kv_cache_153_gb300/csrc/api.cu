@@ -31,6 +31,12 @@ bool cuda_failed(cudaError_t e, const char* what) {
   return true;
 }
 
+unsigned long long wait_limit_ns() {
+  const char* v = std::getenv("PKV_WAIT_LIMIT_NS");
+  const long long lim = (v != nullptr && *v != '\0') ? std::atoll(v) : 0;
+  return lim > 0 ? static_cast<unsigned long long>(lim) : kWaitLimitNs;
+}
+
 // cuTensorMapEncodeTiled, looked up once (null, with the reason kept, when it cannot be had)
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static std::once_flag once;
@@ -262,13 +268,7 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   p.slot_capacity = static_cast<int>(w.slots);
   p.wait_first = wait_first ? 1 : 0;
   p.qk_scale_log2 = scale * kLog2e;
-  // limit of each pipeline wait of the decode kernel: 1 s, or (for tests of
-  // the timeout path) PKV_WAIT_LIMIT_NS nanoseconds
-  {
-    const char* v = std::getenv("PKV_WAIT_LIMIT_NS");
-    const long long lim = (v != nullptr && *v != '\0') ? std::atoll(v) : 0;
-    p.wait_limit_ns = lim > 0 ? static_cast<unsigned long long>(lim) : kWaitLimitNs;
-  }
+  p.wait_limit_ns = wait_limit_ns();
 
   LaunchInfo li{};
   li.num_sms = num_sms;
@@ -611,6 +611,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   p.ml = reinterpret_cast<float*>(ws + w.ml);
   p.o = reinterpret_cast<float*>(ws + w.o);
   p.err = err_flag;
+  p.wait_limit_ns = wait_limit_ns();
   p.num_blocks = num_blocks;
   p.batch = batch;
   p.num_groups = num_groups;

@@ -347,6 +347,7 @@ struct ScoreParams {
   const float* k_scale;          // [Hkv], or null
   float* scores;                 // [B, Hkv, max_blocks_per_seq]
   int32_t* err;
+  unsigned long long wait_limit_ns;   // limit of each pipeline wait (flat form)
   int64_t num_blocks;
   int batch, n_q_heads, n_kv_heads, max_blocks_per_seq;
   int max_nblk;                  // ceil(max_context_len / 16), at most max_blocks_per_seq
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
     for (int64_t u = blockIdx.x; ok; u += gridDim.x, ++k) {
       const int s = k % kScoreStages;
       const Next nxt = fetch(u + gridDim.x);
-      ok = k < kScoreStages || mbar_wait(&empty[s], (k / kScoreStages - 1) & 1, p.err);
+      ok = k < kScoreStages || mbar_poll(&empty[s], (k / kScoreStages - 1) & 1, p.err, p.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ScoreUnit d;
@@ -600,12 +601,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
       __syncwarp();
       cur = nxt;
     }
-    if (!ok) {
-      // a wait ran out: let the copies in flight land (bounded) before the block's memory goes
-      const unsigned long long deadline = global_ns() + kWaitLimitNs;
-      for (uint32_t j = k > kScoreStages ? k - kScoreStages : 0; j < k; ++j)
-        mbar_wait_until(&full[j % kScoreStages], (j / kScoreStages) & 1, deadline);
-    }
+    // The last units' copies land before the block's memory goes (bounded, with
+    // the full limit): a consumer's wait for them may have run out.  Unit k is
+    // the end marker, in a stage whose unit before was consumed, or the one
+    // whose stage never came free.
+    const unsigned long long deadline = global_ns() + kWaitLimitNs;
+    for (uint32_t j = k < kScoreStages ? 0 : k - kScoreStages + (ok ? 1 : 0); j < k; ++j)
+      mbar_wait_until(&full[j % kScoreStages], (j / kScoreStages) & 1, deadline);
     return;
   }
   // ---- consumers ----
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) block_scores_flat_kernel(con
   const int r4 = lane >> 2, q4 = lane & 3;
   for (uint32_t k = 0;; ++k) {
     const int s = k % kScoreStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (k / kScoreStages) & 1, p.err))) return;
+    if (!__all_sync(0xffffffffu, mbar_poll(&full[s], (k / kScoreStages) & 1, p.err, p.wait_limit_ns))) return;
     const ScoreUnit& d = units[s];
     const int n = d.n, b = d.b, i0 = d.i0, g0 = d.g0;
     if (n < 0) return;
@@ -1116,6 +1118,7 @@ extern "C" pkv_status pkv_block_scores(const void* q, const void* bounds, const 
   p.k_scale = k_scale;
   p.scores = scores;
   p.err = err_flag;
+  p.wait_limit_ns = wait_limit_ns();
   p.num_blocks = num_blocks;
   p.batch = batch;
   p.n_q_heads = num_q_heads;

@@ -11,6 +11,10 @@
 
 namespace pkv {
 
+// Limit of each pipeline wait of a kernel: kWaitLimitNs (1 s), or (for tests of
+// the timeout paths) PKV_WAIT_LIMIT_NS nanoseconds.
+unsigned long long wait_limit_ns();
+
 // Record a failed CUDA runtime call (name + error) for pkv_last_error() and
 // clear the runtime's last-error state so it cannot leak into a later call.
 // Returns true when `e` is an error.

@@ -91,6 +91,26 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
   return true;
 }
 
+// mbar_wait that polls, for limits below what a try_wait may hold a warp for
+// (microseconds); another path than mbar_wait's only where a test shortens it.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, int32_t* err, unsigned long long limit_ns) {
+  if (limit_ns >= kWaitLimitNs) return mbar_wait(bar, parity, err, limit_ns);
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (global_ns() - t0 > limit_ns) {
+      record_error(err, PKV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // L2 policy for data read exactly once (private KV blocks)
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;

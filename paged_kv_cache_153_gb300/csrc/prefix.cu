@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       int mine = 0;                                              // operations of this chain in this piece
       const int step = sg.share ? 1 : 2;
       for (int n = sg.share ? 0 : chain; n < n_tiles && ok; n += step, ++mine, ++ops) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[chain], ops & 1, p.err) && !*abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[chain], ops & 1, p.err, p.wait_limit_ns) && !*abort_flag);
         if (!ok) break;
         tc_fence_after();
         // keys of the tile that the prefix holds (whole blocks; the last tile may be short)
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         }
         if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // (the chain's previous P V has completed: these scores were asked for behind it)
-          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
+          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err, p.wait_limit_ns));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         mbar_arrive(&p_full[chain]);
       }
       // the piece's states, once the last P V is done
-      if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err));
+      if (ok && mine > 0)
+        ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[chain], (ops - 1) & 1, p.err, p.wait_limit_ns));
       if (!ok) *abort_flag = 1;
       if (!sg.share) {
         red[chain * kXRows + r] = make_float2(m_ref, l_run);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       waited = true;
       // Q of the piece, once every Q K^T of the one before has read its tiles
       if (tiles > 0) {
-        good = __all_sync(0xffffffffu, mbar_wait(k_empty, (tiles - 1) & 1, p.err) && !*abort_flag);
+        good = __all_sync(0xffffffffu, mbar_wait(k_empty, (tiles - 1) & 1, p.err, p.wait_limit_ns) && !*abort_flag);
         if (!good) break;
       }
       if (lane == 0) mbar_arrive_expect_tx(q_full, L::kQTile * (sg.share ? 2 : 1));
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         const uint32_t shift = is_v ? v_shift : 0, s = tiles & ((1u << shift) - 1), use = tiles >> shift;
         uint64_t* full = is_v ? &v_full[s] : k_full;
         uint64_t* empty = is_v ? &v_empty[s] : k_empty;
-        const bool freed = use == 0 || mbar_wait(empty, (use - 1) & 1, p.err);
+        const bool freed = use == 0 || mbar_wait(empty, (use - 1) & 1, p.err, p.wait_limit_ns);
         if (!__all_sync(0xffffffffu, freed && !*abort_flag)) return false;
         if (lane == 0) mbar_arrive_expect_tx(full, L::kKVTile);
         __syncwarp();
@@ -503,8 +504,10 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     }
     if (!waited) pdl_wait_and_release();
     if (!good) *abort_flag = 1;
-    if (*abort_flag && lane == 0) {
-      // loads this warp issued that nobody may have waited for (bounded)
+    if (lane == 0) {
+      // The last loads of Q, K and every V stage land before the block ends
+      // (bounded, with the full limit): whoever should wait for them may have
+      // stopped, now or after this.
       const unsigned long long deadline = global_ns() + kWaitLimitNs;
       if (issued_q > 0) mbar_wait_until(q_full, (issued_q - 1) & 1, deadline);
       if (issued_k > 0) mbar_wait_until(k_full, (issued_k - 1) & 1, deadline);
@@ -529,15 +532,15 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         pos = sg.next;
         const int n_tiles = sg.t1 - sg.t0;
         const int n_ops = sg.share ? 2 * n_tiles : n_tiles;
-        if (qk_warp) ok = mbar_wait(q_full, piece & 1, p.err);
+        if (qk_warp) ok = mbar_wait(q_full, piece & 1, p.err, p.wait_limit_ns);
         for (int k = 0; k < n_ops && ok; ++k) {
           const uint32_t t = tile0 + (sg.share ? k >> 1 : k);
           const int c = k & 1;
           const bool last_use = !sg.share || c == 1;   // of the tile
           if (qk_warp) {
             // S of the chain once the P V that read P from its columns is done
-            ok = mbar_wait(k_full, t & 1, p.err) &&
-                 (count[c] == 0 || mbar_wait(&pv_done[c], (count[c] - 1) & 1, p.err)) && !*abort_flag;
+            ok = mbar_wait(k_full, t & 1, p.err, p.wait_limit_ns) &&
+                 (count[c] == 0 || mbar_wait(&pv_done[c], (count[c] - 1) & 1, p.err, p.wait_limit_ns)) && !*abort_flag;
             if (!ok) break;
             ++count[c];
             const uint64_t a0 = umma_desc(smem_u32(q_sm + (sg.share ? c * L::kQTile : 0)), 16, 1024);
@@ -551,8 +554,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
             if (last_use) umma_commit(k_empty);
           } else {
             const uint32_t s = t & ((1u << v_shift) - 1);
-            ok = mbar_wait(&v_full[s], (t >> v_shift) & 1, p.err) && mbar_wait(&p_full[c], count[c] & 1, p.err) &&
-                 !*abort_flag;
+            ok = mbar_wait(&v_full[s], (t >> v_shift) & 1, p.err, p.wait_limit_ns) &&
+                 mbar_wait(&p_full[c], count[c] & 1, p.err, p.wait_limit_ns) && !*abort_flag;
             if (!ok) break;
             ++count[c];
             tc_fence_after();

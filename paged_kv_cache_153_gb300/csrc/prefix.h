@@ -32,6 +32,7 @@ struct PrefixParams {
   float* ml;                     // workspace: [rows, 2] (m, l) and
   float* o;                      // [rows, D] o of the pieces
   int32_t* err;
+  unsigned long long wait_limit_ns;   // limit of each pipeline wait
   int64_t num_blocks;
   int batch, num_groups, n_q_heads, n_kv_heads, max_blocks_per_seq;
   int max_nblk;                  // ceil(max_context_len / 16)
