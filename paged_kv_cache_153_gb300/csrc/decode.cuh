@@ -890,6 +890,9 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
   }
 
   // ========================== consumer warps ===============================
+  // (kListed: the producer loads nothing before its own wait for the previous
+  // kernel, so the limits of the waits for it count from that wait's end)
+  if constexpr (SRC == kListed) pdl_wait();
   constexpr int LPT = T::kLPT, TPG = T::kTPG, NF = T::kNF;
   const int li = lane & (LPT - 1);       // CUDA-core: owns elements [8 li, 8 li + 8) of a row
   const int tg = lane / LPT;             // CUDA-core: token group

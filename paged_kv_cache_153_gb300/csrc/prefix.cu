@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     constexpr uint32_t kIdQK = umma_idesc<QT>(false, kXKeys), kIdPV = umma_idesc<QT>(true, D);
     const bool qk_warp = (warp == 9);
     bool ok = true;
+    pdl_wait();   // (the producer loads nothing before: the limits of the waits for it count from here)
     if (lane == 0) {
       uint32_t tile0 = 0, piece = 0;       // K / V tiles and pieces before the current piece
       uint32_t count[2] = {0, 0};          // this issuer's operations of each chain so far
