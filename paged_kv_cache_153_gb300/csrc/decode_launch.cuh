@@ -18,8 +18,7 @@ struct LaunchInfo {
   int grid;                // out: decode grid used
   int64_t part_ranges_cap; // partition mode: max ranges the workspace holds
   size_t rest_smem;        // kRest: shared memory for one block, beside the shared-prefix kernel's
-  pkv_status (*before)(void*);   // kRest: launches that kernel, once nothing can refuse this one any more
-  void* before_arg;
+  bool check_only;         // kRest: whether the launch would be refused, and nothing else
 };
 
 using DecodeLauncher = pkv_status (*)(DecodeParams&, LaunchInfo&, cudaStream_t);
@@ -134,6 +133,7 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
   if (!occupancy(smem, &occ)) return PKV_ERR_CUDA;
   lock.unlock();
   if (occ < 1) return PKV_ERR_UNSUPPORTED;
+  if (SRC == kRest && li.check_only) return PKV_OK;
   occ = std::min(occ, want);
   int grid = li.num_sms * occ;
   if (p.part_blocks > 0 && li.part_ranges_cap < grid) grid = static_cast<int>(li.part_ranges_cap);
@@ -166,10 +166,6 @@ pkv_status launch_decode_variant(DecodeParams& p, LaunchInfo& li, cudaStream_t s
     if (!encode_cache_tmap(&p.tmap_k, p.k_cache, rows, D, Tr::kEsz) ||
         !encode_cache_tmap(&p.tmap_v, p.v_cache, rows, D, Tr::kEsz))
       return PKV_ERR_CUDA;
-  }
-  if constexpr (SRC == kRest) {
-    const pkv_status st = li.before(li.before_arg);
-    if (st != PKV_OK) return st;
   }
   if (cuda_failed(launch_pdl(kern, dim3(grid), dim3(Tr::kThreads), smem, stream, p), "paged_decode_kernel launch"))
     return PKV_ERR_CUDA;

@@ -207,6 +207,23 @@ __device__ __forceinline__ void pdl_wait_and_release() {
   pdl_release();
 }
 
+// mbar_wait for what another warp does only once the previous kernel is over: a
+// limit that runs out while that kernel runs starts anew at its end.  (The rare
+// part is a call: in line it made loops around such waits slower.)
+inline __device__ __noinline__ bool mbar_wait_from_previous_end(uint64_t* bar, uint32_t parity, int32_t* err,
+                                                                unsigned long long limit_ns) {
+  pdl_wait();
+  return mbar_wait(bar, parity, err, limit_ns);
+}
+__device__ __forceinline__ bool mbar_wait_started_early(uint64_t* bar, uint32_t parity, int32_t* err,
+                                                        unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_ns() - t0 > limit_ns) return mbar_wait_from_previous_end(bar, parity, err, limit_ns);
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // element conversions
 // ---------------------------------------------------------------------------

@@ -524,7 +524,6 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     constexpr uint32_t kIdQK = umma_idesc<QT>(false, kXKeys), kIdPV = umma_idesc<QT>(true, D);
     const bool qk_warp = (warp == 9);
     bool ok = true;
-    pdl_wait();   // (the producer loads nothing before: the limits of the waits for it count from here)
     if (lane == 0) {
       uint32_t tile0 = 0, piece = 0;       // K / V tiles and pieces before the current piece
       uint32_t count[2] = {0, 0};          // this issuer's operations of each chain so far
@@ -533,7 +532,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         pos = sg.next;
         const int n_tiles = sg.t1 - sg.t0;
         const int n_ops = sg.share ? 2 * n_tiles : n_tiles;
-        if (qk_warp) ok = mbar_wait(q_full, piece & 1, p.err, p.wait_limit_ns);
+        // (the producer loads nothing while the previous kernel runs)
+        if (qk_warp) ok = mbar_wait_started_early(q_full, piece & 1, p.err, p.wait_limit_ns);
         for (int k = 0; k < n_ops && ok; ++k) {
           const uint32_t t = tile0 + (sg.share ? k >> 1 : k);
           const int c = k & 1;
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
             if (last_use) umma_commit(k_empty);
           } else {
             const uint32_t s = t & ((1u << v_shift) - 1);
-            ok = mbar_wait(&v_full[s], (t >> v_shift) & 1, p.err, p.wait_limit_ns) &&
+            ok = mbar_wait_started_early(&v_full[s], (t >> v_shift) & 1, p.err, p.wait_limit_ns) &&
                  mbar_wait(&p_full[c], count[c] & 1, p.err, p.wait_limit_ns) && !*abort_flag;
             if (!ok) break;
             ++count[c];
@@ -800,28 +800,31 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 namespace {
 
 template <typename QT, int D, int G>
-pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t stream) {
+pkv_status prepare_prefix_variant() {
   auto kern = prefix_kernel<QT, D, G>;
   int dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   if (dev < 0 || dev >= kMaxDevices) return PKV_ERR_UNSUPPORTED;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!done[dev]) {
-      if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(PrefixSmem<D>::bytes(kMaxPrefixGroups))),
-                      "cudaFuncSetAttribute") ||
-          // (the SM's whole shared memory, so that what this kernel leaves is the next one's)
-          cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                           cudaSharedmemCarveoutMaxShared),
-                      "cudaFuncSetAttribute"))
-        return PKV_ERR_CUDA;
-      done[dev] = true;
-    }
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev]) {
+    if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(PrefixSmem<D>::bytes(kMaxPrefixGroups))),
+                    "cudaFuncSetAttribute") ||
+        // (the SM's whole shared memory, so that what this kernel leaves is the next one's)
+        cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared),
+                    "cudaFuncSetAttribute"))
+      return PKV_ERR_CUDA;
+    done[dev] = true;
   }
-  return cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(kXThreads),
+  return PKV_OK;
+}
+
+template <typename QT, int D, int G>
+pkv_status launch_prefix_variant(PrefixParams& p, int ranges, cudaStream_t stream) {
+  return cuda_failed(launch_pdl(prefix_kernel<QT, D, G>, dim3(static_cast<unsigned>(ranges)), dim3(kXThreads),
                                 PrefixSmem<D>::bytes(p.num_groups), stream, p),
                      "prefix_kernel launch")
              ? PKV_ERR_CUDA
@@ -864,6 +867,12 @@ pkv_status dispatch(pkv_dtype dtype, int head_dim, int group, F&& f) {
 
 size_t prefix_smem_bytes(int head_dim, int num_groups) {
   return head_dim == 64 ? PrefixSmem<64>::bytes(num_groups) : PrefixSmem<128>::bytes(num_groups);
+}
+
+pkv_status prepare_prefix(int group, int head_dim, pkv_dtype dtype) {
+  return dispatch(dtype, head_dim, group, [](auto qt, auto d, auto g) {
+    return prepare_prefix_variant<decltype(qt), decltype(d)::value, decltype(g)::value>();
+  });
 }
 
 pkv_status launch_prefix(PrefixParams& p, int ranges, int group, int head_dim, pkv_dtype dtype, cudaStream_t stream) {

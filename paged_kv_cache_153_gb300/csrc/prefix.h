@@ -51,6 +51,8 @@ __host__ __device__ inline int64_t piece_row(int64_t group_start, int n_q_heads,
 
 // dynamic shared memory of the prefix kernel
 size_t prefix_smem_bytes(int head_dim, int num_groups);
+// the prefix kernel's attributes on the current device, once for each device
+pkv_status prepare_prefix(int group, int head_dim, pkv_dtype dtype);
 // ranges: the grid of the prefix kernel
 pkv_status launch_prefix(PrefixParams& p, int ranges, int group, int head_dim, pkv_dtype dtype, cudaStream_t stream);
 pkv_status launch_prefix_merge(const PrefixParams& p, int ranges, const DecodeParams& rest, int rest_grid, int group,
