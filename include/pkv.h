@@ -620,6 +620,9 @@ pkv_status pkv_paged_decode_attention_sparse_e5m2(const void* q, const uint8_t* 
  *   workspace                   at least pkv_prefix_workspace_bytes(...), no
  *                               initialisation needed; not shared by calls
  *                               that run at the same time.
+ * The weights are multiplied in 16 bits as there, fp16 ones rounded once (and
+ * the normaliser sums the rounded ones); bf16 ones, and fp16 ones with one query
+ * head per KV head, as two parts (exact to 2^-16).
  * 16-bit caches; at most 1024 groups, and a batch whose counts (16 bytes a
  * sequence) fit one thread block's shared memory, as 10,000 sequences always do
  * (PKV_ERR_UNSUPPORTED beyond, with nothing launched).  Group

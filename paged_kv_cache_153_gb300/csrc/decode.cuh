@@ -1069,7 +1069,9 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
         // of p (2^-9 relative) can exceed the 2e-3 tolerance on outputs of a
         // few keys, so bf16 p is multiplied as hi = bf16(p) plus
         // lo = bf16(p - hi) (exact to ~2^-17); fp16 p (2^-12) is used as is.
-        constexpr bool kSplitP = std::is_same<MT, BF16>::value;
+        // (kRest with one query head per KV head, where the dense decode keeps p
+        // in fp32: fp16 p in two parts as well)
+        constexpr bool kSplitP = std::is_same<MT, BF16>::value || (SRC == kRest && G == 1);
         const float e00 = exp2f(s00 - ref0), e01 = exp2f(s01 - ref1);
         const float e10 = exp2f(s10 - ref0), e11 = exp2f(s11 - ref1);
         // (INT8: the MMA multiplies the codes by p dv; the v_min sum(p) part is kept apart)

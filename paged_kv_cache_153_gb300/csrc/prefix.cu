@@ -34,7 +34,11 @@
 // pairs, and for bf16 16 more of the remainder); the product reads it from
 // there.  bf16 P is multiplied as two bf16 parts (p truncated, and the rounded
 // remainder: exact to 2^-16), because one bf16 rounding of p (2^-9) would be as
-// large as the output's own; fp16 P (2^-12) is used as it is.  The row
+// large as the output's own.  fp16 P (2^-12) is rounded once, and l sums the
+// rounded values, as in the dense decode; with one query head per KV head, where
+// the dense decode keeps p in fp32, it is two fp16 parts.  (64 sequences behind
+// 32768 tokens in fp16, 32 query and 8 KV heads: 58.4 us, 56.6 with l of the
+// unrounded p; 8 and 8 heads 51.5 us, 49.8 with one part.)  The row
 // reference m moves only when a tile's maximum exceeds it by more than 2^8.
 // 64-key tiles with two score buffers per chain, which hide the softmax's
 // latency entirely, were slower (67 us against 54 alone on 64 sequences behind
@@ -179,7 +183,8 @@ __device__ __forceinline__ PrefixSeg prefix_segment(const PrefixGroup* groups, i
 template <typename QT, int D, int G>
 __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = PrefixSmem<D>;
-  constexpr bool kSplit = std::is_same<QT, BF16>::value;
+  // (the dense decode keeps p in fp32 where a KV head has one query head)
+  constexpr bool kSplit = std::is_same<QT, BF16>::value || G == 1;
   extern __shared__ unsigned char xsm_raw[];
   unsigned char* sm = xsm_raw + ((1024 - (smem_u32(xsm_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
@@ -358,9 +363,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
             for (int i = 0; i < 32; i += 2) {
               const float2 e2 = f32x2_split(fma_f32x2(f32x2(v[32 * c + i], v[32 * c + i + 1]), scale2, nref2));
               const float e0 = ex2_approx(e2.x), e1 = ex2_approx(e2.y);
-              const uint64_t e01 = f32x2(e0, e1);
-              acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
-              if constexpr (kSplit) {
+              uint64_t e01 = f32x2(e0, e1);
+              if constexpr (std::is_same<QT, BF16>::value) {
                 const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
                 pk[i / 2] = __byte_perm(b0, b1, 0x7632);
                 const float2 lo = f32x2_split(
@@ -368,7 +372,14 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                 pk[16 + i / 2] = pack2(lo.x, lo.y, QT{});
               } else {
                 pk[i / 2] = pack2(e0, e1, QT{});
+                const float2 hi = unpack2(pk[i / 2], QT{});
+                if constexpr (kSplit) {
+                  pk[16 + i / 2] = pack2(e0 - hi.x, e1 - hi.y, QT{});
+                } else {
+                  e01 = f32x2(hi.x, hi.y);   // (l sums what is multiplied)
+                }
               }
+              acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
             }
             if constexpr (kSplit)
               tmem_st32u(t_s + 64 * half + 32 * c, pk);
