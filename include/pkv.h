@@ -522,8 +522,8 @@ pkv_status pkv_rope_append_e5m2(const void* q, int64_t q_stride, const void* k_n
  * every sequence that hold its last new_lens[b] tokens: the new ones after an
  * append, whose first block may have held older rows as well.  new_lens NULL:
  * all blocks of the context.  max_new_len: an upper bound of new_lens (of
- * context_lens when NULL); it sizes the launch, and blocks past it are left
- * as they are and reported as PKV_ERR_OOB.  _fp8 / _e5m2: over codes; the
+ * context_lens when NULL); it sizes the launch (0: nothing is done), and blocks
+ * past it are left as they are and reported as PKV_ERR_OOB.  _fp8 / _e5m2: over codes; the
  * bounds are the codes' values, before the per-head scale, in bounds_dtype
  * (exact in both).  A block that two sequences share must hold the same rows
  * for both (full, or equal lengths).  Bounds of other blocks stay.

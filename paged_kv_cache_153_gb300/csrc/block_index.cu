@@ -17,7 +17,8 @@
 // All three are bound by memory (or by latency, for a few sequences): a key
 // slab, a bounds row and a score are each read once.  Early start, as in the
 // decode kernel: before they wait for the previous kernel they read lengths,
-// tables and (bounds) the cache, which no kernel that releases early writes.
+// tables and (bounds) the cache, which no kernel that releases early writes
+// after its release (a fused step releases once its new rows are fenced).
 // They let the next kernel launch as soon as their own wait is over: what they
 // write (bounds, scores, lists) no kernel of this library reads before its own.
 #include <cuda_runtime.h>

@@ -477,7 +477,14 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
   // it loads such a block, and the consumers before their first write --
   // wait_first).  Every global write (the new rows, slots,
   // outputs, partials, prefixes) is made by the consumer warps after their
-  // wait for the previous kernel.
+  // wait for the previous kernel.  Two exceptions:
+  //   kListed  the lists may be the previous kernel's, which releases early: the
+  //            producer waits for it before it reads them;
+  //   kRest    the previous kernel is the shared-prefix kernel, which releases
+  //            this one only once everything before it has completed, and which
+  //            neither reads nor writes what this one writes.  So this one
+  //            writes without a wait, and waits at its end (so that the merge,
+  //            which waits for this grid alone, comes after both).
   //   When the combine is released.  With combine_early = 0 the combine
   // releases its own successor only after its wait, and this kernel releases
   // the combine at once.  With combine_early = 1 the combine releases the

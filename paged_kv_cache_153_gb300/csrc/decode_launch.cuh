@@ -206,7 +206,9 @@ constexpr int kRestWarps = 4;   // and of kRest, which shares its SM with the pr
 // G = 1 uses the CUDA-core consumer; G >= 2 over a 16-bit cache, or over a
 // one-byte (E4M3, E5M2 or INT8) cache with 128-byte rows, uses the tensor-core
 // consumer (the q-group times a 16-token block is an MMA tile), and so does
-// an INT8 cache with 128-byte rows at G = 1.
+// an INT8 cache with 128-byte rows at G = 1.  kRest uses the tensor-core one for
+// every G: its five warps fit beside the prefix kernel's, the CUDA-core one's nine
+// do not.
 template <typename QT, typename KV, int D, int G, Source SRC>
 DecodeLauncher pick_variant() {
   // (an INT8 cache with 128-byte rows takes the tensor-core consumer for every

@@ -197,8 +197,9 @@ __device__ __forceinline__ bool mbar_wait_until(uint64_t* bar, uint32_t parity, 
 // predecessor may read or write, and lets its own successor start launching
 // once that is safe (pdl_release).  A kernel that writes the KV cache, the
 // block tables or the lengths releases its successor only after those writes
-// are fenced (or not at all: then at its completion), so a decode kernel may
-// read those inputs before its own wait.
+// are fenced (or not at all: then at its completion), so a decode or block
+// index kernel may read those inputs before its own wait.  What other kernels
+// write (outputs, scores, bounds, lists, workspaces) is read after it.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
