@@ -94,8 +94,8 @@ struct RowChunk {
 //                 takes an equal run of consecutive units.
 // Flat is taken when the launch by sequence would be more than kFlatWaves
 // times the resident warps.  On GB300: bounds of 32 contexts of 2048..32768
-// tokens (E4M3, 389 MB) 60.6 us flat, 111 by sequence; scores of 64 contexts of
-// 1024..32768 (141 MB) 26.1 against 27.6, but with two of 131072 among 62 of
+// tokens (E4M3, 389 MB) 60.3 us flat, 111 by sequence; scores of 64 contexts of
+// 1024..32768 (141 MB) 26.2 against 27.6, but with two of 131072 among 62 of
 // 1000 (83 MB) 16.0 against 70.4; one step's bounds of 64 sequences stay by
 // sequence (1.8 us).
 // ---------------------------------------------------------------------------
@@ -675,7 +675,7 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 //      of the K-th highest candidate.  The candidates from it on, seldom many
 //      more than K, are listed in order (of up to 8192), and if there are at
 //      most 256 of them, each is ranked among them and the K highest are the
-//      answer (11.3 to 10.4 us in the batch below);
+//      answer (11.3 to 10.3 us in the batch below);
 //   else, among what is left:
 //   3. 2048 bins over the bracket; the bin of the K-th highest candidate
 //      becomes the bracket, until it holds at most 64 (or one key only);
@@ -684,8 +684,9 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 //      the index is found by counting them in order);
 //   5. what lies above the threshold becomes a bit per candidate; a scan over
 //      the words' bit counts gives each word its place in the list.
-// Bound by instructions and barriers, not by the 5.6 MB of scores: 512 pairs of
-// 512 to 8192 blocks take 10.4 us (by steps 3 to 5 alone, before step 2: 14.1 with
+// Bound by instructions and barriers, not by the 5.6 MB of scores, and by a second
+// wave (at 40 registers, 456 thread blocks fit the GPU): 512 pairs of
+// 512 to 8192 blocks take 10.3 us (by steps 3 to 5 alone, before step 2: 14.1 with
 // the keys in registers and every pass unrolled, which missed the instruction
 // cache; 15.3 reading the scores again in each pass; 18 with 256 threads or 1024).
 constexpr int kSelThreads = 512;
