@@ -53,10 +53,10 @@
 // two more; about 94 KiB of shared memory) for one thread block of five warps of
 // the decode over the sequences' own blocks, which is bound by memory where this
 // one is bound by the tensor cores; that kernel launches as soon as the wait for
-// the previous one is over.  64 sequences of 16 to 2048 tokens behind 32768: 63.4 us
-// (on another box 61.8, against 63.8 without the early start; 66.1 also with two stages of V, which leave the
-// other block three consumer warps of two stages each instead of four; 103 where
-// the two do not fit an SM together).
+// the previous one is over.  64 sequences of 16 to 2048 tokens behind 32768:
+// 63.4 us.  (On another GPU 61.8, against 63.8 without the early start; 66.1 also
+// with two stages of V, which leave the other block three consumer warps of two
+// stages each instead of four; 103 where the two do not fit an SM together.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
