@@ -523,10 +523,10 @@ pkv_status pkv_rope_append_e5m2(const void* q, int64_t q_stride, const void* k_n
  * append, whose first block may have held older rows as well.  new_lens NULL:
  * all blocks of the context.  max_new_len: an upper bound of new_lens (of
  * context_lens when NULL); it sizes the launch (0: nothing is done), and blocks
- * past it are left as they are and reported as PKV_ERR_OOB.  _fp8 / _e5m2: over codes; the
- * bounds are the codes' values, before the per-head scale, in bounds_dtype
- * (exact in both).  A block that two sequences share must hold the same rows
- * for both (full, or equal lengths).  Bounds of other blocks stay.
+ * past it are left as they are and reported as PKV_ERR_OOB.  _fp8 / _e5m2: over
+ * codes; the bounds are the codes' values, before the per-head scale, in
+ * bounds_dtype (exact in both).  A block that two sequences share must hold the
+ * same rows for both (full, or equal lengths).  Bounds of other blocks stay.
  *
  * pkv_block_scores: for i < ceil(context_lens[b] / 16), with (lo, hi) the
  * bounds of block_tables[b][i],
