@@ -642,6 +642,143 @@ pkv_status pkv_paged_decode_attention_prefix(const void* q, const void* k_cache,
                                              size_t workspace_bytes, int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Decode attention to the first num_sinks and the last `window` tokens of each
+ * context: pkv_paged_decode_attention with token j of n = context_lens[b] seen
+ * only where j < num_sinks or j >= n - window (so a window of at least n is the
+ * dense decode).  Blocks that hold no such token are not looked up and not
+ * read: their table entries may be anything and their memory may have been
+ * given back.  K and V rows that are not seen may hold anything.
+ *   window      >= 1; num_sinks >= 0 (else PKV_ERR_INVALID_ARG).
+ *   workspace   at least pkv_decode_workspace_bytes(batch, num_q_heads,
+ *               num_kv_heads, head_dim, max_blocks_per_seq, window + num_sinks,
+ *               0).
+ * Other arguments, requirements and errors as in pkv_paged_decode_attention and
+ * its FP8 forms (a context longer than the table is cut to it and reported).
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_paged_decode_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens, int batch,
+                                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                             int max_blocks_per_seq, int64_t num_blocks, int window, int num_sinks,
+                                             float scale, void* out, pkv_dtype dtype, void* workspace,
+                                             size_t workspace_bytes, int32_t* err_flag, void* stream);
+pkv_status pkv_paged_decode_attention_window_fp8(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                                 const float* k_scale, const float* v_scale,
+                                                 const int32_t* block_tables, const int32_t* context_lens, int batch,
+                                                 int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                                 int max_blocks_per_seq, int64_t num_blocks, int window,
+                                                 int num_sinks, float scale, void* out, pkv_dtype q_dtype,
+                                                 void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                                 void* stream);
+pkv_status pkv_paged_decode_attention_window_e5m2(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                                  const float* k_scale, const float* v_scale,
+                                                  const int32_t* block_tables, const int32_t* context_lens, int batch,
+                                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                                  int max_blocks_per_seq, int64_t num_blocks, int window,
+                                                  int num_sinks, float scale, void* out, pkv_dtype q_dtype,
+                                                  void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                                  void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted tokens: one pass over several candidate continuations of each
+ * sequence, and the move of the accepted ones.  The n_b = cu_nodes[b + 1] -
+ * cu_nodes[b] drafted tokens of sequence b (tokens cu_nodes[b] .. cu_nodes[b + 1]
+ * - 1 of a batch's num_tokens) are its last n_b cached ones: context_lens[b]
+ * counts them, and token i of them is cached at position base + i, base =
+ * context_lens[b] - n_b.  cu_nodes: device int32 [batch + 1], cu_nodes[0] >= 0,
+ * cu_nodes[batch] <= num_tokens; a sequence may have none.  What belongs to
+ * tokens behind the last sequence is neither read nor written.
+ *
+ * pkv_tree_plan: the tokens of a sequence form a tree whose root is the
+ * context's last token: parents[t] (device int32 [num_tokens]) is the index of
+ * token t's parent within its sequence, before its own (-1: the root).  With a
+ * token's ancestors in the tree,
+ *     tree_mask[t]     bit j of word j / 64: token j of the sequence is t itself
+ *                      or an ancestor of it ([num_tokens, mask_words] uint64;
+ *                      mask_words <= 4, else PKV_ERR_UNSUPPORTED)
+ *     positions[t]     base + the number of its ancestors (int32; its rotary
+ *                      position; NULL: not wanted)
+ *     slot_mapping[t]  the slot of position base + i, as pkv_slot_mapping (int64;
+ *                      NULL: not wanted, and block_tables is not used)
+ * Device errors (PKV_ERR_OOB): offsets that are not as described (the sequence
+ * is skipped); more tokens than 64 mask_words or than the context has (mask 0,
+ * position and slot -1); a parent that is not before its token (taken as -1); a
+ * table entry outside the pool (slot -1).
+ *
+ * pkv_paged_tree_attention[_fp8 / _e5m2]: token i of sequence b sees the base
+ * tokens before the drafted ones and the drafted tokens j with bit j of its row
+ * of tree_mask set -- any set of them, ancestors or not, itself or not; bits from
+ * n_b on are not used:
+ *     out[t, h] = sum_j softmax_j(scale <q[t, h], K_j>) V_j over those j
+ * (0 where it sees none).  K and V rows of the drafted tokens are read from the
+ * cache like the others.  A drafted token's K and V change nothing for the rows
+ * that do not see it, whatever bits they hold; an element of V that is not finite
+ * gives an output that is not finite where it is seen.
+ *   q, out               [num_tokens, num_q_heads, head_dim].
+ *   max_nodes            an upper bound of n_b, at most 64 mask_words.
+ *   max_context_len      an upper bound of context_lens; it sizes the launch only.
+ *   scale                > 0.
+ *   workspace            at least pkv_tree_workspace_bytes(...), no
+ *                        initialisation needed; not shared by calls that run at
+ *                        the same time.
+ * Weights are multiplied in 16 bits: over fp16 and FP8 caches as fp16 rounded
+ * once (and the normaliser sums the rounded ones), over bf16 caches as two parts
+ * (exact to 2^-16).  q meets an FP8 cache in fp16 (exact in its normal range; |q|
+ * at most 65504).  At most 1024 sequences, num_blocks * num_kv_heads < 2^30
+ * (PKV_ERR_UNSUPPORTED beyond).  Device errors (PKV_ERR_OOB; the sequence is
+ * skipped, its outputs stay as they are): offsets that are not as described, more
+ * tokens than max_nodes or than the context has, a context longer than its table.
+ * A table entry outside the pool reads as zeros and is reported.  Other arguments
+ * and requirements as in pkv_paged_decode_attention and its FP8 forms.
+ *
+ * pkv_tree_commit: the drafted tokens that were accepted become the context's
+ * next ones.  accepted[b] (device int32 [batch, max_accept], max_accept <= 1024)
+ * lists them, strictly ascending indices within the sequence, up to its first
+ * negative entry; K and V of the k-th of them move from position base +
+ * accepted[b][k] to base + k, in every head (bit for bit, any type of elt_bytes 1
+ * or 2; a layer-major cache [num_blocks, num_layers, H_kv, 16, head_dim] is passed
+ * with num_kv_heads = num_layers * H_kv).  Other rows stay as they are.  new_lens
+ * (device int32 [batch], nullable; not context_lens itself: PKV_ERR_INVALID_ARG)
+ * takes base + the number of accepted tokens.  The blocks from position base on
+ * belong to the sequence alone.  Device errors (PKV_ERR_OOB; nothing of the
+ * sequence moves and new_lens[b] stays): a list that does not ascend or passes
+ * the sequence's tokens, offsets or lengths that are not as described, a table
+ * entry outside the pool where a row comes from or goes to.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_tree_plan(const int32_t* parents, const int32_t* cu_nodes, const int32_t* block_tables,
+                         const int32_t* context_lens, int batch, int64_t num_tokens, int mask_words, int block_size,
+                         int max_blocks_per_seq, int64_t num_blocks, uint64_t* tree_mask, int32_t* positions,
+                         int64_t* slot_mapping, int32_t* err_flag, void* stream);
+size_t pkv_tree_workspace_bytes(int batch, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                int max_nodes);
+pkv_status pkv_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens, const int32_t* cu_nodes,
+                                    const uint64_t* tree_mask, int mask_words, int max_nodes, int64_t num_tokens,
+                                    int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, int64_t num_blocks, int max_context_len, float scale,
+                                    void* out, pkv_dtype dtype, void* workspace, size_t workspace_bytes,
+                                    int32_t* err_flag, void* stream);
+pkv_status pkv_paged_tree_attention_fp8(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                        const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                        const int32_t* context_lens, const int32_t* cu_nodes,
+                                        const uint64_t* tree_mask, int mask_words, int max_nodes, int64_t num_tokens,
+                                        int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                        int max_blocks_per_seq, int64_t num_blocks, int max_context_len, float scale,
+                                        void* out, pkv_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                                        int32_t* err_flag, void* stream);
+pkv_status pkv_paged_tree_attention_e5m2(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                         const int32_t* context_lens, const int32_t* cu_nodes,
+                                         const uint64_t* tree_mask, int mask_words, int max_nodes, int64_t num_tokens,
+                                         int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                         int max_blocks_per_seq, int64_t num_blocks, int max_context_len, float scale,
+                                         void* out, pkv_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                                         int32_t* err_flag, void* stream);
+pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+                           const int32_t* cu_nodes, const int32_t* accepted, int max_accept, int batch,
+                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                           int elt_bytes, int32_t* new_lens, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Host-side block pool ("Series 03 ...", sections 3.2-3.3; "What a KV cache
  * is ...", section 3.2): a preallocated set of block ids handed out on demand,
  * with reference counts for blocks shared by several block tables.  Policy: a

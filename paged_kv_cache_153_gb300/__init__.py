@@ -39,6 +39,10 @@ __all__ = [
     "pkv_select_blocks", "pkv_paged_decode_attention_sparse", "pkv_paged_decode_attention_sparse_fp8",
     "pkv_paged_decode_attention_sparse_e5m2",
     "pkv_prefix_workspace_bytes", "pkv_paged_decode_attention_prefix",
+    "pkv_paged_decode_attention_window", "pkv_paged_decode_attention_window_fp8",
+    "pkv_paged_decode_attention_window_e5m2",
+    "pkv_tree_plan", "pkv_tree_workspace_bytes", "pkv_paged_tree_attention", "pkv_paged_tree_attention_fp8",
+    "pkv_paged_tree_attention_e5m2", "pkv_tree_commit",
 ]
 
 PKV_F16 = 0
@@ -150,6 +154,21 @@ _SIGS = {
     "pkv_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "pkv_paged_decode_attention_prefix": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _i, _i,
                                                _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_paged_decode_attention_window": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _i, _f, _p, _i,
+                                               _p, _sz, _p, _p]),
+    "pkv_paged_decode_attention_window_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _i,
+                                                   _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_paged_decode_attention_window_e5m2": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _i,
+                                                    _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_tree_plan": (_i, [_p, _p, _p, _p, _i, _i64, _i, _i, _i, _i64, _p, _p, _p, _p, _p]),
+    "pkv_tree_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i]),
+    "pkv_paged_tree_attention": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i64, _i, _i, _i, _i, _i, _i, _i64, _i, _f,
+                                      _p, _i, _p, _sz, _p, _p]),
+    "pkv_paged_tree_attention_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i64, _i, _i, _i, _i, _i, _i,
+                                          _i64, _i, _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_paged_tree_attention_e5m2": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i64, _i, _i, _i, _i, _i, _i,
+                                           _i64, _i, _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_tree_commit": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _p, _p, _p]),
     "pkv_rope_plan": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, C.POINTER(_f)]),
     "pkv_rope_append": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i, _i, _f, _p, _i64, _p, _p, _i64,
                              _i, _i, _i, _i, _i, _p, _p]),
@@ -629,6 +648,88 @@ def pkv_paged_decode_attention_prefix(q, k_cache, v_cache, block_tables, context
     _check("pkv_paged_decode_attention_prefix", _tensor.prefix_decode(
         q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, out, scale, max_context_len,
         max_prefix_len, workspace, dtype, err_flag, stream))
+
+
+def pkv_paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_lens, out, *, scale: float,
+                                      window: int, num_sinks: int = 0, workspace, dtype=None, err_flag=None,
+                                      stream=None) -> None:
+    """Decode attention to the first num_sinks and the last window tokens of
+    each context; the blocks in between are not read."""
+    _check("pkv_paged_decode_attention_window", _tensor.window_decode(
+        0, q, k_cache, v_cache, None, None, block_tables, context_lens, out, scale, window, num_sinks, workspace,
+        dtype, err_flag, stream))
+
+
+def pkv_paged_decode_attention_window_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, *,
+                                          scale: float, window: int, num_sinks: int = 0, workspace, q_dtype=None,
+                                          err_flag=None, stream=None) -> None:
+    _check("pkv_paged_decode_attention_window_fp8", _tensor.window_decode(
+        1, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, scale, window, num_sinks, workspace,
+        q_dtype, err_flag, stream))
+
+
+def pkv_paged_decode_attention_window_e5m2(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, *,
+                                           scale: float, window: int, num_sinks: int = 0, workspace, q_dtype=None,
+                                           err_flag=None, stream=None) -> None:
+    _check("pkv_paged_decode_attention_window_e5m2", _tensor.window_decode(
+        2, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, scale, window, num_sinks, workspace,
+        q_dtype, err_flag, stream))
+
+
+def pkv_tree_plan(parents, cu_nodes, block_tables, context_lens, tree_mask, positions, slot_mapping, *,
+                  num_blocks: int, err_flag=None, stream=None) -> None:
+    """What each drafted token sees (tree_mask int64 [T, words]: itself and its
+    ancestors, 64 tokens a word), its rotary position and its slot, from its
+    parent in the tree (parents int32 [T], -1: the context's last token).
+    positions, or slot_mapping with block_tables, may be None."""
+    _check("pkv_tree_plan", _tensor.tree_plan(
+        parents, cu_nodes, block_tables, context_lens, tree_mask, positions, slot_mapping, num_blocks, err_flag,
+        stream))
+
+
+def pkv_tree_workspace_bytes(batch: int, num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                             max_nodes: int) -> int:
+    n = lib.pkv_tree_workspace_bytes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim, max_nodes)
+    if n == 0:
+        raise PkvError("pkv_tree_workspace_bytes", 1)
+    return n
+
+
+def pkv_paged_tree_attention(q, k_cache, v_cache, block_tables, context_lens, cu_nodes, tree_mask, out, *,
+                             scale: float, max_context_len: int, max_nodes: int, workspace, dtype=None, err_flag=None,
+                             stream=None) -> None:
+    """Attention of drafted tokens q [T, Hq, D], the last cu_nodes[b + 1] -
+    cu_nodes[b] cached ones of each sequence, over the context before them and
+    the drafted tokens in their rows of tree_mask."""
+    _check("pkv_paged_tree_attention", _tensor.tree_attention(
+        0, q, k_cache, v_cache, None, None, block_tables, context_lens, cu_nodes, tree_mask, out, scale,
+        max_context_len, max_nodes, workspace, dtype, err_flag, stream))
+
+
+def pkv_paged_tree_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_nodes,
+                                 tree_mask, out, *, scale: float, max_context_len: int, max_nodes: int, workspace,
+                                 q_dtype=None, err_flag=None, stream=None) -> None:
+    _check("pkv_paged_tree_attention_fp8", _tensor.tree_attention(
+        1, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_nodes, tree_mask, out, scale,
+        max_context_len, max_nodes, workspace, q_dtype, err_flag, stream))
+
+
+def pkv_paged_tree_attention_e5m2(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_nodes,
+                                  tree_mask, out, *, scale: float, max_context_len: int, max_nodes: int, workspace,
+                                  q_dtype=None, err_flag=None, stream=None) -> None:
+    _check("pkv_paged_tree_attention_e5m2", _tensor.tree_attention(
+        2, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, cu_nodes, tree_mask, out, scale,
+        max_context_len, max_nodes, workspace, q_dtype, err_flag, stream))
+
+
+def pkv_tree_commit(k_cache, v_cache, block_tables, context_lens, cu_nodes, accepted, *, new_lens=None,
+                    err_flag=None, stream=None) -> None:
+    """Move the cached rows of the accepted drafted tokens (accepted int32
+    [batch, max_accept], ascending, -1 behind the list) up behind the context, in
+    every head (and layer, of a layer-major cache); new_lens takes the new
+    context lengths."""
+    _check("pkv_tree_commit", _tensor.tree_commit(
+        k_cache, v_cache, block_tables, context_lens, cu_nodes, accepted, new_lens, err_flag, stream))
 
 
 def pkv_blocks_needed(num_tokens: int, block_size: int = 16) -> int:

@@ -74,28 +74,52 @@ bool encode_cache_tmap(CUtensorMap* map, const void* base, int64_t rows, int hea
   return true;
 }
 
-namespace {
+int sm_count() {
+  static std::atomic<int> counts[kMaxDevices];   // (a device's count does not change: asked once)
+  int dev = 0, n = 0;
+  if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return 0;
+  if (dev >= 0 && dev < kMaxDevices && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cuda_failed(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute"))
+    return 0;
+  if (dev >= 0 && dev < kMaxDevices) counts[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
-// Tiled TMA view of queries [batch, n_q_heads, head_dim] (16-bit) with boxes of
-// [128 / group sequences, group heads, 64 elements] and the 128-byte swizzle.
-bool encode_query_tmap(CUtensorMap* map, const void* base, int batch, int n_q_heads, int head_dim, int group) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(n_q_heads),
-                              static_cast<cuuint64_t>(batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
-                                 static_cast<cuuint64_t>(head_dim) * 2 * n_q_heads};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
-  const cuuint32_t estr[3] = {1, 1, 1};
+static bool encode_16bit(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                         const cuuint32_t* box) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
   if (encode == nullptr) return false;
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank),
+                            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled: CUresult %d", static_cast<int>(r));
     return false;
   }
   return true;
 }
+
+bool encode_query_tmap(CUtensorMap* map, const void* base, int64_t tokens, int n_q_heads, int head_dim, int group,
+                       int box_tokens) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(n_q_heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                                 static_cast<cuuint64_t>(head_dim) * 2 * n_q_heads};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(box_tokens)};
+  return encode_16bit(map, base, 3, dims, strides, box);
+}
+
+bool encode_block_tmap(CUtensorMap* map, const void* base, int64_t slabs, int head_dim) {
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+  const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(head_dim) / 64, static_cast<cuuint64_t>(slabs) * 2};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(head_dim / 64), 2};
+  return encode_16bit(map, base, 4, dims, strides, box);
+}
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -109,17 +133,6 @@ int env_int(const char* name, int fallback) {
 int token_blocks(int n) { return n / kBlockSize + (n % kBlockSize != 0); }
 
 constexpr int kMaxCtasPerSm = 4;   // partial slots are sized for this many blocks per SM
-
-int sm_count() {
-  static std::atomic<int> counts[kMaxDevices];   // (a device's count does not change: asked once)
-  int dev = 0, n = 0;
-  if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return 0;
-  if (dev >= 0 && dev < kMaxDevices && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cuda_failed(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute"))
-    return 0;
-  if (dev >= 0 && dev < kMaxDevices) counts[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -177,7 +190,8 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
                          int32_t* err_flag, void* stream, const void* k_new = nullptr, const void* v_new = nullptr,
                          int64_t* slots_out = nullptr, int num_layers = 1, int layer = 0,
                          const void* slab_params = nullptr, bool wait_first = false,
-                         const int32_t* selected = nullptr, int budget = 0, RestCall* rest = nullptr) {
+                         const int32_t* selected = nullptr, int budget = 0, RestCall* rest = nullptr,
+                         int window = 0, int num_sinks = 0) {
   // kv_kind: 0 = 16-bit cache, 1 = E4M3 with per-head scales, 2 = INT8 with
   // per-(block, head) min-max parameters, 3 = E5M2 with per-head scales
   const bool fp8 = kv_kind == 1 || kv_kind == 3, int8 = kv_kind == 2;
@@ -211,6 +225,8 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   if (int8 && (!slab_params || (reinterpret_cast<uintptr_t>(slab_params) & 15u) || k_new != nullptr))
     return PKV_ERR_INVALID_ARG;
   DecodeLauncher launch = rest != nullptr ? decode_launcher_rest(dtype, head_dim, group)
+                        : window > 0 ? (fp8 ? decode_launcher_window_fp8(kv_kind, dtype, head_dim, group)
+                                            : decode_launcher_window_16(dtype, head_dim, group))
                         : selected != nullptr && !int8
                               ? (fp8 ? decode_launcher_listed_fp8(kv_kind, dtype, head_dim, group)
                                      : decode_launcher_listed_16(dtype, head_dim, group))
@@ -254,6 +270,8 @@ pkv_status decode_common(int kv_kind, const void* q, const void* k_cache, const 
   p.max_nblk = token_blocks(max_context_len);
   p.selected = selected;
   p.budget = budget;
+  p.window = window;
+  p.num_sinks = num_sinks;
   if (rest != nullptr) {
     p.group_starts = rest->group_starts;
     p.prefix_lens = rest->prefix_lens;
@@ -549,6 +567,54 @@ extern "C" pkv_status pkv_paged_decode_attention_sparse_e5m2(
                        q_dtype, workspace, workspace_bytes, err_flag, stream);
 }
 
+// Decode over the first and the last tokens: their blocks bound the work (a
+// block more at either end of the window than its tokens fill).
+static pkv_status window_common(int kv_kind, const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads,
+                                int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks, int window,
+                                int num_sinks, float scale, void* out, pkv_dtype q_dtype, void* workspace,
+                                size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  if (window <= 0 || num_sinks < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+  const int64_t blocks = static_cast<int64_t>(token_blocks(window)) + 1 + token_blocks(num_sinks);
+  const int64_t bound = std::min<int64_t>(std::min<int64_t>(blocks, max_blocks_per_seq), INT32_MAX / kBlockSize);
+  return decode_common(kv_kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, batch,
+                       num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                       static_cast<int>(bound) * kBlockSize, scale, out, q_dtype, 0, workspace, workspace_bytes,
+                       err_flag, stream, nullptr, nullptr, nullptr, 1, 0, nullptr, false, nullptr, 0, nullptr, window,
+                       num_sinks);
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+    int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+    int64_t num_blocks, int window, int num_sinks, float scale, void* out, pkv_dtype dtype, void* workspace,
+    size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  return window_common(0, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, batch, num_q_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, window, num_sinks, scale,
+                       out, dtype, workspace, workspace_bytes, err_flag, stream);
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_window_fp8(
+    const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* block_tables, const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks, int window, int num_sinks, float scale,
+    void* out, pkv_dtype q_dtype, void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  return window_common(1, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, batch, num_q_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, window, num_sinks, scale,
+                       out, q_dtype, workspace, workspace_bytes, err_flag, stream);
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_window_e5m2(
+    const void* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* block_tables, const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks, int window, int num_sinks, float scale,
+    void* out, pkv_dtype q_dtype, void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
+  return window_common(3, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, batch, num_q_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, window, num_sinks, scale,
+                       out, q_dtype, workspace, workspace_bytes, err_flag, stream);
+}
+
 extern "C" size_t pkv_prefix_workspace_bytes(int batch, int num_groups, int num_q_heads, int num_kv_heads,
                                              int head_dim, int max_blocks_per_seq, int max_context_len,
                                              int max_prefix_len) {
@@ -599,7 +665,7 @@ extern "C" pkv_status pkv_paged_decode_attention_prefix(
   PrefixParams p{};
   if (!encode_cache_tmap(&p.tmap_k, k_cache, rows, head_dim, 2) ||
       !encode_cache_tmap(&p.tmap_v, v_cache, rows, head_dim, 2) ||
-      !encode_query_tmap(&p.tmap_q, q, batch, num_q_heads, head_dim, group))
+      !encode_query_tmap(&p.tmap_q, q, batch, num_q_heads, head_dim, group, 128 / group))
     return PKV_ERR_CUDA;
   p.block_tables = block_tables;
   p.context_lens = context_lens;

@@ -65,7 +65,11 @@
 // in the list and then in the table, and hands its valid rows to the consumer
 // with the stage.  kRest: the blocks behind a prefix that the sequence's group
 // shares, attended to elsewhere; a (sequence, KV head) held by one range is
-// left as an fp32 state too, for the merge with the prefix's.
+// left as an fp32 state too, for the merge with the prefix's.  kWindow: the
+// first num_sinks and the last `window` tokens of the context.  Its blocks are
+// those up to the last first token's and those from the window's first on;
+// what lies between is neither looked up nor read, and the rows of a read block
+// that neither holds are masked like those behind the context.
 #pragma once
 
 #include <cuda.h>
@@ -117,6 +121,8 @@ struct DecodeParams {
   const int32_t* group_starts;   // kRest: [num_groups + 1] first sequence of each group
   const int32_t* prefix_lens;    // kRest: [num_groups] tokens each group shares
   int num_groups;
+  int window;                    // kWindow: last tokens attended to (0: another source)
+  int num_sinks;                 // kWindow: first tokens attended to
   float* rest_ml;                // kRest: [B, Hq, 2] (m, l) and
   float* rest_o;                 // [B, Hq, D] o of pairs that one range holds
   int wait_first;                // 1: the previous kernel (the INT8 step's append) writes the last block of
@@ -124,7 +130,7 @@ struct DecodeParams {
                                  // block, the consumers before their first global write
 };
 
-enum Source { kWhole = 0, kListed = 1, kRest = 2 };
+enum Source { kWhole = 0, kListed = 1, kRest = 2, kWindow = 3 };
 
 struct SegDesc {
   int b, g, i0, i1;              // logical blocks [i0, i1) of (b, g)
@@ -140,7 +146,8 @@ struct ProdSeg {
   int slot;                      // as SegDesc::slot
   int64_t r;                     // its range
   int64_t f_end, f_hi;           // flat end of the segment and of its range
-  int skip;                      // kRest: blocks of the shared prefix, ahead of logical block 0
+  int skip;                      // kRest: blocks of the shared prefix, ahead of logical block 0;
+                                 // kWindow: blocks left out behind the first tokens' ones
 };
 
 // blocks of ctx >= 0 tokens (unsigned: the sum may pass 2^31)
@@ -161,6 +168,13 @@ __device__ __forceinline__ int seq_blocks(int cap, int ctx, int32_t* err) {
     nb = cap;
   }
   return nb;
+}
+
+// Blocks that the first `sinks` tokens lie in, and blocks between them and the
+// last `window` of n tokens that hold none of either.
+__device__ __forceinline__ int sink_blocks(int sinks) { return sinks / kBlockSize + (sinks % kBlockSize != 0); }
+__device__ __forceinline__ int window_skip(int n, int window, int sinks) {
+  return max(0, max(0, n - window) / kBlockSize - sink_blocks(sinks));
 }
 
 // Does a sequence of ctx tokens take part in its group's prefix of `blocks`
@@ -433,6 +447,19 @@ __device__ __noinline__ void clear_rows(uint32_t vslab, int r0, int lane) {
   __syncwarp();
 }
 
+// rows r0..r1 - 1 alone (kWindow: the rows between the first and the last tokens)
+template <int D, int ESZ, bool SWZ>
+__device__ __noinline__ void clear_gap(uint32_t vslab, int r0, int r1, int lane) {
+  constexpr int kChunks = D * ESZ / 16;
+  for (int x = lane; x < (r1 - r0) * kChunks; x += 32) {
+    const int r = r0 + x / kChunks, c = x % kChunks;
+    const uint32_t addr = SWZ ? vslab + (c >> 3) * 2048 + r * 128 + (c & 7) * 16 : vslab + r * D * ESZ + c * 16;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------------------
 // the decode kernel
 // ---------------------------------------------------------------------------
@@ -510,9 +537,11 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
     int nb = 0;
     if (b < p.batch) {
       const int ctx = p.context_lens[b];
-      nb = seq_blocks(SRC == kListed ? p.max_blocks_per_seq : min(p.max_blocks_per_seq, p.max_nblk), ctx, p.err);
+      nb = seq_blocks(SRC == kListed || SRC == kWindow ? p.max_blocks_per_seq : min(p.max_blocks_per_seq, p.max_nblk),
+                      ctx, p.err);
       ntok[b] = min(max(ctx, 0), nb * kBlockSize);
       if constexpr (SRC == kListed) nb = min(nb, p.budget);
+      if constexpr (SRC == kWindow) nb -= window_skip(ntok[b], p.window, p.num_sinks);
       if constexpr (SRC == kRest) {
         const int skip = prefix_blocks(p, b);
         skipped[b] = skip;
@@ -695,6 +724,7 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
       sg.f_hi = f_hi;
       sg.skip = 0;
       if constexpr (SRC == kRest) sg.skip = skipped[lo];
+      if constexpr (SRC == kWindow) sg.skip = window_skip(ntok[lo], p.window, p.num_sinks);
       sg.slot = -1;
       if (!(sg.i0 == 0 && sg.i1 == sg.nb)) {
         const int64_t sl = (f == f_lo) ? 2 * r : 2 * r + 1;
@@ -726,7 +756,10 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
     auto table_at = [&](const ProdSeg& sg, int w, int& rows) -> int {
       rows = 0;
       if (sg.i0 + w + lane >= sg.i1) return 0;
-      const int32_t* row = p.block_tables + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + sg.skip;
+      const int32_t* row = p.block_tables + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
+      if constexpr (SRC == kRest) row += sg.skip;
+      if constexpr (SRC == kWindow)
+        if (sg.i0 + w + lane >= sink_blocks(p.num_sinks)) row += sg.skip;
       if constexpr (SRC == kListed) {
         const int i = p.selected[(static_cast<int64_t>(sg.b) * Hkv + sg.g) * p.budget + sg.i0 + w + lane];
         if (i < 0) return kSkip;
@@ -931,6 +964,12 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
     // fused step: local index of the block holding the new token (-1: none here)
     const int patch_ii = (p.k_new != nullptr && d.i1 == d.nblk && d.n_tokens > 0) ? d.nblk - 1 - d.i0 : -1;
     float* mw = merge + warp * G * (D + 2);        // [G][D] o, then [G] m, [G] l
+    // kWindow: the rows of block i between the first and the last tokens, [gap0, gap1)
+    auto gap = [&](int i, int& gap0, int& gap1) {
+      gap0 = min(max(p.num_sinks - i * kBlockSize, 0), kBlockSize);
+      gap1 = min(max(max(0, d.n_tokens - p.window) - i * kBlockSize, gap0), kBlockSize);
+    };
+    const int seg_skip = SRC == kWindow ? window_skip(d.n_tokens, p.window, p.num_sinks) : 0;
 
     if constexpr (MMA) {
       // ------------------------- tensor-core consumer -------------------------
@@ -1002,7 +1041,12 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
           *abort_flag = 1;
           break;
         }
-        const int i = d.i0 + ii;
+        int i = d.i0 + ii;
+        int gap0 = 0, gap1 = 0;
+        if constexpr (SRC == kWindow) {
+          if (i >= sink_blocks(p.num_sinks)) i += seg_skip;
+          gap(i, gap0, gap1);
+        }
         const int n_valid =
             SRC == kListed ? stage_ok[s] : stage_ok[s] ? min(kBlockSize, d.n_tokens - i * kBlockSize) : 0;
         const uint32_t kslab = smem_u32(ring + static_cast<size_t>(s) * T::kStage);
@@ -1017,6 +1061,8 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
         // (INT8 codes are finite: a zero p needs no cleared row)
         if constexpr (!kInt8)
           if ((SRC == kListed || n_valid > 0) && n_valid < kBlockSize) clear_rows<D, T::kEsz, true>(vslab, n_valid, lane);
+        if constexpr (SRC == kWindow)
+          if (gap0 < gap1 && n_valid > 0) clear_gap<D, T::kEsz, true>(vslab, gap0, gap1, lane);
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         if constexpr (kFp8) {
 #pragma unroll
@@ -1060,7 +1106,11 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
           c[2] *= sc;
           c[3] *= sc;
         }
-        const bool v0 = r4 < n_valid, v1 = r4 + 8 < n_valid;
+        bool v0 = r4 < n_valid, v1 = r4 + 8 < n_valid;
+        if constexpr (SRC == kWindow) {
+          v0 = v0 && !(r4 >= gap0 && r4 < gap1);
+          v1 = v1 && !(r4 + 8 >= gap0 && r4 + 8 < gap1);
+        }
         const float s00 = v0 ? c[0] : -INFINITY, s01 = v0 ? c[1] : -INFINITY;
         const float s10 = v1 ? c[2] : -INFINITY, s11 = v1 ? c[3] : -INFINITY;
         float mx0 = fmaxf(s00, s10), mx1 = fmaxf(s01, s11);
@@ -1266,7 +1316,12 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
           *abort_flag = 1;
           break;
         }
-        const int i = d.i0 + ii;
+        int i = d.i0 + ii;
+        int gap0 = 0, gap1 = 0;
+        if constexpr (SRC == kWindow) {
+          if (i >= sink_blocks(p.num_sinks)) i += seg_skip;
+          gap(i, gap0, gap1);
+        }
         const int n_valid =
             SRC == kListed ? stage_ok[s] : stage_ok[s] ? min(kBlockSize, d.n_tokens - i * kBlockSize) : 0;
         const unsigned char* kslab = ring + static_cast<size_t>(s) * T::kStage;
@@ -1280,6 +1335,8 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
         }
         if constexpr (!kInt8)   // (INT8 codes are finite: a zero p needs no cleared row)
           if ((SRC == kListed || n_valid > 0) && n_valid < kBlockSize) clear_rows<D, T::kEsz, false>(smem_u32(vslab), n_valid, lane);
+        if constexpr (SRC == kWindow)
+          if (gap0 < gap1 && n_valid > 0) clear_gap<D, T::kEsz, false>(smem_u32(vslab), gap0, gap1, lane);
 
         // ---- scores: partial dot products over this lane's 8 elements ----
         float part[T::kNV];
@@ -1320,7 +1377,9 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
         float scv[NF], bm[NF];
 #pragma unroll
         for (int x = 0; x < NF; ++x) {
-          scv[x] = (t_held < n_valid) ? part[x] : -INFINITY;
+          bool seen = t_held < n_valid;
+          if constexpr (SRC == kWindow) seen = seen && !(t_held >= gap0 && t_held < gap1);
+          scv[x] = seen ? part[x] : -INFINITY;
           bm[x] = scv[x];
         }
 #pragma unroll
@@ -1674,7 +1733,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     long long v0 = 0, v1 = 0, v2 = 0, v3 = 0, v4 = 0;
     for (int i = lane; i < p.batch; i += 32) {
       const int ctx = p.context_lens[i];
-      const int n = ctx < 0 ? 0 : min(ctx_blocks(ctx), min(p.max_blocks_per_seq, p.max_nblk));
+      int n = ctx < 0 ? 0 : min(ctx_blocks(ctx), p.window > 0 ? p.max_blocks_per_seq
+                                                              : min(p.max_blocks_per_seq, p.max_nblk));
+      if (p.window > 0) n -= window_skip(min(max(ctx, 0), n * kBlockSize), p.window, p.num_sinks);
       v2 += n;
       v3 += n > 0;
       if (i < b) {

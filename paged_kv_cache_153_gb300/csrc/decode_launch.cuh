@@ -196,6 +196,9 @@ DecodeLauncher decode_launcher_int8(int q_dtype, int head_dim, int group);
 // blocks from lists (kv as decode_common's kv_kind: 0 = q's 16-bit type, 1 = E4M3, 3 = E5M2)
 DecodeLauncher decode_launcher_listed_16(int q_dtype, int head_dim, int group);
 DecodeLauncher decode_launcher_listed_fp8(int kv_kind, int q_dtype, int head_dim, int group);
+// the first and the last tokens of each context
+DecodeLauncher decode_launcher_window_16(int q_dtype, int head_dim, int group);
+DecodeLauncher decode_launcher_window_fp8(int kv_kind, int q_dtype, int head_dim, int group);
 // the blocks behind a shared prefix, 16-bit caches
 DecodeLauncher decode_launcher_rest(int q_dtype, int head_dim, int group);
 

@@ -43,6 +43,20 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 
 bool encode_cache_tmap(CUtensorMap* map, const void* base, int64_t rows, int head_dim, int elt_bytes);
 
+// Tiled TMA view of queries [tokens, n_q_heads, head_dim] (16-bit) with boxes of
+// [box_tokens, group heads, 64 elements] and the 128-byte swizzle.
+bool encode_query_tmap(CUtensorMap* map, const void* base, int64_t tokens, int n_q_heads, int head_dim, int group,
+                       int box_tokens);
+
+// Tiled TMA view of a 16-bit KV cache as [2 slabs, head_dim / 64, 8 rows, 64
+// elements] (a slab: the 16 rows of a block and head) with boxes of one slab,
+// which land as 8-row atoms of the 128-byte swizzle, the halves of a row side by
+// side.
+bool encode_block_tmap(CUtensorMap* map, const void* base, int64_t slabs, int head_dim);
+
+// SMs of the current device (0, with the reason kept, when it cannot be asked)
+int sm_count();
+
 // The append of the INT8 decode step (append_int8.cu): slots from the block
 // table, re-quantising append, early release of the decode launch that
 // follows (which waits for it before reading the cache).

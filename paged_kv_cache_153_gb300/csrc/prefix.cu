@@ -95,55 +95,6 @@ struct PrefixSmem {
   }
 };
 
-// tiled TMA load of a 3-D box
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
-      "%3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
-// 32 bytes in one store
-__device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
-// Write 32 consecutive columns of a warp's 32 rows (lane = row; o: its 32
-// columns; dst: column 0 of the warp's row 0; rows from n on are not written).
-// Four lanes exchange 32-byte pieces first, so that a store covers the whole
-// 128 bytes of 8 rows instead of a quarter of 32.
-template <int D>
-__device__ __forceinline__ void store_rows32(float* dst, const float* o, int n, int lane) {
-  float t[4][8];   // piece j: columns 8 j .. of this lane's row, then of row 4 (lane / 4) + j
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[j][e] = o[8 * j + e];
-#pragma unroll
-  for (int m = 1; m <= 2; m <<= 1)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if ((j & m) == 0) {
-        // lanes with bit m clear give piece j + m and get piece j of their partner's row
-        const bool up = (lane & m) != 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float give = up ? t[j][e] : t[j + m][e];
-          const float got = __shfl_xor_sync(0xffffffffu, give, m);
-          if (up) t[j][e] = got; else t[j + m][e] = got;
-        }
-      }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int row = (lane & ~3) + j;
-    if (row < n) st_global_v8(dst + static_cast<int64_t>(row) * D + 8 * (lane & 3), t[j]);
-  }
-}
-
 // a piece of a range: key tiles [t0, t1) of one unit
 struct PrefixSeg {
   int64_t next;                  // cost position behind it

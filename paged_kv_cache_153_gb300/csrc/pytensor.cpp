@@ -421,6 +421,30 @@ PyObject* sparse_decode(PyObject* const* a) {
   });
 }
 
+// kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out,
+// scale, window, num_sinks, workspace, dtype, err_flag, stream
+PyObject* window_decode(PyObject* const* a) {
+  const int kind = number<int>(a[0]);
+  const Attention x(a[1], a[2], a[3], a[6], a[7], a[8], a[12], kind, a[13], a[4], a[5], a[14]);
+  const float scale = number<float>(a[9]);
+  const int window = number<int>(a[10]), sinks = number<int>(a[11]);
+  const pkv_dtype dt = x.dtype;
+  const auto* ks = static_cast<const float*>(address(a[4]));
+  const auto* vs = static_cast<const float*>(address(a[5]));
+  auto* err = static_cast<int32_t*>(address(a[14]));
+  void* s = stream_of(a[15]);
+  if (kind == 0)
+    return status([&] {
+      return pkv_paged_decode_attention_window(x.q, x.k, x.v, x.tab, x.len, x.b, x.hq, x.hkv, x.d, x.bs, x.width, x.nb,
+                                               window, sinks, scale, x.out, dt, x.ws, x.ws_bytes, err, s);
+    });
+  const auto fn = kind == 1 ? pkv_paged_decode_attention_window_fp8 : pkv_paged_decode_attention_window_e5m2;
+  return status([&] {
+    return fn(x.q, static_cast<const uint8_t*>(x.k), static_cast<const uint8_t*>(x.v), ks, vs, x.tab, x.len, x.b, x.hq,
+              x.hkv, x.d, x.bs, x.width, x.nb, window, sinks, scale, x.out, dt, x.ws, x.ws_bytes, err, s);
+  });
+}
+
 // q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens,
 // out, scale, max_context_len, max_prefix_len, workspace, dtype, err_flag, stream
 PyObject* prefix_decode(PyObject* const* a) {
@@ -444,6 +468,151 @@ PyObject* prefix_decode(PyObject* const* a) {
   });
 }
 
+// a step's drafted tokens: offsets [batch + 1], one context length per sequence
+int drafted_batch(const at::Tensor& cu, const at::Tensor& len) {
+  index_check(cu);
+  index_check(len);
+  if (cu.numel() != len.numel() + 1)
+    refuse(PyExc_ValueError, "cu_nodes must have one entry more than context_lens");
+  return to_int(len.numel());
+}
+
+uint64_t* mask_words(const at::Tensor& t, int64_t tokens) {
+  if ((t.scalar_type() != at::kLong && t.scalar_type() != at::kUInt64) || !t.is_contiguous())
+    refuse(PyExc_TypeError, "tree_mask must be contiguous int64");
+  if (t.size(0) != tokens) refuse(PyExc_ValueError, "tree_mask must have a row per token");
+  return static_cast<uint64_t*>(ptr(t));
+}
+constexpr const char* kMaskDims = "tree_mask must be [num_tokens, words]";
+
+// parents, cu_nodes, block_tables, context_lens, tree_mask, positions,
+// slot_mapping, num_blocks, err_flag, stream
+PyObject* tree_plan(PyObject* const* a) {
+  const at::Tensor &par = need(a[0], -1, ""), &cu = need(a[1], -1, ""), &len = need(a[3], -1, ""),
+                   &mask = need(a[4], 2, kMaskDims);
+  index_check(par);
+  const int b = drafted_batch(cu, len), words = to_int(mask.size(1));
+  const int64_t tokens = par.numel(), nb = number<int64_t>(a[7]);
+  const int32_t* tab = nullptr;
+  int width = 0;
+  if (a[6] != Py_None) {
+    const at::Tensor &t = need(a[2], 2, kTableDims), &s = need(a[6], -1, "");
+    index_check(t);
+    per_sequence(b, t, len);
+    if (s.numel() != tokens || s.scalar_type() != at::kLong || !s.is_contiguous())
+      refuse(PyExc_ValueError, "slot_mapping must be contiguous int64, one slot per token");
+    tab = static_cast<const int32_t*>(ptr(t));
+    width = to_int(t.size(1));
+  }
+  if (a[5] != Py_None) {
+    const at::Tensor& t = need(a[5], -1, "");
+    index_check(t);
+    if (t.numel() != tokens) refuse(PyExc_ValueError, "positions must have an entry per token");
+  }
+  flag_check(a[8]);
+  uint64_t* mp = mask_words(mask, tokens);
+  const auto* pp = static_cast<const int32_t*>(ptr(par));
+  const auto* cp = static_cast<const int32_t*>(ptr(cu));
+  const auto* lp = static_cast<const int32_t*>(ptr(len));
+  auto* pos = static_cast<int32_t*>(address(a[5]));
+  auto* slots = static_cast<int64_t*>(address(a[6]));
+  auto* err = static_cast<int32_t*>(address(a[8]));
+  void* s = stream_of(a[9]);
+  return status([&] {
+    return pkv_tree_plan(pp, cp, tab, lp, b, tokens, words, 16, width, nb, mp, pos, slots, err, s);
+  });
+}
+
+// kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+// cu_nodes, tree_mask, out, scale, max_context_len, max_nodes, workspace, dtype,
+// err_flag, stream
+PyObject* tree_attention(PyObject* const* a) {
+  const int kind = number<int>(a[0]);
+  const at::Tensor &q = need(a[1], 3, "q must be [num_tokens, num_q_heads, head_dim]"), &kc = need(a[2], 4, kCacheDims),
+                   &vc = need(a[3], -1, ""), &tab = need(a[6], 2, kTableDims), &len = need(a[7], -1, ""),
+                   &cu = need(a[8], -1, ""), &mask = need(a[9], 2, kMaskDims), &out = need(a[10], -1, ""),
+                   &ws = need(a[14], -1, "");
+  const int b = drafted_batch(cu, len), words = to_int(mask.size(1));
+  index_check(tab);
+  per_sequence(b, tab, len);
+  contiguous(q);
+  contiguous(out);
+  caches_check(kc, vc, kind == 0 ? 2 : 1);
+  if (out.sizes() != q.sizes()) refuse(PyExc_ValueError, "q and out differ in shape");
+  if (kc.size(3) != q.size(2)) refuse(PyExc_ValueError, "q and the caches differ in head_dim");
+  const Type16 type(q, a[15]);
+  type.check(out);
+  cache_type(kc, kind, type);
+  scales_check(a[4], kc.size(1));
+  scales_check(a[5], kc.size(1));
+  flag_check(a[16]);
+  if (!ws.is_contiguous()) refuse(PyExc_ValueError, "the workspace must be contiguous");
+  const int64_t tokens = q.size(0), nb = kc.size(0);
+  const uint64_t* mp = mask_words(mask, tokens);
+  const int hq = to_int(q.size(1)), hkv = to_int(kc.size(1)), d = to_int(q.size(2)), bs = to_int(kc.size(2)),
+            width = to_int(tab.size(1)), max_ctx = number<int>(a[12]), max_nodes = number<int>(a[13]);
+  const float scale = number<float>(a[11]);
+  const pkv_dtype dt = type.code;
+  void *qp = ptr(q), *kp = ptr(kc), *vp = ptr(vc), *op = ptr(out), *wp = ptr(ws);
+  const size_t bytes = ws.nbytes();
+  const auto* tp = static_cast<const int32_t*>(ptr(tab));
+  const auto* lp = static_cast<const int32_t*>(ptr(len));
+  const auto* cp = static_cast<const int32_t*>(ptr(cu));
+  const auto* ks = static_cast<const float*>(address(a[4]));
+  const auto* vs = static_cast<const float*>(address(a[5]));
+  auto* err = static_cast<int32_t*>(address(a[16]));
+  void* s = stream_of(a[17]);
+  if (kind == 0)
+    return status([&] {
+      return pkv_paged_tree_attention(qp, kp, vp, tp, lp, cp, mp, words, max_nodes, tokens, b, hq, hkv, d, bs, width,
+                                      nb, max_ctx, scale, op, dt, wp, bytes, err, s);
+    });
+  const auto fn = kind == 1 ? pkv_paged_tree_attention_fp8 : pkv_paged_tree_attention_e5m2;
+  return status([&] {
+    return fn(qp, static_cast<const uint8_t*>(kp), static_cast<const uint8_t*>(vp), ks, vs, tp, lp, cp, mp, words,
+              max_nodes, tokens, b, hq, hkv, d, bs, width, nb, max_ctx, scale, op, dt, wp, bytes, err, s);
+  });
+}
+
+// k_cache, v_cache, block_tables, context_lens, cu_nodes, accepted, new_lens,
+// err_flag, stream
+PyObject* tree_commit(PyObject* const* a) {
+  const at::Tensor &kc = need(a[0], -1, ""), &vc = need(a[1], -1, ""), &tab = need(a[2], 2, kTableDims),
+                   &len = need(a[3], -1, ""), &cu = need(a[4], -1, ""),
+                   &acc = need(a[5], 2, "accepted must be [batch, max_accept]");
+  if (kc.dim() != 4 && kc.dim() != 5)
+    refuse(PyExc_ValueError, "caches must be [num_blocks, num_kv_heads, 16, head_dim], or with num_layers second");
+  const int b = drafted_batch(cu, len), n = static_cast<int>(kc.dim());
+  index_check(tab);
+  index_check(acc);
+  per_sequence(b, tab, len);
+  if (acc.size(0) != b) refuse(PyExc_ValueError, "accepted must have a row per sequence");
+  if (kc.element_size() != 1 && kc.element_size() != 2)
+    refuse(PyExc_TypeError, "caches must have elements of one or two bytes");
+  caches_check(kc, vc, static_cast<int64_t>(kc.element_size()));
+  if (a[6] != Py_None) {
+    const at::Tensor& t = need(a[6], -1, "");
+    index_check(t);
+    if (t.numel() != b) refuse(PyExc_ValueError, "new_lens and context_lens differ in length");
+  }
+  flag_check(a[7]);
+  const int64_t nb = kc.size(0);
+  const int heads = to_int(n == 5 ? kc.size(1) * kc.size(2) : kc.size(1)), bs = to_int(kc.size(n - 2)),
+            d = to_int(kc.size(n - 1)), elt = static_cast<int>(kc.element_size()), width = to_int(tab.size(1)),
+            most = to_int(acc.size(1));
+  void *kp = ptr(kc), *vp = ptr(vc);
+  const auto* tp = static_cast<const int32_t*>(ptr(tab));
+  const auto* lp = static_cast<const int32_t*>(ptr(len));
+  const auto* cp = static_cast<const int32_t*>(ptr(cu));
+  const auto* ap = static_cast<const int32_t*>(ptr(acc));
+  auto* np = static_cast<int32_t*>(address(a[6]));
+  auto* err = static_cast<int32_t*>(address(a[7]));
+  void* s = stream_of(a[8]);
+  return status([&] {
+    return pkv_tree_commit(kp, vp, tp, lp, cp, ap, most, b, heads, d, bs, width, nb, elt, np, err, s);
+  });
+}
+
 #define PKV_TENSOR_CALL(f, n) \
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<n, &f>)), METH_FASTCALL, nullptr}
 
@@ -454,6 +623,10 @@ PyMethodDef methods[] = {
     PKV_TENSOR_CALL(select_blocks, 7),
     PKV_TENSOR_CALL(sparse_decode, 15),
     PKV_TENSOR_CALL(prefix_decode, 15),
+    PKV_TENSOR_CALL(window_decode, 16),
+    PKV_TENSOR_CALL(tree_plan, 10),
+    PKV_TENSOR_CALL(tree_attention, 18),
+    PKV_TENSOR_CALL(tree_commit, 9),
     {nullptr, nullptr, 0, nullptr},
 };
 
