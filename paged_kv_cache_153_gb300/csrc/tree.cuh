@@ -26,15 +26,19 @@
 // about 25 bytes a clock).  As an operand, 8-key groups are D / 64 KiB apart and
 // the halves of a row 1 KiB, in K (K-major) and V (MN-major) alike.
 // Per operation, one row tile against one key tile:
-//   S = Q K^T     into one of the S / P buffers in TMEM (three, or two where the
-//                 outputs of two row tiles with head_dim 128 take the rest)
-//   softmax       8 warps, two threads per row: 64 columns each, the row's
-//                 maximum exchanged through shared memory; P overwrites S.  bf16
-//                 P is two bf16 parts (p truncated, the rounded remainder: exact
-//                 to 2^-16, where one rounding, 2^-9, would be as large as the
-//                 output's own); fp16 P (2^-12) is rounded once, and l sums the
-//                 rounded values.  The row reference moves only when a tile's
-//                 maximum exceeds it by more than 2^8; only then is O rescaled.
+//   S = Q K^T     into one of the S / P buffers in TMEM (three beside one row
+//                 tile, one per group beside two)
+//   softmax       two groups of 4 warps, one thread per row, take operations in
+//                 turn, so that one group's waits and loads overlap the other's
+//                 exponentials.  Of one row tile the groups take key tiles in turn
+//                 and share its outputs: each passes the row's reference on through
+//                 shared memory before its exponentials.  Of two row tiles, each
+//                 has its own.  P overwrites S.  bf16 P is two bf16 parts (p
+//                 truncated, the rounded remainder: exact to 2^-16, where one
+//                 rounding, 2^-9, would be as large as the output's own); fp16 P
+//                 (2^-12) is rounded once, and l sums the rounded values.  The row
+//                 reference moves only when a tile's maximum exceeds it by more
+//                 than 2^8; only then is O rescaled.
 //   O += P V      P from TMEM.
 // Key tiles go from the last to the first: the ones with drafted tokens need a
 // look at their rows, which then overlaps the first loads.
@@ -45,12 +49,17 @@
 // is not finite is set to 0 there and the token remembered: at the end every row
 // that sees it adds the element itself (an infinity or a NaN whatever the weight).
 //
-// FP8 caches.  Codes are staged by 1-D copies and converted to fp16 tiles by four
-// warps (every E4M3 and E5M2 value is a half); q is fp16 (bf16 q converted in
-// place: exact in fp16's normal range).  The products then run in fp16.
+// FP8 caches.  Codes are staged by 1-D copies and converted to fp16 tiles by eight
+// warps: an E5M2 code is the upper byte of its half; an E4M3 code's bits, moved to
+// their places in a half, are its value times 2^-8 (denormals too), which the
+// scales take back.  (The conversion instruction took 1500 clocks a tile.)  q is
+// fp16 (bf16 q converted in place: exact in fp16's normal range).  The products
+// then run in fp16.
 //
-// Warps 0-7: softmax; 8: producer; 9: TMEM owner and Q K^T issuer; 10: P V
-// issuer; 11-14: rows of V with drafted tokens, or the conversions.  Waits are
+// Warps 0-7: softmax; 8 and 11: producers; 9: TMEM owner and Q K^T issuer; 10:
+// P V issuer; from 12 on: rows of V with drafted tokens (four warps), or the
+// conversions of K (four) and of V (four).  The softmax warps take registers
+// from the others, so that a row half's scores and its P stay in them.  Waits are
 // bounded as in the other kernels.
 #pragma once
 
@@ -66,38 +75,44 @@
 
 namespace pkv {
 
-constexpr int kTThreads = 480;
 constexpr int kTSoftmax = 256;
-constexpr int kTXform = 4;                        // warps 11-14
 constexpr int kTTileBlocks = kTreeKeys / kBlockSize;
 constexpr float kTRescaleLog2 = 8.f;
 constexpr int kTBadSlots = 4;                     // pieces whose remembered tokens live at once
 
 // cost of a unit's set-up (Q, the first tile's latency, its outputs) and of a key
 // tile against one row tile or two, in half tiles
-constexpr int kTUnitCost = 3;
+constexpr int kTUnitCost = 6;
 __host__ __device__ constexpr int tree_tile_cost(int rows) { return rows > kTreeRows ? 3 : 2; }
 
 template <int D, bool FP8, int NQ>
 struct TreeSmem {
+  // warps that convert codes (or look at V rows) behind the first twelve, and the
+  // registers that the softmax warps take from the others
+  static constexpr int kXform = 4;                                 // for K, and for V (16-bit: for V alone)
+  static constexpr int kThreads = 384 + 32 * kXform * (FP8 ? 2 : 1);
+  static constexpr int kRegs = 65536 / kThreads / 8 * 8;           // a thread, at launch
+  static constexpr int kRegsSoftmax = FP8 ? 152 : 168, kRegsOther = FP8 ? 56 : 88;
+  static_assert(kTSoftmax * kRegsSoftmax + (kThreads - kTSoftmax) * kRegsOther <= kThreads * kRegs, "registers");
   static constexpr int kTile = kTreeKeys * D * 2;                  // a Q, K or V tile
   static constexpr int kStage = kTile / 2;                         // FP8: a staged tile of codes
+  static constexpr int kQBufs = 1;
   static constexpr int kKStages = FP8 ? 1 : 2;
   static constexpr int kVStages = FP8 ? 3 - NQ : 4 - NQ;
-  static constexpr int kCodeStages = FP8 ? 4 : 0;
+  static constexpr int kCodeStages = FP8 ? 2 : 0;                  // of K, and of V
   static constexpr int kQ = 0;
-  static constexpr int kK = NQ * kTile;
+  static constexpr int kK = kQBufs * NQ * kTile;
   static constexpr int kV = kK + kKStages * kTile;
   static constexpr int kCodes = kV + kVStages * kTile;
-  static constexpr int kBar = kCodes + kCodeStages * kStage;       // 512 bytes
+  static constexpr int kBar = kCodes + 2 * kCodeStages * kStage;       // 512 bytes
   static constexpr int kBad = kBar + 512;                          // uint32 [slots][warps][8]
-  static constexpr int kRed = kBad + kTBadSlots * kTXform * 32;    // float [3][2][128]
-  static constexpr int kSeqs = kRed + 3 * 2 * kTreeRows * 4;       // TreeSeq [batch + 1]
+  static constexpr int kRed = kBad + kTBadSlots * kXform * 32;     // float [128] references, [2][2][128] sums
+  static constexpr int kSeqs = kRed + 5 * kTreeRows * 4;           // TreeSeq [batch + 1]
   static __host__ __device__ constexpr size_t bytes(int batch) {
     return 1024 + kSeqs + sizeof(TreeSeq) * (static_cast<size_t>(batch) + 1);
   }
   // S / P buffers, and the outputs behind them
-  static constexpr int kSBufs = (512 - NQ * D) / 128 < 3 ? (512 - NQ * D) / 128 : 3;
+  static constexpr int kSBufs = 4 - NQ;
   static constexpr int kOCol = kSBufs * kTreeKeys;
   // 8-key groups of a K / V tile and the 64-element halves of a row
   static constexpr int kGroup = 1024 * (D / 64);
@@ -204,13 +219,55 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return w & keep;
 }
 
+// four codes -> two pairs of halves (E4M3: times 2^-8)
+__device__ __forceinline__ uint2 codes4(uint32_t w, E5M2) {
+  return make_uint2(byte2_to_f16x2(w, E5M2{}), byte2_hi_to_f16x2(w, E5M2{}));
+}
+__device__ __forceinline__ uint2 codes4(uint32_t w, E4M3) {
+  const uint32_t a = byte2_to_f16x2(w, E5M2{}), b = byte2_hi_to_f16x2(w, E5M2{});   // code c as c << 8
+  return make_uint2(((a >> 1) & 0x3f803f80u) | (a & 0x80008000u), ((b >> 1) & 0x3f803f80u) | (b & 0x80008000u));
+}
+// a byte's top bit where an E4M3 code is a NaN (which codes4 makes a number)
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w, E4M3) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+__device__ __forceinline__ uint32_t nan_codes(uint32_t, E5M2) { return 0u; }
+// of the two codes in bits 0-15 of w: the bits that make their halves NaN
+__device__ __forceinline__ uint32_t nan_halves(uint32_t w, E4M3) {
+  return ((w & 0x7fu) == 0x7fu ? 0x7fffu : 0u) | ((w & 0x7f00u) == 0x7f00u ? 0x7fff0000u : 0u);
+}
+__device__ __forceinline__ uint32_t nan_halves(uint32_t, E5M2) { return 0u; }
+
 // MT: 16-bit type of the products; KV: the cache's (MT, or an FP8 format)
+// mbar_wait that gives up early once the block has stopped
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, const TreeParams& p,
+                                          const volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > p.wait_limit_ns) {
+      record_error(p.err, PKV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <typename MT, typename KV, int D, int NQ>
-__global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool kFp8 = KV::kBytes == 1;
   using L = TreeSmem<D, kFp8, NQ>;
   constexpr bool kSplit = std::is_same<MT, BF16>::value;
   constexpr int NB = L::kSBufs;
+  constexpr float kFold = std::is_same<KV, E4M3>::value ? 256.f : 1.f;   // of converted codes
   extern __shared__ unsigned char tsm_raw[];
   unsigned char* sm = tsm_raw + ((1024 - (smem_u32(tsm_raw) & 1023)) & 1023);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);   // [kKStages] K tile landed (FP8: converted)
@@ -218,18 +275,20 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
   uint64_t* v_full = k_empty + L::kKStages;        // [kVStages] V tile landed (16-bit)
   uint64_t* v_ready = v_full + L::kVStages;        // its rows looked at, or converted
   uint64_t* v_empty = v_ready + L::kVStages;       // its P V done
-  uint64_t* c_full = v_empty + L::kVStages;        // [kCodeStages] codes landed
-  uint64_t* c_empty = c_full + L::kCodeStages;     // converted
-  uint64_t* s_full = c_empty + L::kCodeStages;     // [NB] scores ready
+  uint64_t* c_full = v_empty + L::kVStages;        // [2 kCodeStages] codes of K, of V landed
+  uint64_t* c_empty = c_full + 2 * L::kCodeStages; // converted
+  uint64_t* s_full = c_empty + 2 * L::kCodeStages; // [NB] scores ready
   uint64_t* p_full = s_full + NB;                  // [NB] P written, O rescaled
   uint64_t* pv_done = p_full + NB;                 // [NB] P V done
-  uint64_t* q_full = pv_done + NB;                 // Q of a piece landed
-  uint64_t* q_ready = q_full + 1;                  // and converted
-  uint64_t* q_empty = q_ready + 1;                 // its Q K^T done
-  uint64_t* mma_idle = q_empty + 1;                // [2] an issuer's MMAs done
+  uint64_t* q_full = pv_done + NB;                 // [kQBufs] Q of a piece landed
+  uint64_t* q_empty = q_full + L::kQBufs;          // [kQBufs] its Q K^T done
+  uint64_t* q_ready = q_empty + L::kQBufs;         // Q converted (FP8)
+  uint64_t* turn = q_ready + 1;                    // [2][4] a group's warp has passed its rows' references on
+  uint64_t* joined = turn + 8;                     // [2][4] and its sums of a piece
+  uint64_t* mma_idle = joined + 8;                 // [2] an issuer's MMAs done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * 2 + 3 * 3 + 2 * 5 + 3 * 3 + 5 + 1) * 8 <= 512, "barrier block overflows");
+  static_assert((2 * 2 + 3 * 3 + 2 * 4 + 3 * 3 + 5 + 16 + 2 + 1) * 8 <= 512, "barrier block overflows");
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + L::kBad);
   float* red = reinterpret_cast<float*>(sm + L::kRed);
   TreeSeq* seqs = reinterpret_cast<TreeSeq*>(sm + L::kSeqs);
@@ -245,26 +304,32 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
   if (tid == 8 * 32) {
     *abort_flag = 0;
     for (int s = 0; s < L::kKStages; ++s) {
-      mbar_init(&k_full[s], kFp8 ? kTXform : 1);
+      mbar_init(&k_full[s], kFp8 ? L::kXform : 1);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < L::kVStages; ++s) {
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_ready[s], kTXform);
+      mbar_init(&v_ready[s], L::kXform);
       mbar_init(&v_empty[s], 1);
     }
-    for (int s = 0; s < L::kCodeStages; ++s) {
+    for (int s = 0; s < 2 * L::kCodeStages; ++s) {
       mbar_init(&c_full[s], 1);
-      mbar_init(&c_empty[s], kTXform);
+      mbar_init(&c_empty[s], L::kXform);
     }
     for (int s = 0; s < NB; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], kTSoftmax);
+      mbar_init(&p_full[s], kTSoftmax / 2);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_ready, kTXform);
-    mbar_init(q_empty, 1);
+    for (int s = 0; s < L::kQBufs; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    mbar_init(q_ready, L::kXform);
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&turn[s], 1);
+      mbar_init(&joined[s], 1);
+    }
     mbar_init(&mma_idle[0], 1);
     mbar_init(&mma_idle[1], 1);
     fence_mbar_init();
@@ -273,7 +338,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
   // tables only, which no kernel that releases early writes.
 
   // ---- the sequences: drafted tokens, context, cost ----
-  for (int b = tid; b < p.batch; b += kTThreads) {
+  for (int b = tid; b < p.batch; b += L::kThreads) {
     const int64_t t0 = p.cu_nodes[b], t1 = p.cu_nodes[b + 1];
     const int ctx = p.context_lens[b];
     TreeSeq sq{0, 0, 0, 0, 0};
@@ -312,7 +377,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
   tc_fence_after();
   if (blockIdx.x == 0) {
     pdl_wait();
-    for (int b = tid; b <= p.batch; b += kTThreads) p.seqs[b] = seqs[b];
+    for (int b = tid; b <= p.batch; b += L::kThreads) p.seqs[b] = seqs[b];
   }
   const uint32_t tmem = *tmem_slot;
   const int64_t V = seqs[p.batch].cost, R = gridDim.x, range = blockIdx.x;
@@ -323,216 +388,245 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
 
   if (warp < 8) {
     // ============================ softmax / epilogue ============================
-    const int r = tid & (kTreeRows - 1), half = tid >> 7, quarter = warp & 3;
-    const int pair_bar = 2 + quarter;                // named barrier of warps w and w + 4 (one row each)
+    set_max_regs_up<L::kRegsSoftmax>();
+    const int grp = warp >> 2, quarter = warp & 3, r = tid & (kTreeRows - 1);
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    Ring<NB> sr;                                     // S / P buffer of the next operation
+    uint64_t* my_turn = &turn[grp * 4 + quarter];
+    uint64_t* their_turn = &turn[(1 - grp) * 4 + quarter];
+    uint32_t ops = 0;                                // operations of the pieces before
+    uint32_t turns = 0;                              // references taken over so far
+    uint32_t joins = 0;                              // pieces whose sums were exchanged
     uint32_t slot = 0;                               // of remembered tokens
     bool ok = true;
-    int flip = 0;                                    // slot of the row exchange
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, tree_wait(bar, parity, p, abort_flag));
+    };
     pdl_wait();
     for (int64_t pos = first; pos < end && ok;) {
       const TreeSeg sg = segment(pos);
       pos = sg.next;
       if (sg.t0 >= sg.t1) continue;
       const TreeSeq sq = seqs[sg.b];
-      const int base = sq.ctx - sq.n;
-      const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-      const float scale_log2 = p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] : 1.f);
-      float m_ref[NQ], l_run[NQ];
-#pragma unroll
-      for (int c = 0; c < NQ; ++c) m_ref[c] = -INFINITY, l_run[c] = 0.f;
-      Ring<NB> last[NQ];                             // buffer of a row tile's previous operation
-      for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t) {
-#pragma unroll
-        for (int c = 0; c < NQ; ++c) {
-          if (c >= nq || !ok) break;
-          const int row = c * kTreeRows + r;         // of the unit
-          const bool live = c * kTreeRows + quarter * 32 < sg.rows;   // any row of this warp
-          const bool tail = (t + 1) * kTreeKeys > base;
-          uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-          if (tail && live) {
-            const int node = min((sg.unit * kTreeRows * NQ + row) >> shift, sq.n - 1);
-            const uint32_t* words = p.mask + (static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words);
-            const int o = t * kTreeKeys + 64 * half - base;
-            see[0] = tree_bits(words, 2 * p.mask_words, sq.n, o);
-            see[1] = tree_bits(words, 2 * p.mask_words, sq.n, o + 32);
-          }
-          const uint32_t ts = tmem + lane_base + sr.s * kTreeKeys + 64 * half;
-          const uint32_t to = tmem + lane_base + L::kOCol + c * D;
-          ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sr.s], sr.ph, p.err, p.wait_limit_ns) && !*abort_flag);
-          tc_fence_after();
-          float v[64];
-          float mx = -INFINITY;
-          if (ok && live) {
-            tmem_ld64(ts, v);
-            if (tail && __any_sync(0xffffffffu, (see[0] & see[1]) != 0xffffffffu)) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] = (see[i >> 5] >> (i & 31)) & 1u ? v[i] : -INFINITY;
-            }
-            mx = max64(v);
-            red[(flip * 2 + half) * kTreeRows + r] = mx;
-          }
-          // (a failed wait on either side ends both warps of the pair here)
-          if (named_bar_red_or(pair_bar, 64, !ok)) {
-            ok = false;
-            break;
-          }
-          if (live) {
-            mx = fmaxf(mx, red[(flip * 2 + (1 - half)) * kTreeRows + r]);
-            flip ^= 1;
-            const float m_tile = mx * scale_log2;
-            float alpha = 1.f;
-            if (m_tile > m_ref[c] + kTRescaleLog2) {
-              alpha = ex2_approx(m_ref[c] - m_tile);
-              m_ref[c] = m_tile;
-            }
-            bool waited = true;
-            if (t < sg.t1 - 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-              // O may be touched once the row tile's previous P V has completed
-              waited = __all_sync(0xffffffffu, mbar_wait(&pv_done[last[c].s], last[c].ph, p.err, p.wait_limit_ns));
-              tc_fence_after();
-              if (waited) {
-#pragma unroll 1
-                for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
-                  float o[16];
-                  tmem_ld16(to + x, o);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                  tmem_st16(to + x, o);
-                }
-              }
-            }
-            const float nref = (m_ref[c] == -INFINITY) ? 0.f : -m_ref[c];
-            const uint64_t scale2 = f32x2(scale_log2, scale_log2), nref2 = f32x2(nref, nref);
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pk[32];
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 x = f32x2_split(fma_f32x2(f32x2(v[32 * h + i], v[32 * h + i + 1]), scale2, nref2));
-                const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
-                uint64_t e01 = f32x2(e0, e1);
-                if constexpr (kSplit) {
-                  const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
-                  pk[i / 2] = __byte_perm(b0, b1, 0x7632);
-                  const float2 lo = f32x2_split(
-                      sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
-                  pk[16 + i / 2] = pack2(lo.x, lo.y, MT{});
-                } else {
-                  pk[i / 2] = pack2(e0, e1, MT{});
-                  const float2 hi = unpack2(pk[i / 2], MT{});
-                  e01 = f32x2(hi.x, hi.y);           // (l sums what is multiplied)
-                }
-                acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
-              }
-              if constexpr (kSplit)
-                tmem_st32u(ts + 32 * h, pk);
-              else
-                tmem_st16u(ts + 32 * h, pk);
-            }
-            const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
-            tmem_wait_st();
-            l_run[c] = l_run[c] * alpha + (s0.x + s0.y);
-            if (!waited) *abort_flag = 1;            // (the next exchange stops both warps)
-          }
-          tc_fence_before();
-          mbar_arrive(&p_full[sr.s]);
-          last[c] = sr;
-          sr.next();
+      const int base = sq.ctx - sq.n, nt = sg.t1 - sg.t0;
+      const bool two = NQ == 2 && sg.rows > kTreeRows;                // a row tile per group
+      const int tile = two ? grp : 0, row0 = tile * kTreeRows + quarter * 32, row = row0 + lane;
+      const bool live = row0 < sg.rows;                               // any row of this warp
+      const int unit_row = sg.unit * kTreeRows * NQ + row;            // of the sequence's rows
+      const int node = min(unit_row >> shift, sq.n - 1);
+      const uint32_t* words = p.mask + (static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words);
+      const float scale_log2 = p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] * kFold : 1.f);
+      const uint32_t to = tmem + lane_base + L::kOCol + tile * D;
+      float m_ref = -INFINITY, l_run = 0.f;
+      // take over the row's reference of the operation before
+      auto take_turn = [&]() -> bool {
+        const bool got = wait(their_turn, turns & 1);
+        ++turns;
+        const float m = red[r];
+        if (m != m_ref) l_run *= ex2_approx(m_ref - m);
+        m_ref = m;
+        return got;
+      };
+      // (a warp without rows still waits for every operation's scores, so that it
+      // arrives for its own ones in step)
+      for (int n = (two || !live) ? 0 : grp; n < nt; n += (two || !live) ? 1 : 2) {
+        const uint32_t k = ops + (two ? 2 * n + grp : n), buf = k % NB, ph = (k / NB) & 1;
+        if (!live) {
+          ok = wait(&s_full[buf], ph);
+          if (!ok) break;
+          if (two || (n & 1) == grp) mbar_arrive(&p_full[buf]);
+          continue;
         }
+        const int t = sg.t1 - 1 - n;
+        const bool tail = (t + 1) * kTreeKeys > base;
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (tail) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            see[w] = tree_bits(words, 2 * p.mask_words, sq.n, t * kTreeKeys + 32 * w - base);
+        }
+        const uint32_t ts = tmem + lane_base + buf * kTreeKeys;
+        // (its turn first: then the buffer's previous scores are known to be over)
+        if (!two && n > 0) ok = take_turn();
+        ok = ok && wait(&s_full[buf], ph);
+        if (!ok) break;
+        tc_fence_after();
+        float v[64];
+        auto load_half = [&](int h) {
+          tmem_ld64(ts + 64 * h, v);
+          if (tail) {
+            const uint32_t s0 = h ? see[2] : see[0], s1 = h ? see[3] : see[1];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = ((i < 32 ? s0 : s1) >> (i & 31)) & 1u ? v[i] : -INFINITY;
+          }
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          load_half(h);
+          mx = fmaxf(mx, max64(v));
+        }
+        const float m_tile = mx * scale_log2;
+        float alpha = 1.f;
+        if (m_tile > m_ref + kTRescaleLog2) {
+          alpha = ex2_approx(m_ref - m_tile);
+          m_ref = m_tile;
+        }
+        if (!two) {
+          red[r] = m_ref;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(my_turn);
+        }
+        if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O may be touched once the row tile's previous P V has completed
+          const uint32_t before = k - (two ? 2 : 1);
+          ok = wait(&pv_done[before % NB], (before / NB) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < D; x += 16) {
+            float o[16];
+            tmem_ld16(to + x, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(to + x, o);
+          }
+        }
+        const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        const uint64_t scale2 = f32x2(scale_log2, scale_log2), nref2 = f32x2(nref, nref);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        // the upper half is in registers; the lower one is read again
+#pragma unroll 1
+        for (int h = 1; h >= 0; --h) {
+          if (h == 0) load_half(0);
+          // a half's P: bf16, for each 32 keys 16 columns of pairs of the first part and
+          // 16 of the second; fp16, 32 columns of pairs
+          uint32_t pk[kSplit ? 64 : 32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float2 x = f32x2_split(fma_f32x2(f32x2(v[i], v[i + 1]), scale2, nref2));
+            const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+            uint64_t e01 = f32x2(e0, e1);
+            if constexpr (kSplit) {
+              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+              uint32_t* w = pk + 32 * (i / 32) + (i % 32) / 2;
+              w[0] = __byte_perm(b0, b1, 0x7632);
+              const float2 lo = f32x2_split(
+                  sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
+              w[16] = pack2(lo.x, lo.y, MT{});
+            } else {
+              pk[i / 2] = pack2(e0, e1, MT{});
+              const float2 hi = unpack2(pk[i / 2], MT{});
+              e01 = f32x2(hi.x, hi.y);               // (l sums what is multiplied)
+            }
+            acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
+          }
+          if constexpr (kSplit)
+            tmem_st64u(ts + 64 * h, pk);
+          else
+            tmem_st32u(ts + 64 * h, pk);
+        }
+        const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        tmem_wait_st();
+        l_run = l_run * alpha + (s0.x + s0.y);
+        tc_fence_before();
+        mbar_arrive(&p_full[buf]);
       }
       if (!ok) break;
+      const uint32_t last = ops + (two ? 2 * (nt - 1) + grp : nt - 1);
+      ops += two ? 2 * nt : nt;
+      const uint32_t piece_slot = slot++ % kTBadSlots;
+      if (!live) continue;
       // the piece's outputs or states, once the last P V is done
-      const Ring<NB> fin = last[nq - 1];
-      ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[fin.s], fin.ph, p.err, p.wait_limit_ns) && !*abort_flag);
-#pragma unroll
-      for (int c = 0; c < NQ; ++c) red[((2 * c) * 2 + half) * kTreeRows + r] = l_run[c];
-      if (named_bar_red_or(pair_bar, 64, !ok)) {
-        ok = false;
-        break;
+      ok = wait(&pv_done[last % NB], (last / NB) & 1);
+      float l = l_run;
+      if (!two && ok) {
+        if (((nt - 1) & 1) != grp) ok = take_turn();
+        // (two slots: the other group may still read the piece's before)
+        float* sums = red + kTreeRows + (joins & 1) * (2 * kTreeRows);
+        sums[grp * kTreeRows + r] = l_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&joined[grp * 4 + quarter]);
+        ok = ok && wait(&joined[(1 - grp) * 4 + quarter], joins & 1);
+        ++joins;
+        l = l_run + sums[(1 - grp) * kTreeRows + r];
       }
+      if (!ok) break;
       tc_fence_after();
       // drafted tokens of this piece with elements of V that are not finite
-      const uint32_t mine = bad[(slot % kTBadSlots) * (kTXform * 8) + lane];
+      const uint32_t mine = bad[piece_slot * (L::kXform * 8) + lane];
       const bool any_bad = __any_sync(0xffffffffu, mine != 0u);
-      ++slot;
       const bool direct = sg.t0 == 0 && sg.t1 == sg.kt;
-      const float v_scale = kFp8 ? p.v_scale[sg.g] : 1.f;
-#pragma unroll
-      for (int c = 0; c < NQ; ++c) {
-        if (c >= nq) break;
-        const int row0 = c * kTreeRows + quarter * 32, n_rows = sg.rows - row0;
-        if (n_rows <= 0) continue;
-        const int row = row0 + lane;
-        const int unit_row = sg.unit * kTreeRows * NQ + row;           // of the sequence's rows
-        const int node = min(unit_row >> shift, sq.n - 1), head = (sg.g << shift) + (unit_row & ((1 << shift) - 1));
-        const float l = l_run[c] + red[((2 * c) * 2 + (1 - half)) * kTreeRows + r];
-        const float weight = direct ? (l > 0.f ? v_scale / l : 0.f) : v_scale;
+      const float v_scale = kFp8 ? p.v_scale[sg.g] * kFold : 1.f;
+      const int n_rows = sg.rows - row0, head = (sg.g << shift) + (unit_row & ((1 << shift) - 1));
+      const float weight = direct ? (l > 0.f ? v_scale / l : 0.f) : v_scale;
+      // (of one row tile, each group writes half of the columns)
 #pragma unroll 1
-        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
-          float o[32];
-          tmem_ld32(tmem + lane_base + L::kOCol + c * D + x, o);
+      for (int x = two ? 0 : grp * (D / 2); x < (two ? D : (grp + 1) * (D / 2)); x += 32) {
+        float o[32];
+        tmem_ld32(to + x, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= weight;
-          if (any_bad) {
-            // (rare) every row adds what it sees of them
-            for (int w = 0; w < 8; ++w) {
-              uint32_t bits = 0;
+        for (int i = 0; i < 32; ++i) o[i] *= weight;
+        if (any_bad) {
+          // (rare) every row adds what it sees of them
+          for (int w = 0; w < 2 * p.mask_words; ++w) {
+            uint32_t bits = 0;
 #pragma unroll
-              for (int k = 0; k < kTXform; ++k) bits |= __shfl_sync(0xffffffffu, mine, 8 * k + w);
-              if (w >= 2 * p.mask_words) break;
-              bits &= p.mask[(static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words) + w];
-              for (; bits != 0u; bits &= bits - 1u) {
-                const int at = base + 32 * w + __ffs(bits) - 1;
-                const int id = p.block_tables[static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + at / kBlockSize];
-                if (id < 0 || id >= p.num_blocks) continue;
-                const int64_t e = ((static_cast<int64_t>(id) * p.n_kv_heads + sg.g) * kBlockSize + at % kBlockSize) * D;
+            for (int k = 0; k < L::kXform; ++k) bits |= __shfl_sync(0xffffffffu, mine, 8 * k + w);
+            for (bits &= words[w]; bits != 0u; bits &= bits - 1u) {
+              const int at = base + 32 * w + __ffs(bits) - 1;
+              const int id = p.block_tables[static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + at / kBlockSize];
+              if (id < 0 || id >= p.num_blocks) continue;
+              const int64_t e = ((static_cast<int64_t>(id) * p.n_kv_heads + sg.g) * kBlockSize + at % kBlockSize) * D;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                  float f[8];
-                  load8(static_cast<const unsigned char*>(p.v_cache) + (e + x + i) * KV::kBytes, f, KV{});
+              for (int i = 0; i < 32; i += 8) {
+                float f[8];
+                load8(static_cast<const unsigned char*>(p.v_cache) + (e + x + i) * KV::kBytes, f, KV{});
 #pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    if (!isfinite(f[k])) o[i + k] += f[k];
-                }
+                for (int k = 0; k < 8; ++k)
+                  if (!isfinite(f[k])) o[i + k] += f[k];
               }
             }
-            __syncwarp();
           }
-          if (direct) {
-            if (row < sg.rows) {
-              auto* dst = reinterpret_cast<uint4*>(
-                  static_cast<uint16_t*>(p.out) +
-                  ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + x);
-              const bool bf16 = kFp8 ? p.q_bf16 != 0 : kSplit;
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                dst[i / 8] = bf16 ? make_uint4(pack2(o[i], o[i + 1], BF16{}), pack2(o[i + 2], o[i + 3], BF16{}),
-                                               pack2(o[i + 4], o[i + 5], BF16{}), pack2(o[i + 6], o[i + 7], BF16{}))
-                                  : make_uint4(pack2(o[i], o[i + 1], F16{}), pack2(o[i + 2], o[i + 3], F16{}),
-                                               pack2(o[i + 4], o[i + 5], F16{}), pack2(o[i + 6], o[i + 7], F16{}));
-            }
-          } else {
-            store_rows32<D>(p.o + (sg.row + row0) * D + x, o, n_rows, lane);
-          }
+          __syncwarp();
         }
-        if (!direct && half == 0 && lane < n_rows)
-          *reinterpret_cast<float2*>(p.ml + (sg.row + row) * 2) = make_float2(m_ref[c], l);
+        if (direct) {
+          if (row < sg.rows) {
+            auto* dst = reinterpret_cast<uint4*>(
+                static_cast<uint16_t*>(p.out) + ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + x);
+            const bool bf16 = kFp8 ? p.q_bf16 != 0 : kSplit;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              dst[i / 8] = bf16 ? make_uint4(pack2(o[i], o[i + 1], BF16{}), pack2(o[i + 2], o[i + 3], BF16{}),
+                                             pack2(o[i + 4], o[i + 5], BF16{}), pack2(o[i + 6], o[i + 7], BF16{}))
+                                : make_uint4(pack2(o[i], o[i + 1], F16{}), pack2(o[i + 2], o[i + 3], F16{}),
+                                             pack2(o[i + 4], o[i + 5], F16{}), pack2(o[i + 6], o[i + 7], F16{}));
+          }
+        } else {
+          store_rows32<D>(p.o + (sg.row + row0) * D + x, o, n_rows, lane);
+        }
       }
-      // (the partner's sums have been read before the next piece's first maxima overwrite them)
-      named_bar_sync(pair_bar, 64);
+      if (!direct && (two || grp == 0) && lane < n_rows)
+        *reinterpret_cast<float2*>(p.ml + (sg.row + row) * 2) = make_float2(m_ref, l);
+      tc_fence_before();
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp == 8) {
-    // ============================ producer ============================
-    Ring<L::kKStages> kr;
-    Ring<L::kVStages> vr;
-    Ring<(kFp8 ? L::kCodeStages : 1)> cr;
-    uint32_t tiles = 0, pieces = 0, codes = 0;       // issued so far
+  } else if (warp == 8 || warp == 11) {
+    // ============================ producers: Q and K, V ============================
+    // (one warp each: V of a tile waits for an earlier P V than K of the tiles
+    // behind it; one warp for both, K behind V, cost 15 % of the whole)
+    set_max_regs_down<L::kRegsOther>();
+    const bool is_v = warp == 11;
+    constexpr int kKindStages = kFp8 ? L::kCodeStages : L::kVStages;   // V's; K's below
+    const uint32_t stages = kFp8 || is_v ? kKindStages : L::kKStages;
+    uint64_t* full = kFp8 ? c_full + (is_v ? L::kCodeStages : 0) : is_v ? v_full : k_full;
+    uint64_t* empty = kFp8 ? c_empty + (is_v ? L::kCodeStages : 0) : is_v ? v_empty : k_empty;
+    unsigned char* ring = sm + (kFp8 ? L::kCodes + (is_v ? L::kCodeStages * L::kStage : 0) : is_v ? L::kV : L::kK);
+    uint32_t s = 0, use = 0, tiles = 0, pieces = 0;  // stage and its use of the next tile; issued so far
     bool good = true;
-    pdl_wait_and_release();
+    if (is_v)
+      pdl_wait();
+    else
+      pdl_wait_and_release();
     for (int64_t pos = first; pos < end && good;) {
       const TreeSeg sg = segment(pos);
       pos = sg.next;
@@ -547,22 +641,24 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
         return (t >= sg.t0 && lane < kTTileBlocks && blk < nblk) ? row[blk] : -1;
       };
       int id = fetch_id(sg.t1 - 1);
-      // Q of the piece, once every Q K^T of the one before has read its tiles
-      if (pieces > 0)
-        good = __all_sync(0xffffffffu, mbar_wait(q_empty, (pieces - 1) & 1, p.err, p.wait_limit_ns) && !*abort_flag);
-      if (!good) break;
-      if (lane == 0) mbar_arrive_expect_tx(q_full, nq * (D / 64) * (p.q_box << shift) * 128);
-      ++pieces;
-      __syncwarp();
-      if (lane < nq * (D / 64)) {
-        const int c = lane / (D / 64), h = lane % (D / 64);
-        tma_load_3d(sm + L::kQ + c * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
-                    sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), q_full, policy_evict_last());
+      if (!is_v) {
+        // Q of the piece, once every Q K^T of the buffer's piece before has read it
+        const uint32_t qb = pieces % L::kQBufs, q_use = pieces / L::kQBufs;
+        if (q_use > 0) good = __all_sync(0xffffffffu, tree_wait(&q_empty[qb], (q_use - 1) & 1, p, abort_flag));
+        if (!good) break;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], nq * (D / 64) * (p.q_box << shift) * 128);
+        ++pieces;
+        __syncwarp();
+        if (lane < nq * (D / 64)) {
+          const int c = lane / (D / 64), h = lane % (D / 64);
+          tma_load_3d(sm + L::kQ + (qb * NQ + c) * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
+                      sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), &q_full[qb],
+                      policy_evict_last());
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      for (int t = sg.t1 - 1; t >= sg.t0 && good; --t) {
+      for (int t = sg.t1 - 1; t >= sg.t0; --t) {
         // cache slab of this lane's block: -1 behind the context or for a bad id
-        // (16-bit: read from outside the tensor, which fills with zeros)
         const int blk = t * kTTileBlocks + lane;
         bool have = lane < kTTileBlocks && blk < nblk;
         if (have && (id < 0 || id >= p.num_blocks)) {
@@ -571,56 +667,34 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
         }
         const int64_t slab = have ? static_cast<int64_t>(id) * p.n_kv_heads + sg.g : -1;
         id = fetch_id(t - 1);
+        good = __all_sync(0xffffffffu, use == 0 || tree_wait(&empty[s], (use - 1) & 1, p, abort_flag));
+        if (!good) break;
         if constexpr (!kFp8) {
-          auto load = [&](bool is_v) -> bool {
-            const uint32_t s = is_v ? vr.s : kr.s, ph = is_v ? vr.ph : kr.ph;
-            const bool used = tiles >= static_cast<uint32_t>(is_v ? L::kVStages : L::kKStages);
-            uint64_t* full = is_v ? &v_full[s] : &k_full[s];
-            const bool freed =
-                !used || mbar_wait(is_v ? &v_empty[s] : &k_empty[s], ph ^ 1u, p.err, p.wait_limit_ns);
-            if (!__all_sync(0xffffffffu, freed && !*abort_flag)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
-            __syncwarp();
-            if (lane < kTTileBlocks)
-              tma_load_4d(sm + (is_v ? L::kV : L::kK) + s * L::kTile + lane * (kBlockSize * D * 2),
-                          is_v ? &p.tmap_v : &p.tmap_k, static_cast<int>(slab) * 2, full, pol);
-            __syncwarp();
-            return true;
-          };
-          good = load(false);
-          if (good) {
-            kr.next();
-            good = load(true);
-          }
-          if (good) {
-            vr.next();
-            ++tiles;
-          } else if (!*abort_flag) {
-            *abort_flag = 1;
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
+          __syncwarp();
+          // (slab -1 is outside the tensor, which fills with zeros)
+          if (lane < kTTileBlocks)
+            tma_load_4d(ring + s * L::kTile + lane * (kBlockSize * D * 2), is_v ? &p.tmap_v : &p.tmap_k,
+                        static_cast<int>(slab) * 2, &full[s], pol);
         } else {
           constexpr int kSlab = kBlockSize * D;
-          for (int is_v = 0; is_v < 2 && good; ++is_v) {
-            const bool freed = codes < static_cast<uint32_t>(L::kCodeStages) ||
-                               mbar_wait(&c_empty[cr.s], cr.ph ^ 1u, p.err, p.wait_limit_ns);
-            good = __all_sync(0xffffffffu, freed && !*abort_flag);
-            if (!good) break;
-            unsigned char* dst = sm + L::kCodes + cr.s * L::kStage + lane * kSlab;
-            const uint32_t got = __ballot_sync(0xffffffffu, have);
-            if (lane < kTTileBlocks && !have) {      // (codes of 0; rare but for the last tile)
-              for (int x = 0; x < kSlab; x += 16)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(dst + x)), "r"(0u) : "memory");
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&c_full[cr.s], __popc(got) * kSlab);
-            __syncwarp();
-            if (have)
-              bulk_g2s(dst, (is_v ? p.v_codes : p.k_codes) + slab * kSlab, kSlab, &c_full[cr.s], pol);
-            __syncwarp();
-            ++codes;
-            cr.next();
+          unsigned char* dst = ring + s * L::kStage + lane * kSlab;
+          const uint32_t got = __ballot_sync(0xffffffffu, have);
+          if (lane < kTTileBlocks && !have) {        // (codes of 0; rare but for the last tile)
+            for (int x = 0; x < kSlab; x += 16)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(dst + x)), "r"(0u) : "memory");
+            fence_proxy_async_smem();
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(got) * kSlab);
+          __syncwarp();
+          if (have) bulk_g2s(dst, (is_v ? p.v_codes : p.k_codes) + slab * kSlab, kSlab, &full[s], pol);
+        }
+        __syncwarp();
+        ++tiles;
+        if (++s == stages) {
+          s = 0;
+          ++use;
         }
       }
     }
@@ -629,22 +703,14 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
       // The last loads of every stage land before the block ends (bounded, with the
       // full limit): whoever should wait for them may have stopped.
       const unsigned long long deadline = global_ns() + kWaitLimitNs;
-      if (pieces > 0) mbar_wait_until(q_full, (pieces - 1) & 1, deadline);
-      if constexpr (!kFp8) {
-        // (K of a tile whose V was not issued may be one further)
-        for (uint32_t t = tiles > L::kVStages ? tiles - L::kVStages : 0; t < tiles; ++t)
-          mbar_wait_until(&v_full[t % L::kVStages], (t / L::kVStages) & 1, deadline);
-        const uint32_t kt = tiles + (kr.s != tiles % L::kKStages ? 1 : 0);
-        for (uint32_t t = kt > L::kKStages ? kt - L::kKStages : 0; t < kt; ++t)
-          mbar_wait_until(&k_full[t % L::kKStages], (t / L::kKStages) & 1, deadline);
-      } else {
-        constexpr uint32_t n = L::kCodeStages;
-        for (uint32_t t = codes > n ? codes - n : 0; t < codes; ++t)
-          mbar_wait_until(&c_full[t % n], (t / n) & 1, deadline);
-      }
+      for (uint32_t n = pieces > L::kQBufs ? pieces - L::kQBufs : 0; n < pieces; ++n)
+        mbar_wait_until(&q_full[n % L::kQBufs], (n / L::kQBufs) & 1, deadline);
+      for (uint32_t n = tiles > stages ? tiles - stages : 0; n < tiles; ++n)
+        mbar_wait_until(&full[n % stages], (n / stages) & 1, deadline);
     }
     __syncwarp();
   } else if (warp < 11) {
+    set_max_regs_down<L::kRegsOther>();
     // ============================ MMA issuers (warps 9, 10) ============================
     // Warp 9 issues Q K^T, warp 10 P V, one elected lane each: a commit holds its
     // thread until the MMA queue has drained to a few entries; meanwhile the
@@ -663,14 +729,16 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
         pos = sg.next;
         if (sg.t0 >= sg.t1) continue;
         const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
+        const uint32_t qb = pieces % L::kQBufs;
         if (qk_warp) {
           // (the producer loads nothing while the previous kernel runs)
-          ok = mbar_wait_started_early(kFp8 && p.q_bf16 ? q_ready : q_full, pieces & 1, p.err, p.wait_limit_ns);
+          ok = mbar_wait_started_early(kFp8 && p.q_bf16 ? q_ready : &q_full[qb], (pieces / L::kQBufs) & 1, p.err,
+                                       p.wait_limit_ns);
         }
         ++pieces;
         for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t) {
           if (qk_warp)
-            ok = mbar_wait(&k_full[kr.s], kr.ph, p.err, p.wait_limit_ns);
+            ok = tree_wait(&k_full[kr.s], kr.ph, p, abort_flag);
           else
             ok = mbar_wait_started_early(&v_ready[vr.s], vr.ph, p.err, p.wait_limit_ns);
 #pragma unroll
@@ -679,10 +747,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
             const uint32_t d_s = tmem + sr.s * kTreeKeys;
             if (qk_warp) {
               // S once the P V that read P from its columns is done
-              ok = (ops < NB || mbar_wait(&pv_done[sr.s], sr.ph ^ 1u, p.err, p.wait_limit_ns)) && !*abort_flag;
+              ok = ops < NB || tree_wait(&pv_done[sr.s], sr.ph ^ 1u, p, abort_flag);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + c * L::kTile), 16, 1024);
+              const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (qb * NQ + c) * L::kTile), 16, 1024);
               const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
@@ -690,7 +758,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
                          b0 + static_cast<uint64_t>(((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
               umma_commit(&s_full[sr.s]);
             } else {
-              ok = mbar_wait(&p_full[sr.s], sr.ph, p.err, p.wait_limit_ns) && !*abort_flag;
+              ok = tree_wait(&p_full[sr.s], sr.ph, p, abort_flag);
               if (!ok) break;
               tc_fence_after();
               const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + vr.s * L::kTile), L::kHalf, L::kGroup);
@@ -699,7 +767,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
               for (int pass = 0; pass < kPasses; ++pass)
 #pragma unroll
                 for (int ks = 0; ks < kTreeKeys / 16; ++ks)
-                  umma_f16_tmem_a(d_o, d_s + 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1),
+                  umma_f16_tmem_a(d_o,
+                                  d_s + (kSplit ? 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1)
+                                                : 64 * (ks >> 2) + 8 * (ks & 3)),
                                   b0 + static_cast<uint64_t>((ks * 2 * L::kGroup) >> 4), kIdPV,
                                   t < sg.t1 - 1 || ks > 0 || pass > 0);
               umma_commit(&pv_done[sr.s]);
@@ -709,7 +779,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
           }
           if (!ok) break;
           umma_commit(qk_warp ? &k_empty[kr.s] : &v_empty[vr.s]);
-          if (qk_warp && t == sg.t0) umma_commit(q_empty);
+          if (qk_warp && t == sg.t0) umma_commit(&q_empty[qb]);
           kr.next();
           vr.next();
         }
@@ -721,8 +791,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
     }
     __syncwarp();
   } else {
-    // ============ warps 11-14: rows with drafted tokens, conversions ============
-    const int x_tid = tid - 11 * 32, x_warp = x_tid >> 5;
+    // ============ warps from 12 on: rows with drafted tokens, conversions ============
+    set_max_regs_down<L::kRegsOther>();
+    const bool is_v = !kFp8 || warp >= 12 + L::kXform;
+    const int x_tid = tid - (12 + (kFp8 && is_v ? L::kXform : 0)) * 32, x_warp = x_tid >> 5;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a 16-bit row
     Ring<L::kKStages> kr;
     Ring<L::kVStages> vr;
@@ -730,7 +802,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
     uint32_t pieces = 0, tiles = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t ph) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, ph, p.err, p.wait_limit_ns) && !*abort_flag);
+      return __all_sync(0xffffffffu, tree_wait(bar, ph, p, abort_flag));
     };
     pdl_wait();
     for (int64_t pos = first; pos < end && ok;) {
@@ -739,12 +811,19 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
       if (sg.t0 >= sg.t1) continue;
       const TreeSeq sq = seqs[sg.b];
       const int base = sq.ctx - sq.n;
-      uint32_t* my_bad = bad + (pieces % kTBadSlots) * (kTXform * 8) + x_warp * 8;
-      if (lane < 8) my_bad[lane] = 0u;
+      uint32_t* my_bad = bad + (pieces % kTBadSlots) * (L::kXform * 8) + x_warp * 8;
+      if (is_v && lane < 8) my_bad[lane] = 0u;
       __syncwarp();
       auto store = [&](uint32_t addr, const uint4& v) {
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                      : "memory");
+      };
+      auto load = [&](uint32_t addr) -> uint4 {
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(addr));
+        return v;
       };
       // 16-byte chunk c of key row j of a K / V tile
       auto at = [&](int j, int c) -> uint32_t {
@@ -764,12 +843,12 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
         return v;
       };
       if constexpr (kFp8) {
-        if (p.q_bf16) {
+        if (p.q_bf16 && !is_v) {
           // bf16 q to fp16, where it lies
           ok = wait_all(q_full, pieces & 1);
           if (!ok) break;
           const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-          for (int x = x_tid; x < nq * L::kTile / 16; x += kTXform * 32) {
+          for (int x = x_tid; x < nq * L::kTile / 16; x += L::kXform * 32) {
             uint4* w = reinterpret_cast<uint4*>(sm + L::kQ) + x;
             const uint4 v = *w;
             auto half2 = [&](uint32_t u) {
@@ -785,21 +864,15 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
       }
       ++pieces;
       for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t, ++tiles) {
-        const bool tail = (t + 1) * kTreeKeys > base;
         if constexpr (!kFp8) {
           ok = wait_all(&v_full[vr.s], vr.ph);
           if (!ok) break;
-          if (tail) {
+          if ((t + 1) * kTreeKeys > base) {          // rows from the first drafted token on
             const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
-            const int j0 = max(0, base - t * kTreeKeys);
-            for (int x = j0 * kChunks + x_tid; x < kTreeKeys * kChunks; x += kTXform * 32) {
+            for (int x = max(0, base - t * kTreeKeys) * kChunks + x_tid; x < kTreeKeys * kChunks; x += L::kXform * 32) {
               const int j = x / kChunks;
               const uint32_t addr = tile + at(j, x % kChunks);
-              uint4 v;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(addr));
-              const uint4 w = clean(v, t * kTreeKeys + j);
+              const uint4 v = load(addr), w = clean(v, t * kTreeKeys + j);
               if ((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) store(addr, w);
             }
             fence_proxy_async_smem();
@@ -808,45 +881,63 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(&v_ready[vr.s]);
           vr.next();
         } else {
-          for (int is_v = 0; is_v < 2 && ok; ++is_v) {
-            const uint32_t stages = is_v ? L::kVStages : L::kKStages;
-            uint64_t* empty = is_v ? &v_empty[vr.s] : &k_empty[kr.s];
-            ok = wait_all(&c_full[cr.s], cr.ph) &&
-                 (tiles < stages || wait_all(empty, (is_v ? vr.ph : kr.ph) ^ 1u));
-            if (!ok) break;
-            const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + cr.s * L::kStage);
-            const uint32_t tile = smem_u32(sm + (is_v ? L::kV + vr.s * L::kTile : L::kK + kr.s * L::kTile));
-            constexpr int kPer = kTreeKeys * D / 16 / (kTXform * 32);   // 16 codes each
+          const uint32_t stages = is_v ? L::kVStages : L::kKStages, code = (is_v ? L::kCodeStages : 0) + cr.s;
+          ok = wait_all(&c_full[code], cr.ph) &&
+               (tiles < stages || wait_all(is_v ? &v_empty[vr.s] : &k_empty[kr.s], (is_v ? vr.ph : kr.ph) ^ 1u));
+          if (!ok) break;
+          const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + code * L::kStage);
+          const uint32_t tile = smem_u32(sm + (is_v ? L::kV + vr.s * L::kTile : L::kK + kr.s * L::kTile));
+          // Chunk k of 16 codes of this thread is 4096 bytes of the tile behind chunk k - 1
+          // (whole groups of 8 keys), so its two places are constants away.  The lanes of
+          // a row's upper half convert and store its second 8 codes first: both halves of
+          // a row lie in the same banks.
+          constexpr int kAll = kTreeKeys * D / 16, kStep = L::kXform * 32;
+          static_assert(kStep / (D / 16) % 8 == 0 && kStep / (D / 16) / 8 * L::kGroup == 4096, "chunk step");
+          constexpr int kPer = 4;                    // chunks whose instructions interleave
+          const int j0 = x_tid / (D / 16), c0 = x_tid % (D / 16);
+          const bool up = D == 128 && (c0 & 4);
+          const uint32_t first8 = tile + at(j0, 2 * c0 + (up ? 1 : 0)), last8 = tile + at(j0, 2 * c0 + (up ? 0 : 1));
+          uint32_t nan = 0;
+#pragma unroll 1
+          for (int k0 = 0; k0 < kAll / kStep; k0 += kPer) {
             uint4 raw[kPer];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + k * kTXform * 32];
+            for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + (k0 + k) * kStep];
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-              const int x = x_tid + k * kTXform * 32, j = x / (D / 16), c = x % (D / 16);
-              uint4 h[2];
-              const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                h[e] = make_uint4(byte2_to_f16x2(w[2 * e], KV{}), byte2_hi_to_f16x2(w[2 * e], KV{}),
-                                  byte2_to_f16x2(w[2 * e + 1], KV{}), byte2_hi_to_f16x2(w[2 * e + 1], KV{}));
-              if (is_v && tail) {
-                h[0] = clean(h[0], t * kTreeKeys + j);
-                h[1] = clean(h[1], t * kTreeKeys + j);
-              }
-              // (the upper half of a row's lanes stores its second chunk first: the two
-              // halves of the row lie in the same banks)
-              const bool up = D == 128 && (c & 4);
-              store(tile + at(j, 2 * c + (up ? 1 : 0)), up ? h[1] : h[0]);
-              store(tile + at(j, 2 * c + (up ? 0 : 1)), up ? h[0] : h[1]);
+              const uint4 w = raw[k];
+              nan |= nan_codes(w.x, KV{}) | nan_codes(w.y, KV{}) | nan_codes(w.z, KV{}) | nan_codes(w.w, KV{});
+              const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
+              const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
+              store(first8 + (k0 + k) * 4096, make_uint4(w0.x, w0.y, w1.x, w1.y));
+              store(last8 + (k0 + k) * 4096, make_uint4(w2.x, w2.y, w3.x, w3.y));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&c_empty[cr.s]);
-              mbar_arrive(is_v ? &v_ready[vr.s] : &k_full[kr.s]);
-            }
-            cr.next();
           }
+          const bool tail = is_v && (t + 1) * kTreeKeys > base;
+          if (tail || (nan & 0x80808080u)) {
+            // (rare) E4M3's NaN codes became numbers; V rows from the first drafted
+            // token on.  Each thread looks at what it wrote.
+#pragma unroll 1
+            for (int x = x_tid; x < kAll; x += L::kXform * 32) {
+              const int j = x / (D / 16), c = x % (D / 16);
+#pragma unroll 1
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t addr = tile + at(j, 2 * c + e);
+                uint4 v = load(addr);
+                const uint2 w = reinterpret_cast<const uint2*>(codes + x)[e];
+                v.x |= nan_halves(w.x, KV{}), v.y |= nan_halves(w.x >> 16, KV{});
+                v.z |= nan_halves(w.y, KV{}), v.w |= nan_halves(w.y >> 16, KV{});
+                store(addr, tail ? clean(v, t * kTreeKeys + j) : v);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&c_empty[code]);
+            mbar_arrive(is_v ? &v_ready[vr.s] : &k_full[kr.s]);
+          }
+          cr.next();
           kr.next();
           vr.next();
         }
@@ -862,13 +953,13 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------------------
-// The merge: a thread block per 16 query rows of a (sequence, KV head), a warp per
-// row in turn.  Lane x finds range r0 + x's piece of the row's unit (two divisions
-// for all of a warp's rows of one unit); the states are joined as in the other
-// merges, 8 pieces' loads at a time.  Units that one range held are done.
+// The merge: a warp per query row, a thread block per 8 rows of a (sequence, KV
+// head).  Lane x finds range r0 + x's piece of the row's unit; the states are
+// joined as in the other merges, with the first pieces' outputs loaded beside
+// their weights.  Units that one range held are done.  All latency: (a warp for
+// four rows in turn: 24 us behind a 150 us kernel whose units met 19 ranges each).
 // ---------------------------------------------------------------------------
-constexpr int kTMergeRows = 16;
-constexpr int kTMergeWarps = 4;
+constexpr int kTMergeWarps = 8;
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(kTMergeWarps * 32)
@@ -879,82 +970,84 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
   pdl_wait_and_release();
   const TreeSeq sq = p.seqs[b];
   const int64_t V = p.seqs[p.batch].cost, R = ranges;
-  const int rows = sq.n << shift, row0 = blockIdx.x * kTMergeRows;
-  if (row0 >= rows) return;
-  const int units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx), unit = row0 / kUnit;   // (16 rows lie in one unit)
+  const int rows = sq.n << shift, row = blockIdx.x * kTMergeWarps + warp;
+  if (row >= rows) return;
+  const int units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx), unit = row / kUnit;
   const int64_t cost = tree_unit_cost(rows, kt), u0 = sq.cost + (static_cast<int64_t>(g) * units + unit) * cost;
   // ranges whose part of the axis meets the unit: r0 .. r1
   const int64_t r0 = div_nonneg((u0 + 1) * R + V - 1, V) - 1;
   const int64_t r1 = div_nonneg((u0 + cost) * R + V - 1, V) - 1;
-  auto tiles_of = [&](int64_t r, int& t0, int& t1) {
-    t0 = tree_tile_at(max(div_nonneg(r * V, R) - u0, static_cast<int64_t>(0)), rows, kt);
-    t1 = tree_tile_at(max(min(div_nonneg((r + 1) * V, R) - u0, cost), static_cast<int64_t>(0)), rows, kt);
-  };
-  const int64_t base = tree_piece_row(sq.start, p.n_q_heads, g, rows, static_cast<int64_t>(unit) * kUnit, 0, kUnit);
-  for (int row = row0 + warp; row < min(row0 + kTMergeRows, rows); row += kTMergeWarps) {
-    float M = -INFINITY, Lsum = 0.f, O[N] = {};
-    for (int64_t x0 = r0; x0 <= r1; x0 += 32) {
-      const int64_t r = x0 + lane;
-      int t0 = 0, t1 = 0;
-      if (r <= r1) tiles_of(r, t0, t1);
-      if (__any_sync(0xffffffffu, t0 == 0 && t1 == kt)) return;      // written where it was computed
-      const bool have = t0 < t1;
-      const int64_t at = base + r * kUnit + (row - unit * kUnit);
-      const float2 st = have ? *reinterpret_cast<const float2*>(p.ml + at * 2) : make_float2(-INFINITY, 0.f);
-      uint32_t left = __ballot_sync(0xffffffffu, have);
-      float m = st.x;
+  const int64_t base = tree_piece_row(sq.start, p.n_q_heads, g, rows, static_cast<int64_t>(unit) * kUnit, 0, kUnit) +
+                       (row - unit * kUnit);
+  float M = -INFINITY, Lsum = 0.f, O[N] = {};
+  for (int64_t x0 = r0; x0 <= r1; x0 += 32) {
+    const int64_t r = x0 + lane;
+    int t0 = 0, t1 = 0;
+    if (r <= r1) {
+      t0 = tree_tile_at(max(div_nonneg(r * V, R) - u0, static_cast<int64_t>(0)), rows, kt);
+      t1 = tree_tile_at(max(min(div_nonneg((r + 1) * V, R) - u0, cost), static_cast<int64_t>(0)), rows, kt);
+    }
+    if (__any_sync(0xffffffffu, t0 == 0 && t1 == kt)) return;        // written where it was computed
+    const bool have = t0 < t1;
+    const float2 st = have ? *reinterpret_cast<const float2*>(p.ml + (base + r * kUnit) * 2)
+                           : make_float2(-INFINITY, 0.f);
+    uint32_t left = __ballot_sync(0xffffffffu, have);
+    float v[kBatch][N];
+    int src[kBatch];
+    auto load_batch = [&]() {
 #pragma unroll
-      for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-      const float mn = fmaxf(M, m), ref = (mn == -INFINITY) ? 0.f : mn;
-      const float keep = exp2f(M - ref), w = exp2f(st.x - ref);
-      float l = w * st.y;
-#pragma unroll
-      for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-      Lsum = Lsum * keep + l;
-      M = mn;
-#pragma unroll
-      for (int e = 0; e < N; ++e) O[e] *= keep;
-      while (left) {
-        float v[kBatch][N];
-        int src[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          src[q] = left ? __ffs(left) - 1 : -1;
-          left &= left - 1;          // (0 stays 0)
-          if (src[q] >= 0) {
-            const float* from =
-                p.o + (base + (x0 + src[q]) * kUnit + (row - unit * kUnit)) * D + N * lane;
-            if constexpr (N == 4) {
-              const float4 f = *reinterpret_cast<const float4*>(from);
-              v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
-            } else {
-              const float2 f = *reinterpret_cast<const float2*>(from);
-              v[q][0] = f.x, v[q][1] = f.y;
-            }
+      for (int q = 0; q < kBatch; ++q) {
+        src[q] = left ? __ffs(left) - 1 : -1;
+        left &= left - 1;          // (0 stays 0)
+        if (src[q] >= 0) {
+          const float* from = p.o + (base + (x0 + src[q]) * kUnit) * D + N * lane;
+          if constexpr (N == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(from);
+            v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(from);
+            v[q][0] = f.x, v[q][1] = f.y;
           }
         }
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const float wq = __shfl_sync(0xffffffffu, w, src[q] < 0 ? 0 : src[q]);
-          if (src[q] >= 0)
-#pragma unroll
-            for (int e = 0; e < N; ++e) O[e] = fmaf(wq, v[q][e], O[e]);
-        }
       }
-    }
-    const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
-    const int node = row >> shift, head = (g << shift) + (row & ((1 << shift) - 1));
-    uint16_t* out = static_cast<uint16_t*>(p.out) +
-                    ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + N * lane;
-    uint32_t w[N / 2];
+    };
+    load_batch();
+    float m = st.x;
 #pragma unroll
-    for (int e = 0; e < N; e += 2)
-      w[e / 2] = p.q_bf16 ? pack2(O[e] * inv, O[e + 1] * inv, BF16{}) : pack2(O[e] * inv, O[e + 1] * inv, F16{});
-    if constexpr (N == 4)
-      *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(out) = w[0];
+    for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float mn = fmaxf(M, m), ref = (mn == -INFINITY) ? 0.f : mn;
+    const float keep = exp2f(M - ref), w = exp2f(st.x - ref);
+    float l = w * st.y;
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    Lsum = Lsum * keep + l;
+    M = mn;
+#pragma unroll
+    for (int e = 0; e < N; ++e) O[e] *= keep;
+    while (true) {
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const float wq = __shfl_sync(0xffffffffu, w, src[q] < 0 ? 0 : src[q]);
+        if (src[q] >= 0)
+#pragma unroll
+          for (int e = 0; e < N; ++e) O[e] = fmaf(wq, v[q][e], O[e]);
+      }
+      if (left == 0) break;
+      load_batch();
+    }
   }
+  const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
+  const int node = row >> shift, head = (g << shift) + (row & ((1 << shift) - 1));
+  uint16_t* out = static_cast<uint16_t*>(p.out) +
+                  ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + N * lane;
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int e = 0; e < N; e += 2)
+    w[e / 2] = p.q_bf16 ? pack2(O[e] * inv, O[e + 1] * inv, BF16{}) : pack2(O[e] * inv, O[e + 1] * inv, F16{});
+  if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
 template <typename MT, typename KV, int D, int NQ>
@@ -977,10 +1070,10 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
       done[dev] = true;
     }
   }
-  if (cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(kTThreads), L::bytes(p.batch), stream, p),
+  if (cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(L::kThreads), L::bytes(p.batch), stream, p),
                   "tree_kernel launch"))
     return PKV_ERR_CUDA;
-  const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeRows - 1) / kTMergeRows;
+  const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeWarps - 1) / kTMergeWarps;
   const dim3 grid(chunks, static_cast<unsigned>(p.n_kv_heads), static_cast<unsigned>(p.batch));
   return cuda_failed(launch_pdl(tree_merge_kernel<D, NQ>, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges),
                      "tree_merge_kernel launch")
