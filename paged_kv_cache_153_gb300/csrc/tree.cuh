@@ -34,7 +34,7 @@
 //                 and share its outputs: each passes the row's reference on through
 //                 shared memory before its exponentials.  Of two row tiles, each
 //                 has its own.  P overwrites S.  bf16 P is two bf16 parts (p
-//                 truncated, the rounded remainder: exact to 2^-16, where one
+//                 to 8 bits, the remainder to 8: exact to 2^-16, where one
 //                 rounding, 2^-9, would be as large as the output's own); fp16 P
 //                 (2^-12) is rounded once, and l sums the rounded values.  The row
 //                 reference moves only when a tile's maximum exceeds it by more
@@ -278,17 +278,19 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   uint64_t* c_full = v_empty + L::kVStages;        // [2 kCodeStages] codes of K, of V landed
   uint64_t* c_empty = c_full + 2 * L::kCodeStages; // converted
   uint64_t* s_full = c_empty + 2 * L::kCodeStages; // [NB] scores ready
-  uint64_t* p_full = s_full + NB;                  // [NB] P written, O rescaled
+  uint64_t* p_half = s_full + NB;                  // [NB] P of the upper keys written, O rescaled
+  uint64_t* p_full = p_half + NB;                  // [NB] and of the lower ones
   uint64_t* pv_done = p_full + NB;                 // [NB] P V done
   uint64_t* q_full = pv_done + NB;                 // [kQBufs] Q of a piece landed
   uint64_t* q_empty = q_full + L::kQBufs;          // [kQBufs] its Q K^T done
   uint64_t* q_ready = q_empty + L::kQBufs;         // Q converted (FP8)
   uint64_t* turn = q_ready + 1;                    // [2][4] a group's warp has passed its rows' references on
   uint64_t* joined = turn + 8;                     // [2][4] and its sums of a piece
-  uint64_t* mma_idle = joined + 8;                 // [2] an issuer's MMAs done
+  uint64_t* o_read = joined + 8;                   // 8 arrivals: a piece's outputs are out of TMEM
+  uint64_t* mma_idle = o_read + 1;                 // [2] an issuer's MMAs done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * 2 + 3 * 3 + 2 * 4 + 3 * 3 + 5 + 16 + 2 + 1) * 8 <= 512, "barrier block overflows");
+  static_assert((2 * 2 + 3 * 3 + 2 * 4 + 4 * 3 + 5 + 17 + 2 + 1) * 8 <= 512, "barrier block overflows");
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + L::kBad);
   float* red = reinterpret_cast<float*>(sm + L::kRed);
   TreeSeq* seqs = reinterpret_cast<TreeSeq*>(sm + L::kSeqs);
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
     }
     for (int s = 0; s < NB; ++s) {
       mbar_init(&s_full[s], 1);
+      mbar_init(&p_half[s], kTSoftmax / 2);
       mbar_init(&p_full[s], kTSoftmax / 2);
       mbar_init(&pv_done[s], 1);
     }
@@ -330,6 +333,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       mbar_init(&turn[s], 1);
       mbar_init(&joined[s], 1);
     }
+    mbar_init(o_read, kTSoftmax / 32);
     mbar_init(&mma_idle[0], 1);
     mbar_init(&mma_idle[1], 1);
     fence_mbar_init();
@@ -426,14 +430,19 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         m_ref = m;
         return got;
       };
-      // (a warp without rows still waits for every operation's scores, so that it
-      // arrives for its own ones in step)
-      for (int n = (two || !live) ? 0 : grp; n < nt; n += (two || !live) ? 1 : 2) {
+      // A warp waits for a phase of a barrier only where the phase behind it needs
+      // that warp, and only once the phase before it is known to be over (a parity
+      // tells no more than two apart).  So a warp without rows takes part in
+      // everything but the arithmetic.
+      for (int n = two ? 0 : grp; n < nt; n += two ? 1 : 2) {
         const uint32_t k = ops + (two ? 2 * n + grp : n), buf = k % NB, ph = (k / NB) & 1;
         if (!live) {
-          ok = wait(&s_full[buf], ph);
+          if (!two && n > 0) ok = take_turn();
+          ok = ok && wait(&s_full[buf], ph);
           if (!ok) break;
-          if (two || (n & 1) == grp) mbar_arrive(&p_full[buf]);
+          if (!two && lane == 0) mbar_arrive(my_turn);
+          mbar_arrive(&p_half[buf]);
+          mbar_arrive(&p_full[buf]);
           continue;
         }
         const int t = sg.t1 - 1 - n;
@@ -507,11 +516,13 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
             const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
             uint64_t e01 = f32x2(e0, e1);
             if constexpr (kSplit) {
-              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+              // hi = e to 8 bits, as u - (u - e) with u = (2^16 + 1) e (Dekker's splitting):
+              // packed multiplies and additions, where masks would fill the integer pipe
+              const uint64_t u = fma_f32x2(e01, f32x2(65537.f, 65537.f), 0ull);
+              const uint64_t hi = sub_f32x2(u, sub_f32x2(u, e01));
+              const float2 h2 = f32x2_split(hi), lo = f32x2_split(sub_f32x2(e01, hi));
               uint32_t* w = pk + 32 * (i / 32) + (i % 32) / 2;
-              w[0] = __byte_perm(b0, b1, 0x7632);
-              const float2 lo = f32x2_split(
-                  sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
+              w[0] = __byte_perm(__float_as_uint(h2.x), __float_as_uint(h2.y), 0x7632);
               w[16] = pack2(lo.x, lo.y, MT{});
             } else {
               pk[i / 2] = pack2(e0, e1, MT{});
@@ -524,6 +535,12 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
             tmem_st64u(ts + 64 * h, pk);
           else
             tmem_st32u(ts + 64 * h, pk);
+          if (h == 1) {
+            // (their product may run while the lower keys' weights are computed)
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_half[buf]);
+          }
         }
         const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
         tmem_wait_st();
@@ -535,12 +552,12 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const uint32_t last = ops + (two ? 2 * (nt - 1) + grp : nt - 1);
       ops += two ? 2 * nt : nt;
       const uint32_t piece_slot = slot++ % kTBadSlots;
-      if (!live) continue;
-      // the piece's outputs or states, once the last P V is done
-      ok = wait(&pv_done[last % NB], (last / NB) & 1);
+      // the piece's outputs or states, once the last P V is done (with the last turn
+      // taken, its scores are known to be over, and so is the buffer's P V before)
+      if (!two && ((nt - 1) & 1) != grp) ok = take_turn();
+      ok = ok && wait(&pv_done[last % NB], (last / NB) & 1);
       float l = l_run;
       if (!two && ok) {
-        if (((nt - 1) & 1) != grp) ok = take_turn();
         // (two slots: the other group may still read the piece's before)
         float* sums = red + kTreeRows + (joins & 1) * (2 * kTreeRows);
         sums[grp * kTreeRows + r] = l_run;
@@ -552,6 +569,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       }
       if (!ok) break;
       tc_fence_after();
+      if (!live) {
+        if (lane == 0) mbar_arrive(o_read);
+        continue;
+      }
       // drafted tokens of this piece with elements of V that are not finite
       const uint32_t mine = bad[piece_slot * (L::kXform * 8) + lane];
       const bool any_bad = __any_sync(0xffffffffu, mine != 0u);
@@ -608,6 +629,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       if (!direct && (two || grp == 0) && lane < n_rows)
         *reinterpret_cast<float2*>(p.ml + (sg.row + row) * 2) = make_float2(m_ref, l);
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_read);
     }
     if (!ok) *abort_flag = 1;
   } else if (warp == 8 || warp == 11) {
@@ -735,6 +758,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           ok = mbar_wait_started_early(kFp8 && p.q_bf16 ? q_ready : &q_full[qb], (pieces / L::kQBufs) & 1, p.err,
                                        p.wait_limit_ns);
         }
+        // (the piece's first P V overwrites the outputs of the piece before)
+        if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
         ++pieces;
         for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t) {
           if (qk_warp)
@@ -758,20 +783,27 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
                          b0 + static_cast<uint64_t>(((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
               umma_commit(&s_full[sr.s]);
             } else {
-              ok = tree_wait(&p_full[sr.s], sr.ph, p, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
               const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + vr.s * L::kTile), L::kHalf, L::kGroup);
               const uint32_t d_o = tmem + L::kOCol + c * D;
+              // the upper keys' P first
+              auto half = [&](auto upper) {
+                constexpr int h = decltype(upper)::value;
+                tc_fence_after();
 #pragma unroll
-              for (int pass = 0; pass < kPasses; ++pass)
+                for (int pass = 0; pass < kPasses; ++pass)
 #pragma unroll
-                for (int ks = 0; ks < kTreeKeys / 16; ++ks)
-                  umma_f16_tmem_a(d_o,
-                                  d_s + (kSplit ? 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1)
-                                                : 64 * (ks >> 2) + 8 * (ks & 3)),
-                                  b0 + static_cast<uint64_t>((ks * 2 * L::kGroup) >> 4), kIdPV,
-                                  t < sg.t1 - 1 || ks > 0 || pass > 0);
+                  for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                    umma_f16_tmem_a(d_o,
+                                    d_s + (kSplit ? 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1)
+                                                  : 64 * (ks >> 2) + 8 * (ks & 3)),
+                                    b0 + static_cast<uint64_t>((ks * 2 * L::kGroup) >> 4), kIdPV,
+                                    t < sg.t1 - 1 || h == 0 || ks > 4 || pass > 0);
+              };
+              ok = tree_wait(&p_half[sr.s], sr.ph, p, abort_flag);
+              if (ok) half(std::integral_constant<int, 1>{});
+              ok = ok && tree_wait(&p_full[sr.s], sr.ph, p, abort_flag);
+              if (!ok) break;
+              half(std::integral_constant<int, 0>{});
               umma_commit(&pv_done[sr.s]);
             }
             ++ops;
