@@ -34,7 +34,7 @@
 //                 and share its outputs: each passes the row's reference on through
 //                 shared memory before its exponentials.  Of two row tiles, each
 //                 has its own.  P overwrites S.  bf16 P is two bf16 parts (p
-//                 to 8 bits, the remainder to 8: exact to 2^-16, where one
+//                 truncated, the rounded remainder: exact to 2^-16, where one
 //                 rounding, 2^-9, would be as large as the output's own); fp16 P
 //                 (2^-12) is rounded once, and l sums the rounded values.  The row
 //                 reference moves only when a tile's maximum exceeds it by more
@@ -516,13 +516,11 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
             const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
             uint64_t e01 = f32x2(e0, e1);
             if constexpr (kSplit) {
-              // hi = e to 8 bits, as u - (u - e) with u = (2^16 + 1) e (Dekker's splitting):
-              // packed multiplies and additions, where masks would fill the integer pipe
-              const uint64_t u = fma_f32x2(e01, f32x2(65537.f, 65537.f), 0ull);
-              const uint64_t hi = sub_f32x2(u, sub_f32x2(u, e01));
-              const float2 h2 = f32x2_split(hi), lo = f32x2_split(sub_f32x2(e01, hi));
+              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+              const float2 lo = f32x2_split(
+                  sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
               uint32_t* w = pk + 32 * (i / 32) + (i % 32) / 2;
-              w[0] = __byte_perm(__float_as_uint(h2.x), __float_as_uint(h2.y), 0x7632);
+              w[0] = __byte_perm(b0, b1, 0x7632);
               w[16] = pack2(lo.x, lo.y, MT{});
             } else {
               pk[i / 2] = pack2(e0, e1, MT{});
@@ -985,33 +983,41 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
 }
 
 // ---------------------------------------------------------------------------
-// The merge: a warp per query row, a thread block per 8 rows of a (sequence, KV
-// head).  Lane x finds range r0 + x's piece of the row's unit; the states are
-// joined as in the other merges, with the first pieces' outputs loaded beside
-// their weights.  Units that one range held are done.  All latency: (a warp for
-// four rows in turn: 24 us behind a 150 us kernel whose units met 19 ranges each).
+// The merge: a warp per NR query rows of a (sequence, KV head).  Lane x finds range
+// r0 + x's piece of the rows' unit; the states are joined as in the other merges,
+// with the first pieces' outputs loaded beside their weights.  Units that one range
+// held are done.  It is all latency, so a warp takes one row and eight pieces at a
+// time where the rows' warps fit the GPU at once, and else four rows and two pieces.
+// (32 sequences of 1024 to 16384 tokens: 11.4 us; one row a warp 18.5 us.  One
+// of 131072, 19 pieces a row: 8.1 us; four rows one after another 24 us.)
 // ---------------------------------------------------------------------------
 constexpr int kTMergeWarps = 8;
 
-template <int D, int NQ>
+template <int D, int NQ, int NR>
 __global__ void __launch_bounds__(kTMergeWarps * 32)
     tree_merge_kernel(const __grid_constant__ TreeParams p, int ranges) {
-  constexpr int N = D / 32, kBatch = 8, kUnit = kTreeRows * NQ;
+  constexpr int N = D / 32, kBatch = 8 / NR, kUnit = kTreeRows * NQ;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z, g = blockIdx.y, shift = p.group_shift;
   pdl_wait_and_release();
   const TreeSeq sq = p.seqs[b];
   const int64_t V = p.seqs[p.batch].cost, R = ranges;
-  const int rows = sq.n << shift, row = blockIdx.x * kTMergeWarps + warp;
-  if (row >= rows) return;
-  const int units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx), unit = row / kUnit;
+  const int rows = sq.n << shift, row0 = (blockIdx.x * kTMergeWarps + warp) * NR;
+  if (row0 >= rows) return;
+  const int units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx), unit = row0 / kUnit;   // (NR divides kUnit)
   const int64_t cost = tree_unit_cost(rows, kt), u0 = sq.cost + (static_cast<int64_t>(g) * units + unit) * cost;
   // ranges whose part of the axis meets the unit: r0 .. r1
   const int64_t r0 = div_nonneg((u0 + 1) * R + V - 1, V) - 1;
   const int64_t r1 = div_nonneg((u0 + cost) * R + V - 1, V) - 1;
   const int64_t base = tree_piece_row(sq.start, p.n_q_heads, g, rows, static_cast<int64_t>(unit) * kUnit, 0, kUnit) +
-                       (row - unit * kUnit);
-  float M = -INFINITY, Lsum = 0.f, O[N] = {};
+                       (row0 - unit * kUnit);
+  float M[NR], Lsum[NR], O[NR][N];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    M[i] = -INFINITY, Lsum[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) O[i][e] = 0.f;
+  }
   for (int64_t x0 = r0; x0 <= r1; x0 += 32) {
     const int64_t r = x0 + lane;
     int t0 = 0, t1 = 0;
@@ -1021,65 +1027,83 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
     }
     if (__any_sync(0xffffffffu, t0 == 0 && t1 == kt)) return;        // written where it was computed
     const bool have = t0 < t1;
-    const float2 st = have ? *reinterpret_cast<const float2*>(p.ml + (base + r * kUnit) * 2)
-                           : make_float2(-INFINITY, 0.f);
     uint32_t left = __ballot_sync(0xffffffffu, have);
-    float v[kBatch][N];
+    float2 st[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      st[i] = have && row0 + i < rows ? *reinterpret_cast<const float2*>(p.ml + (base + i + r * kUnit) * 2)
+                                      : make_float2(-INFINITY, 0.f);
+    float v[kBatch][NR][N];
     int src[kBatch];
     auto load_batch = [&]() {
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         src[q] = left ? __ffs(left) - 1 : -1;
         left &= left - 1;          // (0 stays 0)
-        if (src[q] >= 0) {
-          const float* from = p.o + (base + (x0 + src[q]) * kUnit) * D + N * lane;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          if (src[q] < 0 || row0 + i >= rows) continue;
+          const float* from = p.o + (base + i + (x0 + src[q]) * kUnit) * D + N * lane;
           if constexpr (N == 4) {
             const float4 f = *reinterpret_cast<const float4*>(from);
-            v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
+            v[q][i][0] = f.x, v[q][i][1] = f.y, v[q][i][2] = f.z, v[q][i][3] = f.w;
           } else {
             const float2 f = *reinterpret_cast<const float2*>(from);
-            v[q][0] = f.x, v[q][1] = f.y;
+            v[q][i][0] = f.x, v[q][i][1] = f.y;
           }
         }
       }
     };
     load_batch();
-    float m = st.x;
+    float w[NR];
 #pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    const float mn = fmaxf(M, m), ref = (mn == -INFINITY) ? 0.f : mn;
-    const float keep = exp2f(M - ref), w = exp2f(st.x - ref);
-    float l = w * st.y;
+    for (int i = 0; i < NR; ++i) {
+      float m = st[i].x;
 #pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    Lsum = Lsum * keep + l;
-    M = mn;
+      for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      const float mn = fmaxf(M[i], m), ref = (mn == -INFINITY) ? 0.f : mn;
+      const float keep = exp2f(M[i] - ref);
+      w[i] = exp2f(st[i].x - ref);
+      float l = w[i] * st[i].y;
 #pragma unroll
-    for (int e = 0; e < N; ++e) O[e] *= keep;
+      for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      Lsum[i] = Lsum[i] * keep + l;
+      M[i] = mn;
+#pragma unroll
+      for (int e = 0; e < N; ++e) O[i][e] *= keep;
+    }
     while (true) {
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const float wq = __shfl_sync(0xffffffffu, w, src[q] < 0 ? 0 : src[q]);
-        if (src[q] >= 0)
+      for (int q = 0; q < kBatch; ++q)
 #pragma unroll
-          for (int e = 0; e < N; ++e) O[e] = fmaf(wq, v[q][e], O[e]);
-      }
+        for (int i = 0; i < NR; ++i) {
+          const float wq = __shfl_sync(0xffffffffu, w[i], src[q] < 0 ? 0 : src[q]);
+          if (src[q] < 0 || row0 + i >= rows) continue;
+#pragma unroll
+          for (int e = 0; e < N; ++e) O[i][e] = fmaf(wq, v[q][i][e], O[i][e]);
+        }
       if (left == 0) break;
       load_batch();
     }
   }
-  const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
-  const int node = row >> shift, head = (g << shift) + (row & ((1 << shift) - 1));
-  uint16_t* out = static_cast<uint16_t*>(p.out) +
-                  ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + N * lane;
-  uint32_t w[N / 2];
 #pragma unroll
-  for (int e = 0; e < N; e += 2)
-    w[e / 2] = p.q_bf16 ? pack2(O[e] * inv, O[e + 1] * inv, BF16{}) : pack2(O[e] * inv, O[e + 1] * inv, F16{});
-  if constexpr (N == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(out) = w[0];
+  for (int i = 0; i < NR; ++i) {
+    const int row = row0 + i;
+    if (row >= rows) break;
+    const float inv = Lsum[i] > 0.f ? 1.f / Lsum[i] : 0.f;
+    const int node = row >> shift, head = (g << shift) + (row & ((1 << shift) - 1));
+    uint16_t* out = static_cast<uint16_t*>(p.out) +
+                    ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + N * lane;
+    uint32_t x[N / 2];
+#pragma unroll
+    for (int e = 0; e < N; e += 2)
+      x[e / 2] = p.q_bf16 ? pack2(O[i][e] * inv, O[i][e + 1] * inv, BF16{})
+                          : pack2(O[i][e] * inv, O[i][e + 1] * inv, F16{});
+    if constexpr (N == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = x[0];
+  }
 }
 
 template <typename MT, typename KV, int D, int NQ>
@@ -1105,10 +1129,12 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   if (cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(L::kThreads), L::bytes(p.batch), stream, p),
                   "tree_kernel launch"))
     return PKV_ERR_CUDA;
-  const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeWarps - 1) / kTMergeWarps;
+  // (64 warps an SM)
+  const int nr = p.num_tokens * p.n_q_heads > 64ll * sm_count() ? 4 : 1;
+  const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeWarps * nr - 1) / (kTMergeWarps * nr);
   const dim3 grid(chunks, static_cast<unsigned>(p.n_kv_heads), static_cast<unsigned>(p.batch));
-  return cuda_failed(launch_pdl(tree_merge_kernel<D, NQ>, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges),
-                     "tree_merge_kernel launch")
+  auto merge = nr == 4 ? tree_merge_kernel<D, NQ, 4> : tree_merge_kernel<D, NQ, 1>;
+  return cuda_failed(launch_pdl(merge, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges), "tree_merge_kernel launch")
              ? PKV_ERR_CUDA
              : PKV_OK;
 }
