@@ -679,6 +679,32 @@ pkv_status pkv_paged_decode_attention_window_e5m2(const void* q, const uint8_t* 
                                                   void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The same rule for the tokens of a prompt chunk (the windowed form of
+ * pkv_paged_prefill_attention, without its clusters): the n_b = cu_seqlens[b +
+ * 1] - cu_seqlens[b] new tokens of sequence b are its last n_b positions, already
+ * in the cache; token i, at position p = context_lens[b] - n_b + i, sees position
+ * j where j <= p and (j < num_sinks or j > p - window).  q and out are
+ * [num_tokens, num_q_heads, head_dim]; 16-bit caches, head_dim 64 or 128, scale >
+ * 0.  Blocks that hold no key of a new token's are not looked up and not read.  K
+ * and V of positions that a token does not see change nothing for it, whatever
+ * bits they hold; an element of V that is not finite gives an output that is not
+ * finite where it is seen.  Weights in 16 bits as in the drafted tokens' attention
+ * below.  max_query_len: an upper bound of n_b.  Tokens behind the last sequence
+ * are neither read nor written.  Device errors (PKV_ERR_OOB; the sequence is
+ * skipped, its outputs stay as they are): offsets that do not ascend within
+ * [0, num_tokens], more tokens than max_query_len or than the context has, a
+ * context longer than its table.  A table entry outside the pool reads as zeros
+ * and is reported.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_tables, const int32_t* context_lens,
+                                              const int32_t* cu_seqlens, int64_t num_tokens, int batch,
+                                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                              int max_blocks_per_seq, int64_t num_blocks, int max_query_len,
+                                              int window, int num_sinks, float scale, void* out, pkv_dtype dtype,
+                                              int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Drafted tokens: one pass over several candidate continuations of each
  * sequence, and the move of the accepted ones.  The n_b = cu_nodes[b + 1] -
  * cu_nodes[b] drafted tokens of sequence b (tokens cu_nodes[b] .. cu_nodes[b + 1]

@@ -40,7 +40,7 @@ __all__ = [
     "pkv_paged_decode_attention_sparse_e5m2",
     "pkv_prefix_workspace_bytes", "pkv_paged_decode_attention_prefix",
     "pkv_paged_decode_attention_window", "pkv_paged_decode_attention_window_fp8",
-    "pkv_paged_decode_attention_window_e5m2",
+    "pkv_paged_decode_attention_window_e5m2", "pkv_paged_prefill_attention_window",
     "pkv_tree_plan", "pkv_tree_workspace_bytes", "pkv_paged_tree_attention", "pkv_paged_tree_attention_fp8",
     "pkv_paged_tree_attention_e5m2", "pkv_tree_commit",
 ]
@@ -160,6 +160,8 @@ _SIGS = {
                                                    _f, _p, _i, _p, _sz, _p, _p]),
     "pkv_paged_decode_attention_window_e5m2": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i, _i,
                                                     _f, _p, _i, _p, _sz, _p, _p]),
+    "pkv_paged_prefill_attention_window": (_i, [_p, _p, _p, _p, _p, _p, _i64, _i, _i, _i, _i, _i, _i, _i64, _i, _i, _i,
+                                                _f, _p, _i, _p, _p]),
     "pkv_tree_plan": (_i, [_p, _p, _p, _p, _i, _i64, _i, _i, _i, _i64, _p, _p, _p, _p, _p]),
     "pkv_tree_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i]),
     "pkv_paged_tree_attention": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i64, _i, _i, _i, _i, _i, _i, _i64, _i, _f,
@@ -674,6 +676,16 @@ def pkv_paged_decode_attention_window_e5m2(q, k_cache, v_cache, k_scale, v_scale
     _check("pkv_paged_decode_attention_window_e5m2", _tensor.window_decode(
         2, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, scale, window, num_sinks, workspace,
         q_dtype, err_flag, stream))
+
+
+def pkv_paged_prefill_attention_window(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, *,
+                                       scale: float, max_query_len: int, window: int, num_sinks: int = 0, dtype=None,
+                                       err_flag=None, stream=None) -> None:
+    """Causal extend attention of the new tokens q [T, Hq, D] to the first
+    num_sinks positions and the last window ones up to their own."""
+    _check("pkv_paged_prefill_attention_window", _tensor.window_prefill(
+        q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, scale, max_query_len, window, num_sinks,
+        dtype, err_flag, stream))
 
 
 def pkv_tree_plan(parents, cu_nodes, block_tables, context_lens, tree_mask, positions, slot_mapping, *,

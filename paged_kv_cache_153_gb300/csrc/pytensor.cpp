@@ -574,6 +574,45 @@ PyObject* tree_attention(PyObject* const* a) {
   });
 }
 
+// q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, scale,
+// max_query_len, window, num_sinks, dtype, err_flag, stream
+PyObject* window_prefill(PyObject* const* a) {
+  const at::Tensor &q = need(a[0], 3, "q must be [num_tokens, num_q_heads, head_dim]"), &kc = need(a[1], 4, kCacheDims),
+                   &vc = need(a[2], -1, ""), &tab = need(a[3], 2, kTableDims), &len = need(a[4], -1, ""),
+                   &cu = need(a[5], -1, ""), &out = need(a[6], -1, "");
+  index_check(len);
+  index_check(cu);
+  index_check(tab);
+  if (cu.numel() != len.numel() + 1)
+    refuse(PyExc_ValueError, "cu_seqlens must have one entry more than context_lens");
+  per_sequence(len.numel(), tab, len);
+  contiguous(q);
+  contiguous(out);
+  caches_check(kc, vc, 2);
+  if (out.sizes() != q.sizes()) refuse(PyExc_ValueError, "q and out differ in shape");
+  if (kc.size(3) != q.size(2)) refuse(PyExc_ValueError, "q and the caches differ in head_dim");
+  const Type16 type(q, a[11]);
+  type.check(out);
+  cache_type(kc, 0, type);
+  flag_check(a[12]);
+  const int64_t tokens = q.size(0), nb = kc.size(0);
+  const int b = to_int(len.numel()), hq = to_int(q.size(1)), hkv = to_int(kc.size(1)), d = to_int(q.size(2)),
+            bs = to_int(kc.size(2)), width = to_int(tab.size(1)), longest = number<int>(a[8]),
+            window = number<int>(a[9]), sinks = number<int>(a[10]);
+  const float scale = number<float>(a[7]);
+  const pkv_dtype dt = type.code;
+  void *qp = ptr(q), *kp = ptr(kc), *vp = ptr(vc), *op = ptr(out);
+  const auto* tp = static_cast<const int32_t*>(ptr(tab));
+  const auto* lp = static_cast<const int32_t*>(ptr(len));
+  const auto* cp = static_cast<const int32_t*>(ptr(cu));
+  auto* err = static_cast<int32_t*>(address(a[12]));
+  void* s = stream_of(a[13]);
+  return status([&] {
+    return pkv_paged_prefill_attention_window(qp, kp, vp, tp, lp, cp, tokens, b, hq, hkv, d, bs, width, nb, longest,
+                                              window, sinks, scale, op, dt, err, s);
+  });
+}
+
 // k_cache, v_cache, block_tables, context_lens, cu_nodes, accepted, new_lens,
 // err_flag, stream
 PyObject* tree_commit(PyObject* const* a) {
@@ -624,6 +663,7 @@ PyMethodDef methods[] = {
     PKV_TENSOR_CALL(sparse_decode, 15),
     PKV_TENSOR_CALL(prefix_decode, 15),
     PKV_TENSOR_CALL(window_decode, 16),
+    PKV_TENSOR_CALL(window_prefill, 14),
     PKV_TENSOR_CALL(tree_plan, 10),
     PKV_TENSOR_CALL(tree_attention, 18),
     PKV_TENSOR_CALL(tree_commit, 9),

@@ -1,5 +1,5 @@
-// C-ABI entry points of the drafted tokens' attention: argument checks, workspace
-// and dispatch.
+// C-ABI entry points of the drafted tokens' attention and of the windowed prompt
+// chunks: argument checks, workspace and dispatch.
 #include "tree.h"
 
 #include <cuda_runtime.h>
@@ -166,4 +166,55 @@ extern "C" pkv_status pkv_paged_tree_attention_e5m2(
                      mask_words, max_nodes, num_tokens, batch, num_q_heads, num_kv_heads, head_dim, block_size,
                      max_blocks_per_seq, num_blocks, max_context_len, scale, out, q_dtype, workspace, workspace_bytes,
                      err_flag, stream);
+}
+
+extern "C" pkv_status pkv_paged_prefill_attention_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+    const int32_t* cu_seqlens, int64_t num_tokens, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int max_blocks_per_seq, int64_t num_blocks, int max_query_len, int window, int num_sinks,
+    float scale, void* out, pkv_dtype dtype, int32_t* err_flag, void* stream) {
+  if (batch < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
+      max_blocks_per_seq <= 0 || num_blocks < 0 || max_query_len < 0 || window <= 0 || num_sinks < 0 ||
+      !std::isfinite(scale) || scale <= 0.f)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+  const int group = num_q_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
+  if (batch > 65535 || num_kv_heads > 65535 || num_tokens > INT32_MAX / group ||
+      num_blocks * num_kv_heads > INT32_MAX / 2)
+    return PKV_ERR_UNSUPPORTED;
+  if (batch == 0 || num_tokens == 0 || max_query_len == 0) return PKV_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out || num_blocks == 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
+  const int64_t longest = std::min<int64_t>(max_query_len, num_tokens);
+  const int q_tiles = longest * group > kTreeRows ? 2 : 1;
+  TreeParams p{};
+  p.group_shift = group == 8 ? 3 : group == 4 ? 2 : group - 1;
+  p.q_box = static_cast<int>(std::min<int64_t>(kTreeRows / group, longest));
+  if (!encode_query_tmap(&p.tmap_q, q, num_tokens, num_q_heads, head_dim, group, p.q_box) ||
+      !encode_block_tmap(&p.tmap_k, k_cache, num_blocks * num_kv_heads, head_dim) ||
+      !encode_block_tmap(&p.tmap_v, v_cache, num_blocks * num_kv_heads, head_dim))
+    return PKV_ERR_CUDA;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.cu_nodes = cu_seqlens;
+  p.out = out;
+  p.err = err_flag;
+  p.wait_limit_ns = wait_limit_ns();
+  p.num_blocks = num_blocks;
+  p.num_tokens = num_tokens;
+  p.batch = batch;
+  p.n_q_heads = num_q_heads;
+  p.n_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_nodes = static_cast<int>(longest);
+  p.window = window;
+  p.num_sinks = num_sinks;
+  p.q_bf16 = dtype == PKV_BF16;
+  p.qk_scale_log2 = scale * kLog2e;
+  const int64_t units = (longest * group + kTreeRows * q_tiles - 1) / (kTreeRows * q_tiles);
+  return chunk_launcher(dtype, head_dim, q_tiles)(p, static_cast<int>(units), static_cast<cudaStream_t>(stream));
 }

@@ -56,6 +56,11 @@
 // fp16 (bf16 q converted in place: exact in fp16's normal range).  The products
 // then run in fp16.
 //
+// Prompt chunks (CHUNK).  The same kernel attends the new tokens of a prompt to the
+// first tokens and a window: a thread block per unit, whose key tiles are those
+// that hold a key of one of its rows; what a row sees is a range of positions and
+// the first num_sinks.
+//
 // Warps 0-7: softmax; 8 and 11: producers; 9: TMEM owner and Q K^T issuer; 10:
 // P V issuer; from 12 on: rows of V with drafted tokens (four warps), or the
 // conversions of K (four) and of V (four).  The softmax warps take registers
@@ -119,6 +124,7 @@ struct TreeSmem {
   static constexpr int kHalf = 1024;
   static constexpr int kHalfQ = kTreeRows * 128;
 };
+static_assert(TreeSmem<128, false, 1>::bytes(kTreeMaxBatch) <= 232448, "16-bit tiles");
 static_assert(TreeSmem<128, false, 2>::bytes(kTreeMaxBatch) <= 232448, "16-bit tiles");
 static_assert(TreeSmem<128, true, 1>::bytes(kTreeMaxBatch) <= 232448, "FP8 tiles");
 
@@ -127,6 +133,9 @@ struct TreeSeg {
   int64_t next;                  // cost position behind it
   int64_t row;                   // first row of its states
   int b, g, unit, rows, t0, t1, kt;
+  int gap_at, skip;              // CHUNK: skip tiles are left out in front of the gap_at-th one
+  int pos0, pos1;                // CHUNK: positions of the unit's first and last token
+  int low0, low1;                // and the first ones of their windows
 };
 
 // units of a sequence's rows, key tiles of its context, cost of one unit
@@ -174,6 +183,35 @@ __device__ __forceinline__ TreeSeg tree_segment(const TreeSeq* seqs, int batch, 
   s.row = tree_piece_row(sq.start, n_q_heads, s.g, rows, static_cast<int64_t>(s.unit) * kTreeRows * NQ, range,
                          kTreeRows * NQ);
   return s;
+}
+
+// CHUNK: the only piece of a thread block, unit `unit` of sequence sq
+__device__ __forceinline__ TreeSeg chunk_segment(const TreeSeq& sq, int b, int g, int unit, int unit_rows, int shift,
+                                                 int window, int sinks) {
+  TreeSeg s{};
+  s.next = 1;
+  s.b = b, s.g = g, s.unit = unit;
+  s.rows = min(unit_rows, (sq.n << shift) - unit * unit_rows);
+  if (s.rows <= 0) return s;     // (t0 == t1)
+  const int tok = (unit * unit_rows) >> shift;
+  s.pos0 = sq.ctx - sq.n + tok;
+  s.pos1 = s.pos0 + (s.rows >> shift) - 1;
+  s.low0 = max(0, s.pos0 - window + 1);
+  s.low1 = max(0, s.pos1 - window + 1);
+  s.gap_at = sinks / kTreeKeys + (sinks % kTreeKeys != 0);
+  s.skip = max(0, s.low0 / kTreeKeys - s.gap_at);
+  s.t1 = s.kt = s.pos1 / kTreeKeys + 1 - s.skip;
+  return s;
+}
+// does every row of the unit see every key of tile t?
+__device__ __forceinline__ bool chunk_plain(const TreeSeg& s, int t, int sinks) {
+  const int k0 = t * kTreeKeys, k1 = k0 + kTreeKeys - 1;
+  return k1 <= s.pos0 && (k0 >= s.low1 || k1 < sinks);
+}
+// bits of the 32 keys from key0 on that are below x
+__device__ __forceinline__ uint32_t keys_below(int x, int key0) {
+  const int d = x - key0;
+  return d <= 0 ? 0u : d >= 32 ? 0xffffffffu : (1u << d) - 1u;
 }
 
 // a position in a ring of N stages
@@ -261,12 +299,15 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <typename MT, typename KV, int D, int NQ>
+template <typename MT, typename KV, int D, int NQ, bool CHUNK>
 __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool kFp8 = KV::kBytes == 1;
   using L = TreeSmem<D, kFp8, NQ>;
   constexpr bool kSplit = std::is_same<MT, BF16>::value;
   constexpr int NB = L::kSBufs;
+  static_assert(!CHUNK || !kFp8, "prompt chunks: 16-bit caches");
+  constexpr int kBadWords = CHUNK ? 16 : 8;        // of remembered tokens
+  static_assert(!CHUNK || L::kXform * 16 <= kTBadSlots * L::kXform * 8, "remembered tokens");
   constexpr float kFold = std::is_same<KV, E4M3>::value ? 256.f : 1.f;   // of converted codes
   extern __shared__ unsigned char tsm_raw[];
   unsigned char* sm = tsm_raw + ((1024 - (smem_u32(tsm_raw) & 1023)) & 1023);
@@ -341,54 +382,66 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   // Until the waits below this kernel reads lengths, offsets and (in the producer)
   // tables only, which no kernel that releases early writes.
 
-  // ---- the sequences: drafted tokens, context, cost ----
-  for (int b = tid; b < p.batch; b += L::kThreads) {
-    const int64_t t0 = p.cu_nodes[b], t1 = p.cu_nodes[b + 1];
+  // ---- the sequences: drafted (or new) tokens, context, cost ----
+  auto sequence = [&](int b) -> TreeSeq {
+    const int64_t t0 = p.cu_nodes[b], t1 = p.cu_nodes[b + 1], n = t1 - t0;
     const int ctx = p.context_lens[b];
-    TreeSeq sq{0, 0, 0, 0, 0};
-    const int64_t n = t1 - t0;
     if (t0 < 0 || n < 0 || t1 > p.num_tokens || n > p.max_nodes || ctx < n ||
         ctx > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize) {
       record_error(p.err, PKV_ERR_OOB);
-    } else if (n > 0) {
-      const int rows = static_cast<int>(n) << shift;
-      sq.start = static_cast<int>(t0);
-      sq.n = static_cast<int>(n);
-      sq.ctx = ctx;
-      sq.cost = p.n_kv_heads * tree_units<NQ>(rows) * tree_unit_cost(rows, tree_tiles(ctx));
+      return TreeSeq{0, 0, 0, 0, 0};
     }
-    seqs[b] = sq;
-  }
-  __syncthreads();
-  if (warp == 0) {   // exclusive prefix of the costs
-    int64_t carry = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t mine = b < p.batch ? seqs[b].cost : 0;
-      int64_t x = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += u;
+    return n > 0 ? TreeSeq{0, static_cast<int>(t0), static_cast<int>(n), ctx, 0} : TreeSeq{0, 0, 0, 0, 0};
+  };
+  if constexpr (CHUNK) {
+    if (tid == 0) seqs[0] = sequence(blockIdx.z);
+  } else {
+    for (int b = tid; b < p.batch; b += L::kThreads) {
+      TreeSeq sq = sequence(b);
+      if (sq.n > 0) {
+        const int rows = sq.n << shift;
+        sq.cost = p.n_kv_heads * tree_units<NQ>(rows) * tree_unit_cost(rows, tree_tiles(sq.ctx));
       }
-      if (b < p.batch) seqs[b].cost = carry + x - mine;
-      carry += __shfl_sync(0xffffffffu, x, 31);
+      seqs[b] = sq;
     }
-    if (lane == 0) seqs[p.batch] = TreeSeq{carry, 0, 0, 0, 0};
+    __syncthreads();
+    if (warp == 0) {   // exclusive prefix of the costs
+      int64_t carry = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int64_t mine = b < p.batch ? seqs[b].cost : 0;
+        int64_t x = mine;
+  #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t u = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += u;
+        }
+        if (b < p.batch) seqs[b].cost = carry + x - mine;
+        carry += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) seqs[p.batch] = TreeSeq{carry, 0, 0, 0, 0};
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (blockIdx.x == 0) {
+  if (!CHUNK && blockIdx.x == 0) {
     pdl_wait();
     for (int b = tid; b <= p.batch; b += L::kThreads) p.seqs[b] = seqs[b];
   }
   const uint32_t tmem = *tmem_slot;
-  const int64_t V = seqs[p.batch].cost, R = gridDim.x, range = blockIdx.x;
+  const int64_t V = CHUNK ? 1 : seqs[p.batch].cost, R = CHUNK ? 1 : gridDim.x, range = CHUNK ? 0 : blockIdx.x;
   const int64_t first = div_nonneg(range * V, R), end = div_nonneg((range + 1) * V, R);
   auto segment = [&](int64_t pos) {
-    return tree_segment<NQ>(seqs, p.batch, shift, p.n_q_heads, pos, end, range);
+    if constexpr (CHUNK)   // (the longest units first)
+      return chunk_segment(seqs[0], blockIdx.z, blockIdx.y, gridDim.x - 1 - blockIdx.x, kTreeRows * NQ, shift, p.window,
+                           p.num_sinks);
+    else
+      return tree_segment<NQ>(seqs, p.batch, shift, p.n_q_heads, pos, end, range);
   };
+  auto sequence_of = [&](const TreeSeg& sg) { return seqs[CHUNK ? 0 : sg.b]; };
+  // key tile at place x of a piece's order
+  auto tile_at = [&](const TreeSeg& sg, int x) { return CHUNK && x >= sg.gap_at ? x + sg.skip : x; };
 
   if (warp < 8) {
     // ============================ softmax / epilogue ============================
@@ -410,7 +463,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const TreeSeg sg = segment(pos);
       pos = sg.next;
       if (sg.t0 >= sg.t1) continue;
-      const TreeSeq sq = seqs[sg.b];
+      const TreeSeq sq = sequence_of(sg);
       const int base = sq.ctx - sq.n, nt = sg.t1 - sg.t0;
       const bool two = NQ == 2 && sg.rows > kTreeRows;                // a row tile per group
       const int tile = two ? grp : 0, row0 = tile * kTreeRows + quarter * 32, row = row0 + lane;
@@ -445,13 +498,19 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           mbar_arrive(&p_full[buf]);
           continue;
         }
-        const int t = sg.t1 - 1 - n;
-        const bool tail = (t + 1) * kTreeKeys > base;
+        const int t = tile_at(sg, sg.t1 - 1 - n);
+        const bool tail = CHUNK ? !chunk_plain(sg, t, p.num_sinks) : (t + 1) * kTreeKeys > base;
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (tail) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            see[w] = tree_bits(words, 2 * p.mask_words, sq.n, t * kTreeKeys + 32 * w - base);
+          for (int w = 0; w < 4; ++w) {
+            const int key0 = t * kTreeKeys + 32 * w;
+            if constexpr (CHUNK)
+              see[w] = keys_below(base + node + 1, key0) &
+                       (~keys_below(max(0, base + node + 1 - p.window), key0) | keys_below(p.num_sinks, key0));
+            else
+              see[w] = tree_bits(words, 2 * p.mask_words, sq.n, key0 - base);
+          }
         }
         const uint32_t ts = tmem + lane_base + buf * kTreeKeys;
         // (its turn first: then the buffer's previous scores are known to be over)
@@ -572,8 +631,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         continue;
       }
       // drafted tokens of this piece with elements of V that are not finite
-      const uint32_t mine = bad[piece_slot * (L::kXform * 8) + lane];
-      const bool any_bad = __any_sync(0xffffffffu, mine != 0u);
+      const uint32_t* noted = bad + piece_slot * (L::kXform * 8);     // [kXform][kBadWords]
+      uint32_t any = 0;
+      for (int w = lane; w < L::kXform * kBadWords; w += 32) any |= noted[w];
+      const bool any_bad = __any_sync(0xffffffffu, any != 0u);
       const bool direct = sg.t0 == 0 && sg.t1 == sg.kt;
       const float v_scale = kFp8 ? p.v_scale[sg.g] * kFold : 1.f;
       const int n_rows = sg.rows - row0, head = (sg.g << shift) + (unit_row & ((1 << shift) - 1));
@@ -587,12 +648,15 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         for (int i = 0; i < 32; ++i) o[i] *= weight;
         if (any_bad) {
           // (rare) every row adds what it sees of them
-          for (int w = 0; w < 2 * p.mask_words; ++w) {
+          for (int w = 0; w < (CHUNK ? kBadWords : 2 * p.mask_words); ++w) {
             uint32_t bits = 0;
 #pragma unroll
-            for (int k = 0; k < L::kXform; ++k) bits |= __shfl_sync(0xffffffffu, mine, 8 * k + w);
-            for (bits &= words[w]; bits != 0u; bits &= bits - 1u) {
-              const int at = base + 32 * w + __ffs(bits) - 1;
+            for (int k = 0; k < L::kXform; ++k) bits |= noted[k * kBadWords + w];
+            if constexpr (!CHUNK) bits &= words[w];
+            for (; bits != 0u; bits &= bits - 1u) {
+              const int i0 = 32 * w + __ffs(bits) - 1;
+              const int at = !CHUNK ? base + i0 : i0 < 256 ? sg.pos0 + 1 + i0 : sg.low0 + i0 - 256;
+              if (CHUNK && !(at <= base + node && (at > base + node - p.window || at < p.num_sinks))) continue;
               const int id = p.block_tables[static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + at / kBlockSize];
               if (id < 0 || id >= p.num_blocks) continue;
               const int64_t e = ((static_cast<int64_t>(id) * p.n_kv_heads + sg.g) * kBlockSize + at % kBlockSize) * D;
@@ -652,14 +716,21 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const TreeSeg sg = segment(pos);
       pos = sg.next;
       if (sg.t0 >= sg.t1) continue;
-      const TreeSeq sq = seqs[sg.b];
+      const TreeSeq sq = sequence_of(sg);
       const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
       const int nblk = ctx_blocks(sq.ctx);
       const uint64_t pol = tree_units<NQ>(sq.n << shift) > 1 ? policy_evict_last() : policy_evict_first();
       const int32_t* row = p.block_tables + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
-      auto fetch_id = [&](int t) -> int {
-        const int blk = t * kTTileBlocks + lane;
-        return (t >= sg.t0 && lane < kTTileBlocks && blk < nblk) ? row[blk] : -1;
+      // (CHUNK: blocks that no row sees a key of are not looked up)
+      auto wanted = [&](int blk) -> bool {
+        if (CHUNK && !(blk * kBlockSize <= sg.pos1 &&
+                       (blk * kBlockSize + kBlockSize > sg.low0 || blk * kBlockSize < p.num_sinks)))
+          return false;
+        return lane < kTTileBlocks && blk < nblk;
+      };
+      auto fetch_id = [&](int x) -> int {
+        const int blk = tile_at(sg, x) * kTTileBlocks + lane;
+        return (x >= sg.t0 && wanted(blk)) ? row[blk] : -1;
       };
       int id = fetch_id(sg.t1 - 1);
       if (!is_v) {
@@ -680,8 +751,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       }
       for (int t = sg.t1 - 1; t >= sg.t0; --t) {
         // cache slab of this lane's block: -1 behind the context or for a bad id
-        const int blk = t * kTTileBlocks + lane;
-        bool have = lane < kTTileBlocks && blk < nblk;
+        bool have = wanted(tile_at(sg, t) * kTTileBlocks + lane);
         if (have && (id < 0 || id >= p.num_blocks)) {
           record_error(p.err, PKV_ERR_OOB);
           have = false;
@@ -839,10 +909,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const TreeSeg sg = segment(pos);
       pos = sg.next;
       if (sg.t0 >= sg.t1) continue;
-      const TreeSeq sq = seqs[sg.b];
+      const TreeSeq sq = sequence_of(sg);
       const int base = sq.ctx - sq.n;
-      uint32_t* my_bad = bad + (pieces % kTBadSlots) * (L::kXform * 8) + x_warp * 8;
-      if (is_v && lane < 8) my_bad[lane] = 0u;
+      uint32_t* my_bad = bad + (pieces % kTBadSlots) * (L::kXform * 8) + x_warp * kBadWords;
+      if (is_v && lane < kBadWords) my_bad[lane] = 0u;
       __syncwarp();
       auto store = [&](uint32_t addr, const uint4& v) {
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -859,15 +929,26 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       auto at = [&](int j, int c) -> uint32_t {
         return (j >> 3) * L::kGroup + (c >> 3) * L::kHalf + (j & 7) * 128 + (((c & 7) ^ (j & 7)) << 4);
       };
-      // an element of V at position key: 0 behind the context; of a drafted token, 0
-      // where it is not finite, and the token is remembered
+      // elements of V at position key: 0 where no row sees them; where only some do, 0
+      // if they are not finite, and the token is remembered
       auto clean = [&](uint4 v, int key) -> uint4 {
-        if (key >= sq.ctx) return make_uint4(0u, 0u, 0u, 0u);
-        if (key >= base) {
+        bool none, all;
+        int note;
+        if constexpr (CHUNK) {
+          none = key > sg.pos1 || (key >= p.num_sinks && key < sg.low0);
+          all = key <= sg.pos0 && (key < p.num_sinks || key >= sg.low1);
+          note = key > sg.pos0 ? key - sg.pos0 - 1 : 256 + key - sg.low0;
+        } else {
+          none = key >= sq.ctx;
+          all = key < base;
+          note = key - base;
+        }
+        if (none) return make_uint4(0u, 0u, 0u, 0u);
+        if (!all) {
           const uint4 f = make_uint4(nonfinite2<MT>(v.x), nonfinite2<MT>(v.y), nonfinite2<MT>(v.z), nonfinite2<MT>(v.w));
           if (f.x | f.y | f.z | f.w) {
             v.x ^= f.x, v.y ^= f.y, v.z ^= f.z, v.w ^= f.w;
-            atomicOr(&my_bad[(key - base) >> 5], 1u << ((key - base) & 31));
+            atomicOr(&my_bad[note >> 5], 1u << (note & 31));
           }
         }
         return v;
@@ -893,13 +974,15 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         }
       }
       ++pieces;
-      for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t, ++tiles) {
+      for (int x0 = sg.t1 - 1; x0 >= sg.t0 && ok; --x0, ++tiles) {
+        const int t = tile_at(sg, x0);
         if constexpr (!kFp8) {
           ok = wait_all(&v_full[vr.s], vr.ph);
           if (!ok) break;
-          if ((t + 1) * kTreeKeys > base) {          // rows from the first drafted token on
+          if (CHUNK ? !chunk_plain(sg, t, p.num_sinks) : (t + 1) * kTreeKeys > base) {
+            // (of drafted tokens: rows from the first one on)
             const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
-            for (int x = max(0, base - t * kTreeKeys) * kChunks + x_tid; x < kTreeKeys * kChunks; x += L::kXform * 32) {
+            for (int x = (CHUNK ? 0 : max(0, base - t * kTreeKeys)) * kChunks + x_tid; x < kTreeKeys * kChunks; x += L::kXform * 32) {
               const int j = x / kChunks;
               const uint32_t addr = tile + at(j, x % kChunks);
               const uint4 v = load(addr), w = clean(v, t * kTreeKeys + j);
@@ -1109,7 +1192,7 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
 template <typename MT, typename KV, int D, int NQ>
 pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   using L = TreeSmem<D, KV::kBytes == 1, NQ>;
-  auto kern = tree_kernel<MT, KV, D, NQ>;
+  auto kern = tree_kernel<MT, KV, D, NQ, false>;
   constexpr int kDevices = 64;
   int dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
@@ -1137,6 +1220,39 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   return cuda_failed(launch_pdl(merge, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges), "tree_merge_kernel launch")
              ? PKV_ERR_CUDA
              : PKV_OK;
+}
+
+// grid: units of the longest sequence x KV heads x sequences
+template <typename MT, int D, int NQ>
+pkv_status launch_chunk(TreeParams& p, int units, cudaStream_t stream) {
+  using L = TreeSmem<D, false, NQ>;
+  auto kern = tree_kernel<MT, MT, D, NQ, true>;
+  constexpr int kDevices = 64;
+  int dev = 0;
+  if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
+  static std::mutex mu;
+  static bool done[kDevices] = {};
+  if (dev < 0 || dev >= kDevices) return PKV_ERR_UNSUPPORTED;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(L::bytes(1))),
+                      "cudaFuncSetAttribute"))
+        return PKV_ERR_CUDA;
+      done[dev] = true;
+    }
+  }
+  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(p.n_kv_heads), static_cast<unsigned>(p.batch));
+  return cuda_failed(launch_pdl(kern, grid, dim3(L::kThreads), L::bytes(1), stream, p), "tree_kernel launch (chunk)")
+             ? PKV_ERR_CUDA
+             : PKV_OK;
+}
+
+template <typename MT>
+TreeLauncher pick_chunk(int head_dim, int q_tiles) {
+  if (head_dim == 64) return q_tiles == 1 ? launch_chunk<MT, 64, 1> : launch_chunk<MT, 64, 2>;
+  return q_tiles == 1 ? launch_chunk<MT, 128, 1> : launch_chunk<MT, 128, 2>;
 }
 
 template <typename MT, typename KV>

@@ -42,7 +42,8 @@ struct TreeParams {
   unsigned long long wait_limit_ns;
   int64_t num_blocks, num_tokens;
   int batch, n_q_heads, n_kv_heads, group_shift, max_blocks_per_seq;
-  int mask_words, max_nodes;
+  int mask_words, max_nodes;     // (chunks: max_nodes is the longest query)
+  int window, num_sinks;         // chunks
   int q_box;                     // tokens of a Q box
   int q_bf16;                    // type of q and out: bf16 (else fp16)
   float qk_scale_log2;
@@ -52,5 +53,7 @@ struct TreeParams {
 using TreeLauncher = pkv_status (*)(TreeParams&, int ranges, cudaStream_t);
 TreeLauncher tree_launcher_16(int q_dtype, int head_dim, int q_tiles);
 TreeLauncher tree_launcher_fp8(int kv_kind, int head_dim, int q_tiles);
+// prompt chunks with a window, 16-bit caches; `ranges` is the units of the longest one
+TreeLauncher chunk_launcher(int q_dtype, int head_dim, int q_tiles);
 
 }  // namespace pkv
