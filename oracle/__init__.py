@@ -36,6 +36,7 @@ e4m3         the OCP FP8 E4M3 code table, encoder and decoder.
 e5m2         the OCP FP8 E5M2 code table, encoder and decoder.
 int8         INT8 codes with per-block min-max scaling (encode, decode, re-quantising append).
 attention    paged decode attention and the contiguous (no-cache) comparator.
+draft        drafted tokens (trees, attention under a visibility, accepted rows) and the window rule.
 prefill      paged prefill / extend attention (causal over the cached context).
 toy_model    a tiny projection model that recomputes K/V from scratch.
 numerics     exact decoding of stored fp16 / bf16 bit patterns to float64.

@@ -477,11 +477,10 @@ int drafted_batch(const at::Tensor& cu, const at::Tensor& len) {
   return to_int(len.numel());
 }
 
-uint64_t* mask_words(const at::Tensor& t, int64_t tokens) {
+void mask_check(const at::Tensor& t, int64_t tokens) {
   if ((t.scalar_type() != at::kLong && t.scalar_type() != at::kUInt64) || !t.is_contiguous())
     refuse(PyExc_TypeError, "tree_mask must be contiguous int64");
   if (t.size(0) != tokens) refuse(PyExc_ValueError, "tree_mask must have a row per token");
-  return static_cast<uint64_t*>(ptr(t));
 }
 constexpr const char* kMaskDims = "tree_mask must be [num_tokens, words]";
 
@@ -493,7 +492,7 @@ PyObject* tree_plan(PyObject* const* a) {
   index_check(par);
   const int b = drafted_batch(cu, len), words = to_int(mask.size(1));
   const int64_t tokens = par.numel(), nb = number<int64_t>(a[7]);
-  const int32_t* tab = nullptr;
+  mask_check(mask, tokens);
   int width = 0;
   if (a[6] != Py_None) {
     const at::Tensor &t = need(a[2], 2, kTableDims), &s = need(a[6], -1, "");
@@ -501,7 +500,6 @@ PyObject* tree_plan(PyObject* const* a) {
     per_sequence(b, t, len);
     if (s.numel() != tokens || s.scalar_type() != at::kLong || !s.is_contiguous())
       refuse(PyExc_ValueError, "slot_mapping must be contiguous int64, one slot per token");
-    tab = static_cast<const int32_t*>(ptr(t));
     width = to_int(t.size(1));
   }
   if (a[5] != Py_None) {
@@ -510,7 +508,8 @@ PyObject* tree_plan(PyObject* const* a) {
     if (t.numel() != tokens) refuse(PyExc_ValueError, "positions must have an entry per token");
   }
   flag_check(a[8]);
-  uint64_t* mp = mask_words(mask, tokens);
+  const auto* tab = static_cast<const int32_t*>(a[6] != Py_None ? address(a[2]) : nullptr);
+  auto* mp = static_cast<uint64_t*>(ptr(mask));
   const auto* pp = static_cast<const int32_t*>(ptr(par));
   const auto* cp = static_cast<const int32_t*>(ptr(cu));
   const auto* lp = static_cast<const int32_t*>(ptr(len));
@@ -548,7 +547,8 @@ PyObject* tree_attention(PyObject* const* a) {
   flag_check(a[16]);
   if (!ws.is_contiguous()) refuse(PyExc_ValueError, "the workspace must be contiguous");
   const int64_t tokens = q.size(0), nb = kc.size(0);
-  const uint64_t* mp = mask_words(mask, tokens);
+  mask_check(mask, tokens);
+  const auto* mp = static_cast<const uint64_t*>(ptr(mask));
   const int hq = to_int(q.size(1)), hkv = to_int(kc.size(1)), d = to_int(q.size(2)), bs = to_int(kc.size(2)),
             width = to_int(tab.size(1)), max_ctx = number<int>(a[12]), max_nodes = number<int>(a[13]);
   const float scale = number<float>(a[11]);
