@@ -650,8 +650,8 @@ pkv_status pkv_paged_decode_attention_prefix(const void* q, const void* k_cache,
  * given back.  K and V rows that are not seen may hold anything.
  *   window      >= 1; num_sinks >= 0 (else PKV_ERR_INVALID_ARG).
  *   workspace   at least pkv_decode_workspace_bytes(batch, num_q_heads,
- *               num_kv_heads, head_dim, max_blocks_per_seq, window + num_sinks,
- *               0).
+ *               num_kv_heads, head_dim, max_blocks_per_seq, n, 0), the same for
+ *               every n.
  * Other arguments, requirements and errors as in pkv_paged_decode_attention and
  * its FP8 forms (a context longer than the table is cut to it and reported).
  * ------------------------------------------------------------------------- */
