@@ -54,6 +54,10 @@ bool encode_query_tmap(CUtensorMap* map, const void* base, int64_t tokens, int n
 // side.
 bool encode_block_tmap(CUtensorMap* map, const void* base, int64_t slabs, int head_dim);
 
+// Tiled TMA view of an FP8 cache [rows, head_dim] with boxes of 16 rows and a
+// swizzle of a row's bytes (64 or 128).
+bool encode_code_tmap(CUtensorMap* map, const void* base, int64_t rows, int head_dim);
+
 // SMs of the current device (0, with the reason kept, when it cannot be asked)
 int sm_count();
 

@@ -60,7 +60,8 @@ pkv_status tree_common(int kv_kind, const void* q, const void* k_cache, const vo
   const int group = n_q_heads / n_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
   if (mask_words > kTreeMaxWords || batch > kTreeMaxBatch || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
-  if (num_tokens > INT32_MAX || num_blocks * n_kv_heads > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens > INT32_MAX || num_blocks * n_kv_heads > INT32_MAX / kBlockSize)
+    return PKV_ERR_UNSUPPORTED;                      // (32-bit TMA row coordinates)
   if (batch == 0 || num_tokens == 0 || max_nodes == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_nodes || !tree_mask || !out || !workspace)
     return PKV_ERR_INVALID_ARG;
@@ -79,11 +80,12 @@ pkv_status tree_common(int kv_kind, const void* q, const void* k_cache, const vo
   TreeParams p{};
   p.group_shift = group == 8 ? 3 : group == 4 ? 2 : group - 1;
   p.q_box = std::min(kTreeRows / group, max_nodes);
-  if (!encode_query_tmap(&p.tmap_q, q, num_tokens, n_q_heads, head_dim, group, p.q_box)) return PKV_ERR_CUDA;
-  if (kv_kind == 0 && (!encode_block_tmap(&p.tmap_k, k_cache, num_blocks * n_kv_heads, head_dim) ||
-                       !encode_block_tmap(&p.tmap_v, v_cache, num_blocks * n_kv_heads, head_dim)))
+  if (kv_kind == 0 ? !encode_query_tmap(&p.tmap_q, q, num_tokens, n_q_heads, head_dim, group, p.q_box) ||
+                         !encode_block_tmap(&p.tmap_k, k_cache, num_blocks * n_kv_heads, head_dim) ||
+                         !encode_block_tmap(&p.tmap_v, v_cache, num_blocks * n_kv_heads, head_dim)
+                   : !encode_code_tmap(&p.tmap_k, k_cache, num_blocks * n_kv_heads * kBlockSize, head_dim))
     return PKV_ERR_CUDA;
-  p.k_codes = static_cast<const uint8_t*>(k_cache);
+  p.q = q;
   p.v_codes = static_cast<const uint8_t*>(v_cache);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
@@ -182,7 +184,7 @@ extern "C" pkv_status pkv_paged_prefill_attention_window(
   const int group = num_q_heads / num_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
   if (batch > 65535 || num_kv_heads > 65535 || num_tokens > INT32_MAX / group ||
-      num_blocks * num_kv_heads > INT32_MAX / 2)
+      num_blocks * num_kv_heads > INT32_MAX / kBlockSize)
     return PKV_ERR_UNSUPPORTED;
   if (batch == 0 || num_tokens == 0 || max_query_len == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out || num_blocks == 0)

@@ -49,12 +49,18 @@
 // is not finite is set to 0 there and the token remembered: at the end every row
 // that sees it adds the element itself (an infinity or a NaN whatever the weight).
 //
-// FP8 caches.  Codes are staged by 1-D copies and converted to fp16 tiles by eight
+// FP8 caches.  K's codes are an operand as they are (kind::f8f6f4, twice the rate
+// of fp16), so q is too: per row q 2^k, k such that its largest element lies in
+// [128, 256), is the sum of E4M3 parts -- the code of the element, of what is left,
+// and (fp16 q) of what is left of that -- two for bf16's 8 bits, three for fp16's
+// 11, exact to 2^-17 of the row's largest element (half a step of E4M3's denormals);
+// 2^-k joins the row's softmax scale.  V's codes are converted to fp16 tiles by four
 // warps: an E5M2 code is the upper byte of its half; an E4M3 code's bits, moved to
-// their places in a half, are its value times 2^-8 (denormals too), which the
-// scales take back.  (The conversion instruction took 1500 clocks a tile.)  q is
-// fp16 (bf16 q converted in place: exact in fp16's normal range).  The products
-// then run in fp16.
+// their places in a half, are its value times 2^-8 (denormals too), which the scale
+// takes back.  (With K converted as well, the integer pipe and shared memory took
+// 3900 clocks a tile; the conversion instruction alone 1500 a K tile.)  The moves are
+// masks and multiplications that leave a word's codes 0 2 1 3, so the columns 1 and 2
+// of every four change places in the output.
 //
 // Prompt chunks (CHUNK).  The same kernel attends the new tokens of a prompt to the
 // first tokens and a window: a thread block per unit, whose key tiles are those
@@ -62,8 +68,8 @@
 // the first num_sinks.
 //
 // Warps 0-7: softmax; 8 and 11: producers; 9: TMEM owner and Q K^T issuer; 10:
-// P V issuer; from 12 on: rows of V with drafted tokens (four warps), or the
-// conversions of K (four) and of V (four).  The softmax warps take registers
+// P V issuer; from 12 on: rows of V with drafted tokens (four warps), or q's parts
+// (four) and the conversions of V (four).  The softmax warps take registers
 // from the others, so that a row half's scores and its P stay in them.  Waits are
 // bounded as in the other kernels.
 #pragma once
@@ -94,7 +100,7 @@ template <int D, bool FP8, int NQ>
 struct TreeSmem {
   // warps that convert codes (or look at V rows) behind the first twelve, and the
   // registers that the softmax warps take from the others
-  static constexpr int kXform = 4;                                 // for K, and for V (16-bit: for V alone)
+  static constexpr int kXform = 4;                                 // for q, and for V (16-bit: for V alone)
   static constexpr int kThreads = 384 + 32 * kXform * (FP8 ? 2 : 1);
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;           // a thread, at launch
   static constexpr int kRegsSoftmax = FP8 ? 152 : 168, kRegsOther = FP8 ? 56 : 88;
@@ -102,17 +108,21 @@ struct TreeSmem {
   static constexpr int kTile = kTreeKeys * D * 2;                  // a Q, K or V tile
   static constexpr int kStage = kTile / 2;                         // FP8: a staged tile of codes
   static constexpr int kQBufs = 1;
-  static constexpr int kKStages = FP8 ? 1 : 2;
+  static constexpr int kKStages = FP8 ? 4 - NQ : 2;
   static constexpr int kVStages = FP8 ? 3 - NQ : 4 - NQ;
-  static constexpr int kCodeStages = FP8 ? 2 : 0;                  // of K, and of V
+  static constexpr int kCodeStages = FP8 ? 2 : 0;                  // of V
+  static constexpr int kParts = FP8 ? 3 : 1;                       // of q
+  static constexpr int kQTile = FP8 ? kParts * kStage : kTile;
+  static constexpr int kKTile = FP8 ? kStage : kTile;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQBufs * NQ * kTile;
-  static constexpr int kV = kK + kKStages * kTile;
+  static constexpr int kK = NQ * kQTile;
+  static constexpr int kV = kK + kKStages * kKTile;
   static constexpr int kCodes = kV + kVStages * kTile;
-  static constexpr int kBar = kCodes + 2 * kCodeStages * kStage;       // 512 bytes
+  static constexpr int kBar = kCodes + kCodeStages * kStage;       // 512 bytes
   static constexpr int kBad = kBar + 512;                          // uint32 [slots][warps][8]
   static constexpr int kRed = kBad + kTBadSlots * kXform * 32;     // float [128] references, [2][2][128] sums
-  static constexpr int kSeqs = kRed + 5 * kTreeRows * 4;           // TreeSeq [batch + 1]
+  static constexpr int kRowScale = kRed + 5 * kTreeRows * 4;       // FP8: float [slots][NQ][128]
+  static constexpr int kSeqs = kRowScale + (FP8 ? kTBadSlots * NQ * kTreeRows * 4 : 0);   // TreeSeq [batch + 1]
   static __host__ __device__ constexpr size_t bytes(int batch) {
     return 1024 + kSeqs + sizeof(TreeSeq) * (static_cast<size_t>(batch) + 1);
   }
@@ -123,10 +133,13 @@ struct TreeSmem {
   static constexpr int kGroup = 1024 * (D / 64);
   static constexpr int kHalf = 1024;
   static constexpr int kHalfQ = kTreeRows * 128;
+  // FP8 operands: rows of D bytes, 8-row atoms of the D-byte swizzle
+  static constexpr int kCodeGroup = 8 * D;
 };
 static_assert(TreeSmem<128, false, 1>::bytes(kTreeMaxBatch) <= 232448, "16-bit tiles");
 static_assert(TreeSmem<128, false, 2>::bytes(kTreeMaxBatch) <= 232448, "16-bit tiles");
 static_assert(TreeSmem<128, true, 1>::bytes(kTreeMaxBatch) <= 232448, "FP8 tiles");
+static_assert(TreeSmem<128, true, 2>::bytes(kTreeMaxBatch) <= 232448, "FP8 tiles");
 
 // a piece of a range: key tiles [t0, t1) of one unit
 struct TreeSeg {
@@ -257,22 +270,47 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return w & keep;
 }
 
-// four codes -> two pairs of halves (E4M3: times 2^-8)
-__device__ __forceinline__ uint2 codes4(uint32_t w, E5M2) {
-  return make_uint2(byte2_to_f16x2(w, E5M2{}), byte2_hi_to_f16x2(w, E5M2{}));
+__device__ __forceinline__ uint32_t mad_u32(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
+// codes 0, 2 and 1, 3 of a word -> two pairs of halves (E4M3: times 2^-8).  Per code
+// c: 128 (c + (c & 0x80)) for E4M3, 256 c for E5M2.
+__device__ __forceinline__ uint2 codes4(uint32_t w, E5M2) { return make_uint2((w << 8) & 0xff00ff00u, w & 0xff00ff00u); }
 __device__ __forceinline__ uint2 codes4(uint32_t w, E4M3) {
-  const uint32_t a = byte2_to_f16x2(w, E5M2{}), b = byte2_hi_to_f16x2(w, E5M2{});   // code c as c << 8
-  return make_uint2(((a >> 1) & 0x3f803f80u) | (a & 0x80008000u), ((b >> 1) & 0x3f803f80u) | (b & 0x80008000u));
+  const uint32_t o = w >> 8;
+  return make_uint2(mad_u32(w & 0x00800080u, 128u, mad_u32(w & 0x00ff00ffu, 128u, 0u)),
+                    mad_u32(o & 0x00800080u, 128u, mad_u32(o & 0x00ff00ffu, 128u, 0u)));
 }
 // a byte's top bit where an E4M3 code is a NaN (which codes4 makes a number)
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w, E4M3) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w, E4M3) { return mad_u32(w & 0x7f7f7f7fu, 1u, 0x01010101u); }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t, E5M2) { return 0u; }
-// of the two codes in bits 0-15 of w: the bits that make their halves NaN
+// the bits that make the halves of codes 0, 2 (1, 3 of w >> 8) of a word NaN
 __device__ __forceinline__ uint32_t nan_halves(uint32_t w, E4M3) {
-  return ((w & 0x7fu) == 0x7fu ? 0x7fffu : 0u) | ((w & 0x7f00u) == 0x7f00u ? 0x7fff0000u : 0u);
+  return ((w & 0x7fu) == 0x7fu ? 0x7fffu : 0u) | ((w & 0x7f0000u) == 0x7f0000u ? 0x7fff0000u : 0u);
 }
 __device__ __forceinline__ uint32_t nan_halves(uint32_t, E5M2) { return 0u; }
+
+// descriptor of an FP8 operand: rows of D bytes, K-major, D-byte swizzle
+template <int D>
+__device__ __forceinline__ uint64_t umma_desc_codes(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (1ull << 16) |
+         (static_cast<uint64_t>((8 * D) >> 4) << 32) | (1ull << 46) | ((D == 128 ? 2ull : 4ull) << 61);
+}
+// kind::f8f6f4: A in E4M3, B in KV, fp32 accumulate, both K-major, M = 128
+template <typename KV>
+__host__ __device__ constexpr uint32_t umma_idesc_codes(int n) {
+  return (1u << 4) | ((std::is_same<KV, E5M2>::value ? 1u : 0u) << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
 
 // MT: 16-bit type of the products; KV: the cache's (MT, or an FP8 format)
 // mbar_wait that gives up early once the block has stopped
@@ -311,29 +349,30 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   constexpr float kFold = std::is_same<KV, E4M3>::value ? 256.f : 1.f;   // of converted codes
   extern __shared__ unsigned char tsm_raw[];
   unsigned char* sm = tsm_raw + ((1024 - (smem_u32(tsm_raw) & 1023)) & 1023);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);   // [kKStages] K tile landed (FP8: converted)
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);   // [kKStages] K tile landed
   uint64_t* k_empty = k_full + L::kKStages;        // its Q K^T done
   uint64_t* v_full = k_empty + L::kKStages;        // [kVStages] V tile landed (16-bit)
   uint64_t* v_ready = v_full + L::kVStages;        // its rows looked at, or converted
   uint64_t* v_empty = v_ready + L::kVStages;       // its P V done
-  uint64_t* c_full = v_empty + L::kVStages;        // [2 kCodeStages] codes of K, of V landed
-  uint64_t* c_empty = c_full + 2 * L::kCodeStages; // converted
-  uint64_t* s_full = c_empty + 2 * L::kCodeStages; // [NB] scores ready
+  uint64_t* c_full = v_empty + L::kVStages;        // [kCodeStages] codes of V landed
+  uint64_t* c_empty = c_full + L::kCodeStages;     // converted
+  uint64_t* s_full = c_empty + L::kCodeStages;     // [NB] scores ready
   uint64_t* p_half = s_full + NB;                  // [NB] P of the upper keys written, O rescaled
   uint64_t* p_full = p_half + NB;                  // [NB] and of the lower ones
   uint64_t* pv_done = p_full + NB;                 // [NB] P V done
   uint64_t* q_full = pv_done + NB;                 // [kQBufs] Q of a piece landed
   uint64_t* q_empty = q_full + L::kQBufs;          // [kQBufs] its Q K^T done
-  uint64_t* q_ready = q_empty + L::kQBufs;         // Q converted (FP8)
+  uint64_t* q_ready = q_empty + L::kQBufs;         // q's parts written (FP8)
   uint64_t* turn = q_ready + 1;                    // [2][4] a group's warp has passed its rows' references on
   uint64_t* joined = turn + 8;                     // [2][4] and its sums of a piece
   uint64_t* o_read = joined + 8;                   // 8 arrivals: a piece's outputs are out of TMEM
   uint64_t* mma_idle = o_read + 1;                 // [2] an issuer's MMAs done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * 2 + 3 * 3 + 2 * 4 + 4 * 3 + 5 + 17 + 2 + 1) * 8 <= 512, "barrier block overflows");
+  static_assert((2 * 3 + 3 * 3 + 2 * 2 + 4 * 3 + 5 + 17 + 2 + 1) * 8 <= 512, "barrier block overflows");
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + L::kBad);
   float* red = reinterpret_cast<float*>(sm + L::kRed);
+  float* row_scale = reinterpret_cast<float*>(sm + L::kRowScale);
   TreeSeq* seqs = reinterpret_cast<TreeSeq*>(sm + L::kSeqs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -347,7 +386,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   if (tid == 8 * 32) {
     *abort_flag = 0;
     for (int s = 0; s < L::kKStages; ++s) {
-      mbar_init(&k_full[s], kFp8 ? L::kXform : 1);
+      mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < L::kVStages; ++s) {
@@ -355,7 +394,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       mbar_init(&v_ready[s], L::kXform);
       mbar_init(&v_empty[s], 1);
     }
-    for (int s = 0; s < 2 * L::kCodeStages; ++s) {
+    for (int s = 0; s < L::kCodeStages; ++s) {
       mbar_init(&c_full[s], 1);
       mbar_init(&c_empty[s], L::kXform);
     }
@@ -471,7 +510,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const int unit_row = sg.unit * kTreeRows * NQ + row;            // of the sequence's rows
       const int node = min(unit_row >> shift, sq.n - 1);
       const uint32_t* words = p.mask + (static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words);
-      const float scale_log2 = p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] * kFold : 1.f);
+      const float piece_scale = p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] : 1.f);
       const uint32_t to = tmem + lane_base + L::kOCol + tile * D;
       float m_ref = -INFINITY, l_run = 0.f;
       // take over the row's reference of the operation before
@@ -518,6 +557,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         ok = ok && wait(&s_full[buf], ph);
         if (!ok) break;
         tc_fence_after();
+        // (FP8: q's parts, and so the scores, are scaled by row)
+        const float scale_log2 =
+            kFp8 ? piece_scale * row_scale[((slot % kTBadSlots) * NQ + tile) * kTreeRows + r] : piece_scale;
         float v[64];
         auto load_half = [&](int h) {
           tmem_ld64(ts + 64 * h, v);
@@ -646,6 +688,14 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         tmem_ld32(to + x, o);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] *= weight;
+        if constexpr (kFp8) {
+          // (converted words hold codes 0 2 1 3)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float x1 = o[i + 1];
+            o[i + 1] = o[i + 2], o[i + 2] = x1;
+          }
+        }
         if (any_bad) {
           // (rare) every row adds what it sees of them
           for (int w = 0; w < (CHUNK ? kBadWords : 2 * p.mask_words); ++w) {
@@ -701,11 +751,11 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
     // behind it; one warp for both, K behind V, cost 15 % of the whole)
     set_max_regs_down<L::kRegsOther>();
     const bool is_v = warp == 11;
-    constexpr int kKindStages = kFp8 ? L::kCodeStages : L::kVStages;   // V's; K's below
-    const uint32_t stages = kFp8 || is_v ? kKindStages : L::kKStages;
-    uint64_t* full = kFp8 ? c_full + (is_v ? L::kCodeStages : 0) : is_v ? v_full : k_full;
-    uint64_t* empty = kFp8 ? c_empty + (is_v ? L::kCodeStages : 0) : is_v ? v_empty : k_empty;
-    unsigned char* ring = sm + (kFp8 ? L::kCodes + (is_v ? L::kCodeStages * L::kStage : 0) : is_v ? L::kV : L::kK);
+    const bool codes_v = kFp8 && is_v;               // V's codes go to the conversion
+    const uint32_t stages = codes_v ? L::kCodeStages : is_v ? L::kVStages : L::kKStages;
+    uint64_t* full = codes_v ? c_full : is_v ? v_full : k_full;
+    uint64_t* empty = codes_v ? c_empty : is_v ? v_empty : k_empty;
+    unsigned char* ring = sm + (codes_v ? L::kCodes : is_v ? L::kV : L::kK);
     uint32_t s = 0, use = 0, tiles = 0, pieces = 0;  // stage and its use of the next tile; issued so far
     bool good = true;
     if (is_v)
@@ -733,7 +783,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         return (x >= sg.t0 && wanted(blk)) ? row[blk] : -1;
       };
       int id = fetch_id(sg.t1 - 1);
-      if (!is_v) {
+      if (!kFp8 && !is_v) {
         // Q of the piece, once every Q K^T of the buffer's piece before has read it
         const uint32_t qb = pieces % L::kQBufs, q_use = pieces / L::kQBufs;
         if (q_use > 0) good = __all_sync(0xffffffffu, tree_wait(&q_empty[qb], (q_use - 1) & 1, p, abort_flag));
@@ -767,6 +817,12 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if (lane < kTTileBlocks)
             tma_load_4d(ring + s * L::kTile + lane * (kBlockSize * D * 2), is_v ? &p.tmap_v : &p.tmap_k,
                         static_cast<int>(slab) * 2, &full[s], pol);
+        } else if (!is_v) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kKTile);
+          __syncwarp();
+          if (lane < kTTileBlocks)
+            tma_load_2d(ring + s * L::kKTile + lane * (kBlockSize * D), &p.tmap_k, 0, static_cast<int>(slab) * kBlockSize,
+                        &full[s], pol);
         } else {
           constexpr int kSlab = kBlockSize * D;
           unsigned char* dst = ring + s * L::kStage + lane * kSlab;
@@ -779,7 +835,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(got) * kSlab);
           __syncwarp();
-          if (have) bulk_g2s(dst, (is_v ? p.v_codes : p.k_codes) + slab * kSlab, kSlab, &full[s], pol);
+          if (have) bulk_g2s(dst, p.v_codes + slab * kSlab, kSlab, &full[s], pol);
         }
         __syncwarp();
         ++tiles;
@@ -807,6 +863,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
     // thread until the MMA queue has drained to a few entries; meanwhile the
     // other feeds the queue.
     constexpr int kPasses = kSplit ? 2 : 1;
+    const int parts = p.q_bf16 ? 2 : 3;              // of an FP8 operand q
     constexpr uint32_t kIdQK = umma_idesc<MT>(false, kTreeKeys), kIdPV = umma_idesc<MT>(true, D);
     const bool qk_warp = (warp == 9);
     bool ok = true;
@@ -823,8 +880,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         const uint32_t qb = pieces % L::kQBufs;
         if (qk_warp) {
           // (the producer loads nothing while the previous kernel runs)
-          ok = mbar_wait_started_early(kFp8 && p.q_bf16 ? q_ready : &q_full[qb], (pieces / L::kQBufs) & 1, p.err,
-                                       p.wait_limit_ns);
+          ok = mbar_wait_started_early(kFp8 ? q_ready : &q_full[qb], (pieces / L::kQBufs) & 1, p.err, p.wait_limit_ns);
         }
         // (the piece's first P V overwrites the outputs of the piece before)
         if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
@@ -843,12 +899,27 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
               ok = ops < NB || tree_wait(&pv_done[sr.s], sr.ph ^ 1u, p, abort_flag);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (qb * NQ + c) * L::kTile), 16, 1024);
-              const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
+              if constexpr (kFp8) {
+                const uint64_t a0 = umma_desc_codes<D>(smem_u32(sm + L::kQ + c * L::kQTile));
+                const uint64_t b0 = umma_desc_codes<D>(smem_u32(sm + L::kK + kr.s * L::kKTile));
+                constexpr uint32_t kIdCodes = umma_idesc_codes<KV>(kTreeKeys);
+                // (the smallest parts first)
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                umma_f16(d_s, a0 + static_cast<uint64_t>(((ks >> 2) * L::kHalfQ + (ks & 3) * 32) >> 4),
-                         b0 + static_cast<uint64_t>(((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
+                for (int part = L::kParts - 1; part >= 0; --part) {
+                  if (part >= parts) continue;
+#pragma unroll
+                  for (int ks = 0; ks < D / 32; ++ks)
+                    umma_f8(d_s, a0 + static_cast<uint64_t>((part * L::kStage + ks * 32) >> 4),
+                            b0 + static_cast<uint64_t>((ks * 32) >> 4), kIdCodes, ks > 0 || part < parts - 1);
+                }
+              } else {
+                const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (qb * NQ + c) * L::kTile), 16, 1024);
+                const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                  umma_f16(d_s, a0 + static_cast<uint64_t>(((ks >> 2) * L::kHalfQ + (ks & 3) * 32) >> 4),
+                           b0 + static_cast<uint64_t>(((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
+              }
               umma_commit(&s_full[sr.s]);
             } else {
               const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + vr.s * L::kTile), L::kHalf, L::kGroup);
@@ -896,7 +967,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
     const bool is_v = !kFp8 || warp >= 12 + L::kXform;
     const int x_tid = tid - (12 + (kFp8 && is_v ? L::kXform : 0)) * 32, x_warp = x_tid >> 5;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a 16-bit row
-    Ring<L::kKStages> kr;
     Ring<L::kVStages> vr;
     Ring<(kFp8 ? L::kCodeStages : 1)> cr;
     uint32_t pieces = 0, tiles = 0;
@@ -954,23 +1024,76 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         return v;
       };
       if constexpr (kFp8) {
-        if (p.q_bf16 && !is_v) {
-          // bf16 q to fp16, where it lies
-          ok = wait_all(q_full, pieces & 1);
-          if (!ok) break;
+        if (!is_v) {
+          // q's parts, a thread per row: its largest element, then, once every Q K^T
+          // of the piece before has read them, the parts
           const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-          for (int x = x_tid; x < nq * L::kTile / 16; x += L::kXform * 32) {
-            uint4* w = reinterpret_cast<uint4*>(sm + L::kQ) + x;
-            const uint4 v = *w;
-            auto half2 = [&](uint32_t u) {
-              const float2 f = unpack2(u, BF16{});
-              return pack2(f.x, f.y, F16{});
-            };
-            *w = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+#pragma unroll 1
+          for (int c = 0; c < nq && ok; ++c) {
+            const int row = c * kTreeRows + x_tid, unit_row = sg.unit * kTreeRows * NQ + row;
+            const bool live = row < sg.rows;
+            const int head = (sg.g << shift) + (unit_row & ((1 << shift) - 1));
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(p.q) +
+                ((static_cast<int64_t>(sq.start) + (unit_row >> shift)) * p.n_q_heads + head) * D);
+            auto pair = [&](uint32_t w) { return p.q_bf16 ? unpack2(w, BF16{}) : unpack2(w, F16{}); };
+            float top = 0.f;
+            bool nan = false;
+            if (live) {
+#pragma unroll 4
+              for (int x = 0; x < D / 8; ++x) {
+                const uint4 v = src[x];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = pair(w[e]);
+                  top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                  nan |= !(fabsf(f.x) <= 3.402823466e38f) | !(fabsf(f.y) <= 3.402823466e38f);
+                }
+              }
+            }
+            // top in [2^e, 2^(e + 1)): times 2^(7 - e)
+            const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -113);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+            if (c == 0 && pieces > 0) ok = wait_all(q_empty, (pieces - 1) & 1);
+            if (!ok) break;
+            row_scale[((pieces % kTBadSlots) * NQ + c) * kTreeRows + x_tid] =
+                __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+            if (live) {
+              const uint32_t base_addr = smem_u32(sm + L::kQ + c * L::kQTile) + (x_tid >> 3) * L::kCodeGroup +
+                                         (x_tid & 7) * D;
+              const uint32_t turn_bits = D == 128 ? x_tid & 7 : (x_tid >> 1) & 3;   // of the row's swizzle
+#pragma unroll 1
+              for (int x = 0; x < D / 16; ++x) {
+                const uint4 v[2] = {src[2 * x], src[2 * x + 1]};
+                const uint32_t in[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+                uint32_t w[L::kParts][4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  float2 f = pair(in[e]);
+                  f.x *= up, f.y *= up;
+#pragma unroll
+                  for (int part = 0; part < L::kParts; ++part) {
+                    uint32_t code = fp8x2_from_f32(f.x, f.y, E4M3{});
+                    const float2 back = unpack2_e4m3(static_cast<uint16_t>(code));
+                    f.x -= back.x, f.y -= back.y;
+                    if (nan) code = 0x7f7fu;         // (an infinity or a NaN: so is the row's output)
+                    w[part][e / 2] = e & 1 ? w[part][e / 2] | (code << 16) : code;
+                  }
+                }
+#pragma unroll
+                for (int part = 0; part < L::kParts; ++part)
+                  store(base_addr + part * L::kStage + ((x ^ turn_bits) << 4),
+                        make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]));
+              }
+            }
           }
+          if (!ok) break;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(q_ready);
+          ++pieces;
+          continue;
         }
       }
       ++pieces;
@@ -994,12 +1117,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if (lane == 0) mbar_arrive(&v_ready[vr.s]);
           vr.next();
         } else {
-          const uint32_t stages = is_v ? L::kVStages : L::kKStages, code = (is_v ? L::kCodeStages : 0) + cr.s;
-          ok = wait_all(&c_full[code], cr.ph) &&
-               (tiles < stages || wait_all(is_v ? &v_empty[vr.s] : &k_empty[kr.s], (is_v ? vr.ph : kr.ph) ^ 1u));
+          ok = wait_all(&c_full[cr.s], cr.ph) && (tiles < L::kVStages || wait_all(&v_empty[vr.s], vr.ph ^ 1u));
           if (!ok) break;
-          const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + code * L::kStage);
-          const uint32_t tile = smem_u32(sm + (is_v ? L::kV + vr.s * L::kTile : L::kK + kr.s * L::kTile));
+          const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + cr.s * L::kStage);
+          const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
           // Chunk k of 16 codes of this thread is 4096 bytes of the tile behind chunk k - 1
           // (whole groups of 8 keys), so its two places are constants away.  The lanes of
           // a row's upper half convert and store its second 8 codes first: both halves of
@@ -1026,7 +1147,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
               store(last8 + (k0 + k) * 4096, make_uint4(w2.x, w2.y, w3.x, w3.y));
             }
           }
-          const bool tail = is_v && (t + 1) * kTreeKeys > base;
+          const bool tail = (t + 1) * kTreeKeys > base;
           if (tail || (nan & 0x80808080u)) {
             // (rare) E4M3's NaN codes became numbers; V rows from the first drafted
             // token on.  Each thread looks at what it wrote.
@@ -1038,8 +1159,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
                 const uint32_t addr = tile + at(j, 2 * c + e);
                 uint4 v = load(addr);
                 const uint2 w = reinterpret_cast<const uint2*>(codes + x)[e];
-                v.x |= nan_halves(w.x, KV{}), v.y |= nan_halves(w.x >> 16, KV{});
-                v.z |= nan_halves(w.y, KV{}), v.w |= nan_halves(w.y >> 16, KV{});
+                v.x |= nan_halves(w.x, KV{}), v.y |= nan_halves(w.x >> 8, KV{});
+                v.z |= nan_halves(w.y, KV{}), v.w |= nan_halves(w.y >> 8, KV{});
                 store(addr, tail ? clean(v, t * kTreeKeys + j) : v);
               }
             }
@@ -1047,11 +1168,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&c_empty[code]);
-            mbar_arrive(is_v ? &v_ready[vr.s] : &k_full[kr.s]);
+            mbar_arrive(&c_empty[cr.s]);
+            mbar_arrive(&v_ready[vr.s]);
           }
           cr.next();
-          kr.next();
           vr.next();
         }
       }

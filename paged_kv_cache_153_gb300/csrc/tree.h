@@ -23,9 +23,9 @@ struct TreeSeq {
 
 struct TreeParams {
   CUtensorMap tmap_k;            // 16-bit caches: [NB Hkv 2, D / 64, 8, 64], boxes of a block's rows
-  CUtensorMap tmap_v;
-  CUtensorMap tmap_q;            // [T, Hq, D], boxes of [q_box tokens, G, 64]
-  const uint8_t* k_codes;        // FP8 caches
+  CUtensorMap tmap_v;            // (FP8: tmap_k alone, [NB Hkv 16, D] bytes, boxes of 16 rows, D-byte swizzle)
+  CUtensorMap tmap_q;            // 16-bit caches: [T, Hq, D], boxes of [q_box tokens, G, 64]
+  const void* q;                 // FP8 caches
   const uint8_t* v_codes;
   const float* k_scale;
   const float* v_scale;
