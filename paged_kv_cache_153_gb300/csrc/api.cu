@@ -85,14 +85,14 @@ int sm_count() {
   return n;
 }
 
-static bool encode_16bit(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                         const cuuint32_t* box) {
+static bool encode_tiled(CUtensorMap* map, int elt_bytes, const void* base, int rank, const cuuint64_t* dims,
+                         const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
   if (encode == nullptr) return false;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank),
-                            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = encode(map, elt_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                            static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled: CUresult %d", static_cast<int>(r));
@@ -108,7 +108,7 @@ bool encode_query_tmap(CUtensorMap* map, const void* base, int64_t tokens, int n
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                                  static_cast<cuuint64_t>(head_dim) * 2 * n_q_heads};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(box_tokens)};
-  return encode_16bit(map, base, 3, dims, strides, box);
+  return encode_tiled(map, 2, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool encode_block_tmap(CUtensorMap* map, const void* base, int64_t slabs, int head_dim) {
@@ -116,24 +116,29 @@ bool encode_block_tmap(CUtensorMap* map, const void* base, int64_t slabs, int he
   const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(head_dim) / 64, static_cast<cuuint64_t>(slabs) * 2};
   const cuuint64_t strides[3] = {row, 128, 8 * row};
   const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(head_dim / 64), 2};
-  return encode_16bit(map, base, 4, dims, strides, box);
+  return encode_tiled(map, 2, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// the swizzle of rows of 64 or 128 bytes
+static CUtensorMapSwizzle row_swizzle(int bytes) {
+  return bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
 }
 
 bool encode_code_tmap(CUtensorMap* map, const void* base, int64_t rows, int head_dim) {
-  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
-  if (encode == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(head_dim), 16}, estr[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled: CUresult %d", static_cast<int>(r));
-    return false;
-  }
-  return true;
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(head_dim), 16};
+  return encode_tiled(map, 1, base, 2, dims, strides, box, row_swizzle(head_dim));
+}
+
+bool encode_parts_tmap(CUtensorMap* map, const void* base, int64_t tokens, int n_q_heads, int head_dim, int group,
+                       int box_tokens) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(n_q_heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(head_dim) * n_q_heads};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(head_dim), static_cast<cuuint32_t>(group),
+                             static_cast<cuuint32_t>(box_tokens)};
+  return encode_tiled(map, 1, base, 3, dims, strides, box, row_swizzle(head_dim));
 }
 
 namespace {

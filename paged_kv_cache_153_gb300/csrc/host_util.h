@@ -58,6 +58,11 @@ bool encode_block_tmap(CUtensorMap* map, const void* base, int64_t slabs, int he
 // swizzle of a row's bytes (64 or 128).
 bool encode_code_tmap(CUtensorMap* map, const void* base, int64_t rows, int head_dim);
 
+// encode_query_tmap over one-byte elements: boxes of [box_tokens, group heads,
+// head_dim] and a swizzle of a row's bytes.
+bool encode_parts_tmap(CUtensorMap* map, const void* base, int64_t tokens, int n_q_heads, int head_dim, int group,
+                       int box_tokens);
+
 // SMs of the current device (0, with the reason kept, when it cannot be asked)
 int sm_count();
 

@@ -54,8 +54,9 @@
 // [128, 256), is the sum of E4M3 parts -- the code of the element, of what is left,
 // and (fp16 q) of what is left of that -- two for bf16's 8 bits, three for fp16's
 // 11, exact to 2^-17 of the row's largest element (half a step of E4M3's denormals);
-// 2^-k joins the row's softmax scale.  V's codes are converted to fp16 tiles by four
-// warps: an E5M2 code is the upper byte of its half; an E4M3 code's bits, moved to
+// 2^-k joins the row's softmax scale.  A launch of its own writes the parts to the
+// workspace (in the kernel, per piece, four warps took 6 to 13 us).  V's codes are
+// converted to fp16 tiles by eight warps: an E5M2 code is the upper byte of its half; an E4M3 code's bits, moved to
 // their places in a half, are its value times 2^-8 (denormals too), which the scale
 // takes back.  (With K converted as well, the integer pipe and shared memory took
 // 3900 clocks a tile; the conversion instruction alone 1500 a K tile.)  The moves are
@@ -68,8 +69,8 @@
 // the first num_sinks.
 //
 // Warps 0-7: softmax; 8 and 11: producers; 9: TMEM owner and Q K^T issuer; 10:
-// P V issuer; from 12 on: rows of V with drafted tokens (four warps), or q's parts
-// (four) and the conversions of V (four).  The softmax warps take registers
+// P V issuer; from 12 on: rows of V with drafted tokens (four warps), or the
+// conversions of V (eight).  The softmax warps take registers
 // from the others, so that a row half's scores and its P stay in them.  Waits are
 // bounded as in the other kernels.
 #pragma once
@@ -100,10 +101,10 @@ template <int D, bool FP8, int NQ>
 struct TreeSmem {
   // warps that convert codes (or look at V rows) behind the first twelve, and the
   // registers that the softmax warps take from the others
-  static constexpr int kXform = 4;                                 // for q, and for V (16-bit: for V alone)
-  static constexpr int kThreads = 384 + 32 * kXform * (FP8 ? 2 : 1);
+  static constexpr int kXform = FP8 ? 8 : 4;
+  static constexpr int kThreads = 384 + 32 * kXform;
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;           // a thread, at launch
-  static constexpr int kRegsSoftmax = FP8 ? 152 : 168, kRegsOther = FP8 ? 56 : 88;
+  static constexpr int kRegsSoftmax = FP8 ? 152 : 184, kRegsOther = FP8 ? 56 : 72;
   static_assert(kTSoftmax * kRegsSoftmax + (kThreads - kTSoftmax) * kRegsOther <= kThreads * kRegs, "registers");
   static constexpr int kTile = kTreeKeys * D * 2;                  // a Q, K or V tile
   static constexpr int kStage = kTile / 2;                         // FP8: a staged tile of codes
@@ -121,8 +122,7 @@ struct TreeSmem {
   static constexpr int kBar = kCodes + kCodeStages * kStage;       // 512 bytes
   static constexpr int kBad = kBar + 512;                          // uint32 [slots][warps][8]
   static constexpr int kRed = kBad + kTBadSlots * kXform * 32;     // float [128] references, [2][2][128] sums
-  static constexpr int kRowScale = kRed + 5 * kTreeRows * 4;       // FP8: float [slots][NQ][128]
-  static constexpr int kSeqs = kRowScale + (FP8 ? kTBadSlots * NQ * kTreeRows * 4 : 0);   // TreeSeq [batch + 1]
+  static constexpr int kSeqs = kRed + 5 * kTreeRows * 4;           // TreeSeq [batch + 1]
   static __host__ __device__ constexpr size_t bytes(int batch) {
     return 1024 + kSeqs + sizeof(TreeSeq) * (static_cast<size_t>(batch) + 1);
   }
@@ -362,8 +362,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   uint64_t* pv_done = p_full + NB;                 // [NB] P V done
   uint64_t* q_full = pv_done + NB;                 // [kQBufs] Q of a piece landed
   uint64_t* q_empty = q_full + L::kQBufs;          // [kQBufs] its Q K^T done
-  uint64_t* q_ready = q_empty + L::kQBufs;         // q's parts written (FP8)
-  uint64_t* turn = q_ready + 1;                    // [2][4] a group's warp has passed its rows' references on
+  uint64_t* turn = q_empty + L::kQBufs;                  // [2][4] a group's warp has passed its rows' references on
   uint64_t* joined = turn + 8;                     // [2][4] and its sums of a piece
   uint64_t* o_read = joined + 8;                   // 8 arrivals: a piece's outputs are out of TMEM
   uint64_t* mma_idle = o_read + 1;                 // [2] an issuer's MMAs done
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   static_assert((2 * 3 + 3 * 3 + 2 * 2 + 4 * 3 + 5 + 17 + 2 + 1) * 8 <= 512, "barrier block overflows");
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + L::kBad);
   float* red = reinterpret_cast<float*>(sm + L::kRed);
-  float* row_scale = reinterpret_cast<float*>(sm + L::kRowScale);
   TreeSeq* seqs = reinterpret_cast<TreeSeq*>(sm + L::kSeqs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -408,7 +406,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
     }
-    mbar_init(q_ready, L::kXform);
     for (int s = 0; s < 8; ++s) {
       mbar_init(&turn[s], 1);
       mbar_init(&joined[s], 1);
@@ -510,7 +507,11 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const int unit_row = sg.unit * kTreeRows * NQ + row;            // of the sequence's rows
       const int node = min(unit_row >> shift, sq.n - 1);
       const uint32_t* words = p.mask + (static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words);
-      const float piece_scale = p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] : 1.f);
+      // (FP8: q's parts, and so the scores, are scaled by row)
+      const float scale_log2 =
+          p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
+                                                                   (sg.g << shift) + (unit_row & ((1 << shift) - 1))]
+                                  : 1.f);
       const uint32_t to = tmem + lane_base + L::kOCol + tile * D;
       float m_ref = -INFINITY, l_run = 0.f;
       // take over the row's reference of the operation before
@@ -557,9 +558,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         ok = ok && wait(&s_full[buf], ph);
         if (!ok) break;
         tc_fence_after();
-        // (FP8: q's parts, and so the scores, are scaled by row)
-        const float scale_log2 =
-            kFp8 ? piece_scale * row_scale[((slot % kTBadSlots) * NQ + tile) * kTreeRows + r] : piece_scale;
         float v[64];
         auto load_half = [&](int h) {
           tmem_ld64(ts + 64 * h, v);
@@ -783,15 +781,24 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         return (x >= sg.t0 && wanted(blk)) ? row[blk] : -1;
       };
       int id = fetch_id(sg.t1 - 1);
-      if (!kFp8 && !is_v) {
+      if (!is_v) {
         // Q of the piece, once every Q K^T of the buffer's piece before has read it
         const uint32_t qb = pieces % L::kQBufs, q_use = pieces / L::kQBufs;
         if (q_use > 0) good = __all_sync(0xffffffffu, tree_wait(&q_empty[qb], (q_use - 1) & 1, p, abort_flag));
         if (!good) break;
-        if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], nq * (D / 64) * (p.q_box << shift) * 128);
+        const int parts = kFp8 ? (p.q_bf16 ? 2 : 3) : 1;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&q_full[qb], nq * parts * (p.q_box << shift) * (kFp8 ? D : 2 * D));
         ++pieces;
         __syncwarp();
-        if (lane < nq * (D / 64)) {
+        if (kFp8 && lane < nq * parts) {
+          const int c = lane / parts, part = lane % parts;
+          tma_load_3d(sm + L::kQ + c * L::kQTile + part * L::kStage, &p.tmap_q, 0, sg.g << shift,
+                      static_cast<int>(part * p.num_tokens) + sq.start +
+                          ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift),
+                      &q_full[qb], policy_evict_last());
+        }
+        if (!kFp8 && lane < nq * (D / 64)) {
           const int c = lane / (D / 64), h = lane % (D / 64);
           tma_load_3d(sm + L::kQ + (qb * NQ + c) * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
                       sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), &q_full[qb],
@@ -880,7 +887,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         const uint32_t qb = pieces % L::kQBufs;
         if (qk_warp) {
           // (the producer loads nothing while the previous kernel runs)
-          ok = mbar_wait_started_early(kFp8 ? q_ready : &q_full[qb], (pieces / L::kQBufs) & 1, p.err, p.wait_limit_ns);
+          ok = mbar_wait_started_early(&q_full[qb], (pieces / L::kQBufs) & 1, p.err, p.wait_limit_ns);
         }
         // (the piece's first P V overwrites the outputs of the piece before)
         if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
@@ -964,8 +971,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   } else {
     // ============ warps from 12 on: rows with drafted tokens, conversions ============
     set_max_regs_down<L::kRegsOther>();
-    const bool is_v = !kFp8 || warp >= 12 + L::kXform;
-    const int x_tid = tid - (12 + (kFp8 && is_v ? L::kXform : 0)) * 32, x_warp = x_tid >> 5;
+    const int x_tid = tid - 12 * 32, x_warp = x_tid >> 5;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a 16-bit row
     Ring<L::kVStages> vr;
     Ring<(kFp8 ? L::kCodeStages : 1)> cr;
@@ -982,7 +988,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const TreeSeq sq = sequence_of(sg);
       const int base = sq.ctx - sq.n;
       uint32_t* my_bad = bad + (pieces % kTBadSlots) * (L::kXform * 8) + x_warp * kBadWords;
-      if (is_v && lane < kBadWords) my_bad[lane] = 0u;
+      if (lane < kBadWords) my_bad[lane] = 0u;
       __syncwarp();
       auto store = [&](uint32_t addr, const uint4& v) {
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -1023,79 +1029,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         }
         return v;
       };
-      if constexpr (kFp8) {
-        if (!is_v) {
-          // q's parts, a thread per row: its largest element, then, once every Q K^T
-          // of the piece before has read them, the parts
-          const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-#pragma unroll 1
-          for (int c = 0; c < nq && ok; ++c) {
-            const int row = c * kTreeRows + x_tid, unit_row = sg.unit * kTreeRows * NQ + row;
-            const bool live = row < sg.rows;
-            const int head = (sg.g << shift) + (unit_row & ((1 << shift) - 1));
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(p.q) +
-                ((static_cast<int64_t>(sq.start) + (unit_row >> shift)) * p.n_q_heads + head) * D);
-            auto pair = [&](uint32_t w) { return p.q_bf16 ? unpack2(w, BF16{}) : unpack2(w, F16{}); };
-            float top = 0.f;
-            bool nan = false;
-            if (live) {
-#pragma unroll 4
-              for (int x = 0; x < D / 8; ++x) {
-                const uint4 v = src[x];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float2 f = pair(w[e]);
-                  top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                  nan |= !(fabsf(f.x) <= 3.402823466e38f) | !(fabsf(f.y) <= 3.402823466e38f);
-                }
-              }
-            }
-            // top in [2^e, 2^(e + 1)): times 2^(7 - e)
-            const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -113);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
-            if (c == 0 && pieces > 0) ok = wait_all(q_empty, (pieces - 1) & 1);
-            if (!ok) break;
-            row_scale[((pieces % kTBadSlots) * NQ + c) * kTreeRows + x_tid] =
-                __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
-            if (live) {
-              const uint32_t base_addr = smem_u32(sm + L::kQ + c * L::kQTile) + (x_tid >> 3) * L::kCodeGroup +
-                                         (x_tid & 7) * D;
-              const uint32_t turn_bits = D == 128 ? x_tid & 7 : (x_tid >> 1) & 3;   // of the row's swizzle
-#pragma unroll 1
-              for (int x = 0; x < D / 16; ++x) {
-                const uint4 v[2] = {src[2 * x], src[2 * x + 1]};
-                const uint32_t in[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-                uint32_t w[L::kParts][4];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  float2 f = pair(in[e]);
-                  f.x *= up, f.y *= up;
-#pragma unroll
-                  for (int part = 0; part < L::kParts; ++part) {
-                    uint32_t code = fp8x2_from_f32(f.x, f.y, E4M3{});
-                    const float2 back = unpack2_e4m3(static_cast<uint16_t>(code));
-                    f.x -= back.x, f.y -= back.y;
-                    if (nan) code = 0x7f7fu;         // (an infinity or a NaN: so is the row's output)
-                    w[part][e / 2] = e & 1 ? w[part][e / 2] | (code << 16) : code;
-                  }
-                }
-#pragma unroll
-                for (int part = 0; part < L::kParts; ++part)
-                  store(base_addr + part * L::kStage + ((x ^ turn_bits) << 4),
-                        make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]));
-              }
-            }
-          }
-          if (!ok) break;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_ready);
-          ++pieces;
-          continue;
-        }
-      }
       ++pieces;
       for (int x0 = sg.t1 - 1; x0 >= sg.t0 && ok; --x0, ++tiles) {
         const int t = tile_at(sg, x0);
@@ -1121,31 +1054,29 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if (!ok) break;
           const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + cr.s * L::kStage);
           const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
-          // Chunk k of 16 codes of this thread is 4096 bytes of the tile behind chunk k - 1
+          // Chunk k of 16 codes of this thread is 8192 bytes of the tile behind chunk k - 1
           // (whole groups of 8 keys), so its two places are constants away.  The lanes of
           // a row's upper half convert and store its second 8 codes first: both halves of
           // a row lie in the same banks.
           constexpr int kAll = kTreeKeys * D / 16, kStep = L::kXform * 32;
-          static_assert(kStep / (D / 16) % 8 == 0 && kStep / (D / 16) / 8 * L::kGroup == 4096, "chunk step");
-          constexpr int kPer = 4;                    // chunks whose instructions interleave
+          static_assert(kStep / (D / 16) % 8 == 0 && kStep / (D / 16) / 8 * L::kGroup == 8192, "chunk step");
+          constexpr int kPer = kAll / kStep;
+          static_assert(kPer <= 4 && kPer * kStep == kAll, "chunks");
           const int j0 = x_tid / (D / 16), c0 = x_tid % (D / 16);
           const bool up = D == 128 && (c0 & 4);
           const uint32_t first8 = tile + at(j0, 2 * c0 + (up ? 1 : 0)), last8 = tile + at(j0, 2 * c0 + (up ? 0 : 1));
           uint32_t nan = 0;
-#pragma unroll 1
-          for (int k0 = 0; k0 < kAll / kStep; k0 += kPer) {
-            uint4 raw[kPer];
+          uint4 raw[kPer];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + (k0 + k) * kStep];
+          for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + k * kStep];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const uint4 w = raw[k];
-              nan |= nan_codes(w.x, KV{}) | nan_codes(w.y, KV{}) | nan_codes(w.z, KV{}) | nan_codes(w.w, KV{});
-              const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
-              const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
-              store(first8 + (k0 + k) * 4096, make_uint4(w0.x, w0.y, w1.x, w1.y));
-              store(last8 + (k0 + k) * 4096, make_uint4(w2.x, w2.y, w3.x, w3.y));
-            }
+          for (int k = 0; k < kPer; ++k) {
+            const uint4 w = raw[k];
+            nan |= nan_codes(w.x, KV{}) | nan_codes(w.y, KV{}) | nan_codes(w.z, KV{}) | nan_codes(w.w, KV{});
+            const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
+            const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
+            store(first8 + k * 8192, make_uint4(w0.x, w0.y, w1.x, w1.y));
+            store(last8 + k * 8192, make_uint4(w2.x, w2.y, w3.x, w3.y));
           }
           const bool tail = (t + 1) * kTreeKeys > base;
           if (tail || (nan & 0x80808080u)) {
@@ -1183,6 +1114,60 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   tc_fence_after();
   if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// q as a sum of E4M3 parts (FP8 caches): a warp per row of D elements, a lane per D /
+// 32 of them.  parts [3, rows, D] codes, scale [rows].
+// ---------------------------------------------------------------------------
+constexpr int kTPartWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kTPartWarps * 32)
+    tree_parts_kernel(const void* __restrict__ q, int q_bf16, int64_t rows, uint8_t* __restrict__ parts,
+                      float* __restrict__ scale) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31;
+  pdl_wait_and_release();   // (the next kernel waits for this one before it reads what this writes)
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kTPartWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(q) + row * D) + lane * (N / 2);
+  float f[N];
+  float top = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    const float2 x = q_bf16 ? unpack2(src[e], BF16{}) : unpack2(src[e], F16{});
+    f[2 * e] = x.x, f[2 * e + 1] = x.y;
+    top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    nan |= !isfinite(x.x) | !isfinite(x.y);
+  }
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  nan = __any_sync(0xffffffffu, nan);
+  // top in [2^e, 2^(e + 1)): times 2^(7 - e)
+  const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -113);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+  if (lane == 0) scale[row] = nan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] *= up;
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      uint32_t code = fp8x2_from_f32(f[e], f[e + 1], E4M3{});
+      const float2 back = unpack2_e4m3(static_cast<uint16_t>(code));
+      f[e] -= back.x, f[e + 1] -= back.y;
+      if (nan) code = 0x7f7fu;                       // (an infinity or a NaN: so is the row's output)
+      w |= code << (8 * e);
+    }
+    uint8_t* dst = parts + (part * rows + row) * D + lane * N;
+    if constexpr (N == 4)
+      *reinterpret_cast<uint32_t*>(dst) = w;
+    else
+      *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1328,6 +1313,13 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
         return PKV_ERR_CUDA;
       done[dev] = true;
     }
+  }
+  if constexpr (KV::kBytes == 1) {
+    const int64_t rows = p.num_tokens * p.n_q_heads;
+    if (cuda_failed(launch_pdl(tree_parts_kernel<D>, dim3(static_cast<unsigned>((rows + kTPartWarps - 1) / kTPartWarps)),
+                               dim3(kTPartWarps * 32), 0, stream, p.q, p.q_bf16, rows, p.parts, p.part_scale),
+                    "tree_parts_kernel launch"))
+      return PKV_ERR_CUDA;
   }
   if (cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(L::kThreads), L::bytes(p.batch), stream, p),
                   "tree_kernel launch"))
