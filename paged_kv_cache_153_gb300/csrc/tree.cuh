@@ -559,18 +559,22 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         if (!ok) break;
         tc_fence_after();
         float v[64];
-        auto load_half = [&](int h) {
-          tmem_ld64(ts + 64 * h, v);
-          if (tail) {
-            const uint32_t s0 = h ? see[2] : see[0], s1 = h ? see[3] : see[1];
+        if (tail) {
+          // masked where they lie: the loops below stay short
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = w < 2 ? (w == 0 ? see[0] : see[1]) : (w == 2 ? see[2] : see[3]);
+            float x[32];
+            tmem_ld32(ts + 32 * w, x);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = ((i < 32 ? s0 : s1) >> (i & 31)) & 1u ? v[i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1u ? x[i] : -INFINITY;
+            tmem_st32(ts + 32 * w, x);
           }
-        };
+        }
         float mx = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          load_half(h);
+          tmem_ld64(ts + 64 * h, v);
           mx = fmaxf(mx, max64(v));
         }
         const float m_tile = mx * scale_log2;
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         // the upper half is in registers; the lower one is read again
 #pragma unroll 1
         for (int h = 1; h >= 0; --h) {
-          if (h == 0) load_half(0);
+          if (h == 0) tmem_ld64(ts, v);
           // a half's P: bf16, for each 32 keys 16 columns of pairs of the first part and
           // 16 of the second; fp16, 32 columns of pairs
           uint32_t pk[kSplit ? 64 : 32];
@@ -1054,29 +1058,32 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if (!ok) break;
           const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + cr.s * L::kStage);
           const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
-          // Chunk k of 16 codes of this thread is 8192 bytes of the tile behind chunk k - 1
+          // Chunk k of 16 codes of this thread is kBytes of the tile behind chunk k - 1
           // (whole groups of 8 keys), so its two places are constants away.  The lanes of
           // a row's upper half convert and store its second 8 codes first: both halves of
           // a row lie in the same banks.
           constexpr int kAll = kTreeKeys * D / 16, kStep = L::kXform * 32;
-          static_assert(kStep / (D / 16) % 8 == 0 && kStep / (D / 16) / 8 * L::kGroup == 8192, "chunk step");
-          constexpr int kPer = kAll / kStep;
-          static_assert(kPer <= 4 && kPer * kStep == kAll, "chunks");
+          constexpr int kBytes = kStep / (D / 16) / 8 * L::kGroup;
+          constexpr int kPer = kAll / kStep < 4 ? kAll / kStep : 4;   // chunks whose instructions interleave
+          static_assert(kStep / (D / 16) % 8 == 0 && kAll % (kPer * kStep) == 0, "chunks");
           const int j0 = x_tid / (D / 16), c0 = x_tid % (D / 16);
           const bool up = D == 128 && (c0 & 4);
           const uint32_t first8 = tile + at(j0, 2 * c0 + (up ? 1 : 0)), last8 = tile + at(j0, 2 * c0 + (up ? 0 : 1));
           uint32_t nan = 0;
-          uint4 raw[kPer];
+#pragma unroll 1
+          for (int k0 = 0; k0 < kAll / kStep; k0 += kPer) {
+            uint4 raw[kPer];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + k * kStep];
+            for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + (k0 + k) * kStep];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const uint4 w = raw[k];
-            nan |= nan_codes(w.x, KV{}) | nan_codes(w.y, KV{}) | nan_codes(w.z, KV{}) | nan_codes(w.w, KV{});
-            const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
-            const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
-            store(first8 + k * 8192, make_uint4(w0.x, w0.y, w1.x, w1.y));
-            store(last8 + k * 8192, make_uint4(w2.x, w2.y, w3.x, w3.y));
+            for (int k = 0; k < kPer; ++k) {
+              const uint4 w = raw[k];
+              nan |= nan_codes(w.x, KV{}) | nan_codes(w.y, KV{}) | nan_codes(w.z, KV{}) | nan_codes(w.w, KV{});
+              const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
+              const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
+              store(first8 + (k0 + k) * kBytes, make_uint4(w0.x, w0.y, w1.x, w1.y));
+              store(last8 + (k0 + k) * kBytes, make_uint4(w2.x, w2.y, w3.x, w3.y));
+            }
           }
           const bool tail = (t + 1) * kTreeKeys > base;
           if (tail || (nan & 0x80808080u)) {
