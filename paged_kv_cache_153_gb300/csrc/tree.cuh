@@ -558,7 +558,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         ok = ok && wait(&s_full[buf], ph);
         if (!ok) break;
         tc_fence_after();
-        float v[64];
         if (tail) {
           // masked where they lie: the loops below stay short
 #pragma unroll 1
@@ -574,6 +573,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         float mx = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          float v[64];
           tmem_ld64(ts + 64 * h, v);
           mx = fmaxf(mx, max64(v));
         }
@@ -606,37 +606,38 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const uint64_t scale2 = f32x2(scale_log2, scale_log2), nref2 = f32x2(nref, nref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        // the upper half is in registers; the lower one is read again
+        // 32 keys at a time (a loop that the instruction cache holds beside the other
+        // warps'), the upper half first.  P of a half: bf16, for each 32 keys 16 columns
+        // of pairs of the first part and 16 of the second; fp16, 32 columns of pairs.
 #pragma unroll 1
-        for (int h = 1; h >= 0; --h) {
-          if (h == 0) tmem_ld64(ts, v);
-          // a half's P: bf16, for each 32 keys 16 columns of pairs of the first part and
-          // 16 of the second; fp16, 32 columns of pairs
-          uint32_t pk[kSplit ? 64 : 32];
+        for (int i = 0; i < 4; ++i) {
+          const int c = (i + 2) & 3;
+          float x[32];
+          tmem_ld32(ts + 32 * c, x);
+          uint32_t pk[kSplit ? 32 : 16];
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            const float2 x = f32x2_split(fma_f32x2(f32x2(v[i], v[i + 1]), scale2, nref2));
-            const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+          for (int j = 0; j < 32; j += 2) {
+            const float2 y = f32x2_split(fma_f32x2(f32x2(x[j], x[j + 1]), scale2, nref2));
+            const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
             uint64_t e01 = f32x2(e0, e1);
             if constexpr (kSplit) {
               const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
               const float2 lo = f32x2_split(
                   sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
-              uint32_t* w = pk + 32 * (i / 32) + (i % 32) / 2;
-              w[0] = __byte_perm(b0, b1, 0x7632);
-              w[16] = pack2(lo.x, lo.y, MT{});
+              pk[j / 2] = __byte_perm(b0, b1, 0x7632);
+              pk[16 + j / 2] = pack2(lo.x, lo.y, MT{});
             } else {
-              pk[i / 2] = pack2(e0, e1, MT{});
-              const float2 hi = unpack2(pk[i / 2], MT{});
+              pk[j / 2] = pack2(e0, e1, MT{});
+              const float2 hi = unpack2(pk[j / 2], MT{});
               e01 = f32x2(hi.x, hi.y);               // (l sums what is multiplied)
             }
-            acc[(i / 2) & 3] = add_f32x2(acc[(i / 2) & 3], e01);
+            acc[(j / 2) & 3] = add_f32x2(acc[(j / 2) & 3], e01);
           }
           if constexpr (kSplit)
-            tmem_st64u(ts + 64 * h, pk);
+            tmem_st32u(ts + 32 * c, pk);
           else
-            tmem_st32u(ts + 64 * h, pk);
-          if (h == 1) {
+            tmem_st16u(ts + 64 * (c >> 1) + 16 * (c & 1), pk);
+          if (i == 1) {
             // (their product may run while the lower keys' weights are computed)
             tmem_wait_st();
             tc_fence_before();
