@@ -104,7 +104,7 @@ struct TreeSmem {
   static constexpr int kXform = FP8 ? 8 : 4;
   static constexpr int kThreads = 384 + 32 * kXform;
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;           // a thread, at launch
-  static constexpr int kRegsSoftmax = FP8 ? 152 : 184, kRegsOther = FP8 ? 56 : 72;
+  static constexpr int kRegsSoftmax = FP8 ? 144 : 152, kRegsOther = FP8 ? 64 : 104;
   static_assert(kTSoftmax * kRegsSoftmax + (kThreads - kTSoftmax) * kRegsOther <= kThreads * kRegs, "registers");
   static constexpr int kTile = kTreeKeys * D * 2;                  // a Q, K or V tile
   static constexpr int kStage = kTile / 2;                         // FP8: a staged tile of codes
