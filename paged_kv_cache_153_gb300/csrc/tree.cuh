@@ -270,27 +270,32 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return w & keep;
 }
 
-__device__ __forceinline__ uint32_t mad_u32(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+// four codes of a word -> halves
+__device__ __forceinline__ uint2 codes4(uint32_t w, E5M2) {
+  return make_uint2(__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424));
+}
+__device__ __forceinline__ uint2 codes4(uint32_t w, E4M3) {
+  uint2 d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(d.x), "=r"(d.y)
+      : "r"(w));
   return d;
 }
-// codes 0, 2 and 1, 3 of a word -> two pairs of halves (E4M3: times 2^-8).  Per code
-// c: 128 (c + (c & 0x80)) for E4M3, 256 c for E5M2.
-__device__ __forceinline__ uint2 codes4(uint32_t w, E5M2) { return make_uint2((w << 8) & 0xff00ff00u, w & 0xff00ff00u); }
-__device__ __forceinline__ uint2 codes4(uint32_t w, E4M3) {
-  const uint32_t o = w >> 8;
-  return make_uint2(mad_u32(w & 0x00800080u, 128u, mad_u32(w & 0x00ff00ffu, 128u, 0u)),
-                    mad_u32(o & 0x00800080u, 128u, mad_u32(o & 0x00ff00ffu, 128u, 0u)));
+
+// sums of an fp32 number and a 16-bit one, in one instruction each
+__device__ __forceinline__ void add_halves(uint32_t w, float& a, float& b) {   // a, b += the halves of w
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %1, hi, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
 }
-// a byte's top bit where an E4M3 code is a NaN (which codes4 makes a number)
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w, E4M3) { return mad_u32(w & 0x7f7f7f7fu, 1u, 0x01010101u); }
-__device__ __forceinline__ uint32_t nan_codes(uint32_t, E5M2) { return 0u; }
-// the bits that make the halves of codes 0, 2 (1, 3 of w >> 8) of a word NaN
-__device__ __forceinline__ uint32_t nan_halves(uint32_t w, E4M3) {
-  return ((w & 0x7fu) == 0x7fu ? 0x7fffu : 0u) | ((w & 0x7f0000u) == 0x7f0000u ? 0x7fff0000u : 0u);
+__device__ __forceinline__ float2 less_bf16(float a, float b, uint32_t w) {    // a, b - the bf16 numbers of w
+  float2 d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, lo, %5, %3;\n\tfma.rn.f32.bf16 %1, hi, %5, %4;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(w), "f"(a), "f"(b), "h"(static_cast<uint16_t>(0xbf80)));           // (times -1)
+  return d;
 }
-__device__ __forceinline__ uint32_t nan_halves(uint32_t, E5M2) { return 0u; }
 
 // descriptor of an FP8 operand: rows of D bytes, K-major, D-byte swizzle
 template <int D>
@@ -346,7 +351,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   static_assert(!CHUNK || !kFp8, "prompt chunks: 16-bit caches");
   constexpr int kBadWords = CHUNK ? 16 : 8;        // of remembered tokens
   static_assert(!CHUNK || L::kXform * 16 <= kTBadSlots * L::kXform * 8, "remembered tokens");
-  constexpr float kFold = std::is_same<KV, E4M3>::value ? 256.f : 1.f;   // of converted codes
   extern __shared__ unsigned char tsm_raw[];
   unsigned char* sm = tsm_raw + ((1024 - (smem_u32(tsm_raw) & 1023)) & 1023);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);   // [kKStages] K tile landed
@@ -530,8 +534,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       for (int n = two ? 0 : grp; n < nt; n += two ? 1 : 2) {
         const uint32_t k = ops + (two ? 2 * n + grp : n), buf = k % NB, ph = (k / NB) & 1;
         if (!live) {
-          if (!two && n > 0) ok = take_turn();
-          ok = ok && wait(&s_full[buf], ph);
+          ok = wait(&s_full[buf], ph) && (two || n == 0 || take_turn());
           if (!ok) break;
           if (!two && lane == 0) mbar_arrive(my_turn);
           mbar_arrive(&p_half[buf]);
@@ -553,9 +556,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           }
         }
         const uint32_t ts = tmem + lane_base + buf * kTreeKeys;
-        // (its turn first: then the buffer's previous scores are known to be over)
-        if (!two && n > 0) ok = take_turn();
-        ok = ok && wait(&s_full[buf], ph);
+        // (the scores of two operations before, its own or before its last turn, are
+        // known to be over, and so is the buffer's phase before, at least as old)
+        ok = wait(&s_full[buf], ph);
         if (!ok) break;
         tc_fence_after();
         if (tail) {
@@ -577,6 +580,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           tmem_ld64(ts + 64 * h, v);
           mx = fmaxf(mx, max64(v));
         }
+        // (the turn only now: between the groups only the references are in line)
+        if (!two && n > 0) ok = take_turn();
+        if (!ok) break;
         const float m_tile = mx * scale_log2;
         float alpha = 1.f;
         if (m_tile > m_ref + kTRescaleLog2) {
@@ -605,7 +611,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         }
         const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const uint64_t scale2 = f32x2(scale_log2, scale_log2), nref2 = f32x2(nref, nref);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};            // l's summands of this tile: bf16
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // fp16
         // 32 keys at a time (a loop that the instruction cache holds beside the other
         // warps'), the upper half first.  P of a half: bf16, for each 32 keys 16 columns
         // of pairs of the first part and 16 of the second; fp16, 32 columns of pairs.
@@ -619,19 +626,15 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           for (int j = 0; j < 32; j += 2) {
             const float2 y = f32x2_split(fma_f32x2(f32x2(x[j], x[j + 1]), scale2, nref2));
             const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
-            uint64_t e01 = f32x2(e0, e1);
             if constexpr (kSplit) {
-              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
-              const float2 lo = f32x2_split(
-                  sub_f32x2(e01, f32x2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))));
-              pk[j / 2] = __byte_perm(b0, b1, 0x7632);
+              pk[j / 2] = __byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632);
+              const float2 lo = less_bf16(e0, e1, pk[j / 2]);
               pk[16 + j / 2] = pack2(lo.x, lo.y, MT{});
+              acc[(j / 2) & 3] = add_f32x2(acc[(j / 2) & 3], f32x2(e0, e1));
             } else {
               pk[j / 2] = pack2(e0, e1, MT{});
-              const float2 hi = unpack2(pk[j / 2], MT{});
-              e01 = f32x2(hi.x, hi.y);               // (l sums what is multiplied)
+              add_halves(pk[j / 2], sum[j & 7], sum[(j & 7) + 1]);   // (l sums what is multiplied)
             }
-            acc[(j / 2) & 3] = add_f32x2(acc[(j / 2) & 3], e01);
           }
           if constexpr (kSplit)
             tmem_st32u(ts + 32 * c, pk);
@@ -645,8 +648,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           }
         }
         const float2 s0 = f32x2_split(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        const float s1 = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
         tmem_wait_st();
-        l_run = l_run * alpha + (s0.x + s0.y);
+        l_run = l_run * alpha + (kSplit ? s0.x + s0.y : s1);
         tc_fence_before();
         mbar_arrive(&p_full[buf]);
       }
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       for (int w = lane; w < L::kXform * kBadWords; w += 32) any |= noted[w];
       const bool any_bad = __any_sync(0xffffffffu, any != 0u);
       const bool direct = sg.t0 == 0 && sg.t1 == sg.kt;
-      const float v_scale = kFp8 ? p.v_scale[sg.g] * kFold : 1.f;
+      const float v_scale = kFp8 ? p.v_scale[sg.g] : 1.f;
       const int n_rows = sg.rows - row0, head = (sg.g << shift) + (unit_row & ((1 << shift) - 1));
       const float weight = direct ? (l > 0.f ? v_scale / l : 0.f) : v_scale;
       // (of one row tile, each group writes half of the columns)
@@ -691,14 +695,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         tmem_ld32(to + x, o);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] *= weight;
-        if constexpr (kFp8) {
-          // (converted words hold codes 0 2 1 3)
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float x1 = o[i + 1];
-            o[i + 1] = o[i + 2], o[i + 2] = x1;
-          }
-        }
         if (any_bad) {
           // (rare) every row adds what it sees of them
           for (int w = 0; w < (CHUNK ? kBadWords : 2 * p.mask_words); ++w) {
@@ -1070,7 +1066,6 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           const int j0 = x_tid / (D / 16), c0 = x_tid % (D / 16);
           const bool up = D == 128 && (c0 & 4);
           const uint32_t first8 = tile + at(j0, 2 * c0 + (up ? 1 : 0)), last8 = tile + at(j0, 2 * c0 + (up ? 0 : 1));
-          uint32_t nan = 0;
 #pragma unroll 1
           for (int k0 = 0; k0 < kAll / kStep; k0 += kPer) {
             uint4 raw[kPer];
@@ -1079,28 +1074,21 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
               const uint4 w = raw[k];
-              nan |= nan_codes(w.x, KV{}) | nan_codes(w.y, KV{}) | nan_codes(w.z, KV{}) | nan_codes(w.w, KV{});
               const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
               const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
               store(first8 + (k0 + k) * kBytes, make_uint4(w0.x, w0.y, w1.x, w1.y));
               store(last8 + (k0 + k) * kBytes, make_uint4(w2.x, w2.y, w3.x, w3.y));
             }
           }
-          const bool tail = (t + 1) * kTreeKeys > base;
-          if (tail || (nan & 0x80808080u)) {
-            // (rare) E4M3's NaN codes became numbers; V rows from the first drafted
-            // token on.  Each thread looks at what it wrote.
+          if ((t + 1) * kTreeKeys > base) {
+            // V rows from the first drafted token on: each thread looks at what it wrote
 #pragma unroll 1
             for (int x = x_tid; x < kAll; x += L::kXform * 32) {
               const int j = x / (D / 16), c = x % (D / 16);
 #pragma unroll 1
               for (int e = 0; e < 2; ++e) {
                 const uint32_t addr = tile + at(j, 2 * c + e);
-                uint4 v = load(addr);
-                const uint2 w = reinterpret_cast<const uint2*>(codes + x)[e];
-                v.x |= nan_halves(w.x, KV{}), v.y |= nan_halves(w.x >> 8, KV{});
-                v.z |= nan_halves(w.y, KV{}), v.w |= nan_halves(w.y >> 8, KV{});
-                store(addr, tail ? clean(v, t * kTreeKeys + j) : v);
+                store(addr, clean(load(addr), t * kTreeKeys + j));
               }
             }
           }
