@@ -92,9 +92,11 @@ constexpr int kTTileBlocks = kTreeKeys / kBlockSize;
 constexpr float kTRescaleLog2 = 8.f;
 constexpr int kTBadSlots = 4;                     // pieces whose remembered tokens live at once
 
-// cost of a unit's set-up (Q, the first tile's latency, its outputs) and of a key
-// tile against one row tile or two, in half tiles
-constexpr int kTUnitCost = 6;
+// Cost of a unit's set-up (Q, the first tile's latency, its outputs) and of a key
+// tile against one row tile or two, in half tiles.  An FP8 tile is half the bytes, so
+// the set-up is more of them.  Measured with 6, 12, 16: mixed contexts up to 16384
+// over a 16-bit cache 132, 136, 138 us, up to 32768 over an FP8 one 99.6, 96.6, 96.3.
+constexpr int tree_setup_cost(bool fp8) { return fp8 ? 14 : 6; }
 __host__ __device__ constexpr int tree_tile_cost(int rows) { return rows > kTreeRows ? 3 : 2; }
 
 template <int D, bool FP8, int NQ>
@@ -155,14 +157,14 @@ struct TreeSeg {
 template <int NQ>
 __device__ __forceinline__ int tree_units(int rows) { return (rows + kTreeRows * NQ - 1) / (kTreeRows * NQ); }
 __device__ __forceinline__ int tree_tiles(int ctx) { return ctx / kTreeKeys + (ctx % kTreeKeys != 0); }
-__device__ __forceinline__ int64_t tree_unit_cost(int rows, int kt) {
-  return kTUnitCost + static_cast<int64_t>(kt) * tree_tile_cost(rows);
+__device__ __forceinline__ int64_t tree_unit_cost(int rows, int kt, int setup) {
+  return setup + static_cast<int64_t>(kt) * tree_tile_cost(rows);
 }
 // first tile at or behind position x of its unit's cost
-__device__ __forceinline__ int tree_tile_at(int64_t x, int rows, int kt) {
-  if (x <= kTUnitCost) return 0;
+__device__ __forceinline__ int tree_tile_at(int64_t x, int rows, int kt, int setup) {
+  if (x <= setup) return 0;
   const int w = tree_tile_cost(rows);
-  return static_cast<int>(min(static_cast<int64_t>(kt), div_nonneg(x - kTUnitCost + w - 1, w)));
+  return static_cast<int>(min(static_cast<int64_t>(kt), div_nonneg(x - setup + w - 1, w)));
 }
 // States of unit u's rows in range r lie at rows [tree_piece_row(...), + unit
 // rows) of ml and o.  Successive pieces differ in the unit or in the range, so
@@ -174,7 +176,7 @@ __device__ __forceinline__ int64_t tree_piece_row(int64_t start, int n_q_heads, 
 
 template <int NQ>
 __device__ __forceinline__ TreeSeg tree_segment(const TreeSeq* seqs, int batch, int shift, int n_q_heads, int64_t pos,
-                                                int64_t end, int64_t range) {
+                                                int64_t end, int64_t range, int setup) {
   int lo = 0, hi = batch - 1;    // the last sequence that starts at or before pos (a non-empty one)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -182,15 +184,15 @@ __device__ __forceinline__ TreeSeg tree_segment(const TreeSeq* seqs, int batch, 
   }
   const TreeSeq sq = seqs[lo];
   const int rows = sq.n << shift, units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx);
-  const int64_t cost = tree_unit_cost(rows, kt), rem = pos - sq.cost;
+  const int64_t cost = tree_unit_cost(rows, kt, setup), rem = pos - sq.cost;
   const int64_t u = div_nonneg(rem, cost), off = rem - u * cost;
   TreeSeg s;
   s.b = lo;
   s.g = static_cast<int>(u) / units;
   s.unit = static_cast<int>(u) - s.g * units;
   s.kt = kt;
-  s.t0 = tree_tile_at(off, rows, kt);
-  s.t1 = tree_tile_at(off + (end - pos), rows, kt);
+  s.t0 = tree_tile_at(off, rows, kt, setup);
+  s.t1 = tree_tile_at(off + (end - pos), rows, kt, setup);
   s.next = pos + min(cost - off, end - pos);
   s.rows = min(kTreeRows * NQ, rows - s.unit * kTreeRows * NQ);
   s.row = tree_piece_row(sq.start, n_q_heads, s.g, rows, static_cast<int64_t>(s.unit) * kTreeRows * NQ, range,
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       TreeSeq sq = sequence(b);
       if (sq.n > 0) {
         const int rows = sq.n << shift;
-        sq.cost = p.n_kv_heads * tree_units<NQ>(rows) * tree_unit_cost(rows, tree_tiles(sq.ctx));
+        sq.cost = p.n_kv_heads * tree_units<NQ>(rows) * tree_unit_cost(rows, tree_tiles(sq.ctx), p.setup_cost);
       }
       seqs[b] = sq;
     }
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       return chunk_segment(seqs[0], blockIdx.z, blockIdx.y, gridDim.x - 1 - blockIdx.x, kTreeRows * NQ, shift, p.window,
                            p.num_sinks);
     else
-      return tree_segment<NQ>(seqs, p.batch, shift, p.n_q_heads, pos, end, range);
+      return tree_segment<NQ>(seqs, p.batch, shift, p.n_q_heads, pos, end, range, p.setup_cost);
   };
   auto sequence_of = [&](const TreeSeg& sg) { return seqs[CHUNK ? 0 : sg.b]; };
   // key tile at place x of a piece's order
@@ -1189,7 +1191,7 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
   const int rows = sq.n << shift, row0 = (blockIdx.x * kTMergeWarps + warp) * NR;
   if (row0 >= rows) return;
   const int units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx), unit = row0 / kUnit;   // (NR divides kUnit)
-  const int64_t cost = tree_unit_cost(rows, kt), u0 = sq.cost + (static_cast<int64_t>(g) * units + unit) * cost;
+  const int64_t cost = tree_unit_cost(rows, kt, p.setup_cost), u0 = sq.cost + (static_cast<int64_t>(g) * units + unit) * cost;
   // ranges whose part of the axis meets the unit: r0 .. r1
   const int64_t r0 = div_nonneg((u0 + 1) * R + V - 1, V) - 1;
   const int64_t r1 = div_nonneg((u0 + cost) * R + V - 1, V) - 1;
@@ -1206,8 +1208,8 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
     const int64_t r = x0 + lane;
     int t0 = 0, t1 = 0;
     if (r <= r1) {
-      t0 = tree_tile_at(max(div_nonneg(r * V, R) - u0, static_cast<int64_t>(0)), rows, kt);
-      t1 = tree_tile_at(max(min(div_nonneg((r + 1) * V, R) - u0, cost), static_cast<int64_t>(0)), rows, kt);
+      t0 = tree_tile_at(max(div_nonneg(r * V, R) - u0, static_cast<int64_t>(0)), rows, kt, p.setup_cost);
+      t1 = tree_tile_at(max(min(div_nonneg((r + 1) * V, R) - u0, cost), static_cast<int64_t>(0)), rows, kt, p.setup_cost);
     }
     if (__any_sync(0xffffffffu, t0 == 0 && t1 == kt)) return;        // written where it was computed
     const bool have = t0 < t1;
@@ -1310,6 +1312,7 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
       done[dev] = true;
     }
   }
+  p.setup_cost = tree_setup_cost(KV::kBytes == 1);
   if constexpr (KV::kBytes == 1) {
     const int64_t rows = p.num_tokens * p.n_q_heads;
     if (cuda_failed(launch_pdl(tree_parts_kernel<D>, dim3(static_cast<unsigned>((rows + kTPartWarps - 1) / kTPartWarps)),

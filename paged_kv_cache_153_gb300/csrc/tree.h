@@ -45,6 +45,7 @@ struct TreeParams {
   unsigned long long wait_limit_ns;
   int64_t num_blocks, num_tokens;
   int batch, n_q_heads, n_kv_heads, group_shift, max_blocks_per_seq;
+  int setup_cost;                // of a unit, in half tiles
   int mask_words, max_nodes;     // (chunks: max_nodes is the longest query)
   int window, num_sinks;         // chunks
   int q_box;                     // tokens of a Q box
