@@ -198,7 +198,11 @@ extern "C" pkv_status pkv_paged_prefill_attention_window(
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
   const int64_t longest = std::min<int64_t>(max_query_len, num_tokens);
-  const int q_tiles = longest * group > kTreeRows ? 2 : 1;
+  // Units of 256 rows read K and V half as often (four prompts of 2048 tokens 459 us, 476
+  // with units of 128); while units of 128 leave SMs idle, they are done sooner (300
+  // tokens of 8 heads 13.2 us, 11.8 with 128).
+  const int64_t units128 = (num_tokens * group + kTreeRows - 1) / kTreeRows * num_kv_heads;
+  const int q_tiles = longest * group > kTreeRows && units128 > sm_count() ? 2 : 1;
   TreeParams p{};
   p.group_shift = group == 8 ? 3 : group == 4 ? 2 : group - 1;
   p.q_box = static_cast<int>(std::min<int64_t>(kTreeRows / group, longest));
