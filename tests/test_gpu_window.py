@@ -169,6 +169,22 @@ def test_chunks(pkv, dtype, hq, hkv, d):
         assert bool((out[-3:] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 32, 8, 128), ("f16", 32, 4, 128), ("f16", 32, 16, 64)])
+def test_many_rows_share_the_keys_in_pairs_of_tiles(pkv, dtype, hq, hkv, d):
+    base, new = [0, 130, 77, 1000], [700, 33, 1, 800]
+    for window, sinks in ((100, 4), (1, 0), (600, 200), (5000, 0)):
+        c = chunk_case(base, new, hq=hq, hkv=hkv, d=d, dtype=dtype, seed=window, extra=3)
+        tab = c.tab.copy()
+        for b in range(len(base)):
+            drop(c, window, sinks, b, base[b])
+        out = prefill(pkv, c, window, sinks)
+        assert int(c.err.item()) == 0, (window, sinks)
+        for b in range(len(base)):
+            rows = [i for i in range(new[b]) if i % 97 == 0 or i in (31, 32, 63, 64, 127, 128, new[b] - 1)]
+            check_rows(c, out, b, [base[b] + i for i in rows], [int(c.cu[b]) + i for i in rows], window, sinks, tab)
+        assert bool((out[-3:] == 7.0).all())
+
+
 @pytest.mark.parametrize("dtype,bad", [("bf16", float("nan")), ("f16", float("inf"))])
 def test_chunk_rows_that_are_not_seen_change_nothing(pkv, dtype, bad):
     # not finite: a key that leaves the window within the chunk, and one of the chunk's own
@@ -240,3 +256,24 @@ def test_chunks_captured_and_replayed(pkv):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(c.out, want)
+
+
+def test_not_finite_rows_in_pairs_of_tiles(pkv):
+    # as above with row tiles in pairs: the same rows behind many others
+    base, n, window, sinks = 200, 90, 64, 2
+    c = chunk_case([0, base], [1400, n], hq=32, hkv=8, d=128, dtype="bf16", seed=2)
+    for p in (170, 240):
+        c.vc_h[int(c.tab[1, p // 16]), :, p % 16, 5] = float("inf")
+    out = prefill(pkv, c, window, sinks)
+    assert int(c.err.item()) == 0
+    assert bool(torch.isfinite(out[:1400].float()).all())
+    got = out[1400:].double().cpu().numpy()
+    seen = od.window_seen(range(base, base + n), base + n, window, sinks)
+    assert (np.isfinite(got[:, :, 5]) == ~(seen[:, 170] | seen[:, 240])[:, None]).all()
+    for h in (0, 5, 31):
+        k, v = c.rows(1, h // 4)
+        for i in range(0, n, 3):
+            at = np.flatnonzero(seen[i])
+            ref, lim = attn_limits.attend(c.q_h[1400 + i, h].double().numpy(), k[at], v[at], c.scale, "bf16")
+            cols = np.arange(128) != 5
+            assert (np.abs(got[i, h] - ref)[cols] <= lim[cols]).all(), (i, h)
