@@ -56,12 +56,9 @@
 // 11, exact to 2^-17 of the row's largest element (half a step of E4M3's denormals);
 // 2^-k joins the row's softmax scale.  A launch of its own writes the parts to the
 // workspace (in the kernel, per piece, four warps took 6 to 13 us).  V's codes are
-// converted to fp16 tiles by eight warps: an E5M2 code is the upper byte of its half; an E4M3 code's bits, moved to
-// their places in a half, are its value times 2^-8 (denormals too), which the scale
-// takes back.  (With K converted as well, the integer pipe and shared memory took
-// 3900 clocks a tile; the conversion instruction alone 1500 a K tile.)  The moves are
-// masks and multiplications that leave a word's codes 0 2 1 3, so the columns 1 and 2
-// of every four change places in the output.
+// converted to fp16 tiles, exactly, by eight warps (one instruction for two E4M3
+// codes, one byte permutation for two E5M2 ones; with four warps 106 us instead of
+// 100).  With K converted as well, shared memory took 3900 clocks a tile.
 //
 // Prompt chunks (CHUNK).  The same kernel attends the new tokens of a prompt to the
 // first tokens and a window: a thread block per unit, whose key tiles are those
@@ -70,9 +67,19 @@
 //
 // Warps 0-7: softmax; 8 and 11: producers; 9: TMEM owner and Q K^T issuer; 10:
 // P V issuer; from 12 on: rows of V with drafted tokens (four warps), or the
-// conversions of V (eight).  The softmax warps take registers
-// from the others, so that a row half's scores and its P stay in them.  Waits are
-// bounded as in the other kernels.
+// conversions of V (eight).  The softmax warps take registers from the others.
+// (Sixteen of them, two threads a row, were slower: 149 us instead of 136 for one
+// document of 131072, 557 instead of 479 for the prompts below.)  Waits are bounded
+// as in the other kernels.
+//
+// Measured (back to back, everything with its launches): 32 sequences of 1024 to
+// 16384 tokens with 20 to 32 drafted ones, 32 and 8 heads of 128, bf16: 133 us, of
+// which 11 are the merge; the reads alone take 112 at 6.80 TB/s.  One of 131072 with
+// 64, fp16: 125 us (79); each row tile's softmax, P V and next Q K^T wait for each
+// other (4500 clocks, 2048 of them products).  16 of 4096 to 32768 with 10 to 31,
+// E4M3: 96 us (57): shared memory feeds the products, the conversions and the loads
+// in turn.  Four prompts of 2048 tokens, window 4096: 459 us; the products with
+// bf16's second part take 318.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -110,7 +117,6 @@ struct TreeSmem {
   static_assert(kTSoftmax * kRegsSoftmax + (kThreads - kTSoftmax) * kRegsOther <= kThreads * kRegs, "registers");
   static constexpr int kTile = kTreeKeys * D * 2;                  // a Q, K or V tile
   static constexpr int kStage = kTile / 2;                         // FP8: a staged tile of codes
-  static constexpr int kQBufs = 1;
   static constexpr int kKStages = FP8 ? 4 - NQ : 2;
   static constexpr int kVStages = FP8 ? 3 - NQ : 4 - NQ;
   static constexpr int kCodeStages = FP8 ? 2 : 0;                  // of V
@@ -366,9 +372,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   uint64_t* p_half = s_full + NB;                  // [NB] P of the upper keys written, O rescaled
   uint64_t* p_full = p_half + NB;                  // [NB] and of the lower ones
   uint64_t* pv_done = p_full + NB;                 // [NB] P V done
-  uint64_t* q_full = pv_done + NB;                 // [kQBufs] Q of a piece landed
-  uint64_t* q_empty = q_full + L::kQBufs;          // [kQBufs] its Q K^T done
-  uint64_t* turn = q_empty + L::kQBufs;                  // [2][4] a group's warp has passed its rows' references on
+  uint64_t* q_full = pv_done + NB;                 // Q of a piece landed
+  uint64_t* q_empty = q_full + 1;                  // its Q K^T done
+  uint64_t* turn = q_empty + 1;                    // [2][4] a group's warp has passed its rows' references on
   uint64_t* joined = turn + 8;                     // [2][4] and its sums of a piece
   uint64_t* o_read = joined + 8;                   // 8 arrivals: a piece's outputs are out of TMEM
   uint64_t* mma_idle = o_read + 1;                 // [2] an issuer's MMAs done
@@ -408,10 +414,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       mbar_init(&p_full[s], kTSoftmax / 2);
       mbar_init(&pv_done[s], 1);
     }
-    for (int s = 0; s < L::kQBufs; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
-    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < 8; ++s) {
       mbar_init(&turn[s], 1);
       mbar_init(&joined[s], 1);
@@ -806,13 +810,12 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       };
       int id = fetch_id(sg.t1 - 1);
       if (!is_v) {
-        // Q of the piece, once every Q K^T of the buffer's piece before has read it
-        const uint32_t qb = pieces % L::kQBufs, q_use = pieces / L::kQBufs;
-        if (q_use > 0) good = __all_sync(0xffffffffu, tree_wait(&q_empty[qb], (q_use - 1) & 1, p, abort_flag));
+        // Q of the piece, once every Q K^T of the piece before has read it
+        if (pieces > 0) good = __all_sync(0xffffffffu, tree_wait(q_empty, (pieces - 1) & 1, p, abort_flag));
         if (!good) break;
         const int parts = kFp8 ? (p.q_bf16 ? 2 : 3) : 1;
         if (lane == 0)
-          mbar_arrive_expect_tx(&q_full[qb], nq * parts * (p.q_box << shift) * (kFp8 ? D : 2 * D));
+          mbar_arrive_expect_tx(q_full, nq * parts * (p.q_box << shift) * (kFp8 ? D : 2 * D));
         ++pieces;
         __syncwarp();
         if (kFp8 && lane < nq * parts) {
@@ -820,12 +823,12 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           tma_load_3d(sm + L::kQ + c * L::kQTile + part * L::kStage, &p.tmap_q, 0, sg.g << shift,
                       static_cast<int>(part * p.num_tokens) + sq.start +
                           ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift),
-                      &q_full[qb], policy_evict_last());
+                      q_full, policy_evict_last());
         }
         if (!kFp8 && lane < nq * (D / 64)) {
           const int c = lane / (D / 64), h = lane % (D / 64);
-          tma_load_3d(sm + L::kQ + (qb * NQ + c) * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
-                      sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), &q_full[qb],
+          tma_load_3d(sm + L::kQ + c * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
+                      sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), q_full,
                       policy_evict_last());
         }
         __syncwarp();
@@ -881,8 +884,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       // The last loads of every stage land before the block ends (bounded, with the
       // full limit): whoever should wait for them may have stopped.
       const unsigned long long deadline = global_ns() + kWaitLimitNs;
-      for (uint32_t n = pieces > L::kQBufs ? pieces - L::kQBufs : 0; n < pieces; ++n)
-        mbar_wait_until(&q_full[n % L::kQBufs], (n / L::kQBufs) & 1, deadline);
+      if (pieces > 0) mbar_wait_until(q_full, (pieces - 1) & 1, deadline);
       for (uint32_t n = tiles > stages ? tiles - stages : 0; n < tiles; ++n)
         mbar_wait_until(&full[n % stages], (n / stages) & 1, deadline);
     }
@@ -908,10 +910,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         pos = sg.next;
         if (sg.t0 >= sg.t1) continue;
         const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-        const uint32_t qb = pieces % L::kQBufs;
         if (qk_warp) {
           // (the producer loads nothing while the previous kernel runs)
-          ok = mbar_wait_started_early(&q_full[qb], (pieces / L::kQBufs) & 1, p.err, p.wait_limit_ns);
+          ok = mbar_wait_started_early(q_full, pieces & 1, p.err, p.wait_limit_ns);
         }
         // (the piece's first P V overwrites the outputs of the piece before)
         if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
@@ -944,7 +945,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
                             b0 + static_cast<uint64_t>((ks * 32) >> 4), kIdCodes, ks > 0 || part < parts - 1);
                 }
               } else {
-                const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + (qb * NQ + c) * L::kTile), 16, 1024);
+                const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + c * L::kTile), 16, 1024);
                 const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
@@ -981,7 +982,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           }
           if (!ok) break;
           umma_commit(qk_warp ? &k_empty[kr.s] : &v_empty[vr.s]);
-          if (qk_warp && t == sg.t0) umma_commit(&q_empty[qb]);
+          if (qk_warp && t == sg.t0) umma_commit(q_empty);
           kr.next();
           vr.next();
         }
@@ -1195,8 +1196,8 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
 // with the first pieces' outputs loaded beside their weights.  Units that one range
 // held are done.  It is all latency, so a warp takes one row and eight pieces at a
 // time where the rows' warps fit the GPU at once, and else four rows and two pieces.
-// (32 sequences of 1024 to 16384 tokens: 11.4 us; one row a warp 18.5 us.  One
-// of 131072, 19 pieces a row: 8.1 us; four rows one after another 24 us.)
+// (Cold, 32 sequences of 1024 to 16384 tokens: 11.6 us; one row a warp 18.5 us.  One
+// of 131072, 19 pieces a row: 7.9 us; four rows one after another 24 us.)
 // ---------------------------------------------------------------------------
 constexpr int kTMergeWarps = 8;
 
