@@ -166,6 +166,21 @@ __device__ __forceinline__ int tree_tiles(int ctx) { return ctx / kTreeKeys + (c
 __device__ __forceinline__ int64_t tree_unit_cost(int rows, int kt, int setup) {
   return setup + static_cast<int64_t>(kt) * tree_tile_cost(rows);
 }
+// sequence b with its own cost; one that is not to be attended has no tokens and cost 0
+template <int NQ>
+__device__ __forceinline__ TreeSeq tree_sequence(const TreeParams& p, int b, int32_t* err) {
+  const int64_t t0 = p.cu_nodes[b], t1 = p.cu_nodes[b + 1], n = t1 - t0;
+  const int ctx = p.context_lens[b];
+  if (t0 < 0 || n < 0 || t1 > p.num_tokens || n > p.max_nodes || ctx < n ||
+      ctx > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize) {
+    record_error(err, PKV_ERR_OOB);
+    return TreeSeq{0, 0, 0, 0, 0};
+  }
+  if (n == 0) return TreeSeq{0, 0, 0, 0, 0};
+  const int rows = static_cast<int>(n) << p.group_shift;
+  return TreeSeq{p.n_kv_heads * tree_units<NQ>(rows) * tree_unit_cost(rows, tree_tiles(ctx), p.setup_cost),
+                 static_cast<int>(t0), static_cast<int>(n), ctx, 0};
+}
 // first tile at or behind position x of its unit's cost
 __device__ __forceinline__ int tree_tile_at(int64_t x, int rows, int kt, int setup) {
   if (x <= setup) return 0;
@@ -429,27 +444,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   // tables only, which no kernel that releases early writes.
 
   // ---- the sequences: drafted (or new) tokens, context, cost ----
-  auto sequence = [&](int b) -> TreeSeq {
-    const int64_t t0 = p.cu_nodes[b], t1 = p.cu_nodes[b + 1], n = t1 - t0;
-    const int ctx = p.context_lens[b];
-    if (t0 < 0 || n < 0 || t1 > p.num_tokens || n > p.max_nodes || ctx < n ||
-        ctx > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize) {
-      record_error(p.err, PKV_ERR_OOB);
-      return TreeSeq{0, 0, 0, 0, 0};
-    }
-    return n > 0 ? TreeSeq{0, static_cast<int>(t0), static_cast<int>(n), ctx, 0} : TreeSeq{0, 0, 0, 0, 0};
-  };
   if constexpr (CHUNK) {
-    if (tid == 0) seqs[0] = sequence(blockIdx.z);
+    if (tid == 0) seqs[0] = tree_sequence<NQ>(p, blockIdx.z, p.err);
   } else {
-    for (int b = tid; b < p.batch; b += L::kThreads) {
-      TreeSeq sq = sequence(b);
-      if (sq.n > 0) {
-        const int rows = sq.n << shift;
-        sq.cost = p.n_kv_heads * tree_units<NQ>(rows) * tree_unit_cost(rows, tree_tiles(sq.ctx), p.setup_cost);
-      }
-      seqs[b] = sq;
-    }
+    for (int b = tid; b < p.batch; b += L::kThreads) seqs[b] = tree_sequence<NQ>(p, b, p.err);
     __syncthreads();
     if (warp == 0) {   // exclusive prefix of the costs
       int64_t carry = 0;
@@ -1198,25 +1196,69 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
 // time where the rows' warps fit the GPU at once, and else four rows and two pieces.
 // (Cold, 32 sequences of 1024 to 16384 tokens: 11.6 us; one row a warp 18.5 us.  One
 // of 131072, 19 pieces a row: 7.9 us; four rows one after another 24 us.)
+// With one row a warp, and all thread blocks on the GPU at once, the geometry is
+// worked out from the inputs while the kernel before still runs (one document of
+// 131072: 123 us instead of 125; four chats 9.0 instead of 9.9).
 // ---------------------------------------------------------------------------
 constexpr int kTMergeWarps = 8;
 
 template <int D, int NQ, int NR>
 __global__ void __launch_bounds__(kTMergeWarps * 32)
-    tree_merge_kernel(const __grid_constant__ TreeParams p, int ranges) {
+    tree_merge_kernel(const __grid_constant__ TreeParams p, int ranges, int ahead) {
   constexpr int N = D / 32, kBatch = 8 / NR, kUnit = kTreeRows * NQ;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z, g = blockIdx.y, shift = p.group_shift;
-  pdl_wait_and_release();
-  const TreeSeq sq = p.seqs[b];
-  const int64_t V = p.seqs[p.batch].cost, R = ranges;
+  const bool early = NR == 1 && ahead;
+  TreeSeq sq;
+  int64_t V;
+  if (early) {
+    // (lengths and offsets only, as the kernel before)
+    __shared__ int64_t sums[2][kTMergeWarps];
+    int64_t before = 0, all = 0;
+    for (int x = threadIdx.x; x < p.batch; x += kTMergeWarps * 32) {
+      const int64_t c = tree_sequence<NQ>(p, x, nullptr).cost;
+      all += c;
+      before += x < b ? c : 0;
+    }
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, k);
+      before += __shfl_xor_sync(0xffffffffu, before, k);
+    }
+    if (lane == 0) sums[0][warp] = before, sums[1][warp] = all;
+    __syncthreads();
+    sq = tree_sequence<NQ>(p, b, nullptr);
+    sq.cost = V = 0;
+#pragma unroll
+    for (int k = 0; k < kTMergeWarps; ++k) sq.cost += sums[0][k], V += sums[1][k];
+  } else {
+    pdl_wait_and_release();
+    sq = p.seqs[b];
+    V = p.seqs[p.batch].cost;
+  }
+  const int64_t R = ranges;
   const int rows = sq.n << shift, row0 = (blockIdx.x * kTMergeWarps + warp) * NR;
-  if (row0 >= rows) return;
+  if (row0 >= rows) {
+    if (early) pdl_wait_and_release();
+    return;
+  }
   const int units = tree_units<NQ>(rows), kt = tree_tiles(sq.ctx), unit = row0 / kUnit;   // (NR divides kUnit)
   const int64_t cost = tree_unit_cost(rows, kt, p.setup_cost), u0 = sq.cost + (static_cast<int64_t>(g) * units + unit) * cost;
   // ranges whose part of the axis meets the unit: r0 .. r1
   const int64_t r0 = div_nonneg((u0 + 1) * R + V - 1, V) - 1;
   const int64_t r1 = div_nonneg((u0 + cost) * R + V - 1, V) - 1;
+  // tiles of range r in the unit
+  auto tiles_of = [&](int64_t r) -> int2 {
+    if (r > r1) return make_int2(0, 0);
+    return make_int2(
+        tree_tile_at(max(div_nonneg(r * V, R) - u0, static_cast<int64_t>(0)), rows, kt, p.setup_cost),
+        tree_tile_at(max(min(div_nonneg((r + 1) * V, R) - u0, cost), static_cast<int64_t>(0)), rows, kt, p.setup_cost));
+  };
+  int2 first = make_int2(0, 0);
+  if (early) {
+    first = tiles_of(r0 + lane);
+    pdl_wait_and_release();
+  }
   const int64_t base = tree_piece_row(sq.start, p.n_q_heads, g, rows, static_cast<int64_t>(unit) * kUnit, 0, kUnit) +
                        (row0 - unit * kUnit);
   float M[NR], Lsum[NR], O[NR][N];
@@ -1228,11 +1270,8 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
   }
   for (int64_t x0 = r0; x0 <= r1; x0 += 32) {
     const int64_t r = x0 + lane;
-    int t0 = 0, t1 = 0;
-    if (r <= r1) {
-      t0 = tree_tile_at(max(div_nonneg(r * V, R) - u0, static_cast<int64_t>(0)), rows, kt, p.setup_cost);
-      t1 = tree_tile_at(max(min(div_nonneg((r + 1) * V, R) - u0, cost), static_cast<int64_t>(0)), rows, kt, p.setup_cost);
-    }
+    const int2 of = early && x0 == r0 ? first : tiles_of(r);
+    const int t0 = of.x, t1 = of.y;
     if (__any_sync(0xffffffffu, t0 == 0 && t1 == kt)) return;        // written where it was computed
     const bool have = t0 < t1;
     uint32_t left = __ballot_sync(0xffffffffu, have);
@@ -1350,7 +1389,10 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeWarps * nr - 1) / (kTMergeWarps * nr);
   const dim3 grid(chunks, static_cast<unsigned>(p.n_kv_heads), static_cast<unsigned>(p.batch));
   auto merge = nr == 4 ? tree_merge_kernel<D, NQ, 4> : tree_merge_kernel<D, NQ, 1>;
-  return cuda_failed(launch_pdl(merge, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges), "tree_merge_kernel launch")
+  // (2048 threads an SM)
+  const int ahead = static_cast<int64_t>(chunks) * p.n_kv_heads * p.batch <= 2048 / (kTMergeWarps * 32) * sm_count();
+  return cuda_failed(launch_pdl(merge, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges, ahead),
+                     "tree_merge_kernel launch")
              ? PKV_ERR_CUDA
              : PKV_OK;
 }
