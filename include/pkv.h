@@ -763,7 +763,7 @@ pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache
  * accepted[b][k] to base + k, in every head (bit for bit, any type of elt_bytes 1
  * or 2; a layer-major cache [num_blocks, num_layers, H_kv, 16, head_dim] is passed
  * with num_kv_heads = num_layers * H_kv).  Other rows stay as they are.  new_lens
- * (device int32 [batch], nullable; not context_lens itself: PKV_ERR_INVALID_ARG)
+ * (device int32 [batch], nullable; no part of context_lens: PKV_ERR_INVALID_ARG)
  * takes base + the number of accepted tokens.  The blocks from position base on
  * belong to the sequence alone.  Device errors (PKV_ERR_OOB; nothing of the
  * sequence moves and new_lens[b] stays): a list that does not ascend or passes

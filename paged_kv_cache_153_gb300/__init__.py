@@ -11,8 +11,9 @@ the library has not been built (``__graft_entry__.build()`` or
 
 Tensors: 16-bit data is passed as torch.float16 / torch.bfloat16 (or any
 2-byte dtype, tagged with ``dtype``), E4M3 caches as torch.uint8, tables and
-lengths as torch.int32, slot mappings as torch.int64.  The rotary, block-sparse
-and shared-prefix calls refuse tensors of other types: all 16-bit tensors of a
+lengths as torch.int32, slot mappings as torch.int64.  The rotary, block-sparse,
+shared-prefix, window and drafted tokens' calls refuse tensors of other types (the
+tokens' masks are torch.int64): all 16-bit tensors of a
 call have one type (with ``dtype`` given: two-byte elements), scales are fp32 with
 one entry per KV head, err_flag is int32.
 """

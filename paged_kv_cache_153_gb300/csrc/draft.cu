@@ -212,8 +212,10 @@ extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_
   if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
   if (max_accept > kMaxAccept || batch > 65535) return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
-  if (!k_cache || !v_cache || !block_tables || !context_lens || !cu_nodes || (max_accept > 0 && !accepted) ||
-      new_lens == context_lens)
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !cu_nodes || (max_accept > 0 && !accepted))
+    return PKV_ERR_INVALID_ARG;
+  // (several thread blocks read a sequence's length, one writes its new one)
+  if (new_lens != nullptr && new_lens < context_lens + batch && context_lens < new_lens + batch)
     return PKV_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) return PKV_ERR_INVALID_ARG;
   const int chunks = head_dim * elt_bytes / 16;

@@ -1,5 +1,5 @@
-// Module _tensor: the rotary append, the block index, the sparse and the
-// shared-prefix decode, straight from torch tensors.  Each reads
+// Module _tensor: the rotary append, the block index, the sparse, the shared-prefix
+// and the window decode, and the drafted tokens' calls, straight from torch tensors.  Each reads
 // shapes, strides and addresses, refuses what does not fit, and calls the
 // library's entry point; the same steps in Python take 2 to 6 us of a call
 // whose kernels run for 2 to 8 (rope: 8.3 us a call in Python, 2.9 here; sparse

@@ -308,6 +308,17 @@ def test_workspaces_that_are_too_small_are_refused(pkv):
     c.check(c.attend(pkv, workspace=torch.empty(n, dtype=torch.uint8, device="cuda")))
 
 
+@pytest.mark.parametrize("base,new,hq,hkv,d,seqs", [
+    ([20 + 37 * (i % 17) for i in range(700)], [1 + i % 2 for i in range(700)], 2, 2, 64, (0, 1, 16, 333, 699)),
+    ([50 * i for i in range(12)], [130, 256, 5, 64, 1, 256, 200, 0, 129, 128, 100, 99], 8, 2, 128, (2, 4, 8, 11)),
+])
+def test_states_of_many_and_of_few_rows_are_joined(pkv, base, new, hq, hkv, d, seqs):
+    # more thread blocks of the merge than the GPU holds at once; four rows a warp
+    c = Case(base, new, hq=hq, hkv=hkv, d=d, seed=5)
+    c.check(c.attend(pkv), seqs=seqs)
+    assert int(c.err.item()) == 0
+
+
 def test_many_sequences(pkv):
     # the most that one call takes, some without drafted tokens
     rng = np.random.default_rng(4)

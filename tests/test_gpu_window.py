@@ -277,3 +277,16 @@ def test_not_finite_rows_in_pairs_of_tiles(pkv):
             ref, lim = attn_limits.attend(c.q_h[1400 + i, h].double().numpy(), k[at], v[at], c.scale, "bf16")
             cols = np.arange(128) != 5
             assert (np.abs(got[i, h] - ref)[cols] <= lim[cols]).all(), (i, h)
+
+
+def test_the_largest_windows_and_first_tokens(pkv):
+    most = 2 ** 31 - 1
+    c = Case([300, 17, 0], [1, 1, 1], hq=8, hkv=2, d=64, seed=6)
+    want = decode(pkv, c, 400, 0).clone()
+    for window, sinks in ((most, 0), (most, most), (1, most), (400, 400)):
+        assert torch.equal(decode(pkv, c, window, sinks), want), (window, sinks)
+    c = chunk_case([300, 17], [40, 130], hq=8, hkv=2, d=64, seed=6)
+    want = prefill(pkv, c, 400, 0).clone()
+    for window, sinks in ((most, 0), (most, most), (1, most), (400, 400)):
+        assert torch.equal(prefill(pkv, c, window, sinks), want), (window, sinks)
+    assert int(c.err.item()) == 0

@@ -136,6 +136,12 @@ def test_commit_refusals(pkv):
     assert call(b=0) == 0
 
 
+def test_new_lengths_within_the_old_ones_are_refused(pkv):
+    for shift in (-4, 0, 4):
+        assert pkv.lib.pkv_tree_commit(A, A, A, A, A, A, 4, 2, 2, 128, 16, 4, 8, 2, C.c_void_p(A.value + shift), None,
+                                       None) == 1, shift
+
+
 def test_window_prefill_refusals(pkv):
     def call(q=A, kc=A, vc=A, tab=A, lens=A, cu=A, t=20, b=2, hq=8, hkv=2, d=128, bs=16, mb=4, nb=8, ml=10, w=5, s=1,
              scale=0.1, out=A, dt=1):
