@@ -97,7 +97,10 @@ namespace pkv {
 constexpr int kTSoftmax = 256;
 constexpr int kTTileBlocks = kTreeKeys / kBlockSize;
 constexpr float kTRescaleLog2 = 8.f;
-constexpr int kTBadSlots = 4;                     // pieces whose remembered tokens live at once
+// Pieces whose remembered tokens live at once.  While a piece's outputs are read no P V
+// of the next one runs, so the warps that look at V are at most kVStages tiles ahead,
+// and clear the slot of the piece behind those.
+constexpr int kTBadSlots = 5;
 
 // Cost of a unit's set-up (Q, the first tile's latency, its outputs) and of a key
 // tile against one row tile or two, in half tiles.  An FP8 tile is half the bytes, so
@@ -134,6 +137,7 @@ struct TreeSmem {
   static __host__ __device__ constexpr size_t bytes(int batch) {
     return 1024 + kSeqs + sizeof(TreeSeq) * (static_cast<size_t>(batch) + 1);
   }
+  static_assert(kTBadSlots >= kVStages + 2, "slots");
   // S / P buffers, and the outputs behind them
   static constexpr int kSBufs = 4 - NQ;
   static constexpr int kOCol = kSBufs * kTreeKeys;

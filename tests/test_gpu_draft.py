@@ -208,6 +208,24 @@ def test_rows_that_are_not_seen_change_nothing(pkv, dtype, kv, bad, base):
                 assert (np.abs(got[b_i, h] - ref[columns]) <= lim[columns]).all()
 
 
+@pytest.mark.parametrize("dtype,kv", [("bf16", None), ("f16", None), ("bf16", "e5m2")])
+def test_rows_that_are_not_finite_in_many_short_sequences(pkv, dtype, kv):
+    # tens of one-tile units a thread block, each with a token that is not finite
+    new = [2 + b % 3 for b in range(400)]
+    c = Case([10 + b % 50 for b in range(400)], new, hq=8, hkv=8, d=64, dtype=dtype, kv=kv, seed=9)
+    for b in range(0, 400, 2):
+        p = int(c.ctx[b]) - 1 - (b // 2) % 2
+        c.vc_h[int(c.tab[b, p // 16]), :, p % 16] = 0x7C if kv else float("inf")
+    for _ in range(20):
+        fine = torch.isfinite(c.attend(pkv).float()).cpu().numpy()
+        for b in range(400):
+            want = np.ones(new[b], bool)
+            if b % 2 == 0:
+                want &= ~c.seen[b][:, new[b] - 1 - (b // 2) % 2]
+            assert (fine[c.cu[b]:c.cu[b + 1]] == want[:, None, None]).all(), b
+    assert int(c.err.item()) == 0
+
+
 def test_every_fp8_code(pkv):
     # every finite code of both formats as K and as V, denormals among them
     for kv in FP8:
