@@ -1203,8 +1203,10 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
 // With one row a warp, and all thread blocks on the GPU at once, the geometry is
 // worked out from the inputs while the kernel before still runs (one document of
 // 131072: 123 us instead of 125; four chats 9.0 instead of 9.9).
+// Thread blocks of four warps, not eight: with four rows a warp the registers then
+// hold 20 warps an SM instead of 16 (the 32 sequences 131.6 us instead of 132.8).
 // ---------------------------------------------------------------------------
-constexpr int kTMergeWarps = 8;
+constexpr int kTMergeWarps = 4;
 
 template <int D, int NQ, int NR>
 __global__ void __launch_bounds__(kTMergeWarps * 32)
