@@ -73,9 +73,9 @@
 // as in the other kernels.
 //
 // Measured (back to back, everything with its launches): 32 sequences of 1024 to
-// 16384 tokens with 20 to 32 drafted ones, 32 and 8 heads of 128, bf16: 133 us, of
-// which 11 are the merge; the reads alone take 112 at 6.80 TB/s.  One of 131072 with
-// 64, fp16: 125 us (79); each row tile's softmax, P V and next Q K^T wait for each
+// 16384 tokens with 20 to 32 drafted ones, 32 and 8 heads of 128, bf16: 132 us, of
+// which 10 are the merge; the reads alone take 112 at 6.80 TB/s.  One of 131072 with
+// 64, fp16: 123 us (79); each row tile's softmax, P V and next Q K^T wait for each
 // other (4500 clocks, 2048 of them products).  16 of 4096 to 32768 with 10 to 31,
 // E4M3: 96 us (57): shared memory feeds the products, the conversions and the loads
 // in turn.  Four prompts of 2048 tokens, window 4096: 459 us; the products with
@@ -1395,8 +1395,8 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeWarps * nr - 1) / (kTMergeWarps * nr);
   const dim3 grid(chunks, static_cast<unsigned>(p.n_kv_heads), static_cast<unsigned>(p.batch));
   auto merge = nr == 4 ? tree_merge_kernel<D, NQ, 4> : tree_merge_kernel<D, NQ, 1>;
-  // (2048 threads an SM)
-  const int ahead = static_cast<int64_t>(chunks) * p.n_kv_heads * p.batch <= 2048 / (kTMergeWarps * 32) * sm_count();
+  // (by its registers, five thread blocks an SM)
+  const int ahead = static_cast<int64_t>(chunks) * p.n_kv_heads * p.batch <= 5ll * sm_count();
   return cuda_failed(launch_pdl(merge, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges, ahead),
                      "tree_merge_kernel launch")
              ? PKV_ERR_CUDA
