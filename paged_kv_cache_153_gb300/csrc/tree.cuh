@@ -75,7 +75,7 @@
 // Measured (back to back, everything with its launches): 32 sequences of 1024 to
 // 16384 tokens with 20 to 32 drafted ones, 32 and 8 heads of 128, bf16: 132 us, of
 // which 10 are the merge; the reads alone take 112 at 6.80 TB/s.  One of 131072 with
-// 64, fp16: 123 us (79); each row tile's softmax, P V and next Q K^T wait for each
+// 64, fp16: 121 us (79); each row tile's softmax, P V and next Q K^T wait for each
 // other (4500 clocks, 2048 of them products).  16 of 4096 to 32768 with 10 to 31,
 // E4M3: 96 us (57): shared memory feeds the products, the conversions and the loads
 // in turn.  Four prompts of 2048 tokens, window 4096: 459 us; the products with
@@ -111,12 +111,14 @@ __host__ __device__ constexpr int tree_tile_cost(int rows) { return rows > kTree
 
 template <int D, bool FP8, int NQ>
 struct TreeSmem {
-  // warps that convert codes (or look at V rows) behind the first twelve, and the
-  // registers that the softmax warps take from the others
+  // Warps that convert codes (or look at V rows) behind the first twelve, and the
+  // registers that the softmax warps take from the others.  (One document of 131072,
+  // fp16, with 144, 152, 160, 176: 121.7, 123.2, 120.9, 124.5 us; E4M3 contexts with 120,
+  // 136, 144, 152: 97.6, 95.2, 95.2, 98.1.)
   static constexpr int kXform = FP8 ? 8 : 4;
   static constexpr int kThreads = 384 + 32 * kXform;
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;           // a thread, at launch
-  static constexpr int kRegsSoftmax = FP8 ? 144 : 152, kRegsOther = FP8 ? 64 : 104;
+  static constexpr int kRegsSoftmax = FP8 ? 144 : 160, kRegsOther = FP8 ? 64 : 96;
   static_assert(kTSoftmax * kRegsSoftmax + (kThreads - kTSoftmax) * kRegsOther <= kThreads * kRegs, "registers");
   static constexpr int kTile = kTreeKeys * D * 2;                  // a Q, K or V tile
   static constexpr int kStage = kTile / 2;                         // FP8: a staged tile of codes
@@ -1202,7 +1204,7 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
 // of 131072, 19 pieces a row: 7.9 us; four rows one after another 24 us.)
 // With one row a warp, and all thread blocks on the GPU at once, the geometry is
 // worked out from the inputs while the kernel before still runs (one document of
-// 131072: 123 us instead of 125; four chats 9.0 instead of 9.9).
+// 131072: 123 us instead of 125 then; four chats 9.0 instead of 9.9).
 // Thread blocks of four warps, not eight: with four rows a warp the registers then
 // hold 20 warps an SM instead of 16 (the 32 sequences 131.6 us instead of 132.8).
 // ---------------------------------------------------------------------------
