@@ -747,8 +747,9 @@ pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache
  *                        initialisation needed; not shared by calls that run at
  *                        the same time.
  * Weights are multiplied in 16 bits: over fp16 and FP8 caches as fp16 rounded
- * once (and the normaliser sums the rounded ones), over bf16 caches as two parts
- * (exact to 2^-16).  q meets FP8 keys as a sum of E4M3 values, exact to 2^-17 of
+ * once (and the normaliser sums the rounded ones; weights below 2^-21 of their
+ * row's largest to the nearest multiple of 2^-31 of it at worst), over bf16 caches
+ * as two parts (exact to 2^-16).  q meets FP8 keys as a sum of E4M3 values, exact to 2^-17 of
  * the largest element of its row.  At most 1024 sequences, num_blocks *
  * num_kv_heads < 2^27 (PKV_ERR_UNSUPPORTED beyond).  Device errors (PKV_ERR_OOB; the sequence is
  * skipped, its outputs stay as they are): offsets that are not as described, more

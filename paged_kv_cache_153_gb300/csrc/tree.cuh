@@ -38,7 +38,10 @@
 //                 rounding, 2^-9, would be as large as the output's own); fp16 P
 //                 (2^-12) is rounded once, and l sums the rounded values.  The row
 //                 reference moves only when a tile's maximum exceeds it by more
-//                 than 2^8; only then is O rescaled.
+//                 than 2^8; only then is O rescaled.  fp16 weights are held times
+//                 2^7, so that the largest, 2^15, stays below fp16's and the
+//                 smallest step is 2^-31 of a row's largest weight (unscaled, one
+//                 key 17 nats above a long context took a fifth of the others).
 //   O += P V      P from TMEM.
 // Key tiles go from the last to the first: the ones with drafted tokens need a
 // look at their rows, which then overlaps the first loads.
@@ -97,6 +100,8 @@ namespace pkv {
 constexpr int kTSoftmax = 256;
 constexpr int kTTileBlocks = kTreeKeys / kBlockSize;
 constexpr float kTRescaleLog2 = 8.f;
+constexpr float kTHalfLog2 = 7.f;        // fp16 weights: of 2^15 at most
+static_assert(kTRescaleLog2 + kTHalfLog2 < 16.f, "fp16 weights");
 // Pieces whose remembered tokens live at once.  While a piece's outputs are read no P V
 // of the next one runs, so the warps that look at V are at most kVStages tiles ahead,
 // and clear the slot of the piece behind those.
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
             tmem_st16(to + x, o);
           }
         }
-        const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        const float nref = (m_ref == -INFINITY) ? 0.f : (std::is_same<MT, F16>::value ? kTHalfLog2 : 0.f) - m_ref;
         const uint64_t scale2 = f32x2(scale_log2, scale_log2), nref2 = f32x2(nref, nref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};            // l's summands of this tile: bf16
         float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // fp16
