@@ -57,7 +57,9 @@
 // [128, 256), is the sum of E4M3 parts -- the code of the element, of what is left,
 // and (fp16 q) of what is left of that -- two for bf16's 8 bits, three for fp16's
 // 11, exact to 2^-17 of the row's largest element (half a step of E4M3's denormals);
-// 2^-k joins the row's softmax scale.  A launch of its own writes the parts to the
+// 2^-k joins the row's softmax scale, of which only K's sign goes with the parts: so
+// the maximum of a row's scores is that of the scaled ones.  A scale may be 0 or not a
+// number: scores are masked behind it.  A launch of its own writes the parts to the
 // workspace (in the kernel, per piece, four warps took 6 to 13 us).  V's codes are
 // converted to fp16 tiles, exactly, by eight warps (one instruction for two E4M3
 // codes, one byte permutation for two E5M2 ones; with four warps 106 us instead of
@@ -526,9 +528,9 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const int unit_row = sg.unit * kTreeRows * NQ + row;            // of the sequence's rows
       const int node = min(unit_row >> shift, sq.n - 1);
       const uint32_t* words = p.mask + (static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words);
-      // (FP8: q's parts, and so the scores, are scaled by row)
+      // (FP8: q's parts, and so the scores, are scaled by row, and hold K's sign)
       const float scale_log2 =
-          p.qk_scale_log2 * (kFp8 ? p.k_scale[sg.g] * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
+          p.qk_scale_log2 * (kFp8 ? fabsf(p.k_scale[sg.g]) * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
                                                                    (sg.g << shift) + (unit_row & ((1 << shift) - 1))]
                                   : 1.f);
       const uint32_t to = tmem + lane_base + L::kOCol + tile * D;
@@ -577,14 +579,15 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         if (!ok) break;
         tc_fence_after();
         if (tail) {
-          // masked where they lie: the loops below stay short
+          // masked where they lie: the loops below stay short (FP8: scaled first, for a
+          // scale of 0 would make a NaN of -inf)
 #pragma unroll 1
           for (int w = 0; w < 4; ++w) {
             const uint32_t bits = w < 2 ? (w == 0 ? see[0] : see[1]) : (w == 2 ? see[2] : see[3]);
             float x[32];
             tmem_ld32(ts + 32 * w, x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1u ? x[i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1u ? (kFp8 ? x[i] * scale_log2 : x[i]) : -INFINITY;
             tmem_st32(ts + 32 * w, x);
           }
         }
@@ -598,7 +601,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         // (the turn only now: between the groups only the references are in line)
         if (!two && n > 0) ok = take_turn();
         if (!ok) break;
-        const float m_tile = mx * scale_log2;
+        const float tile_scale = kFp8 && tail ? 1.f : scale_log2;
+        const float m_tile = mx * tile_scale;
         float alpha = 1.f;
         if (m_tile > m_ref + kTRescaleLog2) {
           alpha = ex2_approx(m_ref - m_tile);
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           }
         }
         const float nref = (m_ref == -INFINITY) ? 0.f : (std::is_same<MT, F16>::value ? kTHalfLog2 : 0.f) - m_ref;
-        const uint64_t scale2 = f32x2(scale_log2, scale_log2), nref2 = f32x2(nref, nref);
+        const uint64_t scale2 = f32x2(tile_scale, tile_scale), nref2 = f32x2(nref, nref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};            // l's summands of this tile: bf16
         float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // fp16
         // 32 keys at a time; the upper half first, whose product may run while the lower
@@ -1147,14 +1151,15 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
 
 // ---------------------------------------------------------------------------
 // q as a sum of E4M3 parts (FP8 caches): a warp per row of D elements, a lane per D /
-// 32 of them.  parts [3, rows, D] codes, scale [rows].
+// 32 of them, times the sign of its KV head's K scale.  parts [3, rows, D] codes,
+// scale [rows].
 // ---------------------------------------------------------------------------
 constexpr int kTPartWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kTPartWarps * 32)
-    tree_parts_kernel(const void* __restrict__ q, int q_bf16, int64_t rows, uint8_t* __restrict__ parts,
-                      float* __restrict__ scale) {
+    tree_parts_kernel(const void* __restrict__ q, int q_bf16, int64_t rows, int n_q_heads, int group_shift,
+                      const float* __restrict__ k_scale, uint8_t* __restrict__ parts, float* __restrict__ scale) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x & 31;
   pdl_wait_and_release();   // (the next kernel waits for this one before it reads what this writes)
@@ -1176,7 +1181,8 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
   nan = __any_sync(0xffffffffu, nan);
   // top in [2^e, 2^(e + 1)): times 2^(7 - e)
   const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -113);
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+  const float mag = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+  const float up = k_scale[static_cast<int>(row % n_q_heads) >> group_shift] < 0.f ? -mag : mag;
   if (lane == 0) scale[row] = nan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
 #pragma unroll
   for (int e = 0; e < N; ++e) f[e] *= up;
@@ -1390,7 +1396,8 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   if constexpr (KV::kBytes == 1) {
     const int64_t rows = p.num_tokens * p.n_q_heads;
     if (cuda_failed(launch_pdl(tree_parts_kernel<D>, dim3(static_cast<unsigned>((rows + kTPartWarps - 1) / kTPartWarps)),
-                               dim3(kTPartWarps * 32), 0, stream, p.q, p.q_bf16, rows, p.parts, p.part_scale),
+                               dim3(kTPartWarps * 32), 0, stream, p.q, p.q_bf16, rows, p.n_q_heads, p.group_shift,
+                               p.k_scale, p.parts, p.part_scale),
                     "tree_parts_kernel launch"))
       return PKV_ERR_CUDA;
   }
