@@ -749,10 +749,12 @@ pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache
  * Weights are multiplied in 16 bits: over fp16 and FP8 caches as fp16 rounded
  * once (and the normaliser sums the rounded ones; weights below 2^-21 of their
  * row's largest to the nearest multiple of 2^-31 of it at worst), over bf16 caches
- * as two parts (exact to 2^-16).  q meets FP8 keys as a sum of E4M3 values, exact to 2^-17 of
- * the largest element of its row.  At most 1024 sequences, num_blocks *
- * num_kv_heads < 2^27 (PKV_ERR_UNSUPPORTED beyond).  Device errors (PKV_ERR_OOB; the sequence is
- * skipped, its outputs stay as they are): offsets that are not as described, more
+ * as two parts (exact to 2^-16).  q meets FP8 keys as a sum of FP8 values: exact for
+ * elements down to 2^-9 (bf16) or 2^-6 (fp16) of their row's largest, smaller ones off
+ * by at most 2^-17 of that one; in a row where that concerns an eighth of the elements or
+ * more, exact down to 2^-13, and off by at most 2^-21 (bf16) or 2^-24 (fp16).  At most 1024 sequences, num_blocks *
+ * num_kv_heads < 2^27 (PKV_ERR_UNSUPPORTED beyond).  Device errors (PKV_ERR_OOB; the
+ * sequence is skipped, its outputs stay as they are): offsets that are not as described, more
  * tokens than max_nodes or than the context has, a context longer than its table.
  * A table entry outside the pool reads as zeros and is reported.  Other arguments
  * and requirements as in pkv_paged_decode_attention and its FP8 forms.

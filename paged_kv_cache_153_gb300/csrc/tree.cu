@@ -16,8 +16,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Workspace, from a 256-byte boundary on: the sequences' geometry | [rows, 2]
-// fp32 (m, l) | [rows, D] fp32 o, stored 32 bytes at a time | (FP8 caches) [3, T, Hq,
-// D] codes of q's parts and [T, Hq] fp32 scales.
+// fp32 (m, l) | [rows, D] fp32 o, stored 32 bytes at a time | (FP8 caches) [5, T, Hq,
+// D] codes of q's parts (bf16 q: three of them) and [T, Hq] fp32 scales.
 struct TreeWs {
   size_t seqs, ml, o, parts, part_scale, total;
 };
@@ -42,7 +42,7 @@ bool tree_ws(int batch, int64_t num_tokens, int n_q_heads, int n_kv_heads, int h
   w->seqs = take((static_cast<size_t>(batch) + 1) * sizeof(TreeSeq));
   w->ml = take(rows * 2 * sizeof(float));
   w->o = take(rows * head_dim * sizeof(float));
-  w->parts = take(static_cast<size_t>(num_tokens) * n_q_heads * head_dim * 3);
+  w->parts = take(static_cast<size_t>(num_tokens) * n_q_heads * head_dim * 5);
   w->part_scale = take(static_cast<size_t>(num_tokens) * n_q_heads * sizeof(float));
   w->total = at + 256;
   return true;
@@ -63,7 +63,7 @@ pkv_status tree_common(int kv_kind, const void* q, const void* k_cache, const vo
   const int group = n_q_heads / n_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PKV_ERR_UNSUPPORTED;
   if (mask_words > kTreeMaxWords || batch > kTreeMaxBatch || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
-  if (num_tokens > INT32_MAX / 3 || num_tokens * n_q_heads > INT32_MAX || num_blocks * n_kv_heads > INT32_MAX / kBlockSize)
+  if (num_tokens > INT32_MAX / 5 || num_tokens * n_q_heads > INT32_MAX || num_blocks * n_kv_heads > INT32_MAX / kBlockSize)
     return PKV_ERR_UNSUPPORTED;                      // (32-bit TMA row coordinates)
   if (batch == 0 || num_tokens == 0 || max_nodes == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_nodes || !tree_mask || !out || !workspace)
@@ -87,7 +87,7 @@ pkv_status tree_common(int kv_kind, const void* q, const void* k_cache, const vo
                          !encode_block_tmap(&p.tmap_k, k_cache, num_blocks * n_kv_heads, head_dim) ||
                          !encode_block_tmap(&p.tmap_v, v_cache, num_blocks * n_kv_heads, head_dim)
                    : !encode_code_tmap(&p.tmap_k, k_cache, num_blocks * n_kv_heads * kBlockSize, head_dim) ||
-                         !encode_parts_tmap(&p.tmap_q, ws + w.parts, 3 * num_tokens, n_q_heads, head_dim, group,
+                         !encode_parts_tmap(&p.tmap_q, ws + w.parts, (dtype == PKV_BF16 ? 3 : 5) * num_tokens, n_q_heads, head_dim, group,
                                             p.q_box))
     return PKV_ERR_CUDA;
   p.parts = reinterpret_cast<uint8_t*>(ws + w.parts);

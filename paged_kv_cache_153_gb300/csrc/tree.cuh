@@ -55,15 +55,19 @@
 // FP8 caches.  K's codes are an operand as they are (kind::f8f6f4, twice the rate
 // of fp16), so q is too: per row q 2^k, k such that its largest element lies in
 // [128, 256), is the sum of E4M3 parts -- the code of the element, of what is left,
-// and (fp16 q) of what is left of that -- two for bf16's 8 bits, three for fp16's
-// 11, exact to 2^-17 of the row's largest element (half a step of E4M3's denormals);
-// 2^-k joins the row's softmax scale, of which only K's sign goes with the parts: so
-// the maximum of a row's scores is that of the scaled ones.  A scale may be 0 or not a
-// number: scores are masked behind it.  A launch of its own writes the parts to the
-// workspace (in the kernel, per piece, four warps took 6 to 13 us).  V's codes are
-// converted to fp16 tiles, exactly, by eight warps (one instruction for two E4M3
-// codes, one byte permutation for two E5M2 ones; with four warps 106 us instead of
-// 100).  With K converted as well, shared memory took 3900 clocks a tile.
+// and (fp16 q) of what is left of that -- two for bf16's 8 bits, three for fp16's 11.
+// They hold elements down to 2^-9 (2^-6) of the row's largest, and smaller ones to half
+// a step of E4M3's denormals, 2^-17 of the largest.  Beside an outlier that is too little
+// for the rest of a row: where an eighth of a row's elements or more are not held, its
+// unit takes the parts behind the first in E5M2, which hold elements down to 2^-13 and
+// smaller ones to 2^-21 (2^-24).  (Products with them take longer: E4M3 contexts 105 us
+// where all units took them, else 97.)  2^-k joins the row's softmax scale, of which only
+// K's sign goes with the parts: so the maximum of a row's scores is that of the scaled
+// ones.  A scale may be 0 or not a number: scores are masked behind it.  A launch of its
+// own writes the parts to the workspace (in the kernel, per piece, four warps took 6 to
+// 13 us).  V's codes are converted to fp16 tiles, exactly, by eight warps (one
+// instruction for two E4M3 codes, one byte permutation for two E5M2 ones; with four
+// warps 106 us instead of 100).  With K converted as well, shared memory took 3900 clocks a tile.
 //
 // Prompt chunks (CHUNK).  The same kernel attends the new tokens of a prompt to the
 // first tokens and a window: a thread block per unit, whose key tiles are those
@@ -339,18 +343,38 @@ __device__ __forceinline__ uint64_t umma_desc_codes(uint32_t saddr) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (1ull << 16) |
          (static_cast<uint64_t>((8 * D) >> 4) << 32) | (1ull << 46) | ((D == 128 ? 2ull : 4ull) << 61);
 }
-// kind::f8f6f4: A in E4M3, B in KV, fp32 accumulate, both K-major, M = 128
+// kind::f8f6f4: A in E4M3 or E5M2, B in KV, fp32 accumulate, both K-major, M = 128
 template <typename KV>
-__host__ __device__ constexpr uint32_t umma_idesc_codes(int n) {
-  return (1u << 4) | ((std::is_same<KV, E5M2>::value ? 1u : 0u) << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+__host__ __device__ constexpr uint32_t umma_idesc_codes(int n, bool a_e5m2) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((std::is_same<KV, E5M2>::value ? 1u : 0u) << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
+// D += A B over 32 STEPS elements of K: successive 32-byte steps of the descriptors.  (As
+// statements of their own, E4M3 contexts took 104 us instead of 97 once the instruction
+// descriptor was no constant: the issuer is in the chain of a tile's scores.)
+template <int STEPS>
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
-      : "memory");
+  static_assert(STEPS == 2 || STEPS == 4, "rows of 64 or 128 bytes");
+  if constexpr (STEPS == 4)
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, b1;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        : "memory");
 }
 
 // MT: 16-bit type of the products; KV: the cache's (MT, or an FP8 format)
@@ -408,7 +432,8 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
   uint64_t* mma_idle = o_read + 1;                 // [2] an issuer's MMAs done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * 3 + 3 * 3 + 2 * 2 + 4 * 3 + 5 + 17 + 2 + 1) * 8 <= 512, "barrier block overflows");
+  volatile int* far_parts = abort_flag + 1;        // FP8: the piece's parts behind the first are E5M2
+  static_assert((2 * 3 + 3 * 3 + 2 * 2 + 4 * 3 + 5 + 17 + 2 + 2) * 8 <= 512, "barrier block overflows");
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + L::kBad);
   float* red = reinterpret_cast<float*>(sm + L::kRed);
   TreeSeq* seqs = reinterpret_cast<TreeSeq*>(sm + L::kSeqs);
@@ -528,10 +553,11 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       const int unit_row = sg.unit * kTreeRows * NQ + row;            // of the sequence's rows
       const int node = min(unit_row >> shift, sq.n - 1);
       const uint32_t* words = p.mask + (static_cast<int64_t>(sq.start) + node) * (2 * p.mask_words);
-      // (FP8: q's parts, and so the scores, are scaled by row, and hold K's sign)
+      // (FP8: q's parts, and so the scores, are scaled by row, and hold K's sign; the sign of
+      // a row's scale tells which parts it needs)
       const float scale_log2 =
-          p.qk_scale_log2 * (kFp8 ? fabsf(p.k_scale[sg.g]) * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
-                                                                   (sg.g << shift) + (unit_row & ((1 << shift) - 1))]
+          p.qk_scale_log2 * (kFp8 ? fabsf(p.k_scale[sg.g] * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
+                                                                   (sg.g << shift) + (unit_row & ((1 << shift) - 1))])
                                   : 1.f);
       const uint32_t to = tmem + lane_base + L::kOCol + tile * D;
       float m_ref = -INFINITY, l_run = 0.f;
@@ -823,18 +849,28 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       };
       int id = fetch_id(sg.t1 - 1);
       if (!is_v) {
+        bool far = false;                            // does any row need the E5M2 parts?
+        if constexpr (kFp8) {
+          for (int x = lane; x < sg.rows; x += 32) {
+            const int r = sg.unit * kTreeRows * NQ + x;
+            far |= p.part_scale[(static_cast<int64_t>(sq.start) + (r >> shift)) * p.n_q_heads + (sg.g << shift) +
+                                (r & ((1 << shift) - 1))] < 0.f;
+          }
+          far = __any_sync(0xffffffffu, far);
+        }
         // Q of the piece, once every Q K^T of the piece before has read it
         if (pieces > 0) good = __all_sync(0xffffffffu, tree_wait(q_empty, (pieces - 1) & 1, p, abort_flag));
         if (!good) break;
         const int parts = kFp8 ? (p.q_bf16 ? 2 : 3) : 1;
+        if (kFp8 && lane == 0) *far_parts = far;
         if (lane == 0)
           mbar_arrive_expect_tx(q_full, nq * parts * (p.q_box << shift) * (kFp8 ? D : 2 * D));
         ++pieces;
         __syncwarp();
         if (kFp8 && lane < nq * parts) {
-          const int c = lane / parts, part = lane % parts;
+          const int c = lane / parts, part = lane % parts, kept = part + (far && part > 0 ? parts - 1 : 0);
           tma_load_3d(sm + L::kQ + c * L::kQTile + part * L::kStage, &p.tmap_q, 0, sg.g << shift,
-                      static_cast<int>(part * p.num_tokens) + sq.start +
+                      static_cast<int>(kept * p.num_tokens) + sq.start +
                           ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift),
                       q_full, policy_evict_last());
         }
@@ -914,6 +950,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
     const bool qk_warp = (warp == 9);
     bool ok = true;
     if (lane == 0) {
+      uint32_t id_rest = 0;                          // FP8: of the parts behind the first
       Ring<NB> sr;
       Ring<L::kKStages> kr;
       Ring<L::kVStages> vr;
@@ -926,6 +963,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         if (qk_warp) {
           // (the producer loads nothing while the previous kernel runs)
           ok = mbar_wait_started_early(q_full, pieces & 1, p.err, p.wait_limit_ns);
+          if constexpr (kFp8) id_rest = umma_idesc_codes<KV>(kTreeKeys, *far_parts != 0);
         }
         // (the piece's first P V overwrites the outputs of the piece before)
         if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
@@ -947,16 +985,13 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
               if constexpr (kFp8) {
                 const uint64_t a0 = umma_desc_codes<D>(smem_u32(sm + L::kQ + c * L::kQTile));
                 const uint64_t b0 = umma_desc_codes<D>(smem_u32(sm + L::kK + kr.s * L::kKTile));
-                constexpr uint32_t kIdCodes = umma_idesc_codes<KV>(kTreeKeys);
+                constexpr uint32_t kIdFirst = umma_idesc_codes<KV>(kTreeKeys, false);
                 // (the smallest parts first)
 #pragma unroll
-                for (int part = L::kParts - 1; part >= 0; --part) {
-                  if (part >= parts) continue;
-#pragma unroll
-                  for (int ks = 0; ks < D / 32; ++ks)
-                    umma_f8(d_s, a0 + static_cast<uint64_t>((part * L::kStage + ks * 32) >> 4),
-                            b0 + static_cast<uint64_t>((ks * 32) >> 4), kIdCodes, ks > 0 || part < parts - 1);
-                }
+                for (int part = L::kParts - 1; part >= 0; --part)
+                  if (part < parts)
+                    umma_f8<D / 32>(d_s, a0 + static_cast<uint64_t>((part * L::kStage) >> 4), b0,
+                                    part == 0 ? kIdFirst : id_rest, part < parts - 1);
               } else {
                 const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + c * L::kTile), 16, 1024);
                 const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
@@ -1150,9 +1185,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
 }
 
 // ---------------------------------------------------------------------------
-// q as a sum of E4M3 parts (FP8 caches): a warp per row of D elements, a lane per D /
-// 32 of them, times the sign of its KV head's K scale.  parts [3, rows, D] codes,
-// scale [rows].
+// q as a sum of parts (FP8 caches): a warp per row of D elements, a lane per D / 32 of
+// them, times the sign of its KV head's K scale.  parts [., rows, D] codes: the first in
+// E4M3, the others (one of bf16, two of fp16) in E4M3, then the same in E5M2.  scale
+// [rows], below 0 where the row needs the E5M2 ones.
 // ---------------------------------------------------------------------------
 constexpr int kTPartWarps = 8;
 
@@ -1165,6 +1201,8 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
   pdl_wait_and_release();   // (the next kernel waits for this one before it reads what this writes)
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kTPartWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
+  // (rows fit 32 bits)
+  const float ks = k_scale[(static_cast<uint32_t>(row) % static_cast<uint32_t>(n_q_heads)) >> group_shift];
   const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(q) + row * D) + lane * (N / 2);
   float f[N];
   float top = 0.f;
@@ -1182,27 +1220,47 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
   // top in [2^e, 2^(e + 1)): times 2^(7 - e)
   const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -113);
   const float mag = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
-  const float up = k_scale[static_cast<int>(row % n_q_heads) >> group_shift] < 0.f ? -mag : mag;
-  if (lane == 0) scale[row] = nan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+  const float up = ks < 0.f ? -mag : mag;
 #pragma unroll
   for (int e = 0; e < N; ++e) f[e] *= up;
-#pragma unroll
-  for (int part = 0; part < 3; ++part) {
+  // the codes of r as part `at`; r: what is left
+  auto put = [&](int at, float* r, auto fmt) {
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
-      uint32_t code = fp8x2_from_f32(f[e], f[e + 1], E4M3{});
-      const float2 back = unpack2_e4m3(static_cast<uint16_t>(code));
-      f[e] -= back.x, f[e + 1] -= back.y;
-      if (nan) code = 0x7f7fu;                       // (an infinity or a NaN: so is the row's output)
+      uint32_t code = fp8x2_from_f32(r[e], r[e + 1], fmt);
+      float2 back;
+      if constexpr (std::is_same<decltype(fmt), E4M3>::value)
+        back = unpack2_e4m3(static_cast<uint16_t>(code));
+      else
+        back = unpack2_e5m2(code);
+      r[e] -= back.x, r[e + 1] -= back.y;
+      if (nan) code = 0x7f7fu;                       // (a NaN in both formats; so is the row's output)
       w |= code << (8 * e);
     }
-    uint8_t* dst = parts + (part * rows + row) * D + lane * N;
+    uint8_t* dst = parts + (at * rows + row) * D + lane * N;
     if constexpr (N == 4)
       *reinterpret_cast<uint32_t*>(dst) = w;
     else
       *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w);
+  };
+  put(0, f, E4M3{});
+  float near[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) near[e] = f[e];
+  put(1, near, E4M3{});
+  if (q_bf16) {
+    put(2, f, E5M2{});
+  } else {
+    put(2, near, E4M3{});
+    put(3, f, E5M2{});
+    put(4, f, E5M2{});
   }
+  int left = 0;                                      // elements that the E4M3 parts do not hold
+#pragma unroll
+  for (int e = 0; e < N; ++e) left += __popc(__ballot_sync(0xffffffffu, near[e] != 0.f));
+  const float back = nan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+  if (lane == 0) scale[row] = !nan && left >= D / 8 ? -back : back;
 }
 
 // ---------------------------------------------------------------------------

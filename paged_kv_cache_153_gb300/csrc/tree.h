@@ -25,10 +25,10 @@ struct TreeParams {
   CUtensorMap tmap_k;            // 16-bit caches: [NB Hkv 2, D / 64, 8, 64], boxes of a block's rows
   CUtensorMap tmap_v;            // (FP8: tmap_k alone, [NB Hkv 16, D] bytes, boxes of 16 rows, D-byte swizzle)
   CUtensorMap tmap_q;            // [T, Hq, D], boxes of [q_box tokens, G, 64]
-                                 // (FP8: q's parts, [3 T, Hq, D] bytes, boxes of [q_box tokens, G, D])
+                                 // (FP8: q's parts, [3 or 5 T, Hq, D] bytes, boxes of [q_box tokens, G, D])
   const void* q;                 // FP8 caches
   uint8_t* parts;                // workspace: q's parts
-  float* part_scale;             // [T, Hq]
+  float* part_scale;             // [T, Hq], below 0: the row needs the E5M2 parts
   const uint8_t* v_codes;
   const float* k_scale;
   const float* v_scale;

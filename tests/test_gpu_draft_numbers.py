@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import attn_limits
 from tests.test_gpu_draft import Case
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +48,37 @@ def test_a_scale_that_is_not_a_number_stays_in_its_head(pkv):
             want[2] = True
             assert not out[2].any()
         assert torch.equal(fine, want)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kv", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("outlier,where", [(2.0 ** 10, ...), (2.0 ** 12, ...), (2.0 ** 12, 3), (1.5 * 2.0 ** 14, ...)])
+def test_an_outlier_of_q_leaves_the_other_elements_their_bits(pkv, dtype, kv, outlier, where):
+    """One element of each row of q (or of one row) is far larger than the others, and K
+    is 0 there.  The others are exact as parts down to 2^-13 of the row's largest, and off
+    by 2^-21 (bf16, two parts) or 2^-24 (fp16, three) of it below."""
+    c = Case([300, 20], [12, 5], hq=8, hkv=2, d=64, dtype=dtype, kv=kv, seed=3)
+    c.q_h.clamp_(-2, 2)
+    c.q_h[where, :, 5] = outlier if dtype == "bf16" else min(outlier, 2.0 ** 14)
+    dead = c.kc_h == 0x7F
+    c.kc_h[..., 5] = 0
+    c.kc_h[dead] = 0x7F
+    c.ks[:] = torch.tensor([4.0, 2.0])                         # (logits of tens)
+    part = 2.0 ** -21 if dtype == "bf16" else 2.0 ** -24
+    got = c.attend(pkv).double().cpu().numpy()
+    assert int(c.err.item()) == 0
+    for b in range(2):
+        for g in range(2):
+            k, v = c.rows(b, g)
+            for i in range(int(c.new[b])):
+                at = np.concatenate([np.arange(int(c.base[b])), int(c.base[b]) + np.flatnonzero(c.seen[b][i])])
+                for h in range(4 * g, 4 * g + 4):
+                    q = c.q_h[c.cu[b] + i, h].double().numpy()
+                    ref, lim = attn_limits.attend(q, k[at], v[at], c.scale, dtype, "f16")
+                    logit = k[at] @ q * c.scale
+                    w = np.exp(logit - logit.max())
+                    # a logit off by delta moves weight and normaliser by a factor of e^delta each
+                    delta = c.scale * part * np.abs(q).max() * np.abs(k[at]).sum(1).max()
+                    lim = lim + np.expm1(2 * delta) * (w / w.sum()) @ np.abs(v[at])
+                    x = got[c.cu[b] + i, h]
+                    assert (np.abs(x - ref) <= lim).all(), (b, i, h, float((np.abs(x - ref) / lim).max()))
