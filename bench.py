@@ -83,7 +83,7 @@ KERNEL_SOURCES = {
     "rope": _COMMON_SOURCES + ("rope.cu",),
     "sparse": _COMMON_SOURCES + _DECODE_SOURCES + ("block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu"),
     "window": _COMMON_SOURCES + _DECODE_SOURCES + ("decode_window.cu", "decode_window_fp8.cu"),
-    "draft": _COMMON_SOURCES + ("draft.cu", "tree.h", "tree.cuh", "tree.cu", "tree_16.cu", "tree_fp8.cu",
+    "draft": _COMMON_SOURCES + ("draft.cu", "tree.h", "tree.cuh", "tree.cu", "tree_16.cu", "tree_fp8.cu", "tree_one.cu",
                                 "tree_chunk.cu", "tcgen05.cuh", "decode.cuh"),
     "prefix_decode": _COMMON_SOURCES + _DECODE_SOURCES + ("decode_rest.cu", "prefix.h", "prefix.cu", "tcgen05.cuh"),
 }

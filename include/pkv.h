@@ -689,8 +689,9 @@ pkv_status pkv_paged_decode_attention_window_e5m2(const void* q, const uint8_t* 
  * and V of positions that a token does not see change nothing for it, whatever
  * bits they hold; an element of V that is not finite gives an output that is not
  * finite where it is seen.  Weights in 16 bits as in the drafted tokens' attention
- * below.  max_query_len: an upper bound of n_b.  Tokens behind the last sequence
- * are neither read nor written.  Device errors (PKV_ERR_OOB; the sequence is
+ * below (fp16 ones rounded once, as in pkv_paged_prefill_attention, with one query
+ * head per KV head too).  max_query_len: an upper bound of n_b.  Tokens behind the
+ * last sequence are neither read nor written.  Device errors (PKV_ERR_OOB; the sequence is
  * skipped, its outputs stay as they are): offsets that do not ascend within
  * [0, num_tokens], more tokens than max_query_len or than the context has, a
  * context longer than its table.  A table entry outside the pool reads as zeros
@@ -748,8 +749,9 @@ pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache
  *                        the same time.
  * Weights are multiplied in 16 bits: over fp16 and FP8 caches as fp16 rounded
  * once (and the normaliser sums the rounded ones; weights below 2^-21 of their
- * row's largest to the nearest multiple of 2^-31 of it at worst), over bf16 caches
- * as two parts (exact to 2^-16).  q meets FP8 keys as a sum of FP8 values: exact for
+ * row's largest to the nearest multiple of 2^-31 of it at worst), or, with one
+ * query head per KV head, as two fp16 parts; over bf16 caches as two parts (exact
+ * to 2^-16).  q meets FP8 keys as a sum of FP8 values: exact for
  * elements down to 2^-9 (bf16) or 2^-6 (fp16) of their row's largest, smaller ones off
  * by at most 2^-17 of that one; in a row where that concerns an eighth of the elements or
  * more, exact down to 2^-13, and off by at most 2^-21 (bf16) or 2^-24 (fp16).  At most 1024 sequences, num_blocks *

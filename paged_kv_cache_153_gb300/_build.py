@@ -35,7 +35,7 @@ CUDA_SOURCES = ["append.cu", "api.cu", "decode_f16.cu", "decode_bf16.cu", "decod
                 "noalloc.cu", "decode_int8.cu", "append_int8.cu", "rope.cu",
                 "block_index.cu", "decode_listed.cu", "decode_listed_fp8.cu", "decode_rest.cu", "prefix.cu",
                 "decode_window.cu", "decode_window_fp8.cu", "draft.cu", "tree.cu", "tree_16.cu", "tree_fp8.cu",
-                "tree_chunk.cu"]
+                "tree_one.cu", "tree_chunk.cu"]
 PREFILL_SOURCES = ["prefill.cu"]
 CXX_SOURCES = ["pool.cpp"]
 CALL_SOURCES = ["pycall.cpp"]

@@ -122,8 +122,10 @@ pkv_status tree_common(int kv_kind, const void* q, const void* k_cache, const vo
                         ((max_nodes * group + kTreeRows * q_tiles - 1) / (kTreeRows * q_tiles));
   const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_context_len) + kTreeKeys - 1) / kTreeKeys);
   const int ranges = static_cast<int>(std::min<int64_t>(num_sms, units * tiles));
-  const TreeLauncher launch = kv_kind == 0 ? tree_launcher_16(dtype, head_dim, q_tiles)
-                                           : tree_launcher_fp8(kv_kind, head_dim, q_tiles);
+  const TreeLauncher launch = group == 1 && (kv_kind != 0 || dtype == PKV_F16)
+                                  ? tree_launcher_one(kv_kind, head_dim, q_tiles)
+                              : kv_kind == 0 ? tree_launcher_16(dtype, head_dim, q_tiles)
+                                             : tree_launcher_fp8(kv_kind, head_dim, q_tiles);
   return launch(p, ranges, static_cast<cudaStream_t>(stream));
 }
 

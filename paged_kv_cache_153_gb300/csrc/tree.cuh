@@ -42,6 +42,10 @@
 //                 2^7, so that the largest, 2^15, stays below fp16's and the
 //                 smallest step is 2^-31 of a row's largest weight (unscaled, one
 //                 key 17 nats above a long context took a fifth of the others).
+//                 With one query head per KV head (ONE), where the dense decode
+//                 keeps p in fp32, fp16 P is two fp16 parts.  (8 and 8 heads: the 32
+//                 sequences below in fp16 124 us, 122 with one part; the 16 in E4M3
+//                 109 us, 89: V is read twice from shared memory, which bounds it.)
 //   O += P V      P from TMEM.
 // Key tiles go from the last to the first: the ones with drafted tokens need a
 // look at their rows, which then overlaps the first loads.
@@ -328,7 +332,15 @@ __device__ __forceinline__ void add_halves(uint32_t w, float& a, float& b) {   /
       : "+f"(a), "+f"(b)
       : "r"(w));
 }
-__device__ __forceinline__ float2 less_bf16(float a, float b, uint32_t w) {    // a, b - the bf16 numbers of w
+__device__ __forceinline__ float2 less16(float a, float b, uint32_t w, F16) {  // a, b - the halves of w
+  float2 d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "fma.rn.f32.f16 %0, lo, %5, %3;\n\tfma.rn.f32.f16 %1, hi, %5, %4;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(w), "f"(a), "f"(b), "h"(static_cast<uint16_t>(0xbc00)));           // (times -1)
+  return d;
+}
+__device__ __forceinline__ float2 less16(float a, float b, uint32_t w, BF16) { // a, b - the bf16 numbers of w
   float2 d;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
       "fma.rn.f32.bf16 %0, lo, %5, %3;\n\tfma.rn.f32.bf16 %1, hi, %5, %4;\n\t}"
@@ -402,13 +414,15 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <typename MT, typename KV, int D, int NQ, bool CHUNK>
+// ONE: one query head per KV head (fp16 products)
+template <typename MT, typename KV, int D, int NQ, bool CHUNK, bool ONE>
 __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool kFp8 = KV::kBytes == 1;
   using L = TreeSmem<D, kFp8, NQ>;
-  constexpr bool kSplit = std::is_same<MT, BF16>::value;
+  constexpr bool kSplit = std::is_same<MT, BF16>::value || ONE;   // P in two parts
   constexpr int NB = L::kSBufs;
   static_assert(!CHUNK || !kFp8, "prompt chunks: 16-bit caches");
+  static_assert(!ONE || (!CHUNK && std::is_same<MT, F16>::value), "one query head: fp16 products");
   constexpr int kBadWords = CHUNK ? 16 : 8;        // of remembered tokens
   static_assert(!CHUNK || L::kXform * 16 <= kTBadSlots * L::kXform * 8, "remembered tokens");
   extern __shared__ unsigned char tsm_raw[];
@@ -656,11 +670,11 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         }
         const float nref = (m_ref == -INFINITY) ? 0.f : (std::is_same<MT, F16>::value ? kTHalfLog2 : 0.f) - m_ref;
         const uint64_t scale2 = f32x2(tile_scale, tile_scale), nref2 = f32x2(nref, nref);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};            // l's summands of this tile: bf16
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // fp16
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};            // l's summands of this tile: two parts
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // one
         // 32 keys at a time; the upper half first, whose product may run while the lower
-        // keys' weights are computed.  P of a half: bf16, for each 32 keys 16 columns of
-        // pairs of the first part and 16 of the second; fp16, 32 columns of pairs.
+        // keys' weights are computed.  P of a half: in two parts, for each 32 keys 16 columns
+        // of pairs of the first and 16 of the second; in one, 32 columns of pairs.
         auto weights = [&](const uint32_t* x, uint32_t to_p) {
           uint32_t pk[kSplit ? 32 : 16];
 #pragma unroll
@@ -669,8 +683,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
                 f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale2, nref2));
             const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
             if constexpr (kSplit) {
-              pk[j / 2] = __byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632);
-              const float2 lo = less_bf16(e0, e1, pk[j / 2]);
+              pk[j / 2] = std::is_same<MT, BF16>::value
+                              ? __byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632)
+                              : pack2(e0, e1, MT{});
+              const float2 lo = less16(e0, e1, pk[j / 2], MT{});
               pk[16 + j / 2] = pack2(lo.x, lo.y, MT{});
               acc[(j / 2) & 3] = add_f32x2(acc[(j / 2) & 3], f32x2(e0, e1));
             } else {
@@ -791,7 +807,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if (row < sg.rows) {
             auto* dst = reinterpret_cast<uint4*>(
                 static_cast<uint16_t*>(p.out) + ((static_cast<int64_t>(sq.start) + node) * p.n_q_heads + head) * D + x);
-            const bool bf16 = kFp8 ? p.q_bf16 != 0 : kSplit;
+            const bool bf16 = kFp8 ? p.q_bf16 != 0 : std::is_same<MT, BF16>::value;
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
               dst[i / 8] = bf16 ? make_uint4(pack2(o[i], o[i + 1], BF16{}), pack2(o[i + 2], o[i + 3], BF16{}),
@@ -1430,10 +1446,10 @@ __global__ void __launch_bounds__(kTMergeWarps * 32)
   }
 }
 
-template <typename MT, typename KV, int D, int NQ>
+template <typename MT, typename KV, int D, int NQ, bool ONE>
 pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   using L = TreeSmem<D, KV::kBytes == 1, NQ>;
-  auto kern = tree_kernel<MT, KV, D, NQ, false>;
+  auto kern = tree_kernel<MT, KV, D, NQ, false, ONE>;
   constexpr int kDevices = 64;
   int dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
@@ -1479,7 +1495,7 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
 template <typename MT, int D, int NQ>
 pkv_status launch_chunk(TreeParams& p, int units, cudaStream_t stream) {
   using L = TreeSmem<D, false, NQ>;
-  auto kern = tree_kernel<MT, MT, D, NQ, true>;
+  auto kern = tree_kernel<MT, MT, D, NQ, true, false>;
   constexpr int kDevices = 64;
   int dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
@@ -1508,10 +1524,10 @@ TreeLauncher pick_chunk(int head_dim, int q_tiles) {
   return q_tiles == 1 ? launch_chunk<MT, 128, 1> : launch_chunk<MT, 128, 2>;
 }
 
-template <typename MT, typename KV>
+template <typename MT, typename KV, bool ONE = false>
 TreeLauncher pick_tree(int head_dim, int q_tiles) {
-  if (head_dim == 64) return q_tiles == 1 ? launch_tree<MT, KV, 64, 1> : launch_tree<MT, KV, 64, 2>;
-  return q_tiles == 1 ? launch_tree<MT, KV, 128, 1> : launch_tree<MT, KV, 128, 2>;
+  if (head_dim == 64) return q_tiles == 1 ? launch_tree<MT, KV, 64, 1, ONE> : launch_tree<MT, KV, 64, 2, ONE>;
+  return q_tiles == 1 ? launch_tree<MT, KV, 128, 1, ONE> : launch_tree<MT, KV, 128, 2, ONE>;
 }
 
 }  // namespace pkv

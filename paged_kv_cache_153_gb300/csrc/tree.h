@@ -57,6 +57,8 @@ struct TreeParams {
 using TreeLauncher = pkv_status (*)(TreeParams&, int ranges, cudaStream_t);
 TreeLauncher tree_launcher_16(int q_dtype, int head_dim, int q_tiles);
 TreeLauncher tree_launcher_fp8(int kv_kind, int head_dim, int q_tiles);
+// one query head per KV head, products in fp16 (fp16 and FP8 caches)
+TreeLauncher tree_launcher_one(int kv_kind, int head_dim, int q_tiles);
 // prompt chunks with a window, 16-bit caches; `ranges` is the units of the longest one
 TreeLauncher chunk_launcher(int q_dtype, int head_dim, int q_tiles);
 

@@ -50,6 +50,34 @@ def test_a_scale_that_is_not_a_number_stays_in_its_head(pkv):
         assert torch.equal(fine, want)
 
 
+@pytest.mark.parametrize("dtype,kv", [("f16", None), ("f16", "e4m3"), ("bf16", "e4m3"), ("f16", "e5m2"),
+                                      ("bf16", "e5m2")])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_query_head_per_kv_head_keeps_the_weights_in_two_parts(pkv, dtype, kv, d):
+    """The dense decode holds such weights in fp32.  Two fp16 parts of a weight are off by
+    2^-22 of it; attn_limits' two-part limit (bf16 parts, 2^-15) covers them.  Pairs of
+    opposite values make outputs near 0, whose own rounding is small beside one
+    rounding of the weights to fp16 (2^-12)."""
+    n = [2, 3, 5, 9, 150]
+    c = Case([0, 1, 4, 7, 140], n, hq=4, hkv=4, d=d, dtype=dtype, kv=kv, seed=7,
+             seen=[np.tril(np.ones((x, x), bool)) for x in n])
+    for b in range(len(n)):
+        for p in range(1, int(c.ctx[b]), 2):
+            here, there = ((int(c.tab[b, x // 16]), x % 16) for x in (p, p - 1))
+            c.vc_h[here[0], :, here[1]] = c.vc_h[there[0], :, there[1]] ^ 0x80 if kv else -c.vc_h[there[0], :, there[1]]
+    c.q_h *= 0.25                                              # (logits near each other)
+    got = c.attend(pkv).double().cpu().numpy()
+    assert int(c.err.item()) == 0
+    for b in range(len(n)):
+        for g in range(4):
+            k, v = c.rows(b, g)
+            for i in range(0, n[b], 1 if n[b] < 10 else 31):
+                m = int(c.base[b]) + i + 1
+                ref, lim = attn_limits.attend(c.q_h[c.cu[b] + i, g].double().numpy(), k[:m], v[:m], c.scale, dtype, "bf16")
+                x = got[c.cu[b] + i, g]
+                assert (np.abs(x - ref) <= lim).all(), (b, g, i, float((np.abs(x - ref) / lim).max()))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("kv", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("outlier,where", [(2.0 ** 10, ...), (2.0 ** 12, ...), (2.0 ** 12, 3), (1.5 * 2.0 ** 14, ...)])
