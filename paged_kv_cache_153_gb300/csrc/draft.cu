@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kCommitThreads)
   if (tid == 0) {
     count_s = max_accept;
     moves_s = 0;
-    bad_s = (n < 0 || ctx < n || (ctx + kBlockSize - 1ll) / kBlockSize > max_blocks) ? 1 : 0;
+    bad_s = (cu_nodes[b] < 0 || n < 0 || ctx < n || (ctx + kBlockSize - 1ll) / kBlockSize > max_blocks) ? 1 : 0;
   }
   __syncthreads();
   for (int k = tid; k < max_accept; k += kCommitThreads)
