@@ -1,6 +1,6 @@
 // C-ABI entry points of the drafted tokens' attention and of the windowed prompt
 // chunks: argument checks, workspace and dispatch.
-#include "tree.h"
+#include "tree.cuh"
 
 #include <cuda_runtime.h>
 
@@ -21,6 +21,31 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct TreeWs {
   size_t seqs, ml, o, parts, part_scale, total;
 };
+
+// A call whose bound allows no tokens attends none: what is left of it is the report of
+// the sequences that have some, or do not fit (the bounds are checked as anywhere else).
+__global__ void __launch_bounds__(256) no_tokens_kernel(const __grid_constant__ TreeParams p) {
+  pdl_wait_and_release();
+  for (int b = threadIdx.x; b < p.batch; b += 256) tree_sequence<1>(p, b, p.err);
+}
+
+pkv_status report_tokens(const int32_t* cu, const int32_t* context_lens, int64_t num_tokens, int batch,
+                         int max_blocks_per_seq, int32_t* err_flag, void* stream) {
+  if (err_flag == nullptr) return PKV_OK;
+  if (!cu || !context_lens) return PKV_ERR_INVALID_ARG;
+  TreeParams p{};
+  p.cu_nodes = cu;
+  p.context_lens = context_lens;
+  p.num_tokens = num_tokens;
+  p.batch = batch;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.n_kv_heads = 1;
+  p.err = err_flag;
+  return cuda_failed(launch_pdl(no_tokens_kernel, dim3(1), dim3(256), 0, static_cast<cudaStream_t>(stream), p),
+                     "no_tokens_kernel launch")
+             ? PKV_ERR_CUDA
+             : PKV_OK;
+}
 
 // row tiles of a unit: two where a sequence may have more than one tile of rows
 int tree_q_tiles(int max_nodes, int group) { return max_nodes * group > kTreeRows ? 2 : 1; }
@@ -65,7 +90,9 @@ pkv_status tree_common(int kv_kind, const void* q, const void* k_cache, const vo
   if (mask_words > kTreeMaxWords || batch > kTreeMaxBatch || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
   if (num_tokens > INT32_MAX / 5 || num_tokens * n_q_heads > INT32_MAX || num_blocks * n_kv_heads > INT32_MAX / kBlockSize)
     return PKV_ERR_UNSUPPORTED;                      // (32-bit TMA row coordinates)
-  if (batch == 0 || num_tokens == 0 || max_nodes == 0) return PKV_OK;
+  if (batch == 0 || num_tokens == 0) return PKV_OK;
+  if (max_nodes == 0)
+    return report_tokens(cu_nodes, context_lens, num_tokens, batch, max_blocks_per_seq, err_flag, stream);
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_nodes || !tree_mask || !out || !workspace)
     return PKV_ERR_INVALID_ARG;
   if (kv_kind != 0 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
@@ -195,7 +222,9 @@ extern "C" pkv_status pkv_paged_prefill_attention_window(
   if (batch > 65535 || num_kv_heads > 65535 || num_tokens > INT32_MAX / group ||
       num_blocks * num_kv_heads > INT32_MAX / kBlockSize)
     return PKV_ERR_UNSUPPORTED;
-  if (batch == 0 || num_tokens == 0 || max_query_len == 0) return PKV_OK;
+  if (batch == 0 || num_tokens == 0) return PKV_OK;
+  if (max_query_len == 0)
+    return report_tokens(cu_seqlens, context_lens, num_tokens, batch, max_blocks_per_seq, err_flag, stream);
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out || num_blocks == 0)
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_ERR_INVALID_ARG;

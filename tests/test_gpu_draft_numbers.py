@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from tests import attn_limits
-from tests.test_gpu_draft import Case
+from tests.test_gpu_draft import OOB, Case
+from tests.test_gpu_window import chunk_case, prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,25 @@ def test_an_outlier_of_q_leaves_the_other_elements_their_bits(pkv, dtype, kv, ou
                     lim = lim + np.expm1(2 * delta) * (w / w.sum()) @ np.abs(v[at])
                     x = got[c.cu[b] + i, h]
                     assert (np.abs(x - ref) <= lim).all(), (b, i, h, float((np.abs(x - ref) / lim).max()))
+
+
+@pytest.mark.parametrize("kv", [None, "e4m3"])
+def test_a_bound_of_no_drafted_tokens_is_too_small_for_some(pkv, kv):
+    c = Case([20, 5], [6, 2], hq=8, hkv=2, kv=kv)
+    out = c.attend(pkv, max_nodes=0)
+    assert int(c.err.item()) == OOB and bool((out == 7.0).all())
+    c = Case([20, 5], [0, 0], hq=8, hkv=2, kv=kv, extra=3)     # nothing but padding
+    out = c.attend(pkv, max_nodes=0)
+    assert int(c.err.item()) == 0 and bool((out == 7.0).all())
+    c = Case([20, 5], [6, 2], hq=8, hkv=2, kv=kv)
+    out = c.attend(pkv, max_nodes=0, err_flag=None)            # (nobody to tell)
+    assert bool((out == 7.0).all())
+
+
+def test_a_bound_of_no_new_tokens_is_too_small_for_some(pkv):
+    c = chunk_case([40, 40], [5, 60], hq=8, hkv=2)
+    out = prefill(pkv, c, 30, 2, max_query_len=0)
+    assert int(c.err.item()) == OOB and bool((out == 7.0).all())
+    c = chunk_case([40, 40], [0, 0], hq=8, hkv=2, extra=3)
+    out = prefill(pkv, c, 30, 2, max_query_len=0)
+    assert int(c.err.item()) == 0 and bool((out == 7.0).all())
