@@ -826,372 +826,376 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       if (lane == 0) mbar_arrive(o_read);
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp == 8 || warp == 11) {
-    // ============================ producers: Q and K, V ============================
-    // (one warp each: V of a tile waits for an earlier P V than K of the tiles
-    // behind it; one warp for both, K behind V, cost 15 % of the whole)
+  } else {
+    // (in front of the roles: setmaxnreg is one instruction for the four warps of a
+    // warpgroup, and warps 8 to 11 have three roles)
     set_max_regs_down<L::kRegsOther>();
-    const bool is_v = warp == 11;
-    const bool codes_v = kFp8 && is_v;               // V's codes go to the conversion
-    const uint32_t stages = codes_v ? L::kCodeStages : is_v ? L::kVStages : L::kKStages;
-    uint64_t* full = codes_v ? c_full : is_v ? v_full : k_full;
-    uint64_t* empty = codes_v ? c_empty : is_v ? v_empty : k_empty;
-    unsigned char* ring = sm + (codes_v ? L::kCodes : is_v ? L::kV : L::kK);
-    uint32_t s = 0, use = 0, tiles = 0, pieces = 0;  // stage and its use of the next tile; issued so far
-    bool good = true;
-    if (is_v)
-      pdl_wait();
-    else
-      pdl_wait_and_release();
-    for (int64_t pos = first; pos < end && good;) {
-      const TreeSeg sg = segment(pos);
-      pos = sg.next;
-      if (sg.t0 >= sg.t1) continue;
-      const TreeSeq sq = sequence_of(sg);
-      const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-      const int nblk = ctx_blocks(sq.ctx);
-      const uint64_t pol = tree_units<NQ>(sq.n << shift) > 1 ? policy_evict_last() : policy_evict_first();
-      const int32_t* row = p.block_tables + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
-      // (CHUNK: blocks that no row sees a key of are not looked up)
-      auto wanted = [&](int blk) -> bool {
-        if (CHUNK && !(blk * kBlockSize <= sg.pos1 &&
-                       (blk * kBlockSize + kBlockSize > sg.low0 || blk * kBlockSize < p.num_sinks)))
-          return false;
-        return lane < kTTileBlocks && blk < nblk;
-      };
-      auto fetch_id = [&](int x) -> int {
-        const int blk = tile_at(sg, x) * kTTileBlocks + lane;
-        return (x >= sg.t0 && wanted(blk)) ? row[blk] : -1;
-      };
-      int id = fetch_id(sg.t1 - 1);
-      if (!is_v) {
-        bool far = false;                            // does any row need the E5M2 parts?
-        if constexpr (kFp8) {
-          for (int x = lane; x < sg.rows; x += 32) {
-            const int r = sg.unit * kTreeRows * NQ + x;
-            far |= p.part_scale[(static_cast<int64_t>(sq.start) + (r >> shift)) * p.n_q_heads + (sg.g << shift) +
-                                (r & ((1 << shift) - 1))] < 0.f;
+    if (warp == 8 || warp == 11) {
+      // ============================ producers: Q and K, V ============================
+      // (one warp each: V of a tile waits for an earlier P V than K of the tiles
+      // behind it; one warp for both, K behind V, cost 15 % of the whole)
+      const bool is_v = warp == 11;
+      const bool codes_v = kFp8 && is_v;               // V's codes go to the conversion
+      const uint32_t stages = codes_v ? L::kCodeStages : is_v ? L::kVStages : L::kKStages;
+      uint64_t* full = codes_v ? c_full : is_v ? v_full : k_full;
+      uint64_t* empty = codes_v ? c_empty : is_v ? v_empty : k_empty;
+      unsigned char* ring = sm + (codes_v ? L::kCodes : is_v ? L::kV : L::kK);
+      uint32_t s = 0, use = 0, tiles = 0, pieces = 0;  // stage and its use of the next tile; issued so far
+      bool good = true;
+      if (is_v)
+        pdl_wait();
+      else
+        pdl_wait_and_release();
+      for (int64_t pos = first; pos < end && good;) {
+        const TreeSeg sg = segment(pos);
+        pos = sg.next;
+        if (sg.t0 >= sg.t1) continue;
+        const TreeSeq sq = sequence_of(sg);
+        const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
+        const int nblk = ctx_blocks(sq.ctx);
+        const uint64_t pol = tree_units<NQ>(sq.n << shift) > 1 ? policy_evict_last() : policy_evict_first();
+        const int32_t* row = p.block_tables + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
+        // (CHUNK: blocks that no row sees a key of are not looked up)
+        auto wanted = [&](int blk) -> bool {
+          if (CHUNK && !(blk * kBlockSize <= sg.pos1 &&
+                         (blk * kBlockSize + kBlockSize > sg.low0 || blk * kBlockSize < p.num_sinks)))
+            return false;
+          return lane < kTTileBlocks && blk < nblk;
+        };
+        auto fetch_id = [&](int x) -> int {
+          const int blk = tile_at(sg, x) * kTTileBlocks + lane;
+          return (x >= sg.t0 && wanted(blk)) ? row[blk] : -1;
+        };
+        int id = fetch_id(sg.t1 - 1);
+        if (!is_v) {
+          bool far = false;                            // does any row need the E5M2 parts?
+          if constexpr (kFp8) {
+            for (int x = lane; x < sg.rows; x += 32) {
+              const int r = sg.unit * kTreeRows * NQ + x;
+              far |= p.part_scale[(static_cast<int64_t>(sq.start) + (r >> shift)) * p.n_q_heads + (sg.g << shift) +
+                                  (r & ((1 << shift) - 1))] < 0.f;
+            }
+            far = __any_sync(0xffffffffu, far);
           }
-          far = __any_sync(0xffffffffu, far);
-        }
-        // Q of the piece, once every Q K^T of the piece before has read it
-        if (pieces > 0) good = __all_sync(0xffffffffu, tree_wait(q_empty, (pieces - 1) & 1, p, abort_flag));
-        if (!good) break;
-        const int parts = kFp8 ? (p.q_bf16 ? 2 : 3) : 1;
-        if (kFp8 && lane == 0) *far_parts = far;
-        if (lane == 0)
-          mbar_arrive_expect_tx(q_full, nq * parts * (p.q_box << shift) * (kFp8 ? D : 2 * D));
-        ++pieces;
-        __syncwarp();
-        if (kFp8 && lane < nq * parts) {
-          const int c = lane / parts, part = lane % parts, kept = part + (far && part > 0 ? parts - 1 : 0);
-          tma_load_3d(sm + L::kQ + c * L::kQTile + part * L::kStage, &p.tmap_q, 0, sg.g << shift,
-                      static_cast<int>(kept * p.num_tokens) + sq.start +
-                          ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift),
-                      q_full, policy_evict_last());
-        }
-        if (!kFp8 && lane < nq * (D / 64)) {
-          const int c = lane / (D / 64), h = lane % (D / 64);
-          tma_load_3d(sm + L::kQ + c * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
-                      sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), q_full,
-                      policy_evict_last());
-        }
-        __syncwarp();
-      }
-      for (int t = sg.t1 - 1; t >= sg.t0; --t) {
-        // cache slab of this lane's block: -1 behind the context or for a bad id
-        bool have = wanted(tile_at(sg, t) * kTTileBlocks + lane);
-        if (have && (id < 0 || id >= p.num_blocks)) {
-          record_error(p.err, PKV_ERR_OOB);
-          have = false;
-        }
-        const int64_t slab = have ? static_cast<int64_t>(id) * p.n_kv_heads + sg.g : -1;
-        id = fetch_id(t - 1);
-        good = __all_sync(0xffffffffu, use == 0 || tree_wait(&empty[s], (use - 1) & 1, p, abort_flag));
-        if (!good) break;
-        if constexpr (!kFp8) {
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
+          // Q of the piece, once every Q K^T of the piece before has read it
+          if (pieces > 0) good = __all_sync(0xffffffffu, tree_wait(q_empty, (pieces - 1) & 1, p, abort_flag));
+          if (!good) break;
+          const int parts = kFp8 ? (p.q_bf16 ? 2 : 3) : 1;
+          if (kFp8 && lane == 0) *far_parts = far;
+          if (lane == 0)
+            mbar_arrive_expect_tx(q_full, nq * parts * (p.q_box << shift) * (kFp8 ? D : 2 * D));
+          ++pieces;
           __syncwarp();
-          // (slab -1 is outside the tensor, which fills with zeros)
-          if (lane < kTTileBlocks)
-            tma_load_4d(ring + s * L::kTile + lane * (kBlockSize * D * 2), is_v ? &p.tmap_v : &p.tmap_k,
-                        static_cast<int>(slab) * 2, &full[s], pol);
-        } else if (!is_v) {
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kKTile);
-          __syncwarp();
-          if (lane < kTTileBlocks)
-            tma_load_2d(ring + s * L::kKTile + lane * (kBlockSize * D), &p.tmap_k, 0, static_cast<int>(slab) * kBlockSize,
-                        &full[s], pol);
-        } else {
-          constexpr int kSlab = kBlockSize * D;
-          unsigned char* dst = ring + s * L::kStage + lane * kSlab;
-          const uint32_t got = __ballot_sync(0xffffffffu, have);
-          if (lane < kTTileBlocks && !have) {        // (codes of 0; rare but for the last tile)
-            for (int x = 0; x < kSlab; x += 16)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(dst + x)), "r"(0u) : "memory");
-            fence_proxy_async_smem();
+          if (kFp8 && lane < nq * parts) {
+            const int c = lane / parts, part = lane % parts, kept = part + (far && part > 0 ? parts - 1 : 0);
+            tma_load_3d(sm + L::kQ + c * L::kQTile + part * L::kStage, &p.tmap_q, 0, sg.g << shift,
+                        static_cast<int>(kept * p.num_tokens) + sq.start +
+                            ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift),
+                        q_full, policy_evict_last());
+          }
+          if (!kFp8 && lane < nq * (D / 64)) {
+            const int c = lane / (D / 64), h = lane % (D / 64);
+            tma_load_3d(sm + L::kQ + c * L::kTile + h * L::kHalfQ, &p.tmap_q, h * 64, sg.g << shift,
+                        sq.start + ((sg.unit * kTreeRows * NQ + c * kTreeRows) >> shift), q_full,
+                        policy_evict_last());
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(got) * kSlab);
-          __syncwarp();
-          if (have) bulk_g2s(dst, p.v_codes + slab * kSlab, kSlab, &full[s], pol);
         }
-        __syncwarp();
-        ++tiles;
-        if (++s == stages) {
-          s = 0;
-          ++use;
+        for (int t = sg.t1 - 1; t >= sg.t0; --t) {
+          // cache slab of this lane's block: -1 behind the context or for a bad id
+          bool have = wanted(tile_at(sg, t) * kTTileBlocks + lane);
+          if (have && (id < 0 || id >= p.num_blocks)) {
+            record_error(p.err, PKV_ERR_OOB);
+            have = false;
+          }
+          const int64_t slab = have ? static_cast<int64_t>(id) * p.n_kv_heads + sg.g : -1;
+          id = fetch_id(t - 1);
+          good = __all_sync(0xffffffffu, use == 0 || tree_wait(&empty[s], (use - 1) & 1, p, abort_flag));
+          if (!good) break;
+          if constexpr (!kFp8) {
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
+            __syncwarp();
+            // (slab -1 is outside the tensor, which fills with zeros)
+            if (lane < kTTileBlocks)
+              tma_load_4d(ring + s * L::kTile + lane * (kBlockSize * D * 2), is_v ? &p.tmap_v : &p.tmap_k,
+                          static_cast<int>(slab) * 2, &full[s], pol);
+          } else if (!is_v) {
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kKTile);
+            __syncwarp();
+            if (lane < kTTileBlocks)
+              tma_load_2d(ring + s * L::kKTile + lane * (kBlockSize * D), &p.tmap_k, 0,
+                          static_cast<int>(slab) * kBlockSize, &full[s], pol);
+          } else {
+            constexpr int kSlab = kBlockSize * D;
+            unsigned char* dst = ring + s * L::kStage + lane * kSlab;
+            const uint32_t got = __ballot_sync(0xffffffffu, have);
+            if (lane < kTTileBlocks && !have) {        // (codes of 0; rare but for the last tile)
+              for (int x = 0; x < kSlab; x += 16)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(dst + x)), "r"(0u) : "memory");
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(got) * kSlab);
+            __syncwarp();
+            if (have) bulk_g2s(dst, p.v_codes + slab * kSlab, kSlab, &full[s], pol);
+          }
+          __syncwarp();
+          ++tiles;
+          if (++s == stages) {
+            s = 0;
+            ++use;
+          }
         }
       }
-    }
-    if (!good) *abort_flag = 1;
-    if (lane == 0) {
-      // The last loads of every stage land before the block ends (bounded, with the
-      // full limit): whoever should wait for them may have stopped.
-      const unsigned long long deadline = global_ns() + kWaitLimitNs;
-      if (pieces > 0) mbar_wait_until(q_full, (pieces - 1) & 1, deadline);
-      for (uint32_t n = tiles > stages ? tiles - stages : 0; n < tiles; ++n)
-        mbar_wait_until(&full[n % stages], (n / stages) & 1, deadline);
-    }
-    __syncwarp();
-  } else if (warp < 11) {
-    set_max_regs_down<L::kRegsOther>();
-    // ============================ MMA issuers (warps 9, 10) ============================
-    // Warp 9 issues Q K^T, warp 10 P V, one elected lane each: a commit holds its
-    // thread until the MMA queue has drained to a few entries; meanwhile the
-    // other feeds the queue.
-    constexpr int kPasses = kSplit ? 2 : 1;
-    const int parts = p.q_bf16 ? 2 : 3;              // of an FP8 operand q
-    constexpr uint32_t kIdQK = umma_idesc<MT>(false, kTreeKeys), kIdPV = umma_idesc<MT>(true, D);
-    const bool qk_warp = (warp == 9);
-    bool ok = true;
-    if (lane == 0) {
-      uint32_t id_rest = 0;                          // FP8: of the parts behind the first
-      Ring<NB> sr;
-      Ring<L::kKStages> kr;
+      if (!good) *abort_flag = 1;
+      if (lane == 0) {
+        // The last loads of every stage land before the block ends (bounded, with the
+        // full limit): whoever should wait for them may have stopped.
+        const unsigned long long deadline = global_ns() + kWaitLimitNs;
+        if (pieces > 0) mbar_wait_until(q_full, (pieces - 1) & 1, deadline);
+        for (uint32_t n = tiles > stages ? tiles - stages : 0; n < tiles; ++n)
+          mbar_wait_until(&full[n % stages], (n / stages) & 1, deadline);
+      }
+      __syncwarp();
+    } else if (warp < 11) {
+      // ============================ MMA issuers (warps 9, 10) ============================
+      // Warp 9 issues Q K^T, warp 10 P V, one elected lane each: a commit holds its
+      // thread until the MMA queue has drained to a few entries; meanwhile the
+      // other feeds the queue.
+      constexpr int kPasses = kSplit ? 2 : 1;
+      const int parts = p.q_bf16 ? 2 : 3;              // of an FP8 operand q
+      constexpr uint32_t kIdQK = umma_idesc<MT>(false, kTreeKeys), kIdPV = umma_idesc<MT>(true, D);
+      const bool qk_warp = (warp == 9);
+      bool ok = true;
+      if (lane == 0) {
+        uint32_t id_rest = 0;                          // FP8: of the parts behind the first
+        Ring<NB> sr;
+        Ring<L::kKStages> kr;
+        Ring<L::kVStages> vr;
+        uint32_t pieces = 0, ops = 0;
+        for (int64_t pos = first; pos < end && ok;) {
+          const TreeSeg sg = segment(pos);
+          pos = sg.next;
+          if (sg.t0 >= sg.t1) continue;
+          const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
+          if (qk_warp) {
+            // (the producer loads nothing while the previous kernel runs)
+            ok = mbar_wait_started_early(q_full, pieces & 1, p.err, p.wait_limit_ns);
+            if constexpr (kFp8) id_rest = umma_idesc_codes<KV>(kTreeKeys, *far_parts != 0);
+          }
+          // (the piece's first P V overwrites the outputs of the piece before)
+          if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
+          ++pieces;
+          for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t) {
+            if (qk_warp)
+              ok = tree_wait(&k_full[kr.s], kr.ph, p, abort_flag);
+            else
+              ok = mbar_wait_started_early(&v_ready[vr.s], vr.ph, p.err, p.wait_limit_ns);
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+              if (c >= nq || !ok) break;
+              const uint32_t d_s = tmem + sr.s * kTreeKeys;
+              if (qk_warp) {
+                // S once the P V that read P from its columns is done
+                ok = ops < NB || tree_wait(&pv_done[sr.s], sr.ph ^ 1u, p, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (kFp8) {
+                  const uint64_t a0 = umma_desc_codes<D>(smem_u32(sm + L::kQ + c * L::kQTile));
+                  const uint64_t b0 = umma_desc_codes<D>(smem_u32(sm + L::kK + kr.s * L::kKTile));
+                  constexpr uint32_t kIdFirst = umma_idesc_codes<KV>(kTreeKeys, false);
+                  // (the smallest parts first)
+#pragma unroll
+                  for (int part = L::kParts - 1; part >= 0; --part)
+                    if (part < parts)
+                      umma_f8<D / 32>(d_s, a0 + static_cast<uint64_t>((part * L::kStage) >> 4), b0,
+                                      part == 0 ? kIdFirst : id_rest, part < parts - 1);
+                } else {
+                  const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + c * L::kTile), 16, 1024);
+                  const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
+#pragma unroll
+                  for (int ks = 0; ks < D / 16; ++ks)
+                    umma_f16(d_s, a0 + static_cast<uint64_t>(((ks >> 2) * L::kHalfQ + (ks & 3) * 32) >> 4),
+                             b0 + static_cast<uint64_t>(((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
+                }
+                umma_commit(&s_full[sr.s]);
+              } else {
+                const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + vr.s * L::kTile), L::kHalf, L::kGroup);
+                const uint32_t d_o = tmem + L::kOCol + c * D;
+                // the upper keys' P first
+                auto half = [&](auto upper) {
+                  constexpr int h = decltype(upper)::value;
+                  tc_fence_after();
+#pragma unroll
+                  for (int pass = 0; pass < kPasses; ++pass)
+#pragma unroll
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                      umma_f16_tmem_a(d_o,
+                                      d_s + (kSplit ? 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1)
+                                                    : 64 * (ks >> 2) + 8 * (ks & 3)),
+                                      b0 + static_cast<uint64_t>((ks * 2 * L::kGroup) >> 4), kIdPV,
+                                      t < sg.t1 - 1 || h == 0 || ks > 4 || pass > 0);
+                };
+                ok = tree_wait(&p_half[sr.s], sr.ph, p, abort_flag);
+                if (ok) half(std::integral_constant<int, 1>{});
+                ok = ok && tree_wait(&p_full[sr.s], sr.ph, p, abort_flag);
+                if (!ok) break;
+                half(std::integral_constant<int, 0>{});
+                umma_commit(&pv_done[sr.s]);
+              }
+              ++ops;
+              sr.next();
+            }
+            if (!ok) break;
+            umma_commit(qk_warp ? &k_empty[kr.s] : &v_empty[vr.s]);
+            if (qk_warp && t == sg.t0) umma_commit(q_empty);
+            kr.next();
+            vr.next();
+          }
+        }
+        if (!ok) *abort_flag = 1;
+        // every MMA of this lane has completed before TMEM is released
+        umma_commit(&mma_idle[qk_warp ? 0 : 1]);
+        mbar_wait(&mma_idle[qk_warp ? 0 : 1], 0, p.err);
+      }
+      __syncwarp();
+    } else {
+      // ============ warps from 12 on: rows with drafted tokens, conversions ============
+      const int x_tid = tid - 12 * 32, x_warp = x_tid >> 5;
+      constexpr int kChunks = D / 8;                   // 16-byte chunks of a 16-bit row
       Ring<L::kVStages> vr;
-      uint32_t pieces = 0, ops = 0;
+      Ring<(kFp8 ? L::kCodeStages : 1)> cr;
+      uint32_t pieces = 0, tiles = 0;
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t ph) {
+        return __all_sync(0xffffffffu, tree_wait(bar, ph, p, abort_flag));
+      };
+      pdl_wait();
       for (int64_t pos = first; pos < end && ok;) {
         const TreeSeg sg = segment(pos);
         pos = sg.next;
         if (sg.t0 >= sg.t1) continue;
-        const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
-        if (qk_warp) {
-          // (the producer loads nothing while the previous kernel runs)
-          ok = mbar_wait_started_early(q_full, pieces & 1, p.err, p.wait_limit_ns);
-          if constexpr (kFp8) id_rest = umma_idesc_codes<KV>(kTreeKeys, *far_parts != 0);
-        }
-        // (the piece's first P V overwrites the outputs of the piece before)
-        if (!qk_warp && pieces > 0) ok = tree_wait(o_read, (pieces - 1) & 1, p, abort_flag);
-        ++pieces;
-        for (int t = sg.t1 - 1; t >= sg.t0 && ok; --t) {
-          if (qk_warp)
-            ok = tree_wait(&k_full[kr.s], kr.ph, p, abort_flag);
-          else
-            ok = mbar_wait_started_early(&v_ready[vr.s], vr.ph, p.err, p.wait_limit_ns);
-#pragma unroll
-          for (int c = 0; c < NQ; ++c) {
-            if (c >= nq || !ok) break;
-            const uint32_t d_s = tmem + sr.s * kTreeKeys;
-            if (qk_warp) {
-              // S once the P V that read P from its columns is done
-              ok = ops < NB || tree_wait(&pv_done[sr.s], sr.ph ^ 1u, p, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              if constexpr (kFp8) {
-                const uint64_t a0 = umma_desc_codes<D>(smem_u32(sm + L::kQ + c * L::kQTile));
-                const uint64_t b0 = umma_desc_codes<D>(smem_u32(sm + L::kK + kr.s * L::kKTile));
-                constexpr uint32_t kIdFirst = umma_idesc_codes<KV>(kTreeKeys, false);
-                // (the smallest parts first)
-#pragma unroll
-                for (int part = L::kParts - 1; part >= 0; --part)
-                  if (part < parts)
-                    umma_f8<D / 32>(d_s, a0 + static_cast<uint64_t>((part * L::kStage) >> 4), b0,
-                                    part == 0 ? kIdFirst : id_rest, part < parts - 1);
-              } else {
-                const uint64_t a0 = umma_desc(smem_u32(sm + L::kQ + c * L::kTile), 16, 1024);
-                const uint64_t b0 = umma_desc(smem_u32(sm + L::kK + kr.s * L::kTile), 16, L::kGroup);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                  umma_f16(d_s, a0 + static_cast<uint64_t>(((ks >> 2) * L::kHalfQ + (ks & 3) * 32) >> 4),
-                           b0 + static_cast<uint64_t>(((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), kIdQK, ks > 0);
-              }
-              umma_commit(&s_full[sr.s]);
-            } else {
-              const uint64_t b0 = umma_desc(smem_u32(sm + L::kV + vr.s * L::kTile), L::kHalf, L::kGroup);
-              const uint32_t d_o = tmem + L::kOCol + c * D;
-              // the upper keys' P first
-              auto half = [&](auto upper) {
-                constexpr int h = decltype(upper)::value;
-                tc_fence_after();
-#pragma unroll
-                for (int pass = 0; pass < kPasses; ++pass)
-#pragma unroll
-                  for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                    umma_f16_tmem_a(d_o,
-                                    d_s + (kSplit ? 32 * (ks >> 1) + 16 * pass + 8 * (ks & 1)
-                                                  : 64 * (ks >> 2) + 8 * (ks & 3)),
-                                    b0 + static_cast<uint64_t>((ks * 2 * L::kGroup) >> 4), kIdPV,
-                                    t < sg.t1 - 1 || h == 0 || ks > 4 || pass > 0);
-              };
-              ok = tree_wait(&p_half[sr.s], sr.ph, p, abort_flag);
-              if (ok) half(std::integral_constant<int, 1>{});
-              ok = ok && tree_wait(&p_full[sr.s], sr.ph, p, abort_flag);
-              if (!ok) break;
-              half(std::integral_constant<int, 0>{});
-              umma_commit(&pv_done[sr.s]);
+        const TreeSeq sq = sequence_of(sg);
+        const int base = sq.ctx - sq.n;
+        uint32_t* my_bad = bad + (pieces % kTBadSlots) * (L::kXform * 8) + x_warp * kBadWords;
+        if (lane < kBadWords) my_bad[lane] = 0u;
+        __syncwarp();
+        auto store = [&](uint32_t addr, const uint4& v) {
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        };
+        auto load = [&](uint32_t addr) -> uint4 {
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(addr));
+          return v;
+        };
+        // 16-byte chunk c of key row j of a K / V tile
+        auto at = [&](int j, int c) -> uint32_t {
+          return (j >> 3) * L::kGroup + (c >> 3) * L::kHalf + (j & 7) * 128 + (((c & 7) ^ (j & 7)) << 4);
+        };
+        // elements of V at position key: 0 where no row sees them; where only some do, 0
+        // if they are not finite, and the token is remembered
+        auto clean = [&](uint4 v, int key) -> uint4 {
+          bool none, all;
+          int note;
+          if constexpr (CHUNK) {
+            none = key > sg.pos1 || (key >= p.num_sinks && key < sg.low0);
+            all = key <= sg.pos0 && (key < p.num_sinks || key >= sg.low1);
+            note = key > sg.pos0 ? key - sg.pos0 - 1 : 256 + key - sg.low0;
+          } else {
+            none = key >= sq.ctx;
+            all = key < base;
+            note = key - base;
+          }
+          if (none) return make_uint4(0u, 0u, 0u, 0u);
+          if (!all) {
+            const uint4 f =
+                make_uint4(nonfinite2<MT>(v.x), nonfinite2<MT>(v.y), nonfinite2<MT>(v.z), nonfinite2<MT>(v.w));
+            if (f.x | f.y | f.z | f.w) {
+              v.x ^= f.x, v.y ^= f.y, v.z ^= f.z, v.w ^= f.w;
+              atomicOr(&my_bad[note >> 5], 1u << (note & 31));
             }
-            ++ops;
-            sr.next();
           }
-          if (!ok) break;
-          umma_commit(qk_warp ? &k_empty[kr.s] : &v_empty[vr.s]);
-          if (qk_warp && t == sg.t0) umma_commit(q_empty);
-          kr.next();
-          vr.next();
-        }
-      }
-      if (!ok) *abort_flag = 1;
-      // every MMA of this lane has completed before TMEM is released
-      umma_commit(&mma_idle[qk_warp ? 0 : 1]);
-      mbar_wait(&mma_idle[qk_warp ? 0 : 1], 0, p.err);
-    }
-    __syncwarp();
-  } else {
-    // ============ warps from 12 on: rows with drafted tokens, conversions ============
-    set_max_regs_down<L::kRegsOther>();
-    const int x_tid = tid - 12 * 32, x_warp = x_tid >> 5;
-    constexpr int kChunks = D / 8;                   // 16-byte chunks of a 16-bit row
-    Ring<L::kVStages> vr;
-    Ring<(kFp8 ? L::kCodeStages : 1)> cr;
-    uint32_t pieces = 0, tiles = 0;
-    bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t ph) {
-      return __all_sync(0xffffffffu, tree_wait(bar, ph, p, abort_flag));
-    };
-    pdl_wait();
-    for (int64_t pos = first; pos < end && ok;) {
-      const TreeSeg sg = segment(pos);
-      pos = sg.next;
-      if (sg.t0 >= sg.t1) continue;
-      const TreeSeq sq = sequence_of(sg);
-      const int base = sq.ctx - sq.n;
-      uint32_t* my_bad = bad + (pieces % kTBadSlots) * (L::kXform * 8) + x_warp * kBadWords;
-      if (lane < kBadWords) my_bad[lane] = 0u;
-      __syncwarp();
-      auto store = [&](uint32_t addr, const uint4& v) {
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-      };
-      auto load = [&](uint32_t addr) -> uint4 {
-        uint4 v;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(addr));
-        return v;
-      };
-      // 16-byte chunk c of key row j of a K / V tile
-      auto at = [&](int j, int c) -> uint32_t {
-        return (j >> 3) * L::kGroup + (c >> 3) * L::kHalf + (j & 7) * 128 + (((c & 7) ^ (j & 7)) << 4);
-      };
-      // elements of V at position key: 0 where no row sees them; where only some do, 0
-      // if they are not finite, and the token is remembered
-      auto clean = [&](uint4 v, int key) -> uint4 {
-        bool none, all;
-        int note;
-        if constexpr (CHUNK) {
-          none = key > sg.pos1 || (key >= p.num_sinks && key < sg.low0);
-          all = key <= sg.pos0 && (key < p.num_sinks || key >= sg.low1);
-          note = key > sg.pos0 ? key - sg.pos0 - 1 : 256 + key - sg.low0;
-        } else {
-          none = key >= sq.ctx;
-          all = key < base;
-          note = key - base;
-        }
-        if (none) return make_uint4(0u, 0u, 0u, 0u);
-        if (!all) {
-          const uint4 f = make_uint4(nonfinite2<MT>(v.x), nonfinite2<MT>(v.y), nonfinite2<MT>(v.z), nonfinite2<MT>(v.w));
-          if (f.x | f.y | f.z | f.w) {
-            v.x ^= f.x, v.y ^= f.y, v.z ^= f.z, v.w ^= f.w;
-            atomicOr(&my_bad[note >> 5], 1u << (note & 31));
-          }
-        }
-        return v;
-      };
-      ++pieces;
-      for (int x0 = sg.t1 - 1; x0 >= sg.t0 && ok; --x0, ++tiles) {
-        const int t = tile_at(sg, x0);
-        if constexpr (!kFp8) {
-          ok = wait_all(&v_full[vr.s], vr.ph);
-          if (!ok) break;
-          if (CHUNK ? !chunk_plain(sg, t, p.num_sinks) : (t + 1) * kTreeKeys > base) {
-            // (of drafted tokens: rows from the first one on)
+          return v;
+        };
+        ++pieces;
+        for (int x0 = sg.t1 - 1; x0 >= sg.t0 && ok; --x0, ++tiles) {
+          const int t = tile_at(sg, x0);
+          if constexpr (!kFp8) {
+            ok = wait_all(&v_full[vr.s], vr.ph);
+            if (!ok) break;
+            if (CHUNK ? !chunk_plain(sg, t, p.num_sinks) : (t + 1) * kTreeKeys > base) {
+              // (of drafted tokens: rows from the first one on)
+              const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
+              for (int x = (CHUNK ? 0 : max(0, base - t * kTreeKeys)) * kChunks + x_tid; x < kTreeKeys * kChunks;
+                   x += L::kXform * 32) {
+                const int j = x / kChunks;
+                const uint32_t addr = tile + at(j, x % kChunks);
+                const uint4 v = load(addr), w = clean(v, t * kTreeKeys + j);
+                if ((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) store(addr, w);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&v_ready[vr.s]);
+            vr.next();
+          } else {
+            ok = wait_all(&c_full[cr.s], cr.ph) && (tiles < L::kVStages || wait_all(&v_empty[vr.s], vr.ph ^ 1u));
+            if (!ok) break;
+            const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + cr.s * L::kStage);
             const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
-            for (int x = (CHUNK ? 0 : max(0, base - t * kTreeKeys)) * kChunks + x_tid; x < kTreeKeys * kChunks; x += L::kXform * 32) {
-              const int j = x / kChunks;
-              const uint32_t addr = tile + at(j, x % kChunks);
-              const uint4 v = load(addr), w = clean(v, t * kTreeKeys + j);
-              if ((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) store(addr, w);
+            // Chunk k of 16 codes of this thread is kBytes of the tile behind chunk k - 1
+            // (whole groups of 8 keys), so its two places are constants away.  The lanes of
+            // a row's upper half convert and store its second 8 codes first: both halves of
+            // a row lie in the same banks.
+            constexpr int kAll = kTreeKeys * D / 16, kStep = L::kXform * 32;
+            constexpr int kBytes = kStep / (D / 16) / 8 * L::kGroup;
+            constexpr int kPer = kAll / kStep < 4 ? kAll / kStep : 4;   // chunks whose instructions interleave
+            static_assert(kStep / (D / 16) % 8 == 0 && kAll % (kPer * kStep) == 0, "chunks");
+            const int j0 = x_tid / (D / 16), c0 = x_tid % (D / 16);
+            const bool up = D == 128 && (c0 & 4);
+            const uint32_t first8 = tile + at(j0, 2 * c0 + (up ? 1 : 0)), last8 = tile + at(j0, 2 * c0 + (up ? 0 : 1));
+#pragma unroll 1
+            for (int k0 = 0; k0 < kAll / kStep; k0 += kPer) {
+              uint4 raw[kPer];
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + (k0 + k) * kStep];
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) {
+                const uint4 w = raw[k];
+                const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
+                const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
+                store(first8 + (k0 + k) * kBytes, make_uint4(w0.x, w0.y, w1.x, w1.y));
+                store(last8 + (k0 + k) * kBytes, make_uint4(w2.x, w2.y, w3.x, w3.y));
+              }
+            }
+            if ((t + 1) * kTreeKeys > base) {
+              // V rows from the first drafted token on: each thread looks at what it wrote
+#pragma unroll 1
+              for (int x = x_tid; x < kAll; x += L::kXform * 32) {
+                const int j = x / (D / 16), c = x % (D / 16);
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t addr = tile + at(j, 2 * c + e);
+                  store(addr, clean(load(addr), t * kTreeKeys + j));
+                }
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(&v_ready[vr.s]);
-          vr.next();
-        } else {
-          ok = wait_all(&c_full[cr.s], cr.ph) && (tiles < L::kVStages || wait_all(&v_empty[vr.s], vr.ph ^ 1u));
-          if (!ok) break;
-          const uint4* codes = reinterpret_cast<const uint4*>(sm + L::kCodes + cr.s * L::kStage);
-          const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
-          // Chunk k of 16 codes of this thread is kBytes of the tile behind chunk k - 1
-          // (whole groups of 8 keys), so its two places are constants away.  The lanes of
-          // a row's upper half convert and store its second 8 codes first: both halves of
-          // a row lie in the same banks.
-          constexpr int kAll = kTreeKeys * D / 16, kStep = L::kXform * 32;
-          constexpr int kBytes = kStep / (D / 16) / 8 * L::kGroup;
-          constexpr int kPer = kAll / kStep < 4 ? kAll / kStep : 4;   // chunks whose instructions interleave
-          static_assert(kStep / (D / 16) % 8 == 0 && kAll % (kPer * kStep) == 0, "chunks");
-          const int j0 = x_tid / (D / 16), c0 = x_tid % (D / 16);
-          const bool up = D == 128 && (c0 & 4);
-          const uint32_t first8 = tile + at(j0, 2 * c0 + (up ? 1 : 0)), last8 = tile + at(j0, 2 * c0 + (up ? 0 : 1));
-#pragma unroll 1
-          for (int k0 = 0; k0 < kAll / kStep; k0 += kPer) {
-            uint4 raw[kPer];
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) raw[k] = codes[x_tid + (k0 + k) * kStep];
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const uint4 w = raw[k];
-              const uint2 w0 = codes4(up ? w.z : w.x, KV{}), w1 = codes4(up ? w.w : w.y, KV{});
-              const uint2 w2 = codes4(up ? w.x : w.z, KV{}), w3 = codes4(up ? w.y : w.w, KV{});
-              store(first8 + (k0 + k) * kBytes, make_uint4(w0.x, w0.y, w1.x, w1.y));
-              store(last8 + (k0 + k) * kBytes, make_uint4(w2.x, w2.y, w3.x, w3.y));
+            if (lane == 0) {
+              mbar_arrive(&c_empty[cr.s]);
+              mbar_arrive(&v_ready[vr.s]);
             }
+            cr.next();
+            vr.next();
           }
-          if ((t + 1) * kTreeKeys > base) {
-            // V rows from the first drafted token on: each thread looks at what it wrote
-#pragma unroll 1
-            for (int x = x_tid; x < kAll; x += L::kXform * 32) {
-              const int j = x / (D / 16), c = x % (D / 16);
-#pragma unroll 1
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t addr = tile + at(j, 2 * c + e);
-                store(addr, clean(load(addr), t * kTreeKeys + j));
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&c_empty[cr.s]);
-            mbar_arrive(&v_ready[vr.s]);
-          }
-          cr.next();
-          vr.next();
         }
       }
+      if (!ok) *abort_flag = 1;
     }
-    if (!ok) *abort_flag = 1;
   }
   tc_fence_before();
   __syncthreads();
