@@ -414,6 +414,24 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// and for what another warp does only once the previous kernel is over: a limit that runs
+// out while that kernel runs starts anew at its end
+inline __device__ __noinline__ bool tree_wait_from_previous_end(uint64_t* bar, uint32_t parity, const TreeParams* p,
+                                                                const volatile int* abort_flag) {
+  pdl_wait();
+  return tree_wait(bar, parity, *p, abort_flag);
+}
+__device__ __forceinline__ bool tree_wait_started_early(uint64_t* bar, uint32_t parity, const TreeParams& p,
+                                                        const volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > p.wait_limit_ns) return tree_wait_from_previous_end(bar, parity, &p, abort_flag);
+  }
+  return true;
+}
+
 // ONE: one query head per KV head (fp16 products)
 template <typename MT, typename KV, int D, int NQ, bool CHUNK, bool ONE>
 __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
@@ -980,7 +998,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           const int nq = NQ == 2 && sg.rows > kTreeRows ? 2 : 1;
           if (qk_warp) {
             // (the producer loads nothing while the previous kernel runs)
-            ok = mbar_wait_started_early(q_full, pieces & 1, p.err, p.wait_limit_ns);
+            ok = tree_wait_started_early(q_full, pieces & 1, p, abort_flag);
             if constexpr (kFp8) id_rest = umma_idesc_codes<KV>(kTreeKeys, *far_parts != 0);
           }
           // (the piece's first P V overwrites the outputs of the piece before)
@@ -990,7 +1008,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
             if (qk_warp)
               ok = tree_wait(&k_full[kr.s], kr.ph, p, abort_flag);
             else
-              ok = mbar_wait_started_early(&v_ready[vr.s], vr.ph, p.err, p.wait_limit_ns);
+              ok = tree_wait_started_early(&v_ready[vr.s], vr.ph, p, abort_flag);
 #pragma unroll
             for (int c = 0; c < NQ; ++c) {
               if (c >= nq || !ok) break;
