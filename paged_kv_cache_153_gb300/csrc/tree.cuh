@@ -1306,9 +1306,10 @@ __global__ void __launch_bounds__(kTPartWarps * 32)
 // r0 + x's piece of the rows' unit; the states are joined as in the other merges,
 // with the first pieces' outputs loaded beside their weights.  Units that one range
 // held are done.  It is all latency, so a warp takes one row and eight pieces at a
-// time where the rows' warps fit the GPU at once, and else four rows and two pieces.
-// (Cold, 32 sequences of 1024 to 16384 tokens: 11.6 us; one row a warp 18.5 us.  One
-// of 131072, 19 pieces a row: 7.9 us; four rows one after another 24 us.)
+// time where the rows' warps fit the GPU at once (by the registers, five thread blocks
+// an SM), and else four rows and two pieces.  (Calls with 19 tokens of 32 heads a
+// sequence, contexts of 4096, one row a warp and four: 4 sequences, 2432 rows, 21.3 and
+// 26.1 us; 8, where 3040 fit, 37.2 and 36.1; 16, 62.0 and 57.6; 64, 198 and 187.)
 // With one row a warp, and all thread blocks on the GPU at once, the geometry is
 // worked out from the inputs while the kernel before still runs (one document of
 // 131072: 123 us instead of 125 then; four chats 9.0 instead of 9.9).
@@ -1476,17 +1477,23 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   int dev = 0;
   if (cuda_failed(cudaGetDevice(&dev), "cudaGetDevice")) return PKV_ERR_CUDA;
   static std::mutex mu;
-  static bool done[kDevices] = {};
+  static int per_sm[kDevices] = {};   // thread blocks of the merge, one row a warp (0: not asked yet)
   if (dev < 0 || dev >= kDevices) return PKV_ERR_UNSUPPORTED;
+  int merge_blocks;                   // of them on the GPU at once
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (!done[dev]) {
+    if (per_sm[dev] == 0) {
+      int n = 0;
       if (cuda_failed(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(L::bytes(kTreeMaxBatch))),
-                      "cudaFuncSetAttribute"))
+                      "cudaFuncSetAttribute") ||
+          cuda_failed(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, tree_merge_kernel<D, NQ, 1>,
+                                                                    kTMergeWarps * 32, 0),
+                      "cudaOccupancyMaxActiveBlocksPerMultiprocessor"))
         return PKV_ERR_CUDA;
-      done[dev] = true;
+      per_sm[dev] = std::max(n, 1);
     }
+    merge_blocks = per_sm[dev] * sm_count();
   }
   p.setup_cost = tree_setup_cost(KV::kBytes == 1);
   if constexpr (KV::kBytes == 1) {
@@ -1500,13 +1507,11 @@ pkv_status launch_tree(TreeParams& p, int ranges, cudaStream_t stream) {
   if (cuda_failed(launch_pdl(kern, dim3(static_cast<unsigned>(ranges)), dim3(L::kThreads), L::bytes(p.batch), stream, p),
                   "tree_kernel launch"))
     return PKV_ERR_CUDA;
-  // (64 warps an SM)
-  const int nr = p.num_tokens * p.n_q_heads > 64ll * sm_count() ? 4 : 1;
+  const int nr = p.num_tokens * p.n_q_heads > static_cast<int64_t>(merge_blocks) * kTMergeWarps ? 4 : 1;
   const unsigned chunks = ((p.max_nodes << p.group_shift) + kTMergeWarps * nr - 1) / (kTMergeWarps * nr);
   const dim3 grid(chunks, static_cast<unsigned>(p.n_kv_heads), static_cast<unsigned>(p.batch));
   auto merge = nr == 4 ? tree_merge_kernel<D, NQ, 4> : tree_merge_kernel<D, NQ, 1>;
-  // (by its registers, five thread blocks an SM)
-  const int ahead = static_cast<int64_t>(chunks) * p.n_kv_heads * p.batch <= 5ll * sm_count();
+  const int ahead = static_cast<int64_t>(chunks) * p.n_kv_heads * p.batch <= merge_blocks;
   return cuda_failed(launch_pdl(merge, grid, dim3(kTMergeWarps * 32), 0, stream, p, ranges, ahead),
                      "tree_merge_kernel launch")
              ? PKV_ERR_CUDA
