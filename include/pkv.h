@@ -690,12 +690,12 @@ pkv_status pkv_paged_decode_attention_window_e5m2(const void* q, const uint8_t* 
  * bits they hold; an element of V that is not finite gives an output that is not
  * finite where it is seen.  Weights in 16 bits as in the drafted tokens' attention
  * below (fp16 ones rounded once, as in pkv_paged_prefill_attention, with one query
- * head per KV head too).  max_query_len: an upper bound of n_b.  Tokens behind the
- * last sequence are neither read nor written.  Device errors (PKV_ERR_OOB; the sequence is
- * skipped, its outputs stay as they are): offsets that do not ascend within
- * [0, num_tokens], more tokens than max_query_len or than the context has, a
- * context longer than its table.  A table entry outside the pool reads as zeros
- * and is reported.
+ * head per KV head too).  max_query_len: an upper bound of n_b.  Outputs of tokens
+ * behind the last sequence are not written, and their q changes nothing.  Device
+ * errors (PKV_ERR_OOB; the sequence is skipped, its outputs stay as they are):
+ * offsets that do not ascend within [0, num_tokens], more tokens than
+ * max_query_len or than the context has, a context longer than its table.  A table
+ * entry outside the pool reads as zeros and is reported.
  * ------------------------------------------------------------------------- */
 pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, const int32_t* context_lens,
@@ -713,7 +713,8 @@ pkv_status pkv_paged_prefill_attention_window(const void* q, const void* k_cache
  * counts them, and token i of them is cached at position base + i, base =
  * context_lens[b] - n_b.  cu_nodes: device int32 [batch + 1], cu_nodes[0] >= 0,
  * cu_nodes[batch] <= num_tokens; a sequence may have none.  What belongs to
- * tokens behind the last sequence is neither read nor written.
+ * tokens behind the last sequence is not written, and changes nothing whatever it
+ * holds (rows of q there may be read).
  *
  * pkv_tree_plan: the tokens of a sequence form a tree whose root is the
  * context's last token: parents[t] (device int32 [num_tokens]) is the index of

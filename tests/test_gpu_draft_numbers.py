@@ -113,6 +113,18 @@ def test_an_outlier_of_q_leaves_the_other_elements_their_bits(pkv, dtype, kv, ou
                     assert (np.abs(x - ref) <= lim).all(), (b, i, h, float((np.abs(x - ref) / lim).max()))
 
 
+@pytest.mark.parametrize("dtype,kv", [("bf16", None), ("f16", "e4m3"), ("bf16", "e5m2")])
+def test_rows_behind_the_last_sequence_change_nothing(pkv, dtype, kv):
+    # a batch padded to a fixed number of tokens, whatever the padding holds
+    c = Case([20, 5, 130], [6, 0, 40], hq=8, hkv=2, dtype=dtype, kv=kv, extra=40)
+    want = c.attend(pkv).clone()
+    c.check(want)
+    for bad in (float("nan"), float("inf"), 6e4):
+        c.q_h[46:] = bad
+        out = c.attend(pkv)
+        assert torch.equal(out[:46], want[:46]) and bool((out[46:] == 7.0).all()) and int(c.err.item()) == 0, bad
+
+
 @pytest.mark.parametrize("kv", [None, "e4m3"])
 def test_a_bound_of_no_drafted_tokens_is_too_small_for_some(pkv, kv):
     c = Case([20, 5], [6, 2], hq=8, hkv=2, kv=kv)
