@@ -172,6 +172,12 @@ __device__ __forceinline__ int seq_blocks(int cap, int ctx, int32_t* err) {
   return nb;
 }
 
+// tokens of a context of ctx that its first nb blocks hold, nb as seq_blocks (nb
+// kBlockSize may pass 2^31)
+__device__ __forceinline__ int kept_tokens(int nb, int ctx) {
+  return ctx <= 0 ? 0 : ctx_blocks(ctx) <= nb ? ctx : nb * kBlockSize;
+}
+
 // Blocks that the first `sinks` tokens lie in, and blocks between them and the
 // last `window` of n tokens that hold none of either.
 __device__ __forceinline__ int sink_blocks(int sinks) { return sinks / kBlockSize + (sinks % kBlockSize != 0); }
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(SRC == kRest ? 512 : (NW + 1) * 32, SRC != kRe
       const int ctx = p.context_lens[b];
       nb = seq_blocks(SRC == kListed || SRC == kWindow ? p.max_blocks_per_seq : min(p.max_blocks_per_seq, p.max_nblk),
                       ctx, p.err);
-      ntok[b] = min(max(ctx, 0), nb * kBlockSize);
+      ntok[b] = kept_tokens(nb, ctx);
       if constexpr (SRC == kListed) nb = min(nb, p.budget);
       if constexpr (SRC == kWindow) nb -= window_skip(ntok[b], p.window, p.num_sinks);
       if constexpr (SRC == kRest) {
@@ -1737,7 +1743,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       const int ctx = p.context_lens[i];
       int n = ctx < 0 ? 0 : min(ctx_blocks(ctx), p.window > 0 ? p.max_blocks_per_seq
                                                               : min(p.max_blocks_per_seq, p.max_nblk));
-      if (p.window > 0) n -= window_skip(min(max(ctx, 0), n * kBlockSize), p.window, p.num_sinks);
+      if (p.window > 0) n -= window_skip(kept_tokens(n, ctx), p.window, p.num_sinks);
       v2 += n;
       v3 += n > 0;
       if (i < b) {

@@ -617,7 +617,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           continue;
         }
         const int t = tile_at(sg, sg.t1 - 1 - n);
-        const bool tail = CHUNK ? !chunk_plain(sg, t, p.num_sinks) : (t + 1) * kTreeKeys > base;
+        const bool tail = CHUNK ? !chunk_plain(sg, t, p.num_sinks) : t * kTreeKeys > base - kTreeKeys;
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (tail) {
 #pragma unroll
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
             if constexpr (!CHUNK) bits &= words[w];
             for (; bits != 0u; bits &= bits - 1u) {
               const int i0 = 32 * w + __ffs(bits) - 1;
-              const int at = !CHUNK ? base + i0 : i0 < 256 ? sg.pos0 + 1 + i0 : sg.low0 + i0 - 256;
+              const int at = !CHUNK ? base + i0 : i0 < 256 ? sg.pos0 + 1 + i0 : sg.low0 + (i0 - 256);
               if (CHUNK && !(at <= base + node && (at > base + node - p.window || at < p.num_sinks))) continue;
               const int id = p.block_tables[static_cast<int64_t>(sg.b) * p.max_blocks_per_seq + at / kBlockSize];
               if (id < 0 || id >= p.num_blocks) continue;
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
         // (CHUNK: blocks that no row sees a key of are not looked up)
         auto wanted = [&](int blk) -> bool {
           if (CHUNK && !(blk * kBlockSize <= sg.pos1 &&
-                         (blk * kBlockSize + kBlockSize > sg.low0 || blk * kBlockSize < p.num_sinks)))
+                         (blk * kBlockSize > sg.low0 - kBlockSize || blk * kBlockSize < p.num_sinks)))
             return false;
           return lane < kTTileBlocks && blk < nblk;
         };
@@ -1121,7 +1121,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if constexpr (CHUNK) {
             none = key > sg.pos1 || (key >= p.num_sinks && key < sg.low0);
             all = key <= sg.pos0 && (key < p.num_sinks || key >= sg.low1);
-            note = key > sg.pos0 ? key - sg.pos0 - 1 : 256 + key - sg.low0;
+            note = key > sg.pos0 ? key - sg.pos0 - 1 : 256 + (key - sg.low0);
           } else {
             none = key >= sq.ctx;
             all = key < base;
@@ -1144,7 +1144,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
           if constexpr (!kFp8) {
             ok = wait_all(&v_full[vr.s], vr.ph);
             if (!ok) break;
-            if (CHUNK ? !chunk_plain(sg, t, p.num_sinks) : (t + 1) * kTreeKeys > base) {
+            if (CHUNK ? !chunk_plain(sg, t, p.num_sinks) : t * kTreeKeys > base - kTreeKeys) {
               // (of drafted tokens: rows from the first one on)
               const uint32_t tile = smem_u32(sm + L::kV + vr.s * L::kTile);
               for (int x = (CHUNK ? 0 : max(0, base - t * kTreeKeys)) * kChunks + x_tid; x < kTreeKeys * kChunks;
@@ -1189,7 +1189,7 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
                 store(last8 + (k0 + k) * kBytes, make_uint4(w2.x, w2.y, w3.x, w3.y));
               }
             }
-            if ((t + 1) * kTreeKeys > base) {
+            if (t * kTreeKeys > base - kTreeKeys) {
               // V rows from the first drafted token on: each thread looks at what it wrote
 #pragma unroll 1
               for (int x = x_tid; x < kAll; x += L::kXform * 32) {
