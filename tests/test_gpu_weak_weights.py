@@ -86,3 +86,34 @@ def test_prompt_chunks(pkv, dtype, hq, hkv, new):
     for b in range(4):
         for i in (0, new - 1):
             check(c, out, b, int(c.cu[b]) + i, od.window_seen([base[b] + i], base[b] + new, 3500, 4)[0], 2.0 ** -32)
+
+
+def dense(pkv, c):
+    c.upload()
+    q = c.q[:len(c.ctx)].contiguous()
+    out = torch.full_like(q, 7.0)
+    ws = torch.full((pkv.pkv_decode_workspace_bytes(len(c.ctx), c.hq, c.hkv, c.d, c.width, int(c.ctx.max())),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    kw = dict(scale=c.scale, max_context_len=int(c.ctx.max()), workspace=ws, err_flag=c.err)
+    if c.kv:
+        call = pkv.pkv_paged_decode_attention_fp8 if c.kv == "e4m3" else pkv.pkv_paged_decode_attention_e5m2
+        call(q, c.kc, c.vc, c.ks.cuda(), c.vs.cuda(), c.tables, c.lens, out, **kw)
+    else:
+        pkv.pkv_paged_decode_attention(q, c.kc, c.vc, c.tables, c.lens, out, **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("dtype,kv", [("f16", None), ("bf16", None), ("f16", "e4m3"), ("bf16", "e5m2")])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 4, 64), (16, 4, 128), (32, 4, 128), (4, 4, 64)])
+def test_single_tokens(pkv, dtype, kv, hq, hkv, d):
+    # the first token, as many models prefer it
+    n = 40
+    base = [3000 + 17 * b for b in range(n)]
+    c = preferred(base, [1] * n, [0] * n, hq=hq, hkv=hkv, d=d, dtype=dtype, kv=kv, seed=3)
+    outs = {0: dense(pkv, c), 4096: decode(pkv, c, 4096, 4), 1500: decode(pkv, c, 1500, 4)}
+    assert int(c.err.item()) == 0
+    for window, out in outs.items():
+        for b in range(0, n, 3):
+            seen = od.window_seen([base[b]], base[b] + 1, window, 4)[0] if window else np.ones(base[b] + 1, bool)
+            check(c, out, b, b, seen, 2.0 ** -40)
