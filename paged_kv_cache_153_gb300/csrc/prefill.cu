@@ -98,6 +98,10 @@ constexpr int kKStages = 2, kVStages = 3; // K and V rings in shared memory
 constexpr int kTmemCols = 512;            // S / P buffers at columns 0, 128, 256; O at 384
 constexpr int kOCol = kSBufs * kPN;
 constexpr float kRescaleLog2 = 8.f;      // the row reference moves when the max outgrows it by > 2^8
+constexpr float kHalfLog2 = 7.f;         // fp16 weights are held times 2^7: below 2^16, and the smallest step
+                                         // is 2^-31 of a row's largest (unscaled, one key 17 nats above a
+                                         // context of 4000 took a fifth of what the others give)
+static_assert(kRescaleLog2 + kHalfLog2 < 16.f, "fp16 weights");
 
 // offsets in the 1024-aligned shared block: Q | K ring | V ring | barriers | row exchange
 constexpr int kOffQ = 0;
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_prefill_kernel(const __gri
       // columns: 16 pairs of P_hi, then (bf16) 16 pairs of P_lo.  Masked scores
       // are -inf and give 2^-inf = 0.  For bf16, P_hi is p truncated to bf16
       // (its top 16 bits) and P_lo = bf16(p - P_hi), where p - P_hi is exact.
-      const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
+      const float nref = (m_ref == -INFINITY) ? 0.f : (std::is_same<QT, F16>::value ? kHalfLog2 : 0.f) - m_ref;
       const uint64_t scale2 = f32x2(p.qk_scale_log2, p.qk_scale_log2), nref2 = f32x2(nref, nref);
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};   // (+0, +0) pairs
       uint32_t pk2[64];   // bf16: both chunks' columns, stored at once

@@ -117,3 +117,19 @@ def test_single_tokens(pkv, dtype, kv, hq, hkv, d):
         for b in range(0, n, 3):
             seen = od.window_seen([base[b]], base[b] + 1, window, 4)[0] if window else np.ones(base[b] + 1, bool)
             check(c, out, b, b, seen, 2.0 ** -40)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq", [2, 8])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_prefill(pkv, dtype, hq, where):
+    base, new = [4000, 2500, 3300, 2900], 40
+    at = [{"first": 0, "middle": x // 2, "last": x - 1}[where] for x in base]
+    c = preferred(base, [new] * 4, at, hq=hq, hkv=2, d=128, dtype=dtype, seed=2).upload()
+    pkv.pkv_paged_prefill_attention(c.q, c.kc, c.vc, c.tables, c.lens, c.cu_d, c.out, scale=c.scale, max_query_len=new,
+                                    err_flag=c.err)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    for b in range(4):
+        for i in (0, new - 1):
+            check(c, c.out, b, int(c.cu[b]) + i, np.arange(base[b] + new) <= base[b] + i, 2.0 ** -32)
