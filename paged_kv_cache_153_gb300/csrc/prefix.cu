@@ -76,6 +76,11 @@ constexpr int kXTileBlocks = kXKeys / kBlockSize;
 // K tiles in shared memory: one; V tiles: two beside one row tile, one beside two
 constexpr int kXVStages = 2;
 constexpr float kXRescaleLog2 = 8.f;
+// fp16 weights are held times 2^7 (below 2^16, and the smallest step is 2^-31 of a row's
+// largest; unscaled, one key 18 nats above a prefix of 3000 tokens took a third of what
+// the others give), and the states times 2^-7 as they leave
+constexpr float kXHalfLog2 = 7.f, kXHalfDown = 1.f / 128.f;
+static_assert(kXRescaleLog2 + kXHalfLog2 < 16.f, "fp16 weights");
 constexpr int kXHalfQ = kXRows * 128;             // bytes of a 64-column half of a Q tile
 constexpr int kXHalfKV = kXKeys * 128;            // and of a K / V tile
 
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
             tmem_st16(t_o + chain * D + c, o);
           }
         }
-        const float nref = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        const float nref = (m_ref == -INFINITY) ? 0.f : (std::is_same<QT, F16>::value ? kXHalfLog2 : 0.f) - m_ref;
         const uint64_t scale2 = f32x2(p.qk_scale_log2, p.qk_scale_log2), nref2 = f32x2(nref, nref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
         // the columns in registers are the upper 64; the lower ones are read again
@@ -357,20 +362,23 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
       const int row0 = (sg.share ? chain * kXRows : 0) + (warp & 3) * 32;   // the warp's first row of the unit
       const int n_rows = sg.rows - row0;                                    // those that exist (of 32)
       float* dst = p.o + (sg.row + row0) * D;
+      constexpr float kDown = std::is_same<QT, F16>::value ? kXHalfDown : 1.f;
       if (sg.share) {
 #pragma unroll 1
         for (int c = 0; c < D && ok; c += 32) {
           float o[32];
           tmem_ld32(t_o + chain * D + c, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= kDown;
           store_rows32<D>(dst + c, o, n_rows, lane);
         }
         if (ok && lane < n_rows)
-          *reinterpret_cast<float2*>(p.ml + (sg.row + row0 + lane) * 2) = make_float2(m_ref, l_run);
+          *reinterpret_cast<float2*>(p.ml + (sg.row + row0 + lane) * 2) = make_float2(m_ref, l_run * kDown);
       } else {
         // join the two key streams: each warpgroup takes half of the columns
         const float2 a = red[r], b = red[kXRows + r];
         const float m = fmaxf(a.x, b.x), ref = (m == -INFINITY) ? 0.f : m;
-        const float wa = ex2_approx(a.x - ref), wb = ex2_approx(b.x - ref);
+        const float wa = ex2_approx(a.x - ref) * kDown, wb = ex2_approx(b.x - ref) * kDown;
         if (ok && n_rows > 0) {
 #pragma unroll 1
           for (int c = chain * (D / 2); c < (chain + 1) * (D / 2); c += 32) {

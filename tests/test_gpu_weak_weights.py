@@ -133,3 +133,27 @@ def test_prefill(pkv, dtype, hq, where):
     for b in range(4):
         for i in (0, new - 1):
             check(c, c.out, b, int(c.cu[b]) + i, np.arange(base[b] + new) <= base[b] + i, 2.0 ** -32)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq", [16, 4])
+@pytest.mark.parametrize("members,where", [(5, "first"), (5, "last"), (100, "first"), (100, "last")])
+def test_shared_prefixes(pkv, dtype, hq, members, where):
+    # 40 groups x 4 KV heads: a thread block takes most of a prefix.  One and two row tiles.
+    groups, hkv, n = 40, 4, 2992
+    c = preferred([n - 1] * groups, [1] * groups, [{"first": 0, "last": n - 1}[where]] * groups, hq=hq, hkv=hkv, d=64,
+                  dtype=dtype, seed=4).upload()
+    rows = torch.arange(groups, device="cuda").repeat_interleave(members)
+    q, tab, lens = c.q[rows].contiguous(), c.tables[rows].contiguous(), c.lens[rows].contiguous()
+    starts = torch.arange(0, members * groups + 1, members, dtype=torch.int32, device="cuda")
+    pre = torch.full((groups,), n, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ws = torch.full((pkv.pkv_prefix_workspace_bytes(len(rows), groups, hq, hkv, 64, c.width, n, n),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    pkv.pkv_paged_decode_attention_prefix(q, c.kc, c.vc, tab, lens, starts, pre, out, scale=c.scale, max_context_len=n,
+                                          max_prefix_len=n, workspace=ws, err_flag=c.err)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    for b in range(0, groups, 3):
+        for i in (0, members - 1):
+            check(c, out.view(groups, members, hq, 64)[:, i], b, b, np.ones(n, bool), 2.0 ** -32)
