@@ -20,8 +20,10 @@
 // bytes of the rows of one head of K or V and takes them in order: row k is
 // written only after the rows up to k have been read, and nothing behind k is
 // read from where k is written (a_j >= j > k).  So it can move in place, eight
-// loads ahead of their stores.  Bound by memory once there is enough of it (64
-// sequences, 32 layers of 8 heads: 100 MB in 18.2 us).
+// loads ahead of their stores.  (64 sequences, 32 layers of 8 heads in one cache:
+// 64 to 86 MB of rows move, by the paths; 16 to 19 us with inputs taken in turn, 21 to
+// 24 with nothing of them in L2, about half of the copy rate: 2048 thread blocks, each
+// with a chain of lengths, lists and tables ahead of the few rows that it moves.)
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -85,14 +85,16 @@
 // document of 131072, 557 instead of 479 for the prompts below.)  Waits are bounded
 // as in the other kernels.
 //
-// Measured (back to back, everything with its launches): 32 sequences of 1024 to
-// 16384 tokens with 20 to 32 drafted ones, 32 and 8 heads of 128, bf16: 132 us, of
-// which 10 are the merge; the reads alone take 112 at 6.80 TB/s.  One of 131072 with
-// 64, fp16: 121 us (79); each row tile's softmax, P V and next Q K^T wait for each
-// other (4500 clocks, 2048 of them products).  16 of 4096 to 32768 with 10 to 31,
-// E4M3: 96 us (57): shared memory feeds the products, the conversions and the loads
-// in turn.  Four prompts of 2048 tokens, window 4096: 459 us; the products with
-// bf16's second part take 318.
+// Measured (inputs taken in turn, everything with its launches; figures above and below
+// that compare two forms are calls on one input): 32 sequences of 1024 to 16384 tokens
+// with 20 to 32 drafted ones, 32 and 8 heads of 128, bf16: 136 us, of which 10 are the
+// merge; the reads alone take 112 at 6.80 TB/s.  One of 131072 with 64, fp16: 132 us (79);
+// each row tile's softmax, P V and next Q K^T wait for each other (4500 clocks, 2048 of
+// them products).  16 of 4096 to 32768 with 10 to 31, E4M3 and E5M2: 100 us (57): shared
+// memory feeds the products, the conversions and the loads in turn.  Four prompts of 2048
+// tokens, window 4096: 474 us; the products with bf16's second part take 318.  A prompt
+// chunk of 16 tokens alone: 41 us, eight thread blocks with 33 key tiles each, one after
+// another (no split over the keys).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -127,9 +129,10 @@ __host__ __device__ constexpr int tree_tile_cost(int rows) { return rows > kTree
 template <int D, bool FP8, int NQ>
 struct TreeSmem {
   // Warps that convert codes (or look at V rows) behind the first twelve, and the
-  // registers that the softmax warps take from the others.  (One document of 131072,
-  // fp16, with 144, 152, 160, 176: 121.7, 123.2, 120.9, 124.5 us; E4M3 contexts with 120,
-  // 136, 144, 152: 97.6, 95.2, 95.2, 98.1.)
+  // registers that the softmax warps take from the others.  (144, 152 and 160 make little
+  // difference over 16-bit caches: one document of 131072, fp16, 133.3, 132.8, 132.5 us,
+  // four prompts 469.6, 473.5, 474.8.  E4M3 contexts with 120, 136, 144, 152: 97.6, 95.2,
+  // 95.2, 98.1.)
   static constexpr int kXform = FP8 ? 8 : 4;
   static constexpr int kThreads = 384 + 32 * kXform;
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;           // a thread, at launch
