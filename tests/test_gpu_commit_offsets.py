@@ -42,7 +42,7 @@ def test_bad_offsets_move_nothing(pkv, cu, moved):
 
 @pytest.mark.parametrize("most", [300, 1024])
 def test_long_lists(pkv, most):
-    # more entries than a thread block has threads, in one and in several rounds
+    # more entries than a thread block has threads, in one and in several turns of the loops
     rng = np.random.default_rng(most)
     new = np.array([1500, most, 700])
     base = np.array([9, 100, 0])
