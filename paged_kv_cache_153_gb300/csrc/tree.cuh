@@ -71,7 +71,8 @@
 // own writes the parts to the workspace (in the kernel, per piece, four warps took 6 to
 // 13 us).  V's codes are converted to fp16 tiles, exactly, by eight warps (one
 // instruction for two E4M3 codes, one byte permutation for two E5M2 ones; with four
-// warps 106 us instead of 100).  With K converted as well, shared memory took 3900 clocks a tile.
+// warps 106 us instead of 100).  With K converted as well, shared memory took 3900
+// clocks a tile.
 //
 // Prompt chunks (CHUNK).  The same kernel attends the new tokens of a prompt to the
 // first tokens and a window: a thread block per unit, whose key tiles are those
@@ -361,8 +362,8 @@ __device__ __forceinline__ uint64_t umma_desc_codes(uint32_t saddr) {
 // kind::f8f6f4: A in E4M3 or E5M2, B in KV, fp32 accumulate, both K-major, M = 128
 template <typename KV>
 __host__ __device__ constexpr uint32_t umma_idesc_codes(int n, bool a_e5m2) {
-  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((std::is_same<KV, E5M2>::value ? 1u : 0u) << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(128 >> 4) << 24);
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((std::is_same<KV, E5M2>::value ? 1u : 0u) << 10) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 // D += A B over 32 STEPS elements of K: successive 32-byte steps of the descriptors.  (As
 // statements of their own, E4M3 contexts took 104 us instead of 97 once the instruction
@@ -392,7 +393,6 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
         : "memory");
 }
 
-// MT: 16-bit type of the products; KV: the cache's (MT, or an FP8 format)
 // mbar_wait that gives up early once the block has stopped
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, const TreeParams& p,
                                           const volatile int* abort_flag) {
@@ -435,7 +435,8 @@ __device__ __forceinline__ bool tree_wait_started_early(uint64_t* bar, uint32_t 
   return true;
 }
 
-// ONE: one query head per KV head (fp16 products)
+// MT: 16-bit type of the products; KV: the cache's (MT, or an FP8 format); ONE: one query
+// head per KV head (fp16 products)
 template <typename MT, typename KV, int D, int NQ, bool CHUNK, bool ONE>
 __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 1) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool kFp8 = KV::kBytes == 1;
@@ -591,9 +592,10 @@ __global__ void __launch_bounds__((TreeSmem<D, KV::kBytes == 1, NQ>::kThreads), 
       // (FP8: q's parts, and so the scores, are scaled by row, and hold K's sign; the sign of
       // a row's scale tells which parts it needs)
       const float scale_log2 =
-          p.qk_scale_log2 * (kFp8 ? fabsf(p.k_scale[sg.g] * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
-                                                                   (sg.g << shift) + (unit_row & ((1 << shift) - 1))])
-                                  : 1.f);
+          p.qk_scale_log2 *
+          (kFp8 ? fabsf(p.k_scale[sg.g] * p.part_scale[(static_cast<int64_t>(sq.start) + node) * p.n_q_heads +
+                                                       (sg.g << shift) + (unit_row & ((1 << shift) - 1))])
+                : 1.f);
       const uint32_t to = tmem + lane_base + L::kOCol + tile * D;
       float m_ref = -INFINITY, l_run = 0.f;
       // take over the row's reference of the operation before

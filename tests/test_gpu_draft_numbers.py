@@ -74,7 +74,8 @@ def test_one_query_head_per_kv_head_keeps_the_weights_in_two_parts(pkv, dtype, k
             k, v = c.rows(b, g)
             for i in range(0, n[b], 1 if n[b] < 10 else 31):
                 m = int(c.base[b]) + i + 1
-                ref, lim = attn_limits.attend(c.q_h[c.cu[b] + i, g].double().numpy(), k[:m], v[:m], c.scale, dtype, "bf16")
+                ref, lim = attn_limits.attend(c.q_h[c.cu[b] + i, g].double().numpy(), k[:m], v[:m], c.scale, dtype,
+                                              "bf16")
                 x = got[c.cu[b] + i, g]
                 assert (np.abs(x - ref) <= lim).all(), (b, g, i, float((np.abs(x - ref) / lim).max()))
 

@@ -9,7 +9,7 @@ import torch
 
 from tests.test_gpu_draft import Case
 from tests.test_gpu_wait_limits import expire
-from tests.test_gpu_wait_start import check, slow   # noqa: F401  (a fixture)
+from tests.test_gpu_wait_start import check, slow   # noqa: F401  (slow: a fixture)
 from tests.test_gpu_window import chunk_case
 
 pytestmark = pytest.mark.gpu
@@ -59,9 +59,11 @@ def test_prompt_chunks(pkv, monkeypatch, dtype, hq, hkv, d, base, new):
     expire(monkeypatch, chunk_call(pkv, c, 4096, 4), c.out, c.err)
 
 
-@pytest.mark.parametrize("dtype,kv,hq,hkv,new", [("bf16", None, 8, 2, 9), ("f16", None, 8, 2, 60), ("f16", None, 2, 2, 9),
-                                                 ("bf16", "e4m3", 8, 2, 9), ("f16", "e5m2", 8, 2, 60)])
-def test_the_limit_counts_from_the_end_of_the_previous_kernel(pkv, slow, monkeypatch, dtype, kv, hq, hkv, new):   # noqa: F811
+@pytest.mark.parametrize("dtype,kv,hq,hkv,new", [
+    ("bf16", None, 8, 2, 9), ("f16", None, 8, 2, 60), ("f16", None, 2, 2, 9), ("bf16", "e4m3", 8, 2, 9),
+    ("f16", "e5m2", 8, 2, 60)])
+def test_the_limit_counts_from_the_end_of_the_previous_kernel(pkv, slow, monkeypatch, dtype, kv, hq, hkv,   # noqa: F811
+                                                              new):
     c = Case([300, 40], [new, 3], hq=hq, hkv=hkv, d=64, dtype=dtype, kv=kv, seed=2)
     call, _ = tree_call(pkv, c)
     check(monkeypatch, slow, call, c.out, c.err)

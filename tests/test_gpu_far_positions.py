@@ -70,7 +70,8 @@ def test_windows(pkv, table, n, dtype, window, sinks):
     check(out, q, kc, vc, tab, 0, n - 1, n, window, sinks, dtype)
     out = torch.zeros((new, HQ, D), dtype=t, device="cuda")
     cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
-    pkv.pkv_paged_prefill_attention_window(q.cuda(), kc.cuda(), vc.cuda(), table, lens, cu, out, max_query_len=new, **kw)
+    pkv.pkv_paged_prefill_attention_window(q.cuda(), kc.cuda(), vc.cuda(), table, lens, cu, out, max_query_len=new,
+                                           **kw)
     assert int(err.item()) == 0
     for i in range(new):
         check(out, q, kc, vc, tab, i, n - new + i, n, window, sinks, dtype)
@@ -109,15 +110,16 @@ def test_drafted_tokens(pkv, table, kv):
     seen = np.array([[1, 0, 0], [0, 1, 0], [1, 0, 1]], bool)
     mask = torch.from_numpy(od.mask_words(seen, 1)).cuda()
     i32 = dict(dtype=torch.int32, device="cuda")
-    q, out, err = torch.ones((3, 1, d), dtype=torch.float16, device="cuda"), torch.zeros((3, 1, d), dtype=torch.float16, device="cuda"), torch.zeros(1, **i32)
+    q = torch.ones((3, 1, d), dtype=torch.float16, device="cuda")
+    out, err = torch.zeros_like(q), torch.zeros(1, **i32)
     ws = torch.empty(pkv.pkv_tree_workspace_bytes(1, 3, 1, 1, d, 3), dtype=torch.uint8, device="cuda")
     getattr(pkv, "pkv_paged_tree_attention" + ("_fp8" if kv else ""))(
         q, kc, vc, *scales, table, torch.tensor([n], **i32), torch.tensor([0, 3], **i32), mask, out, scale=0.125,
         max_context_len=n, max_nodes=3, workspace=ws, err_flag=err)
     torch.cuda.synchronize()
     assert int(err.item()) == 0
-    logit = torch.tensor([float(kc[nb, 0, 12 + j, 0].view(torch.float8_e4m3fn).item() if kv else kc[nb, 0, 12 + j, 0]) * 8
-                          for j in range(3)], dtype=torch.float64)
+    keys = kc[nb, 0, 12:15, 0].contiguous()
+    logit = 8 * (keys.view(torch.float8_e4m3fn) if kv else keys).double().cpu()
     for i, (top, value) in enumerate([(logit[0], 2.0), (logit[1], 3.0), (logit[2], 4.0)]):
         rest = (n - 3) * torch.exp(-top) + (torch.exp(logit[0] - top) if i == 2 else 0)
         low = 1.0 if i != 2 else 2.0                           # (token 2 sees token 0 as well)

@@ -58,7 +58,8 @@ def check(c, got, b, row, seen, floor):
     for g in range(c.hkv):
         k, v = (x[at] for x in c.rows(b, g))
         for h in range(g * per, (g + 1) * per):
-            ref, lim = attn_limits.attend(c.q_h[row, h].double().numpy(), k, v, c.scale, c.dtype, "f16" if c.kv else None)
+            ref, lim = attn_limits.attend(c.q_h[row, h].double().numpy(), k, v, c.scale, c.dtype,
+                                          "f16" if c.kv else None)
             lim = lim + len(at) * floor * np.abs(v).max()
             assert (np.abs(got[row, h] - ref) <= lim).all(), (b, h, float((np.abs(got[row, h] - ref) / ref).max()))
 
